@@ -7,6 +7,13 @@
  *   b200norm_skip_rms    com.microsoft.SkipSimplifiedLayerNormalization
  *   b200norm_gated_rms   com.microsoft.GatedRMSNorm
  *   b200norm_skip_group  com.microsoft.SkipGroupNorm
+ * and the operators that stand beside them on a residual stream, in serving
+ * and in training:
+ *   b200norm_skip_layer, b200norm_skip_layer_grad
+ *                        layer normalization (with the residual add fused in),
+ *                        and its gradients
+ *   b200norm_linear, b200norm_linear_grad
+ *                        y = act(x W^T + b) + residual, and its gradients
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer to a dense, contiguous,
@@ -36,8 +43,7 @@
  *     B200NORM_OK and enqueues nothing.
  *   - b200norm_last_error() returns a thread-local, human-readable reason for
  *     the last non-OK status returned on the calling thread.
- *   - Calls are stateless apart from the caller-provided SkipGroupNorm
- *     workspace, and may be issued from several host threads at once.
+ *   - Calls are stateless apart from the caller-provided workspaces, and may be issued from several host threads at once.
  *   - Kernels are launched with programmatic dependent launch allowed: one
  *     may be scheduled while the previous kernel on the stream drains, but it
  *     waits for that kernel to complete (and its writes to be visible) before
@@ -75,7 +81,7 @@ typedef enum {
     B200NORM_ERR_INVALID_ARGUMENT = 1, /* bad pointer, shape, attribute or overlap   */
     B200NORM_ERR_UNSUPPORTED = 2,      /* element type or shape the library refuses   */
     B200NORM_ERR_CUDA = 3,             /* a CUDA runtime call or launch failed        */
-    B200NORM_ERR_WORKSPACE = 4,        /* SkipGroupNorm workspace missing / too small */
+    B200NORM_ERR_WORKSPACE = 4,        /* workspace missing, too small or misaligned  */
     B200NORM_ERR_DEVICE_TIMEOUT = 5    /* a device-side wait gave up (see below)      */
 } b200norm_status;
 
@@ -272,6 +278,126 @@ B200NORM_API b200norm_status b200norm_workspace_init(void* workspace, size_t wor
  * failed. */
 B200NORM_API b200norm_status b200norm_workspace_status(const void* workspace,
                                                        b200norm_stream_t stream);
+
+/*
+ * Layer normalization over the last axis, with the residual add fused in:
+ *
+ *   S[r, j]      = round_T((input[r, j] + skip[r, j]) + bias[j])
+ *   mu[r]        = mean_j(S[r, :]),  var[r] = mean_j((S[r, :] - mu[r])^2)
+ *   output[r, j] = round_T((S[r, j] - mu[r]) * (1 / sqrt(var[r] + epsilon)) * gamma[j]
+ *                          + beta[j])
+ *
+ *   input, skip          T, (rows, hidden).  skip may be NULL: S is then the
+ *                        input, and bias and input_skip_bias_sum must be NULL.
+ *   gamma, beta          M, (hidden); M is T or B200NORM_F32.  beta may be NULL.
+ *   bias                 T, (hidden), or NULL.
+ *   output               T, (rows, hidden).
+ *   input_skip_bias_sum  T, (rows, hidden): receives S; NULL when not requested.
+ *   mean, inv_std_var    float32, (rows): mu and 1 / sqrt(var + epsilon); either
+ *                        may be NULL.  b200norm_skip_layer_grad needs both.
+ *   epsilon              >= 0 and not NaN.
+ *
+ * rows == 0 is a no-op.  hidden must be > 0.
+ */
+B200NORM_API b200norm_status b200norm_skip_layer(
+    const void* input, const void* skip, const void* gamma, const void* beta, const void* bias,
+    void* output, void* input_skip_bias_sum, float* mean, float* inv_std_var, int64_t rows,
+    int64_t hidden, b200norm_dtype T, b200norm_dtype M, float epsilon, b200norm_stream_t stream);
+
+/*
+ * Gradients of b200norm_skip_layer.  With u = (S - mean) * inv_std_var and
+ * g = dy * gamma:
+ *
+ *   dx[r, j]  = round_T(inv_std_var[r] * (g - mean_j(g) - u * mean_j(g * u)) + ds[r, j])
+ *   dgamma[j] = round_M(sum_r dy * u)
+ *   dbeta[j]  = round_M(sum_r dy)
+ *   dbias[j]  = round_T(sum_r of dx before its rounding)
+ *
+ *   dy           T, (rows, hidden): gradient of output.
+ *   s            T, (rows, hidden): input_skip_bias_sum of the forward call, or
+ *                its input where it had no skip.
+ *   mean, inv_std_var  float32, (rows): of the forward call.
+ *   gamma        M, (hidden); M is T or B200NORM_F32.
+ *   ds           T, (rows, hidden): the gradient that reaches S by other paths
+ *                (the residual stream's own), or NULL.
+ *   dx           T: the gradient of S, which is that of input and of skip.
+ *   dgamma, dbeta  M, (hidden).   dbias  T, (hidden).
+ *   Any of dx, dgamma, dbeta and dbias may be NULL when not wanted.
+ *   workspace    at least b200norm_skip_layer_grad_workspace_size() bytes,
+ *                256-byte aligned; its contents before the call do not matter.
+ *                Calls that share one must not overlap on the device.
+ *
+ * Sums over rows are binary32, in a fixed order (equal calls give equal bits).
+ * rows == 0 stores zeros in dgamma, dbeta and dbias.
+ */
+B200NORM_API size_t b200norm_skip_layer_grad_workspace_size(int64_t rows, int64_t hidden);
+
+B200NORM_API b200norm_status b200norm_skip_layer_grad(
+    const void* dy, const void* s, const float* mean, const float* inv_std_var, const void* gamma,
+    const void* ds, void* dx, void* dgamma, void* dbeta, void* dbias, int64_t rows,
+    int64_t hidden, b200norm_dtype T, b200norm_dtype M, void* workspace, size_t workspace_bytes,
+    b200norm_stream_t stream);
+
+/*
+ * The linear operator:
+ *
+ *   z[r, o] = sum_i x[r, i] * weight[o, i] + bias[o]
+ *   y[r, o] = round_T(act(z[r, o]) + residual[r, o])
+ *
+ *   x          T, (rows, in_features).
+ *   weight     T, (out_features, in_features).
+ *   bias       T, (out_features), or NULL.
+ *   residual   T, (rows, out_features), or NULL.
+ *   y          T, (rows, out_features).
+ *   z          T, (rows, out_features): receives round_T(z) for
+ *              b200norm_linear_grad; NULL when not requested.  y is formed from
+ *              the unrounded z, so requesting z does not change it.
+ *   activation 0 none, 1 SiLU (z / (1 + e^-z)), 2 GELU (z times the normal
+ *              distribution function), 3 GELU in its tanh form
+ *              (z / 2 * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3)))),
+ *              4 ReLU.
+ *   workspace  at least b200norm_linear_workspace_size() bytes, 256-byte
+ *              aligned (NULL where that is 0); its contents before the call do
+ *              not matter.  Calls that share one must not overlap on the device.
+ *
+ * Sums are binary32.  rows == 0 is a no-op; in_features and out_features must
+ * be in [1, 2^20].
+ */
+B200NORM_API size_t b200norm_linear_workspace_size(int64_t rows, int64_t in_features,
+                                                   int64_t out_features, b200norm_dtype T,
+                                                   int aligned16);
+
+B200NORM_API b200norm_status b200norm_linear(
+    const void* x, const void* weight, const void* bias, const void* residual, void* y, void* z,
+    int64_t rows, int64_t in_features, int64_t out_features, b200norm_dtype T, int activation,
+    void* workspace, size_t workspace_bytes, b200norm_stream_t stream);
+
+/*
+ * Gradients of b200norm_linear (that of residual is dy itself):
+ *
+ *   dz[r, o] = dy[r, o] * act'(z[r, o])
+ *   dx[r, i] = round_T(sum_o round_T(dz[r, o]) * weight[o, i])
+ *   dw[o, i] = round_T(sum_r round_T(dz[r, o]) * x[r, i])
+ *   db[o]    = round_T(sum_r dz[r, o])
+ *
+ *   dy, z      T, (rows, out_features); z of the forward call, NULL (and not
+ *              read) when activation is 0.  The derivative of ReLU at 0 is 0.
+ *   x, weight  as in the forward call; x may be NULL without dw, weight
+ *              without dx.
+ *   dx, dw, db T, of x's, weight's and bias's shapes; any may be NULL when not
+ *              wanted.
+ *   workspace  at least b200norm_linear_grad_workspace_size() bytes, as above.
+ *
+ * Sums are binary32, in a fixed order.  rows == 0 stores zeros in dw and db.
+ */
+B200NORM_API size_t b200norm_linear_grad_workspace_size(int64_t rows, int64_t in_features,
+                                                        int64_t out_features, b200norm_dtype T,
+                                                        int activation, int aligned16);
+
+B200NORM_API b200norm_status b200norm_linear_grad(
+    const void* dy, const void* x, const void* weight, const void* z, void* dx, void* dw, void* db,
+    int64_t rows, int64_t in_features, int64_t out_features, b200norm_dtype T, int activation,
+    void* workspace, size_t workspace_bytes, b200norm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,16 +14,28 @@ describe them):
   skip_rms_stats  the same, plus the per-row mean / inv_std_var outputs
   gated_rms       com.microsoft.GatedRMSNorm
   skip_group      com.microsoft.SkipGroupNorm
+
+and the operators that stand beside them on a residual stream, in serving and in
+training (gradients are calls of their own, not autograd functions):
+
+  skip_layer        layer normalization with the residual add fused in
+  skip_layer_stats  the same, plus the per-row mean / inv_std_var outputs
+  skip_layer_grad   its gradients
+  linear            act(x W^T + b) + residual
+  linear_grad       its gradients
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
 
 import torch
 
-__all__ = ["skip_rms", "skip_rms_stats", "gated_rms", "skip_group", "workspace_size",
+__all__ = ["skip_rms", "skip_rms_stats", "gated_rms", "skip_group", "skip_layer",
+           "skip_layer_stats", "skip_layer_grad", "linear", "linear_grad", "ACTIVATIONS",
+           "workspace_size",
            "workspace_init", "workspace_status", "noalloc_status", "rows_status", "library",
            "library_path", "B200NormError", "SSLN_EPS_DEFAULT"]
 
@@ -82,6 +94,13 @@ def library() -> ctypes.CDLL:
             "b200norm_workspace_init": ([vp, sz, vp], i32),
             "b200norm_workspace_status": ([vp, vp], i32),
             "b200norm_rows_status": ([vp], i32),
+            "b200norm_skip_layer": ([vp] * 9 + [i64, i64, i32, i32, f32, vp], i32),
+            "b200norm_skip_layer_grad_workspace_size": ([i64, i64], sz),
+            "b200norm_skip_layer_grad": ([vp] * 10 + [i64, i64, i32, i32, vp, sz, vp], i32),
+            "b200norm_linear_workspace_size": ([i64, i64, i64, i32, i32], sz),
+            "b200norm_linear": ([vp] * 6 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
+            "b200norm_linear_grad_workspace_size": ([i64, i64, i64, i32, i32, i32], sz),
+            "b200norm_linear_grad": ([vp] * 7 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
             "b200norm_testing_barrier_timeout": ([vp, sz, ctypes.c_uint64, vp], i32),
             "b200norm_testing_noalloc_barrier_timeout": ([ctypes.c_uint64, vp], i32),
             "b200norm_testing_force": ([i32, i32], i32),
@@ -319,3 +338,248 @@ def skip_group(x, skip, gamma, beta, bias=None, *, groups, activation, epsilon=1
         _ptr(ssum), N, C, H, W, _DTYPES[dt], _DTYPES[gamma.dtype], int(groups), float(epsilon),
         int(activation), cl, _ptr(workspace), workspace.numel(), st))
     return out, ssum
+
+
+# ---------------------------------------------------------------------------
+# Layer normalization and the linear operator
+# ---------------------------------------------------------------------------
+
+# Activation codes of linear / linear_grad.
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+
+
+def _on(device, stream, *inputs):
+    """The context to allocate and launch in.  With a stream of the caller's
+    own, outputs and scratch are allocated on it, and the inputs are kept from
+    reuse until it has passed this call."""
+    if stream is not None:
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _scratch(workspace, nbytes, device):
+    """Workspace arguments: the caller's, or a block of the caching allocator
+    that goes back to it, in stream order, when the call returns."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, n
+
+
+def _shaped(name, t, shape, device, dtype):
+    _cuda(name, t, device, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    return t
+
+
+def _new(name, t, shape, device, dtype):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _shaped(name, t, shape, device, dtype)
+
+
+def _vector(name, t, n, device, dtype):
+    _cuda(name, t, device, dtype)
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return t
+
+
+def _weights(name, t, n, x):
+    """gamma / beta: x's type or float32."""
+    _cuda(name, t, x.device)
+    if t.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"{name} must be {x.dtype} or torch.float32 (got {t.dtype})")
+    return _vector(name, t, n, x.device, t.dtype)
+
+
+def _rows(x, width):
+    if x.dim() < 1 or x.shape[-1] != width or width < 1:
+        raise ValueError("the last axis does not fit, or is empty")
+    return x.numel() // width
+
+
+def _skip_layer(input, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats, stream):
+    x = _cuda("input", input)
+    dev, dt = x.device, x.dtype
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("input needs a last axis of at least one element")
+    hidden = x.shape[-1]
+    rows = x.numel() // hidden
+    _weights("gamma", gamma, hidden, x)
+    if beta is not None:
+        _vector("beta", beta, hidden, dev, gamma.dtype)
+    if skip is not None:
+        _shaped("skip", skip, x.shape, dev, dt)
+    elif bias is not None or sum_out is not None:
+        raise ValueError("bias and sum_out need a skip (S is the input without one)")
+    if bias is not None:
+        _vector("bias", bias, hidden, dev, dt)
+    lib = library()
+    with _on(dev, stream, x, skip, gamma, beta, bias):
+        y = _new("output", output, x.shape, dev, dt)
+        s = None
+        if skip is not None and (want_sum or sum_out is not None):
+            s = _new("input_skip_bias_sum", sum_out, x.shape, dev, dt)
+        mean = inv = None
+        if stats:
+            shape = tuple(x.shape[:-1]) + (1,)
+            mean = torch.empty(shape, dtype=torch.float32, device=dev)
+            inv = torch.empty(shape, dtype=torch.float32, device=dev)
+        _check(lib.b200norm_skip_layer(_ptr(x), _ptr(skip), _ptr(gamma), _ptr(beta), _ptr(bias),
+                                       _ptr(y), _ptr(s), _ptr(mean), _ptr(inv), rows, hidden,
+                                       _DTYPES[dt], _DTYPES[gamma.dtype], float(epsilon),
+                                       _stream(dev, stream)))
+    if skip is None and want_sum:
+        s = x
+    return y, s, mean, inv
+
+
+def skip_layer(input, skip, gamma, beta=None, bias=None, *, epsilon=1e-5, want_sum=True,
+               output=None, sum_out=None, stream=None):
+    """Layer normalization of ``S = (input + skip) + bias`` over the last axis,
+    times ``gamma`` plus ``beta`` (both of ``input``'s type or both float32).
+
+    ``skip=None`` normalizes ``input`` itself.  Returns ``(output, S)``; ``S`` is
+    ``None`` unless ``want_sum`` (default True) or ``sum_out`` is given, and is
+    ``input`` itself without a skip.
+    """
+    return _skip_layer(input, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, False,
+                       stream)[:2]
+
+
+def skip_layer_stats(input, skip, gamma, beta=None, bias=None, *, epsilon=1e-5, want_sum=True,
+                     output=None, sum_out=None, stream=None):
+    """As :func:`skip_layer`, also returning the float32 ``mean`` and
+    ``inv_std_var`` of shape ``input.shape[:-1] + (1,)`` that
+    :func:`skip_layer_grad` takes."""
+    return _skip_layer(input, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, True,
+                       stream)
+
+
+def skip_layer_grad(dy, s, mean, inv_std_var, gamma, *, ds=None, want_input=True,
+                    want_gamma=True, want_beta=True, want_bias=False, dx=None, dgamma=None,
+                    dbeta=None, dbias=None, workspace=None, stream=None):
+    """Gradients of :func:`skip_layer`: ``(dx, dgamma, dbeta, dbias)``.
+
+    ``s``, ``mean`` and ``inv_std_var`` are the forward call's; ``ds`` is the
+    gradient that reaches S by other paths.  ``dx`` is the gradient of S, which
+    is that of both ``input`` and ``skip``.  An output that is not wanted is
+    ``None``; one that is given is wanted.
+    """
+    dy = _cuda("dy", dy)
+    dev, dt = dy.device, dy.dtype
+    if dy.dim() < 1 or dy.shape[-1] < 1:
+        raise ValueError("dy needs a last axis of at least one element")
+    hidden = dy.shape[-1]
+    rows = dy.numel() // hidden
+    _shaped("s", s, dy.shape, dev, dt)
+    _weights("gamma", gamma, hidden, dy)
+    _vector("mean", mean, rows, dev, torch.float32)
+    _vector("inv_std_var", inv_std_var, rows, dev, torch.float32)
+    if ds is not None:
+        _shaped("ds", ds, dy.shape, dev, dt)
+    lib = library()
+    with _on(dev, stream, dy, s, mean, inv_std_var, gamma, ds):
+        if want_input or dx is not None:
+            dx = _new("dx", dx, dy.shape, dev, dt)
+        if want_gamma or dgamma is not None:
+            dgamma = _new("dgamma", dgamma, gamma.shape, dev, gamma.dtype)
+        if want_beta or dbeta is not None:
+            dbeta = _new("dbeta", dbeta, gamma.shape, dev, gamma.dtype)
+        if want_bias or dbias is not None:
+            dbias = _new("dbias", dbias, gamma.shape, dev, dt)
+        need = lib.b200norm_skip_layer_grad_workspace_size(rows, hidden) if rows else 0
+        ws, n = _scratch(workspace, need, dev)
+        _check(lib.b200norm_skip_layer_grad(
+            _ptr(dy), _ptr(s), _ptr(mean), _ptr(inv_std_var), _ptr(gamma), _ptr(ds), _ptr(dx),
+            _ptr(dgamma), _ptr(dbeta), _ptr(dbias), rows, hidden, _DTYPES[dt],
+            _DTYPES[gamma.dtype], _ptr(ws), n, _stream(dev, stream)))
+    return dx, dgamma, dbeta, dbias
+
+
+def _aligned16(*tensors):
+    return 1 if all(t is None or t.data_ptr() % 16 == 0 for t in tensors) else 0
+
+
+def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y=None, z=None,
+           workspace=None, stream=None):
+    """``act(x @ weight.T + bias) + residual`` over the last axis of ``x``;
+    ``weight`` is (out_features, in_features), ``activation`` a code of
+    ``ACTIVATIONS``.
+
+    Returns ``(y, z)``; ``z``, the value before the activation that
+    :func:`linear_grad` takes, is ``None`` unless ``want_z`` or ``z`` is given.
+    """
+    x = _cuda("x", x)
+    dev, dt = x.device, x.dtype
+    _cuda("weight", weight, dev, dt)
+    if weight.dim() != 2:
+        raise ValueError("weight must be (out_features, in_features)")
+    n_out, n_in = weight.shape
+    rows = _rows(x, n_in)
+    shape = tuple(x.shape[:-1]) + (n_out,)
+    if bias is not None:
+        _vector("bias", bias, n_out, dev, dt)
+    if residual is not None:
+        _shaped("residual", residual, shape, dev, dt)
+    lib = library()
+    with _on(dev, stream, x, weight, bias, residual):
+        y = _new("y", y, shape, dev, dt)
+        if want_z or z is not None:
+            z = _new("z", z, shape, dev, dt)
+        need = lib.b200norm_linear_workspace_size(rows, n_in, n_out, _DTYPES[dt],
+                                                  _aligned16(x, weight))
+        ws, n = _scratch(workspace, need, dev)
+        _check(lib.b200norm_linear(_ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(y),
+                                   _ptr(z), rows, n_in, n_out, _DTYPES[dt], int(activation),
+                                   _ptr(ws), n, _stream(dev, stream)))
+    return y, z
+
+
+def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_weight=True,
+                want_bias=True, dx=None, dw=None, db=None, workspace=None, stream=None):
+    """Gradients of :func:`linear`: ``(dx, dw, db)`` (that of ``residual`` is
+    ``dy``).  ``z`` is the forward call's, needed with an activation.  An output
+    that is not wanted is ``None``; one that is given is wanted.
+    """
+    dy = _cuda("dy", dy)
+    dev, dt = dy.device, dy.dtype
+    _cuda("weight", weight, dev, dt)
+    if weight.dim() != 2:
+        raise ValueError("weight must be (out_features, in_features)")
+    n_out, n_in = weight.shape
+    rows = _rows(dy, n_out)
+    in_shape = tuple(dy.shape[:-1]) + (n_in,)
+    _shaped("x", x, in_shape, dev, dt)
+    if activation:
+        if z is None:
+            raise ValueError("z is needed with an activation")
+        _shaped("z", z, dy.shape, dev, dt)
+    else:
+        z = None
+    lib = library()
+    with _on(dev, stream, dy, x, weight, z):
+        if want_input or dx is not None:
+            dx = _new("dx", dx, in_shape, dev, dt)
+        if want_weight or dw is not None:
+            dw = _new("dw", dw, (n_out, n_in), dev, dt)
+        if want_bias or db is not None:
+            db = _new("db", db, (n_out,), dev, dt)
+        al = _aligned16(dy, x if dw is not None else None, weight if dx is not None else None)
+        need = lib.b200norm_linear_grad_workspace_size(rows, n_in, n_out, _DTYPES[dt],
+                                                       int(activation), al)
+        ws, n = _scratch(workspace, need, dev)
+        _check(lib.b200norm_linear_grad(_ptr(dy), _ptr(x), _ptr(weight), _ptr(z), _ptr(dx),
+                                        _ptr(dw), _ptr(db), rows, n_in, n_out, _DTYPES[dt],
+                                        int(activation), _ptr(ws), n, _stream(dev, stream)))
+    return dx, dw, db

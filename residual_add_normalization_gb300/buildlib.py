@@ -46,6 +46,10 @@ FAMILY_SOURCES = {
              "rows_pipe.cuh", "rows_gated.cu", "rows_ssln_f16.cu", "rows_ssln_f32.cu", "rows_bf16.cu"),
     "group": ("common.cuh", "bulk.cuh", "launch.h", "group_kernels.cuh", "group_norm.cu",
               "group_f32.cu", "group_f16.cu", "group_bf16.cu"),
+    "layer": ("common.cuh", "launch.h", "layer.h", "layer.cuh", "layer_launch.cuh",
+              "layer_f32.cu", "layer_f16.cu", "layer_bf16.cu"),
+    "linear": ("common.cuh", "launch.h", "linear.h", "linear.cuh", "layer_launch.cuh",
+               "linear.cu"),
 }
 
 
@@ -68,7 +72,7 @@ def _inputs_digest(family: str | None = None) -> str:
 
 def source_digest(family: str | None = None) -> str:
     """Digest of the kernel sources and headers (identifies a kernel build), or
-    of one kernel family's sources ("rows", "group")."""
+    of one kernel family's sources ("rows", "group", "layer", "linear")."""
     return _inputs_digest(family)[:16]
 
 

@@ -13,6 +13,8 @@
 #include "b200norm.h"
 #include "b200norm_testing.h"
 #include "launch.h"
+#include "layer.h"
+#include "linear.h"
 
 using namespace b200norm;
 
@@ -167,6 +169,74 @@ b200norm_status skip_rms_impl(const void* input, const void* skip, const void* g
   cudaError_t e = launch_skip_rms(c, plan, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "skip_rms launch");
   return ok();
+}
+
+// A tensor argument of the layer and linear entry points (null: absent).
+struct Tensor {
+  const void* p;
+  size_t bytes, elem;
+  const char* name;
+  bool output;
+};
+
+// Element alignment, and no output over an input or another output.
+b200norm_status check_tensors(const Tensor* t, int n) {
+  for (int i = 0; i < n; ++i)
+    if (t[i].p && !aligned(t[i].p, t[i].elem))
+      return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s is not aligned to its element size",
+                  t[i].name);
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (i != j && t[i].output && (!t[j].output || j > i) &&
+          overlaps({t[i].p, t[i].bytes, t[i].name}, {t[j].p, t[j].bytes, t[j].name}))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", t[i].name, t[j].name);
+  return B200NORM_OK;
+}
+
+bool all_aligned16(const Tensor* t, int n) {
+  for (int i = 0; i < n; ++i)
+    if (t[i].p && !aligned(t[i].p, 16)) return false;
+  return true;
+}
+
+b200norm_status check_workspace(const void* ws, size_t bytes, size_t need, const Tensor* t,
+                                int n) {
+  if (need == 0) return B200NORM_OK;
+  if (!ws || bytes < need)
+    return fail(B200NORM_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu at %p)", need, bytes,
+                ws);
+  if (!aligned(ws, 256)) return fail(B200NORM_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  for (int i = 0; i < n; ++i)
+    if (overlaps({ws, need, "workspace"}, {t[i].p, t[i].bytes, t[i].name}))
+      return fail(B200NORM_ERR_WORKSPACE, "workspace overlaps %s", t[i].name);
+  return B200NORM_OK;
+}
+
+b200norm_status check_layer_shape(int64_t rows, int64_t hidden, b200norm_dtype T,
+                                  b200norm_dtype M) {
+  if (!dtype_ok(T) || (M != T && M != B200NORM_F32))
+    return fail(B200NORM_ERR_UNSUPPORTED, "element types T=%d M=%d not supported", T, M);
+  if (rows < 0) return fail(B200NORM_ERR_INVALID_ARGUMENT, "rows must be >= 0");
+  if (hidden <= 0) return fail(B200NORM_ERR_INVALID_ARGUMENT, "hidden must be > 0");
+  if (hidden > 0x7fffffffLL || rows > kMaxGrid)
+    return fail(B200NORM_ERR_UNSUPPORTED, "hidden or rows exceeds 2^31-1");
+  return B200NORM_OK;
+}
+
+constexpr int64_t kMaxFeatures = int64_t{1} << 20;
+
+b200norm_status check_linear_shape(int64_t rows, int64_t in, int64_t out, b200norm_dtype T,
+                                   int activation) {
+  if (!dtype_ok(T)) return fail(B200NORM_ERR_UNSUPPORTED, "element type %d not supported", T);
+  if (rows < 0 || in <= 0 || out <= 0)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "need rows >= 0, in_features > 0, out_features > 0");
+  if (rows > kMaxGrid || in > kMaxFeatures || out > kMaxFeatures)
+    return fail(B200NORM_ERR_UNSUPPORTED, "rows exceeds 2^31-1, or features 2^20");
+  if (activation < 0 || activation >= kActivations)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "activation must be 0 (none), 1 (SiLU), 2 (GELU), 3 (GELU, tanh) or 4 (ReLU)");
+  return B200NORM_OK;
 }
 
 // Skip shape classification (SkipGroupNorm README, Inputs, skip):
@@ -420,6 +490,150 @@ b200norm_status b200norm_rows_status(b200norm_stream_t stream) {
   if (e == cudaSuccess && v != 0) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "row status read");
   if (v != 0) return fail(static_cast<b200norm_status>(v), "a pipelined row wait gave up");
+  return ok();
+}
+
+// ---- layer normalization and the linear operator -----------------------------
+
+b200norm_status b200norm_skip_layer(const void* input, const void* skip, const void* gamma,
+                                    const void* beta, const void* bias, void* output,
+                                    void* input_skip_bias_sum, float* mean, float* inv_std_var,
+                                    int64_t rows, int64_t hidden, b200norm_dtype T,
+                                    b200norm_dtype M, float epsilon, b200norm_stream_t stream) {
+  if (b200norm_status st = check_layer_shape(rows, hidden, T, M)) return st;
+  if (b200norm_status st = check_eps(epsilon)) return st;
+  if (!skip && (bias || input_skip_bias_sum))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "bias and input_skip_bias_sum need a skip (S is the input without one)");
+  if (rows == 0) return ok();
+  if (!input || !gamma || !output)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "input, gamma and output are required");
+  const size_t es = dtype_size(to_dtype(T)), ms = dtype_size(to_dtype(M));
+  const size_t tb = static_cast<size_t>(rows) * hidden * es, sb = static_cast<size_t>(rows) * 4;
+  const Tensor ts[] = {{input, tb, es, "input", false}, {skip, tb, es, "skip", false},
+                       {gamma, hidden * ms, ms, "gamma", false},
+                       {beta, hidden * ms, ms, "beta", false},
+                       {bias, hidden * es, es, "bias", false},
+                       {output, tb, es, "output", true},
+                       {input_skip_bias_sum, tb, es, "input_skip_bias_sum", true},
+                       {mean, sb, 4, "mean", true}, {inv_std_var, sb, 4, "inv_std_var", true}};
+  if (b200norm_status st = check_tensors(ts, 9)) return st;
+  LayerCall c{input, skip, gamma, beta, bias, output, input_skip_bias_sum, mean, inv_std_var,
+              rows, hidden, to_dtype(T), to_dtype(M), epsilon,
+              hidden % static_cast<int64_t>(16 / es) == 0 && all_aligned16(ts, 7)};
+  cudaError_t e = launch_layer(c, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "skip_layer launch");
+  return ok();
+}
+
+size_t b200norm_skip_layer_grad_workspace_size(int64_t rows, int64_t hidden) {
+  if (rows < 0 || hidden <= 0) return 0;
+  return layer_grad_workspace_bytes(rows, hidden);
+}
+
+b200norm_status b200norm_skip_layer_grad(const void* dy, const void* s, const float* mean,
+                                         const float* inv_std_var, const void* gamma,
+                                         const void* ds, void* dx, void* dgamma, void* dbeta,
+                                         void* dbias, int64_t rows, int64_t hidden,
+                                         b200norm_dtype T, b200norm_dtype M, void* workspace,
+                                         size_t workspace_bytes, b200norm_stream_t stream) {
+  if (b200norm_status st = check_layer_shape(rows, hidden, T, M)) return st;
+  if (!dx && !dgamma && !dbeta && !dbias) return ok();
+  if (rows > 0 && (!dy || !s || !mean || !inv_std_var || !gamma))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "dy, s, mean, inv_std_var and gamma are required");
+  const size_t es = dtype_size(to_dtype(T)), ms = dtype_size(to_dtype(M));
+  const size_t tb = static_cast<size_t>(rows) * hidden * es, sb = static_cast<size_t>(rows) * 4;
+  const Tensor ts[] = {{dy, tb, es, "dy", false}, {s, tb, es, "s", false},
+                       {gamma, hidden * ms, ms, "gamma", false}, {ds, tb, es, "ds", false},
+                       {dx, tb, es, "dx", true}, {dgamma, hidden * ms, ms, "dgamma", true},
+                       {dbeta, hidden * ms, ms, "dbeta", true},
+                       {dbias, hidden * es, es, "dbias", true},
+                       {mean, sb, 4, "mean", false}, {inv_std_var, sb, 4, "inv_std_var", false}};
+  if (b200norm_status st = check_tensors(ts, 10)) return st;
+  const size_t need = rows > 0 ? layer_grad_workspace_bytes(rows, hidden) : 0;
+  if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, ts, 10)) return st;
+  LayerGradCall c{dy, s, mean, inv_std_var, gamma, ds, dx, dgamma, dbeta, dbias, rows, hidden,
+                  to_dtype(T), to_dtype(M), workspace,
+                  hidden % static_cast<int64_t>(16 / es) == 0 && all_aligned16(ts, 5)};
+  cudaError_t e = launch_layer_grad(c, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "skip_layer_grad launch");
+  return ok();
+}
+
+size_t b200norm_linear_workspace_size(int64_t rows, int64_t in_features, int64_t out_features,
+                                      b200norm_dtype T, int aligned16) {
+  if (check_linear_shape(rows, in_features, out_features, T, 0) != B200NORM_OK) return 0;
+  return linear_plan(rows, in_features, out_features, to_dtype(T), aligned16 != 0).bytes;
+}
+
+b200norm_status b200norm_linear(const void* x, const void* weight, const void* bias,
+                                const void* residual, void* y, void* z, int64_t rows,
+                                int64_t in_features, int64_t out_features, b200norm_dtype T,
+                                int activation, void* workspace, size_t workspace_bytes,
+                                b200norm_stream_t stream) {
+  if (b200norm_status st = check_linear_shape(rows, in_features, out_features, T, activation))
+    return st;
+  if (rows == 0) return ok();
+  if (!x || !weight || !y)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "x, weight and y are required");
+  const size_t es = dtype_size(to_dtype(T));
+  const size_t xb = static_cast<size_t>(rows) * in_features * es;
+  const size_t yb = static_cast<size_t>(rows) * out_features * es;
+  const Tensor ts[] = {{x, xb, es, "x", false},
+                       {weight, static_cast<size_t>(out_features) * in_features * es, es,
+                        "weight", false},
+                       {bias, out_features * es, es, "bias", false},
+                       {residual, yb, es, "residual", false}, {y, yb, es, "y", true},
+                       {z, yb, es, "z", true}};
+  if (b200norm_status st = check_tensors(ts, 6)) return st;
+  const LinearPlan plan =
+      linear_plan(rows, in_features, out_features, to_dtype(T), all_aligned16(ts, 2));
+  if (b200norm_status st = check_workspace(workspace, workspace_bytes, plan.bytes, ts, 6))
+    return st;
+  LinearCall c{x, weight, bias, residual, y, z, rows, in_features, out_features, to_dtype(T),
+               activation, workspace};
+  cudaError_t e = launch_linear(c, plan, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "linear launch");
+  return ok();
+}
+
+size_t b200norm_linear_grad_workspace_size(int64_t rows, int64_t in_features,
+                                           int64_t out_features, b200norm_dtype T, int activation,
+                                           int aligned16) {
+  if (check_linear_shape(rows, in_features, out_features, T, activation) != B200NORM_OK) return 0;
+  return linear_grad_plan(rows, in_features, out_features, to_dtype(T), activation,
+                          aligned16 != 0).bytes;
+}
+
+b200norm_status b200norm_linear_grad(const void* dy, const void* x, const void* weight,
+                                     const void* z, void* dx, void* dw, void* db, int64_t rows,
+                                     int64_t in_features, int64_t out_features, b200norm_dtype T,
+                                     int activation, void* workspace, size_t workspace_bytes,
+                                     b200norm_stream_t stream) {
+  if (b200norm_status st = check_linear_shape(rows, in_features, out_features, T, activation))
+    return st;
+  if (!dx && !dw && !db) return ok();
+  if (activation == kActNone) z = nullptr;
+  if (rows > 0 && (!dy || (dw && !x) || (dx && !weight) || (activation != kActNone && !z)))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "dy, x (for dw), weight (for dx) and z (with an activation) are required");
+  const size_t es = dtype_size(to_dtype(T));
+  const size_t xb = static_cast<size_t>(rows) * in_features * es;
+  const size_t yb = static_cast<size_t>(rows) * out_features * es;
+  const size_t wb = static_cast<size_t>(out_features) * in_features * es;
+  const Tensor ts[] = {{dy, yb, es, "dy", false}, {dw ? x : nullptr, xb, es, "x", false},
+                       {dx ? weight : nullptr, wb, es, "weight", false}, {z, yb, es, "z", false},
+                       {dx, xb, es, "dx", true}, {dw, wb, es, "dw", true},
+                       {db, out_features * es, es, "db", true}};
+  if (b200norm_status st = check_tensors(ts, 7)) return st;
+  const LinearGradPlan plan = linear_grad_plan(rows, in_features, out_features, to_dtype(T),
+                                               activation, all_aligned16(ts, 3));
+  const size_t need = rows > 0 ? plan.bytes : 0;
+  if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, ts, 7)) return st;
+  LinearGradCall c{dy, x, weight, z, dx, dw, db, rows, in_features, out_features, to_dtype(T),
+                   activation, workspace};
+  cudaError_t e = launch_linear_grad(c, plan, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "linear_grad launch");
   return ok();
 }
 

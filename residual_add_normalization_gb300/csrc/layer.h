@@ -1,0 +1,72 @@
+// layer.h -- host-side interface between the C ABI and the layer-normalization
+// kernels (layer.cuh).  Each function enqueues on `stream` and returns the CUDA
+// error of the launch.
+#pragma once
+
+#include "launch.h"
+
+namespace b200norm {
+
+struct LayerCall {
+  const void* x;
+  const void* skip;   // null: S = x
+  const void* gamma;
+  const void* beta;   // null: none
+  const void* bias;   // null: none
+  void* y;
+  void* s;            // null: not stored
+  float* mean;        // null: not stored
+  float* inv_std;     // null: not stored
+  int64_t rows;
+  int64_t hidden;
+  DType t, m;
+  float eps;
+  bool vec;           // every row and pointer is whole 16-byte vectors
+};
+
+struct LayerGradCall {
+  const void* dy;
+  const void* s;
+  const float* mean;
+  const float* inv_std;
+  const void* gamma;
+  const void* ds;     // null: nothing arrives through S
+  void* dx;           // null: not wanted (as the three below)
+  void* dgamma;
+  void* dbeta;
+  void* dbias;
+  int64_t rows;
+  int64_t hidden;
+  DType t, m;
+  void* workspace;    // layer_grad_workspace_bytes(rows, hidden)
+  bool vec;
+};
+
+// Partial column sums a gradient call keeps: one set of (dgamma, dbeta, dbias)
+// rows per part, later added in part order (no atomics, so equal calls give
+// equal bits).  At most two parts per SM, at least kLayerRowsPerPart rows in
+// each, and fewer for very long rows, whose columns alone fill the GPU.
+constexpr int kLayerMaxParts = 304;
+constexpr int kLayerRowsPerPart = 4;
+inline int layer_grad_parts(int64_t rows, int64_t hidden) {
+  int64_t p = (rows + kLayerRowsPerPart - 1) / kLayerRowsPerPart;
+  const int64_t most = (int64_t{1} << 24) / hidden;
+  if (p > most) p = most;
+  if (p > kLayerMaxParts) p = kLayerMaxParts;
+  return static_cast<int>(p < 1 ? 1 : p);
+}
+inline size_t layer_grad_workspace_bytes(int64_t rows, int64_t hidden) {
+  const size_t stats = (static_cast<size_t>(rows) * 8 + 255) / 256 * 256;
+  return stats + static_cast<size_t>(layer_grad_parts(rows, hidden)) * 3 * hidden * 4;
+}
+
+cudaError_t launch_layer(const LayerCall& c, cudaStream_t stream);
+cudaError_t launch_layer_grad(const LayerGradCall& c, cudaStream_t stream);
+
+// One (T, M) pair each, in its own translation unit.
+template <typename T, typename M>
+cudaError_t launch_layer_tm(const LayerCall& c, cudaStream_t stream);
+template <typename T, typename M>
+cudaError_t launch_layer_grad_tm(const LayerGradCall& c, cudaStream_t stream);
+
+}  // namespace b200norm

@@ -1,0 +1,103 @@
+// linear.h -- host-side interface between the C ABI and the kernels of the
+// linear operator (y = act(x W^T + b) + residual) and its gradients.
+#pragma once
+
+#include "launch.h"
+
+namespace b200norm {
+
+// Activation codes of the ABI.
+enum Activation { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3, kActRelu = 4 };
+constexpr int kActivations = 5;
+
+// One matrix product C[m, n] = sum_k A[m, k] * B[n, k].  An operand is stored
+// with k contiguous (element (i, k) at p[i * ld + k]) or with i contiguous
+// (p[k * ld + i]).
+struct Operand {
+  const void* p;
+  int64_t ld;
+  bool k_contiguous;
+};
+
+// What happens to C before it is stored (dense, row-major, N columns):
+// z = C + bias[n]; y = act(z) + residual[m, n].
+struct Epilogue {
+  const void* bias;      // null: none
+  const void* residual;  // null: none
+  void* y;
+  void* z;               // null: not stored
+  int act;
+};
+
+struct Product {
+  Operand a, b;
+  int64_t M, N, K;
+  Epilogue epi;
+  DType t;
+};
+
+cudaError_t launch_product(const Product& p, cudaStream_t stream);
+
+// dz = round_T(dy * act'(z)) with rows `ldz` apart (null: not stored), and the
+// column sums of dy * act'(z) (null: not wanted) through `part`.
+struct LinearDzCall {
+  const void* dy;
+  const void* z;       // null when act is kActNone
+  void* dz;
+  int64_t ldz;
+  void* db;
+  float* part;         // [linear_db_parts(rows)][out]
+  int64_t rows, out;
+  int act;
+  DType t;
+};
+// Parts of the column sums: at least 16 rows in each, at most 64 parts.
+inline int linear_db_parts(int64_t rows) {
+  const int64_t p = (rows + 15) / 16;
+  return static_cast<int>(p < 1 ? 1 : p > 64 ? 64 : p);
+}
+cudaError_t launch_linear_dz(const LinearDzCall& c, cudaStream_t stream);
+
+struct LinearCall {
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* z;
+  int64_t rows, in, out;
+  DType t;
+  int act;
+  void* workspace;
+};
+
+struct LinearGradCall {
+  const void* dy;
+  const void* x;
+  const void* w;
+  const void* z;
+  void* dx;
+  void* dw;
+  void* db;
+  int64_t rows, in, out;
+  DType t;
+  int act;
+  void* workspace;
+};
+
+// What a call keeps in its workspace: offsets, and the bytes in all.
+struct LinearPlan {
+  size_t bytes;
+};
+struct LinearGradPlan {
+  size_t dz, part, bytes;  // dz: rows x out elements (with an activation)
+};
+// aligned16: x and weight (and dy) start on 16-byte boundaries.
+LinearPlan linear_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);
+LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, int act,
+                                bool aligned16);
+cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStream_t stream);
+cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& plan,
+                               cudaStream_t stream);
+
+}  // namespace b200norm

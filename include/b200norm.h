@@ -399,6 +399,17 @@ B200NORM_API b200norm_status b200norm_linear_grad(
     int64_t rows, int64_t in_features, int64_t out_features, b200norm_dtype T, int activation,
     void* workspace, size_t workspace_bytes, b200norm_stream_t stream);
 
+/* Synchronise `stream`, then read the device-side record of the linear
+ * operator's kernels on the current device.  With 16-bit types their roles wait
+ * on one another through shared memory; the waits are bounded (a second and
+ * more for long sums), and one that gives up records
+ * B200NORM_ERR_DEVICE_TIMEOUT in a per-device word and ends early (that call's
+ * outputs are then undefined).  Returns B200NORM_OK, or
+ * B200NORM_ERR_DEVICE_TIMEOUT (and clears the record) if any such launch on the
+ * device gave up since the last call; B200NORM_ERR_CUDA if the read failed.  No
+ * correct launch records anything. */
+B200NORM_API b200norm_status b200norm_linear_status(b200norm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

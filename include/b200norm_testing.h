@@ -60,6 +60,14 @@ B200NORM_API b200norm_status b200norm_testing_force(int row_mode, int group_rout
  * falls back to the walking schedule. */
 B200NORM_API b200norm_status b200norm_testing_force_split(int csize, int nv);
 
+/* Force the tiling of the linear operator's tensor-core products on the calling
+ * thread: cg CTAs per tile (1 or 2), bn columns per tile, K in `splits` parts
+ * (1, 2, 4 or 8), swap 1 for the form whose lanes hold the result's columns.
+ * (0, 0, 0, 0) restores the automatic choice.  A later call that the tiling has
+ * no kernel for returns B200NORM_ERR_UNSUPPORTED; float32 calls and those whose
+ * operands are not 16-byte aligned do not take one and ignore it. */
+B200NORM_API b200norm_status b200norm_testing_force_linear(int cg, int bn, int splits, int swap);
+
 /* Switch programmatic dependent launch off (0) or on (1, the default) for
  * every later launch of the library, on all threads.  With it on, a kernel
  * may be scheduled while the preceding grid on its stream drains and waits

@@ -34,7 +34,8 @@ import threading
 import torch
 
 __all__ = ["skip_rms", "skip_rms_stats", "gated_rms", "skip_group", "skip_layer",
-           "skip_layer_stats", "skip_layer_grad", "linear", "linear_grad", "ACTIVATIONS",
+           "skip_layer_stats", "skip_layer_grad", "linear", "linear_grad", "linear_status",
+           "ACTIVATIONS",
            "workspace_size",
            "workspace_init", "workspace_status", "noalloc_status", "rows_status", "library",
            "library_path", "B200NormError", "SSLN_EPS_DEFAULT"]
@@ -99,6 +100,7 @@ def library() -> ctypes.CDLL:
             "b200norm_skip_layer_grad": ([vp] * 10 + [i64, i64, i32, i32, vp, sz, vp], i32),
             "b200norm_linear_workspace_size": ([i64, i64, i64, i32, i32], sz),
             "b200norm_linear": ([vp] * 6 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
+            "b200norm_linear_status": ([vp], i32),
             "b200norm_linear_grad_workspace_size": ([i64, i64, i64, i32, i32, i32], sz),
             "b200norm_linear_grad": ([vp] * 7 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
             "b200norm_testing_barrier_timeout": ([vp, sz, ctypes.c_uint64, vp], i32),
@@ -106,6 +108,7 @@ def library() -> ctypes.CDLL:
             "b200norm_testing_force": ([i32, i32], i32),
             "b200norm_testing_force_split": ([i32, i32], i32),
             "b200norm_testing_set_pdl": ([i32], i32),
+            "b200norm_testing_force_linear": ([i32] * 4, i32),
             "b200norm_testing_pipe_stall": ([i32, ctypes.c_uint64], i32),
             "b200norm_testing_plan_rows": ([i64, i64, i32, i32, ctypes.POINTER(ctypes.c_int64)],
                                            i32),
@@ -583,3 +586,12 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
                                         _ptr(dw), _ptr(db), rows, n_in, n_out, _DTYPES[dt],
                                         int(activation), _ptr(ws), n, _stream(dev, stream)))
     return dx, dw, db
+
+
+def linear_status(stream=None, device=None):
+    """Synchronizes ``stream`` and raises B200NormError if a bounded wait of a
+    ``linear`` / ``linear_grad`` kernel on the device gave up since the last
+    call; the record is then cleared."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    with torch.cuda.device(dev):
+        _check(library().b200norm_linear_status(_stream(dev, stream)))

@@ -25,6 +25,7 @@ thread_local int g_force_row_mode = 0;
 thread_local int g_force_group_route = 0;
 thread_local int g_force_csize = 0;  // forced CTA / cluster row split (0: automatic)
 thread_local int g_force_nv = 0;
+thread_local MmaPlan g_force_linear = {0, 0, 0, false};
 
 b200norm_status fail(b200norm_status st, const char* fmt, ...) {
   char buf[512];
@@ -591,8 +592,10 @@ b200norm_status b200norm_linear(const void* x, const void* weight, const void* b
   if (b200norm_status st = check_workspace(workspace, workspace_bytes, plan.bytes, ts, 6))
     return st;
   LinearCall c{x, weight, bias, residual, y, z, rows, in_features, out_features, to_dtype(T),
-               activation, workspace};
+               activation, workspace, g_force_linear};
   cudaError_t e = launch_linear(c, plan, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported && g_force_linear.cg)
+    return fail(B200NORM_ERR_UNSUPPORTED, "forced tiling cannot take this call");
   if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   return ok();
 }
@@ -631,13 +634,41 @@ b200norm_status b200norm_linear_grad(const void* dy, const void* x, const void* 
   const size_t need = rows > 0 ? plan.bytes : 0;
   if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, ts, 7)) return st;
   LinearGradCall c{dy, x, weight, z, dx, dw, db, rows, in_features, out_features, to_dtype(T),
-                   activation, workspace};
+                   activation, workspace, g_force_linear};
   cudaError_t e = launch_linear_grad(c, plan, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported && g_force_linear.cg)
+    return fail(B200NORM_ERR_UNSUPPORTED, "forced tiling cannot take this call");
   if (e != cudaSuccess) return cuda_fail(e, "linear_grad launch");
   return ok();
 }
 
+b200norm_status b200norm_linear_status(b200norm_stream_t stream) {
+  unsigned* words = linear_status_words();
+  if (!words) return fail(B200NORM_ERR_CUDA, "linear status words not available on this device");
+  unsigned v[2] = {0, 0};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(v, words, sizeof(v), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && v[0] != 0) e = cudaMemsetAsync(words, 0, sizeof(v), st);
+  if (e == cudaSuccess && v[0] != 0) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_fail(e, "linear status read");
+  if (v[0] != 0) return fail(static_cast<b200norm_status>(v[0]), "device wait %u gave up", v[1]);
+  return ok();
+}
+
 // ---- testing hooks ---------------------------------------------------------
+
+b200norm_status b200norm_testing_force_linear(int cg, int bn, int splits, int swap) {
+  const bool off = cg == 0 && bn == 0 && splits == 0 && swap == 0;
+  const bool some = (cg == 1 || cg == 2) && (bn == 16 || bn == 32 || bn == 64 || bn == 128 ||
+                                              bn == 256) &&
+                    (splits == 1 || splits == 2 || splits == 4 || splits == 8) &&
+                    (swap == 0 || swap == 1);
+  if (!off && !some) return fail(B200NORM_ERR_INVALID_ARGUMENT, "no such tiling");
+  g_force_linear = {cg, bn, splits, swap == 1};
+  return ok();
+}
 
 b200norm_status b200norm_testing_barrier_timeout(void* workspace, size_t workspace_bytes,
                                                  uint64_t limit_ns, b200norm_stream_t stream) {

@@ -30,6 +30,8 @@ cudaError_t launch_dz(const LinearDzCall& c, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream) {
+  if (mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0)
+    return launch_mma(p, stream);
   switch (p.t) {
     case DType::F32: return launch_plain<float>(p, stream);
     case DType::F16: return launch_plain<__half>(p, stream);
@@ -61,7 +63,7 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t, int64_t out, DType t, int
 
 cudaError_t launch_linear(const LinearCall& c, const LinearPlan&, cudaStream_t stream) {
   const Product p{{c.x, c.in, true}, {c.w, c.in, true}, c.rows, c.out, c.in,
-                  {c.bias, c.residual, c.y, c.z, c.act}, c.t};
+                  {c.bias, c.residual, c.y, c.z, c.act}, c.t, c.forced};
   return launch_product(p, stream);
 }
 
@@ -80,13 +82,13 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& pl
   const void* g = act ? dz : c.dy;
   if (c.dx && c.rows > 0) {
     const Product p{{g, c.out, true}, {c.w, c.in, false}, c.rows, c.in, c.out,
-                    {nullptr, nullptr, c.dx, nullptr, kActNone}, c.t};
+                    {nullptr, nullptr, c.dx, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);
     if (e != cudaSuccess) return e;
   }
   if (c.dw) {
     const Product p{{g, c.out, false}, {c.x, c.in, false}, c.out, c.in, c.rows,
-                    {nullptr, nullptr, c.dw, nullptr, kActNone}, c.t};
+                    {nullptr, nullptr, c.dw, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);
   }
   return e;

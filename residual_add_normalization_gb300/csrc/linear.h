@@ -29,14 +29,42 @@ struct Epilogue {
   int act;
 };
 
+// How a product is tiled: CTAs per tile (cg), columns per tile (bn), parts of K
+// (a cluster each), and whether the result's columns fill the lanes (swap).
+struct MmaPlan {
+  int cg, bn, splits;
+  bool swap;
+};
+
 struct Product {
   Operand a, b;
   int64_t M, N, K;
   Epilogue epi;
   DType t;
+  MmaPlan forced;  // by a test (cg 0: automatic)
 };
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream);
+
+// The tensor-core kernels (16-bit types) -----------------------------------------
+
+// What they need of an operand: 16-byte aligned rows at a 16-byte aligned place.
+inline bool mma_operand_ok(const Operand& o, DType t) {
+  return t != DType::F32 && o.ld % 8 == 0 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0;
+}
+
+MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, int sms);
+cudaError_t launch_mma(const Product& p, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_mma_t(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
+                         cudaStream_t stream);
+
+// Whether a forced plan has a kernel for the product.
+bool mma_plan_ok(const MmaPlan& plan, int64_t M, int64_t K, bool a_kc, bool b_kc);
+
+// Two words per device: a b200norm_status recorded by a wait that gave up, and
+// its site (nullptr if they cannot be resolved).
+unsigned* linear_status_words();
 
 // dz = round_T(dy * act'(z)) with rows `ldz` apart (null: not stored), and the
 // column sums of dy * act'(z) (null: not wanted) through `part`.
@@ -69,6 +97,7 @@ struct LinearCall {
   DType t;
   int act;
   void* workspace;
+  MmaPlan forced;
 };
 
 struct LinearGradCall {
@@ -83,6 +112,7 @@ struct LinearGradCall {
   DType t;
   int act;
   void* workspace;
+  MmaPlan forced;
 };
 
 // What a call keeps in its workspace: offsets, and the bytes in all.

@@ -289,7 +289,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b, const MmaArgs g) {
   using S = MmaShape<CG, BN>;
   constexpr int kStages = S::kStages;
-  constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
+  constexpr bool kBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   extern __shared__ unsigned char raw[];
   // the swizzle counts from 1024-byte boundaries
   unsigned char* ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
@@ -379,13 +379,12 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           }
         }
       }
-      // The copies still in flight land before this CTA's shared memory goes:
-      // without a timeout the matrix instructions have waited for all of them.
-      if (!alive) {
-        const int from = it > kStages ? it - kStages : 0;
-        if (leader)
-          for (int i = from; i < it; ++i)
-            mbar_wait(&full[i % kStages], (i / kStages) & 1, g.limit_ns);
+      // Nothing may still be on its way to this CTA's shared memory when it
+      // ends: not the last commits' arrivals, and after a timeout no copy.
+      const int from = it > kStages ? it - kStages : 0;
+      for (int i = from; i < it; ++i) {
+        if (alive) mbar_wait(&empty[i % kStages], (i / kStages) & 1, g.limit_ns);
+        else if (leader) mbar_wait(&full[i % kStages], (i / kStages) & 1, g.limit_ns);
       }
     }
   } else if (warp == 1) {

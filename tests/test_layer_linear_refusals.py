@@ -145,6 +145,14 @@ def test_linear_workspace_sizes(lib):
     assert lib.b200norm_linear_grad_workspace_size(64, 128, 256, BF16, 9, 1) == 0
 
 
+def test_force_hook_refusals(lib):
+    f = lib.b200norm_testing_force_linear
+    for bad in ((3, 64, 1, 0), (1, 48, 1, 0), (1, 64, 3, 0), (1, 64, 1, 2), (0, 64, 1, 0)):
+        assert f(*bad) == INVALID, bad
+    assert f(1, 64, 8, 0) == OK
+    assert f(0, 0, 0, 0) == OK
+
+
 def test_binding_refuses_cpu_tensors():
     x, w = torch.zeros(4, 8), torch.ones(8)
     with pytest.raises(ValueError, match="CUDA"):

@@ -19,6 +19,13 @@ SHAPES = [(1, 1, 1), (1, 64, 64), (1, 4096, 520), (2, 16, 24), (3, 5, 7), (5, 72
           (200, 2048, 320), (256, 320, 512), (257, 520, 264), (300, 8200, 64), (513, 72, 1283)]
 
 
+@pytest.fixture(autouse=True)
+def _no_wait_gave_up():
+    yield
+    b2.library().b200norm_testing_force_linear(0, 0, 0, 0)
+    b2.linear_status()
+
+
 def make(rows, n_in, n_out, t, seed):
     g = torch.Generator().manual_seed(seed)
 
@@ -249,3 +256,38 @@ def test_writes_exactly_its_outputs(shape, shift, t):
     for raw, view, a, n in blocks:
         assert bool((raw[:a] == 0xFF).all()) and bool((raw[a + n:] == 0xFF).all())
         assert not bool(torch.isnan(view.float()).any())
+
+
+TILINGS = [(2, 256, 1), (1, 128, 1), (1, 128, 2), (1, 128, 8), (1, 64, 1), (1, 64, 4), (1, 64, 8)]
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("tiling", TILINGS)
+@pytest.mark.parametrize("shape", [(1, 512, 8), (300, 520, 264), (520, 1032, 784),
+                                   (257, 4104, 129)])
+def test_every_tiling(shape, tiling, t):
+    """The tilings that the sizes of the other tests may not take, at sizes with
+    ragged edges; (520, 1032, 784) has more tiles than one."""
+    d = make(*shape, t, 11)
+    assert b2.library().b200norm_testing_force_linear(*tiling, 0) == 0
+    check_forward(d, "silu", True, True, True)
+    if shape[0] >= 512 and shape[2] % 8 == 0:  # long enough sums of every product
+        check_grad(d, "gelu_tanh")
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("bn,splits", [(16, 1), (16, 8), (32, 2), (32, 8), (64, 1), (64, 4)])
+@pytest.mark.parametrize("rows", [1, 16])
+def test_every_tiling_for_few_rows(rows, bn, splits, t):
+    d = make(rows, 776, 1000, t, 12)
+    assert b2.library().b200norm_testing_force_linear(1, bn, splits, 1) == 0
+    check_forward(d, "gelu", True, True, True)
+
+
+def test_more_tiles_than_ctas():
+    """Several tiles per CTA pair: both buffers of sums, in turn."""
+    d = make(2600, 136, 4360, "bf16", 13)
+    assert b2.library().b200norm_testing_force_linear(2, 256, 1, 0) == 0
+    check_forward(d, "none", True, False, False)
+    assert b2.library().b200norm_testing_force_linear(1, 64, 1, 0) == 0
+    check_forward(d, "none", True, False, False)

@@ -160,8 +160,9 @@ B200NORM_API b200norm_status b200norm_gated_rms(const void* x, const void* gate,
 
 /* Synchronise `stream`, then read the device-side record of the pipelined row
  * schedule on the current device.  SkipSimplifiedLayerNormalization and
- * GatedRMSNorm calls with short rows (at most 32 16-byte vectors) may run a
- * kernel that streams its inputs through shared memory; its waits on copy
+ * GatedRMSNorm calls with short rows (at most 32 16-byte vectors), and
+ * b200norm_skip_layer_grad calls, may run a kernel that streams its inputs
+ * through shared memory; its waits on copy
  * completion are bounded (about one second), and one that gives up records
  * B200NORM_ERR_DEVICE_TIMEOUT in a per-device word and returns early (that
  * call's outputs are then undefined).  Returns B200NORM_OK, or

@@ -26,7 +26,6 @@ training (gradients are calls of their own, not autograd functions):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -350,48 +349,22 @@ def skip_group(x, skip, gamma, beta, bias=None, *, groups, activation, epsilon=1
 # Activation codes of linear / linear_grad.
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 
-
-def _on(device, stream, *inputs):
-    """The context to allocate and launch in.  With a stream of the caller's
-    own, outputs and scratch are allocated on it, and the inputs are kept from
-    reuse until it has passed this call."""
-    if stream is not None:
-        for t in inputs:
-            if t is not None:
-                t.record_stream(stream)
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+# A call of one token is over in a few microseconds on the GPU, so these
+# bindings keep the host's part short: pointers pass as plain integers, a tensor
+# is checked with one expression, and only a failed check asks what was wrong.
 
 
-def _scratch(workspace, nbytes, device):
-    """Workspace arguments: the caller's, or a block of the caching allocator
-    that goes back to it, in stream order, when the call returns."""
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    else:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return workspace, n
-
-
-def _shaped(name, t, shape, device, dtype):
+def _is(name, t, shape, device, dtype):
+    """``t``, contiguous on ``device`` with that type and shape (None: any)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return t
     _cuda(name, t, device, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    return t
-
-
-def _new(name, t, shape, device, dtype):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _shaped(name, t, shape, device, dtype)
+    raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
 
 
 def _vector(name, t, n, device, dtype):
-    _cuda(name, t, device, dtype)
+    _is(name, t, None, device, dtype)
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements")
     return t
@@ -399,49 +372,98 @@ def _vector(name, t, n, device, dtype):
 
 def _weights(name, t, n, x):
     """gamma / beta: x's type or float32."""
-    _cuda(name, t, x.device)
-    if t.dtype not in (x.dtype, torch.float32):
+    if not isinstance(t, torch.Tensor) or t.dtype not in (x.dtype, torch.float32):
+        _cuda(name, t, x.device)
         raise TypeError(f"{name} must be {x.dtype} or torch.float32 (got {t.dtype})")
     return _vector(name, t, n, x.device, t.dtype)
 
 
-def _rows(x, width):
-    if x.dim() < 1 or x.shape[-1] != width or width < 1:
-        raise ValueError("the last axis does not fit, or is empty")
-    return x.numel() // width
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device, stream):
+    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+            else stream.cuda_stream)
+
+
+def _on(device, stream, *inputs):
+    """None, or the context to allocate and launch in.  With a stream of the
+    caller's own, outputs and scratch are allocated on it, and the inputs are
+    kept from reuse until it has passed this call."""
+    if stream is not None:
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
+
+
+def _scratch(workspace, nbytes, x):
+    """Workspace arguments: the caller's, or a block of the caching allocator
+    that goes back to it, in stream order, when the call returns."""
+    if workspace is None:
+        if not nbytes:
+            return None, 0
+        return x.new_empty(nbytes, dtype=torch.uint8), nbytes
+    if workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _new(name, t, shape, x, dtype):
+    if t is None:
+        return x.new_empty(shape, dtype=dtype)
+    return _is(name, t, shape, x.device, dtype)
+
+
+def _last_axis(name, t):
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} needs a last axis of at least one element")
+    return t.shape[-1]
 
 
 def _skip_layer(input, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats, stream):
     x = _cuda("input", input)
-    dev, dt = x.device, x.dtype
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("input needs a last axis of at least one element")
-    hidden = x.shape[-1]
+    dev, dt, shape = x.device, x.dtype, x.shape
+    hidden = _last_axis("input", x)
     rows = x.numel() // hidden
     _weights("gamma", gamma, hidden, x)
     if beta is not None:
         _vector("beta", beta, hidden, dev, gamma.dtype)
     if skip is not None:
-        _shaped("skip", skip, x.shape, dev, dt)
+        _is("skip", skip, shape, dev, dt)
     elif bias is not None or sum_out is not None:
         raise ValueError("bias and sum_out need a skip (S is the input without one)")
     if bias is not None:
         _vector("bias", bias, hidden, dev, dt)
-    lib = library()
-    with _on(dev, stream, x, skip, gamma, beta, bias):
-        y = _new("output", output, x.shape, dev, dt)
-        s = None
-        if skip is not None and (want_sum or sum_out is not None):
-            s = _new("input_skip_bias_sum", sum_out, x.shape, dev, dt)
-        mean = inv = None
-        if stats:
-            shape = tuple(x.shape[:-1]) + (1,)
-            mean = torch.empty(shape, dtype=torch.float32, device=dev)
-            inv = torch.empty(shape, dtype=torch.float32, device=dev)
-        _check(lib.b200norm_skip_layer(_ptr(x), _ptr(skip), _ptr(gamma), _ptr(beta), _ptr(bias),
-                                       _ptr(y), _ptr(s), _ptr(mean), _ptr(inv), rows, hidden,
-                                       _DTYPES[dt], _DTYPES[gamma.dtype], float(epsilon),
-                                       _stream(dev, stream)))
+    context = _on(dev, stream, x, skip, gamma, beta, bias)
+    if context is not None:
+        with context:
+            return _skip_layer_run(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out,
+                                   stats, stream, rows, hidden)
+    return _skip_layer_run(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats,
+                           stream, rows, hidden)
+
+
+def _skip_layer_run(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats, stream,
+                    rows, hidden):
+    dev, dt, shape = x.device, x.dtype, x.shape
+    y = _new("output", output, shape, x, dt)
+    s = None
+    if skip is not None and (want_sum or sum_out is not None):
+        s = _new("input_skip_bias_sum", sum_out, shape, x, dt)
+    mean = inv = None
+    if stats:
+        stat_shape = tuple(shape[:-1]) + (1,)
+        mean = x.new_empty(stat_shape, dtype=torch.float32)
+        inv = x.new_empty(stat_shape, dtype=torch.float32)
+    _check((_lib or library()).b200norm_skip_layer(
+        x.data_ptr(), _at(skip), gamma.data_ptr(), _at(beta), _at(bias), y.data_ptr(), _at(s),
+        _at(mean), _at(inv), rows, hidden, _DTYPES[dt], _DTYPES[gamma.dtype], epsilon,
+        _raw_stream(dev, stream)))
     if skip is None and want_sum:
         s = x
     return y, s, mean, inv
@@ -481,37 +503,43 @@ def skip_layer_grad(dy, s, mean, inv_std_var, gamma, *, ds=None, want_input=True
     """
     dy = _cuda("dy", dy)
     dev, dt = dy.device, dy.dtype
-    if dy.dim() < 1 or dy.shape[-1] < 1:
-        raise ValueError("dy needs a last axis of at least one element")
-    hidden = dy.shape[-1]
+    hidden = _last_axis("dy", dy)
     rows = dy.numel() // hidden
-    _shaped("s", s, dy.shape, dev, dt)
+    _is("s", s, dy.shape, dev, dt)
     _weights("gamma", gamma, hidden, dy)
     _vector("mean", mean, rows, dev, torch.float32)
     _vector("inv_std_var", inv_std_var, rows, dev, torch.float32)
     if ds is not None:
-        _shaped("ds", ds, dy.shape, dev, dt)
-    lib = library()
-    with _on(dev, stream, dy, s, mean, inv_std_var, gamma, ds):
-        if want_input or dx is not None:
-            dx = _new("dx", dx, dy.shape, dev, dt)
-        if want_gamma or dgamma is not None:
-            dgamma = _new("dgamma", dgamma, gamma.shape, dev, gamma.dtype)
-        if want_beta or dbeta is not None:
-            dbeta = _new("dbeta", dbeta, gamma.shape, dev, gamma.dtype)
-        if want_bias or dbias is not None:
-            dbias = _new("dbias", dbias, gamma.shape, dev, dt)
+        _is("ds", ds, dy.shape, dev, dt)
+
+    def run():
+        lib = _lib or library()
+        m = gamma.dtype
+        outs = (
+            _new("dx", dx, dy.shape, dy, dt) if want_input or dx is not None else None,
+            _new("dgamma", dgamma, gamma.shape, dy, m) if want_gamma or dgamma is not None else None,
+            _new("dbeta", dbeta, gamma.shape, dy, m) if want_beta or dbeta is not None else None,
+            _new("dbias", dbias, gamma.shape, dy, dt) if want_bias or dbias is not None else None)
         need = lib.b200norm_skip_layer_grad_workspace_size(rows, hidden) if rows else 0
-        ws, n = _scratch(workspace, need, dev)
+        ws, n = _scratch(workspace, need, dy)
         _check(lib.b200norm_skip_layer_grad(
-            _ptr(dy), _ptr(s), _ptr(mean), _ptr(inv_std_var), _ptr(gamma), _ptr(ds), _ptr(dx),
-            _ptr(dgamma), _ptr(dbeta), _ptr(dbias), rows, hidden, _DTYPES[dt],
-            _DTYPES[gamma.dtype], _ptr(ws), n, _stream(dev, stream)))
-    return dx, dgamma, dbeta, dbias
+            dy.data_ptr(), s.data_ptr(), mean.data_ptr(), inv_std_var.data_ptr(),
+            gamma.data_ptr(), _at(ds), *map(_at, outs), rows, hidden, _DTYPES[dt], _DTYPES[m],
+            _at(ws), n, _raw_stream(dev, stream)))
+        return outs
+
+    context = _on(dev, stream, dy, s, mean, inv_std_var, gamma, ds)
+    if context is None:
+        return run()
+    with context:
+        return run()
 
 
-def _aligned16(*tensors):
-    return 1 if all(t is None or t.data_ptr() % 16 == 0 for t in tensors) else 0
+def _weight(weight, device, dtype):
+    _is("weight", weight, None, device, dtype)
+    if weight.dim() != 2 or weight.numel() == 0:
+        raise ValueError("weight must be (out_features, in_features), neither zero")
+    return weight.shape
 
 
 def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y=None, z=None,
@@ -525,28 +553,33 @@ def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y
     """
     x = _cuda("x", x)
     dev, dt = x.device, x.dtype
-    _cuda("weight", weight, dev, dt)
-    if weight.dim() != 2:
-        raise ValueError("weight must be (out_features, in_features)")
-    n_out, n_in = weight.shape
-    rows = _rows(x, n_in)
-    shape = tuple(x.shape[:-1]) + (n_out,)
+    n_out, n_in = _weight(weight, dev, dt)
+    if _last_axis("x", x) != n_in:
+        raise ValueError(f"x's last axis must have weight's in_features ({n_in})")
+    rows = x.numel() // n_in
+    shape = x.shape[:-1] + (n_out,)
     if bias is not None:
         _vector("bias", bias, n_out, dev, dt)
     if residual is not None:
-        _shaped("residual", residual, shape, dev, dt)
-    lib = library()
-    with _on(dev, stream, x, weight, bias, residual):
-        y = _new("y", y, shape, dev, dt)
-        if want_z or z is not None:
-            z = _new("z", z, shape, dev, dt)
-        need = lib.b200norm_linear_workspace_size(rows, n_in, n_out, _DTYPES[dt],
-                                                  _aligned16(x, weight))
-        ws, n = _scratch(workspace, need, dev)
-        _check(lib.b200norm_linear(_ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(y),
-                                   _ptr(z), rows, n_in, n_out, _DTYPES[dt], int(activation),
-                                   _ptr(ws), n, _stream(dev, stream)))
-    return y, z
+        _is("residual", residual, shape, dev, dt)
+
+    def run():
+        lib = _lib or library()
+        yv = _new("y", y, shape, x, dt)
+        zv = _new("z", z, shape, x, dt) if want_z or z is not None else None
+        px, pw, code = x.data_ptr(), weight.data_ptr(), _DTYPES[dt]
+        need = lib.b200norm_linear_workspace_size(rows, n_in, n_out, code, (px | pw) % 16 == 0)
+        ws, n = _scratch(workspace, need, x)
+        _check(lib.b200norm_linear(px, pw, _at(bias), _at(residual), yv.data_ptr(), _at(zv), rows,
+                                   n_in, n_out, code, activation, _at(ws), n,
+                                   _raw_stream(dev, stream)))
+        return yv, zv
+
+    context = _on(dev, stream, x, weight, bias, residual)
+    if context is None:
+        return run()
+    with context:
+        return run()
 
 
 def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_weight=True,
@@ -557,35 +590,39 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
     """
     dy = _cuda("dy", dy)
     dev, dt = dy.device, dy.dtype
-    _cuda("weight", weight, dev, dt)
-    if weight.dim() != 2:
-        raise ValueError("weight must be (out_features, in_features)")
-    n_out, n_in = weight.shape
-    rows = _rows(dy, n_out)
-    in_shape = tuple(dy.shape[:-1]) + (n_in,)
-    _shaped("x", x, in_shape, dev, dt)
+    n_out, n_in = _weight(weight, dev, dt)
+    if _last_axis("dy", dy) != n_out:
+        raise ValueError(f"dy's last axis must have weight's out_features ({n_out})")
+    rows = dy.numel() // n_out
+    in_shape = dy.shape[:-1] + (n_in,)
+    _is("x", x, in_shape, dev, dt)
     if activation:
         if z is None:
             raise ValueError("z is needed with an activation")
-        _shaped("z", z, dy.shape, dev, dt)
+        _is("z", z, dy.shape, dev, dt)
     else:
         z = None
-    lib = library()
-    with _on(dev, stream, dy, x, weight, z):
-        if want_input or dx is not None:
-            dx = _new("dx", dx, in_shape, dev, dt)
-        if want_weight or dw is not None:
-            dw = _new("dw", dw, (n_out, n_in), dev, dt)
-        if want_bias or db is not None:
-            db = _new("db", db, (n_out,), dev, dt)
-        al = _aligned16(dy, x if dw is not None else None, weight if dx is not None else None)
-        need = lib.b200norm_linear_grad_workspace_size(rows, n_in, n_out, _DTYPES[dt],
-                                                       int(activation), al)
-        ws, n = _scratch(workspace, need, dev)
-        _check(lib.b200norm_linear_grad(_ptr(dy), _ptr(x), _ptr(weight), _ptr(z), _ptr(dx),
-                                        _ptr(dw), _ptr(db), rows, n_in, n_out, _DTYPES[dt],
-                                        int(activation), _ptr(ws), n, _stream(dev, stream)))
-    return dx, dw, db
+
+    def run():
+        lib = _lib or library()
+        dxv = _new("dx", dx, in_shape, dy, dt) if want_input or dx is not None else None
+        dwv = _new("dw", dw, (n_out, n_in), dy, dt) if want_weight or dw is not None else None
+        dbv = _new("db", db, (n_out,), dy, dt) if want_bias or db is not None else None
+        pd, px, pw, code = dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _DTYPES[dt]
+        aligned = (pd | (px if dwv is not None else 0) | (pw if dxv is not None else 0)) % 16 == 0
+        need = lib.b200norm_linear_grad_workspace_size(rows, n_in, n_out, code, activation,
+                                                       aligned)
+        ws, n = _scratch(workspace, need, dy)
+        _check(lib.b200norm_linear_grad(pd, px, pw, _at(z), _at(dxv), _at(dwv), _at(dbv), rows,
+                                        n_in, n_out, code, activation, _at(ws), n,
+                                        _raw_stream(dev, stream)))
+        return dxv, dwv, dbv
+
+    context = _on(dev, stream, dy, x, weight, z)
+    if context is None:
+        return run()
+    with context:
+        return run()
 
 
 def linear_status(stream=None, device=None):

@@ -14,6 +14,7 @@
 // (dbias sums dS before its rounding).
 #pragma once
 
+#include "bulk.cuh"
 #include "common.cuh"
 
 namespace b200norm {
@@ -48,14 +49,35 @@ struct LayerGradArgs {
   M* __restrict__ dbeta;
   T* __restrict__ dbias;
   float2* __restrict__ coef;    // per row: mean(g), mean(g * u)
-  float* __restrict__ part;     // [parts][3][n]: dgamma, dbeta, dbias
+  float* __restrict__ part;     // [parts][3][n]: dgamma, dbeta, dbias, at part_at()
   int parts;
+  int ve;                       // elements per vector of the kernel that fills part
   int64_t rows;
   int n;
   float inv_n;
 };
 
 constexpr int kLayerThreads = 512;
+
+// Where column `col` lies in a row of `part`: vectors of eight are kept as two
+// planes of four, so that a warp's 16-byte stores are contiguous.
+__device__ __forceinline__ int64_t part_at(int col, int n, int ve) {
+  if (ve != 8) return col;
+  return (static_cast<int64_t>((col >> 2) & 1) * (n >> 3) + (col >> 3)) * 4 + (col & 3);
+}
+
+// VE consecutive columns' sums of vector v.
+template <int VE>
+__device__ __forceinline__ void part_store(float* row, int v, int n, const float (&f)[VE]) {
+  if constexpr (VE == 1) {
+    row[v] = f[0];
+  } else {
+#pragma unroll
+    for (int q = 0; q < VE / 4; ++q)
+      *reinterpret_cast<float4*>(row + (static_cast<int64_t>(q) * (n / VE) + v) * 4) =
+          make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+  }
+}
 
 // VE parameters of type M as binary32 (one or two 16-byte loads, or scalars).
 template <typename M, int VE>
@@ -93,6 +115,167 @@ __device__ __forceinline__ Pack<T, VE> layer_sum(const LayerArgs<T, M>& a, int64
     for (int e = 0; e < VE; ++e) f[e] = __fadd_rn(f[e], bf[e]);
   }
   return pack_from<T, VE>(f);
+}
+
+// ---------------------------------------------------------------------------
+// Forward, the row in registers: read once, normalized, written once.
+// ---------------------------------------------------------------------------
+// Sum over the CTA with one barrier: every thread adds the warps' sums itself,
+// in warp order.  `red` holds one float per warp; a later call on the same
+// `red` needs a barrier between the two.
+__device__ __forceinline__ float cta_sum_1b(float v, float* red) {
+  v = warp_sum(v);
+  const int nwarps = (blockDim.x + 31) >> 5;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.0f;
+  for (int w = 0; w < nwarps; ++w) t += red[w];
+  return t;
+}
+
+// This thread's vectors first, first + step, ... (NV of them, below nvec) of
+// one row: S formed, stored if wanted, and held.
+template <typename T, typename M, int VE, int NV>
+struct LayerRow {
+  Pack<T, VE> s[NV];
+
+  __device__ __forceinline__ void load(const LayerArgs<T, M>& a, int64_t base, int first, int step,
+                                       int nvec) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v < nvec) s[k] = ld_stream<T, VE>(a.x + base + static_cast<int64_t>(v) * VE);
+    }
+    if (!a.skip) return;
+    Pack<T, VE> q[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v < nvec) q[k] = ld_stream<T, VE>(a.skip + base + static_cast<int64_t>(v) * VE);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v >= nvec) continue;
+      float f[VE], kf[VE];
+      unpack(s[k], f);
+      unpack(q[k], kf);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) f[e] = __fadd_rn(f[e], kf[e]);
+      if (a.bias) {
+        float bf[VE];
+        ld_params<T, VE>(a.bias + static_cast<int64_t>(v) * VE, bf);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] = __fadd_rn(f[e], bf[e]);
+      }
+      s[k] = pack_from<T, VE>(f);
+      if (a.s) st_stream<T, VE>(a.s + base + static_cast<int64_t>(v) * VE, s[k]);
+    }
+  }
+
+  __device__ __forceinline__ float sum(int first, int step, int nvec) const {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (first + k * step >= nvec) continue;
+      float f[VE];
+      unpack(s[k], f);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) t += f[e];
+    }
+    return t;
+  }
+
+  __device__ __forceinline__ float squares(float mu, int first, int step, int nvec) const {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (first + k * step >= nvec) continue;
+      float f[VE];
+      unpack(s[k], f);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float d = f[e] - mu;
+        t = fmaf(d, d, t);
+      }
+    }
+    return t;
+  }
+
+  __device__ __forceinline__ void store(const LayerArgs<T, M>& a, int64_t base, int first,
+                                        int step, int nvec, float mu, float r) const {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v >= nvec) continue;
+      float f[VE], p[VE];
+      unpack(s[k], f);
+      ld_params<M, VE>(a.gamma + static_cast<int64_t>(v) * VE, p);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) f[e] = (f[e] - mu) * r * p[e];
+      if (a.beta) {
+        ld_params<M, VE>(a.beta + static_cast<int64_t>(v) * VE, p);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] += p[e];
+      }
+      st_stream<T, VE>(a.y + base + static_cast<int64_t>(v) * VE, pack_from<T, VE>(f));
+    }
+  }
+};
+
+// Short rows: `tpr` <= 32 threads (a power of two) per row, both sums by
+// butterflies over them, no barrier; persistent grid.
+template <typename T, typename M, int VE, int NV>
+__global__ void __launch_bounds__(256) layer_lane_kernel(const LayerArgs<T, M> a, int tpr,
+                                                         int nvec) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, per = blockDim.x / tpr;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * per; row0 < a.rows;
+       row0 += static_cast<int64_t>(gridDim.x) * per) {
+    const int64_t row = row0 + group;
+    const int64_t base = row * a.n;
+    const int nv = row < a.rows ? nvec : 0;  // the whole warp takes part in the sums
+    LayerRow<T, M, VE, NV> x;
+    if (nv) x.load(a, base, lane, tpr, nv);
+    const float mu = seg_sum(x.sum(lane, tpr, nv), tpr) * a.inv_n;
+    const float r = rsqrtf(fmaf(seg_sum(x.squares(mu, lane, tpr, nv), tpr), a.inv_n, a.eps));
+    if (!nv) continue;
+    x.store(a, base, lane, tpr, nv, mu, r);
+    if (lane == 0) {
+      if (a.mean) a.mean[row] = mu;
+      if (a.inv_std) a.inv_std[row] = r;
+    }
+  }
+}
+
+// Longer rows: a CTA each, or a cluster of CTAs whose sums meet through
+// distributed shared memory (tpr = threads of the cluster).
+template <typename T, typename M, int VE, int NV>
+__global__ void __launch_bounds__(kLayerThreads) layer_cta_kernel(const LayerArgs<T, M> a, int tpr,
+                                                                  int nvec) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float red[2][16];
+  __shared__ float slot[2];
+  const unsigned csize = cluster_size();
+  const unsigned rank = csize > 1 ? cluster_rank() : 0u;
+  const int64_t row = blockIdx.x / csize, base = row * a.n;
+  const int first = threadIdx.x + static_cast<int>(rank) * blockDim.x;
+  LayerRow<T, M, VE, NV> x;
+  x.load(a, base, first, tpr, nvec);
+  float t = cta_sum_1b(x.sum(first, tpr, nvec), red[0]);
+  if (csize > 1) t = cluster_sum(t, &slot[0], csize);
+  const float mu = t * a.inv_n;
+  t = cta_sum_1b(x.squares(mu, first, tpr, nvec), red[1]);
+  if (csize > 1) t = cluster_sum(t, &slot[1], csize);
+  const float r = rsqrtf(fmaf(t, a.inv_n, a.eps));
+  x.store(a, base, first, tpr, nvec, mu, r);
+  if (first == 0) {
+    if (a.mean) a.mean[row] = mu;
+    if (a.inv_std) a.inv_std[row] = r;
+  }
+  if (csize > 1) cluster_sync();  // peers may still read slot
 }
 
 // Rows of any length: one CTA walks the row three times (sum, centred squares,
@@ -150,14 +333,344 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
   }
 }
 
-// dS of one vector from its operands (without ds).
-template <int VE>
-__device__ __forceinline__ void layer_dx(const float (&g)[VE], const float (&u)[VE], float r,
-                                         float c1, float c2, float (&d)[VE]) {
+// ---------------------------------------------------------------------------
+// Gradient in one pass: a row's g = dy * gamma and u = (S - mu) * r are held in
+// registers, its two means reduced, dS written, and the row added to the column
+// sums that the threads hold for their own columns.  Each input is read once.
+// About fifteen instructions per element, of which forming g and u a second
+// time instead of holding them would add nine (16384 x 4096 bfloat16: 107 us
+// so, when every third issue slot is already taken at the copy bandwidth).
+// (Products and sums are written with their roundings, so that every
+// instantiation gives the same bits.)
+// ---------------------------------------------------------------------------
+template <typename T, typename M, int VE, int NV, bool BIAS>
+struct LayerGradRow {
+  float dg[NV][VE] = {}, db[NV][VE] = {}, dc[BIAS ? NV : 1][VE] = {};
+  float gm[NV][VE];
+  float g[NV][VE], u[NV][VE];
+
+  // gamma of this thread's columns: vectors first, first + step, ... below nvec
+  __device__ __forceinline__ void load_gamma(const M* gamma, int first, int step, int nvec) {
 #pragma unroll
-  for (int e = 0; e < VE; ++e) d[e] = r * (g[e] - c1 - u[e] * c2);
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v < nvec) ld_params<M, VE>(gamma + static_cast<int64_t>(v) * VE, gm[k]);
+    }
+  }
+
+  // vector k of a row: adds it to dgamma and dbeta, and to the sums of g and g * u
+  __device__ __forceinline__ void take(int k, const Pack<T, VE>& dy, const Pack<T, VE>& s,
+                                       float mu, float r, float2& t) {
+    float dyf[VE];
+    unpack(dy, dyf);
+    unpack(s, u[k]);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      u[k][e] = __fmul_rn(u[k][e] - mu, r);
+      g[k][e] = __fmul_rn(dyf[e], gm[k][e]);
+      dg[k][e] = fmaf(dyf[e], u[k][e], dg[k][e]);
+      db[k][e] = __fadd_rn(db[k][e], dyf[e]);
+      t.x = __fadd_rn(t.x, g[k][e]);
+      t.y = fmaf(g[k][e], u[k][e], t.y);
+    }
+  }
+
+  // dS of vector k, k1 = -r * mean(g), k2 = -r * mean(g * u); stored at dx
+  __device__ __forceinline__ void give(int k, float r, float k1, float k2, const Pack<T, VE>* ds,
+                                       T* dx) {
+    float d[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) d[e] = fmaf(g[k][e], r, fmaf(u[k][e], k2, k1));
+    if (ds) {
+      float h[VE];
+      unpack(*ds, h);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) d[e] = __fadd_rn(d[e], h[e]);
+    }
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) dc[k][e] = __fadd_rn(dc[k][e], d[e]);
+    }
+    if (dx) st_stream<T, VE>(dx, pack_from<T, VE>(d));
+  }
+
+  // a whole row from global memory (the forms without a ring)
+  __device__ __forceinline__ float2 take_row(const LayerGradArgs<T, M>& a, int64_t base, int first,
+                                             int step, int nvec, float mu, float r) {
+    Pack<T, VE> dy[NV], s[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v >= nvec) continue;
+      dy[k] = ld_stream<T, VE>(a.dy + base + static_cast<int64_t>(v) * VE);
+      s[k] = ld_stream<T, VE>(a.s + base + static_cast<int64_t>(v) * VE);
+    }
+    float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (first + k * step < nvec) take(k, dy[k], s[k], mu, r, t);
+    return t;
+  }
+
+  __device__ __forceinline__ void give_row(const LayerGradArgs<T, M>& a, int64_t base, int first,
+                                           int step, int nvec, float r, float2 t) {
+    const float k1 = -r * (t.x * a.inv_n), k2 = -r * (t.y * a.inv_n);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v >= nvec) continue;
+      const int64_t off = base + static_cast<int64_t>(v) * VE;
+      Pack<T, VE> ds;
+      if (a.ds) ds = ld_stream<T, VE>(a.ds + off);
+      give(k, r, k1, k2, a.ds ? &ds : nullptr, a.dx ? a.dx + off : nullptr);
+    }
+  }
+};
+
+// Part p takes rows p, p + parts, ...; a CTA (or a cluster, for long rows) per
+// row, one barrier each.
+template <typename T, typename M, int VE, int NV, bool BIAS>
+__global__ void __launch_bounds__(kLayerThreads) layer_grad_kernel(const LayerGradArgs<T, M> a,
+                                                                   int nvec) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float2 red[2][16];
+  __shared__ float2 slot[2];
+  const unsigned csize = cluster_size();
+  const unsigned rank = csize > 1 ? cluster_rank() : 0u;
+  const int part = blockIdx.x / csize;
+  const int step = blockDim.x * csize;
+  const int first = threadIdx.x + static_cast<int>(rank) * blockDim.x;
+  LayerGradRow<T, M, VE, NV, BIAS> x;
+  x.load_gamma(a.gamma, first, step, nvec);
+  int flip = 0;
+  for (int64_t row = part; row < a.rows; row += a.parts, flip ^= 1) {
+    const int64_t base = row * a.n;
+    const float mu = a.mean[row], r = a.inv_std[row];
+    float2 t = x.take_row(a, base, first, step, nvec, mu, r);
+    if (!BIAS && !a.dx) continue;
+    t = cta_sum2_1b(t, red[flip]);
+    if (csize > 1) t = cluster_sum2(t, &slot[flip].x, &slot[flip].y, csize);
+    x.give_row(a, base, first, step, nvec, r, t);
+  }
+  float* p = a.part + static_cast<int64_t>(part) * 3 * a.n;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int v = first + k * step;
+    if (v >= nvec) continue;
+    part_store<VE>(p, v, a.n, x.dg[k]);
+    part_store<VE>(p + a.n, v, a.n, x.db[k]);
+    if constexpr (BIAS) part_store<VE>(p + 2 * static_cast<int64_t>(a.n), v, a.n, x.dc[k]);
+  }
+  if (csize > 1) cluster_sync();  // peers may still read slot
 }
 
+// At the end of a lane kernel the row groups of a warp add their column sums by
+// butterflies, then the warps theirs through shared memory, in warp order.
+constexpr int kLayerGradLaneThreads = 256;
+template <typename T, typename M, int VE, int NV, bool BIAS>
+__device__ __forceinline__ void layer_grad_lane_sums(
+    const LayerGradArgs<T, M>& a, const LayerGradRow<T, M, VE, NV, BIAS>& x,
+    float (*acc)[32 * NV * VE], int tpr) {
+  constexpr int kOut = BIAS ? 3 : 2;
+  const int lane = threadIdx.x & (tpr - 1);
+  for (int w = 0; w < kLayerGradLaneThreads / 32; ++w) {
+    if (threadIdx.x / 32 == w) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          float g = x.dg[k][e], b = x.db[k][e], c = BIAS ? x.dc[BIAS ? k : 0][e] : 0.0f;
+          for (int o = tpr; o < 32; o *= 2) {
+            g += __shfl_xor_sync(0xffffffffu, g, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+            if constexpr (BIAS) c += __shfl_xor_sync(0xffffffffu, c, o);
+          }
+          const int col = (lane + k * tpr) * VE + e;
+          if ((threadIdx.x & 31) < tpr) {
+            acc[0][col] = w ? acc[0][col] + g : g;
+            acc[1][col] = w ? acc[1][col] + b : b;
+            if constexpr (BIAS) acc[kOut - 1][col] = w ? acc[kOut - 1][col] + c : c;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  float* p = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.n;
+  for (int col = threadIdx.x; col < a.n; col += kLayerGradLaneThreads) {
+#pragma unroll
+    for (int o = 0; o < kOut; ++o)
+      p[static_cast<int64_t>(o) * a.n + part_at(col, a.n, VE)] = acc[o][col];
+  }
+}
+
+// Short rows: `tpr` <= 32 threads (a power of two) per row, no barrier.
+template <typename T, typename M, int VE, int NV, bool BIAS>
+__global__ void __launch_bounds__(kLayerGradLaneThreads)
+layer_grad_lane_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kOut = BIAS ? 3 : 2;
+  __shared__ float acc[kOut][32 * NV * VE];
+  const int lane = threadIdx.x & (tpr - 1), per = kLayerGradLaneThreads / tpr;
+  LayerGradRow<T, M, VE, NV, BIAS> x;
+  x.load_gamma(a.gamma, lane, tpr, nvec);
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * per; row0 < a.rows;
+       row0 += static_cast<int64_t>(a.parts) * per) {
+    const int64_t row = row0 + threadIdx.x / tpr;
+    const int64_t base = row * a.n;
+    const int nv = row < a.rows ? nvec : 0;  // the whole warp takes part in the sums
+    const float mu = nv ? a.mean[row] : 0.0f, r = nv ? a.inv_std[row] : 0.0f;
+    float2 t = x.take_row(a, base, lane, tpr, nv, mu, r);
+    if (!BIAS && !a.dx) continue;
+    t.x = seg_sum(t.x, tpr);
+    t.y = seg_sum(t.y, tpr);
+    x.give_row(a, base, lane, tpr, nv, r, t);
+  }
+  layer_grad_lane_sums<T, M, VE, NV, BIAS>(a, x, acc, tpr);
+}
+
+// The same with the inputs streamed through shared memory: one thread keeps the
+// next `stages` tiles of dy, S and ds (plain contiguous bytes, so one bulk
+// copy each) on their way while the CTA works on the present one.  The register
+// forms above can hold no more than the present row in flight, and stand still
+// for its two means: 16384 x 4096 bfloat16 took 135 us with them.
+//
+// A tile is a row (of a cluster's CTA: its slice of the row), or with LANE the
+// 256 / tpr consecutive rows that the CTA's lane groups take.  A stage is free
+// again once the CTA has met at the next tile's barrier.  The waits for a copy
+// are bounded; a thread whose wait gave up records it and runs on without
+// waiting (its outputs are then undefined), so that every barrier is met.
+constexpr int kLayerStages = 4;  // at most; 2 where that lets an SM hold two CTAs
+constexpr unsigned long long kLayerLimitNs = 1000000000ull;
+
+template <typename T, typename M, int VE, int NV, bool BIAS, bool LANE>
+__global__ void __launch_bounds__(LANE ? kLayerGradLaneThreads : kLayerThreads)
+layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice, int stages,
+                       unsigned* status) {
+  using P = Pack<T, VE>;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ alignas(8) unsigned long long full[kLayerStages];
+  __shared__ float2 red[2][16];
+  __shared__ float2 slot[2];
+  __shared__ float acc[LANE ? (BIAS ? 3 : 2) : 1][LANE ? 32 * NV * VE : 1];
+  const unsigned csize = LANE ? 1u : cluster_size();
+  const unsigned rank = csize > 1 ? cluster_rank() : 0u;
+  const int part = blockIdx.x / csize;
+  // this CTA's vectors of a row: [lo, lo + count)
+  const int lo = static_cast<int>(rank) * slice;
+  const int count = LANE ? nvec : (nvec - lo < slice ? (nvec > lo ? nvec - lo : 0) : slice);
+  const int rows_per = LANE ? kLayerGradLaneThreads / tpr : 1;
+  const int first = LANE ? threadIdx.x & (tpr - 1) : threadIdx.x;
+  const int step = LANE ? tpr : blockDim.x;
+  const int group = LANE ? threadIdx.x / tpr : 0;
+  const int64_t tiles_all = (a.rows + rows_per - 1) / rows_per;
+  const int64_t tiles = tiles_all > part ? (tiles_all - part + a.parts - 1) / a.parts : 0;
+  const int slot_bytes = rows_per * slice * 16;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kLayerStages; ++i) mbar_init(&full[i], 1);
+    mbar_init_fence();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  auto issue = [&](int64_t i, int st) {  // thread 0: tile i into stage st
+    if (count == 0) return;
+    const int64_t row = (part + i * a.parts) * rows_per;
+    const int64_t rows = a.rows - row < rows_per ? a.rows - row : rows_per;
+    const int64_t off = row * a.n + static_cast<int64_t>(lo) * VE;
+    const unsigned bytes = static_cast<unsigned>(rows * count * 16);
+    unsigned char* dst = ring + st * 3 * slot_bytes;
+    unsigned long long* bar = &full[st];
+    mbar_arrive_expect_tx(bar, bytes * (a.ds ? 3 : 2));
+    bulk_load(dst, a.dy + off, bytes, bar);
+    bulk_load(dst + slot_bytes, a.s + off, bytes, bar);
+    if (a.ds) bulk_load(dst + 2 * slot_bytes, a.ds + off, bytes, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < stages && i < tiles; ++i) issue(i, i);
+
+  LayerGradRow<T, M, VE, NV, BIAS> x;
+  x.load_gamma(a.gamma + static_cast<int64_t>(lo) * VE, first, step, count);
+  bool alive = true;
+  // the next row's statistics are on their way as well
+  int64_t row = static_cast<int64_t>(part) * rows_per + group;
+  float mu_next = 0.0f, r_next = 0.0f;
+  if (row < a.rows) {
+    mu_next = a.mean[row];
+    r_next = a.inv_std[row];
+  }
+  int st = 0, before = 0;
+  unsigned parity = 0;
+  for (int64_t i = 0; i < tiles; ++i) {
+    const int nv = row < a.rows ? count : 0;
+    const int64_t base = row * a.n + static_cast<int64_t>(lo) * VE;
+    const float mu = mu_next, r = r_next;
+    row += static_cast<int64_t>(a.parts) * rows_per;
+    if (row < a.rows) {
+      mu_next = a.mean[row];
+      r_next = a.inv_std[row];
+    }
+    const P* dy = reinterpret_cast<const P*>(ring + st * 3 * slot_bytes) + group * count;
+    const P* s = dy + slot_bytes / 16;
+    const P* ds = s + slot_bytes / 16;
+    if (alive && count > 0 && !mbar_wait(&full[st], parity, kLayerLimitNs)) {
+      alive = false;
+      atomicExch(status, kStatusDeviceTimeout);
+    }
+    float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v < nv) x.take(k, dy[v], s[v], mu, r, t);
+    }
+    if constexpr (LANE) {
+      t.x = seg_sum(t.x, tpr);
+      t.y = seg_sum(t.y, tpr);
+      __syncthreads();
+    } else {
+      t = cta_sum2_1b(t, red[i & 1]);
+    }
+    // everyone is done with the tile before this one
+    if (threadIdx.x == 0 && alive && i > 0 && i - 1 + stages < tiles) issue(i - 1 + stages, before);
+    if (csize > 1) t = cluster_sum2(t, &slot[i & 1].x, &slot[i & 1].y, csize);
+    const float k1 = -r * (t.x * a.inv_n), k2 = -r * (t.y * a.inv_n);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v < nv)
+        x.give(k, r, k1, k2, a.ds ? ds + v : nullptr,
+               a.dx ? a.dx + base + static_cast<int64_t>(v) * VE : nullptr);
+    }
+    before = st;
+    if (++st == stages) {
+      st = 0;
+      parity ^= 1;
+    }
+  }
+  if (!alive && threadIdx.x == 0)  // copies still in flight land before the CTA ends
+    for (int i = 0; i < stages; ++i) {
+      mbar_wait(&full[i], 0, kLayerLimitNs);
+      mbar_wait(&full[i], 1, kLayerLimitNs);
+    }
+  if constexpr (LANE) {
+    layer_grad_lane_sums<T, M, VE, NV, BIAS>(a, x, acc, tpr);
+  } else {
+    float* p = a.part + static_cast<int64_t>(part) * 3 * a.n;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      if (v >= count) continue;
+      part_store<VE>(p, lo + v, a.n, x.dg[k]);
+      part_store<VE>(p + a.n, lo + v, a.n, x.db[k]);
+      if constexpr (BIAS) part_store<VE>(p + 2 * static_cast<int64_t>(a.n), lo + v, a.n, x.dc[k]);
+    }
+    if (csize > 1) cluster_sync();  // peers may still read slot
+  }
+}
 // Gradient, rows of any length: one CTA per row takes the two row means, keeps
 // them for the column kernel, and writes dS.
 template <typename T, typename M, int VE>
@@ -178,15 +691,16 @@ layer_grad_rows_kernel(const LayerGradArgs<T, M> a) {
     ld_params<M, VE>(a.gamma + static_cast<int64_t>(v) * VE, gm);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const float g = dy[e] * gm[e];
+      const float g = __fmul_rn(dy[e], gm[e]);
       acc.x += g;
-      acc.y = fmaf(g, (s[e] - mu) * r, acc.y);
+      acc.y = fmaf(g, __fmul_rn(s[e] - mu, r), acc.y);
     }
   }
   acc = cta_sum2(acc, red);
   const float c1 = acc.x * a.inv_n, c2 = acc.y * a.inv_n;
   if (threadIdx.x == 0) a.coef[row] = make_float2(c1, c2);
   if (!a.dx) return;
+  const float k1 = -r * c1, k2 = -r * c2;
   for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
     const int64_t off = base + static_cast<int64_t>(v) * VE;
     float g[VE], u[VE], gm[VE], d[VE];
@@ -198,7 +712,8 @@ layer_grad_rows_kernel(const LayerGradArgs<T, M> a) {
       g[e] *= gm[e];
       u[e] = (u[e] - mu) * r;
     }
-    layer_dx<VE>(g, u, r, c1, c2, d);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) d[e] = fmaf(g[e], r, fmaf(u[e], k2, k1));
     if (a.ds) {
       float h[VE];
       unpack(ld_stream<T, VE>(a.ds + off), h);
@@ -253,17 +768,23 @@ layer_grad_finish_kernel(const LayerGradArgs<T, M> a) {
   const int which = blockIdx.y;
   if (which == 0 ? !a.dgamma : which == 1 ? !a.dbeta : !a.dbias) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float t = 0.0f;
-  if (col < a.n)
+  if (at < a.n)
     for (int p = warp; p < a.parts; p += 32)
-      t += a.part[(static_cast<int64_t>(p) * 3 + which) * a.n + col];
+      t += a.part[(static_cast<int64_t>(p) * 3 + which) * a.n + at];
   red[warp][lane] = t;
   __syncthreads();
   // warp w now adds column w over the 32 warps
   t = warp_sum(red[lane][warp]);
-  const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + warp;
-  if (lane == 0 && out < a.n) {
+  const int64_t from = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && from < a.n) {
+    // the column that lies there (part_at)
+    int64_t out = from;
+    if (a.ve == 8) {
+      const int64_t q = from / 4, plane = q >= a.n / 8 ? 1 : 0;
+      out = (q - plane * (a.n / 8)) * 8 + plane * 4 + from % 4;
+    }
     if (which == 0) a.dgamma[out] = from_f32<M>(t);
     else if (which == 1) a.dbeta[out] = from_f32<M>(t);
     else a.dbias[out] = from_f32<T>(t);

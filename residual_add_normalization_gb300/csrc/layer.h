@@ -44,12 +44,11 @@ struct LayerGradCall {
 
 // Partial column sums a gradient call keeps: one set of (dgamma, dbeta, dbias)
 // rows per part, later added in part order (no atomics, so equal calls give
-// equal bits).  At most two parts per SM, at least kLayerRowsPerPart rows in
-// each, and fewer for very long rows, whose columns alone fill the GPU.
-constexpr int kLayerMaxParts = 304;
-constexpr int kLayerRowsPerPart = 4;
+// equal bits).  At most four parts per SM, and fewer for long rows, which fill
+// the GPU with fewer.
+constexpr int kLayerMaxParts = 608;
 inline int layer_grad_parts(int64_t rows, int64_t hidden) {
-  int64_t p = (rows + kLayerRowsPerPart - 1) / kLayerRowsPerPart;
+  int64_t p = rows;
   const int64_t most = (int64_t{1} << 24) / hidden;
   if (p > most) p = most;
   if (p > kLayerMaxParts) p = kLayerMaxParts;

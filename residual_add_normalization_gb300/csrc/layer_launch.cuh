@@ -8,21 +8,96 @@
 namespace b200norm {
 
 template <class Fn, class... A>
-cudaError_t launch_pdl(Fn fn, dim3 grid, int block, cudaStream_t stream, const A&... args) {
+cudaError_t launch_clusters(Fn fn, dim3 grid, int block, int csize, size_t smem,
+                            cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (csize > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    n = 1;
+  }
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = add_pdl_attr(attr, 0);
+  cfg.numAttrs = add_pdl_attr(attr, n);
   return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <class Fn, class... A>
+cudaError_t launch_pdl(Fn fn, dim3 grid, int block, cudaStream_t stream, const A&... args) {
+  return launch_clusters(fn, grid, block, 1, 0, stream, args...);
 }
 
 // Threads of a walking CTA: whole warps, no more than the row has vectors for.
 inline int layer_walk_block(int64_t nvec) {
   const int64_t b = (nvec + 31) / 32 * 32;
   return static_cast<int>(b < kLayerThreads ? b : kLayerThreads);
+}
+
+// CTAs of the lane-group grid: six of 256 threads per SM.
+constexpr int kLayerLaneCtas = 152 * 6;
+
+constexpr int kLayerMaxCluster = 8;  // the portable cluster size
+
+// How a row is spread: `lane` threads of a warp, or `block` threads of each of
+// `csize` CTAs, nv vectors per thread; nv 0: the row is walked.
+struct LayerPlan {
+  int lane, block, csize, nv;
+};
+
+inline LayerPlan plan_layer(int64_t rows, int64_t nvec) {
+  LayerPlan p{0, 256, 1, 0};
+  if (nvec <= 128) {  // at most four vectors per lane
+    p.nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
+    p.lane = 1;
+    while (p.lane * p.nv < nvec) p.lane *= 2;
+    return p;
+  }
+  // few rows: the latency of a row counts, so one vector per thread; many:
+  // about 256 threads
+  const int64_t want = rows <= 512 ? 512 : 256;
+  int nv = 1;
+  while (nv < 4 && nvec > want * nv) nv *= 2;
+  while (nv < 8 && nvec > static_cast<int64_t>(kLayerThreads) * nv) nv *= 2;
+  int c = 1;
+  while (c < kLayerMaxCluster && nvec > static_cast<int64_t>(kLayerThreads) * nv * c) c *= 2;
+  if (nvec > static_cast<int64_t>(kLayerThreads) * nv * c) return p;
+  p.nv = nv;
+  p.csize = c;
+  p.block = static_cast<int>(((nvec + nv * c - 1) / (nv * c) + 31) / 32 * 32);
+  return p;
+}
+
+template <typename T, typename M, int VE>
+cudaError_t launch_layer_ve(const LayerCall& c, const LayerArgs<T, M>& a, cudaStream_t stream) {
+  const int64_t nvec = c.hidden / VE;
+  const LayerPlan p = plan_layer(c.rows, nvec);
+  if (p.nv == 0 || c.rows * p.csize > 0x7fffffffLL)
+    return launch_pdl(layer_walk_kernel<T, M, VE>, dim3(static_cast<unsigned>(c.rows)),
+                      layer_walk_block(nvec), stream, a);
+  using Fn = void (*)(const LayerArgs<T, M>, int, int);
+  if (p.lane) {
+    const Fn fn = p.nv == 1   ? layer_lane_kernel<T, M, VE, 1>
+                  : p.nv == 2 ? layer_lane_kernel<T, M, VE, 2>
+                              : layer_lane_kernel<T, M, VE, 4>;
+    const int64_t per = p.block / p.lane;
+    int64_t grid = (c.rows + per - 1) / per;
+    if (grid > kLayerLaneCtas) grid = kLayerLaneCtas;
+    return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), p.block, stream, a, p.lane,
+                      static_cast<int>(nvec));
+  }
+  const Fn fn = p.nv == 1   ? layer_cta_kernel<T, M, VE, 1>
+                : p.nv == 2 ? layer_cta_kernel<T, M, VE, 2>
+                : p.nv == 4 ? layer_cta_kernel<T, M, VE, 4>
+                            : layer_cta_kernel<T, M, VE, 8>;
+  return launch_clusters(fn, dim3(static_cast<unsigned>(c.rows * p.csize)), p.block, p.csize,
+                         0, stream, a, p.block * p.csize, static_cast<int>(nvec));
 }
 
 template <typename T, typename M>
@@ -33,11 +108,119 @@ cudaError_t launch_layer_tm(const LayerCall& c, cudaStream_t stream) {
                     static_cast<const T*>(c.bias), static_cast<T*>(c.y), static_cast<T*>(c.s),
                     c.mean, c.inv_std, c.rows, static_cast<int>(c.hidden),
                     1.0f / static_cast<float>(c.hidden), c.eps};
-  const dim3 grid(static_cast<unsigned>(c.rows));
-  if (c.vec)
-    return launch_pdl(layer_walk_kernel<T, M, VE>, grid, layer_walk_block(c.hidden / VE), stream,
-                      a);
-  return launch_pdl(layer_walk_kernel<T, M, 1>, grid, layer_walk_block(c.hidden), stream, a);
+  return c.vec ? launch_layer_ve<T, M, VE>(c, a, stream) : launch_layer_ve<T, M, 1>(c, a, stream);
+}
+
+// The streamed gradient: its shared-memory limit is raised and the CTAs that an
+// SM holds are asked for once per device, kernel and size; the grid is at most
+// one wave of them.
+template <typename T, typename M, class Fn>
+cudaError_t launch_layer_grad_ring(Fn fn, LayerGradArgs<T, M>* a, int block, int csize,
+                                   int tile_bytes, int tpr, int nvec, int slice,
+                                   cudaStream_t stream) {
+  struct Key {
+    int dev, block, smem;
+    const void* fn;
+  };
+  static PlanCache<Key, int> cache;
+  int stages = kLayerStages;
+  while (stages > 2 && stages * tile_bytes > 100 * 1024) --stages;
+  const int smem = tile_bytes * stages;
+  Key k;
+  memset(&k, 0, sizeof(k));
+  cudaError_t e = cudaGetDevice(&k.dev);
+  if (e != cudaSuccess) return e;
+  k.block = block;
+  k.smem = smem;
+  k.fn = reinterpret_cast<const void*>(fn);
+  int resident = 0;
+  if (!cache.get(k, &resident)) {
+    int sms = 0, per_sm = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, k.dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, block, smem);
+    if (e != cudaSuccess) return e;
+    resident = (per_sm > 0 ? per_sm : 1) * sms;
+    cache.put(k, resident);
+  }
+  if (a->parts > resident / csize) a->parts = resident / csize;
+  unsigned* status = pipe_status_word();
+  if (!status) return cudaErrorSymbolNotFound;
+  return launch_clusters(fn, dim3(static_cast<unsigned>(a->parts * csize)), block, csize, smem,
+                         stream, *a, tpr, nvec, slice, stages, status);
+}
+
+// The one-pass gradient, NV vectors per thread of `block` threads of `csize` CTAs.
+template <typename T, typename M, int VE, int NV>
+cudaError_t launch_layer_grad_cta(const LayerGradCall& c, LayerGradArgs<T, M>* a, int csize,
+                                  cudaStream_t stream) {
+  const int nvec = static_cast<int>(c.hidden / VE);
+  const int slice = (nvec + csize - 1) / csize;
+  const int block = ((slice + NV - 1) / NV + 31) / 32 * 32;
+  if constexpr (VE > 1) {
+    auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, false>
+                       : layer_grad_ring_kernel<T, M, VE, NV, false, false>;
+    return launch_layer_grad_ring(fn, a, block, csize, slice * 48, 0, nvec, slice, stream);
+  } else {
+    auto* fn =
+        c.dbias ? layer_grad_kernel<T, M, VE, NV, true> : layer_grad_kernel<T, M, VE, NV, false>;
+    return launch_clusters(fn, dim3(static_cast<unsigned>(a->parts * csize)), block, csize, 0,
+                           stream, *a, nvec);
+  }
+}
+
+template <typename T, typename M, int VE, int NV>
+cudaError_t launch_layer_grad_lane(const LayerGradCall& c, LayerGradArgs<T, M>* a,
+                                   cudaStream_t stream) {
+  const int nvec = static_cast<int>(c.hidden / VE);
+  int tpr = 1;
+  while (tpr * NV < nvec) tpr *= 2;
+  const int64_t per = kLayerGradLaneThreads / tpr, blocks = (c.rows + per - 1) / per;
+  if (a->parts > blocks) a->parts = static_cast<int>(blocks);
+  if constexpr (VE > 1) {
+    auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, true>
+                       : layer_grad_ring_kernel<T, M, VE, NV, false, true>;
+    return launch_layer_grad_ring(fn, a, kLayerGradLaneThreads, 1,
+                                  static_cast<int>(per) * nvec * 48, tpr, nvec, nvec, stream);
+  } else {
+    auto* fn = c.dbias ? layer_grad_lane_kernel<T, M, VE, NV, true>
+                       : layer_grad_lane_kernel<T, M, VE, NV, false>;
+    return launch_pdl(fn, dim3(a->parts), kLayerGradLaneThreads, stream, *a, tpr, nvec);
+  }
+}
+
+// The gradient form that the row's length allows; sets a->parts to the parts
+// that it writes.
+template <typename T, typename M, int VE>
+cudaError_t launch_layer_grad_ve(const LayerGradCall& c, LayerGradArgs<T, M>* a,
+                                 cudaStream_t stream) {
+  // at most sixteen elements per thread: their sums and the row fit 128 registers
+  constexpr int kMost = VE == 8 ? 2 : VE == 4 ? 4 : 8;
+  a->ve = VE;
+  const int64_t nvec = c.hidden / VE;
+  if (nvec <= 32) return launch_layer_grad_lane<T, M, VE, 1>(c, a, stream);
+  if (nvec <= 64) return launch_layer_grad_lane<T, M, VE, 2>(c, a, stream);
+  // a CTA's slice of a row: what its threads hold, or (streamed) four stages of
+  // three slices in 192 KB
+  constexpr int64_t kSlice = VE > 1 ? 1024 : kLayerThreads * kMost;
+  int csize = 1;
+  while (csize < kLayerMaxCluster && nvec > kSlice * csize) csize *= 2;
+  if (nvec <= kSlice * csize) {
+    if (nvec <= 256) return launch_layer_grad_cta<T, M, VE, 1>(c, a, csize, stream);
+    if (kMost == 2 || nvec <= 512)
+      return launch_layer_grad_cta<T, M, VE, 2>(c, a, csize, stream);
+    return launch_layer_grad_cta<T, M, VE, kMost>(c, a, csize, stream);
+  }
+  a->ve = 1;
+  cudaError_t e = launch_pdl(layer_grad_rows_kernel<T, M, VE>, dim3(static_cast<unsigned>(c.rows)),
+                             layer_walk_block(nvec), stream, *a);
+  if (e == cudaSuccess && (c.dgamma || c.dbeta || c.dbias))
+    e = launch_pdl(layer_grad_cols_kernel<T, M>,
+                   dim3(static_cast<unsigned>((c.hidden + 255) / 256), a->parts), 256, stream,
+                   *a);
+  return e;
 }
 
 template <typename T, typename M>
@@ -50,19 +233,12 @@ cudaError_t launch_layer_grad_tm(const LayerGradCall& c, cudaStream_t stream) {
                         static_cast<M*>(c.dbeta), static_cast<T*>(c.dbias),
                         static_cast<float2*>(c.workspace),
                         reinterpret_cast<float*>(static_cast<char*>(c.workspace) + stats),
-                        layer_grad_parts(c.rows, c.hidden), c.rows, static_cast<int>(c.hidden),
+                        layer_grad_parts(c.rows, c.hidden), 1, c.rows, static_cast<int>(c.hidden),
                         1.0f / static_cast<float>(c.hidden)};
   cudaError_t e = cudaSuccess;
   if (c.rows > 0) {
-    const dim3 grid(static_cast<unsigned>(c.rows));
-    e = c.vec ? launch_pdl(layer_grad_rows_kernel<T, M, VE>, grid,
-                           layer_walk_block(c.hidden / VE), stream, a)
-              : launch_pdl(layer_grad_rows_kernel<T, M, 1>, grid, layer_walk_block(c.hidden),
-                           stream, a);
-    if (e != cudaSuccess) return e;
-    if (c.dgamma || c.dbeta || c.dbias)
-      e = launch_pdl(layer_grad_cols_kernel<T, M>,
-                     dim3(static_cast<unsigned>((c.hidden + 255) / 256), a.parts), 256, stream, a);
+    e = c.vec ? launch_layer_grad_ve<T, M, VE>(c, &a, stream)
+              : launch_layer_grad_ve<T, M, 1>(c, &a, stream);
     if (e != cudaSuccess) return e;
   } else {
     a.parts = 0;  // empty sums

@@ -10,6 +10,14 @@ import residual_add_normalization_gb300 as b2
 
 pytestmark = pytest.mark.gpu
 
+
+
+@pytest.fixture(autouse=True)
+def _no_wait_gave_up():
+    yield
+    b2.rows_status()
+
+
 EPS = 1e-5
 TYPES = [("f32", "f32"), ("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32")]
 # rows x hidden: one element, less than a vector, odd widths, every schedule's

@@ -354,40 +354,48 @@ ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 # is checked with one expression, and only a failed check asks what was wrong.
 
 
-def _is(name, t, shape, device, dtype):
-    """``t``, contiguous on ``device`` with that type and shape (None: any)."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+def _first(name, t):
+    """(index of its device, type) of a call's first tensor."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()
+            and t.dtype in _DTYPES):
+        _cuda(name, t)
+    return t.get_device(), t.dtype
+
+
+def _is(name, t, shape, x, index, dtype):
+    """``t``, contiguous on x's device (of that index) with that type and shape
+    (None: any)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
             and (shape is None or t.shape == shape) and t.is_contiguous()):
         return t
-    _cuda(name, t, device, dtype)
+    _cuda(name, t, x.device, dtype)
     raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
 
 
-def _vector(name, t, n, device, dtype):
-    _is(name, t, None, device, dtype)
+def _vector(name, t, n, x, index, dtype):
+    _is(name, t, None, x, index, dtype)
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements")
     return t
 
 
-def _weights(name, t, n, x):
+def _weights(name, t, n, x, index):
     """gamma / beta: x's type or float32."""
     if not isinstance(t, torch.Tensor) or t.dtype not in (x.dtype, torch.float32):
         _cuda(name, t, x.device)
         raise TypeError(f"{name} must be {x.dtype} or torch.float32 (got {t.dtype})")
-    return _vector(name, t, n, x.device, t.dtype)
+    return _vector(name, t, n, x, index, t.dtype)
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(device, stream):
-    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-            else stream.cuda_stream)
+def _raw_stream(index, stream):
+    return (torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
 
 
-def _on(device, stream, *inputs):
+def _on(index, stream, inputs):
     """None, or the context to allocate and launch in.  With a stream of the
     caller's own, outputs and scratch are allocated on it, and the inputs are
     kept from reuse until it has passed this call."""
@@ -396,8 +404,8 @@ def _on(device, stream, *inputs):
             if t is not None:
                 t.record_stream(stream)
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
+    if index != torch._C._cuda_getDevice():
+        return torch.cuda.device(index)
     return None
 
 
@@ -413,10 +421,14 @@ def _scratch(workspace, nbytes, x):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _new(name, t, shape, x, dtype):
-    if t is None:
-        return x.new_empty(shape, dtype=dtype)
-    return _is(name, t, shape, x.device, dtype)
+def _like(name, t, x, index):
+    """An output of x's shape and type: the caller's, or a new one."""
+    return torch.empty_like(x) if t is None else _is(name, t, x.shape, x, index, x.dtype)
+
+
+def _new(name, t, shape, x, index):
+    """An output of x's type and another shape."""
+    return x.new_empty(shape) if t is None else _is(name, t, shape, x, index, x.dtype)
 
 
 def _last_axis(name, t):
@@ -425,48 +437,39 @@ def _last_axis(name, t):
     return t.shape[-1]
 
 
-def _skip_layer(input, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats, stream):
-    x = _cuda("input", input)
-    dev, dt, shape = x.device, x.dtype, x.shape
+def _skip_layer(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats, stream):
+    index, dt = _first("input", x)
     hidden = _last_axis("input", x)
-    rows = x.numel() // hidden
-    _weights("gamma", gamma, hidden, x)
+    _weights("gamma", gamma, hidden, x, index)
     if beta is not None:
-        _vector("beta", beta, hidden, dev, gamma.dtype)
+        _vector("beta", beta, hidden, x, index, gamma.dtype)
     if skip is not None:
-        _is("skip", skip, shape, dev, dt)
+        _is("skip", skip, x.shape, x, index, dt)
     elif bias is not None or sum_out is not None:
         raise ValueError("bias and sum_out need a skip (S is the input without one)")
     if bias is not None:
-        _vector("bias", bias, hidden, dev, dt)
-    context = _on(dev, stream, x, skip, gamma, beta, bias)
-    if context is not None:
-        with context:
-            return _skip_layer_run(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out,
-                                   stats, stream, rows, hidden)
-    return _skip_layer_run(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats,
-                           stream, rows, hidden)
+        _vector("bias", bias, hidden, x, index, dt)
 
+    def run():
+        y = _like("output", output, x, index)
+        s = None
+        if skip is not None and (want_sum or sum_out is not None):
+            s = _like("input_skip_bias_sum", sum_out, x, index)
+        mean = inv = None
+        if stats:
+            mean = x.new_empty(tuple(x.shape[:-1]) + (1,), dtype=torch.float32)
+            inv = torch.empty_like(mean)
+        _check((_lib or library()).b200norm_skip_layer(
+            x.data_ptr(), _at(skip), gamma.data_ptr(), _at(beta), _at(bias), y.data_ptr(), _at(s),
+            _at(mean), _at(inv), x.numel() // hidden, hidden, _DTYPES[dt], _DTYPES[gamma.dtype],
+            epsilon, _raw_stream(index, stream)))
+        return y, (x if skip is None and want_sum else s), mean, inv
 
-def _skip_layer_run(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, stats, stream,
-                    rows, hidden):
-    dev, dt, shape = x.device, x.dtype, x.shape
-    y = _new("output", output, shape, x, dt)
-    s = None
-    if skip is not None and (want_sum or sum_out is not None):
-        s = _new("input_skip_bias_sum", sum_out, shape, x, dt)
-    mean = inv = None
-    if stats:
-        stat_shape = tuple(shape[:-1]) + (1,)
-        mean = x.new_empty(stat_shape, dtype=torch.float32)
-        inv = x.new_empty(stat_shape, dtype=torch.float32)
-    _check((_lib or library()).b200norm_skip_layer(
-        x.data_ptr(), _at(skip), gamma.data_ptr(), _at(beta), _at(bias), y.data_ptr(), _at(s),
-        _at(mean), _at(inv), rows, hidden, _DTYPES[dt], _DTYPES[gamma.dtype], epsilon,
-        _raw_stream(dev, stream)))
-    if skip is None and want_sum:
-        s = x
-    return y, s, mean, inv
+    context = _on(index, stream, (x, skip, gamma, beta, bias))
+    if context is None:
+        return run()
+    with context:
+        return run()
 
 
 def skip_layer(input, skip, gamma, beta=None, bias=None, *, epsilon=1e-5, want_sum=True,
@@ -501,42 +504,41 @@ def skip_layer_grad(dy, s, mean, inv_std_var, gamma, *, ds=None, want_input=True
     is that of both ``input`` and ``skip``.  An output that is not wanted is
     ``None``; one that is given is wanted.
     """
-    dy = _cuda("dy", dy)
-    dev, dt = dy.device, dy.dtype
+    index, dt = _first("dy", dy)
     hidden = _last_axis("dy", dy)
     rows = dy.numel() // hidden
-    _is("s", s, dy.shape, dev, dt)
-    _weights("gamma", gamma, hidden, dy)
-    _vector("mean", mean, rows, dev, torch.float32)
-    _vector("inv_std_var", inv_std_var, rows, dev, torch.float32)
+    _is("s", s, dy.shape, dy, index, dt)
+    _weights("gamma", gamma, hidden, dy, index)
+    _vector("mean", mean, rows, dy, index, torch.float32)
+    _vector("inv_std_var", inv_std_var, rows, dy, index, torch.float32)
     if ds is not None:
-        _is("ds", ds, dy.shape, dev, dt)
+        _is("ds", ds, dy.shape, dy, index, dt)
 
     def run():
         lib = _lib or library()
-        m = gamma.dtype
         outs = (
-            _new("dx", dx, dy.shape, dy, dt) if want_input or dx is not None else None,
-            _new("dgamma", dgamma, gamma.shape, dy, m) if want_gamma or dgamma is not None else None,
-            _new("dbeta", dbeta, gamma.shape, dy, m) if want_beta or dbeta is not None else None,
-            _new("dbias", dbias, gamma.shape, dy, dt) if want_bias or dbias is not None else None)
+            _like("dx", dx, dy, index) if want_input or dx is not None else None,
+            _like("dgamma", dgamma, gamma, index) if want_gamma or dgamma is not None else None,
+            _like("dbeta", dbeta, gamma, index) if want_beta or dbeta is not None else None,
+            _new("dbias", dbias, gamma.shape, dy, index) if want_bias or dbias is not None
+            else None)
         need = lib.b200norm_skip_layer_grad_workspace_size(rows, hidden) if rows else 0
         ws, n = _scratch(workspace, need, dy)
         _check(lib.b200norm_skip_layer_grad(
             dy.data_ptr(), s.data_ptr(), mean.data_ptr(), inv_std_var.data_ptr(),
-            gamma.data_ptr(), _at(ds), *map(_at, outs), rows, hidden, _DTYPES[dt], _DTYPES[m],
-            _at(ws), n, _raw_stream(dev, stream)))
+            gamma.data_ptr(), _at(ds), *map(_at, outs), rows, hidden, _DTYPES[dt],
+            _DTYPES[gamma.dtype], _at(ws), n, _raw_stream(index, stream)))
         return outs
 
-    context = _on(dev, stream, dy, s, mean, inv_std_var, gamma, ds)
+    context = _on(index, stream, (dy, s, mean, inv_std_var, gamma, ds))
     if context is None:
         return run()
     with context:
         return run()
 
 
-def _weight(weight, device, dtype):
-    _is("weight", weight, None, device, dtype)
+def _weight(weight, x, index, dtype):
+    _is("weight", weight, None, x, index, dtype)
     if weight.dim() != 2 or weight.numel() == 0:
         raise ValueError("weight must be (out_features, in_features), neither zero")
     return weight.shape
@@ -551,31 +553,30 @@ def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y
     Returns ``(y, z)``; ``z``, the value before the activation that
     :func:`linear_grad` takes, is ``None`` unless ``want_z`` or ``z`` is given.
     """
-    x = _cuda("x", x)
-    dev, dt = x.device, x.dtype
-    n_out, n_in = _weight(weight, dev, dt)
+    index, dt = _first("x", x)
+    n_out, n_in = _weight(weight, x, index, dt)
     if _last_axis("x", x) != n_in:
         raise ValueError(f"x's last axis must have weight's in_features ({n_in})")
     rows = x.numel() // n_in
     shape = x.shape[:-1] + (n_out,)
     if bias is not None:
-        _vector("bias", bias, n_out, dev, dt)
+        _vector("bias", bias, n_out, x, index, dt)
     if residual is not None:
-        _is("residual", residual, shape, dev, dt)
+        _is("residual", residual, shape, x, index, dt)
 
     def run():
         lib = _lib or library()
-        yv = _new("y", y, shape, x, dt)
-        zv = _new("z", z, shape, x, dt) if want_z or z is not None else None
+        yv = _new("y", y, shape, x, index)
+        zv = _like("z", z, yv, index) if want_z or z is not None else None
         px, pw, code = x.data_ptr(), weight.data_ptr(), _DTYPES[dt]
         need = lib.b200norm_linear_workspace_size(rows, n_in, n_out, code, (px | pw) % 16 == 0)
         ws, n = _scratch(workspace, need, x)
         _check(lib.b200norm_linear(px, pw, _at(bias), _at(residual), yv.data_ptr(), _at(zv), rows,
                                    n_in, n_out, code, activation, _at(ws), n,
-                                   _raw_stream(dev, stream)))
+                                   _raw_stream(index, stream)))
         return yv, zv
 
-    context = _on(dev, stream, x, weight, bias, residual)
+    context = _on(index, stream, (x, weight, bias, residual))
     if context is None:
         return run()
     with context:
@@ -588,26 +589,25 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
     ``dy``).  ``z`` is the forward call's, needed with an activation.  An output
     that is not wanted is ``None``; one that is given is wanted.
     """
-    dy = _cuda("dy", dy)
-    dev, dt = dy.device, dy.dtype
-    n_out, n_in = _weight(weight, dev, dt)
+    index, dt = _first("dy", dy)
+    n_out, n_in = _weight(weight, dy, index, dt)
     if _last_axis("dy", dy) != n_out:
         raise ValueError(f"dy's last axis must have weight's out_features ({n_out})")
     rows = dy.numel() // n_out
     in_shape = dy.shape[:-1] + (n_in,)
-    _is("x", x, in_shape, dev, dt)
+    _is("x", x, in_shape, dy, index, dt)
     if activation:
         if z is None:
             raise ValueError("z is needed with an activation")
-        _is("z", z, dy.shape, dev, dt)
+        _is("z", z, dy.shape, dy, index, dt)
     else:
         z = None
 
     def run():
         lib = _lib or library()
-        dxv = _new("dx", dx, in_shape, dy, dt) if want_input or dx is not None else None
-        dwv = _new("dw", dw, (n_out, n_in), dy, dt) if want_weight or dw is not None else None
-        dbv = _new("db", db, (n_out,), dy, dt) if want_bias or db is not None else None
+        dxv = _like("dx", dx, x, index) if want_input or dx is not None else None
+        dwv = _like("dw", dw, weight, index) if want_weight or dw is not None else None
+        dbv = _new("db", db, (n_out,), dy, index) if want_bias or db is not None else None
         pd, px, pw, code = dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _DTYPES[dt]
         aligned = (pd | (px if dwv is not None else 0) | (pw if dxv is not None else 0)) % 16 == 0
         need = lib.b200norm_linear_grad_workspace_size(rows, n_in, n_out, code, activation,
@@ -615,10 +615,10 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
         ws, n = _scratch(workspace, need, dy)
         _check(lib.b200norm_linear_grad(pd, px, pw, _at(z), _at(dxv), _at(dwv), _at(dbv), rows,
                                         n_in, n_out, code, activation, _at(ws), n,
-                                        _raw_stream(dev, stream)))
+                                        _raw_stream(index, stream)))
         return dxv, dwv, dbv
 
-    context = _on(dev, stream, dy, x, weight, z)
+    context = _on(index, stream, (dy, x, weight, z))
     if context is None:
         return run()
     with context:

@@ -756,39 +756,57 @@ layer_grad_cols_kernel(const LayerGradArgs<T, M> a) {
   if (a.dbias) p[2 * static_cast<int64_t>(a.n)] = dc;
 }
 
-// The parts' sums added in a fixed order: a CTA takes 32 columns of one of the
-// three outputs, its 32 warps every 32nd part, then the warps' sums are added
-// through shared memory.
+// The parts' sums added in a fixed order: a CTA takes 128 columns of one of the
+// three outputs (16 bytes per lane), its 32 warps every 32nd part, then the
+// warps' sums are added through shared memory.
+constexpr int kLayerFinishCols = 128;
 template <typename T, typename M>
 __global__ void __launch_bounds__(1024)
 layer_grad_finish_kernel(const LayerGradArgs<T, M> a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float red[32][33];
+  __shared__ float red[32][kLayerFinishCols];
   const int which = blockIdx.y;
   if (which == 0 ? !a.dgamma : which == 1 ? !a.dbeta : !a.dbias) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float t = 0.0f;
-  if (at < a.n)
-    for (int p = warp; p < a.parts; p += 32)
-      t += a.part[(static_cast<int64_t>(p) * 3 + which) * a.n + at];
-  red[warp][lane] = t;
-  __syncthreads();
-  // warp w now adds column w over the 32 warps
-  t = warp_sum(red[lane][warp]);
-  const int64_t from = static_cast<int64_t>(blockIdx.x) * 32 + warp;
-  if (lane == 0 && from < a.n) {
-    // the column that lies there (part_at)
-    int64_t out = from;
-    if (a.ve == 8) {
-      const int64_t q = from / 4, plane = q >= a.n / 8 ? 1 : 0;
-      out = (q - plane * (a.n / 8)) * 8 + plane * 4 + from % 4;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kLayerFinishCols + lane * 4;
+  const int64_t pitch = 3 * static_cast<int64_t>(a.n);
+  const float* src = a.part + which * static_cast<int64_t>(a.n) + at;
+  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (a.n % 4 == 0 && at < a.n) {
+#pragma unroll 4
+    for (int p = warp; p < a.parts; p += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(src + p * pitch);
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+      t.w += v.w;
     }
-    if (which == 0) a.dgamma[out] = from_f32<M>(t);
-    else if (which == 1) a.dbeta[out] = from_f32<M>(t);
-    else a.dbias[out] = from_f32<T>(t);
+  } else if (at < a.n) {
+    for (int p = warp; p < a.parts; p += 32) {
+      const float* v = src + p * pitch;
+      t.x += v[0];
+      if (at + 1 < a.n) t.y += v[1];
+      if (at + 2 < a.n) t.z += v[2];
+      if (at + 3 < a.n) t.w += v[3];
+    }
   }
+  *reinterpret_cast<float4*>(&red[warp][lane * 4]) = t;
+  __syncthreads();
+  const int64_t from = static_cast<int64_t>(blockIdx.x) * kLayerFinishCols + threadIdx.x;
+  if (threadIdx.x >= kLayerFinishCols || from >= a.n) return;
+  float sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) sum += red[w][threadIdx.x];
+  // the column that lies there (part_at)
+  int64_t out = from;
+  if (a.ve == 8) {
+    const int64_t q = from / 4, plane = q >= a.n / 8 ? 1 : 0;
+    out = (q - plane * (a.n / 8)) * 8 + plane * 4 + from % 4;
+  }
+  if (which == 0) a.dgamma[out] = from_f32<M>(sum);
+  else if (which == 1) a.dbeta[out] = from_f32<M>(sum);
+  else a.dbias[out] = from_f32<T>(sum);
 }
 
 }  // namespace b200norm

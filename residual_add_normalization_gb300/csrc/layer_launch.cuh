@@ -245,7 +245,8 @@ cudaError_t launch_layer_grad_tm(const LayerGradCall& c, cudaStream_t stream) {
   }
   if (c.dgamma || c.dbeta || c.dbias)
     e = launch_pdl(layer_grad_finish_kernel<T, M>,
-                   dim3(static_cast<unsigned>((c.hidden + 31) / 32), 3), 1024, stream, a);
+                   dim3(static_cast<unsigned>((c.hidden + kLayerFinishCols - 1) /
+                                              kLayerFinishCols), 3), 1024, stream, a);
   return e;
 }
 

@@ -49,7 +49,8 @@ struct LayerGradArgs {
   M* __restrict__ dbeta;
   T* __restrict__ dbias;
   float2* __restrict__ coef;    // per row: mean(g), mean(g * u)
-  float* __restrict__ part;     // [parts][3][n]: dgamma, dbeta, dbias, at part_at()
+  float* __restrict__ part;     // [parts][3][pitch]: dgamma, dbeta, dbias, at part_at()
+  int64_t pitch;                // n rounded up to four
   int parts;
   int ve;                       // elements per vector of the kernel that fills part
   int64_t rows;
@@ -334,136 +335,158 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
 }
 
 // ---------------------------------------------------------------------------
+// Two binary32 operations in one instruction, each rounded as by itself.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ unsigned long long pair_bits(float2 v) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 bits_pair(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// ---------------------------------------------------------------------------
 // Gradient in one pass: a row's g = dy * gamma and u = (S - mu) * r are held in
 // registers, its two means reduced, dS written, and the row added to the column
 // sums that the threads hold for their own columns.  Each input is read once.
-// About fifteen instructions per element, of which forming g and u a second
-// time instead of holding them would add nine (16384 x 4096 bfloat16: 107 us
-// so, when every third issue slot is already taken at the copy bandwidth).
-// (Products and sums are written with their roundings, so that every
-// instantiation gives the same bits.)
+// At the copy bandwidth an SM's schedulers have about 45 issue slots per 32
+// elements, so the arithmetic goes two elements at a time.  Every product and
+// sum is rounded by itself, so that every instantiation gives the same bits.
 // ---------------------------------------------------------------------------
 template <typename T, typename M, int VE, int NV, bool BIAS>
 struct LayerGradRow {
-  float dg[NV][VE] = {}, db[NV][VE] = {}, dc[BIAS ? NV : 1][VE] = {};
-  float gm[NV][VE];
-  float g[NV][VE], u[NV][VE];
+  static constexpr int H = (VE + 1) / 2;  // pairs per vector (VE 1: .x alone)
+  float2 dg[NV][H] = {}, db[NV][H] = {}, dc[BIAS ? NV : 1][H] = {};
+  float2 gm[NV][H];
+  float2 g[NV][H], u[NV][H];
+
+  __device__ __forceinline__ static float2 at(const Pack<T, VE>& p, int i) {
+    if constexpr (VE == 1) return make_float2(to_f32(p.v[0]), 0.0f);
+    else return get2(p, i);
+  }
 
   // gamma of this thread's columns: vectors first, first + step, ... below nvec
   __device__ __forceinline__ void load_gamma(const M* gamma, int first, int step, int nvec) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = first + k * step;
-      if (v < nvec) ld_params<M, VE>(gamma + static_cast<int64_t>(v) * VE, gm[k]);
+      float f[2 * H] = {};
+      if (v < nvec) {
+        float q[VE];
+        ld_params<M, VE>(gamma + static_cast<int64_t>(v) * VE, q);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] = q[e];
+      }
+#pragma unroll
+      for (int i = 0; i < H; ++i) gm[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
     }
   }
 
-  // vector k of a row: adds it to dgamma and dbeta, and to the sums of g and g * u
+  // vector k of a row: adds it to dgamma and dbeta, and to the sums of g (tg)
+  // and g * u (tu)
   __device__ __forceinline__ void take(int k, const Pack<T, VE>& dy, const Pack<T, VE>& s,
-                                       float mu, float r, float2& t) {
-    float dyf[VE];
-    unpack(dy, dyf);
-    unpack(s, u[k]);
+                                       float mu, float r, float2& tg, float2& tu) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      u[k][e] = __fmul_rn(u[k][e] - mu, r);
-      g[k][e] = __fmul_rn(dyf[e], gm[k][e]);
-      dg[k][e] = fmaf(dyf[e], u[k][e], dg[k][e]);
-      db[k][e] = __fadd_rn(db[k][e], dyf[e]);
-      t.x = __fadd_rn(t.x, g[k][e]);
-      t.y = fmaf(g[k][e], u[k][e], t.y);
+    for (int i = 0; i < H; ++i) {
+      const float2 d = at(dy, i);
+      u[k][i] = mul2(add2(at(s, i), both(-mu)), both(r));
+      g[k][i] = mul2(d, gm[k][i]);
+      dg[k][i] = fma2(d, u[k][i], dg[k][i]);
+      db[k][i] = add2(db[k][i], d);
+      tg = add2(tg, g[k][i]);
+      tu = fma2(g[k][i], u[k][i], tu);
     }
   }
 
   // dS of vector k, k1 = -r * mean(g), k2 = -r * mean(g * u); stored at dx
   __device__ __forceinline__ void give(int k, float r, float k1, float k2, const Pack<T, VE>* ds,
                                        T* dx) {
-    float d[VE];
+    Pack<T, VE> out;
 #pragma unroll
-    for (int e = 0; e < VE; ++e) d[e] = fmaf(g[k][e], r, fmaf(u[k][e], k2, k1));
-    if (ds) {
-      float h[VE];
-      unpack(*ds, h);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) d[e] = __fadd_rn(d[e], h[e]);
+    for (int i = 0; i < H; ++i) {
+      float2 d = fma2(g[k][i], both(r), fma2(u[k][i], both(k2), both(k1)));
+      if (ds) d = add2(d, at(*ds, i));
+      if constexpr (BIAS) dc[k][i] = add2(dc[k][i], d);
+      if constexpr (VE == 1) out.v[0] = from_f32<T>(d.x);
+      else set2(out, i, d.x, d.y);
     }
-    if constexpr (BIAS) {
-#pragma unroll
-      for (int e = 0; e < VE; ++e) dc[k][e] = __fadd_rn(dc[k][e], d[e]);
-    }
-    if (dx) st_stream<T, VE>(dx, pack_from<T, VE>(d));
+    if (dx) st_stream<T, VE>(dx, out);
   }
 
-  // a whole row from global memory (the forms without a ring)
-  __device__ __forceinline__ float2 take_row(const LayerGradArgs<T, M>& a, int64_t base, int first,
-                                             int step, int nvec, float mu, float r) {
-    Pack<T, VE> dy[NV], s[NV];
+  // one of dg, db and dc of a vector, an element at a time
+  __device__ __forceinline__ static void elements(const float2 (&p)[H], float (&f)[VE]) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = first + k * step;
-      if (v >= nvec) continue;
-      dy[k] = ld_stream<T, VE>(a.dy + base + static_cast<int64_t>(v) * VE);
-      s[k] = ld_stream<T, VE>(a.s + base + static_cast<int64_t>(v) * VE);
-    }
-    float2 t = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (first + k * step < nvec) take(k, dy[k], s[k], mu, r, t);
-    return t;
-  }
-
-  __device__ __forceinline__ void give_row(const LayerGradArgs<T, M>& a, int64_t base, int first,
-                                           int step, int nvec, float r, float2 t) {
-    const float k1 = -r * (t.x * a.inv_n), k2 = -r * (t.y * a.inv_n);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = first + k * step;
-      if (v >= nvec) continue;
-      const int64_t off = base + static_cast<int64_t>(v) * VE;
-      Pack<T, VE> ds;
-      if (a.ds) ds = ld_stream<T, VE>(a.ds + off);
-      give(k, r, k1, k2, a.ds ? &ds : nullptr, a.dx ? a.dx + off : nullptr);
-    }
+    for (int e = 0; e < VE; ++e) f[e] = e % 2 ? p[e / 2].y : p[e / 2].x;
   }
 };
 
-// Part p takes rows p, p + parts, ...; a CTA (or a cluster, for long rows) per
-// row, one barrier each.
-template <typename T, typename M, int VE, int NV, bool BIAS>
-__global__ void __launch_bounds__(kLayerThreads) layer_grad_kernel(const LayerGradArgs<T, M> a,
-                                                                   int nvec) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ float2 red[2][16];
-  __shared__ float2 slot[2];
-  const unsigned csize = cluster_size();
-  const unsigned rank = csize > 1 ? cluster_rank() : 0u;
-  const int part = blockIdx.x / csize;
-  const int step = blockDim.x * csize;
-  const int first = threadIdx.x + static_cast<int>(rank) * blockDim.x;
-  LayerGradRow<T, M, VE, NV, BIAS> x;
-  x.load_gamma(a.gamma, first, step, nvec);
-  int flip = 0;
-  for (int64_t row = part; row < a.rows; row += a.parts, flip ^= 1) {
-    const int64_t base = row * a.n;
-    const float mu = a.mean[row], r = a.inv_std[row];
-    float2 t = x.take_row(a, base, first, step, nvec, mu, r);
-    if (!BIAS && !a.dx) continue;
-    t = cta_sum2_1b(t, red[flip]);
-    if (csize > 1) t = cluster_sum2(t, &slot[flip].x, &slot[flip].y, csize);
-    x.give_row(a, base, first, step, nvec, r, t);
+// One tensor's bytes of a tile: `len` elements from element `off` on, copied to
+// `dst` from the 16-byte boundary below them on (a bulk copy starts and ends on
+// such boundaries).  The copy may take bytes of neighbouring rows, but none
+// outside the tensor: what it leaves out at the tensor's ends, take() reads from
+// global memory.
+template <typename T, int VE>
+struct TileBytes {
+  const T* p;         // element `off`
+  uintptr_t lo, hi;   // what is copied
+  int shift;          // bytes from dst to element `off`
+
+  __device__ __forceinline__ TileBytes(const T* tensor, int64_t numel, int64_t off, int64_t len)
+      : p(tensor + off) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if constexpr (VE > 1) {  // whole vectors
+      shift = 0;
+      lo = a;
+      hi = a + len * sizeof(T);
+    } else {
+      shift = static_cast<int>(a & 15);
+      const uintptr_t begin = (reinterpret_cast<uintptr_t>(tensor) + 15) & ~uintptr_t{15};
+      const uintptr_t end = reinterpret_cast<uintptr_t>(tensor + numel) & ~uintptr_t{15};
+      lo = a & ~uintptr_t{15};
+      hi = (a + len * sizeof(T) + 15) & ~uintptr_t{15};
+      if (lo < begin) lo = begin;
+      if (hi > end) hi = end;
+      if (hi < lo) hi = lo;
+    }
   }
-  float* p = a.part + static_cast<int64_t>(part) * 3 * a.n;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int v = first + k * step;
-    if (v >= nvec) continue;
-    part_store<VE>(p, v, a.n, x.dg[k]);
-    part_store<VE>(p + a.n, v, a.n, x.db[k]);
-    if constexpr (BIAS) part_store<VE>(p + 2 * static_cast<int64_t>(a.n), v, a.n, x.dc[k]);
+
+  __device__ __forceinline__ unsigned bytes() const { return static_cast<unsigned>(hi - lo); }
+
+  __device__ __forceinline__ void copy(unsigned char* dst, unsigned long long* bar) const {
+    if (hi > lo)
+      bulk_load(dst + (lo - (reinterpret_cast<uintptr_t>(p) - shift)),
+                reinterpret_cast<const void*>(lo), bytes(), bar);
   }
-  if (csize > 1) cluster_sync();  // peers may still read slot
-}
+
+  // vector v of the tile
+  __device__ __forceinline__ Pack<T, VE> take(const unsigned char* dst, int v, bool edge) const {
+    if constexpr (VE == 1) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p + v);
+      if (edge && (at < lo || at >= hi)) return ld_stream<T, 1>(p + v);
+    }
+    return *reinterpret_cast<const Pack<T, VE>*>(dst + shift + v * static_cast<int>(sizeof(T)) * VE);
+  }
+};
 
 // At the end of a lane kernel the row groups of a warp add their column sums by
 // butterflies, then the warps theirs through shared memory, in warp order.
@@ -480,7 +503,9 @@ __device__ __forceinline__ void layer_grad_lane_sums(
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          float g = x.dg[k][e], b = x.db[k][e], c = BIAS ? x.dc[BIAS ? k : 0][e] : 0.0f;
+          float g = e % 2 ? x.dg[k][e / 2].y : x.dg[k][e / 2].x;
+          float b = e % 2 ? x.db[k][e / 2].y : x.db[k][e / 2].x;
+          float c = e % 2 ? x.dc[BIAS ? k : 0][e / 2].y : x.dc[BIAS ? k : 0][e / 2].x;
           for (int o = tpr; o < 32; o *= 2) {
             g += __shfl_xor_sync(0xffffffffu, g, o);
             b += __shfl_xor_sync(0xffffffffu, b, o);
@@ -497,45 +522,18 @@ __device__ __forceinline__ void layer_grad_lane_sums(
     }
     __syncthreads();
   }
-  float* p = a.part + static_cast<int64_t>(blockIdx.x) * 3 * a.n;
+  float* p = a.part + blockIdx.x * 3 * a.pitch;
   for (int col = threadIdx.x; col < a.n; col += kLayerGradLaneThreads) {
 #pragma unroll
-    for (int o = 0; o < kOut; ++o)
-      p[static_cast<int64_t>(o) * a.n + part_at(col, a.n, VE)] = acc[o][col];
+    for (int o = 0; o < kOut; ++o) p[o * a.pitch + part_at(col, a.n, VE)] = acc[o][col];
   }
 }
 
-// Short rows: `tpr` <= 32 threads (a power of two) per row, no barrier.
-template <typename T, typename M, int VE, int NV, bool BIAS>
-__global__ void __launch_bounds__(kLayerGradLaneThreads)
-layer_grad_lane_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int kOut = BIAS ? 3 : 2;
-  __shared__ float acc[kOut][32 * NV * VE];
-  const int lane = threadIdx.x & (tpr - 1), per = kLayerGradLaneThreads / tpr;
-  LayerGradRow<T, M, VE, NV, BIAS> x;
-  x.load_gamma(a.gamma, lane, tpr, nvec);
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * per; row0 < a.rows;
-       row0 += static_cast<int64_t>(a.parts) * per) {
-    const int64_t row = row0 + threadIdx.x / tpr;
-    const int64_t base = row * a.n;
-    const int nv = row < a.rows ? nvec : 0;  // the whole warp takes part in the sums
-    const float mu = nv ? a.mean[row] : 0.0f, r = nv ? a.inv_std[row] : 0.0f;
-    float2 t = x.take_row(a, base, lane, tpr, nv, mu, r);
-    if (!BIAS && !a.dx) continue;
-    t.x = seg_sum(t.x, tpr);
-    t.y = seg_sum(t.y, tpr);
-    x.give_row(a, base, lane, tpr, nv, r, t);
-  }
-  layer_grad_lane_sums<T, M, VE, NV, BIAS>(a, x, acc, tpr);
-}
-
-// The same with the inputs streamed through shared memory: one thread keeps the
-// next `stages` tiles of dy, S and ds (plain contiguous bytes, so one bulk
-// copy each) on their way while the CTA works on the present one.  The register
-// forms above can hold no more than the present row in flight, and stand still
-// for its two means: 16384 x 4096 bfloat16 took 135 us with them.
+// The inputs are streamed through shared memory: one thread keeps the next
+// `stages` tiles of dy, S and ds (contiguous bytes, one bulk copy each) on their
+// way while the CTA works on the present one.  Without the stream, threads can
+// hold no more than the present row in flight and stand still for its two means
+// (16384 x 4096 bfloat16: 135 us).  Part p takes tiles p, p + parts, ....
 //
 // A tile is a row (of a cluster's CTA: its slice of the row), or with LANE the
 // 256 / tpr consecutive rows that the CTA's lane groups take.  A stage is free
@@ -545,8 +543,13 @@ layer_grad_lane_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec) {
 constexpr int kLayerStages = 4;  // at most; 2 where that lets an SM hold two CTAs
 constexpr unsigned long long kLayerLimitNs = 1000000000ull;
 
+template <typename T, int VE>
+__host__ __device__ constexpr int layer_slot_bytes(int vectors) {
+  return VE > 1 ? vectors * 16 : (vectors * static_cast<int>(sizeof(T)) + 15) / 16 * 16 + 16;
+}
+
 template <typename T, typename M, int VE, int NV, bool BIAS, bool LANE>
-__global__ void __launch_bounds__(LANE ? kLayerGradLaneThreads : kLayerThreads)
+__global__ void __launch_bounds__(LANE ? kLayerGradLaneThreads : kLayerThreads, 1)
 layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice, int stages,
                        unsigned* status) {
   using P = Pack<T, VE>;
@@ -565,9 +568,10 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   const int first = LANE ? threadIdx.x & (tpr - 1) : threadIdx.x;
   const int step = LANE ? tpr : blockDim.x;
   const int group = LANE ? threadIdx.x / tpr : 0;
-  const int64_t tiles_all = (a.rows + rows_per - 1) / rows_per;
-  const int64_t tiles = tiles_all > part ? (tiles_all - part + a.parts - 1) / a.parts : 0;
-  const int slot_bytes = rows_per * slice * 16;
+  const int tiles_all = static_cast<int>((a.rows + rows_per - 1) / rows_per);
+  const int tiles = tiles_all > part ? (tiles_all - part + a.parts - 1) / a.parts : 0;
+  const int slot_bytes = layer_slot_bytes<T, VE>(rows_per * slice);
+  const int64_t stride = static_cast<int64_t>(a.parts) * rows_per;  // rows from tile to tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kLayerStages; ++i) mbar_init(&full[i], 1);
@@ -577,27 +581,42 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   pdl_wait();
   pdl_trigger();
 
-  auto issue = [&](int64_t i, int st) {  // thread 0: tile i into stage st
-    if (count == 0) return;
-    const int64_t row = (part + i * a.parts) * rows_per;
-    const int64_t rows = a.rows - row < rows_per ? a.rows - row : rows_per;
-    const int64_t off = row * a.n + static_cast<int64_t>(lo) * VE;
-    const unsigned bytes = static_cast<unsigned>(rows * count * 16);
+  // the tile whose first row is `row`: its place in the tensors, its elements
+  auto offset = [&](int64_t row) { return row * a.n + static_cast<int64_t>(lo) * VE; };
+  auto length = [&](int64_t row) {
+    return static_cast<int>(a.rows - row < rows_per ? a.rows - row : rows_per) * count * VE;
+  };
+  auto issue = [&](int64_t row, int st) {  // thread 0: that tile into stage st
+    const int64_t off = offset(row);
+    const int len = length(row);
     unsigned char* dst = ring + st * 3 * slot_bytes;
     unsigned long long* bar = &full[st];
-    mbar_arrive_expect_tx(bar, bytes * (a.ds ? 3 : 2));
-    bulk_load(dst, a.dy + off, bytes, bar);
-    bulk_load(dst + slot_bytes, a.s + off, bytes, bar);
-    if (a.ds) bulk_load(dst + 2 * slot_bytes, a.ds + off, bytes, bar);
+    if constexpr (VE > 1) {
+      const unsigned bytes = len * static_cast<unsigned>(sizeof(T));
+      mbar_arrive_expect_tx(bar, bytes * (a.ds ? 3 : 2));
+      if (bytes == 0) return;
+      bulk_load(dst, a.dy + off, bytes, bar);
+      bulk_load(dst + slot_bytes, a.s + off, bytes, bar);
+      if (a.ds) bulk_load(dst + 2 * slot_bytes, a.ds + off, bytes, bar);
+    } else {
+      const int64_t numel = a.rows * a.n;
+      const TileBytes<T, VE> dy(a.dy, numel, off, len), s(a.s, numel, off, len),
+          ds(a.ds ? a.ds : a.s, numel, off, len);
+      mbar_arrive_expect_tx(bar, dy.bytes() + s.bytes() + (a.ds ? ds.bytes() : 0u));
+      dy.copy(dst, bar);
+      s.copy(dst + slot_bytes, bar);
+      if (a.ds) ds.copy(dst + 2 * slot_bytes, bar);
+    }
   };
+  const int64_t row0 = static_cast<int64_t>(part) * rows_per;
   if (threadIdx.x == 0)
-    for (int i = 0; i < stages && i < tiles; ++i) issue(i, i);
+    for (int i = 0; i < stages && i < tiles; ++i) issue(row0 + i * stride, i);
 
   LayerGradRow<T, M, VE, NV, BIAS> x;
   x.load_gamma(a.gamma + static_cast<int64_t>(lo) * VE, first, step, count);
   bool alive = true;
+  int64_t row = row0 + group;
   // the next row's statistics are on their way as well
-  int64_t row = static_cast<int64_t>(part) * rows_per + group;
   float mu_next = 0.0f, r_next = 0.0f;
   if (row < a.rows) {
     mu_next = a.mean[row];
@@ -605,28 +624,40 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   }
   int st = 0, before = 0;
   unsigned parity = 0;
-  for (int64_t i = 0; i < tiles; ++i) {
+  for (int i = 0; i < tiles; ++i) {
     const int nv = row < a.rows ? count : 0;
-    const int64_t base = row * a.n + static_cast<int64_t>(lo) * VE;
     const float mu = mu_next, r = r_next;
-    row += static_cast<int64_t>(a.parts) * rows_per;
-    if (row < a.rows) {
-      mu_next = a.mean[row];
-      r_next = a.inv_std[row];
+    if (row + stride < a.rows) {
+      mu_next = a.mean[row + stride];
+      r_next = a.inv_std[row + stride];
     }
-    const P* dy = reinterpret_cast<const P*>(ring + st * 3 * slot_bytes) + group * count;
-    const P* s = dy + slot_bytes / 16;
-    const P* ds = s + slot_bytes / 16;
-    if (alive && count > 0 && !mbar_wait(&full[st], parity, kLayerLimitNs)) {
+    const unsigned char* stage = ring + st * 3 * slot_bytes;
+    if (alive && !mbar_wait(&full[st], parity, kLayerLimitNs)) {
       alive = false;
       atomicExch(status, kStatusDeviceTimeout);
     }
-    float2 t = make_float2(0.0f, 0.0f);
+    float2 tg = make_float2(0.0f, 0.0f), tu = tg;
+    if constexpr (VE > 1) {
+      const P* dy = reinterpret_cast<const P*>(stage) + group * count;
+      const P* s = reinterpret_cast<const P*>(stage + slot_bytes) + group * count;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = first + k * step;
-      if (v < nv) x.take(k, dy[v], s[v], mu, r, t);
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + k * step;
+        if (v < nv) x.take(k, dy[v], s[v], mu, r, tg, tu);
+      }
+    } else {
+      const int64_t numel = a.rows * a.n, off = offset(row - group);
+      const int len = length(row - group);
+      const bool edge = off == 0 || off + len + 8 >= numel;  // copies may be cut short there
+      const TileBytes<T, VE> dy(a.dy, numel, off, len), s(a.s, numel, off, len);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + k * step, at = group * count + v;
+        if (v < nv)
+          x.take(k, dy.take(stage, at, edge), s.take(stage + slot_bytes, at, edge), mu, r, tg, tu);
+      }
     }
+    float2 t = VE == 1 ? make_float2(tg.x, tu.x) : make_float2(tg.x + tg.y, tu.x + tu.y);
     if constexpr (LANE) {
       t.x = seg_sum(t.x, tpr);
       t.y = seg_sum(t.y, tpr);
@@ -635,16 +666,33 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
       t = cta_sum2_1b(t, red[i & 1]);
     }
     // everyone is done with the tile before this one
-    if (threadIdx.x == 0 && alive && i > 0 && i - 1 + stages < tiles) issue(i - 1 + stages, before);
+    if (threadIdx.x == 0 && alive && i > 0 && i - 1 + stages < tiles)
+      issue(row - group + (stages - 1) * stride, before);
     if (csize > 1) t = cluster_sum2(t, &slot[i & 1].x, &slot[i & 1].y, csize);
     const float k1 = -r * (t.x * a.inv_n), k2 = -r * (t.y * a.inv_n);
+    T* dx = a.dx ? a.dx + offset(row) : nullptr;
+    if constexpr (VE > 1) {
+      const P* ds = reinterpret_cast<const P*>(stage + 2 * slot_bytes) + group * count;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int v = first + k * step;
-      if (v < nv)
-        x.give(k, r, k1, k2, a.ds ? ds + v : nullptr,
-               a.dx ? a.dx + base + static_cast<int64_t>(v) * VE : nullptr);
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + k * step;
+        if (v < nv) x.give(k, r, k1, k2, a.ds ? ds + v : nullptr, dx ? dx + v * VE : nullptr);
+      }
+    } else {
+      const int64_t numel = a.rows * a.n, off = offset(row - group);
+      const int len = length(row - group);
+      const bool edge = off == 0 || off + len + 8 >= numel;
+      const TileBytes<T, VE> ds(a.ds ? a.ds : a.s, numel, off, len);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + k * step;
+        if (v >= nv) continue;
+        Pack<T, VE> h;
+        if (a.ds) h = ds.take(stage + 2 * slot_bytes, group * count + v, edge);
+        x.give(k, r, k1, k2, a.ds ? &h : nullptr, dx ? dx + v : nullptr);
+      }
     }
+    row += stride;
     before = st;
     if (++st == stages) {
       st = 0;
@@ -656,21 +704,29 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
       mbar_wait(&full[i], 0, kLayerLimitNs);
       mbar_wait(&full[i], 1, kLayerLimitNs);
     }
+  const bool sums = a.dgamma || a.dbeta || a.dbias;
   if constexpr (LANE) {
-    layer_grad_lane_sums<T, M, VE, NV, BIAS>(a, x, acc, tpr);
+    if (sums) layer_grad_lane_sums<T, M, VE, NV, BIAS>(a, x, acc, tpr);
   } else {
-    float* p = a.part + static_cast<int64_t>(part) * 3 * a.n;
+    float* p = a.part + part * 3 * a.pitch;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = first + k * step;
-      if (v >= count) continue;
-      part_store<VE>(p, lo + v, a.n, x.dg[k]);
-      part_store<VE>(p + a.n, lo + v, a.n, x.db[k]);
-      if constexpr (BIAS) part_store<VE>(p + 2 * static_cast<int64_t>(a.n), lo + v, a.n, x.dc[k]);
+      if (v >= count || !sums) continue;
+      float f[VE];
+      x.elements(x.dg[k], f);
+      part_store<VE>(p, lo + v, a.n, f);
+      x.elements(x.db[k], f);
+      part_store<VE>(p + a.pitch, lo + v, a.n, f);
+      if constexpr (BIAS) {
+        x.elements(x.dc[k], f);
+        part_store<VE>(p + 2 * a.pitch, lo + v, a.n, f);
+      }
     }
     if (csize > 1) cluster_sync();  // peers may still read slot
   }
 }
+
 // Gradient, rows of any length: one CTA per row takes the two row means, keeps
 // them for the column kernel, and writes dS.
 template <typename T, typename M, int VE>
@@ -750,10 +806,10 @@ layer_grad_cols_kernel(const LayerGradArgs<T, M> a) {
       dc += d;
     }
   }
-  float* p = a.part + static_cast<int64_t>(part) * 3 * a.n + col;
+  float* p = a.part + part * 3 * a.pitch + col;
   p[0] = dg;
-  p[a.n] = db;
-  if (a.dbias) p[2 * static_cast<int64_t>(a.n)] = dc;
+  p[a.pitch] = db;
+  if (a.dbias) p[2 * a.pitch] = dc;
 }
 
 // The parts' sums added in a fixed order: a CTA takes 128 columns of one of the
@@ -770,25 +826,16 @@ layer_grad_finish_kernel(const LayerGradArgs<T, M> a) {
   if (which == 0 ? !a.dgamma : which == 1 ? !a.dbeta : !a.dbias) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kLayerFinishCols + lane * 4;
-  const int64_t pitch = 3 * static_cast<int64_t>(a.n);
-  const float* src = a.part + which * static_cast<int64_t>(a.n) + at;
+  const float* src = a.part + which * a.pitch + at;
   float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (a.n % 4 == 0 && at < a.n) {
-#pragma unroll 4
+  if (at < a.pitch) {  // what pads a row out to whole vectors is not used
+#pragma unroll 8
     for (int p = warp; p < a.parts; p += 32) {
-      const float4 v = *reinterpret_cast<const float4*>(src + p * pitch);
+      const float4 v = *reinterpret_cast<const float4*>(src + p * 3 * a.pitch);
       t.x += v.x;
       t.y += v.y;
       t.z += v.z;
       t.w += v.w;
-    }
-  } else if (at < a.n) {
-    for (int p = warp; p < a.parts; p += 32) {
-      const float* v = src + p * pitch;
-      t.x += v[0];
-      if (at + 1 < a.n) t.y += v[1];
-      if (at + 2 < a.n) t.z += v[2];
-      if (at + 3 < a.n) t.w += v[3];
     }
   }
   *reinterpret_cast<float4*>(&red[warp][lane * 4]) = t;

@@ -44,9 +44,10 @@ struct LayerGradCall {
 
 // Partial column sums a gradient call keeps: one set of (dgamma, dbeta, dbias)
 // rows per part, later added in part order (no atomics, so equal calls give
-// equal bits).  At most four parts per SM, and fewer for long rows, which fill
-// the GPU with fewer.
-constexpr int kLayerMaxParts = 608;
+// equal bits).  At most six parts per SM (CTAs of short rows; 16384 x 1024
+// bfloat16 takes 33 us with four per SM, 47 with two), fewer for long rows.
+constexpr int kLayerMaxParts = 912;
+inline int64_t layer_part_pitch(int64_t hidden) { return (hidden + 3) / 4 * 4; }
 inline int layer_grad_parts(int64_t rows, int64_t hidden) {
   int64_t p = rows;
   const int64_t most = (int64_t{1} << 24) / hidden;
@@ -56,7 +57,7 @@ inline int layer_grad_parts(int64_t rows, int64_t hidden) {
 }
 inline size_t layer_grad_workspace_bytes(int64_t rows, int64_t hidden) {
   const size_t stats = (static_cast<size_t>(rows) * 8 + 255) / 256 * 256;
-  return stats + static_cast<size_t>(layer_grad_parts(rows, hidden)) * 3 * hidden * 4;
+  return stats + static_cast<size_t>(layer_grad_parts(rows, hidden)) * 3 * layer_part_pitch(hidden) * 4;
 }
 
 cudaError_t launch_layer(const LayerCall& c, cudaStream_t stream);

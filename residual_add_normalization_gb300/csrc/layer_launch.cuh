@@ -123,8 +123,11 @@ cudaError_t launch_layer_grad_ring(Fn fn, LayerGradArgs<T, M>* a, int block, int
     const void* fn;
   };
   static PlanCache<Key, int> cache;
+  // CTAs of more than 256 threads fill an SM's registers alone; of the others
+  // two share its memory
+  const int budget = block > 256 ? 200 * 1024 : 100 * 1024;
   int stages = kLayerStages;
-  while (stages > 2 && stages * tile_bytes > 100 * 1024) --stages;
+  while (stages > 2 && stages * tile_bytes > budget) --stages;
   const int smem = tile_bytes * stages;
   Key k;
   memset(&k, 0, sizeof(k));
@@ -159,16 +162,10 @@ cudaError_t launch_layer_grad_cta(const LayerGradCall& c, LayerGradArgs<T, M>* a
   const int nvec = static_cast<int>(c.hidden / VE);
   const int slice = (nvec + csize - 1) / csize;
   const int block = ((slice + NV - 1) / NV + 31) / 32 * 32;
-  if constexpr (VE > 1) {
-    auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, false>
-                       : layer_grad_ring_kernel<T, M, VE, NV, false, false>;
-    return launch_layer_grad_ring(fn, a, block, csize, slice * 48, 0, nvec, slice, stream);
-  } else {
-    auto* fn =
-        c.dbias ? layer_grad_kernel<T, M, VE, NV, true> : layer_grad_kernel<T, M, VE, NV, false>;
-    return launch_clusters(fn, dim3(static_cast<unsigned>(a->parts * csize)), block, csize, 0,
-                           stream, *a, nvec);
-  }
+  auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, false>
+                     : layer_grad_ring_kernel<T, M, VE, NV, false, false>;
+  return launch_layer_grad_ring(fn, a, block, csize, 3 * layer_slot_bytes<T, VE>(slice), 0, nvec,
+                                slice, stream);
 }
 
 template <typename T, typename M, int VE, int NV>
@@ -177,18 +174,13 @@ cudaError_t launch_layer_grad_lane(const LayerGradCall& c, LayerGradArgs<T, M>* 
   const int nvec = static_cast<int>(c.hidden / VE);
   int tpr = 1;
   while (tpr * NV < nvec) tpr *= 2;
-  const int64_t per = kLayerGradLaneThreads / tpr, blocks = (c.rows + per - 1) / per;
+  const int per = kLayerGradLaneThreads / tpr;
+  const int64_t blocks = (c.rows + per - 1) / per;
   if (a->parts > blocks) a->parts = static_cast<int>(blocks);
-  if constexpr (VE > 1) {
-    auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, true>
-                       : layer_grad_ring_kernel<T, M, VE, NV, false, true>;
-    return launch_layer_grad_ring(fn, a, kLayerGradLaneThreads, 1,
-                                  static_cast<int>(per) * nvec * 48, tpr, nvec, nvec, stream);
-  } else {
-    auto* fn = c.dbias ? layer_grad_lane_kernel<T, M, VE, NV, true>
-                       : layer_grad_lane_kernel<T, M, VE, NV, false>;
-    return launch_pdl(fn, dim3(a->parts), kLayerGradLaneThreads, stream, *a, tpr, nvec);
-  }
+  auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, true>
+                     : layer_grad_ring_kernel<T, M, VE, NV, false, true>;
+  return launch_layer_grad_ring(fn, a, kLayerGradLaneThreads, 1,
+                                3 * layer_slot_bytes<T, VE>(per * nvec), tpr, nvec, nvec, stream);
 }
 
 // The gradient form that the row's length allows; sets a->parts to the parts
@@ -208,7 +200,7 @@ cudaError_t launch_layer_grad_ve(const LayerGradCall& c, LayerGradArgs<T, M>* a,
   int csize = 1;
   while (csize < kLayerMaxCluster && nvec > kSlice * csize) csize *= 2;
   if (nvec <= kSlice * csize) {
-    if (nvec <= 256) return launch_layer_grad_cta<T, M, VE, 1>(c, a, csize, stream);
+    if (nvec <= 128) return launch_layer_grad_cta<T, M, VE, 1>(c, a, csize, stream);
     if (kMost == 2 || nvec <= 512)
       return launch_layer_grad_cta<T, M, VE, 2>(c, a, csize, stream);
     return launch_layer_grad_cta<T, M, VE, kMost>(c, a, csize, stream);
@@ -233,7 +225,8 @@ cudaError_t launch_layer_grad_tm(const LayerGradCall& c, cudaStream_t stream) {
                         static_cast<M*>(c.dbeta), static_cast<T*>(c.dbias),
                         static_cast<float2*>(c.workspace),
                         reinterpret_cast<float*>(static_cast<char*>(c.workspace) + stats),
-                        layer_grad_parts(c.rows, c.hidden), 1, c.rows, static_cast<int>(c.hidden),
+                        layer_part_pitch(c.hidden), layer_grad_parts(c.rows, c.hidden), 1,
+                        c.rows, static_cast<int>(c.hidden),
                         1.0f / static_cast<float>(c.hidden)};
   cudaError_t e = cudaSuccess;
   if (c.rows > 0) {

@@ -6,6 +6,8 @@ namespace b200norm {
 
 namespace {
 
+size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
+
 template <typename T>
 cudaError_t launch_plain(const Product& p, cudaStream_t stream) {
   const PlainProduct a{p.a.p, p.b.p, p.a.ld, p.b.ld, p.a.k_contiguous, p.b.k_contiguous,
@@ -15,23 +17,80 @@ cudaError_t launch_plain(const Product& p, cudaStream_t stream) {
   return launch_pdl(linear_plain_kernel<T>, grid, 256, stream, a);
 }
 
+template <typename T, int VE>
+cudaError_t launch_rows_ve(const Product& p, cudaStream_t stream) {
+  const PlainProduct a{p.a.p, p.b.p, p.a.ld, p.b.ld, true, true, p.M, p.N, p.K, p.epi};
+  constexpr int NO = 2;
+  const dim3 grid(static_cast<unsigned>((p.N + kRowsWarps * NO - 1) / (kRowsWarps * NO)));
+  const int block = 32 * kRowsWarps;
+  if (p.M <= 1) return launch_pdl(linear_rows_kernel<T, VE, 1, NO, 8>, grid, block, stream, a);
+  if (p.M <= 2) return launch_pdl(linear_rows_kernel<T, VE, 2, NO, 4>, grid, block, stream, a);
+  if (p.M <= 4) return launch_pdl(linear_rows_kernel<T, VE, 4, NO, 4>, grid, block, stream, a);
+  return launch_pdl(linear_rows_kernel<T, VE, 8, NO, 4>, grid, block, stream, a);
+}
+
+bool vectors_ok(const Operand& o, int64_t es) {
+  return o.ld * es % 16 == 0 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0;
+}
+
+template <typename T>
+cudaError_t launch_rows(const Product& p, cudaStream_t stream) {
+  constexpr int VE = 16 / sizeof(T);
+  if (p.K % VE == 0 && vectors_ok(p.a, sizeof(T)) && vectors_ok(p.b, sizeof(T)))
+    return launch_rows_ve<T, VE>(p, stream);
+  return launch_rows_ve<T, 1>(p, stream);
+}
+
 template <typename T>
 cudaError_t launch_dz(const LinearDzCall& c, cudaStream_t stream) {
-  const unsigned stripes = static_cast<unsigned>((c.out + 255) / 256);
-  const int parts = c.rows > 0 ? linear_db_parts(c.rows) : 0;
+  constexpr int VE = 16 / sizeof(T);
+  const int parts = c.rows > 0 ? linear_db_parts(c.rows, c.out) : 0;
   cudaError_t e = cudaSuccess;
-  if (parts > 0) e = launch_pdl(linear_dz_kernel<T>, dim3(stripes, parts), 256, stream, c, parts);
+  if (parts > 0) {
+    const Operand dy{c.dy, c.out, true}, z{c.z, c.out, true}, dz{c.dz, c.ldz, true};
+    const bool vec =
+        vectors_ok(dy, sizeof(T)) && vectors_ok(z, sizeof(T)) && vectors_ok(dz, sizeof(T));
+    const int cols = 32 * (vec ? VE : 1);
+    const dim3 grid(static_cast<unsigned>((c.out + cols - 1) / cols), parts);
+    e = vec ? launch_pdl(linear_dz_kernel<T, VE>, grid, 32 * kDzWarps, stream, c, parts)
+            : launch_pdl(linear_dz_kernel<T, 1>, grid, 32 * kDzWarps, stream, c, parts);
+  }
   if (e == cudaSuccess && c.db)
-    e = launch_pdl(linear_db_kernel<T>, dim3(stripes), 256, stream,
-                   static_cast<const float*>(c.part), static_cast<T*>(c.db), c.out, parts);
+    e = launch_pdl(linear_db_kernel<T>, dim3(static_cast<unsigned>((c.out + 31) / 32)), 1024,
+                   stream, static_cast<const float*>(c.part), static_cast<T*>(c.db), c.out, parts);
   return e;
+}
+
+template <typename T>
+cudaError_t launch_pack_t(const void* src, void* dst, int64_t rows, int64_t n,
+                          cudaStream_t stream) {
+  const int64_t words = pitch16(n) / 8;
+  int64_t grid = (rows * words + 255) / 256;
+  if (grid > 152 * 16) grid = 152 * 16;
+  return launch_pdl(linear_pack_kernel<T>, dim3(static_cast<unsigned>(grid)), 256, stream,
+                    static_cast<const T*>(src), static_cast<T*>(dst), rows, n, words);
+}
+
+// (n, k)-shaped dense rows of src to rows pitch16(n) apart at dst.
+cudaError_t launch_pack(DType t, const void* src, void* dst, int64_t rows, int64_t n,
+                        cudaStream_t stream) {
+  return t == DType::F16 ? launch_pack_t<__half>(src, dst, rows, n, stream)
+                         : launch_pack_t<__nv_bfloat16>(src, dst, rows, n, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream) {
-  if (mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0)
-    return launch_mma(p, stream);
+  const bool mma = mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0;
+  if (p.a.k_contiguous && p.b.k_contiguous && !(mma && p.forced.cg) &&
+      p.M <= (mma ? kFewRows : kFewRowsScalar)) {
+    switch (p.t) {
+      case DType::F32: return launch_rows<float>(p, stream);
+      case DType::F16: return launch_rows<__half>(p, stream);
+      default: return launch_rows<__nv_bfloat16>(p, stream);
+    }
+  }
+  if (mma) return launch_mma(p, stream);
   switch (p.t) {
     case DType::F32: return launch_plain<float>(p, stream);
     case DType::F16: return launch_plain<__half>(p, stream);
@@ -47,47 +106,78 @@ cudaError_t launch_linear_dz(const LinearDzCall& c, cudaStream_t stream) {
   }
 }
 
-namespace {
-size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
-}  // namespace
-
-LinearPlan linear_plan(int64_t, int64_t, int64_t, DType, bool) { return {0}; }
-
-LinearGradPlan linear_grad_plan(int64_t rows, int64_t, int64_t out, DType t, int act, bool) {
-  LinearGradPlan p;
-  p.dz = 0;
-  p.part = act != kActNone ? round_256(static_cast<size_t>(rows) * out * dtype_size(t)) : 0;
-  p.bytes = p.part + round_256(static_cast<size_t>(linear_db_parts(rows)) * out * 4);
+LinearPlan linear_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {
+  LinearPlan p = {};
+  p.pack = t != DType::F32 && (in % 8 != 0 || !aligned16) && rows > kFewRowsScalar;
+  if (p.pack) {
+    p.w = round_256(static_cast<size_t>(rows) * pitch16(in) * 2);
+    p.bytes = p.w + round_256(static_cast<size_t>(out) * pitch16(in) * 2);
+  }
   return p;
 }
 
-cudaError_t launch_linear(const LinearCall& c, const LinearPlan&, cudaStream_t stream) {
-  const Product p{{c.x, c.in, true}, {c.w, c.in, true}, c.rows, c.out, c.in,
-                  {c.bias, c.residual, c.y, c.z, c.act}, c.t, c.forced};
+LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, int act,
+                                bool aligned16) {
+  LinearGradPlan p = {};
+  const bool half = t != DType::F32;
+  p.make_dz = act != kActNone || (half && (out % 8 != 0 || !aligned16));
+  p.pack = half && (in % 8 != 0 || !aligned16);
+  p.ldz = half ? pitch16(out) : out;
+  const size_t dz = p.make_dz ? static_cast<size_t>(rows) * p.ldz * dtype_size(t) : 0;
+  p.part = round_256(dz);
+  p.x = p.part + round_256(static_cast<size_t>(linear_db_parts(rows, out)) * out * 4);
+  p.w = p.x + (p.pack ? round_256(static_cast<size_t>(rows) * pitch16(in) * 2) : 0);
+  p.bytes = p.w + (p.pack ? round_256(static_cast<size_t>(out) * pitch16(in) * 2) : 0);
+  return p;
+}
+
+cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStream_t stream) {
+  Operand x{c.x, c.in, true}, w{c.w, c.in, true};
+  if (plan.pack) {
+    char* ws = static_cast<char*>(c.workspace);
+    cudaError_t e = launch_pack(c.t, c.x, ws + plan.x, c.rows, c.in, stream);
+    if (e == cudaSuccess) e = launch_pack(c.t, c.w, ws + plan.w, c.out, c.in, stream);
+    if (e != cudaSuccess) return e;
+    x = {ws + plan.x, pitch16(c.in), true};
+    w = {ws + plan.w, pitch16(c.in), true};
+  }
+  const Product p{x, w, c.rows, c.out, c.in, {c.bias, c.residual, c.y, c.z, c.act}, c.t, c.forced};
   return launch_product(p, stream);
 }
 
 cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& plan,
                                cudaStream_t stream) {
   char* ws = static_cast<char*>(c.workspace);
-  const bool act = c.act != kActNone;
-  void* dz = act && (c.dx || c.dw) ? ws + plan.dz : nullptr;
+  void* made = plan.make_dz && (c.dx || c.dw) ? ws + plan.dz : nullptr;
   cudaError_t e = cudaSuccess;
-  if (dz || c.db) {
-    const LinearDzCall d{c.dy, c.z, dz, c.out, c.db, reinterpret_cast<float*>(ws + plan.part),
+  if (made || c.db) {
+    const LinearDzCall d{c.dy, c.z, made, plan.ldz, c.db, reinterpret_cast<float*>(ws + plan.part),
                          c.rows, c.out, c.act, c.t};
     e = launch_linear_dz(d, stream);
     if (e != cudaSuccess) return e;
   }
-  const void* g = act ? dz : c.dy;
+  const void* dz = plan.make_dz ? made : c.dy;
+  const int64_t ldz = plan.make_dz ? plan.ldz : c.out;
   if (c.dx && c.rows > 0) {
-    const Product p{{g, c.out, true}, {c.w, c.in, false}, c.rows, c.in, c.out,
+    Operand w{c.w, c.in, false};
+    if (plan.pack) {
+      e = launch_pack(c.t, c.w, ws + plan.w, c.out, c.in, stream);
+      if (e != cudaSuccess) return e;
+      w = {ws + plan.w, pitch16(c.in), false};
+    }
+    const Product p{{dz, ldz, true}, w, c.rows, c.in, c.out,
                     {nullptr, nullptr, c.dx, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);
     if (e != cudaSuccess) return e;
   }
   if (c.dw) {
-    const Product p{{g, c.out, false}, {c.x, c.in, false}, c.out, c.in, c.rows,
+    Operand x{c.x, c.in, false};
+    if (plan.pack && c.rows > 0) {
+      e = launch_pack(c.t, c.x, ws + plan.x, c.rows, c.in, stream);
+      if (e != cudaSuccess) return e;
+      x = {ws + plan.x, pitch16(c.in), false};
+    }
+    const Product p{{dz, ldz, false}, x, c.out, c.in, c.rows,
                     {nullptr, nullptr, c.dw, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);
   }

@@ -74,15 +74,19 @@ struct LinearDzCall {
   void* dz;
   int64_t ldz;
   void* db;
-  float* part;         // [linear_db_parts(rows)][out]
+  float* part;         // [linear_db_parts(rows, out)][out]
   int64_t rows, out;
   int act;
   DType t;
 };
-// Parts of the column sums: at least 16 rows in each, at most 64 parts.
-inline int linear_db_parts(int64_t rows) {
-  const int64_t p = (rows + 15) / 16;
-  return static_cast<int>(p < 1 ? 1 : p > 64 ? 64 : p);
+// Parts of the column sums: enough CTAs to fill the GPU (a CTA has 256 columns of
+// a 16-bit type), at least 32 rows in each.
+inline int linear_db_parts(int64_t rows, int64_t out) {
+  int64_t p = (152 * 8 * 256 + out - 1) / out;
+  const int64_t most = (rows + 31) / 32;
+  if (p > most) p = most;
+  if (p > 1024) p = 1024;
+  return static_cast<int>(p < 1 ? 1 : p);
 }
 cudaError_t launch_linear_dz(const LinearDzCall& c, cudaStream_t stream);
 
@@ -115,12 +119,22 @@ struct LinearGradCall {
   MmaPlan forced;
 };
 
-// What a call keeps in its workspace: offsets, and the bytes in all.
+// What a call keeps in its workspace: offsets, and the bytes in all.  Operands
+// of 16-bit types whose rows do not start on 16-byte boundaries are copied to
+// rows that do (`pitch` elements apart), except for few rows of x, where the
+// weight is read once and not worth a copy.
+constexpr int64_t kFewRows = 4;         // rows that the row kernel takes: aligned 16-bit,
+constexpr int64_t kFewRowsScalar = 8;   // and unaligned or float32 ones
+inline int64_t pitch16(int64_t n) { return (n + 7) / 8 * 8; }
 struct LinearPlan {
-  size_t bytes;
+  bool pack;              // x and weight are copied
+  size_t x, w, bytes;
 };
 struct LinearGradPlan {
-  size_t dz, part, bytes;  // dz: rows x out elements (with an activation)
+  bool make_dz;           // dz is stored: with an activation, or to realign dy
+  bool pack;              // x and weight are copied
+  int64_t ldz;
+  size_t dz, part, x, w, bytes;
 };
 // aligned16: x and weight (and dy) start on 16-byte boundaries.
 LinearPlan linear_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);

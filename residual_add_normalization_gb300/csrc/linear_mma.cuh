@@ -59,15 +59,20 @@ struct MmaArgs {
   unsigned long long limit_ns;
 };
 
-template <int CG, int BN>
+// Shared memory of a CTA: the ring, then 8 KB for each epilogue warp's results
+// (unless SWAP).  Two small CTAs share an SM.
+constexpr int kMmaStageRows = 32 * 128;  // 32 rows of 64 results, 128 bytes each
+template <int CG, int BN, bool SWAP>
 struct MmaShape {
   static constexpr int kBRows = BN / CG;                 // of B, per CTA
   static constexpr int kBBytes = kBRows * kMmaK * 2;
   static constexpr int kStageBytes = kMmaABytes + kBBytes;
-  static constexpr int kBudget = BN <= 64 ? 100 * 1024 : 200 * 1024;  // two small CTAs per SM
+  static constexpr int kOut = SWAP ? 0 : 4 * 2 * kMmaStageRows;
+  static constexpr int kBudget = (BN <= 64 ? 112 * 1024 : 225 * 1024) - kOut;
   static constexpr int kStages = kBudget / kStageBytes > 8 ? 8 : kBudget / kStageBytes;
+  static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;  // two buffers of columns
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes;
+  static constexpr size_t kSmem = 1024 + kRing + kOut;
 };
 
 // -- instructions ---------------------------------------------------------------
@@ -186,6 +191,28 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         :: "r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
+// 32 rows of 64 results from shared memory (written by this warp's lanes, then
+// stage_ready() and a warp barrier) to (x, y) of the tensor; what lies past its
+// edges is not stored.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               :: "l"(map), "r"(x), "r"(y), "r"(smem_addr(src)) : "memory");
+}
+__device__ __forceinline__ void stage_ready() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// This thread's stores, all but the latest N groups, have read their source.
+template <int N>
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory");
+}
+__device__ __forceinline__ void stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // A shared-memory operand's descriptor: 128-byte swizzle.  KC: rows of 128
 // bytes, eight of them (1024 bytes) a group; `lead` is not used.  Otherwise
 // the same groups hold 64 of m / n by eight of k, `lead` bytes lie between
@@ -206,53 +233,163 @@ __host__ __device__ constexpr unsigned mma_idesc(bool bf16, bool a_kc, bool b_kc
 
 // -- epilogue -------------------------------------------------------------------
 
-// NC consecutive columns n.. of row m of the result (row-major, N columns).
+// z and y of N results (bias and residual already widened, or absent).
+template <typename T, int NC>
+__device__ __forceinline__ void add_to(float (&v)[NC], const T* p) {
+  float f[NC];
+  unpack(ld_reuse<T, NC>(p), f);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) v[i] += f[i];
+}
+
+// A warp's 32 rows m0.. of a tile, BN columns n0.., whole 16-byte vectors: 64
+// columns at a time to shared memory (a lane per row; the 16-byte chunks of a row
+// permuted by the row, as the tensor copy's 128-byte swizzle has them, so that
+// eight lanes never meet in a bank) and from there by tensor copies.  Stored
+// straight from the registers, a lane per row, each instruction touches 32 lines.
+// The residual comes the other way through the same buffer.
+// `drained` is called once the sums have been read.
+template <typename T, int BN, bool FULL, class Drained, class GiveUp>
+__device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMap* map_y,
+                                              const CUtensorMap* map_z, const CUtensorMap* map_r,
+                                              unsigned d, int64_t m0, int64_t n0, int lane,
+                                              unsigned char* stage, unsigned long long* bar,
+                                              unsigned& phase, Drained&& drained,
+                                              GiveUp&& give_up) {
+  const T* bias = FULL ? static_cast<const T*>(g.e.bias) : nullptr;
+  const bool res = FULL && g.e.residual, keep = FULL && g.e.z;
+  const bool rows = m0 < g.M;
+#pragma unroll 1
+  for (int c = 0; c < BN / 64; ++c) {
+    const int64_t n = n0 + c * 64;
+    const bool some = rows && n < g.N;
+    unsigned char* at_y = stage + (keep ? 0 : (c & 1) * kMmaStageRows);
+    unsigned char* at_z = stage + kMmaStageRows;
+    if (lane == 0) {
+      if (keep) stores_read<0>();
+      else stores_read<1>();
+      if (res && some) {
+        mbar_arrive_expect_tx(bar, kMmaStageRows);
+        tma_load<1>(at_y, map_r, static_cast<int>(n), static_cast<int>(m0), smem_addr(bar));
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      tmem_load32(d + c * 64 + h * 32, v);
+      if (c == BN / 64 - 1 && h == 1) drained();
+      if (!some) continue;
+      if (res && h == 0) {
+        if (!mbar_wait(bar, phase, g.limit_ns) && lane == 0) give_up();
+        phase ^= 1;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = v[j * 8 + i];
+        const int64_t col = n + h * 32 + j * 8;
+        const int chunk = ((h * 4 + j) ^ (lane & 7)) * 16 + lane * 128;
+        if constexpr (FULL) {
+          if (bias && col < g.N) add_to<T, 8>(f, bias + col);
+          if (keep) *reinterpret_cast<Pack<T, 8>*>(at_z + chunk) = pack_from<T, 8>(f);
+          with_act(g.e.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = act_value<decltype(act)::value>(f[i]);
+          });
+          if (res) {
+            float r[8];
+            unpack(*reinterpret_cast<const Pack<T, 8>*>(at_y + chunk), r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += r[i];
+          }
+        }
+        *reinterpret_cast<Pack<T, 8>*>(at_y + chunk) = pack_from<T, 8>(f);
+      }
+    }
+    if (!some) continue;
+    stage_ready();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store(map_y, at_y, static_cast<int>(n), static_cast<int>(m0));
+      if (keep) tma_store(map_z, at_z, static_cast<int>(n), static_cast<int>(m0));
+      store_commit();
+    }
+  }
+}
+
+// The same where rows are not whole vectors: 32 columns at a time are turned
+// around in shared memory, so that a warp's lanes hold neighbouring columns.
+template <typename T, int BN, bool FULL, class Drained>
+__device__ __forceinline__ void epilogue_tile_scalar(const MmaArgs& g, unsigned d, int64_t m0,
+                                                     int64_t n0, int lane, float* stage,
+                                                     Drained&& drained) {
+  const T* bias = FULL ? static_cast<const T*>(g.e.bias) : nullptr;
+  const T* res = FULL ? static_cast<const T*>(g.e.residual) : nullptr;
+  T* y = static_cast<T*>(g.e.y);
+  T* z = FULL ? static_cast<T*>(g.e.z) : nullptr;
+  const int rows = g.M - m0 < 32 ? (g.M > m0 ? static_cast<int>(g.M - m0) : 0) : 32;
+#pragma unroll 1
+  for (int c = 0; c < BN; c += 32) {
+    float v[32];
+    tmem_load32(d + c, v);
+    if (c + 32 == BN) drained();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) stage[lane * 33 + i] = v[i];
+    __syncwarp();
+    const int64_t n = n0 + c + lane;
+    if (n < g.N) {
+      const float b = bias ? to_f32(bias[n]) : 0.0f;
+      const int64_t at = m0 * g.N + n;
+      auto run = [&](auto act) {
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+          float f = stage[r * 33 + lane];
+          if (bias) f += b;
+          if (z) z[at + r * g.N] = from_f32<T>(f);
+          f = act_value<decltype(act)::value>(f);
+          if (res) f += to_f32(res[at + r * g.N]);
+          y[at + r * g.N] = from_f32<T>(f);
+        }
+      };
+      if constexpr (FULL) with_act(g.e.act, run);
+      else run(Const<kActNone>());
+    }
+    __syncwarp();
+  }
+}
+
+// NC consecutive columns n.. of row m of the result, straight from registers.
 template <typename T, int NC>
 __device__ __forceinline__ void epilogue_row(const Epilogue& e, bool vec, int64_t m, int64_t n,
                                              int64_t N, float (&v)[NC]) {
-  constexpr int V = 8;
   const T* bias = static_cast<const T*>(e.bias);
   const T* res = static_cast<const T*>(e.residual);
   T* y = static_cast<T*>(e.y);
   T* z = static_cast<T*>(e.z);
   const int64_t at = m * N + n;
-  if (vec && NC % V == 0 && n + NC <= N) {
+  with_act(e.act, [&](auto act) {
+    if (vec && n + NC <= N) {
+      if (bias) add_to<T, NC>(v, bias + n);
+      if (z) *reinterpret_cast<Pack<T, NC>*>(z + at) = pack_from<T, NC>(v);
 #pragma unroll
-    for (int j = 0; j < NC / V; ++j) {
-      float f[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = v[j * V + i];
-      if (bias) {
-        float bf[V];
-        unpack(ld_reuse<T, V>(bias + n + j * V), bf);
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] += bf[i];
-      }
-      if (z) *reinterpret_cast<Pack<T, V>*>(z + at + j * V) = pack_from<T, V>(f);
-      if (e.act != kActNone) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = act_value(f[i], e.act);
-      }
-      if (res) {
-        float rf[V];
-        unpack(ld_stream<T, V>(res + at + j * V), rf);
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] += rf[i];
-      }
-      *reinterpret_cast<Pack<T, V>*>(y + at + j * V) = pack_from<T, V>(f);
+      for (int i = 0; i < NC; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
+      if (res) add_to<T, NC>(v, res + at);
+      *reinterpret_cast<Pack<T, NC>*>(y + at) = pack_from<T, NC>(v);
+      return;
     }
-    return;
-  }
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    if (n + i >= N) continue;
-    float f = v[i];
-    if (bias) f += to_f32(bias[n + i]);
-    if (z) z[at + i] = from_f32<T>(f);
-    f = act_value(f, e.act);
-    if (res) f += to_f32(res[at + i]);
-    y[at + i] = from_f32<T>(f);
-  }
+    for (int i = 0; i < NC; ++i) {
+      if (n + i >= N) continue;
+      float f = v[i];
+      if (bias) f += to_f32(bias[n + i]);
+      if (z) z[at + i] = from_f32<T>(f);
+      f = act_value<decltype(act)::value>(f);
+      if (res) f += to_f32(res[at + i]);
+      y[at + i] = from_f32<T>(f);
+    }
+  });
 }
 
 // NC consecutive rows (tokens) m.. of column n of the result: lanes hold
@@ -265,35 +402,46 @@ __device__ __forceinline__ void epilogue_col(const Epilogue& e, int64_t m, int64
   T* y = static_cast<T*>(e.y);
   T* z = static_cast<T*>(e.z);
   const float b = bias ? to_f32(bias[n]) : 0.0f;
+  float r[NC];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    if (m + i >= M) continue;
-    const int64_t at = (m + i) * N + n;
-    float f = v[i];
-    if (bias) f += b;
-    if (z) z[at] = from_f32<T>(f);
-    f = act_value(f, e.act);
-    if (res) f += to_f32(res[at]);
-    y[at] = from_f32<T>(f);
-  }
+  for (int i = 0; i < NC; ++i)  // on their way together
+    r[i] = res && m + i < M ? to_f32(res[(m + i) * N + n]) : 0.0f;
+  with_act(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if (m + i >= M) continue;
+      const int64_t at = (m + i) * N + n;
+      float f = v[i];
+      if (bias) f += b;
+      if (z) z[at] = from_f32<T>(f);
+      f = act_value<decltype(act)::value>(f);
+      if (res) f += r[i];
+      y[at] = from_f32<T>(f);
+    }
+  });
 }
 
 // -- kernel ---------------------------------------------------------------------
 
 // The sites recorded when a wait gives up.
-enum MmaSite { kSiteEmpty = 1, kSiteFull = 2, kSiteSums = 3, kSiteDrained = 4 };
+enum MmaSite { kSiteEmpty = 1, kSiteFull = 2, kSiteSums = 3, kSiteDrained = 4, kSiteResidual = 5 };
 
 template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP>
 __global__ void __launch_bounds__(kMmaThreads)
 linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
-                  const __grid_constant__ CUtensorMap map_b, const MmaArgs g) {
-  using S = MmaShape<CG, BN>;
+                  const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_y,
+                  const __grid_constant__ CUtensorMap map_z,
+                  const __grid_constant__ CUtensorMap map_r, const MmaArgs g) {
+  using S = MmaShape<CG, BN, SWAP>;
+  constexpr bool kFull = A_KC && B_KC;  // the gradients' products are stored as they are
   constexpr int kStages = S::kStages;
   constexpr bool kBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   extern __shared__ unsigned char raw[];
   // the swizzle counts from 1024-byte boundaries
   unsigned char* ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
-  __shared__ alignas(8) unsigned long long full[kStages], empty[kStages], sums[2], drained[2];
+  __shared__ alignas(8) unsigned long long full[kStages], empty[kStages], sums[2], drained[2],
+      fetched[4];
   __shared__ unsigned tmem_slot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -309,6 +457,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       mbar_init(&sums[i], 1);
       mbar_init(&drained[i], 4 * CG);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&fetched[i], 1);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc<CG>(&tmem_slot, S::kTmem);
@@ -424,6 +573,8 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
   } else {
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
     const int row = quarter * 32 + lane;
+    unsigned char* stage = ring + S::kRing + quarter * 2 * kMmaStageRows;  // not SWAP
+    unsigned phase = 0;
     int n = 0;
     for (int t = unit; t < tiles; t += units, ++n) {
       const int buf = n & 1;
@@ -435,8 +586,8 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       tc_fence_after();
       int tm, tn;
       tile_at(t, tm, tn);
-      const int64_t m =
-          static_cast<int64_t>(tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kMmaRows + row;
+      const int64_t m0 =
+          static_cast<int64_t>(tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kMmaRows;
       const int64_t n0 = static_cast<int64_t>(tn) * BN;
       const unsigned d = tmem + buf * BN + (static_cast<unsigned>(quarter * 32) << 16);
       if (g.splits > 1) {
@@ -459,35 +610,45 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
         }
         break;  // one tile per cluster
       }
-      if constexpr (BN >= 32) {
-#pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
-          float v[32];
-          tmem_load32(d + c, v);
-          if (m < g.M) {
-            if constexpr (SWAP) epilogue_col<T, 32>(g.e, n0 + c, g.N, m, g.M, v);
-            else epilogue_row<T, 32>(g.e, g.vec, m, n0 + c, g.N, v);
+      auto release = [&] {  // the sums have been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) {
+            mbar_arrive(&drained[buf]);
+          } else {
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                         :: "r"(cluster_addr(&drained[buf], 0)) : "memory");
           }
         }
-      } else {
-        float v[16];
-        tmem_load16(d, v);
-        if (m < g.M) {
-          if constexpr (SWAP) epilogue_col<T, 16>(g.e, n0, g.N, m, g.M, v);
-          else epilogue_row<T, 16>(g.e, g.vec, m, n0, g.N, v);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 1) {
-          mbar_arrive(&drained[buf]);
+      };
+      if constexpr (SWAP) {
+        const int64_t m = m0 + row;
+        if constexpr (BN >= 32) {
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            float v[32];
+            tmem_load32(d + c, v);
+            if (m < g.M) epilogue_col<T, 32>(g.e, n0 + c, g.N, m, g.M, v);
+            __syncwarp();
+          }
         } else {
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                       :: "r"(cluster_addr(&drained[buf], 0)) : "memory");
+          float v[16];
+          tmem_load16(d, v);
+          if (m < g.M) epilogue_col<T, 16>(g.e, n0, g.N, m, g.M, v);
         }
+        release();
+      } else if (g.vec) {
+        epilogue_tile<T, BN, kFull>(g, &map_y, &map_z, &map_r, d, m0 + quarter * 32, n0, lane,
+                                    stage, &fetched[quarter], phase, release,
+                                    [&] { give_up(kSiteResidual); });
+      } else {
+        epilogue_tile_scalar<T, BN, kFull>(g, d, m0 + quarter * 32, n0, lane,
+                                           reinterpret_cast<float*>(stage), release);
       }
     }
+    if constexpr (!SWAP)
+      if (lane == 0) stores_done();
   }
   __syncwarp();
 
@@ -503,7 +664,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       const int64_t m = static_cast<int64_t>(tm) * kMmaRows + row;
       const int64_t n0 = static_cast<int64_t>(tn) * BN;
       const float* mine = reinterpret_cast<const float*>(ring);
-      constexpr int NC = BN >= 64 ? 8 : 2;
+      constexpr int NC = !SWAP ? 8 : 2;
       for (int c = c0; c < c0 + cols; c += NC) {
         float v[NC] = {};
         for (int r = 0; r < g.splits; ++r) {

@@ -15,29 +15,35 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeFn tensor_map_encoder();
 
-// Boxes of `rows` by 64 of k (k contiguous), or squares of 64 by 64; what lies
-// past an edge reads as zero.
+// Boxes of `rows` rows by 64; what lies past an edge reads as zero and is not
+// stored.  An operand: of `rows` by 64 of k (k contiguous), or squares of 64 by 64.
 template <typename T>
-bool encode_operand(CUtensorMap* map, const Operand& o, int64_t n, int64_t k, int rows) {
+bool encode_rows(CUtensorMap* map, const void* p, int64_t inner, int64_t outer, int64_t ld,
+                 int rows) {
   EncodeFn fn = tensor_map_encoder();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.k_contiguous ? k : n),
-                              static_cast<cuuint64_t>(o.k_contiguous ? n : k)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.ld) * sizeof(T)};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(o.k_contiguous ? rows : 64)};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * sizeof(T)};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)};
   const cuuint32_t one[2] = {1, 1};
   constexpr CUtensorMapDataType type = std::is_same<T, __half>::value
                                            ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return fn(map, type, 2, const_cast<void*>(o.p), dims, strides, box, one,
+  return fn(map, type, 2, const_cast<void*>(p), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+bool encode_operand(CUtensorMap* map, const Operand& o, int64_t n, int64_t k, int rows) {
+  return o.k_contiguous ? encode_rows<T>(map, o.p, k, n, o.ld, rows)
+                        : encode_rows<T>(map, o.p, n, k, o.ld, 64);
 }
 
 template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP>
 cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
                              cudaStream_t stream) {
-  using S = MmaShape<CG, BN>;
+  using S = MmaShape<CG, BN, SWAP>;
   auto* fn = linear_mma_kernel<T, CG, BN, A_KC, B_KC, SWAP>;
   const Operand& a = SWAP ? p.b : p.a;
   const Operand& b = SWAP ? p.a : p.b;
@@ -60,6 +66,13 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   if (!encode_operand<T>(&map_a, a, g.M, p.K, kMmaRows) ||
       !encode_operand<T>(&map_b, b, g.N, p.K, S::kBRows))
     return cudaErrorInvalidValue;
+  CUtensorMap map_y = {}, map_z = {}, map_r = {};
+  if (!SWAP && g.vec && g.splits == 1) {  // results go by tensor copies
+    const bool ok = encode_rows<T>(&map_y, p.epi.y, p.N, p.M, p.N, 32) &&
+                    (!p.epi.z || encode_rows<T>(&map_z, p.epi.z, p.N, p.M, p.N, 32)) &&
+                    (!p.epi.residual || encode_rows<T>(&map_r, p.epi.residual, p.N, p.M, p.N, 32));
+    if (!ok) return cudaErrorInvalidValue;
+  }
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -96,7 +109,7 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   }
   cfg.attrs = attr;
   cfg.numAttrs = add_pdl_attr(attr, n);
-  return cudaLaunchKernelEx(&cfg, fn, map_a, map_b, g);
+  return cudaLaunchKernelEx(&cfg, fn, map_a, map_b, map_y, map_z, map_r, g);
 }
 
 template <typename T, bool A_KC, bool B_KC>

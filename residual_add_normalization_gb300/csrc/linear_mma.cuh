@@ -2,14 +2,14 @@
 // (tcgen05, sm_103a), for 16-bit types.
 //
 // C[m, n] = sum_k A[m, k] B[n, k], 128 rows of C per CTA and BN columns per
-// tile.  Six warps:
+// tile.  Six warps, or ten:
 //
 //   warp 0   copies a 64-deep slice of both operands per stage into a ring of
 //            shared-memory stages (TMA, 128-byte swizzle), a full / empty
 //            mbarrier pair per stage;
 //   warp 1   one thread issues the matrix instructions of a stage and commits
 //            them to its empty barrier; the binary32 sums stay in tensor memory;
-//   warps 2-5  read a finished tile's sums (each warp its quarter of the 128
+//   the rest read a finished tile's sums (each warp its quarter of the 128
 //            lanes), apply the epilogue and store.
 //
 // The tile's sums are double-buffered in tensor memory, so that the epilogue of
@@ -42,7 +42,6 @@
 
 namespace b200norm {
 
-constexpr int kMmaThreads = 192;
 constexpr int kMmaK = 64;              // elements of k per stage: 128 bytes
 constexpr int kMmaRows = 128;          // rows of C per CTA
 constexpr int kMmaABytes = kMmaRows * kMmaK * 2;
@@ -67,7 +66,13 @@ struct MmaShape {
   static constexpr int kBRows = BN / CG;                 // of B, per CTA
   static constexpr int kBBytes = kBRows * kMmaK * 2;
   static constexpr int kStageBytes = kMmaABytes + kBBytes;
-  static constexpr int kOut = SWAP ? 0 : 4 * 2 * kMmaStageRows;
+  // warps of the epilogue: a quarter of the lanes each, and of the wide tiles
+  // half of the columns (with four, 16384 x 512 x 512 bf16 took 15.4 us, 12.6
+  // with eight)
+  static constexpr int kWarps = BN >= 128 ? 8 : 4;
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kCols = BN / (kWarps / 4);
+  static constexpr int kOut = SWAP ? 0 : kWarps * 2 * kMmaStageRows;
   static constexpr int kBudget = (BN <= 64 ? 112 * 1024 : 225 * 1024) - kOut;
   static constexpr int kStages = kBudget / kStageBytes > 8 ? 8 : kBudget / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
@@ -77,25 +82,27 @@ struct MmaShape {
 
 // -- instructions ---------------------------------------------------------------
 
+// One warp (of each CTA of a pair) takes the columns, and gives up the right to
+// take more at once: the SM's other CTAs wait for that right.
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(unsigned* dst, unsigned cols) {
-  if constexpr (CG == 1)
+  if constexpr (CG == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_addr(dst)), "r"(cols) : "memory");
-  else
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_addr(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
 }
 
 template <int CG>
 __device__ __forceinline__ void tmem_free(unsigned addr, unsigned cols) {
-  if constexpr (CG == 1) {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  if constexpr (CG == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols));
-  } else {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  else
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols));
-  }
 }
 
 __device__ __forceinline__ void tc_fence_before() {
@@ -242,33 +249,35 @@ __device__ __forceinline__ void add_to(float (&v)[NC], const T* p) {
   for (int i = 0; i < NC; ++i) v[i] += f[i];
 }
 
-// A warp's 32 rows m0.. of a tile, BN columns n0.., whole 16-byte vectors: 64
+// A warp's 32 rows m0.. of a tile, COLS columns n0.., whole 16-byte vectors: 64
 // columns at a time to shared memory (a lane per row; the 16-byte chunks of a row
 // permuted by the row, as the tensor copy's 128-byte swizzle has them, so that
 // eight lanes never meet in a bank) and from there by tensor copies.  Stored
 // straight from the registers, a lane per row, each instruction touches 32 lines.
 // The residual comes the other way through the same buffer.
 // `drained` is called once the sums have been read.
-template <typename T, int BN, bool FULL, class Drained, class GiveUp>
+template <typename T, int COLS, bool FULL, int ACT, class Drained, class GiveUp>
 __device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMap* map_y,
                                               const CUtensorMap* map_z, const CUtensorMap* map_r,
                                               unsigned d, int64_t m0, int64_t n0, int lane,
                                               unsigned char* stage, unsigned long long* bar,
-                                              unsigned& phase, Drained&& drained,
-                                              GiveUp&& give_up) {
+                                              unsigned& phase, unsigned& turn,
+                                              Drained&& drained, GiveUp&& give_up) {
   const T* bias = FULL ? static_cast<const T*>(g.e.bias) : nullptr;
   const bool res = FULL && g.e.residual, keep = FULL && g.e.z;
   const bool rows = m0 < g.M;
 #pragma unroll 1
-  for (int c = 0; c < BN / 64; ++c) {
+  for (int c = 0; c < COLS / 64; ++c) {
     const int64_t n = n0 + c * 64;
     const bool some = rows && n < g.N;
-    unsigned char* at_y = stage + (keep ? 0 : (c & 1) * kMmaStageRows);
+    // the two buffers take turns, from tile to tile as well: the one that the
+    // latest store still reads is not this one
+    unsigned char* at_y = stage + (keep ? 0 : turn * kMmaStageRows);
     unsigned char* at_z = stage + kMmaStageRows;
-    if (lane == 0) {
+    if (lane == 0 && some) {
       if (keep) stores_read<0>();
       else stores_read<1>();
-      if (res && some) {
+      if (res) {
         mbar_arrive_expect_tx(bar, kMmaStageRows);
         tma_load<1>(at_y, map_r, static_cast<int>(n), static_cast<int>(m0), smem_addr(bar));
       }
@@ -278,37 +287,51 @@ __device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMa
     for (int h = 0; h < 2; ++h) {
       float v[32];
       tmem_load32(d + c * 64 + h * 32, v);
-      if (c == BN / 64 - 1 && h == 1) drained();
+      if (c == COLS / 64 - 1 && h == 1) drained();
       if (!some) continue;
-      if (res && h == 0) {
-        if (!mbar_wait(bar, phase, g.limit_ns) && lane == 0) give_up();
-        phase ^= 1;
-      }
+      const int64_t col = n + h * 32;
+      // the row's chunk j of these 32 columns
+      auto chunk = [&](int j) { return ((h * 4 + j) ^ (lane & 7)) * 16 + lane * 128; };
+      if (bias) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float f[8];
+        for (int j = 0; j < 4; ++j) {
+          if (col + j * 8 >= g.N) continue;
+          float b[8];
+          unpack(ld_reuse<T, 8>(bias + col + j * 8), b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = v[j * 8 + i];
-        const int64_t col = n + h * 32 + j * 8;
-        const int chunk = ((h * 4 + j) ^ (lane & 7)) * 16 + lane * 128;
-        if constexpr (FULL) {
-          if (bias && col < g.N) add_to<T, 8>(f, bias + col);
-          if (keep) *reinterpret_cast<Pack<T, 8>*>(at_z + chunk) = pack_from<T, 8>(f);
-          with_act(g.e.act, [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = act_value<decltype(act)::value>(f[i]);
-          });
-          if (res) {
-            float r[8];
-            unpack(*reinterpret_cast<const Pack<T, 8>*>(at_y + chunk), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += r[i];
-          }
+          for (int i = 0; i < 8; ++i) v[j * 8 + i] += b[i];
         }
-        *reinterpret_cast<Pack<T, 8>*>(at_y + chunk) = pack_from<T, 8>(f);
       }
+      auto put = [&](unsigned char* at) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = v[j * 8 + i];
+          *reinterpret_cast<Pack<T, 8>*>(at + chunk(j)) = pack_from<T, 8>(f);
+        }
+      };
+      if (keep) put(at_z);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
+      if (res) {
+        if (h == 0) {
+          if (!mbar_wait(bar, phase, g.limit_ns) && lane == 0) give_up();
+          phase ^= 1;
+          __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float r[8];
+          unpack(*reinterpret_cast<const Pack<T, 8>*>(at_y + chunk(j)), r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[j * 8 + i] += r[i];
+        }
+      }
+      put(at_y);
     }
     if (!some) continue;
+    turn ^= 1;
     stage_ready();
     __syncwarp();
     if (lane == 0) {
@@ -321,7 +344,7 @@ __device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMa
 
 // The same where rows are not whole vectors: 32 columns at a time are turned
 // around in shared memory, so that a warp's lanes hold neighbouring columns.
-template <typename T, int BN, bool FULL, class Drained>
+template <typename T, int COLS, bool FULL, class Drained>
 __device__ __forceinline__ void epilogue_tile_scalar(const MmaArgs& g, unsigned d, int64_t m0,
                                                      int64_t n0, int lane, float* stage,
                                                      Drained&& drained) {
@@ -331,10 +354,10 @@ __device__ __forceinline__ void epilogue_tile_scalar(const MmaArgs& g, unsigned 
   T* z = FULL ? static_cast<T*>(g.e.z) : nullptr;
   const int rows = g.M - m0 < 32 ? (g.M > m0 ? static_cast<int>(g.M - m0) : 0) : 32;
 #pragma unroll 1
-  for (int c = 0; c < BN; c += 32) {
+  for (int c = 0; c < COLS; c += 32) {
     float v[32];
     tmem_load32(d + c, v);
-    if (c + 32 == BN) drained();
+    if (c + 32 == COLS) drained();
 #pragma unroll
     for (int i = 0; i < 32; ++i) stage[lane * 33 + i] = v[i];
     __syncwarp();
@@ -427,7 +450,7 @@ __device__ __forceinline__ void epilogue_col(const Epilogue& e, int64_t m, int64
 enum MmaSite { kSiteEmpty = 1, kSiteFull = 2, kSiteSums = 3, kSiteDrained = 4, kSiteResidual = 5 };
 
 template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP>
-__global__ void __launch_bounds__(kMmaThreads)
+__global__ void __launch_bounds__(MmaShape<CG, BN, SWAP>::kThreads)
 linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_y,
@@ -441,7 +464,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
   // the swizzle counts from 1024-byte boundaries
   unsigned char* ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   __shared__ alignas(8) unsigned long long full[kStages], empty[kStages], sums[2], drained[2],
-      fetched[4];
+      fetched[S::kWarps];
   __shared__ unsigned tmem_slot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -455,9 +478,9 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sums[i], 1);
-      mbar_init(&drained[i], 4 * CG);
+      mbar_init(&drained[i], S::kWarps * CG);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&fetched[i], 1);
+    for (int i = 0; i < S::kWarps; ++i) mbar_init(&fetched[i], 1);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc<CG>(&tmem_slot, S::kTmem);
@@ -573,8 +596,9 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
   } else {
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
     const int row = quarter * 32 + lane;
-    unsigned char* stage = ring + S::kRing + quarter * 2 * kMmaStageRows;  // not SWAP
-    unsigned phase = 0;
+    const int c0 = (warp - 2) / 4 * S::kCols;  // this warp's columns of a tile: c0, kCols of them
+    unsigned char* stage = ring + S::kRing + (warp - 2) * 2 * kMmaStageRows;  // not SWAP
+    unsigned phase = 0, turn = 0;
     int n = 0;
     for (int t = unit; t < tiles; t += units, ++n) {
       const int buf = n & 1;
@@ -589,18 +613,18 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       const int64_t m0 =
           static_cast<int64_t>(tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kMmaRows;
       const int64_t n0 = static_cast<int64_t>(tn) * BN;
-      const unsigned d = tmem + buf * BN + (static_cast<unsigned>(quarter * 32) << 16);
+      const unsigned d = tmem + buf * BN + c0 + (static_cast<unsigned>(quarter * 32) << 16);
       if (g.splits > 1) {
         // to shared memory (every copy and matrix instruction on it is done),
         // a column of 128 rows after another
         float* mine = reinterpret_cast<float*>(ring);
         if constexpr (BN >= 32) {
 #pragma unroll
-          for (int c = 0; c < BN; c += 32) {
+          for (int c = 0; c < S::kCols; c += 32) {
             float v[32];
             tmem_load32(d + c, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mine[(c + i) * kMmaRows + row] = v[i];
+            for (int i = 0; i < 32; ++i) mine[(c0 + c + i) * kMmaRows + row] = v[i];
           }
         } else {
           float v[16];
@@ -639,11 +663,15 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
         }
         release();
       } else if (g.vec) {
-        epilogue_tile<T, BN, kFull>(g, &map_y, &map_z, &map_r, d, m0 + quarter * 32, n0, lane,
-                                    stage, &fetched[quarter], phase, release,
-                                    [&] { give_up(kSiteResidual); });
+        auto run = [&](auto act) {
+          epilogue_tile<T, S::kCols, kFull, decltype(act)::value>(
+              g, &map_y, &map_z, &map_r, d, m0 + quarter * 32, n0 + c0, lane, stage,
+              &fetched[warp - 2], phase, turn, release, [&] { give_up(kSiteResidual); });
+        };
+        if constexpr (kFull) with_act(g.e.act, run);
+        else run(Const<kActNone>());
       } else {
-        epilogue_tile_scalar<T, BN, kFull>(g, d, m0 + quarter * 32, n0, lane,
+        epilogue_tile_scalar<T, S::kCols, kFull>(g, d, m0 + quarter * 32, n0 + c0, lane,
                                            reinterpret_cast<float*>(stage), release);
       }
     }
@@ -655,10 +683,11 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
   if (CG == 1 && g.splits > 1) {
     cluster_sync();
     if (warp >= 2 && unit < tiles) {
-      // this rank's columns, summed over the ranks in order
+      // this rank's columns (this warp's share of them), summed over the ranks in
+      // order
       const int row = (warp & 3) * 32 + lane;
-      const int cols = BN / g.splits;
-      const int c0 = static_cast<int>(rank) * cols;
+      const int cols = BN / g.splits / (S::kWarps / 4);
+      const int c0 = static_cast<int>(rank) * (BN / g.splits) + (warp - 2) / 4 * cols;
       int tm, tn;
       tile_at(unit, tm, tn);
       const int64_t m = static_cast<int64_t>(tm) * kMmaRows + row;

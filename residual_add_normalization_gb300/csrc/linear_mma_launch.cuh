@@ -96,7 +96,7 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
-  cfg.blockDim = dim3(kMmaThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
   unsigned n = 0;

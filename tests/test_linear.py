@@ -284,10 +284,12 @@ def test_every_tiling_for_few_rows(rows, bn, splits, t):
     check_forward(d, "gelu", True, True, True)
 
 
-def test_more_tiles_than_ctas():
-    """Several tiles per CTA pair: both buffers of sums, in turn."""
+@pytest.mark.parametrize("tiling", [(2, 256), (1, 128), (1, 64)])
+@pytest.mark.parametrize("keep,residual", [(False, False), (False, True), (True, False)])
+def test_more_tiles_than_ctas(tiling, keep, residual):
+    """Several tiles per CTA: the buffers of sums and of results in turn, also
+    past the last column's edge (a 64-column piece of a tile is left out)."""
     d = make(2600, 136, 4360, "bf16", 13)
-    assert b2.library().b200norm_testing_force_linear(2, 256, 1, 0) == 0
-    check_forward(d, "none", True, False, False)
-    assert b2.library().b200norm_testing_force_linear(1, 64, 1, 0) == 0
-    check_forward(d, "none", True, False, False)
+    assert b2.library().b200norm_testing_force_linear(*tiling, 1, 0) == 0
+    for _ in range(3):
+        check_forward(d, "none", True, residual, keep)

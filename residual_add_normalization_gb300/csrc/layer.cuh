@@ -16,6 +16,7 @@
 
 #include "bulk.cuh"
 #include "common.cuh"
+#include "pair.cuh"
 
 namespace b200norm {
 
@@ -333,37 +334,6 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
     if (a.inv_std) a.inv_std[blockIdx.x] = r;
   }
 }
-
-// ---------------------------------------------------------------------------
-// Two binary32 operations in one instruction, each rounded as by itself.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ unsigned long long pair_bits(float2 v) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
-  return r;
-}
-__device__ __forceinline__ float2 bits_pair(unsigned long long v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-  return bits_pair(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-  return bits_pair(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
-  return bits_pair(r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // ---------------------------------------------------------------------------
 // Gradient in one pass: a row's g = dy * gamma and u = (S - mu) * r are held in

@@ -6,31 +6,56 @@ namespace b200norm {
 
 namespace {
 
+// Tiles of 128 x 128 from which the plain product takes them.
+constexpr int64_t kPlainLargeTiles = 128;
+
 size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
+
+bool vectors_ok(const Operand& o, int64_t es) {
+  return o.ld * es % 16 == 0 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0;
+}
+
+PlainProduct plain_args(const Product& p) {
+  const int64_t es = static_cast<int64_t>(dtype_size(p.t));
+  return {p.a.p, p.b.p, p.a.ld, p.b.ld, vectors_ok(p.a, es), vectors_ok(p.b, es),
+          p.M, p.N, p.K, p.epi};
+}
+
+template <typename T, int TILE>
+cudaError_t launch_plain_tile(const Product& p, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((p.M + TILE - 1) / TILE),
+                  static_cast<unsigned>((p.N + TILE - 1) / TILE));
+  const int block = PlainShape<TILE>::kThreads;
+  const PlainProduct a = plain_args(p);
+  if (p.a.k_contiguous)
+    return p.b.k_contiguous
+               ? launch_pdl(linear_plain_kernel<T, TILE, true, true>, grid, block, stream, a)
+               : launch_pdl(linear_plain_kernel<T, TILE, true, false>, grid, block, stream, a);
+  return launch_pdl(linear_plain_kernel<T, TILE, false, false>, grid, block, stream, a);
+}
 
 template <typename T>
 cudaError_t launch_plain(const Product& p, cudaStream_t stream) {
-  const PlainProduct a{p.a.p, p.b.p, p.a.ld, p.b.ld, p.a.k_contiguous, p.b.k_contiguous,
-                       p.M, p.N, p.K, p.epi};
-  const dim3 grid(static_cast<unsigned>((p.M + kPlainTile - 1) / kPlainTile),
-                  static_cast<unsigned>((p.N + kPlainTile - 1) / kPlainTile));
-  return launch_pdl(linear_plain_kernel<T>, grid, 256, stream, a);
+  if constexpr (sizeof(T) == 4) {
+    // large tiles once they fill the GPU
+    if ((p.M + 127) / 128 * ((p.N + 127) / 128) >= kPlainLargeTiles)
+      return launch_plain_tile<T, 128>(p, stream);
+  }
+  return launch_plain_tile<T, 64>(p, stream);
 }
 
 template <typename T, int VE>
 cudaError_t launch_rows_ve(const Product& p, cudaStream_t stream) {
-  const PlainProduct a{p.a.p, p.b.p, p.a.ld, p.b.ld, true, true, p.M, p.N, p.K, p.epi};
-  constexpr int NO = 2;
-  const dim3 grid(static_cast<unsigned>((p.N + kRowsWarps * NO - 1) / (kRowsWarps * NO)));
-  const int block = 32 * kRowsWarps;
-  if (p.M <= 1) return launch_pdl(linear_rows_kernel<T, VE, 1, NO, 8>, grid, block, stream, a);
-  if (p.M <= 2) return launch_pdl(linear_rows_kernel<T, VE, 2, NO, 4>, grid, block, stream, a);
-  if (p.M <= 4) return launch_pdl(linear_rows_kernel<T, VE, 4, NO, 4>, grid, block, stream, a);
-  return launch_pdl(linear_rows_kernel<T, VE, 8, NO, 4>, grid, block, stream, a);
-}
-
-bool vectors_ok(const Operand& o, int64_t es) {
-  return o.ld * es % 16 == 0 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0;
+  const PlainProduct a = plain_args(p);
+  auto go = [&](auto* fn, int no) {
+    const int64_t per = static_cast<int64_t>(kRowsWarps) * no;
+    return launch_pdl(fn, dim3(static_cast<unsigned>((p.N + per - 1) / per)), 32 * kRowsWarps,
+                      stream, a);
+  };
+  if (p.M <= 1) return go(linear_rows_kernel<T, VE, 1, 1, 8>, 1);
+  if (p.M <= 2) return go(linear_rows_kernel<T, VE, 2, 2, 4>, 2);
+  if (p.M <= 4) return go(linear_rows_kernel<T, VE, 4, 2, 4>, 2);
+  return go(linear_rows_kernel<T, VE, 8, 2, 4>, 2);
 }
 
 template <typename T>

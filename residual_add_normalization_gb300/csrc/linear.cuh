@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "linear.h"
+#include "pair.cuh"
 
 namespace b200norm {
 
@@ -105,79 +106,153 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 // ---------------------------------------------------------------------------
-// Plain tiled product: any sizes, strides and alignment, binary32 sums.  A CTA
-// of 256 threads makes a 64 x 64 tile, 4 x 4 per thread, through shared memory.
+// Tiled product on the binary32 units: float32 operands, and 16-bit ones for
+// which the tensor cores have nothing to do (an empty sum).  Any sizes, strides
+// and alignment; binary32 sums, k in order.  A CTA makes a TILE x TILE tile, 8
+// rows by 8 (TILE 128) or 4 (64) columns per thread, two products per
+// instruction; operand slices of 16 of k pass through two shared-memory buffers,
+// the next slice on its way from global memory meanwhile.  Bound by the binary32
+// units: 8 + 8 values from shared memory feed 64 products.
 // ---------------------------------------------------------------------------
 struct PlainProduct {
   const void* a;
   const void* b;
   int64_t lda, ldb;
-  bool a_kc, b_kc;
+  bool a_vec, b_vec;   // rows are whole 16-byte vectors
   int64_t M, N, K;
   Epilogue e;
 };
 
-constexpr int kPlainTile = 64;
 constexpr int kPlainK = 16;
 
-template <typename T>
-__device__ __forceinline__ float plain_elem(const T* p, int64_t ld, bool kc, int64_t i, int64_t k,
-                                            int64_t ni, int64_t nk) {
-  if (i >= ni || k >= nk) return 0.0f;
-  return to_f32(kc ? p[i * ld + k] : p[k * ld + i]);
-}
+template <int TILE>
+struct PlainShape {
+  static constexpr int kThreads = TILE == 128 ? 256 : 128;
+  static constexpr int kCols = TILE == 128 ? 8 : 4;   // per thread
+  static constexpr int kQuads = TILE * kPlainK / 4 / kThreads;  // of an operand, per thread
+  static constexpr int kPitch = TILE + 4;
+};
 
-template <typename T>
-__global__ void __launch_bounds__(256) linear_plain_kernel(const PlainProduct p) {
+// One operand's slice [16][TILE] (k major) by way of registers.
+template <typename T, int TILE, bool KC>
+struct PlainSlice {
+  using S = PlainShape<TILE>;
+  float4 q[S::kQuads];
+
+  // quad u of this thread: four of k (KC) or four of i, from (i, k) on
+  __device__ __forceinline__ static void place(int u, int& i, int& k) {
+    const int id = threadIdx.x + u * S::kThreads;
+    if constexpr (KC) {
+      i = id / (kPlainK / 4);
+      k = id % (kPlainK / 4) * 4;
+    } else {
+      i = id % (TILE / 4) * 4;
+      k = id / (TILE / 4);
+    }
+  }
+
+  __device__ __forceinline__ void load(const T* p, int64_t ld, bool vec, int64_t i0, int64_t k0,
+                                       int64_t ni, int64_t nk) {
+#pragma unroll
+    for (int u = 0; u < S::kQuads; ++u) {
+      int di, dk;
+      place(u, di, dk);
+      const int64_t i = i0 + di, k = k0 + dk;
+      const bool in = KC ? (i < ni && k + 3 < nk) : (k < nk && i + 3 < ni);
+      if constexpr (sizeof(T) == 4) {
+        if (vec && in) {
+          q[u] = __ldg(reinterpret_cast<const float4*>(p + (KC ? i * ld + k : k * ld + i)));
+          continue;
+        }
+      }
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t ie = KC ? i : i + e, ke = KC ? k + e : k;
+        f[e] = ie < ni && ke < nk ? to_f32(p[KC ? ie * ld + ke : ke * ld + ie]) : 0.0f;
+      }
+      q[u] = make_float4(f[0], f[1], f[2], f[3]);
+    }
+  }
+
+  __device__ __forceinline__ void put(float (*s)[S::kPitch]) const {
+#pragma unroll
+    for (int u = 0; u < S::kQuads; ++u) {
+      int i, k;
+      place(u, i, k);
+      if constexpr (KC) {
+        s[k][i] = q[u].x;
+        s[k + 1][i] = q[u].y;
+        s[k + 2][i] = q[u].z;
+        s[k + 3][i] = q[u].w;
+      } else {
+        *reinterpret_cast<float4*>(&s[k][i]) = q[u];
+      }
+    }
+  }
+};
+
+template <typename T, int TILE, bool A_KC, bool B_KC>
+__global__ void __launch_bounds__(PlainShape<TILE>::kThreads)
+linear_plain_kernel(const PlainProduct p) {
+  using S = PlainShape<TILE>;
+  constexpr int C = S::kCols;
   pdl_wait();
   pdl_trigger();
-  __shared__ float as[kPlainK][kPlainTile + 4], bs[kPlainK][kPlainTile + 4];
+  __shared__ float as[2][kPlainK][S::kPitch], bs[2][kPlainK][S::kPitch];
   const T* a = static_cast<const T*>(p.a);
   const T* b = static_cast<const T*>(p.b);
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kPlainTile;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kPlainTile;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * TILE;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * TILE;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < p.K; k0 += kPlainK) {
-#pragma unroll
-    for (int j = 0; j < kPlainTile * kPlainK / 256; ++j) {
-      const int e = threadIdx.x + j * 256;
-      // neighbouring threads take neighbouring elements of the contiguous index
-      const int ai = p.a_kc ? e / kPlainK : e % kPlainTile;
-      const int ak = p.a_kc ? e % kPlainK : e / kPlainTile;
-      as[ak][ai] = plain_elem(a, p.lda, p.a_kc, m0 + ai, k0 + ak, p.M, p.K);
-      const int bi = p.b_kc ? e / kPlainK : e % kPlainTile;
-      const int bk = p.b_kc ? e % kPlainK : e / kPlainTile;
-      bs[bk][bi] = plain_elem(b, p.ldb, p.b_kc, n0 + bi, k0 + bk, p.N, p.K);
+  // rows ty * 4 + {0..3} of both halves of the tile (TILE 64: of 32 rows each);
+  // columns tx * 4 + {0..3}, of both halves with eight
+  constexpr int kHalf = TILE / 2;
+  float2 acc[8][C / 2] = {};
+  PlainSlice<T, TILE, A_KC> qa;
+  PlainSlice<T, TILE, B_KC> qb;
+  qa.load(a, p.lda, p.a_vec, m0, 0, p.M, p.K);
+  qb.load(b, p.ldb, p.b_vec, n0, 0, p.N, p.K);
+  int buf = 0;
+  for (int64_t k0 = 0; k0 < p.K; k0 += kPlainK, buf ^= 1) {
+    qa.put(as[buf]);
+    qb.put(bs[buf]);
+    __syncthreads();  // and everyone has left the other buffer
+    if (k0 + kPlainK < p.K) {
+      qa.load(a, p.lda, p.a_vec, m0, k0 + kPlainK, p.M, p.K);
+      qb.load(b, p.ldb, p.b_vec, n0, k0 + kPlainK, p.N, p.K);
     }
-    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kPlainK; ++k) {
-      float av[4], bv[4];
+      float av[8];
+      float2 bv[C / 2];
+      *reinterpret_cast<float4*>(av) = *reinterpret_cast<const float4*>(&as[buf][k][ty * 4]);
+      *reinterpret_cast<float4*>(av + 4) =
+          *reinterpret_cast<const float4*>(&as[buf][k][kHalf + ty * 4]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        av[i] = as[k][ty * 4 + i];
-        bv[i] = bs[k][tx * 4 + i];
+      for (int h = 0; h < C / 4; ++h) {
+        const float4 t = *reinterpret_cast<const float4*>(&bs[buf][k][h * kHalf + tx * 4]);
+        bv[2 * h] = make_float2(t.x, t.y);
+        bv[2 * h + 1] = make_float2(t.z, t.w);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        for (int j = 0; j < C / 2; ++j) acc[i][j] = fma2(both(av[i]), bv[j], acc[i][j]);
     }
-    __syncthreads();
   }
   const T* bias = static_cast<const T*>(p.e.bias);
   const T* res = static_cast<const T*>(p.e.residual);
   with_act(p.e.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t m = m0 + (i / 4) * kHalf + ty * 4 + i % 4;
       if (m >= p.M) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t n = n0 + tx * 4 + j;
+      for (int j = 0; j < C; ++j) {
+        const int64_t n = n0 + (j / 4) * kHalf + tx * 4 + j % 4;
         if (n >= p.N) continue;
-        float z = acc[i][j];
+        float z = j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x;
         if (bias) z += to_f32(bias[n]);
         if (p.e.z) static_cast<T*>(p.e.z)[m * p.N + n] = from_f32<T>(z);
         float y = act_value<decltype(act)::value>(z);
@@ -210,7 +285,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
   const T* row[NO];
 #pragma unroll
   for (int o = 0; o < NO; ++o) row[o] = w + (n0 + o < p.N ? n0 + o : p.N - 1) * p.ldb;
-  float acc[R][NO] = {};
+  // even and odd elements apart, two products per instruction
+  float2 acc[R][NO] = {};
   for (int v0 = lane; v0 < nvec; v0 += 32 * U) {
     Pack<T, VE> q[U][NO];
 #pragma unroll
@@ -224,18 +300,19 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
     for (int u = 0; u < U; ++u) {
       const int v = v0 + 32 * u;
       if (v >= nvec) continue;
-      float wf[NO][VE];
-#pragma unroll
-      for (int o = 0; o < NO; ++o) unpack(q[u][o], wf[o]);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= p.M) continue;
-        float xf[VE];
-        unpack(ld_reuse<T, VE>(x + r * p.lda + static_cast<int64_t>(v) * VE), xf);
+        const Pack<T, VE> xv = ld_reuse<T, VE>(x + r * p.lda + static_cast<int64_t>(v) * VE);
 #pragma unroll
-        for (int o = 0; o < NO; ++o)
+        for (int o = 0; o < NO; ++o) {
+          if constexpr (VE == 1) {
+            acc[r][o].x = fmaf(to_f32(xv.v[0]), to_f32(q[u][o].v[0]), acc[r][o].x);
+          } else {
 #pragma unroll
-          for (int e = 0; e < VE; ++e) acc[r][o] = fmaf(xf[e], wf[o][e], acc[r][o]);
+            for (int i = 0; i < VE / 2; ++i) acc[r][o] = fma2(get2(xv, i), get2(q[u][o], i), acc[r][o]);
+          }
+        }
       }
     }
   }
@@ -245,7 +322,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int o = 0; o < NO; ++o) {
-      const float t = warp_sum(acc[r][o]);
+      const float t = warp_sum(acc[r][o].x + acc[r][o].y);
       if (lane == r * NO + o) mine = t;
     }
   const int r = lane / NO;

@@ -22,16 +22,13 @@ PlainProduct plain_args(const Product& p) {
 }
 
 template <typename T, int TILE>
-cudaError_t launch_plain_tile(const Product& p, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((p.M + TILE - 1) / TILE),
+cudaError_t launch_plain_tile(const Product& p, int splits, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((p.M + TILE - 1) / TILE * splits),
                   static_cast<unsigned>((p.N + TILE - 1) / TILE));
-  const int block = PlainShape<TILE>::kThreads;
-  const PlainProduct a = plain_args(p);
-  if (p.a.k_contiguous)
-    return p.b.k_contiguous
-               ? launch_pdl(linear_plain_kernel<T, TILE, true, true>, grid, block, stream, a)
-               : launch_pdl(linear_plain_kernel<T, TILE, true, false>, grid, block, stream, a);
-  return launch_pdl(linear_plain_kernel<T, TILE, false, false>, grid, block, stream, a);
+  auto* fn = !p.a.k_contiguous    ? linear_plain_kernel<T, TILE, false, false>
+             : p.b.k_contiguous ? linear_plain_kernel<T, TILE, true, true>
+                                : linear_plain_kernel<T, TILE, true, false>;
+  return launch_clusters(fn, grid, PlainShape<TILE>::kThreads, splits, 0, stream, plain_args(p));
 }
 
 template <typename T>
@@ -39,9 +36,14 @@ cudaError_t launch_plain(const Product& p, cudaStream_t stream) {
   if constexpr (sizeof(T) == 4) {
     // large tiles once they fill the GPU
     if ((p.M + 127) / 128 * ((p.N + 127) / 128) >= kPlainLargeTiles)
-      return launch_plain_tile<T, 128>(p, stream);
+      return launch_plain_tile<T, 128>(p, 1, stream);
   }
-  return launch_plain_tile<T, 64>(p, stream);
+  // K split while an SM has fewer than four tiles and a part eight slices
+  const int64_t tiles = (p.M + 63) / 64 * ((p.N + 63) / 64);
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= 4 * 152 && p.K / (splits * 2) >= 8 * kPlainK)
+    splits *= 2;
+  return launch_plain_tile<T, 64>(p, splits, stream);
 }
 
 template <typename T, int VE>
@@ -49,8 +51,9 @@ cudaError_t launch_rows_ve(const Product& p, cudaStream_t stream) {
   const PlainProduct a = plain_args(p);
   auto go = [&](auto* fn, int no) {
     const int64_t per = static_cast<int64_t>(kRowsWarps) * no;
-    return launch_pdl(fn, dim3(static_cast<unsigned>((p.N + per - 1) / per)), 32 * kRowsWarps,
-                      stream, a);
+    return launch_pdl(fn, dim3(static_cast<unsigned>((p.N + per - 1) / per),
+                               static_cast<unsigned>((p.M + 7) / 8)),
+                      32 * kRowsWarps, stream, a);
   };
   if (p.M <= 1) return go(linear_rows_kernel<T, VE, 1, 1, 8>, 1);
   if (p.M <= 2) return go(linear_rows_kernel<T, VE, 2, 2, 4>, 2);
@@ -107,8 +110,9 @@ cudaError_t launch_pack(DType t, const void* src, void* dst, int64_t rows, int64
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream) {
   const bool mma = mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0;
-  if (p.a.k_contiguous && p.b.k_contiguous && !(mma && p.forced.cg) &&
-      p.M <= (mma ? kFewRows : kFewRowsScalar)) {
+  const bool few = mma ? p.M <= kFewRows && p.N * p.K <= kFewWeights && !p.forced.cg
+                       : p.M <= (p.t == DType::F32 ? kFewRowsF32 : kFewRowsScalar);
+  if (p.a.k_contiguous && p.b.k_contiguous && few) {
     switch (p.t) {
       case DType::F32: return launch_rows<float>(p, stream);
       case DType::F16: return launch_rows<__half>(p, stream);

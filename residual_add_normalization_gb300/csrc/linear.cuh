@@ -113,6 +113,9 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 // instruction; operand slices of 16 of k pass through two shared-memory buffers,
 // the next slice on its way from global memory meanwhile.  Bound by the binary32
 // units: 8 + 8 values from shared memory feed 64 products.
+//
+// With few tiles the CTAs of a cluster each take a part of K (TILE 64) and add
+// their sums through distributed shared memory, in rank order.
 // ---------------------------------------------------------------------------
 struct PlainProduct {
   const void* a;
@@ -199,11 +202,20 @@ linear_plain_kernel(const PlainProduct p) {
   constexpr int C = S::kCols;
   pdl_wait();
   pdl_trigger();
-  __shared__ float as[2][kPlainK][S::kPitch], bs[2][kPlainK][S::kPitch];
+  __shared__ __align__(16) float slices_of[2][2][kPlainK][S::kPitch];
+  float(*as)[kPlainK][S::kPitch] = slices_of[0];
+  float(*bs)[kPlainK][S::kPitch] = slices_of[1];
   const T* a = static_cast<const T*>(p.a);
   const T* b = static_cast<const T*>(p.b);
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * TILE;
+  const unsigned csize = TILE == 64 ? cluster_size() : 1u;
+  const unsigned rank = csize > 1 ? cluster_rank() : 0u;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / csize) * TILE;
   const int64_t n0 = static_cast<int64_t>(blockIdx.y) * TILE;
+  // this CTA's part of K: whole slices
+  const int64_t slices = (p.K + kPlainK - 1) / kPlainK;
+  const int64_t k_lo = slices * rank / csize * kPlainK;
+  int64_t k_hi = slices * (rank + 1) / csize * kPlainK;
+  if (k_hi > p.K) k_hi = p.K;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   // rows ty * 4 + {0..3} of both halves of the tile (TILE 64: of 32 rows each);
   // columns tx * 4 + {0..3}, of both halves with eight
@@ -211,16 +223,16 @@ linear_plain_kernel(const PlainProduct p) {
   float2 acc[8][C / 2] = {};
   PlainSlice<T, TILE, A_KC> qa;
   PlainSlice<T, TILE, B_KC> qb;
-  qa.load(a, p.lda, p.a_vec, m0, 0, p.M, p.K);
-  qb.load(b, p.ldb, p.b_vec, n0, 0, p.N, p.K);
+  qa.load(a, p.lda, p.a_vec, m0, k_lo, p.M, k_hi);
+  qb.load(b, p.ldb, p.b_vec, n0, k_lo, p.N, k_hi);
   int buf = 0;
-  for (int64_t k0 = 0; k0 < p.K; k0 += kPlainK, buf ^= 1) {
+  for (int64_t k0 = k_lo; k0 < k_hi; k0 += kPlainK, buf ^= 1) {
     qa.put(as[buf]);
     qb.put(bs[buf]);
     __syncthreads();  // and everyone has left the other buffer
-    if (k0 + kPlainK < p.K) {
-      qa.load(a, p.lda, p.a_vec, m0, k0 + kPlainK, p.M, p.K);
-      qb.load(b, p.ldb, p.b_vec, n0, k0 + kPlainK, p.N, p.K);
+    if (k0 + kPlainK < k_hi) {
+      qa.load(a, p.lda, p.a_vec, m0, k0 + kPlainK, p.M, k_hi);
+      qb.load(b, p.ldb, p.b_vec, n0, k0 + kPlainK, p.N, k_hi);
     }
 #pragma unroll
     for (int k = 0; k < kPlainK; ++k) {
@@ -243,28 +255,60 @@ linear_plain_kernel(const PlainProduct p) {
   }
   const T* bias = static_cast<const T*>(p.e.bias);
   const T* res = static_cast<const T*>(p.e.residual);
+  // z and y of column n0 + c.. of row m0 + r, from their sums
+  auto finish = [&](auto act, int64_t m, int64_t n, float z) {
+    if (m >= p.M || n >= p.N) return;
+    if (bias) z += to_f32(bias[n]);
+    if (p.e.z) static_cast<T*>(p.e.z)[m * p.N + n] = from_f32<T>(z);
+    float y = act_value<decltype(act)::value>(z);
+    if (res) y += to_f32(res[m * p.N + n]);
+    static_cast<T*>(p.e.y)[m * p.N + n] = from_f32<T>(y);
+  };
+  if constexpr (TILE == 64) {
+    if (csize > 1) {
+      static_assert(sizeof(slices_of) >= 64 * 64 * 4, "a tile's sums fit the slices' memory");
+      float* sums = &slices_of[0][0][0][0];  // [64][64]
+      __syncthreads();  // the slices have been read
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(sums + ((i / 4) * kHalf + ty * 4 + i % 4) * 64 + tx * 4) =
+            make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+      cluster_sync();
+      with_act(p.e.act, [&](auto act) {
+        const int per = 64 * 16 / static_cast<int>(csize);  // quads of this rank
+        for (int q = threadIdx.x; q < per; q += S::kThreads) {
+          const int at = static_cast<int>(rank) * per + q;
+          float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (unsigned c = 0; c < csize; ++c) {
+            const float4 v = ld_cluster_f32x4(reinterpret_cast<const float4*>(sums) + at, c);
+            t.x += v.x;
+            t.y += v.y;
+            t.z += v.z;
+            t.w += v.w;
+          }
+          const int64_t m = m0 + at / 16, n = n0 + at % 16 * 4;
+          finish(act, m, n, t.x);
+          finish(act, m, n + 1, t.y);
+          finish(act, m, n + 2, t.z);
+          finish(act, m, n + 3, t.w);
+        }
+      });
+      cluster_sync();  // the peers may still read this CTA's sums
+      return;
+    }
+  }
   with_act(p.e.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t m = m0 + (i / 4) * kHalf + ty * 4 + i % 4;
-      if (m >= p.M) continue;
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const int64_t n = n0 + (j / 4) * kHalf + tx * 4 + j % 4;
-        if (n >= p.N) continue;
-        float z = j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x;
-        if (bias) z += to_f32(bias[n]);
-        if (p.e.z) static_cast<T*>(p.e.z)[m * p.N + n] = from_f32<T>(z);
-        float y = act_value<decltype(act)::value>(z);
-        if (res) y += to_f32(res[m * p.N + n]);
-        static_cast<T*>(p.e.y)[m * p.N + n] = from_f32<T>(y);
-      }
-    }
+      for (int j = 0; j < C; ++j)
+        finish(act, m0 + (i / 4) * kHalf + ty * 4 + i % 4, n0 + (j / 4) * kHalf + tx * 4 + j % 4,
+               j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x);
   });
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of x (at most R): bound by reading the weight once.  A warp takes NO
+// Few rows of x (R at a time): bound by reading the weight once.  A warp takes NO
 // columns of the result; its lanes share the sum, U vectors of each weight row on
 // their way at once, and the rows of x come from L1.  The binary32 sums of the
 // lanes are added by butterflies.
@@ -275,7 +319,9 @@ template <typename T, int VE, int R, int NO, int U>
 __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const PlainProduct p) {
   pdl_wait();
   pdl_trigger();
-  const T* x = static_cast<const T*>(p.a);
+  const int m0 = blockIdx.y * R;  // this CTA's rows: m0 .. m0 + R
+  const int rows = static_cast<int>(p.M) - m0;
+  const T* x = static_cast<const T*>(p.a) + m0 * p.lda;
   const T* w = static_cast<const T*>(p.b);
   const int lane = threadIdx.x & 31;
   const int64_t n0 =
@@ -302,7 +348,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
       if (v >= nvec) continue;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= p.M) continue;
+        if (r >= rows) continue;
         const Pack<T, VE> xv = ld_reuse<T, VE>(x + r * p.lda + static_cast<int64_t>(v) * VE);
 #pragma unroll
         for (int o = 0; o < NO; ++o) {
@@ -327,16 +373,17 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
     }
   const int r = lane / NO;
   const int64_t n = n0 + lane % NO;
-  if (r >= R || r >= p.M || n >= p.N) return;
+  if (r >= R || r >= rows || n >= p.N) return;
+  const int64_t at = (m0 + r) * p.N + n;
   const T* bias = static_cast<const T*>(p.e.bias);
   const T* res = static_cast<const T*>(p.e.residual);
   float z = mine;
   if (bias) z += to_f32(bias[n]);
-  if (p.e.z) static_cast<T*>(p.e.z)[r * p.N + n] = from_f32<T>(z);
+  if (p.e.z) static_cast<T*>(p.e.z)[at] = from_f32<T>(z);
   float y = 0.0f;
   with_act(p.e.act, [&](auto act) { y = act_value<decltype(act)::value>(z); });
-  if (res) y += to_f32(res[r * p.N + n]);
-  static_cast<T*>(p.e.y)[r * p.N + n] = from_f32<T>(y);
+  if (res) y += to_f32(res[at]);
+  static_cast<T*>(p.e.y)[at] = from_f32<T>(y);
 }
 
 // ---------------------------------------------------------------------------

@@ -284,6 +284,14 @@ def test_every_tiling_for_few_rows(rows, bn, splits, t):
     check_forward(d, "gelu", True, True, True)
 
 
+@pytest.mark.parametrize("shape", [(20, 4096, 24), (40, 2000, 130), (17, 300, 64), (9, 1030, 7)])
+def test_float32_sums_in_parts(shape):
+    """Few tiles and long sums: K split over clusters, and the last part ragged."""
+    d = make(*shape, "f32", 14)
+    check_forward(d, "gelu", True, True, True)
+    check_grad(d, "silu")
+
+
 @pytest.mark.parametrize("tiling", [(2, 256), (1, 128), (1, 64)])
 @pytest.mark.parametrize("keep,residual", [(False, False), (False, True), (True, False)])
 def test_more_tiles_than_ctas(tiling, keep, residual):

@@ -255,13 +255,21 @@ linear_plain_kernel(const PlainProduct p) {
   }
   const T* bias = static_cast<const T*>(p.e.bias);
   const T* res = static_cast<const T*>(p.e.residual);
-  // z and y of column n0 + c.. of row m0 + r, from their sums
-  auto finish = [&](auto act, int64_t m, int64_t n, float z) {
+  // (the gradients' products are stored as they are)
+  constexpr bool kFull = A_KC && B_KC;
+  auto before = [&](int64_t m, int64_t n, float z) {  // z of (m, n), from its sum
+    if constexpr (kFull) {
+      if (m >= p.M || n >= p.N) return z;
+      if (bias) z += to_f32(bias[n]);
+      if (p.e.z) static_cast<T*>(p.e.z)[m * p.N + n] = from_f32<T>(z);
+    }
+    return z;
+  };
+  auto after = [&](int64_t m, int64_t n, float y) {
     if (m >= p.M || n >= p.N) return;
-    if (bias) z += to_f32(bias[n]);
-    if (p.e.z) static_cast<T*>(p.e.z)[m * p.N + n] = from_f32<T>(z);
-    float y = act_value<decltype(act)::value>(z);
-    if (res) y += to_f32(res[m * p.N + n]);
+    if constexpr (kFull) {
+      if (res) y += to_f32(res[m * p.N + n]);
+    }
     static_cast<T*>(p.e.y)[m * p.N + n] = from_f32<T>(y);
   };
   if constexpr (TILE == 64) {
@@ -274,41 +282,52 @@ linear_plain_kernel(const PlainProduct p) {
         *reinterpret_cast<float4*>(sums + ((i / 4) * kHalf + ty * 4 + i % 4) * 64 + tx * 4) =
             make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
       cluster_sync();
-      with_act(p.e.act, [&](auto act) {
-        const int per = 64 * 16 / static_cast<int>(csize);  // quads of this rank
-        for (int q = threadIdx.x; q < per; q += S::kThreads) {
-          const int at = static_cast<int>(rank) * per + q;
-          float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (unsigned c = 0; c < csize; ++c) {
-            const float4 v = ld_cluster_f32x4(reinterpret_cast<const float4*>(sums) + at, c);
-            t.x += v.x;
-            t.y += v.y;
-            t.z += v.z;
-            t.w += v.w;
-          }
-          const int64_t m = m0 + at / 16, n = n0 + at % 16 * 4;
-          finish(act, m, n, t.x);
-          finish(act, m, n + 1, t.y);
-          finish(act, m, n + 2, t.z);
-          finish(act, m, n + 3, t.w);
+      const int per = 64 * 16 / static_cast<int>(csize);  // quads of this rank
+      for (int q = threadIdx.x; q < per; q += S::kThreads) {
+        const int at = static_cast<int>(rank) * per + q;
+        float t[4] = {};
+        for (unsigned c = 0; c < csize; ++c) {
+          const float4 v = ld_cluster_f32x4(reinterpret_cast<const float4*>(sums) + at, c);
+          t[0] += v.x;
+          t[1] += v.y;
+          t[2] += v.z;
+          t[3] += v.w;
         }
-      });
+        const int64_t m = m0 + at / 16, n = n0 + at % 16 * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = before(m, n + e, t[e]);
+        if constexpr (kFull)
+          with_act(p.e.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = act_value<decltype(act)::value>(t[e]);
+          });
+#pragma unroll
+        for (int e = 0; e < 4; ++e) after(m, n + e, t[e]);
+      }
       cluster_sync();  // the peers may still read this CTA's sums
       return;
     }
   }
-  with_act(p.e.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 8; ++i) {
+    const int64_t m = m0 + (i / 4) * kHalf + ty * 4 + i % 4;
+    float t[C];
 #pragma unroll
-      for (int j = 0; j < C; ++j)
-        finish(act, m0 + (i / 4) * kHalf + ty * 4 + i % 4, n0 + (j / 4) * kHalf + tx * 4 + j % 4,
-               j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x);
-  });
+    for (int j = 0; j < C; ++j)
+      t[j] = before(m, n0 + (j / 4) * kHalf + tx * 4 + j % 4,
+                    j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x);
+    if constexpr (kFull)
+      with_act(p.e.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) t[j] = act_value<decltype(act)::value>(t[j]);
+      });
+#pragma unroll
+    for (int j = 0; j < C; ++j) after(m, n0 + (j / 4) * kHalf + tx * 4 + j % 4, t[j]);
+  }
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of x (R at a time): bound by reading the weight once.  A warp takes NO
+// Few rows of x (at most R): bound by reading the weight once.  A warp takes NO
 // columns of the result; its lanes share the sum, U vectors of each weight row on
 // their way at once, and the rows of x come from L1.  The binary32 sums of the
 // lanes are added by butterflies.
@@ -319,9 +338,7 @@ template <typename T, int VE, int R, int NO, int U>
 __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const PlainProduct p) {
   pdl_wait();
   pdl_trigger();
-  const int m0 = blockIdx.y * R;  // this CTA's rows: m0 .. m0 + R
-  const int rows = static_cast<int>(p.M) - m0;
-  const T* x = static_cast<const T*>(p.a) + m0 * p.lda;
+  const T* x = static_cast<const T*>(p.a);
   const T* w = static_cast<const T*>(p.b);
   const int lane = threadIdx.x & 31;
   const int64_t n0 =
@@ -348,7 +365,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
       if (v >= nvec) continue;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= rows) continue;
+        if (r >= p.M) continue;
         const Pack<T, VE> xv = ld_reuse<T, VE>(x + r * p.lda + static_cast<int64_t>(v) * VE);
 #pragma unroll
         for (int o = 0; o < NO; ++o) {
@@ -373,8 +390,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
     }
   const int r = lane / NO;
   const int64_t n = n0 + lane % NO;
-  if (r >= R || r >= rows || n >= p.N) return;
-  const int64_t at = (m0 + r) * p.N + n;
+  if (r >= R || r >= p.M || n >= p.N) return;
+  const int64_t at = r * p.N + n;
   const T* bias = static_cast<const T*>(p.e.bias);
   const T* res = static_cast<const T*>(p.e.residual);
   float z = mine;

@@ -125,12 +125,9 @@ struct LinearGradCall {
 // weight is read once and not worth a copy.
 // Rows that the row kernel takes: aligned 16-bit ones up to 16 M weights (1 x 768 x
 // 768 2.1 us against 5.8 on the tensor cores, 1 x 4096 x 4096 11.2 against 11.1,
-// 1 x 16384 x 4096 42 against 28), unaligned ones, and float32 ones, eight at a
-// time (16 x 4096 x 4096: 303 us as a tiled product).
+// 1 x 16384 x 4096 42 against 28), and unaligned or float32 ones.
 constexpr int64_t kFewRows = 4;
 constexpr int64_t kFewWeights = int64_t{1} << 24;
-constexpr int64_t kFewRowsScalar = 8;
-constexpr int64_t kFewRowsF32 = 16;
 inline int64_t pitch16(int64_t n) { return (n + 7) / 8 * 8; }
 struct LinearPlan {
   bool pack;              // x and weight are copied

@@ -409,16 +409,34 @@ def _on(index, stream, inputs):
     return None
 
 
-def _scratch(workspace, nbytes, x):
-    """Workspace arguments: the caller's, or a block of the caching allocator
-    that goes back to it, in stream order, when the call returns."""
-    if workspace is None:
-        if not nbytes:
-            return None, 0
+# Small scratch blocks kept per thread, device and stream: a thread's work on one
+# stream is in order, so its calls may share one (the launches of two threads'
+# calls on a stream may interleave).  A block that is outgrown goes back to the
+# caching allocator, in that stream's order.
+_SCRATCH_KEPT = 32 << 20
+_scratch_of_thread = threading.local()
+
+
+def _scratch(workspace, nbytes, x, index, stream):
+    """Workspace arguments: the caller's, or a kept or new block.  A call that is
+    being captured into a graph gets a block of the graph's own, which lives as
+    long as the graph replays."""
+    if workspace is not None:
+        if workspace.device != x.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
+        return workspace, workspace.numel() * workspace.element_size()
+    if not nbytes:
+        return None, 0
+    if nbytes > _SCRATCH_KEPT or torch.cuda.is_current_stream_capturing():
         return x.new_empty(nbytes, dtype=torch.uint8), nbytes
-    if workspace.device != x.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    blocks = getattr(_scratch_of_thread, "blocks", None)
+    if blocks is None:
+        blocks = _scratch_of_thread.blocks = {}
+    block = blocks.get((index, stream))
+    if block is None or block.numel() < nbytes:
+        block = x.new_empty(max(nbytes, 1 << 20), dtype=torch.uint8)
+        blocks[(index, stream)] = block
+    return block, block.numel()
 
 
 def _like(name, t, x, index):
@@ -523,11 +541,12 @@ def skip_layer_grad(dy, s, mean, inv_std_var, gamma, *, ds=None, want_input=True
             _new("dbias", dbias, gamma.shape, dy, index) if want_bias or dbias is not None
             else None)
         need = lib.b200norm_skip_layer_grad_workspace_size(rows, hidden) if rows else 0
-        ws, n = _scratch(workspace, need, dy)
+        raw = _raw_stream(index, stream)
+        ws, n = _scratch(workspace, need, dy, index, raw)
         _check(lib.b200norm_skip_layer_grad(
             dy.data_ptr(), s.data_ptr(), mean.data_ptr(), inv_std_var.data_ptr(),
             gamma.data_ptr(), _at(ds), *map(_at, outs), rows, hidden, _DTYPES[dt],
-            _DTYPES[gamma.dtype], _at(ws), n, _raw_stream(index, stream)))
+            _DTYPES[gamma.dtype], _at(ws), n, raw))
         return outs
 
     context = _on(index, stream, (dy, s, mean, inv_std_var, gamma, ds))
@@ -570,10 +589,10 @@ def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y
         zv = _like("z", z, yv, index) if want_z or z is not None else None
         px, pw, code = x.data_ptr(), weight.data_ptr(), _DTYPES[dt]
         need = lib.b200norm_linear_workspace_size(rows, n_in, n_out, code, (px | pw) % 16 == 0)
-        ws, n = _scratch(workspace, need, x)
+        raw = _raw_stream(index, stream)
+        ws, n = _scratch(workspace, need, x, index, raw)
         _check(lib.b200norm_linear(px, pw, _at(bias), _at(residual), yv.data_ptr(), _at(zv), rows,
-                                   n_in, n_out, code, activation, _at(ws), n,
-                                   _raw_stream(index, stream)))
+                                   n_in, n_out, code, activation, _at(ws), n, raw))
         return yv, zv
 
     context = _on(index, stream, (x, weight, bias, residual))
@@ -612,10 +631,10 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
         aligned = (pd | (px if dwv is not None else 0) | (pw if dxv is not None else 0)) % 16 == 0
         need = lib.b200norm_linear_grad_workspace_size(rows, n_in, n_out, code, activation,
                                                        aligned)
-        ws, n = _scratch(workspace, need, dy)
+        raw = _raw_stream(index, stream)
+        ws, n = _scratch(workspace, need, dy, index, raw)
         _check(lib.b200norm_linear_grad(pd, px, pw, _at(z), _at(dxv), _at(dwv), _at(dbv), rows,
-                                        n_in, n_out, code, activation, _at(ws), n,
-                                        _raw_stream(index, stream)))
+                                        n_in, n_out, code, activation, _at(ws), n, raw))
         return dxv, dwv, dbv
 
     context = _on(index, stream, (dy, x, weight, z))

@@ -46,10 +46,10 @@ FAMILY_SOURCES = {
              "rows_pipe.cuh", "rows_gated.cu", "rows_ssln_f16.cu", "rows_ssln_f32.cu", "rows_bf16.cu"),
     "group": ("common.cuh", "bulk.cuh", "launch.h", "group_kernels.cuh", "group_norm.cu",
               "group_f32.cu", "group_f16.cu", "group_bf16.cu"),
-    "layer": ("common.cuh", "bulk.cuh", "pair.cuh", "launch.h", "layer.h", "layer.cuh",
-              "layer_launch.cuh", "layer_f32.cu", "layer_f16.cu", "layer_bf16.cu"),
+    "layer": ("common.cuh", "bulk.cuh", "pair.cuh", "launch.h", "launch_kernel.cuh", "layer.h",
+              "layer.cuh", "layer_launch.cuh", "layer_f32.cu", "layer_f16.cu", "layer_bf16.cu"),
     "linear": ("common.cuh", "bulk.cuh", "pair.cuh", "launch.h", "linear.h", "linear.cuh",
-               "layer_launch.cuh", "linear_launch.cuh", "linear.cu", "linear_f32.cu",
+               "launch_kernel.cuh", "linear_launch.cuh", "linear.cu", "linear_f32.cu",
                "linear_f16.cu", "linear_bf16.cu", "linear_mma.cuh", "linear_mma_launch.cuh",
                "linear_mma_f16.cu", "linear_mma_bf16.cu"),
 }

@@ -3,29 +3,26 @@
 
 namespace b200norm {
 
-extern template cudaError_t launch_plain<float>(const Product&, cudaStream_t);
 extern template cudaError_t launch_rows<float>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<float>(const LinearDzCall&, cudaStream_t);
-extern template cudaError_t launch_plain<__half>(const Product&, cudaStream_t);
 extern template cudaError_t launch_rows<__half>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__half>(const LinearDzCall&, cudaStream_t);
-extern template cudaError_t launch_pack<__half>(const void*, void*, int64_t, int64_t,
-                                                cudaStream_t);
-extern template cudaError_t launch_plain<__nv_bfloat16>(const Product&, cudaStream_t);
+extern template cudaError_t launch_pack<__half>(const void*, void*, int64_t, const void*,
+                                      void*, int64_t, int64_t, cudaStream_t);
 extern template cudaError_t launch_rows<__nv_bfloat16>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__nv_bfloat16>(const LinearDzCall&, cudaStream_t);
-extern template cudaError_t launch_pack<__nv_bfloat16>(const void*, void*, int64_t, int64_t,
-                                                       cudaStream_t);
+extern template cudaError_t launch_pack<__nv_bfloat16>(const void*, void*, int64_t, const void*,
+                                             void*, int64_t, int64_t, cudaStream_t);
 
 namespace {
 
 size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
 
-// (n, k)-shaped dense rows of src to rows pitch16(n) apart at dst.
-cudaError_t pack_rows(DType t, const void* src, void* dst, int64_t rows, int64_t n,
-                      cudaStream_t stream) {
-  return t == DType::F16 ? launch_pack<__half>(src, dst, rows, n, stream)
-                         : launch_pack<__nv_bfloat16>(src, dst, rows, n, stream);
+cudaError_t pack_rows(DType t, const void* src0, void* dst0, int64_t rows0, const void* src1,
+                      void* dst1, int64_t rows1, int64_t n, cudaStream_t stream) {
+  return t == DType::F16
+             ? launch_pack<__half>(src0, dst0, rows0, src1, dst1, rows1, n, stream)
+             : launch_pack<__nv_bfloat16>(src0, dst0, rows0, src1, dst1, rows1, n, stream);
 }
 
 }  // namespace
@@ -41,11 +38,8 @@ cudaError_t launch_product(const Product& p, cudaStream_t stream) {
     }
   }
   if (mma) return launch_mma(p, stream);
-  switch (p.t) {
-    case DType::F32: return launch_plain<float>(p, stream);
-    case DType::F16: return launch_plain<__half>(p, stream);
-    default: return launch_plain<__nv_bfloat16>(p, stream);
-  }
+  // the plans see to it that 16-bit operands of more than a few rows are aligned
+  return p.t == DType::F32 ? launch_plain_f32(p, stream) : cudaErrorMisalignedAddress;
 }
 
 cudaError_t launch_linear_dz(const LinearDzCall& c, cudaStream_t stream) {
@@ -85,8 +79,8 @@ cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStrea
   Operand x{c.x, c.in, true}, w{c.w, c.in, true};
   if (plan.pack) {
     char* ws = static_cast<char*>(c.workspace);
-    cudaError_t e = pack_rows(c.t, c.x, ws + plan.x, c.rows, c.in, stream);
-    if (e == cudaSuccess) e = pack_rows(c.t, c.w, ws + plan.w, c.out, c.in, stream);
+    const cudaError_t e = pack_rows(c.t, c.x, ws + plan.x, c.rows, c.w, ws + plan.w, c.out, c.in,
+                                    stream);
     if (e != cudaSuccess) return e;
     x = {ws + plan.x, pitch16(c.in), true};
     w = {ws + plan.w, pitch16(c.in), true};
@@ -106,27 +100,26 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& pl
     e = launch_linear_dz(d, stream);
     if (e != cudaSuccess) return e;
   }
+  if (plan.pack && c.rows > 0 && (c.dx || c.dw)) {
+    e = pack_rows(c.t, c.x, ws + plan.x, c.dw ? c.rows : 0, c.w, ws + plan.w, c.dx ? c.out : 0,
+                  c.in, stream);
+    if (e != cudaSuccess) return e;
+  }
   const void* dz = plan.make_dz ? made : c.dy;
   const int64_t ldz = plan.make_dz ? plan.ldz : c.out;
   if (c.dx && c.rows > 0) {
     Operand w{c.w, c.in, false};
-    if (plan.pack) {
-      e = pack_rows(c.t, c.w, ws + plan.w, c.out, c.in, stream);
-      if (e != cudaSuccess) return e;
-      w = {ws + plan.w, pitch16(c.in), false};
-    }
+    if (plan.pack) w = {ws + plan.w, pitch16(c.in), false};
     const Product p{{dz, ldz, true}, w, c.rows, c.in, c.out,
                     {nullptr, nullptr, c.dx, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);
     if (e != cudaSuccess) return e;
   }
+  if (c.dw && c.rows == 0)  // empty sums: the zero of every type is zero bits
+    return cudaMemsetAsync(c.dw, 0, static_cast<size_t>(c.out) * c.in * dtype_size(c.t), stream);
   if (c.dw) {
     Operand x{c.x, c.in, false};
-    if (plan.pack && c.rows > 0) {
-      e = pack_rows(c.t, c.x, ws + plan.x, c.rows, c.in, stream);
-      if (e != cudaSuccess) return e;
-      x = {ws + plan.x, pitch16(c.in), false};
-    }
+    if (plan.pack) x = {ws + plan.x, pitch16(c.in), false};
     const Product p{{dz, ldz, false}, x, c.out, c.in, c.rows,
                     {nullptr, nullptr, c.dw, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);

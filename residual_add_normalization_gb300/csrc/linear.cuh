@@ -2,6 +2,7 @@
 // derivatives, and the plain tiled product (sm_103a).
 #pragma once
 
+#include "bulk.cuh"
 #include "common.cuh"
 #include "linear.h"
 #include "pair.cuh"
@@ -106,13 +107,14 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiled product on the binary32 units: float32 operands, and 16-bit ones for
-// which the tensor cores have nothing to do (an empty sum).  Any sizes, strides
-// and alignment; binary32 sums, k in order.  A CTA makes a TILE x TILE tile, 8
-// rows by 8 (TILE 128) or 4 (64) columns per thread, two products per
-// instruction; operand slices of 16 of k pass through two shared-memory buffers,
-// the next slice on its way from global memory meanwhile.  Bound by the binary32
-// units: 8 + 8 values from shared memory feed 64 products.
+// float32 product on the binary32 units.  Any sizes, strides and alignment;
+// binary32 sums, k in order.  A CTA makes a TILE x TILE tile, 8 rows by 8 (TILE
+// 128) or 4 (64) columns per thread, two products per instruction.  Slices of 16
+// of k are copied asynchronously into a ring of shared memory, k by i whatever
+// the operand's order: 16 bytes at a time where i is contiguous and aligned, else
+// by elements.  Bound by the binary32 units: 16 values from shared memory feed 64
+// products.  (Pairs along k, which need no value twice, take 254 registers for
+// their sums and lost a third of the rate: 4096^3 3069 us.)
 //
 // With few tiles the CTAs of a cluster each take a part of K (TILE 64) and add
 // their sums through distributed shared memory, in rank order.
@@ -127,125 +129,101 @@ struct PlainProduct {
 };
 
 constexpr int kPlainK = 16;
-
+constexpr int kPlainStages = 4;
 template <int TILE>
 struct PlainShape {
   static constexpr int kThreads = TILE == 128 ? 256 : 128;
-  static constexpr int kCols = TILE == 128 ? 8 : 4;   // per thread
-  static constexpr int kQuads = TILE * kPlainK / 4 / kThreads;  // of an operand, per thread
+  static constexpr int kCols = TILE == 128 ? 8 : 4;  // per thread
   static constexpr int kPitch = TILE + 4;
+  static constexpr int kStage = 2 * kPlainK * kPitch;  // floats
+  static constexpr size_t kSmem = static_cast<size_t>(kPlainStages) * kStage * 4;
 };
 
-// One operand's slice [16][TILE] (k major) by way of registers.
-template <typename T, int TILE, bool KC>
-struct PlainSlice {
-  using S = PlainShape<TILE>;
-  float4 q[S::kQuads];
+template <int BYTES>
+__device__ __forceinline__ void copy_async(float* dst, const float* src, int valid) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(smem_addr(dst)), "l"(src), "r"(valid) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                 :: "r"(smem_addr(dst)), "l"(src), "r"(valid) : "memory");
+}
 
-  // quad u of this thread: four of k (KC) or four of i, from (i, k) on
-  __device__ __forceinline__ static void place(int u, int& i, int& k) {
-    const int id = threadIdx.x + u * S::kThreads;
-    if constexpr (KC) {
-      i = id / (kPlainK / 4);
-      k = id % (kPlainK / 4) * 4;
-    } else {
-      i = id % (TILE / 4) * 4;
-      k = id / (TILE / 4);
-    }
-  }
-
-  __device__ __forceinline__ void load(const T* p, int64_t ld, bool vec, int64_t i0, int64_t k0,
-                                       int64_t ni, int64_t nk) {
+// An operand's slice from (i0, k0) on to s[kPlainK][kPitch]; zero past ni and nk.
+template <int TILE, bool KC>
+__device__ __forceinline__ void plain_slice(float* s, const float* p, int64_t ld, bool vec,
+                                            int64_t i0, int64_t k0, int64_t ni, int64_t nk) {
+  constexpr int kThreads = PlainShape<TILE>::kThreads, kPitch = PlainShape<TILE>::kPitch;
+  if (!KC && vec) {
 #pragma unroll
-    for (int u = 0; u < S::kQuads; ++u) {
-      int di, dk;
-      place(u, di, dk);
-      const int64_t i = i0 + di, k = k0 + dk;
-      const bool in = KC ? (i < ni && k + 3 < nk) : (k < nk && i + 3 < ni);
-      if constexpr (sizeof(T) == 4) {
-        if (vec && in) {
-          q[u] = __ldg(reinterpret_cast<const float4*>(p + (KC ? i * ld + k : k * ld + i)));
-          continue;
-        }
-      }
-      float f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t ie = KC ? i : i + e, ke = KC ? k + e : k;
-        f[e] = ie < ni && ke < nk ? to_f32(p[KC ? ie * ld + ke : ke * ld + ie]) : 0.0f;
-      }
-      q[u] = make_float4(f[0], f[1], f[2], f[3]);
+    for (int u = 0; u < TILE * kPlainK / 4 / kThreads; ++u) {
+      const int id = threadIdx.x + u * kThreads, i = id % (TILE / 4) * 4, k = id / (TILE / 4);
+      const bool in = i0 + i < ni && k0 + k < nk;  // ni is whole vectors
+      copy_async<16>(s + k * kPitch + i, in ? p + (k0 + k) * ld + i0 + i : p, in ? 16 : 0);
     }
+    return;
   }
-
-  __device__ __forceinline__ void put(float (*s)[S::kPitch]) const {
 #pragma unroll
-    for (int u = 0; u < S::kQuads; ++u) {
-      int i, k;
-      place(u, i, k);
-      if constexpr (KC) {
-        s[k][i] = q[u].x;
-        s[k + 1][i] = q[u].y;
-        s[k + 2][i] = q[u].z;
-        s[k + 3][i] = q[u].w;
-      } else {
-        *reinterpret_cast<float4*>(&s[k][i]) = q[u];
-      }
-    }
+  for (int u = 0; u < TILE * kPlainK / kThreads; ++u) {
+    const int id = threadIdx.x + u * kThreads;
+    const int i = KC ? id / kPlainK : id % TILE, k = KC ? id % kPlainK : id / TILE;
+    const bool in = i0 + i < ni && k0 + k < nk;
+    copy_async<4>(s + k * kPitch + i,
+                  in ? p + (KC ? (i0 + i) * ld + k0 + k : (k0 + k) * ld + i0 + i) : p, in ? 4 : 0);
   }
-};
+}
 
-template <typename T, int TILE, bool A_KC, bool B_KC>
+template <int TILE, bool A_KC, bool B_KC>
 __global__ void __launch_bounds__(PlainShape<TILE>::kThreads)
 linear_plain_kernel(const PlainProduct p) {
   using S = PlainShape<TILE>;
-  constexpr int C = S::kCols;
+  constexpr int C = S::kCols, kHalf = TILE / 2;
+  extern __shared__ __align__(16) float ring[];
   pdl_wait();
   pdl_trigger();
-  __shared__ __align__(16) float slices_of[2][2][kPlainK][S::kPitch];
-  float(*as)[kPlainK][S::kPitch] = slices_of[0];
-  float(*bs)[kPlainK][S::kPitch] = slices_of[1];
-  const T* a = static_cast<const T*>(p.a);
-  const T* b = static_cast<const T*>(p.b);
+  const float* a = static_cast<const float*>(p.a);
+  const float* b = static_cast<const float*>(p.b);
   const unsigned csize = TILE == 64 ? cluster_size() : 1u;
   const unsigned rank = csize > 1 ? cluster_rank() : 0u;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x / csize) * TILE;
   const int64_t n0 = static_cast<int64_t>(blockIdx.y) * TILE;
   // this CTA's part of K: whole slices
   const int64_t slices = (p.K + kPlainK - 1) / kPlainK;
-  const int64_t k_lo = slices * rank / csize * kPlainK;
-  int64_t k_hi = slices * (rank + 1) / csize * kPlainK;
-  if (k_hi > p.K) k_hi = p.K;
+  const int64_t first = slices * rank / csize, count = slices * (rank + 1) / csize - first;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  // rows ty * 4 + {0..3} of both halves of the tile (TILE 64: of 32 rows each);
-  // columns tx * 4 + {0..3}, of both halves with eight
-  constexpr int kHalf = TILE / 2;
-  float2 acc[8][C / 2] = {};
-  PlainSlice<T, TILE, A_KC> qa;
-  PlainSlice<T, TILE, B_KC> qb;
-  qa.load(a, p.lda, p.a_vec, m0, k_lo, p.M, k_hi);
-  qb.load(b, p.ldb, p.b_vec, n0, k_lo, p.N, k_hi);
-  int buf = 0;
-  for (int64_t k0 = k_lo; k0 < k_hi; k0 += kPlainK, buf ^= 1) {
-    qa.put(as[buf]);
-    qb.put(bs[buf]);
-    __syncthreads();  // and everyone has left the other buffer
-    if (k0 + kPlainK < k_hi) {
-      qa.load(a, p.lda, p.a_vec, m0, k0 + kPlainK, p.M, k_hi);
-      qb.load(b, p.ldb, p.b_vec, n0, k0 + kPlainK, p.N, k_hi);
+
+  auto fetch = [&](int64_t t) {  // slice `first + t` into its stage (nothing past the last)
+    if (t < count) {
+      float* st = ring + t % kPlainStages * S::kStage;
+      const int64_t k0 = (first + t) * kPlainK;
+      plain_slice<TILE, A_KC>(st, a, p.lda, p.a_vec, m0, k0, p.M, p.K);
+      plain_slice<TILE, B_KC>(st + kPlainK * S::kPitch, b, p.ldb, p.b_vec, n0, k0, p.N, p.K);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int t = 0; t < kPlainStages - 1; ++t) fetch(t);
+  // rows ty * 4 + {0..3} and columns tx * 4 + {0..3} of a half of the tile, of
+  // both halves with eight
+  float2 acc[8][C / 2] = {};
+  for (int64_t t = 0; t < count; ++t) {
+    asm volatile("cp.async.wait_group %0;" :: "n"(kPlainStages - 2) : "memory");
+    __syncthreads();  // the slice is there for all, and the one before has been read by all
+    fetch(t + kPlainStages - 1);
+    const float* as = ring + t % kPlainStages * S::kStage + ty * 4;
+    const float* bs = ring + t % kPlainStages * S::kStage + kPlainK * S::kPitch + tx * 4;
 #pragma unroll
     for (int k = 0; k < kPlainK; ++k) {
       float av[8];
       float2 bv[C / 2];
-      *reinterpret_cast<float4*>(av) = *reinterpret_cast<const float4*>(&as[buf][k][ty * 4]);
+      *reinterpret_cast<float4*>(av) = *reinterpret_cast<const float4*>(as + k * S::kPitch);
       *reinterpret_cast<float4*>(av + 4) =
-          *reinterpret_cast<const float4*>(&as[buf][k][kHalf + ty * 4]);
+          *reinterpret_cast<const float4*>(as + k * S::kPitch + kHalf);
 #pragma unroll
       for (int h = 0; h < C / 4; ++h) {
-        const float4 t = *reinterpret_cast<const float4*>(&bs[buf][k][h * kHalf + tx * 4]);
-        bv[2 * h] = make_float2(t.x, t.y);
-        bv[2 * h + 1] = make_float2(t.z, t.w);
+        const float4 v = *reinterpret_cast<const float4*>(bs + k * S::kPitch + h * kHalf);
+        bv[2 * h] = make_float2(v.x, v.y);
+        bv[2 * h + 1] = make_float2(v.z, v.w);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -253,29 +231,42 @@ linear_plain_kernel(const PlainProduct p) {
         for (int j = 0; j < C / 2; ++j) acc[i][j] = fma2(both(av[i]), bv[j], acc[i][j]);
     }
   }
-  const T* bias = static_cast<const T*>(p.e.bias);
-  const T* res = static_cast<const T*>(p.e.residual);
-  // (the gradients' products are stored as they are)
-  constexpr bool kFull = A_KC && B_KC;
-  auto before = [&](int64_t m, int64_t n, float z) {  // z of (m, n), from its sum
-    if constexpr (kFull) {
-      if (m >= p.M || n >= p.N) return z;
-      if (bias) z += to_f32(bias[n]);
-      if (p.e.z) static_cast<T*>(p.e.z)[m * p.N + n] = from_f32<T>(z);
+  const float* bias = static_cast<const float*>(p.e.bias);
+  const float* res = static_cast<const float*>(p.e.residual);
+  float* zs = static_cast<float*>(p.e.z);
+  float* ys = static_cast<float*>(p.e.y);
+  // four columns n.. of row m, from their sums (the gradients' products are stored
+  // as they are)
+  auto finish = [&](float(&t)[4], int64_t m, int64_t n) {
+    constexpr int N = 4;
+    if (m >= p.M) return;
+    if constexpr (A_KC && B_KC) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int64_t c = n + j;
+        if (c >= p.N) continue;
+        if (bias) t[j] += bias[c];
+        if (zs) zs[m * p.N + c] = t[j];
+      }
+      with_act(p.e.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) t[j] = act_value<decltype(act)::value>(t[j]);
+      });
     }
-    return z;
-  };
-  auto after = [&](int64_t m, int64_t n, float y) {
-    if (m >= p.M || n >= p.N) return;
-    if constexpr (kFull) {
-      if (res) y += to_f32(res[m * p.N + n]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t c = n + j;
+      if (c >= p.N) continue;
+      if constexpr (A_KC && B_KC) {
+        if (res) t[j] += res[m * p.N + c];
+      }
+      ys[m * p.N + c] = t[j];
     }
-    static_cast<T*>(p.e.y)[m * p.N + n] = from_f32<T>(y);
   };
   if constexpr (TILE == 64) {
     if (csize > 1) {
-      static_assert(sizeof(slices_of) >= 64 * 64 * 4, "a tile's sums fit the slices' memory");
-      float* sums = &slices_of[0][0][0][0];  // [64][64]
+      float* sums = ring;  // [64][64]
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();  // the slices have been read
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -293,37 +284,19 @@ linear_plain_kernel(const PlainProduct p) {
           t[2] += v.z;
           t[3] += v.w;
         }
-        const int64_t m = m0 + at / 16, n = n0 + at % 16 * 4;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = before(m, n + e, t[e]);
-        if constexpr (kFull)
-          with_act(p.e.act, [&](auto act) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = act_value<decltype(act)::value>(t[e]);
-          });
-#pragma unroll
-        for (int e = 0; e < 4; ++e) after(m, n + e, t[e]);
+        finish(t, m0 + at / 16, n0 + at % 16 * 4);
       }
       cluster_sync();  // the peers may still read this CTA's sums
       return;
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t m = m0 + (i / 4) * kHalf + ty * 4 + i % 4;
-    float t[C];
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-      t[j] = before(m, n0 + (j / 4) * kHalf + tx * 4 + j % 4,
-                    j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x);
-    if constexpr (kFull)
-      with_act(p.e.act, [&](auto act) {
-#pragma unroll
-        for (int j = 0; j < C; ++j) t[j] = act_value<decltype(act)::value>(t[j]);
-      });
-#pragma unroll
-    for (int j = 0; j < C; ++j) after(m, n0 + (j / 4) * kHalf + tx * 4 + j % 4, t[j]);
-  }
+    for (int h = 0; h < C / 4; ++h) {
+      float t[4] = {acc[i][2 * h].x, acc[i][2 * h].y, acc[i][2 * h + 1].x, acc[i][2 * h + 1].y};
+      finish(t, m0 + (i / 4) * kHalf + ty * 4 + i % 4, n0 + h * kHalf + tx * 4);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -505,17 +478,31 @@ __global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, T* d
 // from the two aligned words that hold it, or, at the tensor's ends, from its
 // elements.
 // ---------------------------------------------------------------------------
+// Two operands in one launch (the second may have no rows).
 template <typename T>
-__global__ void __launch_bounds__(256) linear_pack_kernel(const T* src, T* dst, int64_t rows,
-                                                          int64_t n, int64_t words) {
+struct PackRows {
+  const T* src;
+  T* dst;
+  int64_t rows;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) linear_pack_kernel(const PackRows<T> first,
+                                                          const PackRows<T> second, int64_t n,
+                                                          int64_t words) {
   static_assert(sizeof(T) == 2, "16-bit elements");
   pdl_wait();
   pdl_trigger();
-  const uintptr_t end = reinterpret_cast<uintptr_t>(src + rows * n);
-  const int64_t total = rows * words;
+  const int64_t total = (first.rows + second.rows) * words;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = i / words, k = (i - row * words) * 8;
+    int64_t row = i / words;
+    const int64_t k = (i - row * words) * 8;
+    const bool one = row < first.rows;
+    if (!one) row -= first.rows;
+    const T* src = one ? first.src : second.src;
+    const uintptr_t end =
+        reinterpret_cast<uintptr_t>(src + (one ? first.rows : second.rows) * n);
     const T* p = src + row * n + k;
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), lo = a & ~uintptr_t{15};
     uint4 out;
@@ -539,7 +526,7 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const T* src, T* dst, 
       for (int e = 0; e < 8; ++e) v.v[e] = k + e < n ? p[e] : from_f32<T>(0.0f);
       memcpy(&out, &v, sizeof(out));
     }
-    reinterpret_cast<uint4*>(dst)[i] = out;
+    reinterpret_cast<uint4*>(one ? first.dst : second.dst)[row * words + k / 8] = out;
   }
 }
 

@@ -45,6 +45,7 @@ struct Product {
 };
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream);
+cudaError_t launch_plain_f32(const Product& p, cudaStream_t stream);
 
 // The tensor-core kernels (16-bit types) -----------------------------------------
 

@@ -3,7 +3,8 @@
 
 namespace b200norm {
 
-template cudaError_t launch_plain<float>(const Product&, cudaStream_t);
+cudaError_t launch_plain_f32(const Product& p, cudaStream_t stream) { return launch_plain(p, stream); }
+
 template cudaError_t launch_rows<float>(const Product&, cudaStream_t);
 template cudaError_t launch_dz<float>(const LinearDzCall&, cudaStream_t);
 

@@ -2,7 +2,7 @@
 // operator's kernels that do not use the tensor cores.
 #pragma once
 
-#include "layer_launch.cuh"
+#include "launch_kernel.cuh"
 #include "linear.cuh"
 
 namespace b200norm {
@@ -20,29 +20,33 @@ inline PlainProduct plain_args(const Product& p) {
           p.M, p.N, p.K, p.epi};
 }
 
-template <typename T, int TILE>
+template <int TILE>
 cudaError_t launch_plain_tile(const Product& p, int splits, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.M + TILE - 1) / TILE * splits),
                   static_cast<unsigned>((p.N + TILE - 1) / TILE));
-  auto* fn = !p.a.k_contiguous    ? linear_plain_kernel<T, TILE, false, false>
-             : p.b.k_contiguous ? linear_plain_kernel<T, TILE, true, true>
-                                : linear_plain_kernel<T, TILE, true, false>;
-  return launch_clusters(fn, grid, PlainShape<TILE>::kThreads, splits, 0, stream, plain_args(p));
+  auto* fn = !p.a.k_contiguous    ? linear_plain_kernel<TILE, false, false>
+             : p.b.k_contiguous ? linear_plain_kernel<TILE, true, true>
+                                : linear_plain_kernel<TILE, true, false>;
+  if (PlainShape<TILE>::kSmem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(PlainShape<TILE>::kSmem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_clusters(fn, grid, PlainShape<TILE>::kThreads, splits, PlainShape<TILE>::kSmem,
+                         stream, plain_args(p));
 }
 
-template <typename T>
-cudaError_t launch_plain(const Product& p, cudaStream_t stream) {
-  if constexpr (sizeof(T) == 4) {
-    // large tiles once they fill the GPU
-    if ((p.M + 127) / 128 * ((p.N + 127) / 128) >= kPlainLargeTiles)
-      return launch_plain_tile<T, 128>(p, 1, stream);
-  }
+// float32 products.
+inline cudaError_t launch_plain(const Product& p, cudaStream_t stream) {
+  // large tiles once they fill the GPU
+  if ((p.M + 127) / 128 * ((p.N + 127) / 128) >= kPlainLargeTiles)
+    return launch_plain_tile<128>(p, 1, stream);
   // K split while an SM has fewer than four tiles and a part eight slices
   const int64_t tiles = (p.M + 63) / 64 * ((p.N + 63) / 64);
   int splits = 1;
   while (splits < 8 && tiles * splits * 2 <= 4 * 152 && p.K / (splits * 2) >= 8 * kPlainK)
     splits *= 2;
-  return launch_plain_tile<T, 64>(p, splits, stream);
+  return launch_plain_tile<64>(p, splits, stream);
 }
 
 template <typename T, int VE>
@@ -86,14 +90,17 @@ cudaError_t launch_dz(const LinearDzCall& c, cudaStream_t stream) {
   return e;
 }
 
+// Dense rows of n elements to rows pitch16(n) apart, of one operand or two.
 template <typename T>
-cudaError_t launch_pack(const void* src, void* dst, int64_t rows, int64_t n,
-                          cudaStream_t stream) {
+cudaError_t launch_pack(const void* src0, void* dst0, int64_t rows0, const void* src1, void* dst1,
+                        int64_t rows1, int64_t n, cudaStream_t stream) {
   const int64_t words = pitch16(n) / 8;
-  int64_t grid = (rows * words + 255) / 256;
+  int64_t grid = ((rows0 + rows1) * words + 255) / 256;
   if (grid > 152 * 16) grid = 152 * 16;
-  return launch_pdl(linear_pack_kernel<T>, dim3(static_cast<unsigned>(grid)), 256, stream,
-                    static_cast<const T*>(src), static_cast<T*>(dst), rows, n, words);
+  const PackRows<T> a{static_cast<const T*>(src0), static_cast<T*>(dst0), rows0};
+  const PackRows<T> b{static_cast<const T*>(src1), static_cast<T*>(dst1), rows1};
+  return launch_pdl(linear_pack_kernel<T>, dim3(static_cast<unsigned>(grid)), 256, stream, a, b, n,
+                    words);
 }
 
 }  // namespace b200norm

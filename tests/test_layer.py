@@ -248,3 +248,32 @@ def test_writes_exactly_its_outputs(rows, hidden, shift):
     for raw, view, a, n in blocks:
         assert bool((raw[:a] == 0xFF).all()) and bool((raw[a + n:] == 0xFF).all())
         assert not bool(torch.isnan(view.float()).any())
+
+
+def test_threads_on_one_stream():
+    """Several threads' gradient calls on one stream: each has its own scratch, so
+    their launches may interleave."""
+    import threading
+    cases = [{k: dev(v) for k, v in make(200, 1024, "bf16", "f32", 30 + i).items()}
+             for i in range(4)]
+    stats = [b2.skip_layer_stats(d["x"], None, d["gamma"])[2:] for d in cases]
+
+    def call(i):
+        return b2.skip_layer_grad(cases[i]["dy"], cases[i]["x"], *stats[i], cases[i]["gamma"])[:3]
+    want = [call(i) for i in range(4)]
+    torch.cuda.synchronize()
+    wrong, errors = [], []
+
+    def work(i):
+        try:
+            for _ in range(50):
+                if not all(torch.equal(g, w) for g, w in zip(call(i), want[i])):
+                    wrong.append(i)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and not wrong

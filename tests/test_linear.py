@@ -301,3 +301,33 @@ def test_more_tiles_than_ctas(tiling, keep, residual):
     assert b2.library().b200norm_testing_force_linear(*tiling, 1, 0) == 0
     for _ in range(3):
         check_forward(d, "none", True, residual, keep)
+
+
+def test_threads_on_one_stream():
+    """Several threads' gradient calls on one stream: each has its own scratch, so
+    their launches may interleave."""
+    import threading
+    cases = [make(300, 264, 136, "bf16", 20 + i) for i in range(4)]
+    on_gpu = [{k: v.cuda() for k, v in d.items()} for d in cases]
+
+    def call(d):
+        return b2.linear_grad(d["dy"], d["x"], d["w"], d["z"], activation=2)
+    want = [call(d) for d in on_gpu]
+    torch.cuda.synchronize()
+    wrong, errors = [], []
+
+    def work(i):
+        try:
+            for _ in range(50):
+                got = call(on_gpu[i])
+                same = [torch.equal(g, w) for g, w in zip(got, want[i])]
+                if not all(same):
+                    wrong.append((i, same))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and not wrong

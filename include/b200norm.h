@@ -329,7 +329,8 @@ B200NORM_API b200norm_status b200norm_skip_layer(
  *                Calls that share one must not overlap on the device.
  *
  * Sums over rows are binary32, in a fixed order (equal calls give equal bits).
- * rows == 0 stores zeros in dgamma, dbeta and dbias.
+ * rows == 0 stores zeros in dgamma, dbeta and dbias.  The first call on a device
+ * looks up a device address: make it before any stream capture begins.
  */
 B200NORM_API size_t b200norm_skip_layer_grad_workspace_size(int64_t rows, int64_t hidden);
 
@@ -361,8 +362,9 @@ B200NORM_API b200norm_status b200norm_skip_layer_grad(
  *              aligned (NULL where that is 0); its contents before the call do
  *              not matter.  Calls that share one must not overlap on the device.
  *
- * Sums are binary32.  rows == 0 is a no-op; in_features and out_features must
- * be in [1, 2^20].
+ * Sums are binary32, in a fixed order.  rows == 0 is a no-op; in_features and
+ * out_features must be in [1, 2^20].  The first call on a device looks up a
+ * device address: make it before any stream capture begins.
  */
 B200NORM_API size_t b200norm_linear_workspace_size(int64_t rows, int64_t in_features,
                                                    int64_t out_features, b200norm_dtype T,

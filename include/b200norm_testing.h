@@ -68,17 +68,25 @@ B200NORM_API b200norm_status b200norm_testing_force_split(int csize, int nv);
  * operands are not 16-byte aligned do not take one and ignore it. */
 B200NORM_API b200norm_status b200norm_testing_force_linear(int cg, int bn, int splits, int swap);
 
+/* Stall the linear operator's tensor-core products (process-wide) for later
+ * launches: with on = 1 nothing is copied, so the waits give up after limit_ns
+ * (in (0, 5 s]) each and the kernel records B200NORM_ERR_DEVICE_TIMEOUT (read
+ * with b200norm_linear_status) with nothing in flight; outputs are then
+ * undefined.  on = 0 restores normal launches (limit_ns ignored). */
+B200NORM_API b200norm_status b200norm_testing_linear_stall(int on, uint64_t limit_ns);
+
 /* Switch programmatic dependent launch off (0) or on (1, the default) for
  * every later launch of the library, on all threads.  With it on, a kernel
  * may be scheduled while the preceding grid on its stream drains and waits
  * for that grid before touching memory; results are identical either way. */
 B200NORM_API b200norm_status b200norm_testing_set_pdl(int on);
 
-/* Stall the pipelined row schedule (process-wide) for later launches: with
+/* Stall the pipelined row schedule and the streamed gradient of layer
+ * normalization (process-wide) for later launches: with
  * on = 1 its producer issues no copies, so every consumer wait gives up after
  * limit_ns (in (0, 5 s]) and the kernel records B200NORM_ERR_DEVICE_TIMEOUT
  * (read with b200norm_rows_status) with nothing in flight; outputs are left
- * unwritten.  on = 0 restores normal launches (limit_ns ignored). */
+ * unwritten (the gradient's: undefined).  on = 0 restores normal launches (limit_ns ignored). */
 B200NORM_API b200norm_status b200norm_testing_pipe_stall(int on, uint64_t limit_ns);
 
 /* Schedule the automatic planner picks, without launching anything.

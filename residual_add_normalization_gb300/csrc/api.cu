@@ -670,6 +670,14 @@ b200norm_status b200norm_testing_force_linear(int cg, int bn, int splits, int sw
   return ok();
 }
 
+b200norm_status b200norm_testing_linear_stall(int on, uint64_t limit_ns) {
+  if (on != 0 && on != 1) return fail(B200NORM_ERR_INVALID_ARGUMENT, "on must be 0 or 1");
+  if (on && (limit_ns == 0 || limit_ns > 5000000000ull))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "limit_ns must be in (0, 5 s]");
+  set_linear_stall(on ? limit_ns : 0);
+  return ok();
+}
+
 b200norm_status b200norm_testing_barrier_timeout(void* workspace, size_t workspace_bytes,
                                                  uint64_t limit_ns, b200norm_stream_t stream) {
   if (!workspace || workspace_bytes < kControlBytes || !aligned(workspace, 256))

@@ -521,7 +521,7 @@ __host__ __device__ constexpr int layer_slot_bytes(int vectors) {
 template <typename T, typename M, int VE, int NV, bool BIAS, bool LANE>
 __global__ void __launch_bounds__(LANE ? kLayerGradLaneThreads : kLayerThreads, 1)
 layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice, int stages,
-                       unsigned* status) {
+                       unsigned* status, unsigned long long limit_ns, int stall) {
   using P = Pack<T, VE>;
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ alignas(8) unsigned long long full[kLayerStages];
@@ -580,7 +580,7 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   };
   const int64_t row0 = static_cast<int64_t>(part) * rows_per;
   if (threadIdx.x == 0)
-    for (int i = 0; i < stages && i < tiles; ++i) issue(row0 + i * stride, i);
+    for (int i = 0; i < stages && i < tiles && !stall; ++i) issue(row0 + i * stride, i);
 
   LayerGradRow<T, M, VE, NV, BIAS> x;
   x.load_gamma(a.gamma + static_cast<int64_t>(lo) * VE, first, step, count);
@@ -602,7 +602,7 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
       r_next = a.inv_std[row + stride];
     }
     const unsigned char* stage = ring + st * 3 * slot_bytes;
-    if (alive && !mbar_wait(&full[st], parity, kLayerLimitNs)) {
+    if (alive && !mbar_wait(&full[st], parity, limit_ns)) {
       alive = false;
       atomicExch(status, kStatusDeviceTimeout);
     }
@@ -669,10 +669,10 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
       parity ^= 1;
     }
   }
-  if (!alive && threadIdx.x == 0)  // copies still in flight land before the CTA ends
+  if (!alive && threadIdx.x == 0 && !stall)  // copies still in flight land before the CTA ends
     for (int i = 0; i < stages; ++i) {
-      mbar_wait(&full[i], 0, kLayerLimitNs);
-      mbar_wait(&full[i], 1, kLayerLimitNs);
+      mbar_wait(&full[i], 0, limit_ns);
+      mbar_wait(&full[i], 1, limit_ns);
     }
   const bool sums = a.dgamma || a.dbeta || a.dbias;
   if constexpr (LANE) {

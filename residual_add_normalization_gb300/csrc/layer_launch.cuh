@@ -125,8 +125,10 @@ cudaError_t launch_layer_grad_ring(Fn fn, LayerGradArgs<T, M>* a, int block, int
   if (a->parts > resident / csize) a->parts = resident / csize;
   unsigned* status = pipe_status_word();
   if (!status) return cudaErrorSymbolNotFound;
+  const bool stall = pipe_stalled();
   return launch_clusters(fn, dim3(static_cast<unsigned>(a->parts * csize)), block, csize, smem,
-                         stream, *a, tpr, nvec, slice, stages, status);
+                         stream, *a, tpr, nvec, slice, stages, status,
+                         stall ? pipe_stall_limit_ns() : kLayerLimitNs, stall ? 1 : 0);
 }
 
 // The one-pass gradient, NV vectors per thread of `block` threads of `csize` CTAs.

@@ -66,6 +66,9 @@ bool mma_plan_ok(const MmaPlan& plan, int64_t M, int64_t K, bool a_kc, bool b_kc
 // Two words per device: a b200norm_status recorded by a wait that gave up, and
 // its site (nullptr if they cannot be resolved).
 unsigned* linear_status_words();
+// A test's limit for the waits of launches that copy nothing (0: normal ones).
+unsigned long long linear_stall_limit_ns();
+void set_linear_stall(unsigned long long limit_ns);
 
 // dz = round_T(dy * act'(z)) with rows `ldz` apart (null: not stored), and the
 // column sums of dy * act'(z) (null: not wanted) through `part`.

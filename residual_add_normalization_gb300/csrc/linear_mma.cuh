@@ -45,7 +45,8 @@ namespace b200norm {
 constexpr int kMmaK = 64;              // elements of k per stage: 128 bytes
 constexpr int kMmaRows = 128;          // rows of C per CTA
 constexpr int kMmaABytes = kMmaRows * kMmaK * 2;
-constexpr int kMmaGroup = 8;           // row tiles a column of tiles is walked down by
+constexpr int kMmaGroup = 8;           // row tiles a column of tiles is walked down by (16
+                                       // does as well; 4 and 32 lose 4 and 6 percent)
 
 struct MmaArgs {
   int64_t M, N;        // of the product as the tensor cores see it
@@ -56,6 +57,7 @@ struct MmaArgs {
   bool vec;            // rows of the result, bias and residual are whole 16-byte vectors
   unsigned* status;
   unsigned long long limit_ns;
+  bool stall;          // a test: nothing is copied, and the waits give up
 };
 
 // Shared memory of a CTA: the ring, then 8 KB for each epilogue warp's results
@@ -519,7 +521,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       int it = 0;
       bool alive = true;
       const unsigned full0 = CG == 2 ? cluster_addr(&full[0], 0) : smem_addr(&full[0]);
-      for (int t = unit; t < tiles && alive; t += units) {
+      for (int t = unit; t < tiles && alive && !g.stall; t += units) {
         int tm, tn;
         tile_at(t, tm, tn);
         const int m0 = (tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kMmaRows;

@@ -26,6 +26,10 @@ EncodeFn tensor_map_encoder() {
 }
 
 __device__ unsigned g_linear_status[2];
+static std::atomic<unsigned long long> g_linear_stall{0};
+
+unsigned long long linear_stall_limit_ns() { return g_linear_stall.load(); }
+void set_linear_stall(unsigned long long limit_ns) { g_linear_stall.store(limit_ns); }
 
 unsigned* linear_status_words() {
   constexpr int kCachedDevices = 64;  // devices past these are looked up every time

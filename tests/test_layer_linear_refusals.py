@@ -153,6 +153,14 @@ def test_force_hook_refusals(lib):
     assert f(0, 0, 0, 0) == OK
 
 
+def test_stall_hook_refusals(lib):
+    f = lib.b200norm_testing_linear_stall
+    assert f(2, 1000) == INVALID
+    assert f(1, 0) == INVALID
+    assert f(1, 6_000_000_000) == INVALID
+    assert f(0, 0) == OK
+
+
 def test_binding_refuses_cpu_tensors():
     x, w = torch.zeros(4, 8), torch.ones(8)
     with pytest.raises(ValueError, match="CUDA"):

@@ -128,8 +128,30 @@ struct PlainProduct {
   Epilogue e;
 };
 
+// A sum split over the CTAs of a cluster is read from all of them at once: a read
+// of a peer's shared memory takes as long as one from L2, and one after another
+// eight ranks' took most of a small product's time (64 x 4096 x 4096 bf16 12.5 us).
+constexpr int kMaxSplits = 8;
+
+__device__ __forceinline__ unsigned peer_addr(const void* p, unsigned rank) {
+  unsigned remote;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(p)), "r"(rank));
+  return remote;
+}
+__device__ __forceinline__ float peer_load(unsigned addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_load4(unsigned addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 constexpr int kPlainK = 16;
-constexpr int kPlainStages = 4;
+constexpr int kPlainStages = 4;  // 3 lose 4 percent; 6 as well, by fewer CTAs per SM
 template <int TILE>
 struct PlainShape {
   static constexpr int kThreads = TILE == 128 ? 256 : 128;
@@ -173,8 +195,10 @@ __device__ __forceinline__ void plain_slice(float* s, const float* p, int64_t ld
   }
 }
 
+// (Registers: left to itself the compiler packs the small tile into 96 and loses a
+// sixth; three CTAs per SM, four for the weight's gradient, measured best.)
 template <int TILE, bool A_KC, bool B_KC>
-__global__ void __launch_bounds__(PlainShape<TILE>::kThreads)
+__global__ void __launch_bounds__(PlainShape<TILE>::kThreads, TILE == 128 ? 1 : A_KC ? 3 : 4)
 linear_plain_kernel(const PlainProduct p) {
   using S = PlainShape<TILE>;
   constexpr int C = S::kCols, kHalf = TILE / 2;
@@ -277,12 +301,20 @@ linear_plain_kernel(const PlainProduct p) {
       for (int q = threadIdx.x; q < per; q += S::kThreads) {
         const int at = static_cast<int>(rank) * per + q;
         float t[4] = {};
-        for (unsigned c = 0; c < csize; ++c) {
-          const float4 v = ld_cluster_f32x4(reinterpret_cast<const float4*>(sums) + at, c);
-          t[0] += v.x;
-          t[1] += v.y;
-          t[2] += v.z;
-          t[3] += v.w;
+#pragma unroll
+        for (unsigned c0 = 0; c0 < kMaxSplits; c0 += 4) {
+          float4 v[4];
+#pragma unroll
+          for (unsigned c = 0; c < 4; ++c)
+            if (c0 + c < csize) v[c] = peer_load4(peer_addr(sums + at * 4, c0 + c));
+#pragma unroll
+          for (unsigned c = 0; c < 4; ++c) {
+            if (c0 + c >= csize) continue;
+            t[0] += v[c].x;
+            t[1] += v[c].y;
+            t[2] += v[c].z;
+            t[3] += v[c].w;
+          }
         }
         finish(t, m0 + at / 16, n0 + at % 16 * 4);
       }

@@ -177,12 +177,6 @@ __device__ __forceinline__ void tmem_load16(unsigned addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ unsigned cluster_addr(const void* p, unsigned rank) {
-  unsigned remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(p)), "r"(rank));
-  return remote;
-}
-
 // A box of the tensor map at (x, y) into this CTA's shared memory, completing
 // on `bar` (a shared::cluster address: of the pair's first CTA when CG is 2).
 template <int CG>
@@ -520,7 +514,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     if (lane == 0) {
       int it = 0;
       bool alive = true;
-      const unsigned full0 = CG == 2 ? cluster_addr(&full[0], 0) : smem_addr(&full[0]);
+      const unsigned full0 = CG == 2 ? peer_addr(&full[0], 0) : smem_addr(&full[0]);
       for (int t = unit; t < tiles && alive && !g.stall; t += units) {
         int tm, tn;
         tile_at(t, tm, tn);
@@ -644,7 +638,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
             mbar_arrive(&drained[buf]);
           } else {
             asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                         :: "r"(cluster_addr(&drained[buf], 0)) : "memory");
+                         :: "r"(peer_addr(&drained[buf], 0)) : "memory");
           }
         }
       };
@@ -694,19 +688,39 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       tile_at(unit, tm, tn);
       const int64_t m = static_cast<int64_t>(tm) * kMmaRows + row;
       const int64_t n0 = static_cast<int64_t>(tn) * BN;
-      const float* mine = reinterpret_cast<const float*>(ring);
-      constexpr int NC = !SWAP ? 8 : 2;
-      for (int c = c0; c < c0 + cols; c += NC) {
-        float v[NC] = {};
-        for (int r = 0; r < g.splits; ++r) {
+      unsigned peer[kMaxSplits];
 #pragma unroll
-          for (int i = 0; i < NC; ++i)
-            v[i] += ld_cluster_f32(mine + (c + i) * kMmaRows + row, r);
+      for (int r = 0; r < kMaxSplits; ++r)
+        peer[r] = peer_addr(reinterpret_cast<const float*>(ring) + row, r < g.splits ? r : 0);
+      auto columns = [&](auto nc) {
+        constexpr int NC = decltype(nc)::value;
+        for (int c = c0; c < c0 + cols; c += NC) {
+          float part[kMaxSplits][NC];
+#pragma unroll
+          for (int r = 0; r < kMaxSplits; ++r) {
+            if (r >= g.splits) continue;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) part[r][i] = peer_load(peer[r] + (c + i) * kMmaRows * 4);
+          }
+          float v[NC] = {};
+#pragma unroll
+          for (int r = 0; r < kMaxSplits; ++r) {
+            if (r >= g.splits) continue;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) v[i] += part[r][i];
+          }
+          if (m < g.M) {
+            if constexpr (SWAP) epilogue_col<T, NC>(g.e, n0 + c, g.N, m, g.M, v);
+            else epilogue_row<T, NC>(g.e, g.vec, m, n0 + c, g.N, v);
+          }
         }
-        if (m < g.M) {
-          if constexpr (SWAP) epilogue_col<T, NC>(g.e, n0 + c, g.N, m, g.M, v);
-          else epilogue_row<T, NC>(g.e, g.vec, m, n0 + c, g.N, v);
-        }
+      };
+      if constexpr (SWAP) {
+        if (cols % 8 == 0) columns(Const<8>());
+        else if (cols % 4 == 0) columns(Const<4>());
+        else columns(Const<2>());
+      } else {
+        columns(Const<8>());
       }
     }
     cluster_sync();  // the peers may still read this CTA's sums

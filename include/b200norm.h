@@ -362,8 +362,8 @@ B200NORM_API b200norm_status b200norm_skip_layer_grad(
  *              aligned (NULL where that is 0); its contents before the call do
  *              not matter.  Calls that share one must not overlap on the device.
  *
- * Sums are binary32, in a fixed order.  rows == 0 is a no-op; in_features and
- * out_features must be in [1, 2^20].  The first call on a device looks up a
+ * Sums are binary32, in a fixed order.  rows == 0 is a no-op; rows may
+ * be 2^30 at most, in_features and out_features must be in [1, 2^20].  The first call on a device looks up a
  * device address: make it before any stream capture begins.
  */
 B200NORM_API size_t b200norm_linear_workspace_size(int64_t rows, int64_t in_features,

@@ -225,6 +225,7 @@ b200norm_status check_layer_shape(int64_t rows, int64_t hidden, b200norm_dtype T
 }
 
 constexpr int64_t kMaxFeatures = int64_t{1} << 20;
+constexpr int64_t kMaxLinearRows = int64_t{1} << 30;  // tensor copies take int coordinates
 
 b200norm_status check_linear_shape(int64_t rows, int64_t in, int64_t out, b200norm_dtype T,
                                    int activation) {
@@ -232,8 +233,8 @@ b200norm_status check_linear_shape(int64_t rows, int64_t in, int64_t out, b200no
   if (rows < 0 || in <= 0 || out <= 0)
     return fail(B200NORM_ERR_INVALID_ARGUMENT,
                 "need rows >= 0, in_features > 0, out_features > 0");
-  if (rows > kMaxGrid || in > kMaxFeatures || out > kMaxFeatures)
-    return fail(B200NORM_ERR_UNSUPPORTED, "rows exceeds 2^31-1, or features 2^20");
+  if (rows > kMaxLinearRows || in > kMaxFeatures || out > kMaxFeatures)
+    return fail(B200NORM_ERR_UNSUPPORTED, "rows exceeds 2^30, or features 2^20");
   if (activation < 0 || activation >= kActivations)
     return fail(B200NORM_ERR_INVALID_ARGUMENT,
                 "activation must be 0 (none), 1 (SiLU), 2 (GELU), 3 (GELU, tanh) or 4 (ReLU)");

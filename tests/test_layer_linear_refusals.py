@@ -101,6 +101,7 @@ def test_linear_refusals(lib):
     assert linear(lib, n_out=0) == INVALID
     assert linear(lib, n_out=(1 << 20) + 1) == UNSUPPORTED
     assert linear(lib, rows=1 << 31) == UNSUPPORTED
+    assert linear(lib, rows=(1 << 30) + 1) == UNSUPPORTED
     assert linear(lib, act=5) == INVALID
     assert linear(lib, act=-1) == INVALID
     assert linear(lib, x=None) == INVALID

@@ -45,11 +45,12 @@ struct LayerGradCall {
 // Partial column sums a gradient call keeps: one set of (dgamma, dbeta, dbias)
 // rows per part, later added in part order (no atomics, so equal calls give
 // equal bits).  At most six parts per SM (CTAs of short rows; 16384 x 1024
-// bfloat16 takes 33 us with four per SM, 47 with two), fewer for long rows.
+// bfloat16 takes 33 us with four per SM, 47 with two), fewer for long rows, and
+// two rows in each once every SM has one (608 x 1024: 7.2 us, 8.5 with one row).
 constexpr int kLayerMaxParts = 912;
 inline int64_t layer_part_pitch(int64_t hidden) { return (hidden + 3) / 4 * 4; }
 inline int layer_grad_parts(int64_t rows, int64_t hidden) {
-  int64_t p = rows;
+  int64_t p = rows > 152 ? (rows / 2 > 152 ? rows / 2 : 152) : rows;
   const int64_t most = (int64_t{1} << 24) / hidden;
   if (p > most) p = most;
   if (p > kLayerMaxParts) p = kLayerMaxParts;

@@ -196,9 +196,10 @@ __device__ __forceinline__ void plain_slice(float* s, const float* p, int64_t ld
 }
 
 // (Registers: left to itself the compiler packs the small tile into 96 and loses a
-// sixth; three CTAs per SM, four for the weight's gradient, measured best.)
+// sixth; three CTAs per SM, four for the weight's gradient, measured best.  Two of
+// the large tile cost a few spilled registers and gain a twentieth.)
 template <int TILE, bool A_KC, bool B_KC>
-__global__ void __launch_bounds__(PlainShape<TILE>::kThreads, TILE == 128 ? 1 : A_KC ? 3 : 4)
+__global__ void __launch_bounds__(PlainShape<TILE>::kThreads, TILE == 128 ? 2 : A_KC ? 3 : 4)
 linear_plain_kernel(const PlainProduct p) {
   using S = PlainShape<TILE>;
   constexpr int C = S::kCols, kHalf = TILE / 2;

@@ -29,8 +29,8 @@ cudaError_t pack_rows(DType t, const void* src0, void* dst0, int64_t rows0, cons
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream) {
   const bool mma = mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0;
-  const bool few = p.M <= kFewRows && !(mma && (p.N * p.K > kFewWeights || p.forced.cg));
-  if (p.a.k_contiguous && p.b.k_contiguous && few) {
+  if (p.a.k_contiguous && p.b.k_contiguous && !(mma && p.forced.cg) &&
+      few_rows(p.M, p.N, p.K, p.t, mma)) {
     switch (p.t) {
       case DType::F32: return launch_rows<float>(p, stream);
       case DType::F16: return launch_rows<__half>(p, stream);
@@ -52,7 +52,7 @@ cudaError_t launch_linear_dz(const LinearDzCall& c, cudaStream_t stream) {
 
 LinearPlan linear_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {
   LinearPlan p = {};
-  p.pack = t != DType::F32 && (in % 8 != 0 || !aligned16) && rows > kFewRows;
+  p.pack = t != DType::F32 && (in % 8 != 0 || !aligned16) && !few_rows(rows, out, in, t, false);
   if (p.pack) {
     p.w = round_256(static_cast<size_t>(rows) * pitch16(in) * 2);
     p.bytes = p.w + round_256(static_cast<size_t>(out) * pitch16(in) * 2);

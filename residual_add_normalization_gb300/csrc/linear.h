@@ -127,11 +127,18 @@ struct LinearGradCall {
 // of 16-bit types whose rows do not start on 16-byte boundaries are copied to
 // rows that do (`pitch` elements apart), except for few rows of x, where the
 // weight is read once and not worth a copy.
-// Rows that the row kernel takes: aligned 16-bit ones up to 16 M weights (1 x 768 x
-// 768 2.1 us against 5.8 on the tensor cores, 1 x 4096 x 4096 11.2 against 11.1,
-// 1 x 16384 x 4096 42 against 28), and unaligned or float32 ones.
-constexpr int64_t kFewRows = 4;
-constexpr int64_t kFewWeights = int64_t{1} << 24;
+// Whether the row kernel takes a product.  float32: up to four rows (4 x 4096 x 4096
+// 35 us, 60 as a tiled product).  Unaligned 16-bit operands: one row (1 x 4097 x 4099
+// 14 us), or up to 2 M products (2 x 4097 x 4099 takes 21 us by way of aligned
+// copies).  Aligned ones: up to four rows and 4 M products (1 x 768 x 768 2.1 us
+// against 4.7 on the tensor cores, 4 x 768 x 768 4.1 against 4.7, 1 x 1024 x 4096 2.8
+// against 5.7, but 1 x 4096 x 4096 11.2 against 10.1, 4 x 4096 x 4096 35 against 10).
+inline bool few_rows(int64_t M, int64_t N, int64_t K, DType t, bool aligned) {
+  if (M > 4) return false;
+  if (t == DType::F32) return true;
+  const int64_t products = M * N * K;
+  return aligned ? products <= int64_t{1} << 22 : M == 1 || products <= int64_t{1} << 21;
+}
 inline int64_t pitch16(int64_t n) { return (n + 7) / 8 * 8; }
 struct LinearPlan {
   bool pack;              // x and weight are copied

@@ -345,13 +345,14 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
 // ---------------------------------------------------------------------------
 template <typename T, typename M, int VE, int NV, bool BIAS>
 struct LayerGradRow {
-  static constexpr int H = (VE + 1) / 2;  // pairs per vector (VE 1: .x alone)
-  float2 dg[NV][H] = {}, db[NV][H] = {}, dc[BIAS ? NV : 1][H] = {};
-  float2 gm[NV][H];
-  float2 g[NV][H], u[NV][H];
+  using V = typename std::conditional<VE == 1, float, float2>::type;  // pairs of a vector
+  static constexpr int H = (VE + 1) / 2;
+  V dg[NV][H] = {}, db[NV][H] = {}, dc[BIAS ? NV : 1][H] = {};
+  V gm[NV][H];
+  V g[NV][H], u[NV][H];
 
-  __device__ __forceinline__ static float2 at(const Pack<T, VE>& p, int i) {
-    if constexpr (VE == 1) return make_float2(to_f32(p.v[0]), 0.0f);
+  __device__ __forceinline__ static V at(const Pack<T, VE>& p, int i) {
+    if constexpr (VE == 1) return to_f32(p.v[0]);
     else return get2(p, i);
   }
 
@@ -360,26 +361,24 @@ struct LayerGradRow {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int v = first + k * step;
-      float f[2 * H] = {};
-      if (v < nvec) {
-        float q[VE];
-        ld_params<M, VE>(gamma + static_cast<int64_t>(v) * VE, q);
+      float f[VE] = {};
+      if (v < nvec) ld_params<M, VE>(gamma + static_cast<int64_t>(v) * VE, f);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) f[e] = q[e];
+      for (int i = 0; i < H; ++i) {
+        if constexpr (VE == 1) gm[k][i] = f[0];
+        else gm[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
       }
-#pragma unroll
-      for (int i = 0; i < H; ++i) gm[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
     }
   }
 
   // vector k of a row: adds it to dgamma and dbeta, and to the sums of g (tg)
   // and g * u (tu)
   __device__ __forceinline__ void take(int k, const Pack<T, VE>& dy, const Pack<T, VE>& s,
-                                       float mu, float r, float2& tg, float2& tu) {
+                                       float mu, float r, V& tg, V& tu) {
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      const float2 d = at(dy, i);
-      u[k][i] = mul2(add2(at(s, i), both(-mu)), both(r));
+      const V d = at(dy, i);
+      u[k][i] = mul2(add2(at(s, i), every<V>(-mu)), every<V>(r));
       g[k][i] = mul2(d, gm[k][i]);
       dg[k][i] = fma2(d, u[k][i], dg[k][i]);
       db[k][i] = add2(db[k][i], d);
@@ -394,19 +393,22 @@ struct LayerGradRow {
     Pack<T, VE> out;
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      float2 d = fma2(g[k][i], both(r), fma2(u[k][i], both(k2), both(k1)));
+      V d = fma2(g[k][i], every<V>(r), fma2(u[k][i], every<V>(k2), every<V>(k1)));
       if (ds) d = add2(d, at(*ds, i));
       if constexpr (BIAS) dc[k][i] = add2(dc[k][i], d);
-      if constexpr (VE == 1) out.v[0] = from_f32<T>(d.x);
+      if constexpr (VE == 1) out.v[0] = from_f32<T>(d);
       else set2(out, i, d.x, d.y);
     }
     if (dx) st_stream<T, VE>(dx, out);
   }
 
   // one of dg, db and dc of a vector, an element at a time
-  __device__ __forceinline__ static void elements(const float2 (&p)[H], float (&f)[VE]) {
+  __device__ __forceinline__ static void elements(const V (&p)[H], float (&f)[VE]) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) f[e] = e % 2 ? p[e / 2].y : p[e / 2].x;
+    for (int e = 0; e < VE; ++e) {
+      if constexpr (VE == 1) f[0] = p[0];
+      else f[e] = e % 2 ? p[e / 2].y : p[e / 2].x;
+    }
   }
 };
 
@@ -471,11 +473,13 @@ __device__ __forceinline__ void layer_grad_lane_sums(
     if (threadIdx.x / 32 == w) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
+        float fg[VE], fb[VE], fc[VE];
+        x.elements(x.dg[k], fg);
+        x.elements(x.db[k], fb);
+        x.elements(x.dc[BIAS ? k : 0], fc);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          float g = e % 2 ? x.dg[k][e / 2].y : x.dg[k][e / 2].x;
-          float b = e % 2 ? x.db[k][e / 2].y : x.db[k][e / 2].x;
-          float c = e % 2 ? x.dc[BIAS ? k : 0][e / 2].y : x.dc[BIAS ? k : 0][e / 2].x;
+          float g = fg[e], b = fb[e], c = fc[e];
           for (int o = tpr; o < 32; o *= 2) {
             g += __shfl_xor_sync(0xffffffffu, g, o);
             b += __shfl_xor_sync(0xffffffffu, b, o);
@@ -606,7 +610,8 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
       alive = false;
       atomicExch(status, kStatusDeviceTimeout);
     }
-    float2 tg = make_float2(0.0f, 0.0f), tu = tg;
+    using V = typename LayerGradRow<T, M, VE, NV, BIAS>::V;
+    V tg = every<V>(0.0f), tu = tg;
     if constexpr (VE > 1) {
       const P* dy = reinterpret_cast<const P*>(stage) + group * count;
       const P* s = reinterpret_cast<const P*>(stage + slot_bytes) + group * count;
@@ -627,7 +632,7 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
           x.take(k, dy.take(stage, at, edge), s.take(stage + slot_bytes, at, edge), mu, r, tg, tu);
       }
     }
-    float2 t = VE == 1 ? make_float2(tg.x, tu.x) : make_float2(tg.x + tg.y, tu.x + tu.y);
+    float2 t = make_float2(total(tg), total(tu));
     if constexpr (LANE) {
       t.x = seg_sum(t.x, tpr);
       t.y = seg_sum(t.y, tpr);

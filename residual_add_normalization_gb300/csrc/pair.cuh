@@ -39,4 +39,16 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// The same names for one operation, so that code for pairs serves single values.
+__device__ __forceinline__ float add2(float a, float b) { return __fadd_rn(a, b); }
+__device__ __forceinline__ float mul2(float a, float b) { return __fmul_rn(a, b); }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+
+template <typename V> __device__ __forceinline__ V every(float v);
+template <> __device__ __forceinline__ float every<float>(float v) { return v; }
+template <> __device__ __forceinline__ float2 every<float2>(float v) { return both(v); }
+
+__device__ __forceinline__ float total(float v) { return v; }
+__device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
+
 }  // namespace b200norm

@@ -254,9 +254,9 @@ _ws_lock = threading.Lock()
 
 def rows_status(stream=None, device=None):
     """Synchronizes ``stream`` and raises B200NormError if a pipelined row
-    kernel (short SkipSimplifiedLayerNormalization / GatedRMSNorm rows) on the
-    device gave up a bounded wait since the last call; the record is then
-    cleared."""
+    kernel (short SkipSimplifiedLayerNormalization / GatedRMSNorm rows, or the
+    gradient of layer normalization) on the device gave up a bounded wait
+    since the last call; the record is then cleared."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(dev):
         _check(library().b200norm_rows_status(_stream(dev, stream)))

@@ -113,6 +113,28 @@ def test_linear_past_2_31_elements():
 
 
 @pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n_in,n_out", [(1, 512, 768), (130, 1024, 520)])
+def test_same_results_without_dependent_launch(rows, n_in, n_out, t):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, w, dy = (torch.randn(*s, generator=g, device="cuda").to(t)
+                for s in ((rows, n_in), (n_out, n_in), (rows, n_out)))
+    gamma = torch.rand(n_in, generator=g, device="cuda").to(t)
+
+    def run():
+        n, s, mean, inv = b2.skip_layer_stats(x, x, gamma)
+        y, z = b2.linear(n, w, activation=2, want_z=True)
+        dn, dw, db = b2.linear_grad(dy, n, w, z, activation=2)
+        return (y, z, dn, dw, db) + b2.skip_layer_grad(dn, s, mean, inv, gamma, want_bias=True)
+    first = run()
+    try:
+        assert b2.library().b200norm_testing_set_pdl(0) == 0
+        second = run()
+    finally:
+        b2.library().b200norm_testing_set_pdl(1)
+    assert all(torch.equal(p, q) for p, q in zip(first, second))
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,n_in,n_out", [(2, 512, 768), (40, 4096, 512), (700, 1027, 520)])
 def test_equal_calls_give_equal_bits(rows, n_in, n_out, t):
     g = torch.Generator(device="cuda").manual_seed(3)

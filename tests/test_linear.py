@@ -16,7 +16,8 @@ ACTS = ["none", "silu", "gelu", "gelu_tanh", "relu"]
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 4096, 520), (2, 16, 24), (3, 5, 7), (5, 72, 130),
           (8, 1000, 129), (16, 512, 256), (17, 264, 264), (33, 65, 1000), (64, 768, 768),
           (65, 64, 72), (127, 128, 136), (128, 128, 128), (129, 136, 256), (130, 1027, 99),
-          (200, 2048, 320), (256, 320, 512), (257, 520, 264), (300, 8200, 64), (513, 72, 1283)]
+          (200, 2048, 320), (256, 320, 512), (257, 520, 264), (300, 8200, 64), (513, 72, 1283),
+          (2, 4096, 1030), (3, 2051, 1030), (4, 1030, 1500)]
 
 
 @pytest.fixture(autouse=True)

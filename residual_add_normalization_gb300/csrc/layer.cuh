@@ -119,6 +119,68 @@ __device__ __forceinline__ Pack<T, VE> layer_sum(const LayerArgs<T, M>& a, int64
   return pack_from<T, VE>(f);
 }
 
+// Rows that are not whole vectors, in tensors that start on a vector: a row is
+// taken as the vectors of memory that it touches, the first `shift` elements of
+// which are not its own, and each of these is masked in the first and the last
+// of them alone.  Rows `VE` apart have the same shift, so a CTA that takes only
+// such rows keeps its threads' columns, and their parameters and sums in
+// registers.
+template <int VE>
+struct Window {
+  int n, shift, nvec;
+
+  __device__ __forceinline__ Window(int64_t row, int n_)
+      : n(n_),
+        shift(static_cast<int>(row * n_) & (VE - 1)),
+        nvec((n_ + shift + VE - 1) / VE) {}
+
+  __device__ __forceinline__ int col(int v) const { return v * VE - shift; }  // of v's element 0
+  __device__ __forceinline__ bool has(int col) const {
+    return static_cast<unsigned>(col) < static_cast<unsigned>(n);
+  }
+  __device__ __forceinline__ bool cut(int v) const { return !has(col(v)) || !has(col(v) + VE - 1); }
+
+  // vector v of the row whose window starts at `p`.  What is not the row's may be
+  // anything: a neighbouring row's, or zeros in the tensor's last row, past
+  // whose elements nothing is read.
+  template <typename T>
+  __device__ __forceinline__ Pack<T, VE> load(const T* p, int v, bool last) const {
+    if (!last || !cut(v)) return ld_stream<T, VE>(p + static_cast<int64_t>(v) * VE);
+    Pack<T, VE> out;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      out.v[e] = has(col(v) + e) ? p[static_cast<int64_t>(v) * VE + e] : from_f32<T>(0.0f);
+    return out;
+  }
+
+  // zeros for what is not the row's
+  template <typename T>
+  __device__ __forceinline__ void mask(int v, Pack<T, VE>* f) const {
+    if (!cut(v)) return;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (!has(col(v) + e)) f->v[e] = from_f32<T>(0.0f);
+  }
+
+  template <typename T>
+  __device__ __forceinline__ void store(T* p, int v, const Pack<T, VE>& f) const {
+    if (!cut(v)) return st_stream<T, VE>(p + static_cast<int64_t>(v) * VE, f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (has(col(v) + e)) p[static_cast<int64_t>(v) * VE + e] = f.v[e];
+  }
+
+  // the parameters of v's columns
+  template <typename M>
+  __device__ __forceinline__ Pack<M, VE> params(const M* p, int v) const {
+    Pack<M, VE> out;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      out.v[e] = has(col(v) + e) ? __ldg(p + col(v) + e) : from_f32<M>(0.0f);
+    return out;
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Forward, the row in registers: read once, normalized, written once.
 // ---------------------------------------------------------------------------
@@ -280,6 +342,157 @@ __global__ void __launch_bounds__(kLayerThreads) layer_cta_kernel(const LayerArg
   if (csize > 1) cluster_sync();  // peers may still read slot
 }
 
+// Rows that are not whole vectors, by windows: as above, but a CTA takes every
+// `parts`-th row (a multiple of VE, or one row each).  Each thread keeps its
+// columns' parameters in shared memory, where it alone reads them.
+template <typename P>
+__device__ __forceinline__ void keep16(uint4* at, int step, const P& p) {
+  uint4 raw[sizeof(P) / 16];
+  memcpy(raw, &p, sizeof(P));
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(P) / 16); ++i) at[i * step] = raw[i];
+}
+template <typename P>
+__device__ __forceinline__ P kept16(const uint4* at, int step) {
+  uint4 raw[sizeof(P) / 16];
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(P) / 16); ++i) raw[i] = at[i * step];
+  P p;
+  memcpy(&p, raw, sizeof(P));
+  return p;
+}
+
+// 16-byte pieces that a vector's gamma, beta and bias take
+template <typename T, typename M, int VE>
+__host__ __device__ constexpr int layer_window_pieces() {
+  return 2 * (sizeof(Pack<M, VE>) / 16) + sizeof(Pack<T, VE>) / 16;
+}
+
+// What hides a row's latency is the other rows of the SM, so the registers are
+// held to what lets five CTAs of 256 threads, or three (16-byte vectors of 16
+// bits: 8192 x 4095 float16 takes 83.7 us, 91.0 without) or two (float32: 101,
+// 133) of 512, be resident.
+template <int VE, int NV>
+constexpr int kLayerWindowThreads = NV == 1 || (VE == 4 && NV == 2) ? 256 : kLayerThreads;
+template <int VE, int NV>
+constexpr int kLayerWindowCtas = kLayerWindowThreads<VE, NV> == 256 ? 5 : VE == 4 ? 2 : 3;
+
+template <typename T, typename M, int VE, int NV>
+__global__ void __launch_bounds__(kLayerWindowThreads<VE, NV>, kLayerWindowCtas<VE, NV>)
+layer_window_kernel(const LayerArgs<T, M> a, int tpr, int parts) {
+  pdl_wait();
+  pdl_trigger();
+  using PM = Pack<M, VE>;
+  using PT = Pack<T, VE>;
+  extern __shared__ __align__(16) uint4 params[];
+  __shared__ float red[2][16];
+  __shared__ float slot[2];
+  const unsigned csize = cluster_size();
+  const unsigned rank = csize > 1 ? cluster_rank() : 0u;
+  int64_t row = blockIdx.x / csize;
+  const Window<VE> w(row, a.n);
+  const int first = threadIdx.x + static_cast<int>(rank) * blockDim.x;
+  const int lot = NV * blockDim.x;
+  constexpr int kM = sizeof(PM) / 16;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int v = first + k * tpr;
+    if (v >= w.nvec) continue;
+    uint4* at = params + k * blockDim.x + threadIdx.x;
+    keep16(at, lot, w.params(a.gamma, v));
+    if (a.beta) keep16(at + kM * lot, lot, w.params(a.beta, v));
+    if (a.bias) keep16(at + 2 * kM * lot, lot, w.params(a.bias, v));
+  }
+  for (; row < a.rows; row += parts) {
+    const int64_t base = row * a.n - w.shift;
+    const bool last = row == a.rows - 1;
+    PT s[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * tpr;
+      if (v < w.nvec) s[k] = w.load(a.x + base, v, last);
+    }
+    if (a.skip) {
+      PT q[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + k * tpr;
+        if (v < w.nvec) q[k] = w.load(a.skip + base, v, last);
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + k * tpr;
+        if (v >= w.nvec) continue;
+        float f[VE], kf[VE];
+        unpack(s[k], f);
+        unpack(q[k], kf);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] = __fadd_rn(f[e], kf[e]);
+        if (a.bias) {
+          unpack(kept16<PT>(params + 2 * kM * lot + k * blockDim.x + threadIdx.x, lot), kf);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) f[e] = __fadd_rn(f[e], kf[e]);
+        }
+        s[k] = pack_from<T, VE>(f);
+        if (a.s) w.store(a.s + base, v, s[k]);
+      }
+    }
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * tpr;
+      if (v >= w.nvec) continue;
+      w.mask(v, &s[k]);
+      float f[VE];
+      unpack(s[k], f);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) t += f[e];
+    }
+    t = cta_sum_1b(t, red[0]);
+    if (csize > 1) t = cluster_sum(t, &slot[0], csize);
+    const float mu = t * a.inv_n;
+    t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * tpr;
+      if (v >= w.nvec) continue;
+      float f[VE];
+      unpack(s[k], f);
+      const bool cut = w.cut(v);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float d = f[e] - mu;
+        if (!cut || w.has(w.col(v) + e)) t = fmaf(d, d, t);
+      }
+    }
+    t = cta_sum_1b(t, red[1]);
+    if (csize > 1) t = cluster_sum(t, &slot[1], csize);
+    const float r = rsqrtf(fmaf(t, a.inv_n, a.eps));
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * tpr;
+      if (v >= w.nvec) continue;
+      const uint4* at = params + k * blockDim.x + threadIdx.x;
+      float f[VE], p[VE];
+      unpack(s[k], f);
+      unpack(kept16<PM>(at, lot), p);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) f[e] = (f[e] - mu) * r * p[e];
+      if (a.beta) {
+        unpack(kept16<PM>(at + kM * lot, lot), p);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] += p[e];
+      }
+      w.store(a.y + base, v, pack_from<T, VE>(f));
+    }
+    if (first == 0) {
+      if (a.mean) a.mean[row] = mu;
+      if (a.inv_std) a.inv_std[row] = r;
+    }
+  }
+  if (csize > 1) cluster_sync();  // peers may still read slot
+}
+
 // Rows of any length: one CTA walks the row three times (sum, centred squares,
 // output); the later walks are served by L2 for rows that fit there.  The mean
 // is known before the squares are taken, so an offset costs no digits.
@@ -371,6 +584,22 @@ struct LayerGradRow {
     }
   }
 
+  // the same by windows
+  __device__ __forceinline__ void load_gamma(const M* gamma, const Window<VE>& w, int first,
+                                             int step, int end) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int v = first + k * step;
+      float f[VE] = {};
+      if (v < end) unpack(w.params(gamma, v), f);
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        if constexpr (VE == 1) gm[k][i] = f[0];
+        else gm[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
+      }
+    }
+  }
+
   // vector k of a row: adds it to dgamma and dbeta, and to the sums of g (tg)
   // and g * u (tu)
   __device__ __forceinline__ void take(int k, const Pack<T, VE>& dy, const Pack<T, VE>& s,
@@ -387,9 +616,9 @@ struct LayerGradRow {
     }
   }
 
-  // dS of vector k, k1 = -r * mean(g), k2 = -r * mean(g * u); stored at dx
-  __device__ __forceinline__ void give(int k, float r, float k1, float k2, const Pack<T, VE>* ds,
-                                       T* dx) {
+  // dS of vector k, k1 = -r * mean(g), k2 = -r * mean(g * u)
+  __device__ __forceinline__ Pack<T, VE> give(int k, float r, float k1, float k2,
+                                              const Pack<T, VE>* ds) {
     Pack<T, VE> out;
 #pragma unroll
     for (int i = 0; i < H; ++i) {
@@ -399,7 +628,7 @@ struct LayerGradRow {
       if constexpr (VE == 1) out.v[0] = from_f32<T>(d);
       else set2(out, i, d.x, d.y);
     }
-    if (dx) st_stream<T, VE>(dx, out);
+    return out;
   }
 
   // one of dg, db and dc of a vector, an element at a time
@@ -522,7 +751,10 @@ __host__ __device__ constexpr int layer_slot_bytes(int vectors) {
   return VE > 1 ? vectors * 16 : (vectors * static_cast<int>(sizeof(T)) + 15) / 16 * 16 + 16;
 }
 
-template <typename T, typename M, int VE, int NV, bool BIAS, bool LANE>
+//
+// With WINDOW rows are taken by windows: a part's rows are then a multiple of VE
+// apart.
+template <typename T, typename M, int VE, int NV, bool BIAS, bool LANE, bool WINDOW = false>
 __global__ void __launch_bounds__(LANE ? kLayerGradLaneThreads : kLayerThreads, 1)
 layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice, int stages,
                        unsigned* status, unsigned long long limit_ns, int stall) {
@@ -535,6 +767,9 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   const unsigned csize = LANE ? 1u : cluster_size();
   const unsigned rank = csize > 1 ? cluster_rank() : 0u;
   const int part = blockIdx.x / csize;
+  const Window<VE> w(part, a.n);
+  const int shift = WINDOW ? w.shift : 0;
+  if (WINDOW) nvec = w.nvec;
   // this CTA's vectors of a row: [lo, lo + count)
   const int lo = static_cast<int>(rank) * slice;
   const int count = LANE ? nvec : (nvec - lo < slice ? (nvec > lo ? nvec - lo : 0) : slice);
@@ -556,7 +791,7 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   pdl_trigger();
 
   // the tile whose first row is `row`: its place in the tensors, its elements
-  auto offset = [&](int64_t row) { return row * a.n + static_cast<int64_t>(lo) * VE; };
+  auto offset = [&](int64_t row) { return row * a.n - shift + static_cast<int64_t>(lo) * VE; };
   auto length = [&](int64_t row) {
     return static_cast<int>(a.rows - row < rows_per ? a.rows - row : rows_per) * count * VE;
   };
@@ -566,7 +801,11 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
     unsigned char* dst = ring + st * 3 * slot_bytes;
     unsigned long long* bar = &full[st];
     if constexpr (VE > 1) {
-      const unsigned bytes = len * static_cast<unsigned>(sizeof(T));
+      unsigned bytes = len * static_cast<unsigned>(sizeof(T));
+      if constexpr (WINDOW) {  // the tensor's last vector may not be whole
+        const int64_t left = (a.rows * a.n - off) / VE;
+        if (left < count) bytes = left > 0 ? static_cast<unsigned>(left) * 16 : 0u;
+      }
       mbar_arrive_expect_tx(bar, bytes * (a.ds ? 3 : 2));
       if (bytes == 0) return;
       bulk_load(dst, a.dy + off, bytes, bar);
@@ -586,8 +825,16 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   if (threadIdx.x == 0)
     for (int i = 0; i < stages && i < tiles && !stall; ++i) issue(row0 + i * stride, i);
 
+  // vector v of a stage, cut to the row's elements; the tensor's last elements,
+  // which no copy brings, come from global memory
+  auto at_edge = [&](const T* window, const P* staged, int v, bool last) {
+    P p = last ? w.load(window, lo + v, true) : staged[v];
+    w.mask(lo + v, &p);
+    return p;
+  };
   LayerGradRow<T, M, VE, NV, BIAS> x;
-  x.load_gamma(a.gamma + static_cast<int64_t>(lo) * VE, first, step, count);
+  if constexpr (WINDOW) x.load_gamma(a.gamma, w, lo + first, step, lo + count);
+  else x.load_gamma(a.gamma + static_cast<int64_t>(lo) * VE, first, step, count);
   bool alive = true;
   int64_t row = row0 + group;
   // the next row's statistics are on their way as well
@@ -618,7 +865,15 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int v = first + k * step;
-        if (v < nv) x.take(k, dy[v], s[v], mu, r, tg, tu);
+        if (v >= nv) continue;
+        if (WINDOW && w.cut(lo + v)) {
+          const int64_t off = row * a.n - shift;
+          const bool last = row == a.rows - 1;
+          x.take(k, at_edge(a.dy + off, dy, v, last), at_edge(a.s + off, s, v, last), mu, r, tg,
+                 tu);
+        } else {
+          x.take(k, dy[v], s[v], mu, r, tg, tu);
+        }
       }
     } else {
       const int64_t numel = a.rows * a.n, off = offset(row - group);
@@ -651,7 +906,17 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int v = first + k * step;
-        if (v < nv) x.give(k, r, k1, k2, a.ds ? ds + v : nullptr, dx ? dx + v * VE : nullptr);
+        if (v >= nv) continue;
+        if (WINDOW && w.cut(lo + v)) {
+          const int64_t off = row * a.n - shift;
+          P h;
+          if (a.ds) h = at_edge(a.ds + off, ds, v, row == a.rows - 1);
+          const P out = x.give(k, r, k1, k2, a.ds ? &h : nullptr);
+          if (dx) w.store(a.dx + off, lo + v, out);
+        } else {
+          const P out = x.give(k, r, k1, k2, a.ds ? ds + v : nullptr);
+          if (dx) st_stream<T, VE>(dx + v * VE, out);
+        }
       }
     } else {
       const int64_t numel = a.rows * a.n, off = offset(row - group);
@@ -664,7 +929,8 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
         if (v >= nv) continue;
         Pack<T, VE> h;
         if (a.ds) h = ds.take(stage + 2 * slot_bytes, group * count + v, edge);
-        x.give(k, r, k1, k2, a.ds ? &h : nullptr, dx ? dx + v : nullptr);
+        const Pack<T, VE> out = x.give(k, r, k1, k2, a.ds ? &h : nullptr);
+        if (dx) st_stream<T, VE>(dx + v, out);
       }
     }
     row += stride;
@@ -682,6 +948,28 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   const bool sums = a.dgamma || a.dbeta || a.dbias;
   if constexpr (LANE) {
     if (sums) layer_grad_lane_sums<T, M, VE, NV, BIAS>(a, x, acc, tpr);
+  } else if constexpr (WINDOW) {
+    // through shared memory, where they are turned to their columns' order
+    float* turn = reinterpret_cast<float*>(ring);
+    float* p = a.part + part * 3 * a.pitch;
+    for (int o = 0; o < (BIAS ? 3 : 2) && sums; ++o) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int v = first + k * step;
+        if (v >= count) continue;
+        float f[VE];
+        x.elements(o == 0 ? x.dg[k] : o == 1 ? x.db[k] : x.dc[BIAS ? k : 0], f);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) turn[v * VE + e] = f[e];
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < count * VE; i += blockDim.x) {
+        const int col = w.col(lo) + i;
+        if (w.has(col)) p[o * a.pitch + col] = turn[i];
+      }
+    }
+    if (csize > 1) cluster_sync();  // peers may still read slot
   } else {
     float* p = a.part + part * 3 * a.pitch;
 #pragma unroll

@@ -19,6 +19,14 @@ constexpr int kLayerLaneCtas = 152 * 6;
 
 constexpr int kLayerMaxCluster = 8;  // the portable cluster size
 
+// Rows that are not whole vectors go by windows from these sizes on; smaller calls
+// wait for one row's latency, and of short rows most of a warp is idle.  Element
+// by element against windows, us: forward 1999 x 1027 float16 9.1, 10.2; 3001 x
+// 1027 14.3, 13.6; 16384 x 1027 65.6, 48.4; gradient 304 x 1027 9.5, 10.2; 1999 x
+// 1027 19.6, 18.5; 16384 x 1027 99, 62; 65536 x 67 84, 117; 65536 x 129 127, 118.
+constexpr int kWindowHidden = 65, kWindowGradHidden = 128;
+constexpr int64_t kWindowElements = 5 << 19, kWindowGradElements = 3 << 18;
+
 // How a row is spread: `lane` threads of a warp, or `block` threads of each of
 // `csize` CTAs, nv vectors per thread; nv 0: the row is walked.
 struct LayerPlan {
@@ -74,6 +82,76 @@ cudaError_t launch_layer_ve(const LayerCall& c, const LayerArgs<T, M>& a, cudaSt
                          0, stream, a, p.block * p.csize, static_cast<int>(nvec));
 }
 
+// The CTAs of `fn` that the device holds at once; its shared-memory limit is
+// raised and the driver is asked once per device, kernel and size.
+template <class Fn>
+cudaError_t layer_resident(Fn fn, int block, int smem, int* resident) {
+  struct Key {
+    int dev, block, smem;
+    const void* fn;
+  };
+  static PlanCache<Key, int> cache;
+  Key k;
+  memset(&k, 0, sizeof(k));
+  cudaError_t e = cudaGetDevice(&k.dev);
+  if (e != cudaSuccess) return e;
+  k.block = block;
+  k.smem = smem;
+  k.fn = reinterpret_cast<const void*>(fn);
+  if (cache.get(k, resident)) return cudaSuccess;
+  int sms = 0, per_sm = 0;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, k.dev);
+  if (e == cudaSuccess && smem > 0)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, block, smem);
+  if (e != cudaSuccess) return e;
+  *resident = (per_sm > 0 ? per_sm : 1) * sms;
+  cache.put(k, *resident);
+  return cudaSuccess;
+}
+
+inline bool on_vector(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The most vectors that a row's window has.
+template <int VE>
+int64_t window_vectors(int64_t hidden) {
+  return (hidden + 2 * (VE - 1)) / VE;
+}
+
+// `parts` CTAs (clusters) of which each takes every parts-th of `rows` rows, if
+// rows of one part must be a multiple of `ve` apart.
+inline int window_parts(int64_t rows, int64_t parts, int ve) {
+  if (parts >= rows) return static_cast<int>(rows);
+  return static_cast<int>(parts > ve ? parts - parts % ve : ve);
+}
+
+// Rows that are not whole vectors, by windows; *done: whether their length allows it.
+template <typename T, typename M, int VE>
+cudaError_t launch_layer_window(const LayerCall& c, const LayerArgs<T, M>& a, cudaStream_t stream,
+                                bool* done) {
+  *done = false;
+  const int64_t nvec = window_vectors<VE>(c.hidden);
+  const int nv = nvec <= 256 ? 1 : VE == 4 && nvec > 512 ? 4 : 2;
+  int csize = 1;
+  while (csize < kLayerMaxCluster && nvec > static_cast<int64_t>(kLayerThreads) * nv * csize)
+    csize *= 2;
+  if (nvec > static_cast<int64_t>(kLayerThreads) * nv * csize) return cudaSuccess;
+  const int block = static_cast<int>(((nvec + nv * csize - 1) / (nv * csize) + 31) / 32 * 32);
+  constexpr int kMost = VE == 4 ? 4 : 2;
+  auto* fn = nv == 1   ? layer_window_kernel<T, M, VE, 1>
+             : nv == 2 ? layer_window_kernel<T, M, VE, 2>
+                       : layer_window_kernel<T, M, VE, kMost>;
+  int resident = 0;
+  const int smem = nv * block * 16 * layer_window_pieces<T, M, VE>();
+  cudaError_t e = layer_resident(fn, block, smem, &resident);
+  if (e != cudaSuccess) return e;
+  *done = true;
+  const int parts = window_parts(c.rows, resident / csize, VE);
+  return launch_clusters(fn, dim3(static_cast<unsigned>(parts * csize)), block, csize, smem,
+                         stream, a, block * csize, parts);
+}
+
 template <typename T, typename M>
 cudaError_t launch_layer_tm(const LayerCall& c, cudaStream_t stream) {
   constexpr int VE = 16 / sizeof(T);
@@ -82,47 +160,33 @@ cudaError_t launch_layer_tm(const LayerCall& c, cudaStream_t stream) {
                     static_cast<const T*>(c.bias), static_cast<T*>(c.y), static_cast<T*>(c.s),
                     c.mean, c.inv_std, c.rows, static_cast<int>(c.hidden),
                     1.0f / static_cast<float>(c.hidden), c.eps};
-  return c.vec ? launch_layer_ve<T, M, VE>(c, a, stream) : launch_layer_ve<T, M, 1>(c, a, stream);
+  if (c.vec) return launch_layer_ve<T, M, VE>(c, a, stream);
+  if (c.hidden >= kWindowHidden && c.rows * c.hidden >= kWindowElements && on_vector(c.x) &&
+      on_vector(c.skip) && on_vector(c.y) && on_vector(c.s)) {
+    bool done;
+    const cudaError_t e = launch_layer_window<T, M, VE>(c, a, stream, &done);
+    if (done || e != cudaSuccess) return e;
+  }
+  return launch_layer_ve<T, M, 1>(c, a, stream);
 }
 
-// The streamed gradient: its shared-memory limit is raised and the CTAs that an
-// SM holds are asked for once per device, kernel and size; the grid is at most
-// one wave of them.
+// The streamed gradient: at most one wave of CTAs.  `apart`: rows of a part are a
+// multiple of it apart.
 template <typename T, typename M, class Fn>
 cudaError_t launch_layer_grad_ring(Fn fn, LayerGradArgs<T, M>* a, int block, int csize,
                                    int tile_bytes, int tpr, int nvec, int slice,
-                                   cudaStream_t stream) {
-  struct Key {
-    int dev, block, smem;
-    const void* fn;
-  };
-  static PlanCache<Key, int> cache;
+                                   cudaStream_t stream, int apart = 1) {
   // CTAs of more than 256 threads fill an SM's registers alone; of the others
   // two share its memory
   const int budget = block > 256 ? 200 * 1024 : 100 * 1024;
   int stages = kLayerStages;
   while (stages > 2 && stages * tile_bytes > budget) --stages;
   const int smem = tile_bytes * stages;
-  Key k;
-  memset(&k, 0, sizeof(k));
-  cudaError_t e = cudaGetDevice(&k.dev);
-  if (e != cudaSuccess) return e;
-  k.block = block;
-  k.smem = smem;
-  k.fn = reinterpret_cast<const void*>(fn);
   int resident = 0;
-  if (!cache.get(k, &resident)) {
-    int sms = 0, per_sm = 0;
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, k.dev);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, block, smem);
-    if (e != cudaSuccess) return e;
-    resident = (per_sm > 0 ? per_sm : 1) * sms;
-    cache.put(k, resident);
-  }
+  const cudaError_t e = layer_resident(fn, block, smem, &resident);
+  if (e != cudaSuccess) return e;
   if (a->parts > resident / csize) a->parts = resident / csize;
+  if (apart > 1) a->parts = window_parts(a->rows, a->parts, apart);
   unsigned* status = pipe_status_word();
   if (!status) return cudaErrorSymbolNotFound;
   const bool stall = pipe_stalled();
@@ -132,16 +196,16 @@ cudaError_t launch_layer_grad_ring(Fn fn, LayerGradArgs<T, M>* a, int block, int
 }
 
 // The one-pass gradient, NV vectors per thread of `block` threads of `csize` CTAs.
-template <typename T, typename M, int VE, int NV>
+template <typename T, typename M, int VE, int NV, bool WINDOW = false>
 cudaError_t launch_layer_grad_cta(const LayerGradCall& c, LayerGradArgs<T, M>* a, int csize,
                                   cudaStream_t stream) {
-  const int nvec = static_cast<int>(c.hidden / VE);
+  const int nvec = static_cast<int>(WINDOW ? window_vectors<VE>(c.hidden) : c.hidden / VE);
   const int slice = (nvec + csize - 1) / csize;
   const int block = ((slice + NV - 1) / NV + 31) / 32 * 32;
-  auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, false>
-                     : layer_grad_ring_kernel<T, M, VE, NV, false, false>;
+  auto* fn = c.dbias ? layer_grad_ring_kernel<T, M, VE, NV, true, false, WINDOW>
+                     : layer_grad_ring_kernel<T, M, VE, NV, false, false, WINDOW>;
   return launch_layer_grad_ring(fn, a, block, csize, 3 * layer_slot_bytes<T, VE>(slice), 0, nvec,
-                                slice, stream);
+                                slice, stream, WINDOW ? VE : 1);
 }
 
 template <typename T, typename M, int VE, int NV>
@@ -161,26 +225,29 @@ cudaError_t launch_layer_grad_lane(const LayerGradCall& c, LayerGradArgs<T, M>* 
 
 // The gradient form that the row's length allows; sets a->parts to the parts
 // that it writes.
-template <typename T, typename M, int VE>
+template <typename T, typename M, int VE, bool WINDOW = false>
 cudaError_t launch_layer_grad_ve(const LayerGradCall& c, LayerGradArgs<T, M>* a,
                                  cudaStream_t stream) {
   // at most sixteen elements per thread: their sums and the row fit 128 registers
   constexpr int kMost = VE == 8 ? 2 : VE == 4 ? 4 : 8;
-  a->ve = VE;
-  const int64_t nvec = c.hidden / VE;
-  if (nvec <= 32) return launch_layer_grad_lane<T, M, VE, 1>(c, a, stream);
-  if (nvec <= 64) return launch_layer_grad_lane<T, M, VE, 2>(c, a, stream);
+  a->ve = WINDOW ? 1 : VE;
+  const int64_t nvec = WINDOW ? window_vectors<VE>(c.hidden) : c.hidden / VE;
+  if constexpr (!WINDOW) {
+    if (nvec <= 32) return launch_layer_grad_lane<T, M, VE, 1>(c, a, stream);
+    if (nvec <= 64) return launch_layer_grad_lane<T, M, VE, 2>(c, a, stream);
+  }
   // a CTA's slice of a row: what its threads hold, or (streamed) four stages of
   // three slices in 192 KB
-  constexpr int64_t kSlice = VE > 1 ? 1024 : kLayerThreads * kMost;
+  constexpr int64_t kSlice = VE == 8 ? 1024 : VE == 4 ? 1032 : kLayerThreads * kMost;
   int csize = 1;
   while (csize < kLayerMaxCluster && nvec > kSlice * csize) csize *= 2;
   if (nvec <= kSlice * csize) {
-    if (nvec <= 128) return launch_layer_grad_cta<T, M, VE, 1>(c, a, csize, stream);
+    if (nvec <= 128) return launch_layer_grad_cta<T, M, VE, 1, WINDOW>(c, a, csize, stream);
     if (kMost == 2 || nvec <= 512)
-      return launch_layer_grad_cta<T, M, VE, 2>(c, a, csize, stream);
-    return launch_layer_grad_cta<T, M, VE, kMost>(c, a, csize, stream);
+      return launch_layer_grad_cta<T, M, VE, 2, WINDOW>(c, a, csize, stream);
+    return launch_layer_grad_cta<T, M, VE, kMost, WINDOW>(c, a, csize, stream);
   }
+  if constexpr (WINDOW) return launch_layer_grad_ve<T, M, 1>(c, a, stream);
   a->ve = 1;
   cudaError_t e = launch_pdl(layer_grad_rows_kernel<T, M, VE>, dim3(static_cast<unsigned>(c.rows)),
                              layer_walk_block(nvec), stream, *a);
@@ -206,8 +273,13 @@ cudaError_t launch_layer_grad_tm(const LayerGradCall& c, cudaStream_t stream) {
                         1.0f / static_cast<float>(c.hidden)};
   cudaError_t e = cudaSuccess;
   if (c.rows > 0) {
-    e = c.vec ? launch_layer_grad_ve<T, M, VE>(c, &a, stream)
-              : launch_layer_grad_ve<T, M, 1>(c, &a, stream);
+    if (c.vec)
+      e = launch_layer_grad_ve<T, M, VE>(c, &a, stream);
+    else if (c.hidden >= kWindowGradHidden && c.rows * c.hidden >= kWindowGradElements &&
+             on_vector(c.dy) && on_vector(c.s) && on_vector(c.ds) && on_vector(c.dx))
+      e = launch_layer_grad_ve<T, M, VE, true>(c, &a, stream);
+    else
+      e = launch_layer_grad_ve<T, M, 1>(c, &a, stream);
     if (e != cudaSuccess) return e;
   } else {
     a.parts = 0;  // empty sums

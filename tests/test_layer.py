@@ -145,6 +145,59 @@ def test_grad_unaligned(rows, hidden, t, m):
     check_grad(make(rows, hidden, t, m, hidden), True, True, shift=1)
 
 
+# Many rows that are not whole 16-byte vectors: one row or more per CTA, rows of one
+# to several CTAs, every shift, a last row whose last vector is cut
+ODD_SHAPES = [(40001, 67), (20400, 131), (3000, 1027), (1300, 2050), (700, 4095), (330, 8195),
+              (141, 20001), (61, 50003)]
+
+
+@pytest.mark.parametrize("t,m", TYPES)
+@pytest.mark.parametrize("rows,hidden", ODD_SHAPES)
+def test_forward_many_odd_rows(rows, hidden, t, m):
+    d = make(rows, hidden, t, m, rows + hidden)
+    check_forward(d, t, True, True, True)
+    check_forward(d, t, False, False, False)
+
+
+@pytest.mark.parametrize("t,m", TYPES)
+@pytest.mark.parametrize("rows,hidden", ODD_SHAPES + [(6100, 129), (800, 1027), (13, 65001)])
+def test_grad_many_odd_rows(rows, hidden, t, m):
+    d = make(rows, hidden, t, m, rows + hidden)
+    check_grad(d, True, True)
+    check_grad(d, False, False)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,hidden", [(3000, 1027), (330, 8195)])
+def test_many_odd_rows_special_values(rows, hidden, t):
+    """NaN and infinities stay in their rows, whose elements share vectors with
+    those of their neighbours, and in dgamma and dbeta in their columns."""
+    d = make(rows, hidden, t, t, 12)
+    clean = {k: dev(v) for k, v in d.items()}
+    bad = {k: v.clone() for k, v in clean.items()}
+    marked = [1, 8, rows // 2, rows - 1]
+    for i, r in enumerate(marked):
+        bad["x"][r, 0 if i % 2 else hidden - 1] = math.nan if i < 2 else math.inf
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[marked] = False
+    args = ("skip", "gamma", "beta", "bias")
+    want = b2.skip_layer_stats(clean["x"], *(clean[k] for k in args), epsilon=EPS)
+    got = b2.skip_layer_stats(bad["x"], *(bad[k] for k in args), epsilon=EPS)
+    for w, g in zip(want, got):
+        assert torch.equal(w[keep], g[keep])
+    assert bool(torch.isnan(got[0][~keep].float()).all())
+    bad["dy"][marked, 5] = math.nan
+    stats = want[1:]
+    dx, dg, db, dc = b2.skip_layer_grad(clean["dy"], *stats, clean["gamma"], want_bias=True)
+    bx, bg, bb, bc = b2.skip_layer_grad(bad["dy"], *stats, bad["gamma"], want_bias=True)
+    assert torch.equal(dx[keep], bx[keep]) and bool(torch.isnan(bx[~keep].float()).all())
+    for w, g in ((dg, bg), (db, bb)):
+        columns = torch.isnan(g.float())
+        assert bool(columns[5]) and int(columns.sum()) == 1
+        assert torch.equal(w[~columns], g[~columns])
+    assert bool(torch.isnan(bc.float()).all())
+
+
 def test_grad_wanted_outputs():
     """Each output alone has the bits it has among the others; equal calls give
     equal bits."""
@@ -220,7 +273,8 @@ def test_on_a_stream_of_its_own_and_in_a_graph():
 
 
 @pytest.mark.parametrize("rows,hidden,shift", [(5, 4096, 0), (37, 64, 0), (7, 1027, 1),
-                                               (600, 768, 0)])
+                                               (600, 768, 0), (3001, 1027, 0),
+                                               (331, 8195, 0)])
 def test_writes_exactly_its_outputs(rows, hidden, shift):
     """Outputs inside 0xFF-filled blocks: nothing beside them changes, and the
     workspace's size is enough."""

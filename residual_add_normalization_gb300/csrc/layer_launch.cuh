@@ -284,11 +284,15 @@ cudaError_t launch_layer_grad_tm(const LayerGradCall& c, cudaStream_t stream) {
   } else {
     a.parts = 0;  // empty sums
   }
-  if (c.dgamma || c.dbeta || c.dbias)
-    e = launch_pdl(layer_grad_finish_kernel<T, M>,
-                   dim3(static_cast<unsigned>((c.hidden + kLayerFinishCols - 1) /
-                                              kLayerFinishCols), 3), 1024, stream, a);
-  return e;
+  if (!c.dgamma && !c.dbeta && !c.dbias) return e;
+  const auto blocks = [&](int cols) {
+    return dim3(static_cast<unsigned>((c.hidden + cols - 1) / cols), 3);
+  };
+  if (c.hidden <= 2048)
+    return launch_pdl(layer_grad_finish_kernel<T, M, 32>, blocks(32), kLayerFinishThreads<32>,
+                      stream, a);
+  return launch_pdl(layer_grad_finish_kernel<T, M, 128>, blocks(128), kLayerFinishThreads<128>,
+                    stream, a);
 }
 
 }  // namespace b200norm

@@ -556,6 +556,12 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
 // elements, so the arithmetic goes two elements at a time.  Every product and
 // sum is rounded by itself, so that every instantiation gives the same bits.
 // ---------------------------------------------------------------------------
+// Vectors a thread holds at most: sixteen elements, whose sums and row fit 128 registers.
+template <int VE>
+__host__ __device__ constexpr int layer_grad_most() {
+  return VE == 8 ? 2 : VE == 4 ? 4 : 8;
+}
+
 template <typename T, typename M, int VE, int NV, bool BIAS>
 struct LayerGradRow {
   using V = typename std::conditional<VE == 1, float, float2>::type;  // pairs of a vector
@@ -732,6 +738,17 @@ __device__ __forceinline__ void layer_grad_lane_sums(
   }
 }
 
+// Writes v at `local`'s place in CTA `rank` of the cluster; its 8 bytes complete on
+// the barrier at `bar`'s place there.
+__device__ __forceinline__ void send_to_peer(float2* local, unsigned rank, float2 v,
+                                             unsigned long long* bar) {
+  unsigned to, at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(local)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(bar)), "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+               :: "r"(to), "f"(v.x), "f"(v.y), "r"(at) : "memory");
+}
+
 // The inputs are streamed through shared memory: one thread keeps the next
 // `stages` tiles of dy, S and ds (contiguous bytes, one bulk copy each) on their
 // way while the CTA works on the present one.  Without the stream, threads can
@@ -739,7 +756,10 @@ __device__ __forceinline__ void layer_grad_lane_sums(
 // (16384 x 4096 bfloat16: 135 us).  Part p takes tiles p, p + parts, ....
 //
 // A tile is a row (of a cluster's CTA: its slice of the row), or with LANE the
-// 256 / tpr consecutive rows that the CTA's lane groups take.  A stage is free
+// 256 / tpr consecutive rows that the CTA's lane groups take.  The CTAs of a
+// cluster send their sums of a row to one another; two sets of slots are enough,
+// for a CTA sends its sums of the next row only once it has all of this one.
+// A stage is free
 // again once the CTA has met at the next tile's barrier.  The waits for a copy
 // are bounded; a thread whose wait gave up records it and runs on without
 // waiting (its outputs are then undefined), so that every barrier is met.
@@ -762,9 +782,11 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ alignas(8) unsigned long long full[kLayerStages];
   __shared__ float2 red[2][16];
-  __shared__ float2 slot[2];
+  __shared__ float2 slot[2][8];
+  __shared__ alignas(8) unsigned long long sent[2];
   __shared__ float acc[LANE ? (BIAS ? 3 : 2) : 1][LANE ? 32 * NV * VE : 1];
-  const unsigned csize = LANE ? 1u : cluster_size();
+  // only slices that take every vector a thread can hold are parts of longer rows
+  const unsigned csize = !LANE && NV == layer_grad_most<VE>() ? cluster_size() : 1u;
   const unsigned rank = csize > 1 ? cluster_rank() : 0u;
   const int part = blockIdx.x / csize;
   const Window<VE> w(part, a.n);
@@ -784,9 +806,11 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kLayerStages; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sent[i], 1);
     mbar_init_fence();
   }
-  __syncthreads();
+  if (csize > 1) cluster_sync();  // peers complete on `sent`
+  else __syncthreads();
   pdl_wait();
   pdl_trigger();
 
@@ -898,7 +922,20 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
     // everyone is done with the tile before this one
     if (threadIdx.x == 0 && alive && i > 0 && i - 1 + stages < tiles)
       issue(row - group + (stages - 1) * stride, before);
-    if (csize > 1) t = cluster_sum2(t, &slot[i & 1].x, &slot[i & 1].y, csize);
+    if (csize > 1) {
+      const int b = i & 1;
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(&sent[b], csize * 8);
+      if (threadIdx.x < csize) send_to_peer(&slot[b][rank], threadIdx.x, t, &sent[b]);
+      if (alive && !mbar_wait(&sent[b], i >> 1 & 1, limit_ns)) {
+        alive = false;
+        atomicExch(status, kStatusDeviceTimeout);
+      }
+      t = slot[b][0];
+      for (unsigned q = 1; q < csize; ++q) {
+        t.x += slot[b][q].x;
+        t.y += slot[b][q].y;
+      }
+    }
     const float k1 = -r * (t.x * a.inv_n), k2 = -r * (t.y * a.inv_n);
     T* dx = a.dx ? a.dx + offset(row) : nullptr;
     if constexpr (VE > 1) {
@@ -969,7 +1006,6 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
         if (w.has(col)) p[o * a.pitch + col] = turn[i];
       }
     }
-    if (csize > 1) cluster_sync();  // peers may still read slot
   } else {
     float* p = a.part + part * 3 * a.pitch;
 #pragma unroll
@@ -986,7 +1022,12 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
         part_store<VE>(p + 2 * a.pitch, lo + v, a.n, f);
       }
     }
-    if (csize > 1) cluster_sync();  // peers may still read slot
+  }
+  if (csize > 1) {
+    cluster_sync();  // peers' sums may still be on their way to this CTA
+    if (!alive && threadIdx.x == 0)
+      for (int i = 0; i < 2 && i < tiles; ++i)
+        mbar_wait(&sent[(tiles - 1 - i) & 1], (tiles - 1 - i) >> 1 & 1, limit_ns);
   }
 }
 

@@ -228,8 +228,7 @@ cudaError_t launch_layer_grad_lane(const LayerGradCall& c, LayerGradArgs<T, M>* 
 template <typename T, typename M, int VE, bool WINDOW = false>
 cudaError_t launch_layer_grad_ve(const LayerGradCall& c, LayerGradArgs<T, M>* a,
                                  cudaStream_t stream) {
-  // at most sixteen elements per thread: their sums and the row fit 128 registers
-  constexpr int kMost = VE == 8 ? 2 : VE == 4 ? 4 : 8;
+  constexpr int kMost = layer_grad_most<VE>();
   a->ve = WINDOW ? 1 : VE;
   const int64_t nvec = WINDOW ? window_vectors<VE>(c.hidden) : c.hidden / VE;
   if constexpr (!WINDOW) {

@@ -757,8 +757,9 @@ __device__ __forceinline__ void send_to_peer(float2* local, unsigned rank, float
 //
 // A tile is a row (of a cluster's CTA: its slice of the row), or with LANE the
 // 256 / tpr consecutive rows that the CTA's lane groups take.  The CTAs of a
-// cluster send their sums of a row to one another; two sets of slots are enough,
-// for a CTA sends its sums of the next row only once it has all of this one.
+// cluster send their sums of a row to one another (4096 x 16384 bfloat16: 120 us,
+// 173 with a cluster barrier and remote loads); two sets of slots are enough, for
+// a CTA sends its sums of the next row only once it has all of this one.
 // A stage is free
 // again once the CTA has met at the next tile's barrier.  The waits for a copy
 // are bounded; a thread whose wait gave up records it and runs on without
@@ -924,8 +925,9 @@ layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice
       issue(row - group + (stages - 1) * stride, before);
     if (csize > 1) {
       const int b = i & 1;
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(&sent[b], csize * 8);
-      if (threadIdx.x < csize) send_to_peer(&slot[b][rank], threadIdx.x, t, &sent[b]);
+      // after a wait that gave up nothing is armed or sent, and the peers give up too
+      if (threadIdx.x == 0 && alive) mbar_arrive_expect_tx(&sent[b], csize * 8);
+      if (threadIdx.x < csize && alive) send_to_peer(&slot[b][rank], threadIdx.x, t, &sent[b]);
       if (alive && !mbar_wait(&sent[b], i >> 1 & 1, limit_ns)) {
         alive = false;
         atomicExch(status, kStatusDeviceTimeout);

@@ -167,6 +167,15 @@ def test_grad_many_odd_rows(rows, hidden, t, m):
     check_grad(d, False, False)
 
 
+@pytest.mark.parametrize("t,m", TYPES)
+@pytest.mark.parametrize("rows,hidden", [(400, 9000), (300, 16384), (130, 32768), (50, 65536)])
+def test_grad_many_long_rows(rows, hidden, t, m):
+    """More rows than clusters of CTAs, of two to eight CTAs each."""
+    d = make(rows, hidden, t, m, rows + hidden)
+    check_grad(d, True, True)
+    check_grad(d, False, False)
+
+
 @pytest.mark.parametrize("t", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,hidden", [(3000, 1027), (330, 8195)])
 def test_many_odd_rows_special_values(rows, hidden, t):

@@ -429,13 +429,13 @@ def _scratch(workspace, nbytes, x, index, stream):
     if not nbytes:
         return None, 0
     if nbytes > _SCRATCH_KEPT or torch.cuda.is_current_stream_capturing():
-        return x.new_empty(nbytes, dtype=torch.uint8), nbytes
+        return torch.empty(nbytes, dtype=torch.uint8, device=x.device), nbytes
     blocks = getattr(_scratch_of_thread, "blocks", None)
     if blocks is None:
         blocks = _scratch_of_thread.blocks = {}
     block = blocks.get((index, stream))
     if block is None or block.numel() < nbytes:
-        block = x.new_empty(max(nbytes, 1 << 20), dtype=torch.uint8)
+        block = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
         blocks[(index, stream)] = block
     return block, block.numel()
 
@@ -447,7 +447,9 @@ def _like(name, t, x, index):
 
 def _new(name, t, shape, x, index):
     """An output of x's type and another shape."""
-    return x.new_empty(shape) if t is None else _is(name, t, shape, x, index, x.dtype)
+    if t is not None:
+        return _is(name, t, shape, x, index, x.dtype)
+    return torch.empty(shape, dtype=x.dtype, device=x.device)
 
 
 def _last_axis(name, t):
@@ -476,7 +478,7 @@ def _skip_layer(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, 
             s = _like("input_skip_bias_sum", sum_out, x, index)
         mean = inv = None
         if stats:
-            mean = x.new_empty(tuple(x.shape[:-1]) + (1,), dtype=torch.float32)
+            mean = torch.empty(x.shape[:-1] + (1,), dtype=torch.float32, device=x.device)
             inv = torch.empty_like(mean)
         _check((_lib or library()).b200norm_skip_layer(
             x.data_ptr(), _at(skip), gamma.data_ptr(), _at(beta), _at(bias), y.data_ptr(), _at(s),

@@ -23,7 +23,8 @@ constexpr int kLayerMaxCluster = 8;  // the portable cluster size
 // wait for one row's latency, and of short rows most of a warp is idle.  Element
 // by element against windows, us: forward 1999 x 1027 float16 9.1, 10.2; 3001 x
 // 1027 14.3, 13.6; 16384 x 1027 65.6, 48.4; gradient 304 x 1027 9.5, 10.2; 1999 x
-// 1027 19.6, 18.5; 16384 x 1027 99, 62; 65536 x 67 84, 117; 65536 x 129 127, 118.
+// 1027 (without ds) 16.0, 12.7; 16384 x 1027 88.7, 53.2; 65536 x 67 84, 117; 65536 x
+// 129 127, 118.
 constexpr int kWindowHidden = 65, kWindowGradHidden = 128;
 constexpr int64_t kWindowElements = 5 << 19, kWindowGradElements = 3 << 18;
 

@@ -75,6 +75,15 @@ B200NORM_API b200norm_status b200norm_testing_force_linear(int cg, int bn, int s
  * undefined.  on = 0 restores normal launches (limit_ns ignored). */
 B200NORM_API b200norm_status b200norm_testing_linear_stall(int on, uint64_t limit_ns);
 
+/* Leave out the event that one kind of wait of the linear operator's tensor-core
+ * products waits for (process-wide, later launches): site 1 the release of a
+ * stage of the ring, 4 that of a buffer of sums, 5 the copy of a residual.  A
+ * launch that needs the event gives up after limit_ns (in (0, 100 ms]), the other
+ * waits after 20 times that, and records B200NORM_ERR_DEVICE_TIMEOUT with that
+ * site (read with b200norm_linear_status); outputs are then undefined.  site = 0
+ * restores normal launches (limit_ns ignored). */
+B200NORM_API b200norm_status b200norm_testing_linear_withhold(int site, uint64_t limit_ns);
+
 /* Switch programmatic dependent launch off (0) or on (1, the default) for
  * every later launch of the library, on all threads.  With it on, a kernel
  * may be scheduled while the preceding grid on its stream drains and waits

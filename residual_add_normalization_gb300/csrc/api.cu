@@ -679,6 +679,16 @@ b200norm_status b200norm_testing_linear_stall(int on, uint64_t limit_ns) {
   return ok();
 }
 
+b200norm_status b200norm_testing_linear_withhold(int site, uint64_t limit_ns) {
+  if (site && (limit_ns == 0 || limit_ns > 100000000ull))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "limit_ns must be in (0, 100 ms]");
+  if (site < 0 ||
+      !set_linear_withhold(static_cast<unsigned>(site),
+                           site ? static_cast<unsigned>(limit_ns) : 0u))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "no such site");
+  return ok();
+}
+
 b200norm_status b200norm_testing_barrier_timeout(void* workspace, size_t workspace_bytes,
                                                  uint64_t limit_ns, b200norm_stream_t stream) {
   if (!workspace || workspace_bytes < kControlBytes || !aligned(workspace, 256))

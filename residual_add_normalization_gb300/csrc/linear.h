@@ -69,6 +69,13 @@ unsigned* linear_status_words();
 // A test's limit for the waits of launches that copy nothing (0: normal ones).
 unsigned long long linear_stall_limit_ns();
 void set_linear_stall(unsigned long long limit_ns);
+// A test's site whose event is left out, and how long its wait lasts (site 0: none;
+// false: not a site that can be).
+struct LinearWithhold {
+  unsigned site, limit_ns;
+};
+LinearWithhold linear_withhold();
+bool set_linear_withhold(unsigned site, unsigned limit_ns);
 
 // dz = round_T(dy * act'(z)) with rows `ldz` apart (null: not stored), and the
 // column sums of dy * act'(z) (null: not wanted) through `part`.

@@ -30,9 +30,10 @@
 // gradients' operands): the copy brings 64 x 64 squares then, and the matrix
 // instruction's descriptors say so; nothing is transposed in memory.
 //
-// Every wait is bounded: one that gives up records its site in `status` and
-// ends its role, the others then run out as well, and all meet at the end to
-// free the tensor memory.
+// Every wait is bounded: the first that gives up records its site in `status`;
+// one that gives up ends its role, the others then run out as well, and all meet
+// at the end to free the tensor memory.  A warp that waits as a whole decides as
+// a whole.
 #pragma once
 
 #include <cuda.h>
@@ -45,6 +46,7 @@ namespace b200norm {
 constexpr int kMmaK = 64;              // elements of k per stage: 128 bytes
 constexpr int kMmaRows = 128;          // rows of C per CTA
 constexpr int kMmaABytes = kMmaRows * kMmaK * 2;
+constexpr int kMmaWithheld = 20;       // how much sooner a test's site gives up
 constexpr int kMmaGroup = 8;           // row tiles a column of tiles is walked down by (16
                                        // does as well; 4 and 32 lose 4 and 6 percent)
 
@@ -58,6 +60,7 @@ struct MmaArgs {
   unsigned* status;
   unsigned long long limit_ns;
   bool stall;          // a test: nothing is copied, and the waits give up
+  unsigned withhold;   // a test: the site whose event is left out (0: none)
 };
 
 // Shared memory of a CTA: the ring, then 8 KB for each epilogue warp's results
@@ -234,6 +237,25 @@ __host__ __device__ constexpr unsigned mma_idesc(bool bf16, bool a_kc, bool b_kc
          (static_cast<unsigned>(n >> 3) << 17) | (static_cast<unsigned>(m >> 4) << 24);
 }
 
+// -- waits ----------------------------------------------------------------------
+
+// The sites recorded when a wait gives up.
+enum MmaSite : unsigned {
+  kSiteEmpty = 1, kSiteFull = 2, kSiteSums = 3, kSiteDrained = 4, kSiteResidual = 5
+};
+
+// A test's site gives up long before the others do.
+__device__ __forceinline__ unsigned long long wait_limit(const MmaArgs& g, unsigned site) {
+  return site == g.withhold ? g.limit_ns / kMmaWithheld : g.limit_ns;
+}
+
+// The whole warp's wait: each lane sees the barrier's phase, and one that gave up
+// stops them all, so that they go on together.
+__device__ __forceinline__ bool warp_wait(unsigned long long* bar, unsigned parity,
+                                          unsigned long long limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
+}
+
 // -- epilogue -------------------------------------------------------------------
 
 // z and y of N results (bias and residual already widened, or absent).
@@ -251,14 +273,15 @@ __device__ __forceinline__ void add_to(float (&v)[NC], const T* p) {
 // eight lanes never meet in a bank) and from there by tensor copies.  Stored
 // straight from the registers, a lane per row, each instruction touches 32 lines.
 // The residual comes the other way through the same buffer.
-// `drained` is called once the sums have been read.
-template <typename T, int COLS, bool FULL, int ACT, class Drained, class GiveUp>
-__device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMap* map_y,
+// `drained` is called once the sums have been read.  False: the wait for a residual
+// gave up.
+template <typename T, int COLS, bool FULL, int ACT, class Drained>
+__device__ __forceinline__ bool epilogue_tile(const MmaArgs& g, const CUtensorMap* map_y,
                                               const CUtensorMap* map_z, const CUtensorMap* map_r,
                                               unsigned d, int64_t m0, int64_t n0, int lane,
                                               unsigned char* stage, unsigned long long* bar,
                                               unsigned& phase, unsigned& turn,
-                                              Drained&& drained, GiveUp&& give_up) {
+                                              Drained&& drained) {
   const T* bias = FULL ? static_cast<const T*>(g.e.bias) : nullptr;
   const bool res = FULL && g.e.residual, keep = FULL && g.e.z;
   const bool rows = m0 < g.M;
@@ -275,7 +298,8 @@ __device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMa
       else stores_read<1>();
       if (res) {
         mbar_arrive_expect_tx(bar, kMmaStageRows);
-        tma_load<1>(at_y, map_r, static_cast<int>(n), static_cast<int>(m0), smem_addr(bar));
+        if (g.withhold != kSiteResidual)
+          tma_load<1>(at_y, map_r, static_cast<int>(n), static_cast<int>(m0), smem_addr(bar));
       }
     }
     __syncwarp();
@@ -312,7 +336,11 @@ __device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMa
       for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
       if (res) {
         if (h == 0) {
-          if (!mbar_wait(bar, phase, g.limit_ns) && lane == 0) give_up();
+          if (!warp_wait(bar, phase, wait_limit(g, kSiteResidual))) {
+            // the copy may still be on its way to this CTA's shared memory
+            if (lane == 0) mbar_wait(bar, phase, wait_limit(g, kSiteResidual));
+            return false;
+          }
           phase ^= 1;
           __syncwarp();
         }
@@ -336,6 +364,7 @@ __device__ __forceinline__ void epilogue_tile(const MmaArgs& g, const CUtensorMa
       store_commit();
     }
   }
+  return true;
 }
 
 // The same where rows are not whole vectors: 32 columns at a time are turned
@@ -442,9 +471,6 @@ __device__ __forceinline__ void epilogue_col(const Epilogue& e, int64_t m, int64
 
 // -- kernel ---------------------------------------------------------------------
 
-// The sites recorded when a wait gives up.
-enum MmaSite { kSiteEmpty = 1, kSiteFull = 2, kSiteSums = 3, kSiteDrained = 4, kSiteResidual = 5 };
-
 template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP>
 __global__ void __launch_bounds__(MmaShape<CG, BN, SWAP>::kThreads)
 linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -506,8 +532,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     tn = t % per / size;
   };
   auto give_up = [&](unsigned site) {
-    atomicExch(g.status, kStatusDeviceTimeout);
-    atomicExch(g.status + 1, site);
+    if (atomicCAS(g.status, 0u, kStatusDeviceTimeout) == 0u) atomicExch(g.status + 1, site);
   };
 
   if (warp == 0) {
@@ -522,7 +547,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
         const int n0 = tn * BN + (CG == 2 ? static_cast<int>(rank) * S::kBRows : 0);
         for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
           const int s = it % kStages;
-          if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, g.limit_ns)) {
+          if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, wait_limit(g, kSiteEmpty))) {
             give_up(kSiteEmpty);
             alive = false;
             break;
@@ -564,7 +589,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       bool alive = true;
       for (int t = unit; t < tiles && alive; t += units, ++n) {
         const int buf = n & 1;
-        if (!mbar_wait(&drained[buf], ((n >> 1) & 1) ^ 1, g.limit_ns)) {
+        if (!mbar_wait(&drained[buf], ((n >> 1) & 1) ^ 1, wait_limit(g, kSiteDrained))) {
           give_up(kSiteDrained);
           break;
         }
@@ -584,7 +609,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
 #pragma unroll
           for (int k = 0; k < kMmaK / 16; ++k)
             mma_f16<CG>(d, da + k * step_a, db + k * step_b, idesc, kb > k_lo || k > 0);
-          mma_commit<CG>(&empty[s]);
+          if (g.withhold != kSiteEmpty) mma_commit<CG>(&empty[s]);
         }
         mma_commit<CG>(&sums[buf]);
       }
@@ -598,11 +623,10 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     int n = 0;
     for (int t = unit; t < tiles; t += units, ++n) {
       const int buf = n & 1;
-      if (!mbar_wait(&sums[buf], (n >> 1) & 1, g.limit_ns)) {
+      if (!warp_wait(&sums[buf], (n >> 1) & 1, g.limit_ns)) {
         if (lane == 0) give_up(kSiteSums);
         break;
       }
-      __syncwarp();
       tc_fence_after();
       int tm, tn;
       tile_at(t, tm, tn);
@@ -633,7 +657,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       auto release = [&] {  // the sums have been read
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && g.withhold != kSiteDrained) {
           if constexpr (CG == 1) {
             mbar_arrive(&drained[buf]);
           } else {
@@ -659,13 +683,18 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
         }
         release();
       } else if (g.vec) {
+        bool fetched_all = true;
         auto run = [&](auto act) {
-          epilogue_tile<T, S::kCols, kFull, decltype(act)::value>(
+          fetched_all = epilogue_tile<T, S::kCols, kFull, decltype(act)::value>(
               g, &map_y, &map_z, &map_r, d, m0 + quarter * 32, n0 + c0, lane, stage,
-              &fetched[warp - 2], phase, turn, release, [&] { give_up(kSiteResidual); });
+              &fetched[warp - 2], phase, turn, release);
         };
         if constexpr (kFull) with_act(g.e.act, run);
         else run(Const<kActNone>());
+        if (!fetched_all) {
+          if (lane == 0) give_up(kSiteResidual);
+          break;
+        }
       } else {
         epilogue_tile_scalar<T, S::kCols, kFull>(g, d, m0 + quarter * 32, n0 + c0, lane,
                                            reinterpret_cast<float*>(stage), release);

@@ -31,6 +31,16 @@ static std::atomic<unsigned long long> g_linear_stall{0};
 unsigned long long linear_stall_limit_ns() { return g_linear_stall.load(); }
 void set_linear_stall(unsigned long long limit_ns) { g_linear_stall.store(limit_ns); }
 
+static std::atomic<LinearWithhold> g_linear_withhold{LinearWithhold{0, 0}};
+
+LinearWithhold linear_withhold() { return g_linear_withhold.load(); }
+bool set_linear_withhold(unsigned site, unsigned limit_ns) {
+  if (site != 0 && site != kSiteEmpty && site != kSiteDrained && site != kSiteResidual)
+    return false;
+  g_linear_withhold.store({site, limit_ns});
+  return true;
+}
+
 unsigned* linear_status_words() {
   constexpr int kCachedDevices = 64;  // devices past these are looked up every time
   static std::atomic<unsigned*> cache[kCachedDevices];

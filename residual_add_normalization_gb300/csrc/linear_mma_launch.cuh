@@ -64,6 +64,9 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   g.limit_ns = 1000000000ull + 4000ull * g.kblocks;
   g.stall = linear_stall_limit_ns() != 0;
   if (g.stall) g.limit_ns = linear_stall_limit_ns();
+  const LinearWithhold withhold = linear_withhold();
+  g.withhold = withhold.site;
+  if (g.withhold) g.limit_ns = withhold.limit_ns * kMmaWithheld;
   CUtensorMap map_a, map_b;
   if (!encode_operand<T>(&map_a, a, g.M, p.K, kMmaRows) ||
       !encode_operand<T>(&map_b, b, g.N, p.K, S::kBRows))

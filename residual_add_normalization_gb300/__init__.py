@@ -397,13 +397,16 @@ def _raw_stream(index, stream):
     return (torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
 
 
-def _on(index, stream, inputs):
+def _on(index, stream, tensors):
     """None, or the context to allocate and launch in.  With a stream of the
-    caller's own, outputs and scratch are allocated on it, and the inputs are
-    kept from reuse until it has passed this call."""
+    caller's own, outputs and scratch are allocated on it, and the caller's
+    tensors (inputs, outputs and workspace) are kept from reuse until it has
+    passed this call."""
     if stream is not None:
-        for t in inputs:
-            if t is not None:
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
                 t.record_stream(stream)
         return torch.cuda.stream(stream)
     if index != torch._C._cuda_getDevice():
@@ -487,7 +490,7 @@ def _skip_layer(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, 
             epsilon, _raw_stream(index, stream)))
         return y, (x if skip is None and want_sum else s), mean, inv
 
-    context = _on(index, stream, (x, skip, gamma, beta, bias))
+    context = _on(index, stream, (x, skip, gamma, beta, bias, output, sum_out))
     if context is None:
         return run()
     with context:
@@ -553,7 +556,8 @@ def skip_layer_grad(dy, s, mean, inv_std_var, gamma, *, ds=None, want_input=True
             _DTYPES[gamma.dtype], _at(ws), n, raw))
         return outs
 
-    context = _on(index, stream, (dy, s, mean, inv_std_var, gamma, ds))
+    context = _on(index, stream, (dy, s, mean, inv_std_var, gamma, ds, dx, dgamma, dbeta, dbias,
+                                  workspace))
     if context is None:
         return run()
     with context:
@@ -599,7 +603,7 @@ def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y
                                    n_in, n_out, code, activation, _at(ws), n, raw))
         return yv, zv
 
-    context = _on(index, stream, (x, weight, bias, residual))
+    context = _on(index, stream, (x, weight, bias, residual, y, z, workspace))
     if context is None:
         return run()
     with context:
@@ -641,7 +645,7 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
                                         n_in, n_out, code, activation, _at(ws), n, raw))
         return dxv, dwv, dbv
 
-    context = _on(index, stream, (dy, x, weight, z))
+    context = _on(index, stream, (dy, x, weight, z, dx, dw, db, workspace))
     if context is None:
         return run()
     with context:

@@ -138,8 +138,18 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _of_device(stream, index):
+    """The caller's stream, of the device of that index."""
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream
+
+
 def _torch_stream(device, stream):
-    return stream if stream is not None else torch.cuda.current_stream(device)
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    index = torch.device(device).index  # None: "cuda", the current device
+    return stream if index is None else _of_device(stream, index)
 
 
 def _stream(device, stream):
@@ -403,8 +413,7 @@ def _on(index, stream, tensors):
     tensors (inputs, outputs and workspace) are kept from reuse until it has
     passed this call."""
     if stream is not None:
-        if stream.device.index != index:
-            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        _of_device(stream, index)
         for t in tensors:
             if isinstance(t, torch.Tensor) and t.is_cuda:
                 t.record_stream(stream)

@@ -45,6 +45,26 @@ def test_each_entry_refuses_a_stream_of_another_device():
             call()
 
 
+def test_the_older_entries_helper_refuses_it_too():
+    with pytest.raises(ValueError, match="cuda:1"):
+        b2._stream(torch.device("cuda", 0), OtherDevice())
+    assert b2._stream(torch.device("cuda", 1), OtherDevice()).value is None
+    assert b2._stream("cuda", OtherDevice()).value is None
+
+
+@pytest.mark.gpu
+def test_each_older_entry_refuses_a_stream_of_another_device():
+    x, w = torch.ones(4, 8, device="cuda"), torch.ones(8, device="cuda")
+    x4 = torch.ones(1, 2, 2, 8, device="cuda")
+    st = OtherDevice()
+    for call in (lambda: b2.skip_rms(x, x, w, stream=st),
+                 lambda: b2.skip_rms_stats(x, x, w, stream=st),
+                 lambda: b2.gated_rms(x, x, w, stream=st),
+                 lambda: b2.skip_group(x4, x4, w, w, groups=2, activation=0, stream=st)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+
+
 MIB = 1 << 20
 
 

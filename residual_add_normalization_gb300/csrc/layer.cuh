@@ -503,9 +503,9 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
   pdl_trigger();
   __shared__ float red[33];
   const int64_t base = static_cast<int64_t>(blockIdx.x) * a.n;
-  const int nvec = a.n / VE;
+  const unsigned nvec = a.n / VE;  // unsigned: v passes 2^31 past the longest rows
   float sum = 0.0f;
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (unsigned v = threadIdx.x; v < nvec; v += blockDim.x) {
     const int64_t off = base + static_cast<int64_t>(v) * VE;
     const Pack<T, VE> s = layer_sum<T, M, VE>(a, off, v);
     float f[VE];
@@ -516,7 +516,7 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
   }
   const float mu = cta_sum(sum, red) * a.inv_n;
   float sq = 0.0f;
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (unsigned v = threadIdx.x; v < nvec; v += blockDim.x) {
     float f[VE];
     unpack(layer_sum<T, M, VE>(a, base + static_cast<int64_t>(v) * VE, v), f);
 #pragma unroll
@@ -527,7 +527,7 @@ layer_walk_kernel(const LayerArgs<T, M> a) {
   }
   __syncthreads();  // red is read by every thread above
   const float r = rsqrtf(fmaf(cta_sum(sq, red), a.inv_n, a.eps));
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (unsigned v = threadIdx.x; v < nvec; v += blockDim.x) {
     const int64_t off = base + static_cast<int64_t>(v) * VE;
     float f[VE], gf[VE];
     unpack(layer_sum<T, M, VE>(a, off, v), f);
@@ -1042,10 +1042,10 @@ layer_grad_rows_kernel(const LayerGradArgs<T, M> a) {
   pdl_trigger();
   __shared__ float2 red[33];
   const int64_t row = blockIdx.x, base = row * a.n;
-  const int nvec = a.n / VE;
+  const unsigned nvec = a.n / VE;  // unsigned: v passes 2^31 past the longest rows
   const float mu = a.mean[row], r = a.inv_std[row];
   float2 acc = make_float2(0.0f, 0.0f);
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (unsigned v = threadIdx.x; v < nvec; v += blockDim.x) {
     const int64_t off = base + static_cast<int64_t>(v) * VE;
     float dy[VE], s[VE], gm[VE];
     unpack(ld_reuse<T, VE>(a.dy + off), dy);
@@ -1063,7 +1063,7 @@ layer_grad_rows_kernel(const LayerGradArgs<T, M> a) {
   if (threadIdx.x == 0) a.coef[row] = make_float2(c1, c2);
   if (!a.dx) return;
   const float k1 = -r * c1, k2 = -r * c2;
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (unsigned v = threadIdx.x; v < nvec; v += blockDim.x) {
     const int64_t off = base + static_cast<int64_t>(v) * VE;
     float g[VE], u[VE], gm[VE], d[VE];
     unpack(ld_reuse<T, VE>(a.dy + off), g);

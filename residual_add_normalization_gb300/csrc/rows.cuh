@@ -377,8 +377,9 @@ rows_walk_kernel(const typename Op::Args a, int nvec) {
   pdl_trigger();
   __shared__ float red[33];
   const int64_t row = blockIdx.x;
+  const unsigned vectors = nvec;  // unsigned: v passes 2^31 past the longest rows
   float acc = 0.0f;
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (unsigned v = threadIdx.x; v < vectors; v += blockDim.x) {
     typename Op::In in;
     typename Op::Hold h;
     typename Op::Wt w;
@@ -387,7 +388,7 @@ rows_walk_kernel(const typename Op::Args a, int nvec) {
     acc += Op::combine(a, row, v, in, w, h);
   }
   const float r = Op::rstd(a, cta_sum(acc, red));
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+  for (unsigned v = threadIdx.x; v < vectors; v += blockDim.x) {
     typename Op::In in;
     typename Op::Hold h;
     typename Op::Wt w;

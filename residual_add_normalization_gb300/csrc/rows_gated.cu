@@ -53,7 +53,7 @@ static int pow2_ceil(int64_t v) {
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-static int round32(int64_t v) { return static_cast<int>(ceil_div(v, 32) * 32); }
+static int64_t round32(int64_t v) { return ceil_div(v, 32) * 32; }
 
 RowPlan plan_rows(int64_t rows, int64_t n, DType t, bool vector_ok, RowOp op) {
   RowPlan p = {};
@@ -85,7 +85,7 @@ RowPlan plan_rows(int64_t rows, int64_t n, DType t, bool vector_ok, RowOp op) {
         (op == RowOp::Gated ||
          (t != DType::F32 && nvec < kSslnPairBelowVec && nvec % 32 != 0)))
       nv = 2;
-    int cta = round32(ceil_div(nvec, nv));
+    int64_t cta = round32(ceil_div(nvec, nv));
     const int target = rows <= kFewRows ? kRowsMaxThreads
                        : (op == RowOp::SkipRms && t != DType::F32 && nvec >= kSslnWideFromVec)
                            ? kRowsMaxThreads
@@ -113,8 +113,8 @@ RowPlan plan_rows(int64_t rows, int64_t n, DType t, bool vector_ok, RowOp op) {
     }
     p.nv = nv;
     p.csize = csize;
-    p.block = cta;
-    p.tpr = cta * csize;
+    p.block = static_cast<int>(cta);
+    p.tpr = p.block * csize;
     p.grid = rows * csize;
   }
   return p;

@@ -85,3 +85,30 @@ def test_layer_grad(row):
     for g, b, d, x in chunks(dgamma, dbeta, dy, row):
         assert torch.equal(b, d)
         check(g, d * (x - 0.25) * 0.5, 0.0)
+
+
+def test_skip_rms(row):
+    skip = digits(3)
+    gamma = torch.full((N,), 1.5, dtype=torch.bfloat16, device="cuda")
+    y, s, _, inv = b2.skip_rms_stats(row, skip, gamma, epsilon=1e-5)
+    squares = 0
+    for got, a, b in chunks(s, row, skip):
+        assert torch.equal(got, a + b)
+        squares += int(((a + b) ** 2).sum())
+    # a thread's sum stays below 2^24 and is exact; ten sums of threads and warps, the
+    # mean, epsilon, and the reciprocal square root (2 half steps) of half of these
+    r = (squares / N + 1e-5) ** -0.5
+    assert abs(inv.item() - r) <= 10 * F.U * r
+    for got, c in chunks(y, s):
+        check(got, c * inv.item() * 1.5, 3 * F.U)
+
+
+def test_gated_rms(row):
+    gate = digits(4)
+    scale = torch.full((N,), 1.5, dtype=torch.bfloat16, device="cuda")
+    y = b2.gated_rms(row, gate, scale, epsilon=1e-5)
+    r = (sum(int((c ** 2).sum()) for c, in chunks(row)) / N + 1e-5) ** -0.5
+    for got, c, z in chunks(y, row, gate):
+        # r's 10 half steps; SiLU's exponential (2 |z| + 4), sum, reciprocal (2) and
+        # product; three products more
+        check(got, c * r * 1.5 * z * torch.sigmoid(z), 24 * F.U)

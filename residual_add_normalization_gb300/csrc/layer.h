@@ -61,6 +61,14 @@ inline size_t layer_grad_workspace_bytes(int64_t rows, int64_t hidden) {
   return stats + static_cast<size_t>(layer_grad_parts(rows, hidden)) * 3 * layer_part_pitch(hidden) * 4;
 }
 
+// `parts` CTAs (clusters) of which each takes every parts-th of `rows` rows, if
+// rows of one part must be a multiple of `ve` apart: one row each, or a multiple of
+// `ve` of them, never more than there are rows (the workspace has no more parts).
+inline int window_parts(int64_t rows, int64_t parts, int ve) {
+  if (parts >= rows || rows <= ve) return static_cast<int>(rows);
+  return static_cast<int>(parts > ve ? parts - parts % ve : ve);
+}
+
 cudaError_t launch_layer(const LayerCall& c, cudaStream_t stream);
 cudaError_t launch_layer_grad(const LayerGradCall& c, cudaStream_t stream);
 

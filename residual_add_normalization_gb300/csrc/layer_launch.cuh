@@ -120,13 +120,6 @@ int64_t window_vectors(int64_t hidden) {
   return (hidden + 2 * (VE - 1)) / VE;
 }
 
-// `parts` CTAs (clusters) of which each takes every parts-th of `rows` rows, if
-// rows of one part must be a multiple of `ve` apart.
-inline int window_parts(int64_t rows, int64_t parts, int ve) {
-  if (parts >= rows) return static_cast<int>(rows);
-  return static_cast<int>(parts > ve ? parts - parts % ve : ve);
-}
-
 // Rows that are not whole vectors, by windows; *done: whether their length allows it.
 template <typename T, typename M, int VE>
 cudaError_t launch_layer_window(const LayerCall& c, const LayerArgs<T, M>& a, cudaStream_t stream,
@@ -186,7 +179,8 @@ cudaError_t launch_layer_grad_ring(Fn fn, LayerGradArgs<T, M>* a, int block, int
   int resident = 0;
   const cudaError_t e = layer_resident(fn, block, smem, &resident);
   if (e != cudaSuccess) return e;
-  if (a->parts > resident / csize) a->parts = resident / csize;
+  const int fit = resident / csize > 1 ? resident / csize : 1;
+  if (a->parts > fit) a->parts = fit;
   if (apart > 1) a->parts = window_parts(a->rows, a->parts, apart);
   unsigned* status = pipe_status_word();
   if (!status) return cudaErrorSymbolNotFound;

@@ -496,7 +496,7 @@ def _skip_layer(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, 
         _check((_lib or library()).b200norm_skip_layer(
             x.data_ptr(), _at(skip), gamma.data_ptr(), _at(beta), _at(bias), y.data_ptr(), _at(s),
             _at(mean), _at(inv), x.numel() // hidden, hidden, _DTYPES[dt], _DTYPES[gamma.dtype],
-            epsilon, _raw_stream(index, stream)))
+            float(epsilon), _raw_stream(index, stream)))
         return y, (x if skip is None and want_sum else s), mean, inv
 
     context = _on(index, stream, (x, skip, gamma, beta, bias, output, sum_out))
@@ -590,6 +590,7 @@ def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y
     :func:`linear_grad` takes, is ``None`` unless ``want_z`` or ``z`` is given.
     """
     index, dt = _first("x", x)
+    activation = int(activation)
     n_out, n_in = _weight(weight, x, index, dt)
     if _last_axis("x", x) != n_in:
         raise ValueError(f"x's last axis must have weight's in_features ({n_in})")
@@ -626,6 +627,7 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
     that is not wanted is ``None``; one that is given is wanted.
     """
     index, dt = _first("dy", dy)
+    activation = int(activation)
     n_out, n_in = _weight(weight, dy, index, dt)
     if _last_axis("dy", dy) != n_out:
         raise ValueError(f"dy's last axis must have weight's out_features ({n_out})")

@@ -426,9 +426,17 @@ def _on(index, stream, tensors):
 # Small scratch blocks kept per thread, device and stream: a thread's work on one
 # stream is in order, so its calls may share one (the launches of two threads'
 # calls on a stream may interleave).  A block that is outgrown goes back to the
-# caching allocator, in that stream's order.
+# caching allocator, in that stream's order.  Streams that torch did not make get
+# blocks of the caching allocator's call by call: such a stream may be destroyed, and
+# its handle come back for another while its work still runs.
 _SCRATCH_KEPT = 32 << 20
 _scratch_of_thread = threading.local()
+
+
+def _from_torch(index, stream):
+    """Whether the current stream, of that handle, is one of torch's own, which live as
+    long as the process: the others' ids are their handles."""
+    return stream == 0 or torch._C._cuda_getCurrentStream(index)[0] != stream
 
 
 def _scratch(workspace, nbytes, x, index, stream):
@@ -441,7 +449,8 @@ def _scratch(workspace, nbytes, x, index, stream):
         return workspace, workspace.numel() * workspace.element_size()
     if not nbytes:
         return None, 0
-    if nbytes > _SCRATCH_KEPT or torch.cuda.is_current_stream_capturing():
+    if (nbytes > _SCRATCH_KEPT or not _from_torch(index, stream)
+            or torch.cuda.is_current_stream_capturing()):
         return torch.empty(nbytes, dtype=torch.uint8, device=x.device), nbytes
     blocks = getattr(_scratch_of_thread, "blocks", None)
     if blocks is None:

@@ -112,3 +112,25 @@ def test_dropped_outputs_and_workspace_are_not_reused_at_once(entry):
     assert not side.query()  # the call is still ahead
     assert not used & {t.data_ptr() for t in again}
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+def test_no_scratch_is_kept_for_a_stream_made_elsewhere(given):
+    """Its handle may come back for another stream; torch's own streams keep theirs."""
+    x, w = torch.randn(300, 1024, device="cuda"), torch.ones(1024, device="cuda")
+    y, s, mean, inv = b2.skip_layer_stats(x, None, w)
+    want = b2.skip_layer_grad(y, s, mean, inv, w)
+    made = torch.cuda.Stream()
+    key = (x.get_device(), made.cuda_stream)
+    for stream in (torch.cuda.ExternalStream(made.cuda_stream), made):
+        b2._scratch_of_thread.blocks.pop(key, None)
+        stream.wait_stream(torch.cuda.current_stream())
+        if given:
+            got = b2.skip_layer_grad(y, s, mean, inv, w, stream=stream)
+        else:
+            with torch.cuda.stream(stream):
+                got = b2.skip_layer_grad(y, s, mean, inv, w)
+        stream.synchronize()
+        assert all(torch.equal(g, v) for g, v in zip(got[:3], want[:3]))
+        assert (key in b2._scratch_of_thread.blocks) == (stream is made)

@@ -98,6 +98,14 @@ B200NORM_API b200norm_status b200norm_testing_set_pdl(int on);
  * unwritten (the gradient's: undefined).  on = 0 restores normal launches (limit_ns ignored). */
 B200NORM_API b200norm_status b200norm_testing_pipe_stall(int on, uint64_t limit_ns);
 
+/* Leave out the messages by which the CTAs of a long row send one another their
+ * sums of it in the streamed gradient of layer normalization (process-wide, later
+ * launches): with on = 1 the waits for them give up after limit_ns (in (0, 100 ms])
+ * and the kernel records B200NORM_ERR_DEVICE_TIMEOUT (read with
+ * b200norm_rows_status); outputs are then undefined.  on = 0 restores normal
+ * launches (limit_ns ignored). */
+B200NORM_API b200norm_status b200norm_testing_layer_withhold(int on, uint64_t limit_ns);
+
 /* Schedule the automatic planner picks, without launching anything.
  * Rows (SSLN / GatedRMSNorm): out = {mode, ve, tpr, nv, rpg, block, csize, grid}.
  * SkipGroupNorm: out = {route, ve, nv, block, csize, grid, ctas_per_item,

@@ -109,6 +109,7 @@ def library() -> ctypes.CDLL:
             "b200norm_testing_set_pdl": ([i32], i32),
             "b200norm_testing_force_linear": ([i32] * 4, i32),
             "b200norm_testing_linear_stall": ([i32, ctypes.c_uint64], i32),
+            "b200norm_testing_layer_withhold": ([i32, ctypes.c_uint64], i32),
             "b200norm_testing_linear_withhold": ([i32, ctypes.c_uint64], i32),
             "b200norm_testing_pipe_stall": ([i32, ctypes.c_uint64], i32),
             "b200norm_testing_plan_rows": ([i64, i64, i32, i32, ctypes.POINTER(ctypes.c_int64)],

@@ -679,6 +679,14 @@ b200norm_status b200norm_testing_linear_stall(int on, uint64_t limit_ns) {
   return ok();
 }
 
+b200norm_status b200norm_testing_layer_withhold(int on, uint64_t limit_ns) {
+  if (on != 0 && on != 1) return fail(B200NORM_ERR_INVALID_ARGUMENT, "on must be 0 or 1");
+  if (on && (limit_ns == 0 || limit_ns > 100000000ull))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "limit_ns must be in (0, 100 ms]");
+  set_layer_withhold(on ? limit_ns : 0);
+  return ok();
+}
+
 b200norm_status b200norm_testing_linear_withhold(int site, uint64_t limit_ns) {
   if (site && (limit_ns == 0 || limit_ns > 100000000ull))
     return fail(B200NORM_ERR_INVALID_ARGUMENT, "limit_ns must be in (0, 100 ms]");

@@ -69,6 +69,11 @@ inline int window_parts(int64_t rows, int64_t parts, int ve) {
   return static_cast<int>(parts > ve ? parts - parts % ve : ve);
 }
 
+// A test's limit for the waits of launches whose CTAs do not send one another their
+// sums of a long row (0: normal ones).
+unsigned long long layer_withhold_limit_ns();
+void set_layer_withhold(unsigned long long limit_ns);
+
 cudaError_t launch_layer(const LayerCall& c, cudaStream_t stream);
 cudaError_t launch_layer_grad(const LayerGradCall& c, cudaStream_t stream);
 

@@ -1,4 +1,6 @@
 // Layer normalization, float32 rows; and the switch over the (T, M) pairs.
+#include <atomic>
+
 #include "layer_launch.cuh"
 
 namespace b200norm {
@@ -19,6 +21,11 @@ extern template cudaError_t launch_layer_grad_tm<__nv_bfloat16, __nv_bfloat16>(
     const LayerGradCall&, cudaStream_t);
 extern template cudaError_t launch_layer_grad_tm<__nv_bfloat16, float>(const LayerGradCall&,
                                                                        cudaStream_t);
+
+static std::atomic<unsigned long long> g_layer_withhold{0};
+
+unsigned long long layer_withhold_limit_ns() { return g_layer_withhold.load(); }
+void set_layer_withhold(unsigned long long limit_ns) { g_layer_withhold.store(limit_ns); }
 
 cudaError_t launch_layer(const LayerCall& c, cudaStream_t stream) {
   const bool m32 = c.m == DType::F32;

@@ -184,10 +184,17 @@ cudaError_t launch_layer_grad_ring(Fn fn, LayerGradArgs<T, M>* a, int block, int
   if (apart > 1) a->parts = window_parts(a->rows, a->parts, apart);
   unsigned* status = pipe_status_word();
   if (!status) return cudaErrorSymbolNotFound;
-  const bool stall = pipe_stalled();
+  int stall = 0;
+  unsigned long long limit_ns = kLayerLimitNs;
+  if (pipe_stalled()) {
+    stall = kLayerNoCopies;
+    limit_ns = pipe_stall_limit_ns();
+  } else if (const unsigned long long ns = layer_withhold_limit_ns()) {
+    stall = kLayerNoSums;
+    limit_ns = ns;
+  }
   return launch_clusters(fn, dim3(static_cast<unsigned>(a->parts * csize)), block, csize, smem,
-                         stream, *a, tpr, nvec, slice, stages, status,
-                         stall ? pipe_stall_limit_ns() : kLayerLimitNs, stall ? 1 : 0);
+                         stream, *a, tpr, nvec, slice, stages, status, limit_ns, stall);
 }
 
 // The one-pass gradient, NV vectors per thread of `block` threads of `csize` CTAs.

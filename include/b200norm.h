@@ -43,7 +43,8 @@
  *     B200NORM_OK and enqueues nothing.
  *   - b200norm_last_error() returns a thread-local, human-readable reason for
  *     the last non-OK status returned on the calling thread.
- *   - Calls are stateless apart from the caller-provided workspaces, and may be issued from several host threads at once.
+ *   - Calls are stateless apart from the caller-provided workspaces, and may
+ *     be issued from several host threads at once.
  *   - Kernels are launched with programmatic dependent launch allowed: one
  *     may be scheduled while the previous kernel on the stream drains, but it
  *     waits for that kernel to complete (and its writes to be visible) before
@@ -362,9 +363,9 @@ B200NORM_API b200norm_status b200norm_skip_layer_grad(
  *              aligned (NULL where that is 0); its contents before the call do
  *              not matter.  Calls that share one must not overlap on the device.
  *
- * Sums are binary32, in a fixed order.  rows == 0 is a no-op; rows may
- * be 2^30 at most, in_features and out_features must be in [1, 2^20].  The first call on a device looks up a
- * device address: make it before any stream capture begins.
+ * Sums are binary32, in a fixed order.  rows == 0 is a no-op; rows may be 2^30
+ * at most, in_features and out_features must be in [1, 2^20].  The first call on
+ * a device looks up a device address: make it before any stream capture begins.
  */
 B200NORM_API size_t b200norm_linear_workspace_size(int64_t rows, int64_t in_features,
                                                    int64_t out_features, b200norm_dtype T,
@@ -406,8 +407,8 @@ B200NORM_API b200norm_status b200norm_linear_grad(
  * operator's kernels on the current device.  With 16-bit types their roles wait
  * on one another through shared memory; the waits are bounded (a second and
  * more for long sums), and one that gives up records
- * B200NORM_ERR_DEVICE_TIMEOUT in a per-device word and ends early (that call's
- * outputs are then undefined).  Returns B200NORM_OK, or
+ * B200NORM_ERR_DEVICE_TIMEOUT in a per-device word, with the kind of the first
+ * such wait, and ends early (that call's outputs are then undefined).  Returns B200NORM_OK, or
  * B200NORM_ERR_DEVICE_TIMEOUT (and clears the record) if any such launch on the
  * device gave up since the last call; B200NORM_ERR_CUDA if the read failed.  No
  * correct launch records anything. */

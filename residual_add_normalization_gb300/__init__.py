@@ -519,7 +519,8 @@ def _skip_layer(x, skip, gamma, beta, bias, epsilon, want_sum, output, sum_out, 
 def skip_layer(input, skip, gamma, beta=None, bias=None, *, epsilon=1e-5, want_sum=True,
                output=None, sum_out=None, stream=None):
     """Layer normalization of ``S = (input + skip) + bias`` over the last axis,
-    times ``gamma`` plus ``beta`` (both of ``input``'s type or both float32).
+    times ``gamma`` plus ``beta`` (both of ``input``'s type or both float32).  No
+    autograd graph is made, whatever requires gradients (as of every entry here).
 
     ``skip=None`` normalizes ``input`` itself.  Returns ``(output, S)``; ``S`` is
     ``None`` unless ``want_sum`` (default True) or ``sum_out`` is given, and is
@@ -594,7 +595,7 @@ def linear(x, weight, bias=None, residual=None, *, activation=0, want_z=False, y
            workspace=None, stream=None):
     """``act(x @ weight.T + bias) + residual`` over the last axis of ``x``;
     ``weight`` is (out_features, in_features), ``activation`` a code of
-    ``ACTIVATIONS``.
+    ``ACTIVATIONS``.  No autograd graph is made.
 
     Returns ``(y, z)``; ``z``, the value before the activation that
     :func:`linear_grad` takes, is ``None`` unless ``want_z`` or ``z`` is given.

@@ -760,10 +760,14 @@ __device__ __forceinline__ void send_to_peer(float2* local, unsigned rank, float
 // cluster send their sums of a row to one another (4096 x 16384 bfloat16: 120 us,
 // 173 with a cluster barrier and remote loads); two sets of slots are enough, for
 // a CTA sends its sums of the next row only once it has all of this one.
-// A stage is free
-// again once the CTA has met at the next tile's barrier.  The waits for a copy
-// are bounded; a thread whose wait gave up records it and runs on without
-// waiting (its outputs are then undefined), so that every barrier is met.
+//
+// A stage is free again once the CTA has met at the next tile's barrier.  The waits
+// for a copy and for the other CTAs' sums are bounded; a thread whose wait gave up
+// records it and runs on without waiting (its outputs are then undefined), so that
+// every barrier is met.
+//
+// With WINDOW rows are taken by windows: a part's rows are then a multiple of VE
+// apart.
 constexpr int kLayerStages = 4;  // at most; 2 where that lets an SM hold two CTAs
 constexpr unsigned long long kLayerLimitNs = 1000000000ull;
 // what a test leaves out, so that the waits for it give up
@@ -774,9 +778,6 @@ __host__ __device__ constexpr int layer_slot_bytes(int vectors) {
   return VE > 1 ? vectors * 16 : (vectors * static_cast<int>(sizeof(T)) + 15) / 16 * 16 + 16;
 }
 
-//
-// With WINDOW rows are taken by windows: a part's rows are then a multiple of VE
-// apart.
 template <typename T, typename M, int VE, int NV, bool BIAS, bool LANE, bool WINDOW = false>
 __global__ void __launch_bounds__(LANE ? kLayerGradLaneThreads : kLayerThreads, 1)
 layer_grad_ring_kernel(const LayerGradArgs<T, M> a, int tpr, int nvec, int slice, int stages,

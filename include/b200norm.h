@@ -14,10 +14,13 @@
  *                        and its gradients
  *   b200norm_linear, b200norm_linear_grad
  *                        y = act(x W^T + b) + residual, and its gradients
+ *   b200norm_rotary, b200norm_head_rms_rotary, b200norm_head_rms_rotary_grad
+ *                        position rotation of query and key heads, with or
+ *                        without an RMS norm of each head, and its gradients
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer to a dense, contiguous,
- *     row-major tensor owned by the caller.  The library never allocates,
+ *     row-major tensor owned by the caller (heads have strides of their own).  The library never allocates,
  *     frees or synchronises; it only enqueues kernels on `stream`.
  *   - Pointers need only be aligned to their element size.  16-byte aligned
  *     pointers (with spans that are whole 16-byte vectors) take the vector
@@ -413,6 +416,124 @@ B200NORM_API b200norm_status b200norm_linear_grad(
  * device gave up since the last call; B200NORM_ERR_CUDA if the read failed.  No
  * correct launch records anything. */
 B200NORM_API b200norm_status b200norm_linear_status(b200norm_stream_t stream);
+
+/*
+ * Query and key heads on the way to attention.
+ *
+ * Rotation: the pair (a, b) of a head with frequency f, of a token at position p,
+ * becomes (a c - b s, b c + a s) with c = scale * cos(p f), s = scale * sin(p f);
+ * the inverse has -s, and is the rotation's gradient.  With R = rotary_size, pair i
+ * (i < R / 2) is elements (i, i + R / 2) of the head, or (2 i, 2 i + 1) when
+ * interleaved; elements from R on stay as they are.  Angles are exact to about
+ * 2^-25 of a radian, and 2^-53 of p f, at any position.
+ *
+ * RMS norm of a head, before its rotation: u = x / sqrt(mean(x^2) + epsilon) * gamma.
+ */
+typedef struct b200norm_rotation {
+  const void* positions;   /* int32 or int64: of token t of sequence b at
+                              [b * batch_stride + t * token_stride]; any sign */
+  int position_bytes;      /* 4 or 8 */
+  int64_t batch_stride, token_stride; /* >= 0, in elements */
+  const double* inv_freq;  /* device, rotary_size / 2 frequencies in radians per position
+                              (b200norm_rotary_frequencies makes them) */
+  int64_t rotary_size;     /* R: even, in [0, head_size]; 0: no rotation, and positions
+                              and inv_freq are not read */
+  int interleaved;         /* 0: pairs (i, i + R / 2); 1: pairs (2 i, 2 i + 1) */
+  float scale;             /* 1, or what a scaled context wants; finite */
+} b200norm_rotation;
+
+/* Queries, or keys: element d of head h of token t of sequence b of a tensor is at
+ * [b * strides[0] + t * strides[1] + h * strides[2] + d], strides >= 0 in elements.  So
+ * heads may lie inside a product's rows, next to others, or be permuted. */
+typedef struct b200norm_heads {
+  const void* x;
+  void* y;                 /* the result: x itself with x's strides (in place), or no
+                              element of any input */
+  const void* gamma;       /* M, (head_size), or NULL (ones); NULL for b200norm_rotary */
+  int64_t heads;           /* 0: none (the pointers are not used) */
+  int64_t x_strides[3], y_strides[3];
+} b200norm_heads;
+
+/*
+ * y = round_T(rotation(x)), or round_T(rotation(u)), of queries and of keys, in one
+ * launch.  Either tensor may be NULL.
+ *
+ *   batch, seq   tokens are (batch, seq); their product may be 2^31 - 1 at most.
+ *   head_size    elements of a head, in [1, 1024]; heads: at most 2^16.
+ *   T, M         element types of heads and gamma; M is T or B200NORM_F32.
+ *   epsilon      >= 0 and not NaN.
+ *
+ * The outputs may interleave (heads next to one another in one row), but no element
+ * may be written twice.  batch * seq == 0 is a no-op.
+ */
+B200NORM_API b200norm_status b200norm_rotary(const b200norm_heads* queries,
+                                             const b200norm_heads* keys,
+                                             const b200norm_rotation* rotation, int64_t batch,
+                                             int64_t seq, int64_t head_size, b200norm_dtype T,
+                                             int inverse, b200norm_stream_t stream);
+
+B200NORM_API b200norm_status b200norm_head_rms_rotary(
+    const b200norm_heads* queries, const b200norm_heads* keys, const b200norm_rotation* rotation,
+    int64_t batch, int64_t seq, int64_t head_size, b200norm_dtype T, b200norm_dtype M,
+    float epsilon, b200norm_stream_t stream);
+
+/* The same of the gradient. */
+typedef struct b200norm_heads_grad {
+  const void* dy;          /* T: gradient of y */
+  const void* x;           /* T: the forward call's input */
+  const void* gamma;       /* M, or NULL (ones) */
+  void* dx;                /* T, or NULL when not wanted */
+  void* dgamma;            /* M, (head_size), or NULL when not wanted */
+  int64_t heads;           /* 0: none (the pointers are not used) */
+  int64_t dy_strides[3], x_strides[3], dx_strides[3];
+} b200norm_heads_grad;
+
+/*
+ * Gradients of b200norm_head_rms_rotary.  With da the inverse rotation of dy, r =
+ * 1 / sqrt(mean(x^2) + epsilon), v = x r and g = da * gamma, over each head:
+ *
+ *   dx     = round_T(r * (g - v * mean(g * v)))
+ *   dgamma = round_M(sum over tokens and heads of da * v)
+ *
+ *   workspace  at least b200norm_head_rms_rotary_grad_workspace_size() bytes, 256-byte
+ *              aligned; its contents before the call do not matter.  Calls that share
+ *              one must not overlap on the device.
+ *
+ * Outputs overlap nothing (dx of queries and of keys may interleave).  Sums are
+ * binary32, in a fixed order (equal calls give equal bits).  batch * seq == 0 stores
+ * zeros in dgamma.
+ */
+B200NORM_API size_t b200norm_head_rms_rotary_grad_workspace_size(int64_t batch, int64_t seq,
+                                                                 int64_t query_heads,
+                                                                 int64_t key_heads,
+                                                                 int64_t head_size);
+
+B200NORM_API b200norm_status b200norm_head_rms_rotary_grad(
+    const b200norm_heads_grad* queries, const b200norm_heads_grad* keys,
+    const b200norm_rotation* rotation, int64_t batch, int64_t seq, int64_t head_size,
+    b200norm_dtype T, b200norm_dtype M, float epsilon, void* workspace, size_t workspace_bytes,
+    b200norm_stream_t stream);
+
+/*
+ * Frequencies of rotary positions: f_i = base^(-2 i / rotary_size), i < rotary_size / 2,
+ * scaled for a context longer than the one the model was trained on:
+ *
+ *   scaling 0  as they are (factor, original_length, low and high are not used)
+ *           1  positions interpolated: f_i / factor
+ *           2  another base: base * factor^(R / (R - 2)), which divides the lowest
+ *              frequency by factor and keeps the highest (R > 2)
+ *           3  by the turns t_i = original_length * f_i / (2 pi) that a pair makes over
+ *              the original length: kept for t_i >= high, divided by factor for
+ *              t_i <= low, and a mixture in proportion between them
+ *
+ * inv_freq is a HOST array of rotary_size / 2.  rotary_size is even, in [2, 1024];
+ * base > 0; factor > 0; original_length > 0; 0 <= low < high; all finite.  Touches no
+ * GPU.  (Scaled contexts often want a `scale` of 0.1 ln(factor) + 1 in the rotation.)
+ */
+B200NORM_API b200norm_status b200norm_rotary_frequencies(double* inv_freq, int64_t rotary_size,
+                                                         double base, int scaling, double factor,
+                                                         double original_length, double low,
+                                                         double high);
 
 #ifdef __cplusplus
 }

@@ -23,18 +23,27 @@ training (gradients are calls of their own, not autograd functions):
   skip_layer_grad   its gradients
   linear            act(x W^T + b) + residual
   linear_grad       its gradients
+
+and on query and key heads, on their way to attention:
+
+  rotary                position rotation, or its inverse (its gradient)
+  head_rms_rotary       an RMS norm of each head, then the rotation
+  head_rms_rotary_grad  its gradients
+  rotary_frequencies    the frequencies of a rotation, scaled for long contexts
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
 
 __all__ = ["skip_rms", "skip_rms_stats", "gated_rms", "skip_group", "skip_layer",
            "skip_layer_stats", "skip_layer_grad", "linear", "linear_grad", "linear_status",
-           "ACTIVATIONS",
+           "ACTIVATIONS", "rotary", "head_rms_rotary", "head_rms_rotary_grad",
+           "rotary_frequencies", "ROTARY_SCALINGS",
            "workspace_size",
            "workspace_init", "workspace_status", "noalloc_status", "rows_status", "library",
            "library_path", "B200NormError", "SSLN_EPS_DEFAULT"]
@@ -102,6 +111,13 @@ def library() -> ctypes.CDLL:
             "b200norm_linear_status": ([vp], i32),
             "b200norm_linear_grad_workspace_size": ([i64, i64, i64, i32, i32, i32], sz),
             "b200norm_linear_grad": ([vp] * 7 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
+            "b200norm_rotary": ([vp] * 3 + [i64] * 3 + [i32, i32, vp], i32),
+            "b200norm_head_rms_rotary": ([vp] * 3 + [i64] * 3 + [i32, i32, f32, vp], i32),
+            "b200norm_head_rms_rotary_grad_workspace_size": ([i64] * 5, sz),
+            "b200norm_head_rms_rotary_grad": ([vp] * 3 + [i64] * 3 + [i32, i32, f32, vp, sz, vp],
+                                              i32),
+            "b200norm_rotary_frequencies": ([ctypes.POINTER(ctypes.c_double), i64,
+                                             ctypes.c_double, i32] + [ctypes.c_double] * 4, i32),
             "b200norm_testing_barrier_timeout": ([vp, sz, ctypes.c_uint64, vp], i32),
             "b200norm_testing_noalloc_barrier_timeout": ([ctypes.c_uint64, vp], i32),
             "b200norm_testing_force": ([i32, i32], i32),
@@ -681,3 +697,256 @@ def linear_status(stream=None, device=None):
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(dev):
         _check(library().b200norm_linear_status(_stream(dev, stream)))
+
+
+# ---------------------------------------------------------------------------
+# Query and key heads
+# ---------------------------------------------------------------------------
+
+# Codes of rotary_frequencies.
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "turns": 3}
+
+# The C structs b200norm_rotation, b200norm_heads and b200norm_heads_grad.
+_ROTATION = struct.Struct("@PiqqPqif")
+_HEADS = struct.Struct("@PPPq6q")
+_HEADS_GRAD = struct.Struct("@PPPPPq9q")
+_NO_STRIDES = (0, 0, 0)
+
+
+def rotary_frequencies(rotary_size, base=10000.0, *, scaling=0, factor=1.0, original_length=0.0,
+                       low=1.0, high=32.0, device="cuda"):
+    """Frequencies ``base ** (-2 i / rotary_size)`` of a rotation's pairs, in
+    radians per position: float64 on ``device``, as :func:`rotary` takes them.
+
+    ``scaling``, a code of ``ROTARY_SCALINGS``, is for contexts ``factor`` times
+    longer than the ``original_length`` a model was trained on: "linear" divides
+    all by ``factor``; "base" raises the base so that the lowest is divided by it
+    and the highest kept; "turns" keeps those that turn ``high`` times or more over
+    the original length, divides those that turn ``low`` times or less, and mixes
+    the others in proportion.  (A ``scale`` of ``0.1 * log(factor) + 1`` in the
+    rotation goes with it where a model wants that.)
+    """
+    n = int(rotary_size)
+    out = (ctypes.c_double * max(1, n // 2))()
+    _check((_lib or library()).b200norm_rotary_frequencies(
+        out, n, float(base), int(scaling), float(factor), float(original_length), float(low),
+        float(high)))
+    return torch.tensor(list(out), dtype=torch.float64).to(device)
+
+
+def _heads(name, t, x, index, dtype):
+    """``t``, heads of x's leading shape and head size, with any steps between heads."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index):
+        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.dtype in _DTYPES:
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+        _cuda(name, t)
+    shape = t.shape
+    if len(shape) not in (3, 4) or shape[:-2] != x.shape[:-2] or shape[-1] != x.shape[-1]:
+        raise ValueError(f"{name} must have shape (..., heads, head_size) with one or two leading "
+                         f"axes, the same for all (got {tuple(shape)})")
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}'s elements must be next to one another in a head")
+    return t
+
+
+def _head_steps(t):
+    s = t.stride()
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
+
+
+def _positions(positions, inv_freq, x, index, interleaved, scale):
+    """The C rotation."""
+    if inv_freq is None:
+        if positions is not None:
+            raise ValueError("positions need inv_freq")
+        return _ROTATION.pack(0, 8, 0, 0, 0, 0, 1 if interleaved else 0, scale)
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float64):
+        raise TypeError("inv_freq must be a float64 torch.Tensor")
+    if inv_freq.get_device() != index or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be contiguous, of one axis, on {x.device}")
+    if not (isinstance(positions, torch.Tensor) and positions.dtype in (torch.int64, torch.int32)):
+        raise TypeError("positions must be an int64 or int32 torch.Tensor")
+    if positions.get_device() != index:
+        raise ValueError(f"positions is on {positions.device}, expected {x.device}")
+    lead = x.shape[:-2]
+    if positions.shape == lead:
+        steps = positions.stride() if len(lead) == 2 else (0, positions.stride(0))
+    elif len(lead) == 2 and positions.shape == lead[1:]:
+        steps = (0, positions.stride(0))
+    else:
+        raise ValueError(f"positions must have shape {tuple(lead)}"
+                         + (f" or {tuple(lead[1:])}" if len(lead) == 2 else "")
+                         + f" (got {tuple(positions.shape)})")
+    return _ROTATION.pack(positions.data_ptr(), positions.element_size(), *steps,
+                          inv_freq.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0,
+                          scale)
+
+
+def _first_heads(tensors):
+    """(the first tensor of heads that is given, index of its device, type)."""
+    for name, t in tensors:
+        if t is not None:
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPES):
+                _cuda(name, t)
+            if t.dim() not in (3, 4) or t.shape[-1] < 1:
+                raise ValueError(f"{name} must have shape (..., heads, head_size) with one or two "
+                                 f"leading axes (got {tuple(t.shape)})")
+            return t, t.get_device(), t.dtype
+    raise ValueError("queries or keys are needed")
+
+
+def _gammas(q, gamma_q, k, gamma_k, x, index):
+    """The type of both gammas (x's without any)."""
+    m = None
+    for name, heads, gamma in (("gamma_q", q, gamma_q), ("gamma_k", k, gamma_k)):
+        if gamma is None:
+            continue
+        if heads is None:
+            raise ValueError(f"{name} needs its heads")
+        _weights(name, gamma, x.shape[-1], x, index)
+        if m is not None and gamma.dtype is not m:
+            raise TypeError("gamma_q and gamma_k must be of one type")
+        m = gamma.dtype
+    return m or x.dtype
+
+
+def _rotated(norm, q, k, gamma_q, gamma_k, positions, inv_freq, epsilon, interleaved, inverse,
+             scale, q_out, k_out, stream):
+    x, index, dt = _first_heads((("q", q), ("k", k)))
+    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is not None:
+            _heads(name, t, x, index, dt)
+        if o is not None:
+            if t is None:
+                raise ValueError(f"{name}_out needs {name}")
+            if _heads(name + "_out", o, x, index, dt).shape != t.shape:
+                raise ValueError(f"{name}_out must have shape {tuple(t.shape)} "
+                                 f"(got {tuple(o.shape)})")
+    m = _gammas(q, gamma_q, k, gamma_k, x, index) if norm else dt
+    rotation = _positions(positions, inv_freq, x, index, interleaved, scale)
+    batch, seq = x.shape[:2] if x.dim() == 4 else (1, x.shape[0])
+
+    def run():
+        outs = [None, None]
+        args = [None, None]
+        for i, (t, gamma, o) in enumerate(((q, gamma_q, q_out), (k, gamma_k, k_out))):
+            if t is None:
+                continue
+            outs[i] = torch.empty(t.shape, dtype=dt, device=t.device) if o is None else o
+            args[i] = _HEADS.pack(t.data_ptr(), outs[i].data_ptr(), _at(gamma) or 0, t.shape[-2],
+                                  *_head_steps(t), *_head_steps(outs[i]))
+        lib = _lib or library()
+        raw = _raw_stream(index, stream)
+        if norm:
+            _check(lib.b200norm_head_rms_rotary(*args, rotation, batch, seq, x.shape[-1],
+                                                _DTYPES[dt], _DTYPES[m], float(epsilon), raw))
+        else:
+            _check(lib.b200norm_rotary(*args, rotation, batch, seq, x.shape[-1], _DTYPES[dt],
+                                       1 if inverse else 0, raw))
+        return tuple(outs)
+
+    context = _on(index, stream, (q, k, gamma_q, gamma_k, positions, inv_freq, q_out, k_out))
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+def rotary(q, k, positions, inv_freq, *, interleaved=False, scale=1.0, inverse=False, q_out=None,
+           k_out=None, stream=None):
+    """Rotate the heads of ``q`` and ``k`` by their tokens' positions, or back
+    (``inverse``: the gradient of the rotation).  Returns ``(q, k)``, rotated.
+
+    ``q`` and ``k`` are (tokens, heads, head_size) or (batch, seq, heads,
+    head_size), of one type; either may be ``None``.  Only a head's elements need
+    be next to one another: views of a product's rows, or of permuted tensors, are
+    taken as they are.  ``positions``, int64 or int32 of any sign, has the tokens'
+    shape, or (seq,).  ``inv_freq`` holds a frequency (radians per position,
+    float64) for each pair: elements (i, i + n) of the first 2 n = 2
+    ``inv_freq.numel()``, or (2 i, 2 i + 1) when ``interleaved``; the others stay
+    as they are.  ``scale`` multiplies the rotated elements.  ``q_out`` may be
+    ``q`` itself, and ``k_out`` ``k``.
+    """
+    return _rotated(False, q, k, None, None, positions, inv_freq, 0.0, interleaved, inverse, scale,
+                    q_out, k_out, stream)
+
+
+def head_rms_rotary(q, k, gamma_q, gamma_k, positions, inv_freq, *, epsilon=1e-6,
+                    interleaved=False, scale=1.0, q_out=None, k_out=None, stream=None):
+    """RMS-normalize each head of ``q`` and ``k``, ``x / sqrt(mean(x^2) + epsilon) *
+    gamma``, then rotate it as :func:`rotary` does.  Returns ``(q, k)``.
+
+    ``gamma_q`` and ``gamma_k`` have head_size elements of the heads' type or
+    float32; ``None`` is ones.  ``positions=None, inv_freq=None`` leaves out the
+    rotation.
+    """
+    return _rotated(True, q, k, gamma_q, gamma_k, positions, inv_freq, epsilon, interleaved, False,
+                    scale, q_out, k_out, stream)
+
+
+def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *, epsilon=1e-6,
+                         interleaved=False, scale=1.0, want_input=True, want_gamma=True,
+                         dq_out=None, dk_out=None, dgamma_q=None, dgamma_k=None, workspace=None,
+                         stream=None):
+    """Gradients of :func:`head_rms_rotary`: ``(dq, dk, dgamma_q, dgamma_k)``.
+
+    ``dq`` and ``dk`` are the gradients of its results, ``q`` and ``k`` its inputs.
+    ``dq_out`` and ``dk_out`` receive those of the inputs (views of one tensor of
+    rows, for the gradient of the product they came from).  An output that is not
+    wanted is ``None``; one that is given is wanted; a gamma of ``None`` has no
+    gradient.
+    """
+    x, index, dt = _first_heads((("q", q), ("k", k)))
+    sets = []
+    for name, t, d, gamma, o, dg in (("q", q, dq, gamma_q, dq_out, dgamma_q),
+                                     ("k", k, dk, gamma_k, dk_out, dgamma_k)):
+        if t is None:
+            if not (d is None and o is None and dg is None):
+                raise ValueError(f"d{name}, d{name}_out and dgamma_{name} need {name}")
+            sets.append(None)
+            continue
+        _heads(name, t, x, index, dt)
+        for n, v in (("d" + name, d), (f"d{name}_out", o)):
+            if v is None and n == f"d{name}_out":
+                continue
+            if _heads(n, v, x, index, dt).shape != t.shape:
+                raise ValueError(f"{n} must have shape {tuple(t.shape)} (got {tuple(v.shape)})")
+        if dg is not None and gamma is None:
+            raise ValueError(f"dgamma_{name} needs gamma_{name}")
+        sets.append((name, t, d, gamma, o, dg))
+    m = _gammas(q, gamma_q, k, gamma_k, x, index)
+    rotation = _positions(positions, inv_freq, x, index, interleaved, scale)
+    batch, seq = x.shape[:2] if x.dim() == 4 else (1, x.shape[0])
+
+    def run():
+        lib = _lib or library()
+        dxs, dgs, args, heads = [None, None], [None, None], [None, None], [0, 0]
+        for i, one in enumerate(sets):
+            if one is None:
+                continue
+            name, t, d, gamma, o, dg = one
+            if o is not None or want_input:
+                dxs[i] = torch.empty(t.shape, dtype=dt, device=t.device) if o is None else o
+            if gamma is not None and (dg is not None or want_gamma):
+                dgs[i] = _like("dgamma_" + name, dg, gamma, index)
+            heads[i] = t.shape[-2]
+            args[i] = _HEADS_GRAD.pack(
+                d.data_ptr(), t.data_ptr(), _at(gamma) or 0, _at(dxs[i]) or 0, _at(dgs[i]) or 0,
+                heads[i], *_head_steps(d), *_head_steps(t),
+                *(_NO_STRIDES if dxs[i] is None else _head_steps(dxs[i])))
+        need = lib.b200norm_head_rms_rotary_grad_workspace_size(batch, seq, *heads, x.shape[-1])
+        raw = _raw_stream(index, stream)
+        ws, n = _scratch(workspace, need, x, index, raw)
+        _check(lib.b200norm_head_rms_rotary_grad(*args, rotation, batch, seq, x.shape[-1],
+                                                 _DTYPES[dt], _DTYPES[m], float(epsilon),
+                                                 _at(ws), n, raw))
+        return dxs[0], dxs[1], dgs[0], dgs[1]
+
+    context = _on(index, stream, (dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, dq_out,
+                                  dk_out, dgamma_q, dgamma_k, workspace))
+    if context is None:
+        return run()
+    with context:
+        return run()

@@ -52,6 +52,8 @@ FAMILY_SOURCES = {
                "launch_kernel.cuh", "linear_launch.cuh", "linear.cu", "linear_f32.cu",
                "linear_f16.cu", "linear_bf16.cu", "linear_mma.cuh", "linear_mma_launch.cuh",
                "linear_mma_f16.cu", "linear_mma_bf16.cu"),
+    "heads": ("common.cuh", "launch.h", "launch_kernel.cuh", "heads.h", "heads.cuh",
+              "heads_launch.cuh", "heads.cu", "heads_f32.cu", "heads_f16.cu", "heads_bf16.cu"),
 }
 
 
@@ -74,7 +76,7 @@ def _inputs_digest(family: str | None = None) -> str:
 
 def source_digest(family: str | None = None) -> str:
     """Digest of the kernel sources and headers (identifies a kernel build), or
-    of one kernel family's sources ("rows", "group", "layer", "linear")."""
+    of one kernel family's sources ("rows", "group", "layer", "linear", "heads")."""
     return _inputs_digest(family)[:16]
 
 

@@ -12,6 +12,7 @@
 
 #include "b200norm.h"
 #include "b200norm_testing.h"
+#include "heads.h"
 #include "launch.h"
 #include "layer.h"
 #include "linear.h"
@@ -239,6 +240,222 @@ b200norm_status check_linear_shape(int64_t rows, int64_t in, int64_t out, b200no
     return fail(B200NORM_ERR_INVALID_ARGUMENT,
                 "activation must be 0 (none), 1 (SiLU), 2 (GELU), 3 (GELU, tanh) or 4 (ReLU)");
   return B200NORM_OK;
+}
+
+// ---- query and key heads ----
+
+// A strided tensor of heads, as an argument.
+struct HeadsArg {
+  const void* p;
+  int64_t heads;
+  const int64_t* strides;
+  const char* name;
+};
+
+using Wide = unsigned __int128;
+
+// Elements from the first to one past the last.
+Wide heads_extent(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size) {
+  return static_cast<Wide>(batch - 1) * a.strides[0] + static_cast<Wide>(seq - 1) * a.strides[1] +
+         static_cast<Wide>(a.heads - 1) * a.strides[2] + size;
+}
+
+b200norm_status check_heads(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size, size_t es) {
+  if (!a.p) return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s is required", a.name);
+  if (!aligned(a.p, es))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s is not aligned to its element size", a.name);
+  for (int i = 0; i < 3; ++i)
+    if (a.strides[i] < 0)
+      return fail(B200NORM_ERR_INVALID_ARGUMENT, "strides of %s must be >= 0", a.name);
+  if (heads_extent(a, batch, seq, size) > static_cast<Wide>(INT64_MAX) / 8)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "strides of %s reach past the address space", a.name);
+  return B200NORM_OK;
+}
+
+// Whether no element of an output has two places: each axis steps past all that the
+// axes of smaller steps reach.
+bool heads_distinct(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size) {
+  const int64_t n[3] = {batch, seq, a.heads};
+  bool used[3] = {false, false, false};
+  Wide extent = static_cast<Wide>(size);
+  for (int round = 0; round < 3; ++round) {
+    int least = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!used[i] && n[i] > 1 && (least < 0 || a.strides[i] < a.strides[least])) least = i;
+    if (least < 0) break;
+    used[least] = true;
+    if (static_cast<Wide>(a.strides[least]) < extent) return false;
+    extent += static_cast<Wide>(n[least] - 1) * a.strides[least];
+  }
+  return true;
+}
+
+// Whether two tensors of heads share no element, as far as it can be told: they lie
+// apart, or side by side inside rows of one step (queries and keys of one product).
+bool heads_apart(const HeadsArg& a, const HeadsArg& b, int64_t batch, int64_t seq, int64_t size,
+                 size_t es) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  if (a0 > b0) return heads_apart(b, a, batch, seq, size, es);
+  const uintptr_t gap = (b0 - a0) / es;
+  if (heads_extent(a, batch, seq, size) <= gap) return true;
+  // the step that all rows of both share: of the sequences, or of the tokens as well
+  auto beside = [&](int64_t step, int64_t tokens) {
+    const Wide an = static_cast<Wide>(tokens - 1) * a.strides[1] +
+                    static_cast<Wide>(a.heads - 1) * a.strides[2] + size;
+    const Wide bn = static_cast<Wide>(tokens - 1) * b.strides[1] +
+                    static_cast<Wide>(b.heads - 1) * b.strides[2] + size;
+    if (step <= 0) return false;
+    const Wide at = gap % static_cast<uintptr_t>(step);
+    return an <= at && at + bn <= static_cast<Wide>(step);
+  };
+  if (batch > 1 && a.strides[0] == b.strides[0] && beside(a.strides[0], seq)) return true;
+  const int64_t step = a.strides[1];
+  return seq > 1 && step > 0 && step == b.strides[1] &&
+         (batch == 1 || (a.strides[0] % step == 0 && b.strides[0] % step == 0)) && beside(step, 1);
+}
+
+bool heads_same(const HeadsArg& a, const HeadsArg& b, int64_t batch, int64_t seq) {
+  return a.p == b.p && a.heads == b.heads && (batch == 1 || a.strides[0] == b.strides[0]) &&
+         (seq == 1 || a.strides[1] == b.strides[1]) &&
+         (a.heads == 1 || a.strides[2] == b.strides[2]);
+}
+
+// What the rotation reads and gamma, as ranges of memory.
+Range heads_range(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size, size_t es) {
+  return {a.p, static_cast<size_t>(heads_extent(a, batch, seq, size)) * es, a.name};
+}
+
+b200norm_status check_rotation(const b200norm_rotation* r, int64_t batch, int64_t seq,
+                               int64_t head_size) {
+  if (!r) return fail(B200NORM_ERR_INVALID_ARGUMENT, "rotation is required");
+  if (r->rotary_size < 0 || r->rotary_size > head_size || r->rotary_size % 2)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "rotary_size must be even, in [0, head_size]");
+  if (r->interleaved != 0 && r->interleaved != 1)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "interleaved must be 0 or 1");
+  if (r->rotary_size == 0) return B200NORM_OK;
+  if (!std::isfinite(r->scale))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (r->position_bytes != 4 && r->position_bytes != 8)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "position_bytes must be 4 or 8");
+  if (batch == 0 || seq == 0) return B200NORM_OK;
+  if (!r->positions || !r->inv_freq)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "positions and inv_freq are required");
+  if (!aligned(r->positions, r->position_bytes) || !aligned(r->inv_freq, 8))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "positions or inv_freq is not aligned to its element size");
+  if (r->batch_stride < 0 || r->token_stride < 0 ||
+      static_cast<Wide>(batch - 1) * r->batch_stride +
+              static_cast<Wide>(seq - 1) * r->token_stride >
+          static_cast<Wide>(INT64_MAX) / 16)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "strides of positions out of range");
+  return B200NORM_OK;
+}
+
+b200norm_status check_heads_shape(int64_t batch, int64_t seq, int64_t q, int64_t k, int64_t size,
+                                  b200norm_dtype T, b200norm_dtype M) {
+  if (!dtype_ok(T) || (M != T && M != B200NORM_F32))
+    return fail(B200NORM_ERR_UNSUPPORTED, "element types T=%d M=%d not supported", T, M);
+  if (batch < 0 || seq < 0 || q < 0 || k < 0 || size <= 0)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "need batch >= 0, seq >= 0, heads >= 0, head_size > 0");
+  if (size > kMaxHeadSize || q > kMaxHeads || k > kMaxHeads)
+    return fail(B200NORM_ERR_UNSUPPORTED, "head_size exceeds 1024, or heads 2^16");
+  if (batch > kMaxGrid || seq > kMaxGrid || batch * seq > kMaxGrid)
+    return fail(B200NORM_ERR_UNSUPPORTED, "batch * seq exceeds 2^31-1");
+  return B200NORM_OK;
+}
+
+HeadStrides to_strides(const int64_t* s) { return {s[0], s[1], s[2]}; }
+
+HeadsCall heads_call(const b200norm_rotation* r, int64_t batch, int64_t seq, int64_t size,
+                     b200norm_dtype T, b200norm_dtype M) {
+  HeadsCall c = {};
+  c.positions = r->positions;
+  c.pos64 = r->position_bytes == 8;
+  c.pos_batch = r->batch_stride;
+  c.pos_token = r->token_stride;
+  c.inv_freq = r->inv_freq;
+  c.batch = batch;
+  c.seq = seq;
+  c.size = static_cast<int>(size);
+  c.rot = static_cast<int>(r->rotary_size);
+  c.interleaved = r->interleaved != 0;
+  c.scale = r->scale;
+  c.t = to_dtype(T);
+  c.m = to_dtype(M);
+  return c;
+}
+
+// The rotation's inputs.
+int rotation_ranges(const HeadsCall& c, Range* out) {
+  if (c.rot == 0) return 0;
+  const size_t n = static_cast<size_t>((c.batch - 1) * c.pos_batch + (c.seq - 1) * c.pos_token + 1);
+  out[0] = {c.positions, n * (c.pos64 ? 8 : 4), "positions"};
+  out[1] = {c.inv_freq, static_cast<size_t>(c.rot / 2) * 8, "inv_freq"};
+  return 2;
+}
+
+// The forward call of both entries.
+b200norm_status heads_forward(const b200norm_heads* queries, const b200norm_heads* keys,
+                              const b200norm_rotation* rotation, int64_t batch, int64_t seq,
+                              int64_t head_size, b200norm_dtype T, b200norm_dtype M, bool norm,
+                              int inverse, float epsilon, b200norm_stream_t stream) {
+  const b200norm_heads* given[2] = {queries, keys};
+  if (b200norm_status st = check_heads_shape(batch, seq, queries ? queries->heads : 0,
+                                             keys ? keys->heads : 0, head_size, T, M))
+    return st;
+  if (b200norm_status st = check_rotation(rotation, batch, seq, head_size)) return st;
+  if (inverse != 0 && inverse != 1)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "inverse must be 0 or 1");
+  if (norm)
+    if (b200norm_status st = check_eps(epsilon)) return st;
+  if (batch * seq == 0) return ok();
+  HeadsCall c = heads_call(rotation, batch, seq, head_size, T, M);
+  c.inverse = inverse != 0;
+  c.norm = norm;
+  c.eps = epsilon;
+  const size_t es = dtype_size(c.t), ms = dtype_size(c.m);
+  static const char* names[2][3] = {{"queries x", "queries y", "queries gamma"},
+                                    {"keys x", "keys y", "keys gamma"}};
+  HeadsArg xs[2], ys[2];
+  Range reads[4];
+  int n = 0, nreads = rotation_ranges(c, reads);
+  for (int i = 0; i < 2; ++i) {
+    const b200norm_heads* h = given[i];
+    if (!h || h->heads == 0) continue;
+    xs[n] = {h->x, h->heads, h->x_strides, names[i][0]};
+    ys[n] = {h->y, h->heads, h->y_strides, names[i][1]};
+    for (const HeadsArg* a : {&xs[n], &ys[n]})
+      if (b200norm_status st = check_heads(*a, batch, seq, head_size, es)) return st;
+    if (h->gamma) {
+      if (!norm) return fail(B200NORM_ERR_INVALID_ARGUMENT, "b200norm_rotary takes no gamma");
+      if (!aligned(h->gamma, ms))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s is not aligned to its element size",
+                    names[i][2]);
+      reads[nreads++] = {h->gamma, static_cast<size_t>(head_size) * ms, names[i][2]};
+    }
+    c.set[i] = {h->x, nullptr, h->gamma, h->y, nullptr, h->heads, to_strides(h->x_strides), {},
+                to_strides(h->y_strides)};
+    ++n;
+  }
+  if (n == 0) return ok();
+  for (int i = 0; i < n; ++i) {
+    if (!heads_distinct(ys[i], batch, seq, head_size))
+      return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s overlaps itself", ys[i].name);
+    for (int j = 0; j < n; ++j)
+      if (!(i == j && heads_same(ys[i], xs[j], batch, seq)) &&
+          !heads_apart(ys[i], xs[j], batch, seq, head_size, es))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", ys[i].name, xs[j].name);
+    for (int j = 0; j < nreads; ++j)
+      if (overlaps(heads_range(ys[i], batch, seq, head_size, es), reads[j]))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", ys[i].name,
+                    reads[j].name);
+  }
+  if (n == 2 && !heads_apart(ys[0], ys[1], batch, seq, head_size, es))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "outputs overlap");
+  cudaError_t e = launch_heads(c, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, norm ? "head_rms_rotary launch" : "rotary launch");
+  return ok();
 }
 
 // Skip shape classification (SkipGroupNorm README, Inputs, skip):
@@ -655,6 +872,159 @@ b200norm_status b200norm_linear_status(b200norm_stream_t stream) {
   if (e == cudaSuccess && v[0] != 0) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "linear status read");
   if (v[0] != 0) return fail(static_cast<b200norm_status>(v[0]), "device wait %u gave up", v[1]);
+  return ok();
+}
+
+// ---- query and key heads -----------------------------------------------------
+
+b200norm_status b200norm_rotary(const b200norm_heads* queries, const b200norm_heads* keys,
+                                const b200norm_rotation* rotation, int64_t batch, int64_t seq,
+                                int64_t head_size, b200norm_dtype T, int inverse,
+                                b200norm_stream_t stream) {
+  return heads_forward(queries, keys, rotation, batch, seq, head_size, T, T, false, inverse, 0.0f,
+                       stream);
+}
+
+b200norm_status b200norm_head_rms_rotary(const b200norm_heads* queries, const b200norm_heads* keys,
+                                         const b200norm_rotation* rotation, int64_t batch,
+                                         int64_t seq, int64_t head_size, b200norm_dtype T,
+                                         b200norm_dtype M, float epsilon,
+                                         b200norm_stream_t stream) {
+  return heads_forward(queries, keys, rotation, batch, seq, head_size, T, M, true, 0, epsilon,
+                       stream);
+}
+
+size_t b200norm_head_rms_rotary_grad_workspace_size(int64_t batch, int64_t seq,
+                                                    int64_t query_heads, int64_t key_heads,
+                                                    int64_t head_size) {
+  if (check_heads_shape(batch, seq, query_heads, key_heads, head_size, B200NORM_F32, B200NORM_F32))
+    return 0;
+  if (batch * seq == 0 || query_heads + key_heads == 0) return 0;
+  return head_parts_bytes(head_parts(batch * seq, query_heads, key_heads), head_size);
+}
+
+b200norm_status b200norm_head_rms_rotary_grad(
+    const b200norm_heads_grad* queries, const b200norm_heads_grad* keys,
+    const b200norm_rotation* rotation, int64_t batch, int64_t seq, int64_t head_size,
+    b200norm_dtype T, b200norm_dtype M, float epsilon, void* workspace, size_t workspace_bytes,
+    b200norm_stream_t stream) {
+  const b200norm_heads_grad* given[2] = {queries, keys};
+  if (b200norm_status st = check_heads_shape(batch, seq, queries ? queries->heads : 0,
+                                             keys ? keys->heads : 0, head_size, T, M))
+    return st;
+  if (b200norm_status st = check_rotation(rotation, batch, seq, head_size)) return st;
+  if (b200norm_status st = check_eps(epsilon)) return st;
+  HeadsCall c = heads_call(rotation, batch, seq, head_size, T, M);
+  c.inverse = true;
+  c.norm = true;
+  c.eps = epsilon;
+  const size_t es = dtype_size(c.t), ms = dtype_size(c.m), gb = static_cast<size_t>(head_size) * ms;
+  static const char* names[2][5] = {
+      {"queries dy", "queries x", "queries dx", "queries gamma", "queries dgamma"},
+      {"keys dy", "keys x", "keys dx", "keys gamma", "keys dgamma"}};
+  const bool empty = batch * seq == 0;
+  HeadsArg in[4], out[2];
+  Range flat_in[4], flat_out[2];
+  int nin = 0, nout = 0, nfin = empty ? 0 : rotation_ranges(c, flat_in), nfout = 0;
+  for (int i = 0; i < 2; ++i) {
+    const b200norm_heads_grad* h = given[i];
+    if (!h || h->heads == 0 || (!h->dx && !h->dgamma)) continue;
+    if (!aligned(h->gamma, ms) || !aligned(h->dgamma, ms))
+      return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s or %s is not aligned to its element size",
+                  names[i][3], names[i][4]);
+    if (h->gamma) flat_in[nfin++] = {h->gamma, gb, names[i][3]};
+    if (h->dgamma) flat_out[nfout++] = {h->dgamma, gb, names[i][4]};
+    c.set[i] = {h->x, h->dy, h->gamma, h->dx, h->dgamma, h->heads, to_strides(h->x_strides),
+                to_strides(h->dy_strides), to_strides(h->dx_strides)};
+    if (empty) continue;
+    in[nin++] = {h->dy, h->heads, h->dy_strides, names[i][0]};
+    in[nin++] = {h->x, h->heads, h->x_strides, names[i][1]};
+    if (h->dx) out[nout++] = {h->dx, h->heads, h->dx_strides, names[i][2]};
+  }
+  for (int i = 0; i < nin; ++i)
+    if (b200norm_status st = check_heads(in[i], batch, seq, head_size, es)) return st;
+  for (int i = 0; i < nout; ++i) {
+    if (b200norm_status st = check_heads(out[i], batch, seq, head_size, es)) return st;
+    if (!heads_distinct(out[i], batch, seq, head_size))
+      return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s overlaps itself", out[i].name);
+  }
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (!heads_apart(out[i], in[j], batch, seq, head_size, es))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", out[i].name, in[j].name);
+    const Range r = heads_range(out[i], batch, seq, head_size, es);
+    for (int j = 0; j < nfin; ++j)
+      if (overlaps(r, flat_in[j]))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", r.name, flat_in[j].name);
+    for (int j = 0; j < nfout; ++j)
+      if (overlaps(r, flat_out[j]))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "outputs %s and %s overlap", r.name,
+                    flat_out[j].name);
+  }
+  if (nout == 2 && !heads_apart(out[0], out[1], batch, seq, head_size, es))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "outputs overlap");
+  for (int i = 0; i < nin; ++i)
+    for (int j = 0; j < nfout; ++j)
+      if (overlaps(heads_range(in[i], batch, seq, head_size, es), flat_out[j]))
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", flat_out[j].name,
+                    in[i].name);
+  if (b200norm_status st = check_overlaps(flat_in, nfin, flat_out, nfout)) return st;
+  if (!c.set[0].heads && !c.set[1].heads) return ok();
+  if (!empty) {
+    Tensor all[12];
+    int n = 0;
+    for (int i = 0; i < nin; ++i) {
+      const Range r = heads_range(in[i], batch, seq, head_size, es);
+      all[n++] = {r.p, r.bytes, es, r.name, false};
+    }
+    for (int i = 0; i < nout; ++i) {
+      const Range r = heads_range(out[i], batch, seq, head_size, es);
+      all[n++] = {r.p, r.bytes, es, r.name, true};
+    }
+    for (int i = 0; i < nfin; ++i) all[n++] = {flat_in[i].p, flat_in[i].bytes, 1, flat_in[i].name, false};
+    for (int i = 0; i < nfout; ++i) all[n++] = {flat_out[i].p, flat_out[i].bytes, 1, flat_out[i].name, true};
+    const size_t need =
+        head_parts_bytes(head_parts(batch * seq, c.set[0].heads, c.set[1].heads), head_size);
+    if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, all, n)) return st;
+    c.part = static_cast<float*>(workspace);
+  }
+  cudaError_t e = launch_heads_grad(c, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "head_rms_rotary_grad launch");
+  return ok();
+}
+
+b200norm_status b200norm_rotary_frequencies(double* inv_freq, int64_t rotary_size, double base,
+                                            int scaling, double factor, double original_length,
+                                            double low, double high) {
+  if (rotary_size < 2 || rotary_size > kMaxHeadSize || rotary_size % 2 || !inv_freq)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "rotary_size must be even, in [2, 1024], and inv_freq given");
+  if (!std::isfinite(base) || base <= 0.0)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "base must be > 0 and finite");
+  if (scaling < 0 || scaling > 3)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "scaling must be 0 (none), 1 (positions), 2 (base) or 3 (by turns)");
+  if (scaling != 0 && (!std::isfinite(factor) || factor <= 0.0))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "factor must be > 0 and finite");
+  if (scaling == 2 && rotary_size == 2)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "scaling 2 needs more than one pair");
+  if (scaling == 3 && (!std::isfinite(original_length) || original_length <= 0.0 ||
+                       !std::isfinite(low) || !std::isfinite(high) || low < 0.0 || low >= high))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "need original_length > 0 and 0 <= low < high, all finite");
+  const double size = static_cast<double>(rotary_size);
+  if (scaling == 2) base *= std::pow(factor, size / (size - 2.0));
+  constexpr double kTwoPi = 6.283185307179586;
+  for (int64_t i = 0; i < rotary_size / 2; ++i) {
+    double f = std::pow(base, -2.0 * static_cast<double>(i) / size);
+    if (scaling == 1) f /= factor;
+    if (scaling == 3) {
+      double keep = (original_length * f / kTwoPi - low) / (high - low);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    inv_freq[i] = f;
+  }
   return ok();
 }
 

@@ -55,10 +55,11 @@ HeadParts head_parts(int64_t tokens, int64_t q_heads, int64_t k_heads) {
   const int64_t most = (tokens * heads + 8 * kHeadWarps - 1) / (8 * kHeadWarps);
   if (all > most) all = most;
   if (all < 2) all = 2;
-  HeadParts p = {0, 0};
-  if (q_heads > 0) p.q = static_cast<int>((all * q_heads + heads - 1) / heads);
-  if (k_heads > 0) p.k = static_cast<int>((all * k_heads + heads - 1) / heads);
-  return p;
+  if (k_heads == 0) return {static_cast<int>(all), 0};
+  if (q_heads == 0) return {0, static_cast<int>(all)};
+  int64_t q = (all * q_heads + heads / 2) / heads;
+  q = q < 1 ? 1 : q > all - 1 ? all - 1 : q;
+  return {static_cast<int>(q), static_cast<int>(all - q)};
 }
 
 cudaError_t launch_heads(const HeadsCall& c, cudaStream_t stream) {

@@ -17,8 +17,10 @@
 // positions cost no digits, and no binary64 operation is made per token.
 #pragma once
 
+#include "bulk.cuh"
 #include "common.cuh"
 #include "heads.h"
+#include "pair.cuh"
 
 namespace b200norm {
 
@@ -28,10 +30,34 @@ struct HeadsArgs {
   HeadsCall c;
   unsigned tokens, seq;
   int units, lanes;
+  int pitch;       // angles a warp keeps: whole units
   int steps[2];    // per token: the heads in groups of 32 / lanes
-  int splits;      // parts of a token's steps, a warp each
+  unsigned splits; // parts of a token's steps, a warp each, of `chunk` steps
+  int chunk;
   int parts[2];    // gradient: CTAs of queries and of keys
+  bool whole;      // a unit's pairs are all rotated, or none
 };
+
+// Rows on their way to a warp: each lane copies its own accesses to shared memory
+// asynchronously and reads them back itself, so that a step waits for copies issued
+// stages ago and nothing is exchanged.  With the next row in registers instead
+// (97 registers, 16 warps an SM), 16384 x 40 x 128 bf16 took 117 us: 16 KB an SM in flight.
+template <typename T, int VE, int K>
+struct HeadRow {
+  static constexpr int kStages = 64 * VE * K * sizeof(T) <= 1024 ? 4 : VE * K * sizeof(T) <= 32 ? 3 : 2;
+  Pack<T, VE> lo[K][32], hi[K][32];  // [lane]
+};
+
+// Dynamic shared memory: turns per position (8 bytes a pair), gamma widened (queries',
+// keys'), each warp's cosines and sines, and its rows.
+__host__ __device__ inline int head_table_floats(const HeadsArgs& g) {
+  return g.pitch * (2 * (1 + kHeadWarps) + (g.c.norm ? 4 : 0));
+}
+template <typename T, int VE, int K>
+size_t head_smem(const HeadsArgs& g, bool gradient) {
+  return static_cast<size_t>(head_table_floats(g)) * 4 +
+         sizeof(HeadRow<T, VE, K>) * HeadRow<T, VE, K>::kStages * kHeadWarps * (gradient ? 2 : 1);
+}
 
 // -- angles -----------------------------------------------------------------------
 
@@ -68,11 +94,93 @@ __device__ __forceinline__ void phase_cos_sin(unsigned phase, float& c, float& s
 
 // -- rows -------------------------------------------------------------------------
 
-// Where a lane's units lie: elements lo.. and hi.. of the row, VE each.
+// A row's elements in registers: two at a time, for one instruction on both, where an
+// access holds two or more.
+template <int VE>
+struct HeadVec {
+  using V = typename std::conditional<VE == 1, float, float2>::type;
+  static constexpr int N = VE == 1 ? 1 : VE / 2;
+};
+
+// The first (a) and second (b) elements of a unit's VE pairs, widened, from its accesses lo
+// and hi: these themselves, or, interleaved, the even and odd elements of both.
+template <typename T, int VE>
+__device__ __forceinline__ void unit_widen(const Pack<T, VE>& lo, const Pack<T, VE>& hi,
+                                           bool interleaved, typename HeadVec<VE>::V (&a)[HeadVec<VE>::N],
+                                           typename HeadVec<VE>::V (&b)[HeadVec<VE>::N]) {
+  if constexpr (VE == 1) {
+    a[0] = to_f32(lo.v[0]);
+    b[0] = to_f32(hi.v[0]);
+  } else if (!interleaved) {
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+      a[i] = get2(lo, i);
+      b[i] = get2(hi, i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+      const int j = 2 * i, k = 2 * i + 1, n = VE / 2;  // pairs j and k
+      const float2 x = j < n ? get2(lo, j) : get2(hi, j - n);
+      const float2 y = k < n ? get2(lo, k) : get2(hi, k - n);
+      a[i] = make_float2(x.x, y.x);
+      b[i] = make_float2(x.y, y.y);
+    }
+  }
+}
+
+template <typename T, int VE>
+__device__ __forceinline__ void unit_narrow(const typename HeadVec<VE>::V (&a)[HeadVec<VE>::N],
+                                            const typename HeadVec<VE>::V (&b)[HeadVec<VE>::N],
+                                            bool interleaved, Pack<T, VE>& lo, Pack<T, VE>& hi) {
+  if constexpr (VE == 1) {
+    lo.v[0] = from_f32<T>(a[0]);
+    hi.v[0] = from_f32<T>(b[0]);
+  } else if (!interleaved) {
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+      set2(lo, i, a[i].x, a[i].y);
+      set2(hi, i, b[i].x, b[i].y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+      const int j = 2 * i, k = 2 * i + 1, n = VE / 2;
+      if (j < n) set2(lo, j, a[i].x, b[i].x);
+      else set2(hi, j - n, a[i].x, b[i].x);
+      if (k < n) set2(lo, k, a[i].y, b[i].y);
+      else set2(hi, k - n, a[i].y, b[i].y);
+    }
+  }
+}
+
+// VE floats of shared memory, 16 bytes at a time where they are whole.
+template <int VE>
+__device__ __forceinline__ Pack<float, VE> read_floats(const float* p) {
+  Pack<float, VE> v;
+  if constexpr (VE <= 2) {
+    v = *reinterpret_cast<const Pack<float, VE>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VE / 4; ++i) {
+      const float4 f = reinterpret_cast<const float4*>(p)[i];
+      v.v[4 * i] = f.x;
+      v.v[4 * i + 1] = f.y;
+      v.v[4 * i + 2] = f.z;
+      v.v[4 * i + 3] = f.w;
+    }
+  }
+  return v;
+}
+
+// Where a lane's units lie: accesses lo and hi of the row, VE elements each, such that
+// neighbouring lanes' accesses are neighbours in memory.  A unit's VE pairs are, in the half
+// layout, elements i of lo and i of hi; interleaved, neighbours inside lo (the first VE / 2
+// pairs) and inside hi.
 template <int VE, int K>
 struct HeadUnits {
   int lo[K], hi[K];    // element of the row, -1: none
-  int pair[K];         // first of the unit's VE pairs
+  int pa[K], pb[K];    // pair of the first and of the second half of the unit's pairs
 };
 
 template <int VE, int K>
@@ -83,330 +191,611 @@ __device__ __forceinline__ HeadUnits<VE, K> head_units(const HeadsArgs& g, int s
   for (int k = 0; k < K; ++k) {
     const int i = sub + k * g.lanes;
     const bool in = i < g.units;
-    u.pair[k] = i * VE;
-    if (i * VE < half) {
-      u.lo[k] = in ? i * VE : -1;
-      u.hi[k] = in ? i * VE + half : -1;
-    } else {
-      u.lo[k] = in ? 2 * i * VE : -1;
-      u.hi[k] = in && 2 * i * VE + VE < g.c.size ? 2 * i * VE + VE : -1;
+    int lo = i * VE, hi = lo + half;
+    u.pa[k] = lo;
+    u.pb[k] = lo + VE / 2;
+    if (lo >= half) {  // past the half layout's pairs: the row's last part, in two halves
+      if (VE == 1 && g.c.interleaved) {
+        lo = 2 * i;
+        hi = lo + 1;
+      } else {
+        lo += half;
+        hi = lo + (g.units - half / VE) * VE;
+        u.pa[k] = lo / 2;
+        u.pb[k] = hi / 2;
+      }
     }
+    u.lo[k] = in ? lo : -1;
+    u.hi[k] = in && hi < g.c.size ? hi : -1;
+    if (!in) u.pa[k] = u.pb[k] = 0;
   }
   return u;
 }
 
-template <typename T, int VE, int K>
-struct HeadRow {
-  Pack<T, VE> lo[K], hi[K];
-};
-
-template <typename T, int VE, int K>
-__device__ __forceinline__ void head_load(HeadRow<T, VE, K>& r, const T* p, bool in,
-                                          const HeadUnits<VE, K>& u) {
-  const Pack<T, VE> zero = {};
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    r.lo[k] = in && u.lo[k] >= 0 ? ld_stream<T, VE>(p + u.lo[k]) : zero;
-    r.hi[k] = in && u.hi[k] >= 0 ? ld_stream<T, VE>(p + u.hi[k]) : zero;
-  }
+// This lane's accesses of a row to its place of a stage (zeros where it has none).  Two
+// bytes alone cannot be copied asynchronously: they are loaded.
+template <typename T, int VE>
+__device__ __forceinline__ void head_copy(Pack<T, VE>* dst, const T* src, bool in) {
+  constexpr int kBytes = sizeof(T) * VE;
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(smem_addr(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+  else if constexpr (kBytes == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                 :: "r"(smem_addr(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+  else
+    *dst = in ? ld_stream<T, VE>(src) : Pack<T, VE>{};
 }
 
 template <typename T, int VE, int K>
-__device__ __forceinline__ void head_store(T* p, bool in, const HeadUnits<VE, K>& u,
-                                           const float (&lo)[K][VE], const float (&hi)[K][VE]) {
+__device__ __forceinline__ void head_fetch(HeadRow<T, VE, K>& r, const T* p, bool in,
+                                           const HeadUnits<VE, K>& u) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (in && u.lo[k] >= 0) st_stream<T, VE>(p + u.lo[k], pack_from<T, VE>(lo[k]));
-    if (in && u.hi[k] >= 0) st_stream<T, VE>(p + u.hi[k], pack_from<T, VE>(hi[k]));
+    const bool l = in && u.lo[k] >= 0, h = in && u.hi[k] >= 0;
+    head_copy<T, VE>(&r.lo[k][lane], l ? p + u.lo[k] : p, l);
+    head_copy<T, VE>(&r.hi[k][lane], h ? p + u.hi[k] : p, h);
   }
 }
 
-// Cosine and sine (scaled, the sine's sign turned for the inverse) of a lane's pairs.
-template <int VE, int K>
-struct HeadAngles {
-  float c[K][VE], s[K][VE];
-};
+__device__ __forceinline__ void fetch_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the latest N groups of this thread have arrived.
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
 
 template <int VE, int K>
-__device__ __forceinline__ void head_angles(const HeadsArgs& g, const unsigned long long* steps,
-                                            const HeadUnits<VE, K>& u, unsigned b, unsigned t,
-                                            float sine, HeadAngles<VE, K>& a) {
-  const int pairs = g.c.rot / 2;
-  if (pairs == 0) return;
-  const int64_t at = b * g.c.pos_batch + t * g.c.pos_token;
-  const long long p = g.c.pos64 ? static_cast<const long long*>(g.c.positions)[at]
-                                : static_cast<const int*>(g.c.positions)[at];
+struct HeadValues {
+  typename HeadVec<VE>::V a[K][HeadVec<VE>::N], b[K][HeadVec<VE>::N];
+};
+
+template <typename T, int VE, int K>
+__device__ __forceinline__ void head_widen(const HeadRow<T, VE, K>& r, bool interleaved,
+                                           HeadValues<VE, K>& v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const int n = u.pair[k] + i;
-      const unsigned long long phase =
-          static_cast<unsigned long long>(p) * steps[n < pairs ? n : 0];
-      phase_cos_sin(static_cast<unsigned>(phase >> 32), a.c[k][i], a.s[k][i]);
-      a.c[k][i] *= g.c.scale;
-      a.s[k][i] *= sine;
-    }
+    unit_widen<T, VE>(r.lo[k][lane], r.hi[k][lane], interleaved, v.a[k], v.b[k]);
 }
 
-// The pairs of a unit turned; elements past rot stay as they are.
-template <int VE>
-__device__ __forceinline__ void turn(const HeadsArgs& g, int pair, const float (&c)[VE],
-                                     const float (&s)[VE], float (&lo)[VE], float (&hi)[VE]) {
-  const int pairs = g.c.rot / 2;
-  if (pair >= pairs) return;
-  if (VE == 1 || !g.c.interleaved) {  // all of the unit's pairs, each across lo and hi
+template <typename T, int VE, int K>
+__device__ __forceinline__ void head_store(T* p, bool in, bool interleaved,
+                                           const HeadUnits<VE, K>& u, const HeadValues<VE, K>& v) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float a = lo[i], b = hi[i];
-      lo[i] = fmaf(a, c[i], -(b * s[i]));
-      hi[i] = fmaf(b, c[i], a * s[i]);
+  for (int k = 0; k < K; ++k) {
+    Pack<T, VE> lo, hi;
+    unit_narrow<T, VE>(v.a[k], v.b[k], interleaved, lo, hi);
+    if (in && u.lo[k] >= 0) st_stream<T, VE>(p + u.lo[k], lo);
+    if (in && u.hi[k] >= 0) st_stream<T, VE>(p + u.hi[k], hi);
+  }
+}
+
+// Sum over the row's lanes (a power of two); fixed steps where LANES says how many.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, int lanes) {
+  if constexpr (LANES == 0) {
+    return seg_sum(v, lanes);
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+}
+
+// -- what a CTA's rows share --------------------------------------------------------
+
+struct HeadShared {
+  unsigned long long* steps;  // [pitch]
+  float* gamma;               // [2][2 * pitch]
+  float* cosines;             // this warp's [pitch], and its sines behind them
+};
+
+__device__ __forceinline__ HeadShared head_shared(const HeadsArgs& g, unsigned char* raw) {
+  HeadShared sh;
+  sh.steps = reinterpret_cast<unsigned long long*>(raw);
+  sh.gamma = reinterpret_cast<float*>(sh.steps + g.pitch);
+  sh.cosines = sh.gamma + (g.c.norm ? 4 * g.pitch : 0) + (threadIdx.x >> 5) * 2 * g.pitch;
+  return sh;
+}
+
+__device__ __forceinline__ float head_gamma_at(const HeadsArgs& g, int n, int j) {
+  const void* p = g.c.set[n].gamma;
+  if (!p || j >= g.c.size || g.c.set[n].heads == 0) return 1.0f;
+  return g.c.m == DType::F32   ? static_cast<const float*>(p)[j]
+         : g.c.m == DType::F16 ? to_f32(static_cast<const __half*>(p)[j])
+                               : to_f32(static_cast<const __nv_bfloat16*>(p)[j]);
+}
+
+__device__ __forceinline__ void head_fill(const HeadsArgs& g, const HeadShared& sh) {
+  for (int i = threadIdx.x; i < g.c.rot / 2; i += blockDim.x)
+    sh.steps[i] = phase_step(__ldg(g.c.inv_freq + i));
+  if (g.c.norm)
+    for (int i = threadIdx.x; i < 4 * g.pitch; i += blockDim.x) {
+      const int n = i >= 2 * g.pitch;
+      sh.gamma[i] = head_gamma_at(g, n, i - n * 2 * g.pitch);
+    }
+  __syncthreads();
+}
+
+__device__ __forceinline__ long long head_position(const HeadsArgs& g, unsigned b, unsigned t) {
+  if (g.c.rot == 0) return 0;
+  const int64_t at = b * g.c.pos_batch + t * g.c.pos_token;
+  return g.c.pos64 ? static_cast<const long long*>(g.c.positions)[at]
+                   : static_cast<const int*>(g.c.positions)[at];
+}
+
+// This warp's token: scaled cosines, and sines of the sign wanted; 1 and 0 past the pairs.
+__device__ __forceinline__ void head_angles(const HeadsArgs& g, const HeadShared& sh, long long p,
+                                            float sine) {
+  __syncwarp();
+  for (int n = threadIdx.x & 31; n < g.pitch; n += 32) {
+    float c = 1.0f, s = 0.0f;
+    if (n < g.c.rot / 2) {
+      const unsigned long long phase = static_cast<unsigned long long>(p) * sh.steps[n];
+      phase_cos_sin(static_cast<unsigned>(phase >> 32), c, s);
+      c *= g.c.scale;
+      s *= sine;
+    }
+    sh.cosines[n] = c;
+    sh.cosines[g.pitch + n] = s;
+  }
+  __syncwarp();
+}
+
+// A warp's item: a token, or a part of its heads.  The next one is a fixed number of items
+// away: no division is made but for the first.
+struct HeadItem {
+  unsigned b, t, split;
+};
+
+__device__ __forceinline__ HeadItem head_item(const HeadsArgs& g, unsigned long long item) {
+  HeadItem r;
+  const unsigned token = static_cast<unsigned>(item / g.splits);
+  r.split = static_cast<unsigned>(item - static_cast<unsigned long long>(token) * g.splits);
+  r.b = token / g.seq;
+  r.t = token - r.b * g.seq;
+  return r;
+}
+
+__device__ __forceinline__ void head_next(const HeadsArgs& g, HeadItem& r, const HeadItem& stride) {
+  r.split += stride.split;
+  r.t += stride.t;
+  r.b += stride.b;
+  if (r.split >= g.splits) {
+    r.split -= g.splits;
+    ++r.t;
+  }
+  if (r.t >= g.seq) {
+    r.t -= g.seq;
+    ++r.b;
+  }
+}
+
+// gamma of a unit's pairs.
+template <int VE, int K>
+__device__ __forceinline__ void unit_gamma(const float* gamma, const HeadUnits<VE, K>& u, int k,
+                                           bool interleaved, typename HeadVec<VE>::V (&a)[HeadVec<VE>::N],
+                                           typename HeadVec<VE>::V (&b)[HeadVec<VE>::N]) {
+  // (a unit that is not there has values of 0: any finite factor will do, gamma's first
+  // if that is one)
+  unit_widen<float, VE>(read_floats<VE>(gamma + (u.lo[k] >= 0 ? u.lo[k] : 0)),
+                        read_floats<VE>(gamma + (u.hi[k] >= 0 ? u.hi[k] : 0)), interleaved, a, b);
+}
+
+// Cosines and sines of a unit's pairs.
+template <int VE, int K>
+__device__ __forceinline__ void unit_angles(const float* p, const HeadUnits<VE, K>& u, int k,
+                                            typename HeadVec<VE>::V (&v)[HeadVec<VE>::N]) {
+  if constexpr (VE == 1) {
+    v[0] = p[u.pa[k]];
+  } else {
+    const Pack<float, VE / 2> a = read_floats<VE / 2>(p + u.pa[k]), b = read_floats<VE / 2>(p + u.pb[k]);
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+      const int j = 2 * i, k2 = 2 * i + 1, n = VE / 2;
+      v[i] = make_float2(j < n ? a.v[j] : b.v[j - n], k2 < n ? a.v[k2] : b.v[k2 - n]);
+    }
+  }
+}
+
+// (a, b) -> (a ca + b sa, b cb + a sb), what a pair of the rotation becomes; one past the
+// pairs (a ca, b cb): an infinity must not reach the neighbour through a factor of zero.
+template <int VE, int K, typename V, int N>
+__device__ __forceinline__ void unit_turn(const HeadsArgs& g, const HeadUnits<VE, K>& u, int k,
+                                          V (&a)[N], V (&b)[N], const V (&ca)[N],
+                                          const V (&sa)[N], const V (&cb)[N], const V (&sb)[N]) {
+  const int left_a = g.c.rot / 2 - u.pa[k], left_b = g.c.rot / 2 - u.pb[k];
+  V x[N], y[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = a[i];
+    y[i] = b[i];
+    a[i] = mul2(a[i], ca[i]);
+    b[i] = mul2(b[i], cb[i]);
+  }
+  if (VE != 2 && g.whole) {
+    if (left_a > 0) {
+#pragma unroll
+      for (int i = 0; i < (N + 1) / 2; ++i) {
+        a[i] = fma2(y[i], sa[i], a[i]);
+        b[i] = fma2(x[i], sb[i], b[i]);
+      }
+    }
+    if (left_b > 0) {
+#pragma unroll
+      for (int i = (N + 1) / 2; i < N; ++i) {
+        a[i] = fma2(y[i], sa[i], a[i]);
+        b[i] = fma2(x[i], sb[i], b[i]);
+      }
     }
     return;
   }
   if constexpr (VE > 1) {
+    auto turns = [&](int i) { return i < VE / 2 ? i < left_a : i - VE / 2 < left_b; };
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      if (pair + i >= pairs) continue;
-      float& x = i < VE / 2 ? lo[2 * i] : hi[2 * i - VE];
-      float& y = i < VE / 2 ? lo[2 * i + 1] : hi[2 * i + 1 - VE];
-      const float a = x, b = y;
-      x = fmaf(a, c[i], -(b * s[i]));
-      y = fmaf(b, c[i], a * s[i]);
-    }
-  }
-}
-
-// What a CTA's rows share, in shared memory: turns per position, and gamma widened.
-struct HeadShared {
-  unsigned long long steps[kMaxHeadSize / 2];
-  alignas(16) float gamma[2][kMaxHeadSize];
-};
-
-__device__ __forceinline__ void head_shared(const HeadsArgs& g, HeadShared& sh) {
-  for (int i = threadIdx.x; i < g.c.rot / 2; i += blockDim.x)
-    sh.steps[i] = phase_step(__ldg(g.c.inv_freq + i));
-  if (g.c.norm) {
-    for (int i = threadIdx.x; i < 2 * g.c.size; i += blockDim.x) {
-      const int n = i >= g.c.size, j = i - n * g.c.size;
-      const void* p = g.c.set[n].gamma;
-      float v = 1.0f;
-      if (p && g.c.set[n].heads > 0) {
-        v = g.c.m == DType::F32   ? static_cast<const float*>(p)[j]
-            : g.c.m == DType::F16 ? to_f32(static_cast<const __half*>(p)[j])
-                                  : to_f32(static_cast<const __nv_bfloat16*>(p)[j]);
+    for (int i = 0; i < N; ++i) {
+      if (turns(2 * i)) {
+        a[i].x = fmaf(y[i].x, sa[i].x, a[i].x);
+        b[i].x = fmaf(x[i].x, sb[i].x, b[i].x);
       }
-      sh.gamma[n][j] = v;
+      if (turns(2 * i + 1)) {
+        a[i].y = fmaf(y[i].y, sa[i].y, a[i].y);
+        b[i].y = fmaf(x[i].y, sb[i].y, b[i].y);
+      }
     }
   }
-  __syncthreads();
-}
-
-template <int VE, int K>
-__device__ __forceinline__ void head_gamma(const float* gamma, const HeadUnits<VE, K>& u,
-                                           float (&lo)[K][VE], float (&hi)[K][VE]) {
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      lo[k][i] = u.lo[k] >= 0 ? gamma[u.lo[k] + i] : 0.0f;
-      hi[k][i] = u.hi[k] >= 0 ? gamma[u.hi[k] + i] : 0.0f;
-    }
 }
 
 // -- forward ----------------------------------------------------------------------
 
-template <typename T, int VE, int K, bool NORM>
-__global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs g) {
-  __shared__ HeadShared sh;
-  pdl_wait();
-  pdl_trigger();
-  head_shared(g, sh);
-  const int lane = threadIdx.x & 31;
-  const int sub = lane & (g.lanes - 1), row = lane / g.lanes, rows = 32 / g.lanes;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kHeadWarps + (threadIdx.x >> 5);
-  const unsigned token = static_cast<unsigned>(item / g.splits);
-  if (token >= g.tokens) return;
-  const int split = static_cast<int>(item - static_cast<int64_t>(token) * g.splits);
-  const unsigned b = token / g.seq, t = token - b * g.seq;
-  const HeadUnits<VE, K> u = head_units<VE, K>(g, sub);
-  HeadAngles<VE, K> angle;
-  head_angles<VE, K>(g, sh.steps, u, b, t, g.c.inverse ? -g.c.scale : g.c.scale, angle);
-  const float inv_size = 1.0f / static_cast<float>(g.c.size);
-  const int all = g.steps[0] + g.steps[1];
-  const int first = static_cast<int>(static_cast<int64_t>(all) * split / g.splits);
-  const int last = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / g.splits);
-#pragma unroll 1
-  for (int n = 0; n < 2; ++n) {
-    const HeadSet& set = g.c.set[n];
-    const int off = n ? g.steps[0] : 0;
-    const int lo = first > off ? first - off : 0;
-    const int hi = last - off < g.steps[n] ? last - off : g.steps[n];
-    if (lo >= hi) continue;
-    const T* x = static_cast<const T*>(set.x) + b * set.xs.batch + t * set.xs.token;
-    T* y = static_cast<T*>(set.y) + b * set.ys.batch + t * set.ys.token;
-    float gl[K][VE], gh[K][VE];
-    if constexpr (NORM) head_gamma<VE, K>(sh.gamma[n], u, gl, gh);
-    HeadRow<T, VE, K> next;
-    int64_t h = static_cast<int64_t>(lo) * rows + row;
-    head_load<T, VE, K>(next, x + h * set.xs.head, h < set.heads, u);
-#pragma unroll 1
-    for (int i = lo; i < hi; ++i, h += rows) {
-      const HeadRow<T, VE, K> now = next;
-      if (i + 1 < hi)
-        head_load<T, VE, K>(next, x + (h + rows) * set.xs.head, h + rows < set.heads, u);
-      float vl[K][VE], vh[K][VE];
+// What multiplies a lane's pairs: gamma and the angles in one.
+template <int VE, int K>
+struct HeadFactors {
+  using V = typename HeadVec<VE>::V;
+  static constexpr int N = HeadVec<VE>::N;
+  V ca[K][N], sa[K][N], cb[K][N], sb[K][N];
+};
+
+template <int VE, int K, bool NORM>
+__device__ __forceinline__ void head_factors(const HeadsArgs& g, const HeadShared& sh,
+                                             const float* gamma, const HeadUnits<VE, K>& u,
+                                             HeadFactors<VE, K>& f) {
+  using V = typename HeadVec<VE>::V;
+  constexpr int N = HeadVec<VE>::N;
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        unpack(now.lo[k], vl[k]);
-        unpack(now.hi[k], vh[k]);
-      }
-      if constexpr (NORM) {
-        float sum = 0.0f;
+  for (int k = 0; k < K; ++k) {
+    V c[N], s[N], ga[N], gb[N];
+    unit_angles<VE, K>(sh.cosines, u, k, c);
+    unit_angles<VE, K>(sh.cosines + g.pitch, u, k, s);
+    if constexpr (NORM) unit_gamma<VE, K>(gamma, u, k, g.c.interleaved, ga, gb);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            sum = fmaf(vl[k][e], vl[k][e], sum);
-            sum = fmaf(vh[k][e], vh[k][e], sum);
-          }
-        sum = seg_sum(sum, g.lanes);
-        const float r = rsqrtf(sum * inv_size + g.c.eps);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            vl[k][e] = vl[k][e] * r * gl[k][e];
-            vh[k][e] = vh[k][e] * r * gh[k][e];
-          }
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k) turn<VE>(g, u.pair[k], angle.c[k], angle.s[k], vl[k], vh[k]);
-      head_store<T, VE, K>(y + h * set.ys.head, h < set.heads, u, vl, vh);
+    for (int i = 0; i < N; ++i) {
+      if constexpr (!NORM) ga[i] = gb[i] = every<V>(1.0f);
+      f.ca[k][i] = mul2(ga[i], c[i]);
+      f.sa[k][i] = mul2(mul2(gb[i], s[i]), every<V>(-1.0f));
+      f.cb[k][i] = mul2(gb[i], c[i]);
+      f.sb[k][i] = mul2(ga[i], s[i]);
     }
   }
+}
+
+// The rows that a warp takes, in order: item by item, step by step, a row of one tensor
+// for each group of lanes.  `p` is this lane's row.
+template <typename T>
+struct HeadCursor {
+  unsigned long long item;
+  HeadItem at;
+  int i, last;     // steps of the item
+  const T* p;
+  int64_t step;    // elements from a step's row to the next
+  int left;        // this lane's rows from here on end at 0 (of the tensor)
+};
+
+template <typename T, int VE, int K, int LANES, bool NORM>
+__global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs g) {
+  using V = typename HeadVec<VE>::V;
+  constexpr int N = HeadVec<VE>::N, S = HeadRow<T, VE, K>::kStages;
+  extern __shared__ __align__(16) unsigned char raw[];
+  const HeadShared sh = head_shared(g, raw);
+  HeadRow<T, VE, K>* ring = reinterpret_cast<HeadRow<T, VE, K>*>(raw + head_table_floats(g) * 4) +
+                            (threadIdx.x >> 5) * S;
+  const int lanes = LANES ? LANES : g.lanes;
+  const int lane = threadIdx.x & 31;
+  const int sub = lane & (lanes - 1), row = lane / lanes, rows = 32 / lanes;
+  const HeadUnits<VE, K> u = head_units<VE, K>(g, sub);
+  const int steps = g.steps[0] + g.steps[1];
+  const float inv_size = 1.0f / static_cast<float>(g.c.size);
+  const unsigned long long items = static_cast<unsigned long long>(g.tokens) * g.splits;
+  const unsigned long long stride = static_cast<unsigned long long>(gridDim.x) * kHeadWarps;
+  unsigned long long item = static_cast<unsigned long long>(blockIdx.x) * kHeadWarps +
+                            (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
+
+  // what is fetched, some steps ahead of what is worked on
+  const HeadItem hop = head_item(g, stride);
+  HeadItem at = head_item(g, item);
+  HeadCursor<T> c;
+  c.item = item;
+  c.at = at;
+  auto seek = [&] {  // to step i of the item: queries first, then keys
+    const int n = c.i >= g.steps[0];
+    const HeadSet& set = g.c.set[n];
+    const int64_t h = static_cast<int64_t>(c.i - (n ? g.steps[0] : 0)) * rows + row;
+    c.p = static_cast<const T*>(set.x) + c.at.b * set.xs.batch + c.at.t * set.xs.token +
+          h * set.xs.head;
+    c.step = rows * set.xs.head;
+    c.left = static_cast<int>(set.heads - h);
+  };
+  auto open = [&] {
+    c.i = static_cast<int>(c.at.split) * g.chunk;
+    c.last = c.i + g.chunk < steps ? c.i + g.chunk : steps;
+    if (c.item < items) seek();
+  };
+  auto fetch = [&](int stage) {
+    if (c.item < items) {
+      head_fetch<T, VE, K>(ring[stage], c.p, c.left > 0, u);
+      if (++c.i == c.last) {
+        c.item += stride;
+        head_next(g, c.at, hop);
+        open();
+      } else if (c.i == g.steps[0]) {
+        seek();
+      } else {
+        c.p += c.step;
+        c.left -= rows;
+      }
+    }
+    fetch_commit();
+  };
+  open();
+  long long position = item < items ? head_position(g, at.b, at.t) : 0;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i);
+  head_fill(g, sh);
+  int stage = 0;
+  while (item < items) {
+    head_angles(g, sh, position, g.c.inverse ? -g.c.scale : g.c.scale);
+    HeadItem then = at;
+    head_next(g, then, hop);
+    item += stride;
+    if (item < items) position = head_position(g, then.b, then.t);
+    const int begin = static_cast<int>(at.split) * g.chunk;
+    const int end = begin + g.chunk < steps ? begin + g.chunk : steps;
+#pragma unroll 1
+    for (int n = 0; n < 2; ++n) {
+      const HeadSet& set = g.c.set[n];
+      const int off = n ? g.steps[0] : 0;
+      const int first = begin > off ? begin - off : 0;
+      const int last = end - off < g.steps[n] ? end - off : g.steps[n];
+      if (first >= last) continue;
+      HeadFactors<VE, K> f;
+      head_factors<VE, K, NORM>(g, sh, sh.gamma + (n ? 2 * g.pitch : 0), u, f);
+      const int64_t h = static_cast<int64_t>(first) * rows + row;
+      T* y = static_cast<T*>(set.y) + at.b * set.ys.batch + at.t * set.ys.token + h * set.ys.head;
+      const int64_t step = rows * set.ys.head;
+      int left = static_cast<int>(set.heads - h);
+#pragma unroll 1
+      for (int i = first; i < last; ++i, y += step, left -= rows) {
+        fetch_wait<S - 2>();
+        HeadValues<VE, K> x;
+        head_widen<T, VE, K>(ring[stage], g.c.interleaved, x);
+        float r = 1.0f;
+        if constexpr (NORM) {
+          V sa = every<V>(0.0f), sb = every<V>(0.0f);
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              sa = fma2(x.a[k][e], x.a[k][e], sa);
+              sb = fma2(x.b[k][e], x.b[k][e], sb);
+            }
+          r = rsqrtf(row_sum<LANES>(total(add2(sa, sb)), lanes) * inv_size + g.c.eps);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          unit_turn<VE, K>(g, u, k, x.a[k], x.b[k], f.ca[k], f.sa[k], f.cb[k], f.sb[k]);
+        if constexpr (NORM) {
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              x.a[k][e] = mul2(x.a[k][e], every<V>(r));
+              x.b[k][e] = mul2(x.b[k][e], every<V>(r));
+            }
+        }
+        head_store<T, VE, K>(y, left > 0, g.c.interleaved, u, x);
+        // into the stage before this one, whose values have all been used
+        fetch(stage == 0 ? S - 1 : stage - 1);
+        stage = stage + 1 == S ? 0 : stage + 1;
+      }
+    }
+    at = then;
+  }
+  fetch_wait<0>();
 }
 
 // -- gradient ---------------------------------------------------------------------
 
 // With da = the rotation transposed of dy and g = da gamma:
-//   dx = r (g - u mean(g u)),  dgamma = sum over rows of da u.
+//   dx = r (g - u mean(g u)) = r g - x r^3 mean(g x),  dgamma = sum over rows of da u.
 // The first parts[0] CTAs take the queries, the others the keys; each keeps its
 // columns' sums in registers over all its rows and stores them as one part.
-template <typename T, int VE, int K>
-__global__ void __launch_bounds__(32 * kHeadWarps) heads_grad_kernel(const HeadsArgs g) {
-  __shared__ HeadShared sh;
-  __shared__ float red[kHeadWarps][kMaxHeadSize];
-  pdl_wait();
-  pdl_trigger();
-  head_shared(g, sh);
+template <typename T, int VE, int K, int LANES>
+__global__ void __launch_bounds__(32 * kHeadWarps, 2 * VE * K <= 16 ? 2 : 1)
+heads_grad_kernel(const HeadsArgs g) {
+  using V = typename HeadVec<VE>::V;
+  constexpr int N = HeadVec<VE>::N, S = HeadRow<T, VE, K>::kStages;
+  extern __shared__ __align__(16) unsigned char raw[];
+  const HeadShared sh = head_shared(g, raw);
+  HeadRow<T, VE, K>* ring = reinterpret_cast<HeadRow<T, VE, K>*>(raw + head_table_floats(g) * 4) +
+                            (threadIdx.x >> 5) * 2 * S;
+  const int lanes = LANES ? LANES : g.lanes;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane & (g.lanes - 1), row = lane / g.lanes, rows = 32 / g.lanes;
+  const int sub = lane & (lanes - 1), row = lane / lanes, rows = 32 / lanes;
   const int n = blockIdx.x >= static_cast<unsigned>(g.parts[0]);
   const HeadSet& set = g.c.set[n];
   const unsigned part = blockIdx.x - (n ? g.parts[0] : 0);
   const HeadUnits<VE, K> u = head_units<VE, K>(g, sub);
   const float inv_size = 1.0f / static_cast<float>(g.c.size);
-  float gl[K][VE], gh[K][VE];
-  head_gamma<VE, K>(sh.gamma[n], u, gl, gh);
-  float dl[K][VE] = {}, dh[K][VE] = {};
   const unsigned long long items = static_cast<unsigned long long>(g.tokens) * g.splits;
   const unsigned long long stride = static_cast<unsigned long long>(g.parts[n]) * kHeadWarps;
-#pragma unroll 1
-  for (unsigned long long item = static_cast<unsigned long long>(part) * kHeadWarps + warp;
-       item < items; item += stride) {
-    const unsigned token = static_cast<unsigned>(item / g.splits);
-    const int split = static_cast<int>(item - static_cast<unsigned long long>(token) * g.splits);
-    const unsigned b = token / g.seq, t = token - b * g.seq;
-    const int first = static_cast<int>(static_cast<int64_t>(g.steps[n]) * split / g.splits);
-    const int last = static_cast<int>(static_cast<int64_t>(g.steps[n]) * (split + 1) / g.splits);
-    if (first >= last) continue;
-    HeadAngles<VE, K> angle;
-    head_angles<VE, K>(g, sh.steps, u, b, t, -g.c.scale, angle);
-    const T* x = static_cast<const T*>(set.x) + b * set.xs.batch + t * set.xs.token;
-    const T* dy = static_cast<const T*>(set.dy) + b * set.dys.batch + t * set.dys.token;
-    T* dx = static_cast<T*>(set.y);
-    if (dx) dx += b * set.ys.batch + t * set.ys.token;
-    HeadRow<T, VE, K> nx, nd;
-    int64_t h = static_cast<int64_t>(first) * rows + row;
-    head_load<T, VE, K>(nx, x + h * set.xs.head, h < set.heads, u);
-    head_load<T, VE, K>(nd, dy + h * set.dys.head, h < set.heads, u);
-#pragma unroll 1
-    for (int i = first; i < last; ++i, h += rows) {
-      const HeadRow<T, VE, K> rx = nx, rd = nd;
-      if (i + 1 < last) {
-        head_load<T, VE, K>(nx, x + (h + rows) * set.xs.head, h + rows < set.heads, u);
-        head_load<T, VE, K>(nd, dy + (h + rows) * set.dys.head, h + rows < set.heads, u);
-      }
-      float al[K][VE], ah[K][VE], xl[K][VE], xh[K][VE];
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        unpack(rx.lo[k], xl[k]);
-        unpack(rx.hi[k], xh[k]);
-        unpack(rd.lo[k], al[k]);
-        unpack(rd.hi[k], ah[k]);
-        turn<VE>(g, u.pair[k], angle.c[k], angle.s[k], al[k], ah[k]);
-      }
-      float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          sum = fmaf(xl[k][e], xl[k][e], sum);
-          sum = fmaf(xh[k][e], xh[k][e], sum);
-        }
-      const float r = rsqrtf(seg_sum(sum, g.lanes) * inv_size + g.c.eps);
-      float dot = 0.0f;
-      // a lane without a row here has dy = 0, and x = 0: nothing is added unless r is
-      // infinite (eps 0), so its sums are left alone
-      const bool in = h < set.heads;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          xl[k][e] *= r;
-          xh[k][e] *= r;
-          if (in) {
-            dl[k][e] = fmaf(al[k][e], xl[k][e], dl[k][e]);
-            dh[k][e] = fmaf(ah[k][e], xh[k][e], dh[k][e]);
-          }
-          al[k][e] *= gl[k][e];
-          ah[k][e] *= gh[k][e];
-          dot = fmaf(al[k][e], xl[k][e], dot);
-          dot = fmaf(ah[k][e], xh[k][e], dot);
-        }
-      if (!dx) continue;
-      const float m = seg_sum(dot, g.lanes) * inv_size;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          al[k][e] = r * fmaf(-m, xl[k][e], al[k][e]);
-          ah[k][e] = r * fmaf(-m, xh[k][e], ah[k][e]);
-        }
-      head_store<T, VE, K>(dx + h * set.ys.head, in, u, al, ah);
+  pdl_wait();
+  pdl_trigger();
+
+  // what is fetched, some steps ahead of what is worked on
+  HeadCursor<T> c;
+  const T* pd = nullptr;
+  const int64_t step_d = rows * set.dys.head, step_y = rows * set.ys.head;
+  c.step = rows * set.xs.head;
+  const HeadItem hop = head_item(g, stride);
+  // to an item with steps (where the other tensor has more heads, a split may have none)
+  auto skip = [&](unsigned long long& item, HeadItem& at) {
+    while (item < items && static_cast<int>(at.split) * g.chunk >= g.steps[n]) {
+      item += stride;
+      head_next(g, at, hop);
     }
-  }
-  if (!set.dgamma) return;
-  // the groups of a warp, then the warps in order
+  };
+  auto open = [&] {
+    skip(c.item, c.at);
+    if (c.item >= items) return;
+    c.i = static_cast<int>(c.at.split) * g.chunk;
+    c.last = c.i + g.chunk < g.steps[n] ? c.i + g.chunk : g.steps[n];
+    const int64_t h = static_cast<int64_t>(c.i) * rows + row;
+    c.p = static_cast<const T*>(set.x) + c.at.b * set.xs.batch + c.at.t * set.xs.token +
+          h * set.xs.head;
+    pd = static_cast<const T*>(set.dy) + c.at.b * set.dys.batch + c.at.t * set.dys.token +
+         h * set.dys.head;
+    c.left = static_cast<int>(set.heads - h);
+  };
+  auto fetch = [&](int stage) {
+    if (c.item < items) {
+      head_fetch<T, VE, K>(ring[2 * stage], c.p, c.left > 0, u);
+      head_fetch<T, VE, K>(ring[2 * stage + 1], pd, c.left > 0, u);
+      if (++c.i == c.last) {
+        c.item += stride;
+        head_next(g, c.at, hop);
+        open();
+      } else {
+        c.p += c.step;
+        pd += step_d;
+        c.left -= rows;
+      }
+    }
+    fetch_commit();
+  };
+  c.item = static_cast<unsigned long long>(part) * kHeadWarps + warp;
+  c.at = head_item(g, c.item);
+  open();
+  unsigned long long item = c.item;
+  HeadItem at = c.at;
+  long long position = item < items ? head_position(g, at.b, at.t) : 0;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(i);
+  head_fill(g, sh);
+  int stage = 0;
+  V da[K][N], db[K][N];
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
+    for (int e = 0; e < N; ++e) da[k][e] = db[k][e] = every<V>(0.0f);
+  while (item < items) {
+    head_angles(g, sh, position, g.c.scale);
+    HeadItem then = at;
+    head_next(g, then, hop);
+    item += stride;
+    skip(item, then);
+    if (item < items) position = head_position(g, then.b, then.t);
+    const int first = static_cast<int>(at.split) * g.chunk;
+    const int last = first + g.chunk < g.steps[n] ? first + g.chunk : g.steps[n];
+    const int64_t h = static_cast<int64_t>(first) * rows + row;
+    T* y = static_cast<T*>(set.y) + at.b * set.ys.batch + at.t * set.ys.token + h * set.ys.head;
+    int left = static_cast<int>(set.heads - h);
+#pragma unroll 1
+    for (int i = first; i < last; ++i, y += step_y, left -= rows) {
+      fetch_wait<S - 2>();
+      HeadValues<VE, K> x, d;
+      head_widen<T, VE, K>(ring[2 * stage], g.c.interleaved, x);
+      head_widen<T, VE, K>(ring[2 * stage + 1], g.c.interleaved, d);
+      V sum = every<V>(0.0f), dot = every<V>(0.0f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        // turned back; angles and gamma come from shared memory every time: kept in
+        // registers they took 40 of them, and spilled
+        V c[N], s[N], t[N], ga[N], gb[N];
+        unit_angles<VE, K>(sh.cosines, u, k, c);
+        unit_angles<VE, K>(sh.cosines + g.pitch, u, k, s);
+#pragma unroll
+        for (int e = 0; e < N; ++e) t[e] = mul2(s[e], every<V>(-1.0f));
+        unit_turn<VE, K>(g, u, k, d.a[k], d.b[k], c, s, c, t);
+        unit_gamma<VE, K>(sh.gamma + n * 2 * g.pitch, u, k, g.c.interleaved, ga, gb);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          sum = fma2(x.a[k][e], x.a[k][e], sum);
+          dot = fma2(mul2(d.a[k][e], ga[e]), x.a[k][e], dot);
+          sum = fma2(x.b[k][e], x.b[k][e], sum);
+          dot = fma2(mul2(d.b[k][e], gb[e]), x.b[k][e], dot);
+        }
+      }
+      const float r = rsqrtf(row_sum<LANES>(total(sum), lanes) * inv_size + g.c.eps);
+      const float m = row_sum<LANES>(total(dot), lanes) * inv_size * r * r;
+      const bool in = left > 0;
+      // (a lane without a row here has zeros, but r may be infinite for eps 0)
+      if (in) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          V ga[N], gb[N];
+          unit_gamma<VE, K>(sh.gamma + n * 2 * g.pitch, u, k, g.c.interleaved, ga, gb);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const V ua = mul2(x.a[k][e], every<V>(r)), ub = mul2(x.b[k][e], every<V>(r));
+            da[k][e] = fma2(d.a[k][e], ua, da[k][e]);
+            db[k][e] = fma2(d.b[k][e], ub, db[k][e]);
+            d.a[k][e] = mul2(mul2(d.a[k][e], ga[e]), every<V>(r));
+            d.b[k][e] = mul2(mul2(d.b[k][e], gb[e]), every<V>(r));
+            d.a[k][e] = fma2(ua, every<V>(-m), d.a[k][e]);
+            d.b[k][e] = fma2(ub, every<V>(-m), d.b[k][e]);
+          }
+        }
+      }
+      if (set.y) head_store<T, VE, K>(y, in, g.c.interleaved, u, d);
+      // into the stage before this one, whose values have all been used
+      fetch(stage == 0 ? S - 1 : stage - 1);
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    at = then;
+  }
+  fetch_wait<0>();
+  if (!set.dgamma) return;
+  // the groups of a warp, then the warps in order, through the shared memory that held
+  // the angles and gammas
+  float* red = reinterpret_cast<float*>(raw);  // [kHeadWarps][2 * pitch]
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    Pack<float, VE> lo, hi;
+    unit_narrow<float, VE>(da[k], db[k], g.c.interleaved, lo, hi);
+#pragma unroll
     for (int e = 0; e < VE; ++e) {
-      for (int o = g.lanes; o < 32; o <<= 1) {
-        dl[k][e] += __shfl_xor_sync(0xffffffffu, dl[k][e], o);
-        dh[k][e] += __shfl_xor_sync(0xffffffffu, dh[k][e], o);
+      for (int o = lanes; o < 32; o <<= 1) {
+        lo.v[e] += __shfl_xor_sync(0xffffffffu, lo.v[e], o);
+        hi.v[e] += __shfl_xor_sync(0xffffffffu, hi.v[e], o);
       }
       if (row == 0) {
-        if (u.lo[k] >= 0) red[warp][u.lo[k] + e] = dl[k][e];
-        if (u.hi[k] >= 0) red[warp][u.hi[k] + e] = dh[k][e];
+        if (u.lo[k] >= 0) red[warp * 2 * g.pitch + u.lo[k] + e] = lo.v[e];
+        if (u.hi[k] >= 0) red[warp * 2 * g.pitch + u.hi[k] + e] = hi.v[e];
       }
     }
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < g.c.size; i += blockDim.x) {
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kHeadWarps; ++w) t += red[w][i];
+    for (int w = 0; w < kHeadWarps; ++w) t += red[w * 2 * g.pitch + i];
     g.c.part[static_cast<int64_t>(blockIdx.x) * g.c.size + i] = t;
   }
 }

@@ -1,13 +1,15 @@
 // heads_launch.cuh -- host-side launch of the head kernels for one element type.
 #pragma once
 
+#include <atomic>
+
 #include "heads.cuh"
 #include "launch_kernel.cuh"
 
 namespace b200norm {
 
-// Warps that a forward call spreads a token's heads over while the GPU has room.
-constexpr int64_t kHeadFill = 152 * 16;
+// Warps that a call spreads a token's heads over while the GPU has room.
+constexpr int64_t kHeadFill = 152 * 32;
 
 inline HeadsArgs head_args(const HeadsCall& c, const HeadsPlan& p) {
   HeadsArgs g = {};
@@ -16,30 +18,73 @@ inline HeadsArgs head_args(const HeadsCall& c, const HeadsPlan& p) {
   g.seq = static_cast<unsigned>(c.seq);
   g.units = p.units;
   g.lanes = p.lanes;
+  g.whole = p.ve < 4 || c.rot / 2 % (p.ve / 2) == 0;  // (half layout: of whole accesses)
   const int rows = 32 / p.lanes;
   for (int n = 0; n < 2; ++n)
     g.steps[n] = static_cast<int>((c.set[n].heads + rows - 1) / rows);
   return g;
 }
 
-// f(VE, K) for the row layout: K is rounded up to what has a kernel.
+// A token's steps in about `wanted` parts, none empty.
+inline void head_split(HeadsArgs& g, int64_t wanted, int64_t steps) {
+  if (wanted > steps) wanted = steps;
+  if (wanted < 1) wanted = 1;
+  g.chunk = static_cast<int>((steps + wanted - 1) / wanted);
+  g.splits = static_cast<unsigned>((steps + g.chunk - 1) / g.chunk);
+}
+
+template <int N>
+using Num = std::integral_constant<int, N>;
+
+// f(VE, K, LANES) for the row layout: K is rounded up to what has a kernel, and LANES is 0
+// (known at run time) but for the usual rows of whole 16-byte vectors.
 template <typename T, class F>
 cudaError_t with_head_layout(const HeadsPlan& p, F&& f) {
   constexpr int kVec = 16 / sizeof(T);
   if (p.ve == kVec) {
-    if (p.sets <= 1) return f(std::integral_constant<int, kVec>(), std::integral_constant<int, 1>());
-    if (p.sets <= 2) return f(std::integral_constant<int, kVec>(), std::integral_constant<int, 2>());
-    if constexpr (sizeof(T) == 4)
-      return f(std::integral_constant<int, kVec>(), std::integral_constant<int, 4>());
+    if (p.sets <= 1) {
+      if (p.lanes == 8) return f(Num<kVec>(), Num<1>(), Num<8>());
+      if (p.lanes == 16) return f(Num<kVec>(), Num<1>(), Num<16>());
+      return f(Num<kVec>(), Num<1>(), Num<0>());
+    }
+    if (p.sets <= 2) return f(Num<kVec>(), Num<2>(), Num<0>());
+    if constexpr (sizeof(T) == 4) return f(Num<kVec>(), Num<4>(), Num<0>());
   }
   if constexpr (sizeof(T) == 2) {
     if (p.ve == 2) {
-      if (p.sets <= 2) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
-      return f(std::integral_constant<int, 2>(), std::integral_constant<int, 8>());
+      if (p.sets <= 2) return f(Num<2>(), Num<2>(), Num<0>());
+      return f(Num<2>(), Num<8>(), Num<0>());
     }
   }
-  if (p.sets <= 4) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
-  return f(std::integral_constant<int, 1>(), std::integral_constant<int, 16>());
+  if (p.sets <= 4) return f(Num<1>(), Num<4>(), Num<0>());
+  return f(Num<1>(), Num<16>(), Num<0>());
+}
+
+// Raises a kernel's dynamic shared-memory limit once per device (every time on devices
+// past the first 64).
+template <class Fn>
+cudaError_t head_raise(Fn fn, size_t smem, std::atomic<unsigned long long>& raised) {
+  if (smem <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (raised.load() & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess) raised.fetch_or(bit);
+  return e;
+}
+
+// CTAs of a kernel that are resident at once (0: unknown).
+template <class Fn>
+int64_t head_resident(Fn fn, size_t smem) {
+  int dev = 0, sms = 0, per = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, 32 * kHeadWarps, smem) !=
+          cudaSuccess)
+    return 0;
+  return static_cast<int64_t>(sms) * per;
 }
 
 template <typename T>
@@ -47,15 +92,23 @@ cudaError_t launch_heads_t(const HeadsCall& c, cudaStream_t stream) {
   const HeadsPlan p = plan_heads(c, false);
   HeadsArgs g = head_args(c, p);
   const int64_t all = static_cast<int64_t>(g.steps[0]) + g.steps[1];
-  int64_t splits = (kHeadFill + g.tokens - 1) / g.tokens;
-  if (splits > all) splits = all;
-  g.splits = static_cast<int>(splits);
-  const int64_t items = splits * g.tokens;
-  const dim3 grid(static_cast<unsigned>((items + kHeadWarps - 1) / kHeadWarps));
-  return with_head_layout<T>(p, [&](auto ve, auto k) {
-    constexpr int VE = decltype(ve)::value, K = decltype(k)::value;
-    return c.norm ? launch_pdl(heads_kernel<T, VE, K, true>, grid, 32 * kHeadWarps, stream, g)
-                  : launch_pdl(heads_kernel<T, VE, K, false>, grid, 32 * kHeadWarps, stream, g);
+  head_split(g, kHeadFill / g.tokens, all);
+  const int64_t items = static_cast<int64_t>(g.splits) * g.tokens;
+  return with_head_layout<T>(p, [&](auto ve, auto k, auto lanes) {
+    constexpr int VE = decltype(ve)::value, K = decltype(k)::value, L = decltype(lanes)::value;
+    auto go = [&](auto norm) {
+      auto* fn = heads_kernel<T, VE, K, L, decltype(norm)::value>;
+      static std::atomic<unsigned long long> raised{0};
+      g.pitch = p.lanes * K * VE;
+      const size_t smem = head_smem<T, VE, K>(g, false);
+      if (const cudaError_t e = head_raise(fn, smem, raised)) return e;
+      int64_t grid = (items + kHeadWarps - 1) / kHeadWarps;
+      const int64_t most = head_resident(fn, smem);
+      if (most > 0 && grid > most) grid = most;
+      return launch_clusters(fn, dim3(static_cast<unsigned>(grid)), 32 * kHeadWarps, 1, smem,
+                             stream, g);
+    };
+    return c.norm ? go(std::true_type()) : go(std::false_type());
   });
 }
 
@@ -69,15 +122,17 @@ cudaError_t launch_heads_grad_t(const HeadsCall& c, cudaStream_t stream) {
   // a part's warps take tokens, or parts of a token's heads where there are more warps
   const int most = g.steps[0] > g.steps[1] ? g.steps[0] : g.steps[1];
   const int64_t warps = static_cast<int64_t>(parts.q + parts.k) * kHeadWarps;
-  int64_t splits = warps / (2 * static_cast<int64_t>(g.tokens));
-  if (splits > most) splits = most;
-  g.splits = static_cast<int>(splits < 1 ? 1 : splits);
-  const dim3 grid(static_cast<unsigned>(parts.q + parts.k));
-  cudaError_t e = with_head_layout<T>(p, [&](auto ve, auto k) {
-    return launch_pdl(heads_grad_kernel<T, decltype(ve)::value, decltype(k)::value>, grid,
-                      32 * kHeadWarps, stream, g);
+  head_split(g, warps / g.tokens, most);
+  return with_head_layout<T>(p, [&](auto ve, auto k, auto lanes) {
+    constexpr int VE = decltype(ve)::value, K = decltype(k)::value, L = decltype(lanes)::value;
+    static std::atomic<unsigned long long> raised{0};
+    g.pitch = p.lanes * K * VE;
+    auto* fn = heads_grad_kernel<T, VE, K, L>;
+    const size_t smem = head_smem<T, VE, K>(g, true);
+    if (const cudaError_t e = head_raise(fn, smem, raised)) return e;
+    return launch_clusters(fn, dim3(static_cast<unsigned>(parts.q + parts.k)), 32 * kHeadWarps, 1,
+                           smem, stream, g);
   });
-  return e;
 }
 
 // dgamma of both tensors from `parts`, of type M.

@@ -458,7 +458,8 @@ typedef struct b200norm_heads {
  * y = round_T(rotation(x)), or round_T(rotation(u)), of queries and of keys, in one
  * launch.  Either tensor may be NULL.
  *
- *   batch, seq   tokens are (batch, seq); their product may be 2^31 - 1 at most.
+ *   batch, seq   tokens are (batch, seq); their product may be 2^31 - 1 at most,
+ *                times the heads 2^40.
  *   head_size    elements of a head, in [1, 1024]; heads: at most 2^16.
  *   T, M         element types of heads and gamma; M is T or B200NORM_F32.
  *   epsilon      >= 0 and not NaN.

@@ -362,6 +362,8 @@ b200norm_status check_heads_shape(int64_t batch, int64_t seq, int64_t q, int64_t
     return fail(B200NORM_ERR_UNSUPPORTED, "head_size exceeds 1024, or heads 2^16");
   if (batch > kMaxGrid || seq > kMaxGrid || batch * seq > kMaxGrid)
     return fail(B200NORM_ERR_UNSUPPORTED, "batch * seq exceeds 2^31-1");
+  if (batch * seq * (q + k) > int64_t{1} << 40)
+    return fail(B200NORM_ERR_UNSUPPORTED, "batch * seq * heads exceeds 2^40");
   return B200NORM_OK;
 }
 
@@ -900,7 +902,7 @@ size_t b200norm_head_rms_rotary_grad_workspace_size(int64_t batch, int64_t seq,
   if (check_heads_shape(batch, seq, query_heads, key_heads, head_size, B200NORM_F32, B200NORM_F32))
     return 0;
   if (batch * seq == 0 || query_heads + key_heads == 0) return 0;
-  return head_parts_bytes(head_parts(batch * seq, query_heads, key_heads), head_size);
+  return head_parts_bytes(head_parts(batch * seq, query_heads, key_heads, head_size), head_size);
 }
 
 b200norm_status b200norm_head_rms_rotary_grad(
@@ -984,7 +986,7 @@ b200norm_status b200norm_head_rms_rotary_grad(
     for (int i = 0; i < nfin; ++i) all[n++] = {flat_in[i].p, flat_in[i].bytes, 1, flat_in[i].name, false};
     for (int i = 0; i < nfout; ++i) all[n++] = {flat_out[i].p, flat_out[i].bytes, 1, flat_out[i].name, true};
     const size_t need =
-        head_parts_bytes(head_parts(batch * seq, c.set[0].heads, c.set[1].heads), head_size);
+        head_parts_bytes(head_parts(batch * seq, c.set[0].heads, c.set[1].heads, head_size), head_size);
     if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, all, n)) return st;
     c.part = static_cast<float*>(workspace);
   }

@@ -47,19 +47,22 @@ HeadsPlan plan_heads(const HeadsCall& c, bool gradient) {
   return p;
 }
 
-HeadParts head_parts(int64_t tokens, int64_t q_heads, int64_t k_heads) {
-  // CTAs in proportion to the heads, two for each of 152 SMs while each has a few rows
-  // for every warp
-  const int64_t heads = q_heads + k_heads;
+HeadParts head_parts(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t size) {
+  // CTAs in proportion to the steps that the tensors' rows take (of a 16-bit type's whole
+  // accesses; other layouts are balanced less well), two for each of 152 SMs while a warp
+  // has two steps
+  int64_t rows = 32;
+  while (rows > 1 && rows * size > 32 * 16) rows /= 2;
+  const int64_t q = (q_heads + rows - 1) / rows, k = (k_heads + rows - 1) / rows;
   int64_t all = 152 * 2;
-  const int64_t most = (tokens * heads + 8 * kHeadWarps - 1) / (8 * kHeadWarps);
+  const int64_t most = (tokens * (q + k) + 2 * kHeadWarps - 1) / (2 * kHeadWarps);
   if (all > most) all = most;
   if (all < 2) all = 2;
   if (k_heads == 0) return {static_cast<int>(all), 0};
   if (q_heads == 0) return {0, static_cast<int>(all)};
-  int64_t q = (all * q_heads + heads / 2) / heads;
-  q = q < 1 ? 1 : q > all - 1 ? all - 1 : q;
-  return {static_cast<int>(q), static_cast<int>(all - q)};
+  int64_t part = (all * q + (q + k) / 2) / (q + k);
+  part = part < 1 ? 1 : part > all - 1 ? all - 1 : part;
+  return {static_cast<int>(part), static_cast<int>(all - part)};
 }
 
 cudaError_t launch_heads(const HeadsCall& c, cudaStream_t stream) {
@@ -74,7 +77,7 @@ cudaError_t launch_heads_grad(const HeadsCall& c, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   HeadParts parts = {0, 0};
   if (c.batch * c.seq > 0) {
-    parts = head_parts(c.batch * c.seq, c.set[0].heads, c.set[1].heads);
+    parts = head_parts(c.batch * c.seq, c.set[0].heads, c.set[1].heads, c.size);
     switch (c.t) {
       case DType::F32: e = launch_heads_grad_t<float>(c, stream); break;
       case DType::F16: e = launch_heads_grad_t<__half>(c, stream); break;

@@ -32,8 +32,6 @@ struct HeadsArgs {
   int units, lanes;
   int pitch;       // angles a warp keeps: whole units
   int steps[2];    // per token: the heads in groups of 32 / lanes
-  unsigned splits; // parts of a token's steps, a warp each, of `chunk` steps
-  int chunk;
   int parts[2];    // gradient: CTAs of queries and of keys
   bool whole;      // a unit's pairs are all rotated, or none
 };
@@ -47,11 +45,13 @@ struct HeadRow {
   static constexpr int kStages = 64 * VE * K * sizeof(T) <= 1024 ? 4 : VE * K * sizeof(T) <= 32 ? 3 : 2;
   Pack<T, VE> lo[K][32], hi[K][32];  // [lane]
 };
+constexpr int kHeadStages = 4;  // at most
 
 // Dynamic shared memory: turns per position (8 bytes a pair), gamma widened (queries',
-// keys'), each warp's cosines and sines, and its rows.
+// keys'), each warp's cosines and sines, positions that are on their way with a token's
+// first row, and rows.
 __host__ __device__ inline int head_table_floats(const HeadsArgs& g) {
-  return g.pitch * (2 * (1 + kHeadWarps) + (g.c.norm ? 4 : 0));
+  return g.pitch * (2 * (1 + kHeadWarps) + (g.c.norm ? 4 : 0)) + kHeadWarps * kHeadStages * 2;
 }
 template <typename T, int VE, int K>
 size_t head_smem(const HeadsArgs& g, bool gradient) {
@@ -292,13 +292,17 @@ struct HeadShared {
   unsigned long long* steps;  // [pitch]
   float* gamma;               // [2][2 * pitch]
   float* cosines;             // this warp's [pitch], and its sines behind them
+  long long* position;        // this warp's [stage]
 };
 
 __device__ __forceinline__ HeadShared head_shared(const HeadsArgs& g, unsigned char* raw) {
   HeadShared sh;
   sh.steps = reinterpret_cast<unsigned long long*>(raw);
   sh.gamma = reinterpret_cast<float*>(sh.steps + g.pitch);
-  sh.cosines = sh.gamma + (g.c.norm ? 4 * g.pitch : 0) + (threadIdx.x >> 5) * 2 * g.pitch;
+  float* tables = sh.gamma + (g.c.norm ? 4 * g.pitch : 0);
+  sh.cosines = tables + (threadIdx.x >> 5) * 2 * g.pitch;
+  sh.position = reinterpret_cast<long long*>(tables + kHeadWarps * 2 * g.pitch) +
+                (threadIdx.x >> 5) * kHeadStages;
   return sh;
 }
 
@@ -321,17 +325,26 @@ __device__ __forceinline__ void head_fill(const HeadsArgs& g, const HeadShared& 
   __syncthreads();
 }
 
-__device__ __forceinline__ long long head_position(const HeadsArgs& g, unsigned b, unsigned t) {
-  if (g.c.rot == 0) return 0;
+// A token's position on its way to a stage (lane 0 copies it, the warp reads it).
+__device__ __forceinline__ void head_fetch_position(const HeadsArgs& g, const HeadShared& sh,
+                                                    int stage, unsigned b, unsigned t) {
+  if (g.c.rot == 0 || (threadIdx.x & 31) != 0) return;
   const int64_t at = b * g.c.pos_batch + t * g.c.pos_token;
-  return g.c.pos64 ? static_cast<const long long*>(g.c.positions)[at]
-                   : static_cast<const int*>(g.c.positions)[at];
+  const unsigned dst = smem_addr(sh.position + stage);
+  if (g.c.pos64)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
+                 :: "r"(dst), "l"(static_cast<const long long*>(g.c.positions) + at) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                 :: "r"(dst), "l"(static_cast<const int*>(g.c.positions) + at) : "memory");
 }
 
 // This warp's token: scaled cosines, and sines of the sign wanted; 1 and 0 past the pairs.
-__device__ __forceinline__ void head_angles(const HeadsArgs& g, const HeadShared& sh, long long p,
+__device__ __forceinline__ void head_angles(const HeadsArgs& g, const HeadShared& sh, int stage,
                                             float sine) {
-  __syncwarp();
+  __syncwarp();  // the position is there for all lanes; the angles before are no longer read
+  const long long p =
+      g.c.pos64 ? sh.position[stage] : *reinterpret_cast<const int*>(sh.position + stage);
   for (int n = threadIdx.x & 31; n < g.pitch; n += 32) {
     float c = 1.0f, s = 0.0f;
     if (n < g.c.rot / 2) {
@@ -346,33 +359,38 @@ __device__ __forceinline__ void head_angles(const HeadsArgs& g, const HeadShared
   __syncwarp();
 }
 
-// A warp's item: a token, or a part of its heads.  The next one is a fixed number of items
-// away: no division is made but for the first.
-struct HeadItem {
-  unsigned b, t, split;
+// A warp's share: `left` steps on end of all tokens' steps, the same for every warp but for
+// one; the first is step i of token t of sequence b.
+struct HeadShare {
+  unsigned b, t;
+  int i, left;
 };
 
-__device__ __forceinline__ HeadItem head_item(const HeadsArgs& g, unsigned long long item) {
-  HeadItem r;
-  const unsigned token = static_cast<unsigned>(item / g.splits);
-  r.split = static_cast<unsigned>(item - static_cast<unsigned long long>(token) * g.splits);
-  r.b = token / g.seq;
-  r.t = token - r.b * g.seq;
-  return r;
+__device__ __forceinline__ HeadShare head_share(const HeadsArgs& g, int steps, int64_t warp,
+                                                int64_t warps) {
+  const unsigned long long all = static_cast<unsigned long long>(g.tokens) * steps;
+  const unsigned long long lo = all * warp / warps, hi = all * (warp + 1) / warps;
+  HeadShare s;
+  const unsigned token = steps ? static_cast<unsigned>(lo / steps) : 0;
+  s.i = static_cast<int>(lo - static_cast<unsigned long long>(token) * steps);
+  s.left = static_cast<int>(hi - lo);
+  s.b = token / g.seq;
+  s.t = token - s.b * g.seq;
+  return s;
 }
 
-__device__ __forceinline__ void head_next(const HeadsArgs& g, HeadItem& r, const HeadItem& stride) {
-  r.split += stride.split;
-  r.t += stride.t;
-  r.b += stride.b;
-  if (r.split >= g.splits) {
-    r.split -= g.splits;
-    ++r.t;
+// To the next token, `done` steps on.
+__device__ __forceinline__ void head_next(const HeadsArgs& g, HeadShare& s, int done) {
+  s.left -= done;
+  s.i = 0;
+  if (++s.t == g.seq) {
+    s.t = 0;
+    ++s.b;
   }
-  if (r.t >= g.seq) {
-    r.t -= g.seq;
-    ++r.b;
-  }
+}
+
+__device__ __forceinline__ int head_end(const HeadShare& s, int steps) {
+  return s.left < steps - s.i ? s.i + s.left : steps;
 }
 
 // gamma of a unit's pairs.
@@ -483,16 +501,16 @@ __device__ __forceinline__ void head_factors(const HeadsArgs& g, const HeadShare
   }
 }
 
-// The rows that a warp takes, in order: item by item, step by step, a row of one tensor
-// for each group of lanes.  `p` is this lane's row.
+// What a warp fetches next: step i of its share, a row of one tensor for each group of
+// lanes.  `p` is this lane's row.
 template <typename T>
 struct HeadCursor {
-  unsigned long long item;
-  HeadItem at;
-  int i, last;     // steps of the item
+  HeadShare at;
+  int end;         // of the token's steps
   const T* p;
   int64_t step;    // elements from a step's row to the next
-  int left;        // this lane's rows from here on end at 0 (of the tensor)
+  int left;        // this lane's rows from here on, of the tensor
+  bool fresh;      // a token's first row: its position comes with it
 };
 
 template <typename T, int VE, int K, int LANES, bool NORM>
@@ -509,41 +527,38 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
   const HeadUnits<VE, K> u = head_units<VE, K>(g, sub);
   const int steps = g.steps[0] + g.steps[1];
   const float inv_size = 1.0f / static_cast<float>(g.c.size);
-  const unsigned long long items = static_cast<unsigned long long>(g.tokens) * g.splits;
-  const unsigned long long stride = static_cast<unsigned long long>(gridDim.x) * kHeadWarps;
-  unsigned long long item = static_cast<unsigned long long>(blockIdx.x) * kHeadWarps +
-                            (threadIdx.x >> 5);
+  HeadShare at = head_share(g, steps, static_cast<int64_t>(blockIdx.x) * kHeadWarps + (threadIdx.x >> 5),
+                            static_cast<int64_t>(gridDim.x) * kHeadWarps);
   pdl_wait();
   pdl_trigger();
 
   // what is fetched, some steps ahead of what is worked on
-  const HeadItem hop = head_item(g, stride);
-  HeadItem at = head_item(g, item);
   HeadCursor<T> c;
-  c.item = item;
   c.at = at;
-  auto seek = [&] {  // to step i of the item: queries first, then keys
-    const int n = c.i >= g.steps[0];
+  auto seek = [&] {  // to step i of the token: queries first, then keys
+    const int n = c.at.i >= g.steps[0];
     const HeadSet& set = g.c.set[n];
-    const int64_t h = static_cast<int64_t>(c.i - (n ? g.steps[0] : 0)) * rows + row;
+    const int64_t h = static_cast<int64_t>(c.at.i - (n ? g.steps[0] : 0)) * rows + row;
     c.p = static_cast<const T*>(set.x) + c.at.b * set.xs.batch + c.at.t * set.xs.token +
           h * set.xs.head;
     c.step = rows * set.xs.head;
     c.left = static_cast<int>(set.heads - h);
   };
   auto open = [&] {
-    c.i = static_cast<int>(c.at.split) * g.chunk;
-    c.last = c.i + g.chunk < steps ? c.i + g.chunk : steps;
-    if (c.item < items) seek();
+    c.end = head_end(c.at, steps);
+    c.fresh = true;
+    if (c.at.left > 0) seek();
   };
   auto fetch = [&](int stage) {
-    if (c.item < items) {
+    if (c.at.left > 0) {
       head_fetch<T, VE, K>(ring[stage], c.p, c.left > 0, u);
-      if (++c.i == c.last) {
-        c.item += stride;
-        head_next(g, c.at, hop);
+      if (c.fresh) head_fetch_position(g, sh, stage, c.at.b, c.at.t);
+      c.fresh = false;
+      --c.at.left;
+      if (++c.at.i == c.end) {
+        head_next(g, c.at, 0);
         open();
-      } else if (c.i == g.steps[0]) {
+      } else if (c.at.i == g.steps[0]) {
         seek();
       } else {
         c.p += c.step;
@@ -553,19 +568,14 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
     fetch_commit();
   };
   open();
-  long long position = item < items ? head_position(g, at.b, at.t) : 0;
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch(i);
   head_fill(g, sh);
   int stage = 0;
-  while (item < items) {
-    head_angles(g, sh, position, g.c.inverse ? -g.c.scale : g.c.scale);
-    HeadItem then = at;
-    head_next(g, then, hop);
-    item += stride;
-    if (item < items) position = head_position(g, then.b, then.t);
-    const int begin = static_cast<int>(at.split) * g.chunk;
-    const int end = begin + g.chunk < steps ? begin + g.chunk : steps;
+  while (at.left > 0) {
+    fetch_wait<S - 2>();
+    head_angles(g, sh, stage, g.c.inverse ? -g.c.scale : g.c.scale);
+    const int begin = at.i, end = head_end(at, steps);
 #pragma unroll 1
     for (int n = 0; n < 2; ++n) {
       const HeadSet& set = g.c.set[n];
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
         stage = stage + 1 == S ? 0 : stage + 1;
       }
     }
-    at = then;
+    head_next(g, at, end - begin);
   }
   fetch_wait<0>();
 }
@@ -642,8 +652,9 @@ heads_grad_kernel(const HeadsArgs g) {
   const unsigned part = blockIdx.x - (n ? g.parts[0] : 0);
   const HeadUnits<VE, K> u = head_units<VE, K>(g, sub);
   const float inv_size = 1.0f / static_cast<float>(g.c.size);
-  const unsigned long long items = static_cast<unsigned long long>(g.tokens) * g.splits;
-  const unsigned long long stride = static_cast<unsigned long long>(g.parts[n]) * kHeadWarps;
+  const int steps = g.steps[n];
+  HeadShare at = head_share(g, steps, static_cast<int64_t>(part) * kHeadWarps + warp,
+                            static_cast<int64_t>(g.parts[n]) * kHeadWarps);
   pdl_wait();
   pdl_trigger();
 
@@ -652,20 +663,12 @@ heads_grad_kernel(const HeadsArgs g) {
   const T* pd = nullptr;
   const int64_t step_d = rows * set.dys.head, step_y = rows * set.ys.head;
   c.step = rows * set.xs.head;
-  const HeadItem hop = head_item(g, stride);
-  // to an item with steps (where the other tensor has more heads, a split may have none)
-  auto skip = [&](unsigned long long& item, HeadItem& at) {
-    while (item < items && static_cast<int>(at.split) * g.chunk >= g.steps[n]) {
-      item += stride;
-      head_next(g, at, hop);
-    }
-  };
+  c.at = at;
   auto open = [&] {
-    skip(c.item, c.at);
-    if (c.item >= items) return;
-    c.i = static_cast<int>(c.at.split) * g.chunk;
-    c.last = c.i + g.chunk < g.steps[n] ? c.i + g.chunk : g.steps[n];
-    const int64_t h = static_cast<int64_t>(c.i) * rows + row;
+    c.end = head_end(c.at, steps);
+    c.fresh = true;
+    if (c.at.left <= 0) return;
+    const int64_t h = static_cast<int64_t>(c.at.i) * rows + row;
     c.p = static_cast<const T*>(set.x) + c.at.b * set.xs.batch + c.at.t * set.xs.token +
           h * set.xs.head;
     pd = static_cast<const T*>(set.dy) + c.at.b * set.dys.batch + c.at.t * set.dys.token +
@@ -673,12 +676,14 @@ heads_grad_kernel(const HeadsArgs g) {
     c.left = static_cast<int>(set.heads - h);
   };
   auto fetch = [&](int stage) {
-    if (c.item < items) {
+    if (c.at.left > 0) {
       head_fetch<T, VE, K>(ring[2 * stage], c.p, c.left > 0, u);
       head_fetch<T, VE, K>(ring[2 * stage + 1], pd, c.left > 0, u);
-      if (++c.i == c.last) {
-        c.item += stride;
-        head_next(g, c.at, hop);
+      if (c.fresh) head_fetch_position(g, sh, stage, c.at.b, c.at.t);
+      c.fresh = false;
+      --c.at.left;
+      if (++c.at.i == c.end) {
+        head_next(g, c.at, 0);
         open();
       } else {
         c.p += c.step;
@@ -688,12 +693,7 @@ heads_grad_kernel(const HeadsArgs g) {
     }
     fetch_commit();
   };
-  c.item = static_cast<unsigned long long>(part) * kHeadWarps + warp;
-  c.at = head_item(g, c.item);
   open();
-  unsigned long long item = c.item;
-  HeadItem at = c.at;
-  long long position = item < items ? head_position(g, at.b, at.t) : 0;
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch(i);
   head_fill(g, sh);
@@ -703,15 +703,10 @@ heads_grad_kernel(const HeadsArgs g) {
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int e = 0; e < N; ++e) da[k][e] = db[k][e] = every<V>(0.0f);
-  while (item < items) {
-    head_angles(g, sh, position, g.c.scale);
-    HeadItem then = at;
-    head_next(g, then, hop);
-    item += stride;
-    skip(item, then);
-    if (item < items) position = head_position(g, then.b, then.t);
-    const int first = static_cast<int>(at.split) * g.chunk;
-    const int last = first + g.chunk < g.steps[n] ? first + g.chunk : g.steps[n];
+  while (at.left > 0) {
+    fetch_wait<S - 2>();
+    head_angles(g, sh, stage, g.c.scale);
+    const int first = at.i, last = head_end(at, steps);
     const int64_t h = static_cast<int64_t>(first) * rows + row;
     T* y = static_cast<T*>(set.y) + at.b * set.ys.batch + at.t * set.ys.token + h * set.ys.head;
     int left = static_cast<int>(set.heads - h);
@@ -721,7 +716,7 @@ heads_grad_kernel(const HeadsArgs g) {
       HeadValues<VE, K> x, d;
       head_widen<T, VE, K>(ring[2 * stage], g.c.interleaved, x);
       head_widen<T, VE, K>(ring[2 * stage + 1], g.c.interleaved, d);
-      V sum = every<V>(0.0f), dot = every<V>(0.0f);
+      V sa = every<V>(0.0f), sb = every<V>(0.0f), ta = every<V>(0.0f), tb = every<V>(0.0f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         // turned back; angles and gamma come from shared memory every time: kept in
@@ -735,14 +730,14 @@ heads_grad_kernel(const HeadsArgs g) {
         unit_gamma<VE, K>(sh.gamma + n * 2 * g.pitch, u, k, g.c.interleaved, ga, gb);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          sum = fma2(x.a[k][e], x.a[k][e], sum);
-          dot = fma2(mul2(d.a[k][e], ga[e]), x.a[k][e], dot);
-          sum = fma2(x.b[k][e], x.b[k][e], sum);
-          dot = fma2(mul2(d.b[k][e], gb[e]), x.b[k][e], dot);
+          sa = fma2(x.a[k][e], x.a[k][e], sa);
+          sb = fma2(x.b[k][e], x.b[k][e], sb);
+          ta = fma2(mul2(d.a[k][e], ga[e]), x.a[k][e], ta);
+          tb = fma2(mul2(d.b[k][e], gb[e]), x.b[k][e], tb);
         }
       }
-      const float r = rsqrtf(row_sum<LANES>(total(sum), lanes) * inv_size + g.c.eps);
-      const float m = row_sum<LANES>(total(dot), lanes) * inv_size * r * r;
+      const float r = rsqrtf(row_sum<LANES>(total(add2(sa, sb)), lanes) * inv_size + g.c.eps);
+      const float m = row_sum<LANES>(total(add2(ta, tb)), lanes) * inv_size * r * r;
       const bool in = left > 0;
       // (a lane without a row here has zeros, but r may be infinite for eps 0)
       if (in) {
@@ -767,7 +762,7 @@ heads_grad_kernel(const HeadsArgs g) {
       fetch(stage == 0 ? S - 1 : stage - 1);
       stage = stage + 1 == S ? 0 : stage + 1;
     }
-    at = then;
+    head_next(g, at, last - first);
   }
   fetch_wait<0>();
   if (!set.dgamma) return;

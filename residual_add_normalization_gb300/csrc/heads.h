@@ -52,7 +52,7 @@ HeadsPlan plan_heads(const HeadsCall& c, bool gradient);
 struct HeadParts {
   int q, k;
 };
-HeadParts head_parts(int64_t tokens, int64_t q_heads, int64_t k_heads);
+HeadParts head_parts(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t size);
 inline size_t head_parts_bytes(HeadParts p, int64_t size) {
   return (static_cast<size_t>(p.q + p.k) * size * 4 + 255) / 256 * 256;
 }

@@ -8,9 +8,6 @@
 
 namespace b200norm {
 
-// Warps that a call spreads a token's heads over while the GPU has room.
-constexpr int64_t kHeadFill = 152 * 32;
-
 inline HeadsArgs head_args(const HeadsCall& c, const HeadsPlan& p) {
   HeadsArgs g = {};
   g.c = c;
@@ -23,14 +20,6 @@ inline HeadsArgs head_args(const HeadsCall& c, const HeadsPlan& p) {
   for (int n = 0; n < 2; ++n)
     g.steps[n] = static_cast<int>((c.set[n].heads + rows - 1) / rows);
   return g;
-}
-
-// A token's steps in about `wanted` parts, none empty.
-inline void head_split(HeadsArgs& g, int64_t wanted, int64_t steps) {
-  if (wanted > steps) wanted = steps;
-  if (wanted < 1) wanted = 1;
-  g.chunk = static_cast<int>((steps + wanted - 1) / wanted);
-  g.splits = static_cast<unsigned>((steps + g.chunk - 1) / g.chunk);
 }
 
 template <int N>
@@ -91,9 +80,7 @@ template <typename T>
 cudaError_t launch_heads_t(const HeadsCall& c, cudaStream_t stream) {
   const HeadsPlan p = plan_heads(c, false);
   HeadsArgs g = head_args(c, p);
-  const int64_t all = static_cast<int64_t>(g.steps[0]) + g.steps[1];
-  head_split(g, kHeadFill / g.tokens, all);
-  const int64_t items = static_cast<int64_t>(g.splits) * g.tokens;
+  const int64_t all = (static_cast<int64_t>(g.steps[0]) + g.steps[1]) * g.tokens;
   return with_head_layout<T>(p, [&](auto ve, auto k, auto lanes) {
     constexpr int VE = decltype(ve)::value, K = decltype(k)::value, L = decltype(lanes)::value;
     auto go = [&](auto norm) {
@@ -102,7 +89,7 @@ cudaError_t launch_heads_t(const HeadsCall& c, cudaStream_t stream) {
       g.pitch = p.lanes * K * VE;
       const size_t smem = head_smem<T, VE, K>(g, false);
       if (const cudaError_t e = head_raise(fn, smem, raised)) return e;
-      int64_t grid = (items + kHeadWarps - 1) / kHeadWarps;
+      int64_t grid = (all + kHeadWarps - 1) / kHeadWarps;
       const int64_t most = head_resident(fn, smem);
       if (most > 0 && grid > most) grid = most;
       return launch_clusters(fn, dim3(static_cast<unsigned>(grid)), 32 * kHeadWarps, 1, smem,
@@ -116,13 +103,9 @@ template <typename T>
 cudaError_t launch_heads_grad_t(const HeadsCall& c, cudaStream_t stream) {
   const HeadsPlan p = plan_heads(c, true);
   HeadsArgs g = head_args(c, p);
-  const HeadParts parts = head_parts(g.tokens, c.set[0].heads, c.set[1].heads);
+  const HeadParts parts = head_parts(g.tokens, c.set[0].heads, c.set[1].heads, c.size);
   g.parts[0] = parts.q;
   g.parts[1] = parts.k;
-  // a part's warps take tokens, or parts of a token's heads where there are more warps
-  const int most = g.steps[0] > g.steps[1] ? g.steps[0] : g.steps[1];
-  const int64_t warps = static_cast<int64_t>(parts.q + parts.k) * kHeadWarps;
-  head_split(g, warps / g.tokens, most);
   return with_head_layout<T>(p, [&](auto ve, auto k, auto lanes) {
     constexpr int VE = decltype(ve)::value, K = decltype(k)::value, L = decltype(lanes)::value;
     static std::atomic<unsigned long long> raised{0};

@@ -62,6 +62,7 @@ def test_forward_refusals(lib):
     assert norm(lib, one(heads=-1)) == INVALID
     assert norm(lib, one(heads=(1 << 16) + 1)) == UNSUPPORTED
     assert norm(lib, q, batch=1 << 16, seq=1 << 16) == UNSUPPORTED
+    assert norm(lib, one(heads=1 << 12), batch=1 << 14, seq=1 << 15) == UNSUPPORTED
     assert norm(lib, q, eps=-1.0) == INVALID
     assert norm(lib, q, eps=float("nan")) == INVALID
     assert rotary(lib, q, inverse=2) == INVALID

@@ -14,6 +14,8 @@
  *                        and its gradients
  *   b200norm_linear, b200norm_linear_grad
  *                        y = act(x W^T + b) + residual, and its gradients
+ *   b200norm_gated_linear, b200norm_gated_linear_grad
+ *                        h = act(x Wg^T + bg) * (x Wu^T + bu), and its gradients
  *   b200norm_rotary, b200norm_head_rms_rotary, b200norm_head_rms_rotary_grad
  *                        position rotation of query and key heads, with or
  *                        without an RMS norm of each head, and its gradients
@@ -406,8 +408,60 @@ B200NORM_API b200norm_status b200norm_linear_grad(
     int64_t rows, int64_t in_features, int64_t out_features, b200norm_dtype T, int activation,
     void* workspace, size_t workspace_bytes, b200norm_stream_t stream);
 
+/*
+ * The gated linear operator: two products of the same rows, one of them the other's gate.
+ * With out_features = F:
+ *
+ *   z[r, o] = sum_i x[r, i] * weight[o, i] + bias[o],  o < 2 F
+ *   h[r, o] = round_T(act(z[r, o]) * z[r, F + o]),     o < F
+ *
+ *   x          T, (rows, in_features).
+ *   weight     T, (2 F, in_features): the gate's rows, then those of what it gates.
+ *   bias       T, (2 F), in the same order, or NULL.
+ *   h          T, (rows, F).
+ *   z          T, (rows, 2 F): receives round_T(z) for b200norm_gated_linear_grad; NULL
+ *              when not requested.  h is formed from the unrounded z.
+ *   activation, workspace  as in b200norm_linear (of its own _workspace_size()).
+ *
+ * Limits as in b200norm_linear, with F in [1, 2^19]; rows == 0 is a no-op.
+ */
+B200NORM_API size_t b200norm_gated_linear_workspace_size(int64_t rows, int64_t in_features,
+                                                         int64_t out_features, b200norm_dtype T,
+                                                         int aligned16);
+
+B200NORM_API b200norm_status b200norm_gated_linear(
+    const void* x, const void* weight, const void* bias, void* h, void* z, int64_t rows,
+    int64_t in_features, int64_t out_features, b200norm_dtype T, int activation, void* workspace,
+    size_t workspace_bytes, b200norm_stream_t stream);
+
+/*
+ * Gradients of b200norm_gated_linear:
+ *
+ *   dz[r, o]     = dh[r, o] * z[r, F + o] * act'(z[r, o])
+ *   dz[r, F + o] = dh[r, o] * act(z[r, o])
+ *   dx[r, i] = round_T(sum_o round_T(dz[r, o]) * weight[o, i])
+ *   dw[o, i] = round_T(sum_r round_T(dz[r, o]) * x[r, i])
+ *   db[o]    = round_T(sum_r dz[r, o])
+ *
+ *   dh         T, (rows, F): gradient of h.   z   of the forward call.
+ *   x, weight  as in the forward call; x may be NULL without dw, weight without dx.
+ *   dx, dw, db T, of x's, weight's and bias's shapes; any may be NULL when not wanted.
+ *   workspace  at least b200norm_gated_linear_grad_workspace_size() bytes, as above;
+ *              aligned16: x and weight start on 16-byte boundaries.
+ *
+ * Sums are binary32, in a fixed order.  rows == 0 stores zeros in dw and db.
+ */
+B200NORM_API size_t b200norm_gated_linear_grad_workspace_size(int64_t rows, int64_t in_features,
+                                                              int64_t out_features,
+                                                              b200norm_dtype T, int aligned16);
+
+B200NORM_API b200norm_status b200norm_gated_linear_grad(
+    const void* dh, const void* x, const void* weight, const void* z, void* dx, void* dw, void* db,
+    int64_t rows, int64_t in_features, int64_t out_features, b200norm_dtype T, int activation,
+    void* workspace, size_t workspace_bytes, b200norm_stream_t stream);
+
 /* Synchronise `stream`, then read the device-side record of the linear
- * operator's kernels on the current device.  With 16-bit types their roles wait
+ * operator's kernels (the gated ones as well) on the current device.  With 16-bit types their roles wait
  * on one another through shared memory; the waits are bounded (a second and
  * more for long sums), and one that gives up records
  * B200NORM_ERR_DEVICE_TIMEOUT in a per-device word, with the kind of the first

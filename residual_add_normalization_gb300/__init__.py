@@ -23,6 +23,8 @@ training (gradients are calls of their own, not autograd functions):
   skip_layer_grad   its gradients
   linear            act(x W^T + b) + residual
   linear_grad       its gradients
+  gated_linear      act(x Wg^T + bg) * (x Wu^T + bu)
+  gated_linear_grad its gradients
 
 and on query and key heads, on their way to attention:
 
@@ -42,6 +44,7 @@ import torch
 
 __all__ = ["skip_rms", "skip_rms_stats", "gated_rms", "skip_group", "skip_layer",
            "skip_layer_stats", "skip_layer_grad", "linear", "linear_grad", "linear_status",
+           "gated_linear", "gated_linear_grad",
            "ACTIVATIONS", "rotary", "head_rms_rotary", "head_rms_rotary_grad",
            "rotary_frequencies", "ROTARY_SCALINGS",
            "workspace_size",
@@ -111,6 +114,10 @@ def library() -> ctypes.CDLL:
             "b200norm_linear_status": ([vp], i32),
             "b200norm_linear_grad_workspace_size": ([i64, i64, i64, i32, i32, i32], sz),
             "b200norm_linear_grad": ([vp] * 7 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
+            "b200norm_gated_linear_workspace_size": ([i64, i64, i64, i32, i32], sz),
+            "b200norm_gated_linear": ([vp] * 5 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
+            "b200norm_gated_linear_grad_workspace_size": ([i64, i64, i64, i32, i32], sz),
+            "b200norm_gated_linear_grad": ([vp] * 7 + [i64, i64, i64, i32, i32, vp, sz, vp], i32),
             "b200norm_rotary": ([vp] * 3 + [i64] * 3 + [i32, i32, vp], i32),
             "b200norm_head_rms_rotary": ([vp] * 3 + [i64] * 3 + [i32, i32, f32, vp], i32),
             "b200norm_head_rms_rotary_grad_workspace_size": ([i64] * 5, sz),
@@ -690,10 +697,95 @@ def linear_grad(dy, x, weight, z=None, *, activation=0, want_input=True, want_we
         return run()
 
 
+def _gated_weight(weight, x, index, dtype):
+    n, n_in = _weight(weight, x, index, dtype)
+    if n % 2:
+        raise ValueError("weight must have as many rows for the gate as for what it gates")
+    return n // 2, n_in
+
+
+def gated_linear(x, weight, bias=None, *, activation=1, want_z=False, h=None, z=None,
+                 workspace=None, stream=None):
+    """``act(x @ gate.T + b_gate) * (x @ up.T + b_up)`` over the last axis of ``x``;
+    ``weight`` is (2 out_features, in_features), the rows of ``gate`` before those of
+    ``up``, and ``bias`` in the same order.  ``activation`` is a code of
+    ``ACTIVATIONS`` (SiLU by default).  No autograd graph is made.
+
+    Returns ``(h, z)``; ``z`` (..., 2 out_features), both products as
+    :func:`gated_linear_grad` takes them, is ``None`` unless ``want_z`` or ``z`` is
+    given.
+    """
+    index, dt = _first("x", x)
+    activation = int(activation)
+    n_out, n_in = _gated_weight(weight, x, index, dt)
+    if _last_axis("x", x) != n_in:
+        raise ValueError(f"x's last axis must have weight's in_features ({n_in})")
+    rows = x.numel() // n_in
+    lead = x.shape[:-1]
+    if bias is not None:
+        _vector("bias", bias, 2 * n_out, x, index, dt)
+
+    def run():
+        lib = _lib or library()
+        hv = _new("h", h, lead + (n_out,), x, index)
+        zv = _new("z", z, lead + (2 * n_out,), x, index) if want_z or z is not None else None
+        px, pw, code = x.data_ptr(), weight.data_ptr(), _DTYPES[dt]
+        need = lib.b200norm_gated_linear_workspace_size(rows, n_in, n_out, code,
+                                                        (px | pw) % 16 == 0)
+        raw = _raw_stream(index, stream)
+        ws, n = _scratch(workspace, need, x, index, raw)
+        _check(lib.b200norm_gated_linear(px, pw, _at(bias), hv.data_ptr(), _at(zv), rows, n_in,
+                                         n_out, code, activation, _at(ws), n, raw))
+        return hv, zv
+
+    context = _on(index, stream, (x, weight, bias, h, z, workspace))
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+def gated_linear_grad(dh, x, weight, z, *, activation=1, want_input=True, want_weight=True,
+                      want_bias=True, dx=None, dw=None, db=None, workspace=None, stream=None):
+    """Gradients of :func:`gated_linear`: ``(dx, dw, db)``, the latter two in the order of
+    ``weight``'s rows.  ``z`` is the forward call's.  An output that is not wanted is
+    ``None``; one that is given is wanted.
+    """
+    index, dt = _first("dh", dh)
+    activation = int(activation)
+    n_out, n_in = _gated_weight(weight, dh, index, dt)
+    if _last_axis("dh", dh) != n_out:
+        raise ValueError(f"dh's last axis must have half of weight's rows ({n_out})")
+    rows = dh.numel() // n_out
+    _is("x", x, dh.shape[:-1] + (n_in,), dh, index, dt)
+    _is("z", z, dh.shape[:-1] + (2 * n_out,), dh, index, dt)
+
+    def run():
+        lib = _lib or library()
+        dxv = _like("dx", dx, x, index) if want_input or dx is not None else None
+        dwv = _like("dw", dw, weight, index) if want_weight or dw is not None else None
+        dbv = _new("db", db, (2 * n_out,), dh, index) if want_bias or db is not None else None
+        px, pw, code = x.data_ptr(), weight.data_ptr(), _DTYPES[dt]
+        aligned = ((px if dwv is not None else 0) | (pw if dxv is not None else 0)) % 16 == 0
+        need = lib.b200norm_gated_linear_grad_workspace_size(rows, n_in, n_out, code, aligned)
+        raw = _raw_stream(index, stream)
+        ws, n = _scratch(workspace, need, dh, index, raw)
+        _check(lib.b200norm_gated_linear_grad(dh.data_ptr(), px, pw, z.data_ptr(), _at(dxv),
+                                              _at(dwv), _at(dbv), rows, n_in, n_out, code,
+                                              activation, _at(ws), n, raw))
+        return dxv, dwv, dbv
+
+    context = _on(index, stream, (dh, x, weight, z, dx, dw, db, workspace))
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
 def linear_status(stream=None, device=None):
     """Synchronizes ``stream`` and raises B200NormError if a bounded wait of a
-    ``linear`` / ``linear_grad`` kernel on the device gave up since the last
-    call; the record is then cleared."""
+    kernel of ``linear``, ``gated_linear`` or their gradients on the device gave up
+    since the last call; the record is then cleared."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(dev):
         _check(library().b200norm_linear_status(_stream(dev, stream)))

@@ -226,6 +226,7 @@ b200norm_status check_layer_shape(int64_t rows, int64_t hidden, b200norm_dtype T
 }
 
 constexpr int64_t kMaxFeatures = int64_t{1} << 20;
+constexpr int64_t kMaxGated = kMaxFeatures / 2;
 constexpr int64_t kMaxLinearRows = int64_t{1} << 30;  // tensor copies take int coordinates
 
 b200norm_status check_linear_shape(int64_t rows, int64_t in, int64_t out, b200norm_dtype T,
@@ -239,6 +240,14 @@ b200norm_status check_linear_shape(int64_t rows, int64_t in, int64_t out, b200no
   if (activation < 0 || activation >= kActivations)
     return fail(B200NORM_ERR_INVALID_ARGUMENT,
                 "activation must be 0 (none), 1 (SiLU), 2 (GELU), 3 (GELU, tanh) or 4 (ReLU)");
+  return B200NORM_OK;
+}
+
+b200norm_status check_gated_shape(int64_t rows, int64_t in, int64_t out, b200norm_dtype T,
+                                  int activation) {
+  if (b200norm_status st = check_linear_shape(rows, in, out, T, activation)) return st;
+  if (out > kMaxGated)
+    return fail(B200NORM_ERR_UNSUPPORTED, "out_features of a gated call exceeds 2^19");
   return B200NORM_OK;
 }
 
@@ -859,6 +868,87 @@ b200norm_status b200norm_linear_grad(const void* dy, const void* x, const void* 
   if (e == cudaErrorNotSupported && g_force_linear.cg)
     return fail(B200NORM_ERR_UNSUPPORTED, "forced tiling cannot take this call");
   if (e != cudaSuccess) return cuda_fail(e, "linear_grad launch");
+  return ok();
+}
+
+size_t b200norm_gated_linear_workspace_size(int64_t rows, int64_t in_features,
+                                            int64_t out_features, b200norm_dtype T,
+                                            int aligned16) {
+  if (check_gated_shape(rows, in_features, out_features, T, 0) != B200NORM_OK) return 0;
+  return linear_plan(rows, in_features, 2 * out_features, to_dtype(T), aligned16 != 0).bytes;
+}
+
+b200norm_status b200norm_gated_linear(const void* x, const void* weight, const void* bias, void* h,
+                                      void* z, int64_t rows, int64_t in_features,
+                                      int64_t out_features, b200norm_dtype T, int activation,
+                                      void* workspace, size_t workspace_bytes,
+                                      b200norm_stream_t stream) {
+  if (b200norm_status st = check_gated_shape(rows, in_features, out_features, T, activation))
+    return st;
+  if (rows == 0) return ok();
+  if (!x || !weight || !h)
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "x, weight and h are required");
+  const size_t es = dtype_size(to_dtype(T));
+  const size_t xb = static_cast<size_t>(rows) * in_features * es;
+  const size_t hb = static_cast<size_t>(rows) * out_features * es;
+  const Tensor ts[] = {{x, xb, es, "x", false},
+                       {weight, static_cast<size_t>(2 * out_features) * in_features * es, es,
+                        "weight", false},
+                       {bias, 2 * out_features * es, es, "bias", false}, {h, hb, es, "h", true},
+                       {z, 2 * hb, es, "z", true}};
+  if (b200norm_status st = check_tensors(ts, 5)) return st;
+  const LinearPlan plan =
+      linear_plan(rows, in_features, 2 * out_features, to_dtype(T), all_aligned16(ts, 2));
+  if (b200norm_status st = check_workspace(workspace, workspace_bytes, plan.bytes, ts, 5))
+    return st;
+  LinearCall c{x, weight, bias, nullptr, h, z, rows, in_features, out_features, to_dtype(T),
+               activation, workspace, g_force_linear, true};
+  cudaError_t e = launch_linear(c, plan, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported && g_force_linear.cg)
+    return fail(B200NORM_ERR_UNSUPPORTED, "forced tiling cannot take this call");
+  if (e != cudaSuccess) return cuda_fail(e, "gated_linear launch");
+  return ok();
+}
+
+size_t b200norm_gated_linear_grad_workspace_size(int64_t rows, int64_t in_features,
+                                                 int64_t out_features, b200norm_dtype T,
+                                                 int aligned16) {
+  if (check_gated_shape(rows, in_features, out_features, T, 0) != B200NORM_OK) return 0;
+  return linear_grad_plan(rows, in_features, 2 * out_features, to_dtype(T), kActSilu,
+                          aligned16 != 0).bytes;
+}
+
+b200norm_status b200norm_gated_linear_grad(const void* dh, const void* x, const void* weight,
+                                           const void* z, void* dx, void* dw, void* db,
+                                           int64_t rows, int64_t in_features,
+                                           int64_t out_features, b200norm_dtype T, int activation,
+                                           void* workspace, size_t workspace_bytes,
+                                           b200norm_stream_t stream) {
+  if (b200norm_status st = check_gated_shape(rows, in_features, out_features, T, activation))
+    return st;
+  if (!dx && !dw && !db) return ok();
+  if (rows > 0 && (!dh || !z || (dw && !x) || (dx && !weight)))
+    return fail(B200NORM_ERR_INVALID_ARGUMENT,
+                "dh, z, x (for dw) and weight (for dx) are required");
+  const size_t es = dtype_size(to_dtype(T));
+  const size_t xb = static_cast<size_t>(rows) * in_features * es;
+  const size_t hb = static_cast<size_t>(rows) * out_features * es;
+  const size_t wb = static_cast<size_t>(2 * out_features) * in_features * es;
+  const Tensor ts[] = {{dh, hb, es, "dh", false}, {dw ? x : nullptr, xb, es, "x", false},
+                       {dx ? weight : nullptr, wb, es, "weight", false},
+                       {z, 2 * hb, es, "z", false}, {dx, xb, es, "dx", true},
+                       {dw, wb, es, "dw", true}, {db, 2 * out_features * es, es, "db", true}};
+  if (b200norm_status st = check_tensors(ts, 7)) return st;
+  const LinearGradPlan plan = linear_grad_plan(rows, in_features, 2 * out_features, to_dtype(T),
+                                               kActSilu, all_aligned16(ts + 1, 2));
+  const size_t need = rows > 0 ? plan.bytes : 0;
+  if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, ts, 7)) return st;
+  LinearGradCall c{dh, x, weight, z, dx, dw, db, rows, in_features, out_features, to_dtype(T),
+                   activation, workspace, g_force_linear, true};
+  cudaError_t e = launch_linear_grad(c, plan, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported && g_force_linear.cg)
+    return fail(B200NORM_ERR_UNSUPPORTED, "forced tiling cannot take this call");
+  if (e != cudaSuccess) return cuda_fail(e, "gated_linear_grad launch");
   return ok();
 }
 

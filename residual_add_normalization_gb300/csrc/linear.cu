@@ -5,12 +5,15 @@ namespace b200norm {
 
 extern template cudaError_t launch_rows<float>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<float>(const LinearDzCall&, cudaStream_t);
+extern template cudaError_t launch_gated_dz<float>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_rows<__half>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__half>(const LinearDzCall&, cudaStream_t);
+extern template cudaError_t launch_gated_dz<__half>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_pack<__half>(const void*, void*, int64_t, const void*,
                                       void*, int64_t, int64_t, cudaStream_t);
 extern template cudaError_t launch_rows<__nv_bfloat16>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__nv_bfloat16>(const LinearDzCall&, cudaStream_t);
+extern template cudaError_t launch_gated_dz<__nv_bfloat16>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_pack<__nv_bfloat16>(const void*, void*, int64_t, const void*,
                                              void*, int64_t, int64_t, cudaStream_t);
 
@@ -30,7 +33,7 @@ cudaError_t pack_rows(DType t, const void* src0, void* dst0, int64_t rows0, cons
 cudaError_t launch_product(const Product& p, cudaStream_t stream) {
   const bool mma = mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0;
   if (p.a.k_contiguous && p.b.k_contiguous && !(mma && p.forced.cg) &&
-      few_rows(p.M, p.N, p.K, p.t, mma)) {
+      few_rows(p.M, p.gated ? 2 * p.N : p.N, p.K, p.t, mma)) {
     switch (p.t) {
       case DType::F32: return launch_rows<float>(p, stream);
       case DType::F16: return launch_rows<__half>(p, stream);
@@ -42,11 +45,12 @@ cudaError_t launch_product(const Product& p, cudaStream_t stream) {
   return p.t == DType::F32 ? launch_plain_f32(p, stream) : cudaErrorMisalignedAddress;
 }
 
-cudaError_t launch_linear_dz(const LinearDzCall& c, cudaStream_t stream) {
+cudaError_t launch_linear_dz(const LinearDzCall& c, bool gated, cudaStream_t stream) {
   switch (c.t) {
-    case DType::F32: return launch_dz<float>(c, stream);
-    case DType::F16: return launch_dz<__half>(c, stream);
-    default: return launch_dz<__nv_bfloat16>(c, stream);
+    case DType::F32: return gated ? launch_gated_dz<float>(c, stream) : launch_dz<float>(c, stream);
+    case DType::F16: return gated ? launch_gated_dz<__half>(c, stream) : launch_dz<__half>(c, stream);
+    default:
+      return gated ? launch_gated_dz<__nv_bfloat16>(c, stream) : launch_dz<__nv_bfloat16>(c, stream);
   }
 }
 
@@ -79,48 +83,50 @@ cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStrea
   Operand x{c.x, c.in, true}, w{c.w, c.in, true};
   if (plan.pack) {
     char* ws = static_cast<char*>(c.workspace);
-    const cudaError_t e = pack_rows(c.t, c.x, ws + plan.x, c.rows, c.w, ws + plan.w, c.out, c.in,
-                                    stream);
+    const cudaError_t e = pack_rows(c.t, c.x, ws + plan.x, c.rows, c.w, ws + plan.w,
+                                    c.gated ? 2 * c.out : c.out, c.in, stream);
     if (e != cudaSuccess) return e;
     x = {ws + plan.x, pitch16(c.in), true};
     w = {ws + plan.w, pitch16(c.in), true};
   }
-  const Product p{x, w, c.rows, c.out, c.in, {c.bias, c.residual, c.y, c.z, c.act}, c.t, c.forced};
+  const Product p{x, w, c.rows, c.out, c.in, {c.bias, c.residual, c.y, c.z, c.act}, c.t, c.forced,
+                  c.gated};
   return launch_product(p, stream);
 }
 
 cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& plan,
                                cudaStream_t stream) {
   char* ws = static_cast<char*>(c.workspace);
+  const int64_t out = c.gated ? 2 * c.out : c.out;  // rows of the weight
   void* made = plan.make_dz && (c.dx || c.dw) ? ws + plan.dz : nullptr;
   cudaError_t e = cudaSuccess;
   if (made || c.db) {
     const LinearDzCall d{c.dy, c.z, made, plan.ldz, c.db, reinterpret_cast<float*>(ws + plan.part),
                          c.rows, c.out, c.act, c.t};
-    e = launch_linear_dz(d, stream);
+    e = launch_linear_dz(d, c.gated, stream);
     if (e != cudaSuccess) return e;
   }
   if (plan.pack && c.rows > 0 && (c.dx || c.dw)) {
-    e = pack_rows(c.t, c.x, ws + plan.x, c.dw ? c.rows : 0, c.w, ws + plan.w, c.dx ? c.out : 0,
+    e = pack_rows(c.t, c.x, ws + plan.x, c.dw ? c.rows : 0, c.w, ws + plan.w, c.dx ? out : 0,
                   c.in, stream);
     if (e != cudaSuccess) return e;
   }
   const void* dz = plan.make_dz ? made : c.dy;
-  const int64_t ldz = plan.make_dz ? plan.ldz : c.out;
+  const int64_t ldz = plan.make_dz ? plan.ldz : out;
   if (c.dx && c.rows > 0) {
     Operand w{c.w, c.in, false};
     if (plan.pack) w = {ws + plan.w, pitch16(c.in), false};
-    const Product p{{dz, ldz, true}, w, c.rows, c.in, c.out,
+    const Product p{{dz, ldz, true}, w, c.rows, c.in, out,
                     {nullptr, nullptr, c.dx, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);
     if (e != cudaSuccess) return e;
   }
   if (c.dw && c.rows == 0)  // empty sums: the zero of every type is zero bits
-    return cudaMemsetAsync(c.dw, 0, static_cast<size_t>(c.out) * c.in * dtype_size(c.t), stream);
+    return cudaMemsetAsync(c.dw, 0, static_cast<size_t>(out) * c.in * dtype_size(c.t), stream);
   if (c.dw) {
     Operand x{c.x, c.in, false};
     if (plan.pack) x = {ws + plan.x, pitch16(c.in), false};
-    const Product p{{dz, ldz, false}, x, c.out, c.in, c.rows,
+    const Product p{{dz, ldz, false}, x, out, c.in, c.rows,
                     {nullptr, nullptr, c.dw, nullptr, kActNone}, c.t, c.forced};
     e = launch_product(p, stream);
   }

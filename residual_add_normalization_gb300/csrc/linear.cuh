@@ -100,6 +100,20 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.0f;
 }
 
+// Value and derivative at once: both need the same exponential.
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& value, float& slope) {
+  if constexpr (ACT == kActSilu) {
+    float p, q;
+    sigmoid_pair(z, p, q);
+    value = z * p;
+    slope = fabsf(z) >= 104.0f ? (z > 0.0f ? 1.0f : 0.0f) : p + z * p * q;
+  } else {
+    value = act_value<ACT>(z);
+    slope = act_slope<ACT>(z);
+  }
+}
+
 // f(integral constant) for the activation code, so that loops over elements
 // hold one activation each.
 template <int N>
@@ -184,7 +198,8 @@ __device__ __forceinline__ void copy_async(float* dst, const float* src, int val
 }
 
 // An operand's slice from (i0, k0) on to s[kPlainK][kPitch]; zero past ni and nk.
-template <int TILE, bool KC>
+// GATED: half of the slice is rows i0.. and half ni + i0.. of 2 ni.
+template <int TILE, bool KC, bool GATED = false>
 __device__ __forceinline__ void plain_slice(float* s, const float* p, int64_t ld, bool vec,
                                             int64_t i0, int64_t k0, int64_t ni, int64_t nk) {
   constexpr int kThreads = PlainShape<TILE>::kThreads, kPitch = PlainShape<TILE>::kPitch;
@@ -201,6 +216,13 @@ __device__ __forceinline__ void plain_slice(float* s, const float* p, int64_t ld
   for (int u = 0; u < TILE * kPlainK / kThreads; ++u) {
     const int id = threadIdx.x + u * kThreads;
     const int i = KC ? id / kPlainK : id % TILE, k = KC ? id % kPlainK : id / TILE;
+    if constexpr (GATED) {
+      const int64_t j = i0 + i % (TILE / 2);
+      const bool in = j < ni && k0 + k < nk;
+      copy_async<4>(s + k * kPitch + i,
+                    in ? p + (i < TILE / 2 ? j : ni + j) * ld + k0 + k : p, in ? 4 : 0);
+      continue;
+    }
     const bool in = i0 + i < ni && k0 + k < nk;
     copy_async<4>(s + k * kPitch + i,
                   in ? p + (KC ? (i0 + i) * ld + k0 + k : (k0 + k) * ld + i0 + i) : p, in ? 4 : 0);
@@ -210,9 +232,13 @@ __device__ __forceinline__ void plain_slice(float* s, const float* p, int64_t ld
 // (Registers: left to itself the compiler packs the small tile into 96 and loses a
 // sixth; three CTAs per SM, four for the weight's gradient, measured best.  Two of
 // the large tile cost a few spilled registers and gain a twentieth.)
-template <int TILE, bool A_KC, bool B_KC>
+//
+// GATED: the columns of a tile are half a gate's and half what it gates; with the small
+// tile both meet in shared memory, as the parts of a cluster do.
+template <int TILE, bool A_KC, bool B_KC, bool GATED = false>
 __global__ void __launch_bounds__(PlainShape<TILE>::kThreads, TILE == 128 ? 2 : A_KC ? 3 : 4)
 linear_plain_kernel(const PlainProduct p) {
+  static_assert(!GATED || (A_KC && B_KC), "a gate is of the forward product");
   using S = PlainShape<TILE>;
   constexpr int C = S::kCols, kHalf = TILE / 2;
   extern __shared__ __align__(16) float ring[];
@@ -223,7 +249,7 @@ linear_plain_kernel(const PlainProduct p) {
   const unsigned csize = TILE == 64 ? cluster_size() : 1u;
   const unsigned rank = csize > 1 ? cluster_rank() : 0u;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x / csize) * TILE;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * TILE;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * (GATED ? TILE / 2 : TILE);
   // this CTA's part of K: whole slices
   const int64_t slices = (p.K + kPlainK - 1) / kPlainK;
   const int64_t first = slices * rank / csize, count = slices * (rank + 1) / csize - first;
@@ -234,7 +260,8 @@ linear_plain_kernel(const PlainProduct p) {
       float* st = ring + t % kPlainStages * S::kStage;
       const int64_t k0 = (first + t) * kPlainK;
       plain_slice<TILE, A_KC>(st, a, p.lda, p.a_vec, m0, k0, p.M, p.K);
-      plain_slice<TILE, B_KC>(st + kPlainK * S::kPitch, b, p.ldb, p.b_vec, n0, k0, p.N, p.K);
+      plain_slice<TILE, B_KC, GATED>(st + kPlainK * S::kPitch, b, p.ldb, p.b_vec, n0, k0, p.N,
+                                     p.K);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -300,8 +327,30 @@ linear_plain_kernel(const PlainProduct p) {
       ys[m * p.N + c] = t[j];
     }
   };
+  // the same of a gate's sums and of what it gates
+  auto finish_gated = [&](float(&t)[4], float(&up)[4], int64_t m, int64_t n) {
+    if (m >= p.M) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = n + j;
+      if (c >= p.N) continue;
+      if (bias) {
+        t[j] += bias[c];
+        up[j] += bias[p.N + c];
+      }
+      if (zs) {
+        zs[m * 2 * p.N + c] = t[j];
+        zs[(m * 2 + 1) * p.N + c] = up[j];
+      }
+    }
+    with_act(p.e.act, [&](auto act) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < p.N) ys[m * p.N + n + j] = act_value<decltype(act)::value>(t[j]) * up[j];
+    });
+  };
   if constexpr (TILE == 64) {
-    if (csize > 1) {
+    if (GATED || csize > 1) {
       float* sums = ring;  // [64][64]
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();  // the slices have been read
@@ -310,16 +359,13 @@ linear_plain_kernel(const PlainProduct p) {
         *reinterpret_cast<float4*>(sums + ((i / 4) * kHalf + ty * 4 + i % 4) * 64 + tx * 4) =
             make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
       cluster_sync();
-      const int per = 64 * 16 / static_cast<int>(csize);  // quads of this rank
-      for (int q = threadIdx.x; q < per; q += S::kThreads) {
-        const int at = static_cast<int>(rank) * per + q;
-        float t[4] = {};
+      auto total_of = [&](int place, float(&t)[4]) {  // four sums over the ranks, in order
 #pragma unroll
         for (unsigned c0 = 0; c0 < kMaxSplits; c0 += 4) {
           float4 v[4];
 #pragma unroll
           for (unsigned c = 0; c < 4; ++c)
-            if (c0 + c < csize) v[c] = peer_load4(peer_addr(sums + at * 4, c0 + c));
+            if (c0 + c < csize) v[c] = peer_load4(peer_addr(sums + place, c0 + c));
 #pragma unroll
           for (unsigned c = 0; c < 4; ++c) {
             if (c0 + c >= csize) continue;
@@ -329,11 +375,34 @@ linear_plain_kernel(const PlainProduct p) {
             t[3] += v[c].w;
           }
         }
-        finish(t, m0 + at / 16, n0 + at % 16 * 4);
+      };
+      constexpr int kQuads = GATED ? 8 : 16;  // of a row of the result
+      const int per = 64 * kQuads / static_cast<int>(csize);  // of this rank
+      for (int q = threadIdx.x; q < per; q += S::kThreads) {
+        const int at = static_cast<int>(rank) * per + q;
+        float t[4] = {};
+        total_of(at / kQuads * 64 + at % kQuads * 4, t);
+        if constexpr (GATED) {
+          float up[4] = {};
+          total_of(at / kQuads * 64 + 32 + at % kQuads * 4, up);
+          finish_gated(t, up, m0 + at / kQuads, n0 + at % kQuads * 4);
+        } else {
+          finish(t, m0 + at / kQuads, n0 + at % kQuads * 4);
+        }
       }
       cluster_sync();  // the peers may still read this CTA's sums
       return;
     }
+  }
+  if constexpr (GATED && TILE == 128) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float t[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
+      float up[4] = {acc[i][C / 2 - 2].x, acc[i][C / 2 - 2].y, acc[i][C / 2 - 1].x,
+                     acc[i][C / 2 - 1].y};
+      finish_gated(t, up, m0 + (i / 4) * kHalf + ty * 4 + i % 4, n0 + tx * 4);
+    }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -352,20 +421,23 @@ linear_plain_kernel(const PlainProduct p) {
 // ---------------------------------------------------------------------------
 constexpr int kRowsWarps = 8;
 
-template <typename T, int VE, int R, int NO, int U>
+// GATED: one column, of a gate and of what it gates (NO is 2).
+template <typename T, int VE, int R, int NO, int U, bool GATED = false>
 __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const PlainProduct p) {
+  static_assert(!GATED || NO == 2, "a gate and what it gates");
   pdl_wait();
   pdl_trigger();
   const T* x = static_cast<const T*>(p.a);
   const T* w = static_cast<const T*>(p.b);
   const int lane = threadIdx.x & 31;
   const int64_t n0 =
-      (static_cast<int64_t>(blockIdx.x) * kRowsWarps + (threadIdx.x >> 5)) * NO;
+      (static_cast<int64_t>(blockIdx.x) * kRowsWarps + (threadIdx.x >> 5)) * (GATED ? 1 : NO);
   if (n0 >= p.N) return;
   const int nvec = static_cast<int>(p.K / VE);
   const T* row[NO];
 #pragma unroll
-  for (int o = 0; o < NO; ++o) row[o] = w + (n0 + o < p.N ? n0 + o : p.N - 1) * p.ldb;
+  for (int o = 0; o < NO; ++o)
+    row[o] = w + (GATED ? n0 + o * p.N : n0 + o < p.N ? n0 + o : p.N - 1) * p.ldb;
   // even and odd elements apart, two products per instruction
   float2 acc[R][NO] = {};
   for (int v0 = lane; v0 < nvec; v0 += 32 * U) {
@@ -407,6 +479,23 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
       if (lane == r * NO + o) mine = t;
     }
   const int r = lane / NO;
+  if constexpr (GATED) {
+    float up = __shfl_down_sync(0xffffffffu, mine, 1);
+    if (lane % 2 || r >= R || r >= p.M) return;
+    const T* bias = static_cast<const T*>(p.e.bias);
+    if (bias) {
+      mine += to_f32(bias[n0]);
+      up += to_f32(bias[p.N + n0]);
+    }
+    if (p.e.z) {
+      T* z = static_cast<T*>(p.e.z) + r * 2 * p.N + n0;
+      z[0] = from_f32<T>(mine);
+      z[p.N] = from_f32<T>(up);
+    }
+    with_act(p.e.act, [&](auto act) { mine = act_value<decltype(act)::value>(mine) * up; });
+    static_cast<T*>(p.e.y)[r * p.N + n0] = from_f32<T>(mine);
+    return;
+  }
   const int64_t n = n0 + lane % NO;
   if (r >= R || r >= p.M || n >= p.N) return;
   const int64_t at = r * p.N + n;
@@ -490,6 +579,82 @@ __global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const LinearDz
 #pragma unroll
     for (int w = 0; w < kDzWarps; ++w) t += red[w][i];
     c.part[part * c.out + at] = t;
+  }
+}
+
+// Of a gate and what it gates: dz = [dh * up * act'(gate) | dh * act(gate)], and the column
+// sums of both, in the same way: three reads and two writes per element of the result.
+template <typename T, int VE, int ACT>
+__device__ __forceinline__ void gated_dz_rows(const LinearDzCall& c, int64_t r0, int64_t r1,
+                                              int64_t col, float (&sum)[2][VE]) {
+  const T* dh = static_cast<const T*>(c.dy) + col;
+  const T* z = static_cast<const T*>(c.z) + col;
+  T* dz = static_cast<T*>(c.dz);
+  constexpr int U = 4;  // rows on their way at once
+  for (int64_t r = r0; r < r1; r += U * kDzWarps) {
+    Pack<T, VE> d[U], a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r + u * kDzWarps;
+      if (row >= r1) continue;
+      d[u] = ld_stream<T, VE>(dh + row * c.out);
+      a[u] = ld_stream<T, VE>(z + row * 2 * c.out);
+      b[u] = ld_stream<T, VE>(z + (row * 2 + 1) * c.out);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r + u * kDzWarps;
+      if (row >= r1) continue;
+      float f[VE], gate[VE], up[VE];
+      unpack(d[u], f);
+      unpack(a[u], gate);
+      unpack(b[u], up);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        float value, slope;
+        act_both<ACT>(gate[e], value, slope);
+        gate[e] = __fmul_rn(__fmul_rn(f[e], up[e]), slope);
+        up[e] = __fmul_rn(f[e], value);
+        sum[0][e] = __fadd_rn(sum[0][e], gate[e]);  // same bits without dz
+        sum[1][e] = __fadd_rn(sum[1][e], up[e]);
+      }
+      if (dz) {
+        *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + col) = pack_from<T, VE>(gate);
+        *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + c.out + col) = pack_from<T, VE>(up);
+      }
+    }
+  }
+}
+
+template <typename T, int VE>
+__global__ void __launch_bounds__(32 * kDzWarps) gated_dz_kernel(const LinearDzCall c, int parts) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float red[kDzWarps][32 * VE];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * VE;
+  const int part = blockIdx.y;
+  const int64_t r0 = c.rows * part / parts, r1 = c.rows * (part + 1) / parts;
+  float sum[2][VE] = {};
+  if (col < c.out)
+    with_act(c.act, [&](auto act) {
+      gated_dz_rows<T, VE, decltype(act)::value>(c, r0 + warp, r1, col, sum);
+    });
+  if (!c.db) return;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int e = 0; e < VE; ++e) red[warp][lane * VE + e] = sum[s][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * VE; i += 32 * kDzWarps) {
+      const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 * VE + i;
+      if (at >= c.out) continue;
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kDzWarps; ++w) t += red[w][i];
+      c.part[part * 2 * c.out + s * c.out + at] = t;
+    }
+    __syncthreads();
   }
 }
 

@@ -42,6 +42,9 @@ struct Product {
   Epilogue epi;
   DType t;
   MmaPlan forced;  // by a test (cg 0: automatic)
+  // B has 2 N rows, a gate's and what it gates; C[m, n] = act(z[m, n]) * z[m, N + n] with
+  // z = A B^T + bias (M x 2 N); no residual
+  bool gated = false;
 };
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream);
@@ -54,14 +57,14 @@ inline bool mma_operand_ok(const Operand& o, DType t) {
   return t != DType::F32 && o.ld % 8 == 0 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0;
 }
 
-MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, int sms);
+MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, bool gated, int sms);
 cudaError_t launch_mma(const Product& p, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_mma_t(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
                          cudaStream_t stream);
 
 // Whether a forced plan has a kernel for the product.
-bool mma_plan_ok(const MmaPlan& plan, int64_t M, int64_t K, bool a_kc, bool b_kc);
+bool mma_plan_ok(const MmaPlan& plan, int64_t M, int64_t K, bool a_kc, bool b_kc, bool gated);
 
 // Two words per device: a b200norm_status recorded by a wait that gave up, and
 // its site (nullptr if they cannot be resolved).
@@ -99,8 +102,10 @@ inline int linear_db_parts(int64_t rows, int64_t out) {
   if (p > 1024) p = 1024;
   return static_cast<int>(p < 1 ? 1 : p);
 }
-cudaError_t launch_linear_dz(const LinearDzCall& c, cudaStream_t stream);
+// gated: `out` columns of the result, z and dz with twice as many.
+cudaError_t launch_linear_dz(const LinearDzCall& c, bool gated, cudaStream_t stream);
 
+// gated: y = act(gate) * up of out columns each; weight, bias, z (and db, dw) of both.
 struct LinearCall {
   const void* x;
   const void* w;
@@ -113,6 +118,7 @@ struct LinearCall {
   int act;
   void* workspace;
   MmaPlan forced;
+  bool gated = false;
 };
 
 struct LinearGradCall {
@@ -128,6 +134,7 @@ struct LinearGradCall {
   int act;
   void* workspace;
   MmaPlan forced;
+  bool gated = false;
 };
 
 // What a call keeps in its workspace: offsets, and the bytes in all.  Operands
@@ -157,7 +164,8 @@ struct LinearGradPlan {
   int64_t ldz;
   size_t dz, part, x, w, bytes;
 };
-// aligned16: x and weight (and dy) start on 16-byte boundaries.
+// aligned16: x and weight (and dy) start on 16-byte boundaries.  `out` counts the weight's
+// rows, a gate's and what it gates alike; a gated gradient has an activation (any).
 LinearPlan linear_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);
 LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, int act,
                                 bool aligned16);

@@ -7,5 +7,6 @@ cudaError_t launch_plain_f32(const Product& p, cudaStream_t stream) { return lau
 
 template cudaError_t launch_rows<float>(const Product&, cudaStream_t);
 template cudaError_t launch_dz<float>(const LinearDzCall&, cudaStream_t);
+template cudaError_t launch_gated_dz<float>(const LinearDzCall&, cudaStream_t);
 
 }  // namespace b200norm

@@ -22,9 +22,11 @@ inline PlainProduct plain_args(const Product& p) {
 
 template <int TILE>
 cudaError_t launch_plain_tile(const Product& p, int splits, cudaStream_t stream) {
+  const int cols = p.gated ? TILE / 2 : TILE;
   const dim3 grid(static_cast<unsigned>((p.M + TILE - 1) / TILE * splits),
-                  static_cast<unsigned>((p.N + TILE - 1) / TILE));
-  auto* fn = !p.a.k_contiguous    ? linear_plain_kernel<TILE, false, false>
+                  static_cast<unsigned>((p.N + cols - 1) / cols));
+  auto* fn = p.gated            ? linear_plain_kernel<TILE, true, true, true>
+             : !p.a.k_contiguous    ? linear_plain_kernel<TILE, false, false>
              : p.b.k_contiguous ? linear_plain_kernel<TILE, true, true>
                                 : linear_plain_kernel<TILE, true, false>;
   if (PlainShape<TILE>::kSmem > 48 * 1024) {
@@ -39,10 +41,11 @@ cudaError_t launch_plain_tile(const Product& p, int splits, cudaStream_t stream)
 // float32 products.
 inline cudaError_t launch_plain(const Product& p, cudaStream_t stream) {
   // large tiles once they fill the GPU
-  if ((p.M + 127) / 128 * ((p.N + 127) / 128) >= kPlainLargeTiles)
+  const int64_t N = p.gated ? 2 * p.N : p.N;
+  if ((p.M + 127) / 128 * ((N + 127) / 128) >= kPlainLargeTiles)
     return launch_plain_tile<128>(p, 1, stream);
   // K split while an SM has fewer than four tiles and a part eight slices
-  const int64_t tiles = (p.M + 63) / 64 * ((p.N + 63) / 64);
+  const int64_t tiles = (p.M + 63) / 64 * ((N + 63) / 64);
   int splits = 1;
   while (splits < 8 && tiles * splits * 2 <= 4 * 152 && p.K / (splits * 2) >= 8 * kPlainK)
     splits *= 2;
@@ -57,6 +60,11 @@ cudaError_t launch_rows_ve(const Product& p, cudaStream_t stream) {
     return launch_pdl(fn, dim3(static_cast<unsigned>((p.N + per - 1) / per)), 32 * kRowsWarps,
                       stream, a);
   };
+  if (p.gated) {
+    if (p.M <= 1) return go(linear_rows_kernel<T, VE, 1, 2, 4, true>, 1);
+    if (p.M <= 2) return go(linear_rows_kernel<T, VE, 2, 2, 4, true>, 1);
+    return go(linear_rows_kernel<T, VE, 4, 2, 4, true>, 1);
+  }
   if (p.M <= 1) return go(linear_rows_kernel<T, VE, 1, 1, 8>, 1);
   if (p.M <= 2) return go(linear_rows_kernel<T, VE, 2, 2, 4>, 2);
   return go(linear_rows_kernel<T, VE, 4, 2, 4>, 2);
@@ -87,6 +95,28 @@ cudaError_t launch_dz(const LinearDzCall& c, cudaStream_t stream) {
   if (e == cudaSuccess && c.db)
     e = launch_pdl(linear_db_kernel<T>, dim3(static_cast<unsigned>((c.out + 31) / 32)), 1024,
                    stream, static_cast<const float*>(c.part), static_cast<T*>(c.db), c.out, parts);
+  return e;
+}
+
+// The same of a gate and what it gates: c.out columns of the result, db and dz of both.
+template <typename T>
+cudaError_t launch_gated_dz(const LinearDzCall& c, cudaStream_t stream) {
+  constexpr int VE = 16 / sizeof(T);
+  const int parts = c.rows > 0 ? linear_db_parts(c.rows, 2 * c.out) : 0;
+  cudaError_t e = cudaSuccess;
+  if (parts > 0) {
+    const Operand dh{c.dy, c.out, true}, z{c.z, c.out, true}, dz{c.dz, c.ldz, true};
+    const bool vec =
+        vectors_ok(dh, sizeof(T)) && vectors_ok(z, sizeof(T)) && vectors_ok(dz, sizeof(T));
+    const int cols = 32 * (vec ? VE : 1);
+    const dim3 grid(static_cast<unsigned>((c.out + cols - 1) / cols), parts);
+    e = vec ? launch_pdl(gated_dz_kernel<T, VE>, grid, 32 * kDzWarps, stream, c, parts)
+            : launch_pdl(gated_dz_kernel<T, 1>, grid, 32 * kDzWarps, stream, c, parts);
+  }
+  if (e == cudaSuccess && c.db)
+    e = launch_pdl(linear_db_kernel<T>, dim3(static_cast<unsigned>((2 * c.out + 31) / 32)), 1024,
+                   stream, static_cast<const float*>(c.part), static_cast<T*>(c.db), 2 * c.out,
+                   parts);
   return e;
 }
 

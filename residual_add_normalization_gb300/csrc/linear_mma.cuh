@@ -22,6 +22,10 @@
 // SWAP: C is stored transposed (row = column of C): with few rows of x, the
 // weight's rows fill the 128 lanes and the tokens are the columns.
 //
+// GATED: the weight's rows are those of a gate, then as many of what it gates; a tile
+// holds the same columns of both (half of its B operand each: of a pair, one CTA's
+// half; with SWAP, half of the lanes), and the epilogue stores act(gate) * up.
+//
 // splits > 1: the CTAs of a cluster each take a part of K, and add their sums
 // through distributed shared memory in rank order (no atomics: equal calls give
 // equal bits).
@@ -55,6 +59,7 @@ struct MmaArgs {
   int kblocks;         // 64-deep slices of K
   int tiles_m, tiles_n;
   int splits;
+  int64_t gate;        // GATED: columns of the result (the weight has twice as many rows)
   Epilogue e;
   bool vec;            // rows of the result, bias and residual are whole 16-byte vectors
   unsigned* status;
@@ -66,7 +71,7 @@ struct MmaArgs {
 // Shared memory of a CTA: the ring, then 8 KB for each epilogue warp's results
 // (unless SWAP).  Two small CTAs share an SM.
 constexpr int kMmaStageRows = 32 * 128;  // 32 rows of 64 results, 128 bytes each
-template <int CG, int BN, bool SWAP>
+template <int CG, int BN, bool SWAP, bool GATED = false>
 struct MmaShape {
   static constexpr int kBRows = BN / CG;                 // of B, per CTA
   static constexpr int kBBytes = kBRows * kMmaK * 2;
@@ -74,7 +79,8 @@ struct MmaShape {
   // warps of the epilogue: a quarter of the lanes each, and of the wide tiles
   // half of the columns (with four, 16384 x 512 x 512 bf16 took 15.4 us, 12.6
   // with eight)
-  static constexpr int kWarps = BN >= 128 ? 8 : 4;
+  // (GATED: 64 columns of the result each)
+  static constexpr int kWarps = BN >= (GATED ? 256 : 128) ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kWarps;
   static constexpr int kCols = BN / (kWarps / 4);
   static constexpr int kOut = SWAP ? 0 : kWarps * 2 * kMmaStageRows;
@@ -469,17 +475,209 @@ __device__ __forceinline__ void epilogue_col(const Epilogue& e, int64_t m, int64
   });
 }
 
+// -- epilogue of a gate and what it gates -----------------------------------------
+
+// z from the sums of columns n.., and then act(gate) * up, into `gate`.
+template <typename T, int NC>
+__device__ __forceinline__ void gated_bias(const Epilogue& e, int64_t n, int64_t N,
+                                           float (&gate)[NC], float (&up)[NC]) {
+  const T* bias = static_cast<const T*>(e.bias);
+  if (!bias) return;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (n + i >= N) continue;
+    gate[i] += to_f32(bias[n + i]);
+    up[i] += to_f32(bias[N + n + i]);
+  }
+}
+template <int NC>
+__device__ __forceinline__ void gated_values(const Epilogue& e, float (&gate)[NC],
+                                             const float (&up)[NC]) {
+  with_act(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) gate[i] = act_value<decltype(act)::value>(gate[i]) * up[i];
+  });
+}
+
+// A warp's 32 rows m0.. of a tile, 64 columns n0.. of the result, whole 16-byte vectors,
+// through shared memory as in epilogue_tile; `gate` and `up` are their sums' places.  With z
+// its two parts leave first, from both buffers, and the sums are read once more.
+template <typename T, int ACT, class Drained>
+__device__ __forceinline__ void epilogue_gated(const MmaArgs& g, const CUtensorMap* map_y,
+                                               const CUtensorMap* map_gate,
+                                               const CUtensorMap* map_up, unsigned gate,
+                                               unsigned up, int64_t m0, int64_t n0, int lane,
+                                               unsigned char* stage, unsigned& turn,
+                                               Drained&& drained) {
+  const T* bias = static_cast<const T*>(g.e.bias);
+  const bool some = m0 < g.M && n0 < g.N, keep = g.e.z;
+  unsigned char* at_y = stage + (keep ? 0 : turn * kMmaStageRows);
+  unsigned char* at_up = stage + kMmaStageRows;
+  if (lane == 0 && some) {
+    if (keep) stores_read<0>();
+    else stores_read<1>();
+  }
+  __syncwarp();
+  // f(place of 8 columns in the row's 128 bytes, gate, up) over the 64 columns
+  auto columns = [&](bool last, auto&& f) {
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+      float a[16], b[16];
+      tmem_load16(gate + h * 16, a);
+      tmem_load16(up + h * 16, b);
+      if (last && h == 3) drained();
+      if (!some) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t col = n0 + h * 16 + j * 8;
+        float v[8], w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = a[j * 8 + i];
+          w[i] = b[j * 8 + i];
+        }
+        if (bias && col < g.N) {
+          add_to<T, 8>(v, bias + col);
+          add_to<T, 8>(w, bias + g.N + col);
+        }
+        f(((h * 2 + j) ^ (lane & 7)) * 16 + lane * 128, v, w);
+      }
+    }
+  };
+  if (keep) {
+    columns(false, [&](int at, float(&v)[8], float(&w)[8]) {
+      *reinterpret_cast<Pack<T, 8>*>(stage + at) = pack_from<T, 8>(v);
+      *reinterpret_cast<Pack<T, 8>*>(at_up + at) = pack_from<T, 8>(w);
+    });
+    if (some) {
+      stage_ready();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store(map_gate, stage, static_cast<int>(n0), static_cast<int>(m0));
+        store_commit();
+        tma_store(map_up, at_up, static_cast<int>(n0), static_cast<int>(m0));
+        store_commit();
+        stores_read<1>();
+      }
+      __syncwarp();
+    }
+  }
+  columns(true, [&](int at, float(&v)[8], float(&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_value<ACT>(v[i]) * w[i];
+    *reinterpret_cast<Pack<T, 8>*>(at_y + at) = pack_from<T, 8>(v);
+  });
+  if (!some) return;
+  turn ^= 1;
+  stage_ready();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store(map_y, at_y, static_cast<int>(n0), static_cast<int>(m0));
+    store_commit();
+  }
+}
+
+// The same where rows are not whole vectors: 32 columns of z and of the result at a time are
+// turned around in shared memory, so that a warp's lanes hold neighbouring columns.
+template <typename T, class Drained>
+__device__ __forceinline__ void epilogue_gated_scalar(const MmaArgs& g, unsigned gate, unsigned up,
+                                                      int64_t m0, int64_t n0, int lane,
+                                                      float* stage, Drained&& drained) {
+  const int rows = g.M - m0 < 32 ? (g.M > m0 ? static_cast<int>(g.M - m0) : 0) : 32;
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 32) {
+    float v[32], w[32];
+    tmem_load32(gate + c, v);
+    tmem_load32(up + c, w);
+    if (c == 32) drained();
+    gated_bias<T, 32>(g.e, n0 + c, g.N, v, w);
+    const int64_t n = n0 + c + lane;
+    auto put = [&](float (&f)[32], T* p, int64_t ld) {  // element (m, n) at p[m * ld + n]
+#pragma unroll
+      for (int i = 0; i < 32; ++i) stage[lane * 33 + i] = f[i];
+      __syncwarp();
+      if (n < g.N) {
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) p[(m0 + r) * ld + n] = from_f32<T>(stage[r * 33 + lane]);
+      }
+      __syncwarp();
+    };
+    if (g.e.z) {
+      put(v, static_cast<T*>(g.e.z), 2 * g.N);
+      put(w, static_cast<T*>(g.e.z) + g.N, 2 * g.N);
+    }
+    gated_values<32>(g.e, v, w);
+    put(v, static_cast<T*>(g.e.y), g.N);
+  }
+}
+
+// NC consecutive columns n.. of row m of the result, straight from registers.
+template <typename T, int NC>
+__device__ __forceinline__ void gated_row(const Epilogue& e, bool vec, int64_t m, int64_t n,
+                                          int64_t N, float (&gate)[NC], float (&up)[NC]) {
+  gated_bias<T, NC>(e, n, N, gate, up);
+  T* y = static_cast<T*>(e.y) + m * N + n;
+  T* z = e.z ? static_cast<T*>(e.z) + m * 2 * N + n : nullptr;
+  if (vec && n + NC <= N) {
+    if (z) {
+      *reinterpret_cast<Pack<T, NC>*>(z) = pack_from<T, NC>(gate);
+      *reinterpret_cast<Pack<T, NC>*>(z + N) = pack_from<T, NC>(up);
+    }
+    gated_values<NC>(e, gate, up);
+    *reinterpret_cast<Pack<T, NC>*>(y) = pack_from<T, NC>(gate);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (n + i >= N || !z) continue;
+    z[i] = from_f32<T>(gate[i]);
+    z[N + i] = from_f32<T>(up[i]);
+  }
+  gated_values<NC>(e, gate, up);
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    if (n + i < N) y[i] = from_f32<T>(gate[i]);
+}
+
+// NC consecutive rows (tokens) m.. of column n of the result: lanes hold neighbouring columns.
+template <typename T, int NC>
+__device__ __forceinline__ void gated_col(const Epilogue& e, int64_t m, int64_t M, int64_t n,
+                                          int64_t N, float (&gate)[NC], float (&up)[NC]) {
+  const T* bias = static_cast<const T*>(e.bias);
+  T* y = static_cast<T*>(e.y);
+  T* z = static_cast<T*>(e.z);
+  const float bg = bias ? to_f32(bias[n]) : 0.0f, bu = bias ? to_f32(bias[N + n]) : 0.0f;
+  with_act(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if (m + i >= M) continue;
+      const float a = bias ? gate[i] + bg : gate[i], b = bias ? up[i] + bu : up[i];
+      if (z) {
+        z[(m + i) * 2 * N + n] = from_f32<T>(a);
+        z[((m + i) * 2 + 1) * N + n] = from_f32<T>(b);
+      }
+      y[(m + i) * N + n] = from_f32<T>(act_value<decltype(act)::value>(a) * b);
+    }
+  });
+}
+
 // -- kernel ---------------------------------------------------------------------
 
-template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP>
-__global__ void __launch_bounds__(MmaShape<CG, BN, SWAP>::kThreads)
+// (GATED: map_z is of z's gate columns, map_r of the others.)
+template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false>
+__global__ void __launch_bounds__(MmaShape<CG, BN, SWAP, GATED>::kThreads, GATED ? 1 : 0)
 linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_y,
                   const __grid_constant__ CUtensorMap map_z,
                   const __grid_constant__ CUtensorMap map_r, const MmaArgs g) {
-  using S = MmaShape<CG, BN, SWAP>;
+  using S = MmaShape<CG, BN, SWAP, GATED>;
   constexpr bool kFull = A_KC && B_KC;  // the gradients' products are stored as they are
+  static_assert(!GATED || kFull, "a gate is of the forward product");
+  // a gate and what it gates lie in different lanes: they meet in shared memory
+  constexpr bool kMeet = GATED && SWAP;
+  constexpr int kTileM = kMeet ? kMmaRows / 2 : kMmaRows;  // rows and columns of the result
+  constexpr int kTileN = GATED && !SWAP ? BN / 2 : BN;
   constexpr int kStages = S::kStages;
   constexpr bool kBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   extern __shared__ unsigned char raw[];
@@ -543,8 +741,11 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       for (int t = unit; t < tiles && alive && !g.stall; t += units) {
         int tm, tn;
         tile_at(t, tm, tn);
-        const int m0 = (tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kMmaRows;
-        const int n0 = tn * BN + (CG == 2 ? static_cast<int>(rank) * S::kBRows : 0);
+        const int m0 = (tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kTileM;
+        const int gate = static_cast<int>(g.gate);  // rows of the weight from a gate's to its other
+        const int n0 = GATED && !SWAP
+                           ? tn * kTileN + (CG == 2 ? static_cast<int>(rank) * gate : 0)
+                           : tn * BN + (CG == 2 ? static_cast<int>(rank) * S::kBRows : 0);
         for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
           const int s = it % kStages;
           if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, wait_limit(g, kSiteEmpty))) {
@@ -556,14 +757,20 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           unsigned char* a = ring + s * S::kStageBytes;
           unsigned char* b = a + kMmaABytes;
           const unsigned bar = full0 + s * 8;
-          if constexpr (A_KC) {
+          if constexpr (kMeet) {
+            tma_load<CG>(a, &map_a, kb * kMmaK, m0, bar);
+            tma_load<CG>(a + kMmaABytes / 2, &map_a, kb * kMmaK, gate + m0, bar);
+          } else if constexpr (A_KC) {
             tma_load<CG>(a, &map_a, kb * kMmaK, m0, bar);
           } else {
 #pragma unroll
             for (int i = 0; i < kMmaRows / 64; ++i)
               tma_load<CG>(a + i * 8192, &map_a, m0 + i * 64, kb * kMmaK, bar);
           }
-          if constexpr (B_KC) {
+          if constexpr (GATED && !SWAP && CG == 1) {
+            tma_load<CG>(b, &map_b, kb * kMmaK, n0, bar);
+            tma_load<CG>(b + S::kBBytes / 2, &map_b, kb * kMmaK, gate + n0, bar);
+          } else if constexpr (B_KC) {
             tma_load<CG>(b, &map_b, kb * kMmaK, n0, bar);
           } else {
 #pragma unroll
@@ -631,10 +838,10 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       int tm, tn;
       tile_at(t, tm, tn);
       const int64_t m0 =
-          static_cast<int64_t>(tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kMmaRows;
-      const int64_t n0 = static_cast<int64_t>(tn) * BN;
+          static_cast<int64_t>(tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kTileM;
+      const int64_t n0 = static_cast<int64_t>(tn) * kTileN;
       const unsigned d = tmem + buf * BN + c0 + (static_cast<unsigned>(quarter * 32) << 16);
-      if (g.splits > 1) {
+      if (kMeet || g.splits > 1) {
         // to shared memory (every copy and matrix instruction on it is done),
         // a column of 128 rows after another
         float* mine = reinterpret_cast<float*>(ring);
@@ -666,7 +873,22 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           }
         }
       };
-      if constexpr (SWAP) {
+      if constexpr (GATED) {
+        if constexpr (!SWAP) {
+          const int64_t n = n0 + (warp - 2) / 4 * 64;
+          const unsigned first = d - c0 + (warp - 2) / 4 * 64;
+          if (g.vec) {
+            with_act(g.e.act, [&](auto act) {
+              epilogue_gated<T, decltype(act)::value>(g, &map_y, &map_z, &map_r, first,
+                                                      first + BN / 2, m0 + quarter * 32, n, lane,
+                                                      stage, turn, release);
+            });
+          } else {
+            epilogue_gated_scalar<T>(g, first, first + BN / 2, m0 + quarter * 32, n, lane,
+                                     reinterpret_cast<float*>(stage), release);
+          }
+        }
+      } else if constexpr (SWAP) {
         const int64_t m = m0 + row;
         if constexpr (BN >= 32) {
 #pragma unroll 1
@@ -705,9 +927,59 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
   }
   __syncwarp();
 
-  if (CG == 1 && g.splits > 1) {
+  if (CG == 1 && (kMeet || g.splits > 1)) {
     cluster_sync();
-    if (warp >= 2 && unit < tiles) {
+    if constexpr (GATED) {
+      if (warp >= 2 && unit < tiles) {
+        // this rank's columns of the result, summed over the ranks in order: with SWAP a
+        // thread takes one of the tile's 64 features and half of the tokens, otherwise a row
+        const int row = (warp & 3) * 32 + lane;
+        const int cols = kTileN / g.splits / (SWAP ? 2 : 1);
+        const int c0 = static_cast<int>(rank) * (kTileN / g.splits) + (SWAP ? row / 64 * cols : 0);
+        const int lead = SWAP ? row % 64 : row;                // the gate's place, and
+        const int other = SWAP ? 64 : BN / 2 * kMmaRows;       // the other's from it on
+        int tm, tn;
+        tile_at(unit, tm, tn);
+        const int64_t m = static_cast<int64_t>(tm) * kTileM + lead;
+        const int64_t n0 = static_cast<int64_t>(tn) * kTileN;
+        unsigned peer[kMaxSplits];
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          peer[r] = peer_addr(reinterpret_cast<const float*>(ring) + lead, r < g.splits ? r : 0);
+        auto columns = [&](auto nc) {
+          constexpr int NC = decltype(nc)::value;
+          for (int c = c0; c < c0 + cols; c += NC) {
+            float part[2][kMaxSplits][NC];
+#pragma unroll
+            for (int r = 0; r < kMaxSplits; ++r) {
+              if (r >= g.splits) continue;
+#pragma unroll
+              for (int i = 0; i < NC; ++i) {
+                part[0][r][i] = peer_load(peer[r] + (c + i) * kMmaRows * 4);
+                part[1][r][i] = peer_load(peer[r] + ((c + i) * kMmaRows + other) * 4);
+              }
+            }
+            float v[NC] = {}, w[NC] = {};
+#pragma unroll
+            for (int r = 0; r < kMaxSplits; ++r) {
+              if (r >= g.splits) continue;
+#pragma unroll
+              for (int i = 0; i < NC; ++i) {
+                v[i] += part[0][r][i];
+                w[i] += part[1][r][i];
+              }
+            }
+            if (m < g.M) {
+              if constexpr (SWAP) gated_col<T, NC>(g.e, n0 + c, g.N, m, g.M, v, w);
+              else gated_row<T, NC>(g.e, g.vec, m, n0 + c, g.N, v, w);
+            }
+          }
+        };
+        if (cols % 4 == 0) columns(Const<4>());
+        else if (cols % 2 == 0) columns(Const<2>());
+        else columns(Const<1>());
+      }
+    } else if (warp >= 2 && unit < tiles) {
       // this rank's columns (this warp's share of them), summed over the ranks in
       // order
       const int row = (warp & 3) * 32 + lane;

@@ -8,6 +8,11 @@ template cudaError_t launch_mma_t<__half>(const Product&, const MmaPlan&, int, u
 extern template cudaError_t launch_mma_t<__nv_bfloat16>(const Product&, const MmaPlan&, int,
                                                         unsigned*, cudaStream_t);
 
+extern template cudaError_t launch_mma_gated_t<__half>(const Product&, const MmaPlan&, int,
+                                                       unsigned*, cudaStream_t);
+extern template cudaError_t launch_mma_gated_t<__nv_bfloat16>(const Product&, const MmaPlan&, int,
+                                                              unsigned*, cudaStream_t);
+
 EncodeFn tensor_map_encoder() {
   static std::atomic<EncodeFn> cached{nullptr};
   EncodeFn fn = cached.load();
@@ -66,10 +71,12 @@ unsigned* linear_status_words() {
 // them within a tenth: a slice of 64 of k takes 0.345 us in a pair's 256 x 256
 // tile, 0.30 in a CTA's 128 x 128 and 0.36 in one of two 128 x 64 on an SM; a
 // tile's end that nothing hides 0.8, a launch 3.0, and a sum split over a
-// cluster 2.0 and 0.5 per part.
-MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, int sms) {
+// cluster 2.0 and 0.5 per part.  With a gate a tile has half as many of the result's N
+// columns, and none is 128 x 64.
+MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, bool gated, int sms) {
   const int64_t kblocks = (K + kMmaK - 1) / kMmaK;
-  const int64_t swapped = (N + kMmaRows - 1) / kMmaRows;
+  const int per = gated ? 2 : 1;
+  const int64_t swapped = (N * per + kMmaRows - 1) / kMmaRows;
   // Few rows: the weight's rows fill the lanes.  (For 33 to 64 rows the ordinary
   // form is as fast unless there are few tiles to split K over: 64 x 16384 x 4096
   // 29.8 us against 35.2, but 64 x 4096 x 16384 31.8 against 32.8 without and
@@ -80,16 +87,17 @@ MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, int sms) {
       p.splits *= 2;
     return p;
   }
-  MmaPlan best{1, 64, 1, false};
+  MmaPlan best{1, gated ? 128 : 64, 1, false};
   double least = 0.0;
   const struct {
     int cg, bn, slots, most;
     double slice;
   } shapes[] = {{2, 256, sms / 2, 1, 0.345}, {1, 128, sms, 4, 0.30}, {1, 64, 2 * sms, 8, 0.36}};
-  for (const auto& s : shapes)
+  for (const auto& s : shapes) {
+    if (gated && s.bn == 64) continue;
     for (int splits = 1; splits <= s.most && splits <= kblocks; splits *= 2) {
       const int64_t rows = s.cg * kMmaRows;
-      const int64_t tiles = (M + rows - 1) / rows * ((N + s.bn - 1) / s.bn) * splits;
+      const int64_t tiles = (M + rows - 1) / rows * ((N * per + s.bn - 1) / s.bn) * splits;
       const int64_t waves = (tiles + s.slots - 1) / s.slots;
       const int64_t slices = (kblocks + splits - 1) / splits;
       const double t = 3.0 + static_cast<double>(waves) *
@@ -100,17 +108,18 @@ MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, int sms) {
         best = {s.cg, s.bn, splits, false};
       }
     }
+  }
   return best;
 }
 
-bool mma_plan_ok(const MmaPlan& p, int64_t M, int64_t K, bool a_kc, bool b_kc) {
+bool mma_plan_ok(const MmaPlan& p, int64_t M, int64_t K, bool a_kc, bool b_kc, bool gated) {
   const int64_t kblocks = (K + kMmaK - 1) / kMmaK;
   if (p.splits < 1 || p.splits > 8 || (p.splits & (p.splits - 1)) || p.splits > kblocks)
     return false;
   if (p.swap)
     return a_kc && b_kc && p.cg == 1 && M <= p.bn && (p.bn == 16 || p.bn == 32 || p.bn == 64);
   return (p.cg == 2 && p.bn == 256 && p.splits == 1) ||
-         (p.cg == 1 && (p.bn == 64 || p.bn == 128));
+         (p.cg == 1 && ((p.bn == 64 && !gated) || p.bn == 128));
 }
 
 cudaError_t launch_mma(const Product& p, cudaStream_t stream) {
@@ -122,8 +131,11 @@ cudaError_t launch_mma(const Product& p, cudaStream_t stream) {
   if (!status) return cudaErrorSymbolNotFound;
   const bool a_kc = p.a.k_contiguous, b_kc = p.b.k_contiguous;
   MmaPlan plan = p.forced;
-  if (plan.cg == 0) plan = plan_mma(p.M, p.N, p.K, b_kc, sms);
-  else if (!mma_plan_ok(plan, p.M, p.K, a_kc, b_kc)) return cudaErrorNotSupported;
+  if (plan.cg == 0) plan = plan_mma(p.M, p.N, p.K, b_kc, p.gated, sms);
+  else if (!mma_plan_ok(plan, p.M, p.K, a_kc, b_kc, p.gated)) return cudaErrorNotSupported;
+  if (p.gated)
+    return p.t == DType::F16 ? launch_mma_gated_t<__half>(p, plan, sms, status, stream)
+                             : launch_mma_gated_t<__nv_bfloat16>(p, plan, sms, status, stream);
   return p.t == DType::F16 ? launch_mma_t<__half>(p, plan, sms, status, stream)
                            : launch_mma_t<__nv_bfloat16>(p, plan, sms, status, stream);
 }

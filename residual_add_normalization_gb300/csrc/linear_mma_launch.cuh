@@ -40,19 +40,23 @@ bool encode_operand(CUtensorMap* map, const Operand& o, int64_t n, int64_t k, in
                         : encode_rows<T>(map, o.p, n, k, o.ld, 64);
 }
 
-template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP>
+template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false>
 cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
                              cudaStream_t stream) {
-  using S = MmaShape<CG, BN, SWAP>;
-  auto* fn = linear_mma_kernel<T, CG, BN, A_KC, B_KC, SWAP>;
+  using S = MmaShape<CG, BN, SWAP, GATED>;
+  auto* fn = linear_mma_kernel<T, CG, BN, A_KC, B_KC, SWAP, GATED>;
+  constexpr bool kMeet = GATED && SWAP;
+  constexpr int kTileM = kMeet ? kMmaRows / 2 : kMmaRows;
+  constexpr int kTileN = GATED && !SWAP ? BN / 2 : BN;
   const Operand& a = SWAP ? p.b : p.a;
   const Operand& b = SWAP ? p.a : p.b;
   MmaArgs g;
   g.M = SWAP ? p.N : p.M;
   g.N = SWAP ? p.M : p.N;
   g.kblocks = static_cast<int>((p.K + kMmaK - 1) / kMmaK);
-  g.tiles_m = static_cast<int>((g.M + CG * kMmaRows - 1) / (CG * kMmaRows));
-  g.tiles_n = static_cast<int>((g.N + BN - 1) / BN);
+  g.tiles_m = static_cast<int>((g.M + CG * kTileM - 1) / (CG * kTileM));
+  g.tiles_n = static_cast<int>((g.N + kTileN - 1) / kTileN);
+  g.gate = GATED ? p.N : 0;
   g.splits = plan.splits;
   g.e = p.epi;
   const void* outs[] = {p.epi.y, p.epi.z, p.epi.bias, p.epi.residual};
@@ -68,11 +72,20 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   g.withhold = withhold.site;
   if (g.withhold) g.limit_ns = withhold.limit_ns * kMmaWithheld;
   CUtensorMap map_a, map_b;
-  if (!encode_operand<T>(&map_a, a, g.M, p.K, kMmaRows) ||
-      !encode_operand<T>(&map_b, b, g.N, p.K, S::kBRows))
+  // the weight's rows: twice the result's columns with a gate, in two copies for a CTA
+  const int64_t rows_a = kMeet ? 2 * g.M : g.M, rows_b = GATED && !SWAP ? 2 * g.N : g.N;
+  constexpr int kBoxB = GATED && !SWAP && CG == 1 ? S::kBRows / 2 : S::kBRows;
+  if (!encode_operand<T>(&map_a, a, rows_a, p.K, kTileM) ||
+      !encode_operand<T>(&map_b, b, rows_b, p.K, kBoxB))
     return cudaErrorInvalidValue;
   CUtensorMap map_y = {}, map_z = {}, map_r = {};
-  if (!SWAP && g.vec && g.splits == 1) {  // results go by tensor copies
+  if (GATED && !SWAP && g.vec && g.splits == 1) {
+    T* z = static_cast<T*>(p.epi.z);
+    const bool ok = encode_rows<T>(&map_y, p.epi.y, p.N, p.M, p.N, 32) &&
+                    (!z || (encode_rows<T>(&map_z, z, p.N, p.M, 2 * p.N, 32) &&
+                            encode_rows<T>(&map_r, z + p.N, p.N, p.M, 2 * p.N, 32)));
+    if (!ok) return cudaErrorInvalidValue;
+  } else if (!SWAP && g.vec && g.splits == 1) {  // results go by tensor copies
     const bool ok = encode_rows<T>(&map_y, p.epi.y, p.N, p.M, p.N, 32) &&
                     (!p.epi.z || encode_rows<T>(&map_z, p.epi.z, p.N, p.M, p.N, 32)) &&
                     (!p.epi.residual || encode_rows<T>(&map_r, p.epi.residual, p.N, p.M, p.N, 32));
@@ -94,7 +107,7 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
   const int cluster = CG == 2 ? 2 : g.splits;
   int64_t units = tiles;
-  if (g.splits == 1) {  // persistent: as many as are resident at once
+  if (g.splits == 1 && !kMeet) {  // persistent: as many as are resident at once
     const int64_t most = static_cast<int64_t>(sms) * (BN <= 64 ? 2 : 1) / CG;
     if (units > most) units = most;
   }
@@ -134,6 +147,25 @@ cudaError_t launch_mma_layout(const Product& p, const MmaPlan& plan, int sms, un
   if (plan.bn == 128)
     return launch_mma_shape<T, 1, 128, A_KC, B_KC, false>(p, plan, sms, status, stream);
   return launch_mma_shape<T, 1, 64, A_KC, B_KC, false>(p, plan, sms, status, stream);
+}
+
+// A gate and what it gates.
+template <typename T>
+cudaError_t launch_mma_gated_t(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
+                               cudaStream_t stream) {
+  if (plan.swap) {
+    switch (plan.bn) {
+      case 16:
+        return launch_mma_shape<T, 1, 16, true, true, true, true>(p, plan, sms, status, stream);
+      case 32:
+        return launch_mma_shape<T, 1, 32, true, true, true, true>(p, plan, sms, status, stream);
+      default:
+        return launch_mma_shape<T, 1, 64, true, true, true, true>(p, plan, sms, status, stream);
+    }
+  }
+  if (plan.cg == 2)
+    return launch_mma_shape<T, 2, 256, true, true, false, true>(p, plan, sms, status, stream);
+  return launch_mma_shape<T, 1, 128, true, true, false, true>(p, plan, sms, status, stream);
 }
 
 template <typename T>

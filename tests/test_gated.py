@@ -1,0 +1,301 @@
+"""GPU: the gated linear operator and its gradients against binary64."""
+import time
+
+import pytest
+import torch
+
+import gated_formulas as G
+import residual_add_normalization_gb300 as b2
+from formulas import ACTIVATIONS, DTYPES, assert_within
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = 5
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    yield
+    lib = b2.library()
+    lib.b200norm_testing_force_linear(0, 0, 0, 0)
+    lib.b200norm_testing_linear_stall(0, 0)
+    b2.linear_status()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def tensor(g, shape, t, scale=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(t)
+
+
+def at_odd(t):
+    """The same values one element past a boundary."""
+    base = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    base[1:] = t.flatten()
+    return base[1:].view(t.shape)
+
+
+def check_forward(rows, n_in, n_out, t, act="silu", bias=True, want_z=True, odd=False, seed=1):
+    g = gen(seed)
+    x, w = tensor(g, (rows, n_in), t), tensor(g, (2 * n_out, n_in), t, n_in ** -0.5)
+    b = tensor(g, (2 * n_out,), t, 0.5) if bias else None
+    if odd:
+        x, w = at_odd(x), at_odd(w)
+    h, z = b2.gated_linear(x, w, b, activation=ACTIVATIONS[act], want_z=want_z)
+    (rh, rz), (eh, ez) = G.gated(x.cpu(), w.cpu(), None if b is None else b.cpu(), act)
+    assert_within(h, rh, eh, "h")
+    assert (z is None) == (not want_z)
+    if want_z:
+        assert_within(z, rz, ez, "z")
+        # h does not depend on whether z is wanted
+        assert torch.equal(b2.gated_linear(x, w, b, activation=ACTIVATIONS[act])[0], h)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,n_in,n_out", [
+    (1, 1, 1), (1, 64, 8), (1, 768, 768), (2, 300, 33), (3, 512, 40), (4, 4096, 64),
+    (5, 200, 72), (16, 512, 100), (17, 1027, 130), (33, 256, 264), (64, 512, 512),
+    (65, 128, 72), (129, 64, 200), (130, 96, 1000), (300, 520, 1027), (777, 136, 96)])
+def test_forward(rows, n_in, n_out, t):
+    check_forward(rows, n_in, n_out, DTYPES[t], bias=rows % 2 == 1, want_z=True)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("act", sorted(ACTIVATIONS))
+@pytest.mark.parametrize("rows,n_in,n_out", [(1, 256, 64), (9, 320, 96), (200, 320, 200)])
+def test_activations(rows, n_in, n_out, act, t):
+    check_forward(rows, n_in, n_out, DTYPES[t], act=act, want_z=rows == 9)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,n_in,n_out", [(1, 256, 64), (2, 1000, 3000), (40, 264, 72),
+                                             (300, 72, 136)])
+def test_operands_at_odd_places(rows, n_in, n_out, t):
+    check_forward(rows, n_in, n_out, DTYPES[t], odd=True)
+
+
+TILINGS = ([(2, 256, 1, 0)] + [(1, 128, s, 0) for s in (1, 2, 4, 8)]
+           + [(1, bn, s, 1) for bn in (16, 32, 64) for s in (1, 2, 4, 8)])
+
+
+@pytest.mark.parametrize("tiling", TILINGS)
+@pytest.mark.parametrize("rows,n_in,n_out", [(16, 520, 8), (13, 576, 64), (11, 1000, 300),
+                                             (16, 512, 1096), (7, 640, 131)])
+def test_every_tiling(rows, n_in, n_out, tiling):
+    """Edges of each tiling: the gate's last columns lie next to what it gates, and must not
+    reach it.  (The results of 131 columns are not whole vectors.)"""
+    assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+    check_forward(rows, n_in, n_out, torch.bfloat16, seed=3)
+    check_forward(rows, n_in, n_out, torch.float16, bias=False, want_z=False, seed=4)
+
+
+@pytest.mark.parametrize("tiling", [(2, 256, 1, 0), (1, 128, 1, 0)])
+@pytest.mark.parametrize("rows,n_in,n_out", [(2100, 128, 2056), (1500, 72, 3001)])
+def test_many_tiles(rows, n_in, n_out, tiling):
+    """Several tiles a CTA: both buffers of sums and of results come round again.  In whole
+    numbers, exactly: x and w in {-1, 0, 1}, no activation, |z| at most 128."""
+    assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+    g = gen(5)
+    x, w = (torch.randint(-1, 2, s, generator=g, device="cuda").half()
+            for s in ((rows, n_in), (2 * n_out, n_in)))
+    want = x.float() @ w.float().t()
+    for want_z in (True, False):
+        h, z = b2.gated_linear(x, w, activation=0, want_z=want_z)
+        assert torch.equal(h, (want[:, :n_out] * want[:, n_out:]).half())
+        if want_z:
+            assert torch.equal(z, want.half())
+
+
+def test_a_tiling_without_a_kernel_is_refused():
+    x, w = (torch.ones(s, device="cuda").bfloat16() for s in ((40, 64), (128, 64)))
+    for tiling in ((1, 64, 1, 0), (1, 16, 1, 1), (2, 256, 2, 0)):
+        assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+        with pytest.raises(b2.B200NormError):
+            b2.gated_linear(x, w)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("rows,n_in,n_out", [(1, 64, 8), (3, 100, 33), (64, 128, 72),
+                                             (130, 256, 320), (333, 77, 131)])
+def test_gradient(rows, n_in, n_out, act, t):
+    g = gen(6)
+    x, w = tensor(g, (rows, n_in), DTYPES[t]), tensor(g, (2 * n_out, n_in), DTYPES[t], n_in ** -0.5)
+    dh, z = tensor(g, (rows, n_out), DTYPES[t], 0.3), tensor(g, (rows, 2 * n_out), DTYPES[t], 2.0)
+    got = b2.gated_linear_grad(dh, x, w, z, activation=ACTIVATIONS[act])
+    ref, bound = G.gated_grad(dh.cpu(), x.cpu(), w.cpu(), z.cpu(), act)
+    for a, r, e, name in zip(got, ref, bound, ("dx", "dw", "db")):
+        assert_within(a, r, e, name)
+    for i, one in enumerate((dict(want_weight=False, want_bias=False),
+                             dict(want_input=False, want_bias=False),
+                             dict(want_input=False, want_weight=False))):
+        alone = b2.gated_linear_grad(dh, x, w, z, activation=ACTIVATIONS[act], **one)
+        assert torch.equal(alone[i], got[i])
+        assert sum(v is not None for v in alone) == 1
+
+
+@pytest.mark.parametrize("act", sorted(ACTIVATIONS))
+def test_slopes(act):
+    """dz element by element: a row a token, the weight a unit matrix, so that dx is dz's
+    rows; over the whole range of gates."""
+    n = 64
+    gate = torch.cat((torch.linspace(-120, 120, 4001), torch.linspace(-6, 6, 4000)))
+    rows = gate.numel() // 3
+    g = gen(7)
+    z = torch.randn(rows, 2 * n, generator=g, device="cuda")
+    z[:, :3] = gate[:rows * 3].view(rows, 3).cuda()
+    dh = torch.randn(rows, n, generator=g, device="cuda")
+    w = torch.eye(2 * n, device="cuda")
+    dx, _, _ = b2.gated_linear_grad(dh, w[:1].expand(rows, -1).contiguous(), w, z,
+                                    activation=ACTIVATIONS[act], want_weight=False,
+                                    want_bias=False)
+    dz, e = G.dz_of(dh.cpu(), z.cpu(), act)
+    assert_within(dx, dz, e, "dz")
+
+
+def test_gradient_against_differences():
+    g = gen(8)
+    x, w = tensor(g, (3, 6), torch.float32), tensor(g, (10, 6), torch.float32)
+    b, dh = tensor(g, (10,), torch.float32), tensor(g, (3, 5), torch.float32)
+    h, z = b2.gated_linear(x, w, b, want_z=True)
+    dx, dw, db = b2.gated_linear_grad(dh, x, w, z)
+    args = [v.cpu().double() for v in (x, w, b)]
+
+    def loss(v):
+        return float((G.gated(*v, "silu")[0][0] * dh.cpu().double()).sum())
+    step = 1e-5
+    for which, got in enumerate((dx, dw, db)):
+        for at in [(0,) * got.dim(), tuple(s - 1 for s in got.shape)]:
+            up, down = [[v.clone() for v in args] for _ in range(2)]
+            up[which][at] += step
+            down[which][at] -= step
+            want = (loss(up) - loss(down)) / (2 * step)
+            assert abs(float(got[at]) - want) <= 1e-5 * (1 + abs(want))
+
+
+def test_nothing_there():
+    w = torch.ones(16, 8, device="cuda")
+    x = torch.ones(0, 8, device="cuda")
+    h, z = b2.gated_linear(x, w, want_z=True)
+    assert h.shape == (0, 8) and z.shape == (0, 16)
+    dx, dw, db = b2.gated_linear_grad(h, x, w, z)
+    assert dx.shape == x.shape and bool((dw == 0).all()) and bool((db == 0).all())
+    x3 = torch.randn(2, 3, 8, device="cuda")
+    h, z = b2.gated_linear(x3, w, want_z=True)
+    assert h.shape == (2, 3, 8) and z.shape == (2, 3, 16)
+    assert b2.gated_linear_grad(h, x3, w, z)[0].shape == x3.shape
+
+
+@pytest.mark.parametrize("rows", [1, 40, 300])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_nan_stays_in_its_row_and_column(rows, t):
+    g = gen(9)
+    x, w = tensor(g, (rows, 200), DTYPES[t]), tensor(g, (240, 200), DTYPES[t], 0.1)
+    clean, _ = b2.gated_linear(x, w)
+    bad = w.clone()
+    bad[7, 3] = float("nan")        # a gate's row
+    bad[120 + 50, 9] = float("inf")  # a row of what it gates
+    h, _ = b2.gated_linear(x, bad)
+    keep = [i for i in range(120) if i not in (7, 50)]
+    assert torch.equal(h[:, keep], clean[:, keep])
+    assert bool(torch.isnan(h[:, 7]).all()) and not bool(torch.isfinite(h[:, 50]).any())
+    if rows > 1:
+        xb = x.clone()
+        xb[rows // 2, 0] = float("nan")
+        h, _ = b2.gated_linear(xb, w)
+        rest = torch.arange(rows) != rows // 2
+        assert torch.equal(h[rest.cuda()], clean[rest.cuda()])
+        assert bool(torch.isnan(h[rows // 2]).all())
+
+
+def test_equal_calls_give_equal_bits():
+    g = gen(10)
+    for rows, n_in, n_out, t in ((1, 4096, 512, "bf16"), (300, 1024, 520, "bf16"),
+                                 (50, 512, 300, "f32"), (4000, 320, 264, "f16")):
+        x, w = tensor(g, (rows, n_in), DTYPES[t]), tensor(g, (2 * n_out, n_in), DTYPES[t], 0.05)
+        first = b2.gated_linear(x, w, want_z=True)
+        grads = b2.gated_linear_grad(first[0], x, w, first[1])
+        for _ in range(3):
+            again = b2.gated_linear(x, w, want_z=True)
+            assert all(torch.equal(a, b) for a, b in zip(first, again))
+            assert all(torch.equal(a, b) for a, b in
+                       zip(grads, b2.gated_linear_grad(first[0], x, w, first[1])))
+
+
+@pytest.mark.parametrize("tiling", [(2, 256, 1, 0), (1, 128, 1, 0), (1, 128, 4, 0), (1, 16, 1, 1),
+                                    (1, 16, 2, 1)])
+def test_waits_give_up(tiling):
+    """With nothing copied, the roles' waits run out: the call returns, the status says so
+    once, and the next call is right."""
+    lib = b2.library()
+    g = gen(11)
+    x, w = tensor(g, (16, 1024), torch.bfloat16), tensor(g, (600, 1024), torch.bfloat16)
+    assert lib.b200norm_testing_force_linear(*tiling) == 0
+    want, _ = b2.gated_linear(x, w)
+    b2.linear_status()
+    assert lib.b200norm_testing_linear_stall(1, 20_000_000) == 0
+    t0 = time.monotonic()
+    b2.gated_linear(x, w)
+    with pytest.raises(b2.B200NormError) as e:
+        b2.linear_status()
+    assert e.value.status == TIMEOUT and time.monotonic() - t0 < 2.0
+    assert lib.b200norm_testing_linear_stall(0, 0) == 0
+    assert torch.equal(b2.gated_linear(x, w)[0], want)
+
+
+def test_captured_and_replayed():
+    """Two graphs, with scratch of their own (operands that are copied to aligned rows), give
+    the eager call's bits with new inputs."""
+    g = gen(12)
+    x, w = tensor(g, (50, 131), torch.float16), tensor(g, (2 * 67, 131), torch.float16, 0.1)
+    b2.gated_linear_grad(*[b2.gated_linear(x, w)[0], x, w, b2.gated_linear(x, w, want_z=True)[1]])
+
+    def step():
+        h, z = b2.gated_linear(x, w, want_z=True)
+        return (h, z) + b2.gated_linear_grad(h, x, w, z)
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for one in graphs:
+        with torch.cuda.graph(one):
+            outs.append(step())
+    for seed in (1, 2):
+        x.copy_(tensor(gen(seed), (50, 131), torch.float16))
+        for one in graphs:
+            one.replay()
+        want = step()
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_another_stream_and_given_outputs():
+    g = gen(13)
+    x, w = tensor(g, (70, 256), torch.bfloat16), tensor(g, (192, 256), torch.bfloat16, 0.1)
+    want = b2.gated_linear(x, w, want_z=True)
+    grads = b2.gated_linear_grad(want[0], x, w, want[1])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    h, z = torch.empty_like(want[0]), torch.empty_like(want[1])
+    got = b2.gated_linear(x, w, h=h, z=z, stream=st)
+    gg = b2.gated_linear_grad(want[0], x, w, want[1], stream=st)
+    torch.cuda.current_stream().wait_stream(st)
+    assert got[0] is h and got[1] is z
+    assert torch.equal(h, want[0]) and torch.equal(z, want[1])
+    assert all(torch.equal(a, b) for a, b in zip(gg, grads))
+
+
+def test_results_past_2_31_elements():
+    """z of more than 2^31 elements: its last rows against the same rows by themselves."""
+    rows, n_in, n_out = (1 << 31) // 16384 + 300, 64, 8192
+    g = gen(14)
+    x, w = tensor(g, (rows, n_in), torch.bfloat16), tensor(g, (2 * n_out, n_in), torch.bfloat16, 0.1)
+    h, z = b2.gated_linear(x, w, want_z=True)
+    last, lz = b2.gated_linear(x[-300:].contiguous(), w, want_z=True)
+    dx, _, _ = b2.gated_linear_grad(h, x, w, z, want_weight=False, want_bias=False)
+    d, _, _ = b2.gated_linear_grad(last, x[-300:].contiguous(), w, lz, want_weight=False,
+                                   want_bias=False)
+    # other tilings, so other orders of the sums: a last place (2^-7 at most, relative) turned
+    # here and there; wrong rows would be off by their whole size
+    for a, b in ((h[-300:], last), (z[-300:], lz), (dx[-300:], d)):
+        assert float((a.float() - b.float()).norm() / b.float().norm()) <= 2.0 ** -8

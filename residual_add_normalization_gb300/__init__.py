@@ -826,29 +826,46 @@ def rotary_frequencies(rotary_size, base=10000.0, *, scaling=0, factor=1.0, orig
     return torch.tensor(list(out), dtype=torch.float64).to(device)
 
 
-def _heads(name, t, x, index, dtype):
-    """``t``, heads of x's leading shape and head size, with any steps between heads."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index):
-        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.dtype in _DTYPES:
-            if t.dtype is not dtype:
-                raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-        _cuda(name, t)
-    shape = t.shape
-    if len(shape) not in (3, 4) or shape[:-2] != x.shape[:-2] or shape[-1] != x.shape[-1]:
-        raise ValueError(f"{name} must have shape (..., heads, head_size) with one or two leading "
-                         f"axes, the same for all (got {tuple(shape)})")
-    if t.stride(-1) != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}'s elements must be next to one another in a head")
-    return t
+def _heads(name, t, lead, size, index, dtype):
+    """(heads, their steps): of ``t``, heads of that leading shape and size, with any steps
+    between them."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index:
+        shape, st = t.shape, t.stride()
+        if len(lead) == 2:
+            if (len(shape) == 4 and shape[3] == size and shape[0] == lead[0]
+                    and shape[1] == lead[1] and (st[3] == 1 or size == 1)):
+                return shape[2], st[0], st[1], st[2]
+        elif (len(shape) == 3 and shape[2] == size and shape[0] == lead[0]
+              and (st[2] == 1 or size == 1)):
+            return shape[1], 0, st[0], st[1]
+        if shape[:-2] == lead and shape[-1] == size:
+            raise ValueError(f"{name}'s elements must be next to one another in a head")
+        raise ValueError(f"{name} must have shape {tuple(lead)} + (heads, {size}) "
+                         f"(got {tuple(shape)})")
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPES:
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    _cuda(name, t)
+    raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
-def _head_steps(t):
-    s = t.stride()
-    return s[:3] if len(s) == 4 else (0, s[0], s[1])
+def _heads_like(name, t, lead, size, heads, index, dtype):
+    """The steps of ``t``, with that many heads."""
+    n, *steps = _heads(name, t, lead, size, index, dtype)
+    if n != heads:
+        raise ValueError(f"{name} must have {heads} heads (got {n})")
+    return steps
 
 
-def _positions(positions, inv_freq, x, index, interleaved, scale):
+def _new_heads(lead, heads, size, x, dtype):
+    """New heads, dense, and their steps."""
+    t = torch.empty((*lead, heads, size), dtype=dtype, device=x.device)
+    row = heads * size
+    return t, (lead[1] * row if len(lead) == 2 else 0, row, size)
+
+
+def _rotation(positions, inv_freq, lead, index, interleaved, scale):
     """The C rotation."""
     if inv_freq is None:
         if positions is not None:
@@ -857,47 +874,53 @@ def _positions(positions, inv_freq, x, index, interleaved, scale):
     if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float64):
         raise TypeError("inv_freq must be a float64 torch.Tensor")
     if inv_freq.get_device() != index or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError(f"inv_freq must be contiguous, of one axis, on {x.device}")
-    if not (isinstance(positions, torch.Tensor) and positions.dtype in (torch.int64, torch.int32)):
+        raise ValueError(f"inv_freq must be contiguous, of one axis, on cuda:{index}")
+    wide = isinstance(positions, torch.Tensor) and positions.dtype is torch.int64
+    if not wide and not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32):
         raise TypeError("positions must be an int64 or int32 torch.Tensor")
     if positions.get_device() != index:
-        raise ValueError(f"positions is on {positions.device}, expected {x.device}")
-    lead = x.shape[:-2]
-    if positions.shape == lead:
-        steps = positions.stride() if len(lead) == 2 else (0, positions.stride(0))
-    elif len(lead) == 2 and positions.shape == lead[1:]:
-        steps = (0, positions.stride(0))
+        raise ValueError(f"positions is on {positions.device}, expected cuda:{index}")
+    shape, st = positions.shape, positions.stride()
+    if shape == lead:
+        b, s = st if len(st) == 2 else (0, st[0])
+    elif len(lead) == 2 and shape == lead[1:]:
+        b, s = 0, st[0]
     else:
         raise ValueError(f"positions must have shape {tuple(lead)}"
                          + (f" or {tuple(lead[1:])}" if len(lead) == 2 else "")
-                         + f" (got {tuple(positions.shape)})")
-    return _ROTATION.pack(positions.data_ptr(), positions.element_size(), *steps,
-                          inv_freq.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0,
-                          scale)
+                         + f" (got {tuple(shape)})")
+    return _ROTATION.pack(positions.data_ptr(), 8 if wide else 4, b, s, inv_freq.data_ptr(),
+                          2 * inv_freq.numel(), 1 if interleaved else 0, scale)
 
 
-def _first_heads(tensors):
-    """(the first tensor of heads that is given, index of its device, type)."""
-    for name, t in tensors:
-        if t is not None:
-            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPES):
-                _cuda(name, t)
-            if t.dim() not in (3, 4) or t.shape[-1] < 1:
-                raise ValueError(f"{name} must have shape (..., heads, head_size) with one or two "
-                                 f"leading axes (got {tuple(t.shape)})")
-            return t, t.get_device(), t.dtype
-    raise ValueError("queries or keys are needed")
+def _first_heads(q, k):
+    """(queries, or keys without them; their leading shape and size, device index, type)."""
+    x, name = (q, "q") if q is not None else (k, "k")
+    if x is None:
+        raise ValueError("queries or keys are needed")
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _DTYPES):
+        _cuda(name, x)
+    shape = x.shape
+    if len(shape) not in (3, 4) or shape[-1] < 1:
+        raise ValueError(f"{name} must have shape (..., heads, head_size) with one or two leading "
+                         f"axes (got {tuple(shape)})")
+    return x, shape[:-2], shape[-1], x.get_device(), x.dtype
 
 
-def _gammas(q, gamma_q, k, gamma_k, x, index):
+def _gammas(q, gamma_q, k, gamma_k, size, x, index):
     """The type of both gammas (x's without any)."""
+    if (gamma_q is not None and gamma_k is not None and q is not None and k is not None
+            and gamma_q.dtype is gamma_k.dtype):
+        _weights("gamma_q", gamma_q, size, x, index)
+        _weights("gamma_k", gamma_k, size, x, index)
+        return gamma_q.dtype
     m = None
     for name, heads, gamma in (("gamma_q", q, gamma_q), ("gamma_k", k, gamma_k)):
         if gamma is None:
             continue
         if heads is None:
             raise ValueError(f"{name} needs its heads")
-        _weights(name, gamma, x.shape[-1], x, index)
+        _weights(name, gamma, size, x, index)
         if m is not None and gamma.dtype is not m:
             raise TypeError("gamma_q and gamma_k must be of one type")
         m = gamma.dtype
@@ -906,38 +929,46 @@ def _gammas(q, gamma_q, k, gamma_k, x, index):
 
 def _rotated(norm, q, k, gamma_q, gamma_k, positions, inv_freq, epsilon, interleaved, inverse,
              scale, q_out, k_out, stream):
-    x, index, dt = _first_heads((("q", q), ("k", k)))
-    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
-        if t is not None:
-            _heads(name, t, x, index, dt)
-        if o is not None:
-            if t is None:
-                raise ValueError(f"{name}_out needs {name}")
-            if _heads(name + "_out", o, x, index, dt).shape != t.shape:
-                raise ValueError(f"{name}_out must have shape {tuple(t.shape)} "
-                                 f"(got {tuple(o.shape)})")
-    m = _gammas(q, gamma_q, k, gamma_k, x, index) if norm else dt
-    rotation = _positions(positions, inv_freq, x, index, interleaved, scale)
-    batch, seq = x.shape[:2] if x.dim() == 4 else (1, x.shape[0])
+    x, lead, size, index, dt = _first_heads(q, k)
+    q_at = k_at = qo_at = ko_at = None
+    if q is not None:
+        q_at = _heads("q", q, lead, size, index, dt)
+    if k is not None:
+        k_at = _heads("k", k, lead, size, index, dt)
+    if q_out is not None:
+        if q is None:
+            raise ValueError("q_out needs q")
+        qo_at = _heads_like("q_out", q_out, lead, size, q_at[0], index, dt)
+    if k_out is not None:
+        if k is None:
+            raise ValueError("k_out needs k")
+        ko_at = _heads_like("k_out", k_out, lead, size, k_at[0], index, dt)
+    m = _gammas(q, gamma_q, k, gamma_k, size, x, index) if norm else dt
+    rotation = _rotation(positions, inv_freq, lead, index, interleaved, scale)
 
     def run():
-        outs = [None, None]
-        args = [None, None]
-        for i, (t, gamma, o) in enumerate(((q, gamma_q, q_out), (k, gamma_k, k_out))):
-            if t is None:
-                continue
-            outs[i] = torch.empty(t.shape, dtype=dt, device=t.device) if o is None else o
-            args[i] = _HEADS.pack(t.data_ptr(), outs[i].data_ptr(), _at(gamma) or 0, t.shape[-2],
-                                  *_head_steps(t), *_head_steps(outs[i]))
-        lib = _lib or library()
-        raw = _raw_stream(index, stream)
+        a = b = None
+        qo, ko, qs, ks = q_out, k_out, qo_at, ko_at
+        if q is not None:
+            if qo is None:
+                qo, qs = _new_heads(lead, q_at[0], size, x, dt)
+            a = _HEADS.pack(q.data_ptr(), qo.data_ptr(),
+                            0 if gamma_q is None else gamma_q.data_ptr(), *q_at, *qs)
+        if k is not None:
+            if ko is None:
+                ko, ks = _new_heads(lead, k_at[0], size, x, dt)
+            b = _HEADS.pack(k.data_ptr(), ko.data_ptr(),
+                            0 if gamma_k is None else gamma_k.data_ptr(), *k_at, *ks)
+        batch, seq = lead if len(lead) == 2 else (1, lead[0])
         if norm:
-            _check(lib.b200norm_head_rms_rotary(*args, rotation, batch, seq, x.shape[-1],
-                                                _DTYPES[dt], _DTYPES[m], float(epsilon), raw))
+            _check((_lib or library()).b200norm_head_rms_rotary(
+                a, b, rotation, batch, seq, size, _DTYPES[dt], _DTYPES[m], float(epsilon),
+                _raw_stream(index, stream)))
         else:
-            _check(lib.b200norm_rotary(*args, rotation, batch, seq, x.shape[-1], _DTYPES[dt],
-                                       1 if inverse else 0, raw))
-        return tuple(outs)
+            _check((_lib or library()).b200norm_rotary(
+                a, b, rotation, batch, seq, size, _DTYPES[dt], 1 if inverse else 0,
+                _raw_stream(index, stream)))
+        return qo, ko
 
     context = _on(index, stream, (q, k, gamma_q, gamma_k, positions, inv_freq, q_out, k_out))
     if context is None:
@@ -990,7 +1021,7 @@ def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *,
     wanted is ``None``; one that is given is wanted; a gamma of ``None`` has no
     gradient.
     """
-    x, index, dt = _first_heads((("q", q), ("k", k)))
+    x, lead, size, index, dt = _first_heads(q, k)
     sets = []
     for name, t, d, gamma, o, dg in (("q", q, dq, gamma_q, dq_out, dgamma_q),
                                      ("k", k, dk, gamma_k, dk_out, dgamma_k)):
@@ -999,18 +1030,15 @@ def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *,
                 raise ValueError(f"d{name}, d{name}_out and dgamma_{name} need {name}")
             sets.append(None)
             continue
-        _heads(name, t, x, index, dt)
-        for n, v in (("d" + name, d), (f"d{name}_out", o)):
-            if v is None and n == f"d{name}_out":
-                continue
-            if _heads(n, v, x, index, dt).shape != t.shape:
-                raise ValueError(f"{n} must have shape {tuple(t.shape)} (got {tuple(v.shape)})")
         if dg is not None and gamma is None:
             raise ValueError(f"dgamma_{name} needs gamma_{name}")
-        sets.append((name, t, d, gamma, o, dg))
-    m = _gammas(q, gamma_q, k, gamma_k, x, index)
-    rotation = _positions(positions, inv_freq, x, index, interleaved, scale)
-    batch, seq = x.shape[:2] if x.dim() == 4 else (1, x.shape[0])
+        t_at = _heads(name, t, lead, size, index, dt)
+        d_at = _heads_like("d" + name, d, lead, size, t_at[0], index, dt)
+        o_at = _NO_STRIDES if o is None else _heads_like(f"d{name}_out", o, lead, size, t_at[0],
+                                                         index, dt)
+        sets.append((name, t, d, gamma, o, dg, t_at, d_at, o_at))
+    m = _gammas(q, gamma_q, k, gamma_k, size, x, index)
+    rotation = _rotation(positions, inv_freq, lead, index, interleaved, scale)
 
     def run():
         lib = _lib or library()
@@ -1018,22 +1046,23 @@ def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *,
         for i, one in enumerate(sets):
             if one is None:
                 continue
-            name, t, d, gamma, o, dg = one
-            if o is not None or want_input:
-                dxs[i] = torch.empty(t.shape, dtype=dt, device=t.device) if o is None else o
+            name, t, d, gamma, o, dg, t_at, d_at, o_at = one
+            if o is None and want_input:
+                o, o_at = _new_heads(lead, t_at[0], size, x, dt)
             if gamma is not None and (dg is not None or want_gamma):
-                dgs[i] = _like("dgamma_" + name, dg, gamma, index)
-            heads[i] = t.shape[-2]
+                dg = _like("dgamma_" + name, dg, gamma, index)
+            dxs[i], dgs[i], heads[i] = o, dg, t_at[0]
             args[i] = _HEADS_GRAD.pack(
-                d.data_ptr(), t.data_ptr(), _at(gamma) or 0, _at(dxs[i]) or 0, _at(dgs[i]) or 0,
-                heads[i], *_head_steps(d), *_head_steps(t),
-                *(_NO_STRIDES if dxs[i] is None else _head_steps(dxs[i])))
-        need = lib.b200norm_head_rms_rotary_grad_workspace_size(batch, seq, *heads, x.shape[-1])
+                d.data_ptr(), t.data_ptr(), 0 if gamma is None else gamma.data_ptr(),
+                0 if o is None else o.data_ptr(), 0 if dg is None else dg.data_ptr(), t_at[0],
+                *d_at, *t_at[1:], *o_at)
+        batch, seq = lead if len(lead) == 2 else (1, lead[0])
+        need = lib.b200norm_head_rms_rotary_grad_workspace_size(batch, seq, *heads, size)
         raw = _raw_stream(index, stream)
         ws, n = _scratch(workspace, need, x, index, raw)
-        _check(lib.b200norm_head_rms_rotary_grad(*args, rotation, batch, seq, x.shape[-1],
-                                                 _DTYPES[dt], _DTYPES[m], float(epsilon),
-                                                 _at(ws), n, raw))
+        _check(lib.b200norm_head_rms_rotary_grad(*args, rotation, batch, seq, size, _DTYPES[dt],
+                                                 _DTYPES[m], float(epsilon), _at(ws), n,
+                                                 raw))
         return dxs[0], dxs[1], dgs[0], dgs[1]
 
     context = _on(index, stream, (dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, dq_out,

@@ -33,7 +33,8 @@ struct HeadsArgs {
   int pitch;       // angles a warp keeps: whole units
   int steps[2];    // per token: the heads in groups of 32 / lanes
   int parts[2];    // gradient: CTAs of queries and of keys
-  bool whole;      // a unit's pairs are all rotated, or none
+  bool whole;      // half a unit's pairs are all rotated, or none
+  bool full;       // every pair of a head is rotated
 };
 
 // Rows on their way to a warp: each lane copies its own accesses to shared memory
@@ -393,6 +394,14 @@ __device__ __forceinline__ int head_end(const HeadShare& s, int steps) {
   return s.left < steps - s.i ? s.i + s.left : steps;
 }
 
+// FORM 1 and 2: all of a head is rotated, in the half layout or interleaved; 0: known at run
+// time (branches on it inside the gradient's step cost a tenth: they keep its instructions
+// in order).
+template <int FORM>
+__device__ __forceinline__ bool is_interleaved(const HeadsArgs& g) {
+  return FORM == 0 ? g.c.interleaved : FORM == 2;
+}
+
 // gamma of a unit's pairs.
 template <int VE, int K>
 __device__ __forceinline__ void unit_gamma(const float* gamma, const HeadUnits<VE, K>& u, int k,
@@ -422,7 +431,7 @@ __device__ __forceinline__ void unit_angles(const float* p, const HeadUnits<VE, 
 
 // (a, b) -> (a ca + b sa, b cb + a sb), what a pair of the rotation becomes; one past the
 // pairs (a ca, b cb): an infinity must not reach the neighbour through a factor of zero.
-template <int VE, int K, typename V, int N>
+template <int FORM, int VE, int K, typename V, int N>
 __device__ __forceinline__ void unit_turn(const HeadsArgs& g, const HeadUnits<VE, K>& u, int k,
                                           V (&a)[N], V (&b)[N], const V (&ca)[N],
                                           const V (&sa)[N], const V (&cb)[N], const V (&sb)[N]) {
@@ -434,6 +443,14 @@ __device__ __forceinline__ void unit_turn(const HeadsArgs& g, const HeadUnits<VE
     y[i] = b[i];
     a[i] = mul2(a[i], ca[i]);
     b[i] = mul2(b[i], cb[i]);
+  }
+  if (FORM != 0 || g.full) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      a[i] = fma2(y[i], sa[i], a[i]);
+      b[i] = fma2(x[i], sb[i], b[i]);
+    }
+    return;
   }
   if (VE != 2 && g.whole) {
     if (left_a > 0) {
@@ -478,7 +495,7 @@ struct HeadFactors {
   V ca[K][N], sa[K][N], cb[K][N], sb[K][N];
 };
 
-template <int VE, int K, bool NORM>
+template <int FORM, int VE, int K, bool NORM>
 __device__ __forceinline__ void head_factors(const HeadsArgs& g, const HeadShared& sh,
                                              const float* gamma, const HeadUnits<VE, K>& u,
                                              HeadFactors<VE, K>& f) {
@@ -489,7 +506,7 @@ __device__ __forceinline__ void head_factors(const HeadsArgs& g, const HeadShare
     V c[N], s[N], ga[N], gb[N];
     unit_angles<VE, K>(sh.cosines, u, k, c);
     unit_angles<VE, K>(sh.cosines + g.pitch, u, k, s);
-    if constexpr (NORM) unit_gamma<VE, K>(gamma, u, k, g.c.interleaved, ga, gb);
+    if constexpr (NORM) unit_gamma<VE, K>(gamma, u, k, is_interleaved<FORM>(g), ga, gb);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if constexpr (!NORM) ga[i] = gb[i] = every<V>(1.0f);
@@ -513,7 +530,7 @@ struct HeadCursor {
   bool fresh;      // a token's first row: its position comes with it
 };
 
-template <typename T, int VE, int K, int LANES, bool NORM>
+template <typename T, int VE, int K, int LANES, int FORM, bool NORM>
 __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs g) {
   using V = typename HeadVec<VE>::V;
   constexpr int N = HeadVec<VE>::N, S = HeadRow<T, VE, K>::kStages;
@@ -526,6 +543,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
   const int sub = lane & (lanes - 1), row = lane / lanes, rows = 32 / lanes;
   const HeadUnits<VE, K> u = head_units<VE, K>(g, sub);
   const int steps = g.steps[0] + g.steps[1];
+  const bool inter = is_interleaved<FORM>(g);
   const float inv_size = 1.0f / static_cast<float>(g.c.size);
   HeadShare at = head_share(g, steps, static_cast<int64_t>(blockIdx.x) * kHeadWarps + (threadIdx.x >> 5),
                             static_cast<int64_t>(gridDim.x) * kHeadWarps);
@@ -584,7 +602,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
       const int last = end - off < g.steps[n] ? end - off : g.steps[n];
       if (first >= last) continue;
       HeadFactors<VE, K> f;
-      head_factors<VE, K, NORM>(g, sh, sh.gamma + (n ? 2 * g.pitch : 0), u, f);
+      head_factors<FORM, VE, K, NORM>(g, sh, sh.gamma + (n ? 2 * g.pitch : 0), u, f);
       const int64_t h = static_cast<int64_t>(first) * rows + row;
       T* y = static_cast<T*>(set.y) + at.b * set.ys.batch + at.t * set.ys.token + h * set.ys.head;
       const int64_t step = rows * set.ys.head;
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
       for (int i = first; i < last; ++i, y += step, left -= rows) {
         fetch_wait<S - 2>();
         HeadValues<VE, K> x;
-        head_widen<T, VE, K>(ring[stage], g.c.interleaved, x);
+        head_widen<T, VE, K>(ring[stage], inter, x);
         float r = 1.0f;
         if constexpr (NORM) {
           V sa = every<V>(0.0f), sb = every<V>(0.0f);
@@ -608,7 +626,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          unit_turn<VE, K>(g, u, k, x.a[k], x.b[k], f.ca[k], f.sa[k], f.cb[k], f.sb[k]);
+          unit_turn<FORM, VE, K>(g, u, k, x.a[k], x.b[k], f.ca[k], f.sa[k], f.cb[k], f.sb[k]);
         if constexpr (NORM) {
 #pragma unroll
           for (int k = 0; k < K; ++k)
@@ -618,7 +636,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
               x.b[k][e] = mul2(x.b[k][e], every<V>(r));
             }
         }
-        head_store<T, VE, K>(y, left > 0, g.c.interleaved, u, x);
+        head_store<T, VE, K>(y, left > 0, inter, u, x);
         // into the stage before this one, whose values have all been used
         fetch(stage == 0 ? S - 1 : stage - 1);
         stage = stage + 1 == S ? 0 : stage + 1;
@@ -635,7 +653,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
 //   dx = r (g - u mean(g u)) = r g - x r^3 mean(g x),  dgamma = sum over rows of da u.
 // The first parts[0] CTAs take the queries, the others the keys; each keeps its
 // columns' sums in registers over all its rows and stores them as one part.
-template <typename T, int VE, int K, int LANES>
+template <typename T, int VE, int K, int LANES, int FORM>
 __global__ void __launch_bounds__(32 * kHeadWarps, 2 * VE * K <= 16 ? 2 : 1)
 heads_grad_kernel(const HeadsArgs g) {
   using V = typename HeadVec<VE>::V;
@@ -653,6 +671,7 @@ heads_grad_kernel(const HeadsArgs g) {
   const HeadUnits<VE, K> u = head_units<VE, K>(g, sub);
   const float inv_size = 1.0f / static_cast<float>(g.c.size);
   const int steps = g.steps[n];
+  const bool inter = is_interleaved<FORM>(g);
   HeadShare at = head_share(g, steps, static_cast<int64_t>(part) * kHeadWarps + warp,
                             static_cast<int64_t>(g.parts[n]) * kHeadWarps);
   pdl_wait();
@@ -714,8 +733,8 @@ heads_grad_kernel(const HeadsArgs g) {
     for (int i = first; i < last; ++i, y += step_y, left -= rows) {
       fetch_wait<S - 2>();
       HeadValues<VE, K> x, d;
-      head_widen<T, VE, K>(ring[2 * stage], g.c.interleaved, x);
-      head_widen<T, VE, K>(ring[2 * stage + 1], g.c.interleaved, d);
+      head_widen<T, VE, K>(ring[2 * stage], inter, x);
+      head_widen<T, VE, K>(ring[2 * stage + 1], inter, d);
       V sa = every<V>(0.0f), sb = every<V>(0.0f), ta = every<V>(0.0f), tb = every<V>(0.0f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -726,8 +745,8 @@ heads_grad_kernel(const HeadsArgs g) {
         unit_angles<VE, K>(sh.cosines + g.pitch, u, k, s);
 #pragma unroll
         for (int e = 0; e < N; ++e) t[e] = mul2(s[e], every<V>(-1.0f));
-        unit_turn<VE, K>(g, u, k, d.a[k], d.b[k], c, s, c, t);
-        unit_gamma<VE, K>(sh.gamma + n * 2 * g.pitch, u, k, g.c.interleaved, ga, gb);
+        unit_turn<FORM, VE, K>(g, u, k, d.a[k], d.b[k], c, s, c, t);
+        unit_gamma<VE, K>(sh.gamma + n * 2 * g.pitch, u, k, inter, ga, gb);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           sa = fma2(x.a[k][e], x.a[k][e], sa);
@@ -736,28 +755,27 @@ heads_grad_kernel(const HeadsArgs g) {
           tb = fma2(mul2(d.b[k][e], gb[e]), x.b[k][e], tb);
         }
       }
-      const float r = rsqrtf(row_sum<LANES>(total(add2(sa, sb)), lanes) * inv_size + g.c.eps);
-      const float m = row_sum<LANES>(total(add2(ta, tb)), lanes) * inv_size * r * r;
+      // (lanes without a row here hold zeros, and r would be infinite for eps 0)
       const bool in = left > 0;
-      // (a lane without a row here has zeros, but r may be infinite for eps 0)
-      if (in) {
+      const float length = row_sum<LANES>(total(add2(sa, sb)), lanes) * inv_size + g.c.eps;
+      const float r = in ? rsqrtf(length) : 0.0f;
+      const float m = row_sum<LANES>(total(add2(ta, tb)), lanes) * inv_size * r * r;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          V ga[N], gb[N];
-          unit_gamma<VE, K>(sh.gamma + n * 2 * g.pitch, u, k, g.c.interleaved, ga, gb);
+      for (int k = 0; k < K; ++k) {
+        V ga[N], gb[N];
+        unit_gamma<VE, K>(sh.gamma + n * 2 * g.pitch, u, k, inter, ga, gb);
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const V ua = mul2(x.a[k][e], every<V>(r)), ub = mul2(x.b[k][e], every<V>(r));
-            da[k][e] = fma2(d.a[k][e], ua, da[k][e]);
-            db[k][e] = fma2(d.b[k][e], ub, db[k][e]);
-            d.a[k][e] = mul2(mul2(d.a[k][e], ga[e]), every<V>(r));
-            d.b[k][e] = mul2(mul2(d.b[k][e], gb[e]), every<V>(r));
-            d.a[k][e] = fma2(ua, every<V>(-m), d.a[k][e]);
-            d.b[k][e] = fma2(ub, every<V>(-m), d.b[k][e]);
-          }
+        for (int e = 0; e < N; ++e) {
+          const V ua = mul2(x.a[k][e], every<V>(r)), ub = mul2(x.b[k][e], every<V>(r));
+          da[k][e] = fma2(d.a[k][e], ua, da[k][e]);
+          db[k][e] = fma2(d.b[k][e], ub, db[k][e]);
+          d.a[k][e] = mul2(mul2(d.a[k][e], ga[e]), every<V>(r));
+          d.b[k][e] = mul2(mul2(d.b[k][e], gb[e]), every<V>(r));
+          d.a[k][e] = fma2(ua, every<V>(-m), d.a[k][e]);
+          d.b[k][e] = fma2(ub, every<V>(-m), d.b[k][e]);
         }
       }
-      if (set.y) head_store<T, VE, K>(y, in, g.c.interleaved, u, d);
+      if (set.y) head_store<T, VE, K>(y, in, inter, u, d);
       // into the stage before this one, whose values have all been used
       fetch(stage == 0 ? S - 1 : stage - 1);
       stage = stage + 1 == S ? 0 : stage + 1;
@@ -773,7 +791,7 @@ heads_grad_kernel(const HeadsArgs g) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     Pack<float, VE> lo, hi;
-    unit_narrow<float, VE>(da[k], db[k], g.c.interleaved, lo, hi);
+    unit_narrow<float, VE>(da[k], db[k], inter, lo, hi);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       for (int o = lanes; o < 32; o <<= 1) {

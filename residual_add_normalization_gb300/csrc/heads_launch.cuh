@@ -15,6 +15,7 @@ inline HeadsArgs head_args(const HeadsCall& c, const HeadsPlan& p) {
   g.seq = static_cast<unsigned>(c.seq);
   g.units = p.units;
   g.lanes = p.lanes;
+  g.full = c.rot == c.size;
   g.whole = p.ve < 4 || c.rot / 2 % (p.ve / 2) == 0;  // (half layout: of whole accesses)
   const int rows = 32 / p.lanes;
   for (int n = 0; n < 2; ++n)
@@ -25,28 +26,34 @@ inline HeadsArgs head_args(const HeadsCall& c, const HeadsPlan& p) {
 template <int N>
 using Num = std::integral_constant<int, N>;
 
-// f(VE, K, LANES) for the row layout: K is rounded up to what has a kernel, and LANES is 0
-// (known at run time) but for the usual rows of whole 16-byte vectors.
+// f(VE, K, LANES, FORM) for the row layout: K is rounded up to what has a kernel; LANES and
+// FORM are 0 (known at run time) but for the usual rows of whole 16-byte vectors.
 template <typename T, class F>
-cudaError_t with_head_layout(const HeadsPlan& p, F&& f) {
+cudaError_t with_head_layout(const HeadsCall& c, const HeadsPlan& p, F&& f) {
   constexpr int kVec = 16 / sizeof(T);
+  const int form = c.rot != c.size ? 0 : c.interleaved ? 2 : 1;
   if (p.ve == kVec) {
     if (p.sets <= 1) {
-      if (p.lanes == 8) return f(Num<kVec>(), Num<1>(), Num<8>());
-      if (p.lanes == 16) return f(Num<kVec>(), Num<1>(), Num<16>());
-      return f(Num<kVec>(), Num<1>(), Num<0>());
+      auto lanes = [&](auto n) {
+        if (form == 1) return f(Num<kVec>(), Num<1>(), n, Num<1>());
+        if (form == 2) return f(Num<kVec>(), Num<1>(), n, Num<2>());
+        return f(Num<kVec>(), Num<1>(), n, Num<0>());
+      };
+      if (p.lanes == 8) return lanes(Num<8>());
+      if (p.lanes == 16) return lanes(Num<16>());
+      return f(Num<kVec>(), Num<1>(), Num<0>(), Num<0>());
     }
-    if (p.sets <= 2) return f(Num<kVec>(), Num<2>(), Num<0>());
-    if constexpr (sizeof(T) == 4) return f(Num<kVec>(), Num<4>(), Num<0>());
+    if (p.sets <= 2) return f(Num<kVec>(), Num<2>(), Num<0>(), Num<0>());
+    if constexpr (sizeof(T) == 4) return f(Num<kVec>(), Num<4>(), Num<0>(), Num<0>());
   }
   if constexpr (sizeof(T) == 2) {
     if (p.ve == 2) {
-      if (p.sets <= 2) return f(Num<2>(), Num<2>(), Num<0>());
-      return f(Num<2>(), Num<8>(), Num<0>());
+      if (p.sets <= 2) return f(Num<2>(), Num<2>(), Num<0>(), Num<0>());
+      return f(Num<2>(), Num<8>(), Num<0>(), Num<0>());
     }
   }
-  if (p.sets <= 4) return f(Num<1>(), Num<4>(), Num<0>());
-  return f(Num<1>(), Num<16>(), Num<0>());
+  if (p.sets <= 4) return f(Num<1>(), Num<4>(), Num<0>(), Num<0>());
+  return f(Num<1>(), Num<16>(), Num<0>(), Num<0>());
 }
 
 // Raises a kernel's dynamic shared-memory limit once per device (every time on devices
@@ -87,10 +94,10 @@ cudaError_t launch_heads_t(const HeadsCall& c, cudaStream_t stream) {
   const HeadsPlan p = plan_heads(c, false);
   HeadsArgs g = head_args(c, p);
   const int64_t all = (static_cast<int64_t>(g.steps[0]) + g.steps[1]) * g.tokens;
-  return with_head_layout<T>(p, [&](auto ve, auto k, auto lanes) {
+  return with_head_layout<T>(c, p, [&](auto ve, auto k, auto lanes, auto form) {
     constexpr int VE = decltype(ve)::value, K = decltype(k)::value, L = decltype(lanes)::value;
     auto go = [&](auto norm) {
-      auto* fn = heads_kernel<T, VE, K, L, decltype(norm)::value>;
+      auto* fn = heads_kernel<T, VE, K, L, decltype(form)::value, decltype(norm)::value>;
       static std::atomic<unsigned long long> raised{0}, seen{0};
       g.pitch = p.lanes * K * VE;
       const size_t smem = head_smem<T, VE, K>(g, false);
@@ -112,11 +119,11 @@ cudaError_t launch_heads_grad_t(const HeadsCall& c, cudaStream_t stream) {
   const HeadParts parts = head_parts(g.tokens, c.set[0].heads, c.set[1].heads, c.size);
   g.parts[0] = parts.q;
   g.parts[1] = parts.k;
-  return with_head_layout<T>(p, [&](auto ve, auto k, auto lanes) {
+  return with_head_layout<T>(c, p, [&](auto ve, auto k, auto lanes, auto form) {
     constexpr int VE = decltype(ve)::value, K = decltype(k)::value, L = decltype(lanes)::value;
     static std::atomic<unsigned long long> raised{0};
     g.pitch = p.lanes * K * VE;
-    auto* fn = heads_grad_kernel<T, VE, K, L>;
+    auto* fn = heads_grad_kernel<T, VE, K, L, decltype(form)::value>;
     const size_t smem = head_smem<T, VE, K>(g, true);
     if (const cudaError_t e = head_raise(fn, smem, raised)) return e;
     return launch_clusters(fn, dim3(static_cast<unsigned>(parts.q + parts.k)), 32 * kHeadWarps, 1,

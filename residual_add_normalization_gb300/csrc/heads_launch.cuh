@@ -39,6 +39,7 @@ cudaError_t with_head_layout(const HeadsCall& c, const HeadsPlan& p, F&& f) {
         if (form == 2) return f(Num<kVec>(), Num<1>(), n, Num<2>());
         return f(Num<kVec>(), Num<1>(), n, Num<0>());
       };
+      if (p.lanes == 4) return lanes(Num<4>());
       if (p.lanes == 8) return lanes(Num<8>());
       if (p.lanes == 16) return lanes(Num<16>());
       return f(Num<kVec>(), Num<1>(), Num<0>(), Num<0>());

@@ -402,15 +402,15 @@ linear_plain_kernel(const PlainProduct p) {
                      acc[i][C / 2 - 1].y};
       finish_gated(t, up, m0 + (i / 4) * kHalf + ty * 4 + i % 4, n0 + tx * 4);
     }
-    return;
+  } else if constexpr (!GATED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int h = 0; h < C / 4; ++h) {
+        float t[4] = {acc[i][2 * h].x, acc[i][2 * h].y, acc[i][2 * h + 1].x, acc[i][2 * h + 1].y};
+        finish(t, m0 + (i / 4) * kHalf + ty * 4 + i % 4, n0 + h * kHalf + tx * 4);
+      }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int h = 0; h < C / 4; ++h) {
-      float t[4] = {acc[i][2 * h].x, acc[i][2 * h].y, acc[i][2 * h + 1].x, acc[i][2 * h + 1].y};
-      finish(t, m0 + (i / 4) * kHalf + ty * 4 + i % 4, n0 + h * kHalf + tx * 4);
-    }
 }
 
 // ---------------------------------------------------------------------------

@@ -423,7 +423,13 @@ B200NORM_API b200norm_status b200norm_linear_grad(
  *              when not requested.  h is formed from the unrounded z.
  *   activation, workspace  as in b200norm_linear (of its own _workspace_size()).
  *
- * Limits as in b200norm_linear, with F in [1, 2^19]; rows == 0 is a no-op.
+ * Limits as in b200norm_linear, with F in [1, 2^19]; rows == 0 is a no-op.  Sums are
+ * binary32, in a fixed order.  Large float32 calls (from 16 rows and 2^26 products of
+ * rows, in_features and F) run on the tensor cores: every value is split into three
+ * bfloat16 numbers that add up to it (24 bits; below 2^-110 of magnitude some of the last
+ * are lost), and six of their nine products are summed, which leaves errors of about
+ * 2^-24 of a product.  An infinity there gives NaN where the product itself would be
+ * infinite; the workspace holds the pieces.
  */
 B200NORM_API size_t b200norm_gated_linear_workspace_size(int64_t rows, int64_t in_features,
                                                          int64_t out_features, b200norm_dtype T,
@@ -449,7 +455,8 @@ B200NORM_API b200norm_status b200norm_gated_linear(
  *   workspace  at least b200norm_gated_linear_grad_workspace_size() bytes, as above;
  *              aligned16: x and weight start on 16-byte boundaries.
  *
- * Sums are binary32, in a fixed order.  rows == 0 stores zeros in dw and db.
+ * Sums are binary32, in a fixed order; large float32 calls as in b200norm_gated_linear (and
+ * dz in pieces too).  rows == 0 stores zeros in dw and db.
  */
 B200NORM_API size_t b200norm_gated_linear_grad_workspace_size(int64_t rows, int64_t in_features,
                                                               int64_t out_features,

@@ -64,8 +64,9 @@ B200NORM_API b200norm_status b200norm_testing_force_split(int csize, int nv);
  * thread: cg CTAs per tile (1 or 2), bn columns per tile, K in `splits` parts
  * (1, 2, 4 or 8), swap 1 for the form whose lanes hold the result's columns.
  * (0, 0, 0, 0) restores the automatic choice.  A later call that the tiling has
- * no kernel for returns B200NORM_ERR_UNSUPPORTED; float32 calls and those whose
- * operands are not 16-byte aligned do not take one and ignore it. */
+ * no kernel for returns B200NORM_ERR_UNSUPPORTED; float32 calls (but for gated ones
+ * large enough for the tensor cores) and those whose operands are not 16-byte
+ * aligned do not take one and ignore it. */
 B200NORM_API b200norm_status b200norm_testing_force_linear(int cg, int bn, int splits, int swap);
 
 /* Stall the linear operator's tensor-core products (process-wide) for later

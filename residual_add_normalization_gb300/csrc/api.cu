@@ -875,7 +875,7 @@ size_t b200norm_gated_linear_workspace_size(int64_t rows, int64_t in_features,
                                             int64_t out_features, b200norm_dtype T,
                                             int aligned16) {
   if (check_gated_shape(rows, in_features, out_features, T, 0) != B200NORM_OK) return 0;
-  return linear_plan(rows, in_features, 2 * out_features, to_dtype(T), aligned16 != 0).bytes;
+  return gated_plan(rows, in_features, out_features, to_dtype(T), aligned16 != 0).bytes;
 }
 
 b200norm_status b200norm_gated_linear(const void* x, const void* weight, const void* bias, void* h,
@@ -898,7 +898,7 @@ b200norm_status b200norm_gated_linear(const void* x, const void* weight, const v
                        {z, 2 * hb, es, "z", true}};
   if (b200norm_status st = check_tensors(ts, 5)) return st;
   const LinearPlan plan =
-      linear_plan(rows, in_features, 2 * out_features, to_dtype(T), all_aligned16(ts, 2));
+      gated_plan(rows, in_features, out_features, to_dtype(T), all_aligned16(ts, 2));
   if (b200norm_status st = check_workspace(workspace, workspace_bytes, plan.bytes, ts, 5))
     return st;
   LinearCall c{x, weight, bias, nullptr, h, z, rows, in_features, out_features, to_dtype(T),
@@ -914,8 +914,7 @@ size_t b200norm_gated_linear_grad_workspace_size(int64_t rows, int64_t in_featur
                                                  int64_t out_features, b200norm_dtype T,
                                                  int aligned16) {
   if (check_gated_shape(rows, in_features, out_features, T, 0) != B200NORM_OK) return 0;
-  return linear_grad_plan(rows, in_features, 2 * out_features, to_dtype(T), kActSilu,
-                          aligned16 != 0).bytes;
+  return gated_grad_plan(rows, in_features, out_features, to_dtype(T), aligned16 != 0).bytes;
 }
 
 b200norm_status b200norm_gated_linear_grad(const void* dh, const void* x, const void* weight,
@@ -939,8 +938,8 @@ b200norm_status b200norm_gated_linear_grad(const void* dh, const void* x, const 
                        {z, 2 * hb, es, "z", false}, {dx, xb, es, "dx", true},
                        {dw, wb, es, "dw", true}, {db, 2 * out_features * es, es, "db", true}};
   if (b200norm_status st = check_tensors(ts, 7)) return st;
-  const LinearGradPlan plan = linear_grad_plan(rows, in_features, 2 * out_features, to_dtype(T),
-                                               kActSilu, all_aligned16(ts + 1, 2));
+  const LinearGradPlan plan = gated_grad_plan(rows, in_features, out_features, to_dtype(T),
+                                              all_aligned16(ts + 1, 2));
   const size_t need = rows > 0 ? plan.bytes : 0;
   if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, ts, 7)) return st;
   LinearGradCall c{dh, x, weight, z, dx, dw, db, rows, in_features, out_features, to_dtype(T),

@@ -17,6 +17,9 @@ extern template cudaError_t launch_gated_dz<__nv_bfloat16>(const LinearDzCall&, 
 extern template cudaError_t launch_pack<__nv_bfloat16>(const void*, void*, int64_t, const void*,
                                              void*, int64_t, int64_t, cudaStream_t);
 
+cudaError_t launch_pieces(const void* src0, void* dst0, int64_t rows0, const void* src1,
+                          void* dst1, int64_t rows1, int64_t n, cudaStream_t stream);
+
 namespace {
 
 size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
@@ -31,6 +34,7 @@ cudaError_t pack_rows(DType t, const void* src0, void* dst0, int64_t rows0, cons
 }  // namespace
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream) {
+  if (p.piece_a) return launch_mma(p, stream);
   const bool mma = mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0;
   if (p.a.k_contiguous && p.b.k_contiguous && !(mma && p.forced.cg) &&
       few_rows(p.M, p.gated ? 2 * p.N : p.N, p.K, p.t, mma)) {
@@ -79,6 +83,38 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, 
   return p;
 }
 
+// Below 2^26 products of a half the copies cost what the tensor cores gain: 128 x 768 x 768
+// (rows, in, out) takes 16.1 us forward on the binary32 units and 16.2 in pieces, 512 x 768 x 768
+// 40 and 24.5, its gradients 72 and 48, 2048 x 1024 x 2048 387 and 89, 1086 and 246, but
+// 256 x 256 x 256 9.4 and 10.5, 21 and 27.  The weight's copy wants a few rows to serve:
+// 32 x 4096 x 4096 126 and 110.
+bool gated_pieces(int64_t rows, int64_t in, int64_t out) {
+  return rows >= 16 && rows * in * out >= int64_t{1} << 26;
+}
+
+LinearPlan gated_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {
+  if (t != DType::F32 || !gated_pieces(rows, in, out))
+    return linear_plan(rows, in, 2 * out, t, aligned16);
+  LinearPlan p = {};
+  p.pieces = true;
+  p.w = round_256(static_cast<size_t>(rows) * 3 * piece_of(in) * 2);
+  p.bytes = p.w + round_256(static_cast<size_t>(2 * out) * 3 * piece_of(in) * 2);
+  return p;
+}
+
+LinearGradPlan gated_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {
+  if (t != DType::F32 || !gated_pieces(rows, in, out))
+    return linear_grad_plan(rows, in, 2 * out, t, kActSilu, aligned16);
+  LinearGradPlan p = {};
+  p.make_dz = p.pieces = true;
+  p.ldz = 3 * piece_of(2 * out);
+  p.part = round_256(static_cast<size_t>(rows) * p.ldz * 2);
+  p.x = p.part + round_256(static_cast<size_t>(linear_db_parts(rows, 2 * out)) * 2 * out * 4);
+  p.w = p.x + round_256(static_cast<size_t>(rows) * 3 * piece_of(in) * 2);
+  p.bytes = p.w + round_256(static_cast<size_t>(2 * out) * 3 * piece_of(in) * 2);
+  return p;
+}
+
 cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStream_t stream) {
   Operand x{c.x, c.in, true}, w{c.w, c.in, true};
   if (plan.pack) {
@@ -89,8 +125,17 @@ cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStrea
     x = {ws + plan.x, pitch16(c.in), true};
     w = {ws + plan.w, pitch16(c.in), true};
   }
-  const Product p{x, w, c.rows, c.out, c.in, {c.bias, c.residual, c.y, c.z, c.act}, c.t, c.forced,
-                  c.gated};
+  Product p{x, w, c.rows, c.out, c.in, {c.bias, c.residual, c.y, c.z, c.act}, c.t, c.forced,
+            c.gated};
+  if (plan.pieces) {
+    char* ws = static_cast<char*>(c.workspace);
+    const cudaError_t e =
+        launch_pieces(c.x, ws + plan.x, c.rows, c.w, ws + plan.w, 2 * c.out, c.in, stream);
+    if (e != cudaSuccess) return e;
+    p.piece_a = p.piece_b = piece_of(c.in);
+    p.a = {ws + plan.x, 3 * p.piece_a, true};
+    p.b = {ws + plan.w, 3 * p.piece_b, true};
+  }
   return launch_product(p, stream);
 }
 
@@ -102,8 +147,13 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& pl
   cudaError_t e = cudaSuccess;
   if (made || c.db) {
     const LinearDzCall d{c.dy, c.z, made, plan.ldz, c.db, reinterpret_cast<float*>(ws + plan.part),
-                         c.rows, c.out, c.act, c.t};
+                         c.rows, c.out, c.act, c.t, plan.pieces ? piece_of(out) : 0};
     e = launch_linear_dz(d, c.gated, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (plan.pieces && (c.dx || c.dw)) {
+    e = launch_pieces(c.x, ws + plan.x, c.dw ? c.rows : 0, c.w, ws + plan.w, c.dx ? out : 0, c.in,
+                      stream);
     if (e != cudaSuccess) return e;
   }
   if (plan.pack && c.rows > 0 && (c.dx || c.dw)) {
@@ -116,8 +166,13 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& pl
   if (c.dx && c.rows > 0) {
     Operand w{c.w, c.in, false};
     if (plan.pack) w = {ws + plan.w, pitch16(c.in), false};
-    const Product p{{dz, ldz, true}, w, c.rows, c.in, out,
-                    {nullptr, nullptr, c.dx, nullptr, kActNone}, c.t, c.forced};
+    Product p{{dz, ldz, true}, w, c.rows, c.in, out,
+              {nullptr, nullptr, c.dx, nullptr, kActNone}, c.t, c.forced};
+    if (plan.pieces) {
+      p.piece_a = piece_of(out);
+      p.piece_b = piece_of(c.in);
+      p.b = {ws + plan.w, 3 * p.piece_b, false};
+    }
     e = launch_product(p, stream);
     if (e != cudaSuccess) return e;
   }
@@ -126,8 +181,13 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& pl
   if (c.dw) {
     Operand x{c.x, c.in, false};
     if (plan.pack) x = {ws + plan.x, pitch16(c.in), false};
-    const Product p{{dz, ldz, false}, x, out, c.in, c.rows,
-                    {nullptr, nullptr, c.dw, nullptr, kActNone}, c.t, c.forced};
+    Product p{{dz, ldz, false}, x, out, c.in, c.rows,
+              {nullptr, nullptr, c.dw, nullptr, kActNone}, c.t, c.forced};
+    if (plan.pieces) {
+      p.piece_a = piece_of(out);
+      p.piece_b = piece_of(c.in);
+      p.b = {ws + plan.x, 3 * p.piece_b, false};
+    }
     e = launch_product(p, stream);
   }
   return e;

@@ -584,7 +584,41 @@ __global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const LinearDz
 
 // Of a gate and what it gates: dz = [dh * up * act'(gate) | dh * act(gate)], and the column
 // sums of both, in the same way: three reads and two writes per element of the result.
-template <typename T, int VE, int ACT>
+// PIECES (float32): dz as the products' operand, three bfloat16 pieces.
+__device__ __forceinline__ void pieces_of(float v, __nv_bfloat16 (&p)[3]) {
+  // each piece the rounding of what the ones before leave, which is exact in binary32; what
+  // is not finite, or rounds past the largest bfloat16, is cut instead and has one piece
+  p[0] = __float2bfloat16_rn(v);
+  if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) {
+    p[0] = __ushort_as_bfloat16(static_cast<unsigned short>(__float_as_uint(v) >> 16));
+    // (a NaN whose payload lies in the lower half stays one)
+    if (v != v) p[0] = __float2bfloat16_rn(v);
+    p[1] = p[2] = __float2bfloat16_rn(0.0f);
+    return;
+  }
+  if ((__bfloat16_as_ushort(p[0]) & 0x7f80) == 0x7f80)
+    p[0] = __ushort_as_bfloat16(static_cast<unsigned short>(__float_as_uint(v) >> 16));
+  const float r = v - to_f32(p[0]);
+  p[1] = __float2bfloat16_rn(r);
+  p[2] = __float2bfloat16_rn(r - to_f32(p[1]));
+}
+
+template <int VE>
+__device__ __forceinline__ void store_pieces(__nv_bfloat16* dst, int64_t piece,
+                                             const float (&f)[VE]) {
+  Pack<__nv_bfloat16, VE> p[3];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    __nv_bfloat16 v[3];
+    pieces_of(f[e], v);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) p[i].v[e] = v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) *reinterpret_cast<Pack<__nv_bfloat16, VE>*>(dst + i * piece) = p[i];
+}
+
+template <typename T, int VE, int ACT, bool PIECES>
 __device__ __forceinline__ void gated_dz_rows(const LinearDzCall& c, int64_t r0, int64_t r1,
                                               int64_t col, float (&sum)[2][VE]) {
   const T* dh = static_cast<const T*>(c.dy) + col;
@@ -618,7 +652,13 @@ __device__ __forceinline__ void gated_dz_rows(const LinearDzCall& c, int64_t r0,
         sum[0][e] = __fadd_rn(sum[0][e], gate[e]);  // same bits without dz
         sum[1][e] = __fadd_rn(sum[1][e], up[e]);
       }
-      if (dz) {
+      if constexpr (PIECES) {
+        __nv_bfloat16* at = static_cast<__nv_bfloat16*>(c.dz);
+        if (at) {
+          store_pieces<VE>(at + row * c.ldz + col, c.piece, gate);
+          store_pieces<VE>(at + row * c.ldz + c.out + col, c.piece, up);
+        }
+      } else if (dz) {
         *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + col) = pack_from<T, VE>(gate);
         *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + c.out + col) = pack_from<T, VE>(up);
       }
@@ -626,7 +666,7 @@ __device__ __forceinline__ void gated_dz_rows(const LinearDzCall& c, int64_t r0,
   }
 }
 
-template <typename T, int VE>
+template <typename T, int VE, bool PIECES = false>
 __global__ void __launch_bounds__(32 * kDzWarps) gated_dz_kernel(const LinearDzCall c, int parts) {
   pdl_wait();
   pdl_trigger();
@@ -638,8 +678,15 @@ __global__ void __launch_bounds__(32 * kDzWarps) gated_dz_kernel(const LinearDzC
   float sum[2][VE] = {};
   if (col < c.out)
     with_act(c.act, [&](auto act) {
-      gated_dz_rows<T, VE, decltype(act)::value>(c, r0 + warp, r1, col, sum);
+      gated_dz_rows<T, VE, decltype(act)::value, PIECES>(c, r0 + warp, r1, col, sum);
     });
+  if (PIECES && c.dz && blockIdx.x == 0) {  // the rest of each piece: zeros
+    const int rest = static_cast<int>(c.piece - 2 * c.out);
+    for (int64_t r = r0 + warp; r < r1; r += kDzWarps)
+      for (int i = lane; i < 3 * rest; i += 32)
+        static_cast<__nv_bfloat16*>(c.dz)[r * c.ldz + i / rest * c.piece + 2 * c.out + i % rest] =
+            from_f32<__nv_bfloat16>(0.0f);
+  }
   if (!c.db) return;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -739,5 +786,17 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const PackRows<T> firs
     reinterpret_cast<uint4*>(one ? first.dst : second.dst)[row * words + k / 8] = out;
   }
 }
+
+// Rows of n float32 values as rows of three bfloat16 pieces, `piece` elements apart, zeros
+// behind them.  Of two operands in one launch; a thread makes eight values of each piece.
+struct PieceRows {
+  const float* src;
+  __nv_bfloat16* dst;
+  int64_t rows;
+};
+
+__global__ void __launch_bounds__(256) linear_pieces_kernel(const PieceRows first,
+                                                            const PieceRows second, int64_t n,
+                                                            int64_t piece, bool vec);
 
 }  // namespace b200norm

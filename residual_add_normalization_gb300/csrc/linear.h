@@ -45,6 +45,10 @@ struct Product {
   // B has 2 N rows, a gate's and what it gates; C[m, n] = act(z[m, n]) * z[m, N + n] with
   // z = A B^T + bias (M x 2 N); no residual
   bool gated = false;
+  // Both operands are three bfloat16 pieces of float32 values, this many elements apart in a
+  // row (a multiple of 64; where k is contiguous, the rest of a piece is zeros); t is F32.
+  // (0: operands of type t.)
+  int64_t piece_a = 0, piece_b = 0;
 };
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream);
@@ -62,6 +66,9 @@ cudaError_t launch_mma(const Product& p, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_mma_t(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
                          cudaStream_t stream);
+
+cudaError_t launch_mma_f32(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
+                           cudaStream_t stream);
 
 // Whether a forced plan has a kernel for the product.
 bool mma_plan_ok(const MmaPlan& plan, int64_t M, int64_t K, bool a_kc, bool b_kc, bool gated);
@@ -92,6 +99,7 @@ struct LinearDzCall {
   int64_t rows, out;
   int act;
   DType t;
+  int64_t piece = 0;   // gated float32: dz as three bfloat16 pieces, this many elements apart
 };
 // Parts of the column sums: enough CTAs to fill the GPU (a CTA has 256 columns of
 // a 16-bit type), at least 32 rows in each.
@@ -156,11 +164,13 @@ inline bool few_rows(int64_t M, int64_t N, int64_t K, DType t, bool aligned) {
 inline int64_t pitch16(int64_t n) { return (n + 7) / 8 * 8; }
 struct LinearPlan {
   bool pack;              // x and weight are copied
+  bool pieces;            // in three pieces (float32)
   size_t x, w, bytes;
 };
 struct LinearGradPlan {
   bool make_dz;           // dz is stored: with an activation, or to realign dy
   bool pack;              // x and weight are copied
+  bool pieces;            // dz, x and weight are stored in three pieces (float32)
   int64_t ldz;
   size_t dz, part, x, w, bytes;
 };
@@ -169,6 +179,12 @@ struct LinearGradPlan {
 LinearPlan linear_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);
 LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, int act,
                                 bool aligned16);
+// The plans of a gated call (`out` counts the result's columns).  float32 products are made
+// on the tensor cores where the copies in pieces pay (gated_pieces).
+bool gated_pieces(int64_t rows, int64_t in, int64_t out);
+inline int64_t piece_of(int64_t n) { return (n + 63) / 64 * 64; }
+LinearPlan gated_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);
+LinearGradPlan gated_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);
 cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStream_t stream);
 cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& plan,
                                cudaStream_t stream);

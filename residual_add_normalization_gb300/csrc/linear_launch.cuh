@@ -105,13 +105,17 @@ cudaError_t launch_gated_dz(const LinearDzCall& c, cudaStream_t stream) {
   const int parts = c.rows > 0 ? linear_db_parts(c.rows, 2 * c.out) : 0;
   cudaError_t e = cudaSuccess;
   if (parts > 0) {
+    // (pieces start at multiples of 64 elements, and so do their rows)
     const Operand dh{c.dy, c.out, true}, z{c.z, c.out, true}, dz{c.dz, c.ldz, true};
-    const bool vec =
-        vectors_ok(dh, sizeof(T)) && vectors_ok(z, sizeof(T)) && vectors_ok(dz, sizeof(T));
+    const bool vec = vectors_ok(dh, sizeof(T)) && vectors_ok(z, sizeof(T)) &&
+                     (c.piece || vectors_ok(dz, sizeof(T)));
     const int cols = 32 * (vec ? VE : 1);
     const dim3 grid(static_cast<unsigned>((c.out + cols - 1) / cols), parts);
-    e = vec ? launch_pdl(gated_dz_kernel<T, VE>, grid, 32 * kDzWarps, stream, c, parts)
-            : launch_pdl(gated_dz_kernel<T, 1>, grid, 32 * kDzWarps, stream, c, parts);
+    auto go = [&](auto* fn) { return launch_pdl(fn, grid, 32 * kDzWarps, stream, c, parts); };
+    if constexpr (sizeof(T) == 4) {
+      if (c.piece) e = go(vec ? gated_dz_kernel<T, VE, true> : gated_dz_kernel<T, 1, true>);
+    }
+    if (!c.piece) e = go(vec ? gated_dz_kernel<T, VE> : gated_dz_kernel<T, 1>);
   }
   if (e == cudaSuccess && c.db)
     e = launch_pdl(linear_db_kernel<T>, dim3(static_cast<unsigned>((2 * c.out + 31) / 32)), 1024,

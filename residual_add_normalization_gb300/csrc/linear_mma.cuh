@@ -34,6 +34,14 @@
 // gradients' operands): the copy brings 64 x 64 squares then, and the matrix
 // instruction's descriptors say so; nothing is transposed in memory.
 //
+// TO float with bfloat16 operands: float32 products.  An operand's row holds three pieces
+// of its values side by side (each the rounding of what the ones before leave: 24 bits in
+// all), and K is walked six times, over the pairs of pieces whose products reach 2^-24 of
+// the whole, the smallest first.  The tensor cores cut a sum's last place at each addition of
+// 16 products (4.4e-6 in the norm over 4096 of k), so the last walk is added up in short
+// chunks, and the chunks' sums are added with rounding, in tensor memory, by the epilogue's
+// warps (5e-7 then; the library's float32 product 1.2e-6).
+//
 // Every wait is bounded: the first that gives up records its site in `status`;
 // one that gives up ends its role, the others then run out as well, and all meet
 // at the end to free the tensor memory.  A warp that waits as a whole decides as
@@ -60,6 +68,8 @@ struct MmaArgs {
   int tiles_m, tiles_n;
   int splits;
   int64_t gate;        // GATED: columns of the result (the weight has twice as many rows)
+  int walk;            // pieces: slices of one walk over K, and elements from an operand's
+  int piece_a, piece_b;  // piece to the next
   Epilogue e;
   bool vec;            // rows of the result, bias and residual are whole 16-byte vectors
   unsigned* status;
@@ -71,7 +81,7 @@ struct MmaArgs {
 // Shared memory of a CTA: the ring, then 8 KB for each epilogue warp's results
 // (unless SWAP).  Two small CTAs share an SM.
 constexpr int kMmaStageRows = 32 * 128;  // 32 rows of 64 results, 128 bytes each
-template <int CG, int BN, bool SWAP, bool GATED = false>
+template <int CG, int BN, bool SWAP, bool GATED = false, bool PIECES = false>
 struct MmaShape {
   static constexpr int kBRows = BN / CG;                 // of B, per CTA
   static constexpr int kBBytes = kBRows * kMmaK * 2;
@@ -87,7 +97,15 @@ struct MmaShape {
   static constexpr int kBudget = (BN <= 64 ? 112 * 1024 : 225 * 1024) - kOut;
   static constexpr int kStages = kBudget / kStageBytes > 8 ? 8 : kBudget / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;  // two buffers of columns
+  // buffers of columns for sums (with pieces of 256 columns, there is room for one beside
+  // the chunks' total), and what is allocated: a power of two
+  static constexpr int kBuffers = PIECES && BN == 256 ? 1 : 2;
+  static constexpr int kColumns = (kBuffers + (PIECES ? 1 : 0)) * BN;
+  static constexpr int kTmem = kColumns <= 32    ? 32
+                               : kColumns <= 64  ? 64
+                               : kColumns <= 128 ? 128
+                               : kColumns <= 256 ? 256
+                                                 : 512;
   static constexpr size_t kSmem = 1024 + kRing + kOut;
 };
 
@@ -184,6 +202,19 @@ __device__ __forceinline__ void tmem_load16(unsigned addr, float (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_store16(unsigned addr, const float (&v)[16]) {
+  unsigned r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+      :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+         "r"(r[15]), "r"(addr) : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // A box of the tensor map at (x, y) into this CTA's shared memory, completing
@@ -663,17 +694,27 @@ __device__ __forceinline__ void gated_col(const Epilogue& e, int64_t m, int64_t 
 
 // -- kernel ---------------------------------------------------------------------
 
+// The pieces of A and of B on walk w over K, a hexadecimal digit each.
+constexpr unsigned kPieceA = 0x001012, kPieceB = 0x010210;
+constexpr int kWalks = 6;
+constexpr int kChunk = 4;         // slices of a chunk on the last walk,
+constexpr int kChunkBefore = 256;  // and on those before, whose sums are 2^-8 of the whole
+
 // (GATED: map_z is of z's gate columns, map_r of the others.)
-template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false>
-__global__ void __launch_bounds__(MmaShape<CG, BN, SWAP, GATED>::kThreads, GATED ? 1 : 0)
+template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false,
+          typename TO = T>
+__global__ void __launch_bounds__(MmaShape<CG, BN, SWAP, GATED, sizeof(TO) == 4>::kThreads,
+                                  GATED ? 1 : 0)
 linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_y,
                   const __grid_constant__ CUtensorMap map_z,
                   const __grid_constant__ CUtensorMap map_r, const MmaArgs g) {
-  using S = MmaShape<CG, BN, SWAP, GATED>;
+  constexpr bool kPieces = !std::is_same<T, TO>::value;
+  using S = MmaShape<CG, BN, SWAP, GATED, kPieces>;
   constexpr bool kFull = A_KC && B_KC;  // the gradients' products are stored as they are
   static_assert(!GATED || kFull, "a gate is of the forward product");
+  static_assert(!kPieces || !SWAP || GATED, "pieces with few rows are of a gated product");
   // a gate and what it gates lie in different lanes: they meet in shared memory
   constexpr bool kMeet = GATED && SWAP;
   constexpr int kTileM = kMeet ? kMmaRows / 2 : kMmaRows;  // rows and columns of the result
@@ -729,6 +770,16 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     tm = first + t % per % size;
     tn = t % per / size;
   };
+  // past the last slice of the chunk that slice kb begins: all of K, but for pieces
+  auto chunk_end = [&](int kb) {
+    if constexpr (kPieces) {
+      const int last = (kWalks - 1) * g.walk;
+      const int end = kb < last ? (last - kb < kChunkBefore ? last : kb + kChunkBefore)
+                                : kb + kChunk;
+      return end < k_hi ? end : k_hi;
+    }
+    return k_hi;
+  };
   auto give_up = [&](unsigned site) {
     if (atomicCAS(g.status, 0u, kStatusDeviceTimeout) == 0u) atomicExch(g.status + 1, site);
   };
@@ -757,25 +808,32 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           unsigned char* a = ring + s * S::kStageBytes;
           unsigned char* b = a + kMmaABytes;
           const unsigned bar = full0 + s * 8;
+          int k = kb * kMmaK, xa = 0, xb = 0;  // along K, and along the operands' rows
+          if constexpr (kPieces) {
+            const int w = kb / g.walk;
+            k = (kb - w * g.walk) * kMmaK;
+            xa = static_cast<int>(kPieceA >> (4 * w) & 15) * g.piece_a;
+            xb = static_cast<int>(kPieceB >> (4 * w) & 15) * g.piece_b;
+          }
           if constexpr (kMeet) {
-            tma_load<CG>(a, &map_a, kb * kMmaK, m0, bar);
-            tma_load<CG>(a + kMmaABytes / 2, &map_a, kb * kMmaK, gate + m0, bar);
+            tma_load<CG>(a, &map_a, xa + k, m0, bar);
+            tma_load<CG>(a + kMmaABytes / 2, &map_a, xa + k, gate + m0, bar);
           } else if constexpr (A_KC) {
-            tma_load<CG>(a, &map_a, kb * kMmaK, m0, bar);
+            tma_load<CG>(a, &map_a, xa + k, m0, bar);
           } else {
 #pragma unroll
             for (int i = 0; i < kMmaRows / 64; ++i)
-              tma_load<CG>(a + i * 8192, &map_a, m0 + i * 64, kb * kMmaK, bar);
+              tma_load<CG>(a + i * 8192, &map_a, xa + m0 + i * 64, k, bar);
           }
           if constexpr (GATED && !SWAP && CG == 1) {
-            tma_load<CG>(b, &map_b, kb * kMmaK, n0, bar);
-            tma_load<CG>(b + S::kBBytes / 2, &map_b, kb * kMmaK, gate + n0, bar);
+            tma_load<CG>(b, &map_b, xb + k, n0, bar);
+            tma_load<CG>(b + S::kBBytes / 2, &map_b, xb + k, gate + n0, bar);
           } else if constexpr (B_KC) {
-            tma_load<CG>(b, &map_b, kb * kMmaK, n0, bar);
+            tma_load<CG>(b, &map_b, xb + k, n0, bar);
           } else {
 #pragma unroll
             for (int i = 0; i < S::kBRows / 64; ++i)
-              tma_load<CG>(b + i * 8192, &map_b, n0 + i * 64, kb * kMmaK, bar);
+              tma_load<CG>(b + i * 8192, &map_b, xb + n0 + i * 64, k, bar);
           }
         }
       }
@@ -794,31 +852,35 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       constexpr unsigned step_a = (A_KC ? 32 : 2048) >> 4, step_b = (B_KC ? 32 : 2048) >> 4;
       int it = 0, n = 0;
       bool alive = true;
-      for (int t = unit; t < tiles && alive; t += units, ++n) {
-        const int buf = n & 1;
-        if (!mbar_wait(&drained[buf], ((n >> 1) & 1) ^ 1, wait_limit(g, kSiteDrained))) {
-          give_up(kSiteDrained);
-          break;
-        }
-        tc_fence_after();
-        const unsigned d = tmem + buf * BN;
-        for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(&full[s], (it / kStages) & 1, g.limit_ns)) {
-            give_up(kSiteFull);
+      for (int t = unit; t < tiles && alive; t += units) {
+        for (int kb = k_lo; kb < k_hi && alive; ++n) {
+          const int buf = n % S::kBuffers;
+          if (!mbar_wait(&drained[buf], ((n / S::kBuffers) & 1) ^ 1, wait_limit(g, kSiteDrained))) {
+            give_up(kSiteDrained);
             alive = false;
             break;
           }
           tc_fence_after();
-          const unsigned a = smem_addr(ring + s * S::kStageBytes);
-          const unsigned long long da = smem_desc(a, 8192);
-          const unsigned long long db = smem_desc(a + kMmaABytes, 8192);
+          const unsigned d = tmem + buf * BN;
+          const int first = kb;
+          for (const int end = chunk_end(kb); kb < end; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait(&full[s], (it / kStages) & 1, g.limit_ns)) {
+              give_up(kSiteFull);
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            const unsigned a = smem_addr(ring + s * S::kStageBytes);
+            const unsigned long long da = smem_desc(a, 8192);
+            const unsigned long long db = smem_desc(a + kMmaABytes, 8192);
 #pragma unroll
-          for (int k = 0; k < kMmaK / 16; ++k)
-            mma_f16<CG>(d, da + k * step_a, db + k * step_b, idesc, kb > k_lo || k > 0);
-          if (g.withhold != kSiteEmpty) mma_commit<CG>(&empty[s]);
+            for (int k = 0; k < kMmaK / 16; ++k)
+              mma_f16<CG>(d, da + k * step_a, db + k * step_b, idesc, kb > first || k > 0);
+            if (g.withhold != kSiteEmpty) mma_commit<CG>(&empty[s]);
+          }
+          mma_commit<CG>(&sums[buf]);
         }
-        mma_commit<CG>(&sums[buf]);
       }
     }
   } else {
@@ -828,19 +890,66 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     unsigned char* stage = ring + S::kRing + (warp - 2) * 2 * kMmaStageRows;  // not SWAP
     unsigned phase = 0, turn = 0;
     int n = 0;
-    for (int t = unit; t < tiles; t += units, ++n) {
-      const int buf = n & 1;
-      if (!warp_wait(&sums[buf], (n >> 1) & 1, g.limit_ns)) {
-        if (lane == 0) give_up(kSiteSums);
+    bool alive = true;
+    for (int t = unit; t < tiles && alive; t += units, ++n) {
+      auto await = [&] {  // a chunk's sums
+        alive = warp_wait(&sums[n % S::kBuffers], (n / S::kBuffers) & 1, g.limit_ns);
+        if (!alive && lane == 0) give_up(kSiteSums);
+        tc_fence_after();
+        return alive;
+      };
+      auto release = [&] {  // they have been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && g.withhold != kSiteDrained) {
+          if constexpr (CG == 1) {
+            mbar_arrive(&drained[n % S::kBuffers]);
+          } else {
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                         :: "r"(peer_addr(&drained[n % S::kBuffers], 0)) : "memory");
+          }
+        }
+      };
+      unsigned at = tmem + n % S::kBuffers * BN + (static_cast<unsigned>(quarter * 32) << 16);
+      if constexpr (kPieces) {
+        // the chunks added up behind the buffers, the columns that this warp stores
+        const unsigned lanes = static_cast<unsigned>(quarter * 32) << 16;
+        const unsigned total = tmem + S::kBuffers * BN + lanes;
+        constexpr bool kApart = GATED && !SWAP && BN == 256;  // 64 of each half
+        for (int kb = k_lo; kb < k_hi;) {
+          if (!await()) break;
+          const unsigned from = tmem + n % S::kBuffers * BN + lanes;
+#pragma unroll 1
+          for (int c = 0; c < S::kCols; c += 16) {
+            const int col = kApart ? (warp - 2) / 4 * 64 + c % 64 + c / 64 * 128 : c0 + c;
+            float v[16];
+            tmem_load16(from + col, v);
+            if (kb > k_lo) {
+              float w[16];
+              tmem_load16(total + col, w);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += w[i];
+            }
+            tmem_store16(total + col, v);
+          }
+          release();
+          kb = chunk_end(kb);
+          if (kb < k_hi) ++n;
+        }
+        if (!alive) break;
+        at = total;
+      } else if (!await()) {
         break;
       }
-      tc_fence_after();
+      auto drain = [&] {
+        if constexpr (!kPieces) release();
+      };
       int tm, tn;
       tile_at(t, tm, tn);
       const int64_t m0 =
           static_cast<int64_t>(tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) * kTileM;
       const int64_t n0 = static_cast<int64_t>(tn) * kTileN;
-      const unsigned d = tmem + buf * BN + c0 + (static_cast<unsigned>(quarter * 32) << 16);
+      const unsigned d = at + c0;
       if (kMeet || g.splits > 1) {
         // to shared memory (every copy and matrix instruction on it is done),
         // a column of 128 rows after another
@@ -861,31 +970,22 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
         }
         break;  // one tile per cluster
       }
-      auto release = [&] {  // the sums have been read
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && g.withhold != kSiteDrained) {
-          if constexpr (CG == 1) {
-            mbar_arrive(&drained[buf]);
-          } else {
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                         :: "r"(peer_addr(&drained[buf], 0)) : "memory");
-          }
-        }
-      };
       if constexpr (GATED) {
         if constexpr (!SWAP) {
           const int64_t n = n0 + (warp - 2) / 4 * 64;
           const unsigned first = d - c0 + (warp - 2) / 4 * 64;
-          if (g.vec) {
+          bool stored = false;
+          if constexpr (!kPieces) if (g.vec) {
+            stored = true;
             with_act(g.e.act, [&](auto act) {
               epilogue_gated<T, decltype(act)::value>(g, &map_y, &map_z, &map_r, first,
                                                       first + BN / 2, m0 + quarter * 32, n, lane,
-                                                      stage, turn, release);
+                                                      stage, turn, drain);
             });
-          } else {
-            epilogue_gated_scalar<T>(g, first, first + BN / 2, m0 + quarter * 32, n, lane,
-                                     reinterpret_cast<float*>(stage), release);
+          }
+          if (!stored) {
+            epilogue_gated_scalar<TO>(g, first, first + BN / 2, m0 + quarter * 32, n, lane,
+                                     reinterpret_cast<float*>(stage), drain);
           }
         }
       } else if constexpr (SWAP) {
@@ -895,31 +995,37 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           for (int c = 0; c < BN; c += 32) {
             float v[32];
             tmem_load32(d + c, v);
-            if (m < g.M) epilogue_col<T, 32>(g.e, n0 + c, g.N, m, g.M, v);
+            if (m < g.M) epilogue_col<TO, 32>(g.e, n0 + c, g.N, m, g.M, v);
             __syncwarp();
           }
         } else {
           float v[16];
           tmem_load16(d, v);
-          if (m < g.M) epilogue_col<T, 16>(g.e, n0, g.N, m, g.M, v);
+          if (m < g.M) epilogue_col<TO, 16>(g.e, n0, g.N, m, g.M, v);
         }
-        release();
-      } else if (g.vec) {
-        bool fetched_all = true;
-        auto run = [&](auto act) {
-          fetched_all = epilogue_tile<T, S::kCols, kFull, decltype(act)::value>(
-              g, &map_y, &map_z, &map_r, d, m0 + quarter * 32, n0 + c0, lane, stage,
-              &fetched[warp - 2], phase, turn, release);
-        };
-        if constexpr (kFull) with_act(g.e.act, run);
-        else run(Const<kActNone>());
-        if (!fetched_all) {
-          if (lane == 0) give_up(kSiteResidual);
-          break;
-        }
+        drain();
       } else {
-        epilogue_tile_scalar<T, S::kCols, kFull>(g, d, m0 + quarter * 32, n0 + c0, lane,
-                                           reinterpret_cast<float*>(stage), release);
+        bool stored = false;
+        if constexpr (!kPieces) {
+          if (g.vec) {
+            stored = true;
+            bool fetched_all = true;
+            auto run = [&](auto act) {
+              fetched_all = epilogue_tile<T, S::kCols, kFull, decltype(act)::value>(
+                  g, &map_y, &map_z, &map_r, d, m0 + quarter * 32, n0 + c0, lane, stage,
+                  &fetched[warp - 2], phase, turn, drain);
+            };
+            if constexpr (kFull) with_act(g.e.act, run);
+            else run(Const<kActNone>());
+            if (!fetched_all) {
+              if (lane == 0) give_up(kSiteResidual);
+              break;
+            }
+          }
+        }
+        if (!stored)
+          epilogue_tile_scalar<TO, S::kCols, kFull>(g, d, m0 + quarter * 32, n0 + c0, lane,
+                                                    reinterpret_cast<float*>(stage), drain);
       }
     }
     if constexpr (!SWAP)
@@ -970,8 +1076,8 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
               }
             }
             if (m < g.M) {
-              if constexpr (SWAP) gated_col<T, NC>(g.e, n0 + c, g.N, m, g.M, v, w);
-              else gated_row<T, NC>(g.e, g.vec, m, n0 + c, g.N, v, w);
+              if constexpr (SWAP) gated_col<TO, NC>(g.e, n0 + c, g.N, m, g.M, v, w);
+              else gated_row<TO, NC>(g.e, g.vec, m, n0 + c, g.N, v, w);
             }
           }
         };
@@ -1011,8 +1117,8 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
             for (int i = 0; i < NC; ++i) v[i] += part[r][i];
           }
           if (m < g.M) {
-            if constexpr (SWAP) epilogue_col<T, NC>(g.e, n0 + c, g.N, m, g.M, v);
-            else epilogue_row<T, NC>(g.e, g.vec, m, n0 + c, g.N, v);
+            if constexpr (SWAP) epilogue_col<TO, NC>(g.e, n0 + c, g.N, m, g.M, v);
+            else epilogue_row<TO, NC>(g.e, g.vec, m, n0 + c, g.N, v);
           }
         }
       };
@@ -1021,7 +1127,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
         else if (cols % 4 == 0) columns(Const<4>());
         else columns(Const<2>());
       } else {
-        columns(Const<8>());
+        columns(Const<16 / sizeof(TO)>());
       }
     }
     cluster_sync();  // the peers may still read this CTA's sums

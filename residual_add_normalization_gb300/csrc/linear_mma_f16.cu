@@ -131,8 +131,10 @@ cudaError_t launch_mma(const Product& p, cudaStream_t stream) {
   if (!status) return cudaErrorSymbolNotFound;
   const bool a_kc = p.a.k_contiguous, b_kc = p.b.k_contiguous;
   MmaPlan plan = p.forced;
-  if (plan.cg == 0) plan = plan_mma(p.M, p.N, p.K, b_kc, p.gated, sms);
-  else if (!mma_plan_ok(plan, p.M, p.K, a_kc, b_kc, p.gated)) return cudaErrorNotSupported;
+  const int64_t K = p.piece_a ? (p.K + kMmaK - 1) / kMmaK * kMmaK * kWalks : p.K;
+  if (plan.cg == 0) plan = plan_mma(p.M, p.N, K, b_kc, p.gated, sms);
+  else if (!mma_plan_ok(plan, p.M, K, a_kc, b_kc, p.gated)) return cudaErrorNotSupported;
+  if (p.piece_a) return launch_mma_f32(p, plan, sms, status, stream);
   if (p.gated)
     return p.t == DType::F16 ? launch_mma_gated_t<__half>(p, plan, sms, status, stream)
                              : launch_mma_gated_t<__nv_bfloat16>(p, plan, sms, status, stream);

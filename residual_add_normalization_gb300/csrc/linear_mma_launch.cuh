@@ -40,11 +40,13 @@ bool encode_operand(CUtensorMap* map, const Operand& o, int64_t n, int64_t k, in
                         : encode_rows<T>(map, o.p, n, k, o.ld, 64);
 }
 
-template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false>
+template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false,
+          typename TO = T>
 cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
                              cudaStream_t stream) {
-  using S = MmaShape<CG, BN, SWAP, GATED>;
-  auto* fn = linear_mma_kernel<T, CG, BN, A_KC, B_KC, SWAP, GATED>;
+  using S = MmaShape<CG, BN, SWAP, GATED, !std::is_same<T, TO>::value>;
+  auto* fn = linear_mma_kernel<T, CG, BN, A_KC, B_KC, SWAP, GATED, TO>;
+  constexpr bool kPieces = !std::is_same<T, TO>::value;
   constexpr bool kMeet = GATED && SWAP;
   constexpr int kTileM = kMeet ? kMmaRows / 2 : kMmaRows;
   constexpr int kTileN = GATED && !SWAP ? BN / 2 : BN;
@@ -57,6 +59,10 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   g.tiles_m = static_cast<int>((g.M + CG * kTileM - 1) / (CG * kTileM));
   g.tiles_n = static_cast<int>((g.N + kTileN - 1) / kTileN);
   g.gate = GATED ? p.N : 0;
+  g.walk = g.kblocks;
+  g.piece_a = static_cast<int>(SWAP ? p.piece_b : p.piece_a);
+  g.piece_b = static_cast<int>(SWAP ? p.piece_a : p.piece_b);
+  if (kPieces) g.kblocks *= kWalks;
   g.splits = plan.splits;
   g.e = p.epi;
   const void* outs[] = {p.epi.y, p.epi.z, p.epi.bias, p.epi.residual};
@@ -75,11 +81,18 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   // the weight's rows: twice the result's columns with a gate, in two copies for a CTA
   const int64_t rows_a = kMeet ? 2 * g.M : g.M, rows_b = GATED && !SWAP ? 2 * g.N : g.N;
   constexpr int kBoxB = GATED && !SWAP && CG == 1 ? S::kBRows / 2 : S::kBRows;
-  if (!encode_operand<T>(&map_a, a, rows_a, p.K, kTileM) ||
-      !encode_operand<T>(&map_b, b, rows_b, p.K, kBoxB))
+  // (a row of pieces is read over its whole length, zeros between them included)
+  auto encode = [&](CUtensorMap* map, const Operand& o, int64_t n, int64_t piece, int box) {
+    if (!kPieces) return encode_operand<T>(map, o, n, p.K, box);
+    return o.k_contiguous ? encode_operand<T>(map, o, n, 3 * piece, box)
+                          : encode_operand<T>(map, o, 3 * piece, p.K, box);
+  };
+  if (!encode(&map_a, a, rows_a, g.piece_a, kTileM) || !encode(&map_b, b, rows_b, g.piece_b, kBoxB))
     return cudaErrorInvalidValue;
   CUtensorMap map_y = {}, map_z = {}, map_r = {};
-  if (GATED && !SWAP && g.vec && g.splits == 1) {
+  if (kPieces) {
+    // results leave by ordinary stores
+  } else if (GATED && !SWAP && g.vec && g.splits == 1) {
     T* z = static_cast<T*>(p.epi.z);
     const bool ok = encode_rows<T>(&map_y, p.epi.y, p.N, p.M, p.N, 32) &&
                     (!z || (encode_rows<T>(&map_z, z, p.N, p.M, 2 * p.N, 32) &&
@@ -150,22 +163,36 @@ cudaError_t launch_mma_layout(const Product& p, const MmaPlan& plan, int sms, un
 }
 
 // A gate and what it gates.
-template <typename T>
+template <typename T, typename TO = T>
 cudaError_t launch_mma_gated_t(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
                                cudaStream_t stream) {
   if (plan.swap) {
     switch (plan.bn) {
       case 16:
-        return launch_mma_shape<T, 1, 16, true, true, true, true>(p, plan, sms, status, stream);
+        return launch_mma_shape<T, 1, 16, true, true, true, true, TO>(p, plan, sms, status, stream);
       case 32:
-        return launch_mma_shape<T, 1, 32, true, true, true, true>(p, plan, sms, status, stream);
+        return launch_mma_shape<T, 1, 32, true, true, true, true, TO>(p, plan, sms, status, stream);
       default:
-        return launch_mma_shape<T, 1, 64, true, true, true, true>(p, plan, sms, status, stream);
+        return launch_mma_shape<T, 1, 64, true, true, true, true, TO>(p, plan, sms, status, stream);
     }
   }
   if (plan.cg == 2)
-    return launch_mma_shape<T, 2, 256, true, true, false, true>(p, plan, sms, status, stream);
-  return launch_mma_shape<T, 1, 128, true, true, false, true>(p, plan, sms, status, stream);
+    return launch_mma_shape<T, 2, 256, true, true, false, true, TO>(p, plan, sms, status, stream);
+  return launch_mma_shape<T, 1, 128, true, true, false, true, TO>(p, plan, sms, status, stream);
+}
+
+// float32 results of operands in pieces: a gradient's two products.
+template <bool A_KC>
+cudaError_t launch_mma_pieces(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
+                              cudaStream_t stream) {
+  using T = __nv_bfloat16;
+  if (plan.cg == 2)
+    return launch_mma_shape<T, 2, 256, A_KC, false, false, false, float>(p, plan, sms, status,
+                                                                         stream);
+  if (plan.bn == 128)
+    return launch_mma_shape<T, 1, 128, A_KC, false, false, false, float>(p, plan, sms, status,
+                                                                         stream);
+  return launch_mma_shape<T, 1, 64, A_KC, false, false, false, float>(p, plan, sms, status, stream);
 }
 
 template <typename T>

@@ -299,3 +299,120 @@ def test_results_past_2_31_elements():
     # here and there; wrong rows would be off by their whole size
     for a, b in ((h[-300:], last), (z[-300:], lz), (dx[-300:], d)):
         assert float((a.float() - b.float()).norm() / b.float().norm()) <= 2.0 ** -8
+
+
+# -- float32 products in pieces: rows, in, out with 16 rows and 2^26 products or more ----------
+
+PIECES = [(700, 640, 160), (513, 1027, 131), (20, 2048, 1700), (40, 1500, 1200), (2100, 128, 260),
+          (90, 520, 1537)]
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", PIECES)
+def test_float32_in_pieces(rows, n_in, n_out):
+    """Within the bounds of binary32 sums, and in the norm better than a binary32 step; the
+    gradients too."""
+    check_forward(rows, n_in, n_out, torch.float32, seed=21)
+    g = gen(22)
+    x, w = tensor(g, (rows, n_in), torch.float32), tensor(g, (2 * n_out, n_in), torch.float32, 0.05)
+    dh, z = tensor(g, (rows, n_out), torch.float32, 0.3), tensor(g, (rows, 2 * n_out), torch.float32)
+    ref, bound = G.gated_grad(dh.cpu(), x.cpu(), w.cpu(), z.cpu(), "silu")
+    got = b2.gated_linear_grad(dh, x, w, z)
+    for a, r, e, name in zip(got, ref, bound, ("dx", "dw", "db")):
+        assert_within(a, r, e, name)
+        assert float((a.double().cpu() - r).norm() / r.norm()) <= 8 * 2.0 ** -24, name
+    for i, one in enumerate((dict(want_weight=False, want_bias=False),
+                             dict(want_input=False, want_bias=False),
+                             dict(want_input=False, want_weight=False))):
+        assert torch.equal(b2.gated_linear_grad(dh, x, w, z, **one)[i], got[i])
+
+
+@pytest.mark.parametrize("tiling", TILINGS)
+def test_every_tiling_in_pieces(tiling):
+    """Whole numbers with 11 and 13 bits, which need two pieces each; sums stay below 2^24 (2^35
+    by magnitude in pieces' products, each exact), so that every bit is known."""
+    rows, n_in, n_out = (16, 2112, 2001) if tiling[3] else (300, 640, 363)
+    assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+    g = gen(23)
+    x = torch.randint(-1500, 1501, (rows, n_in), generator=g, device="cuda")
+    x *= torch.rand(x.shape, generator=g, device="cuda") < 0.01
+    w = torch.randint(-400, 401, (2 * n_out, n_in), generator=g, device="cuda")
+    want = x.double() @ w.double().t()
+    assert float((x.double().abs() @ w.double().abs().t()).max()) < 2 ** 24
+    h, z = b2.gated_linear(x.float(), w.float(), activation=0, want_z=True)
+    assert torch.equal(z.double(), want)
+    assert torch.equal(h, (want[:, :n_out].float() * want[:, n_out:].float()))
+
+
+def test_the_gradients_tilings_in_pieces():
+    """The same of both products of a gradient: z of gates 1 without an activation, so that dz
+    is dh twice."""
+    rows, n_in, n_out = 333, 580, 420
+    g = gen(24)
+    x = torch.randint(-300, 301, (rows, n_in), generator=g, device="cuda")
+    w = torch.randint(-300, 301, (2 * n_out, n_in), generator=g, device="cuda")
+    dh = torch.randint(-700, 701, (rows, n_out), generator=g, device="cuda")
+    dh *= torch.rand(dh.shape, generator=g, device="cuda") < 0.05
+    z = torch.ones(rows, 2 * n_out, device="cuda")
+    dz = torch.cat((dh, dh), 1).double()
+    wants = dz @ w.double(), dz.t() @ x.double(), dz.sum(0)
+    assert max(float((dz.abs() @ w.double().abs()).max()),
+               float((dz.abs().t() @ x.double().abs()).max())) < 2 ** 24
+    for tiling in [(0, 0, 0, 0), (2, 256, 1, 0), (1, 128, 1, 0), (1, 128, 4, 0), (1, 64, 1, 0),
+                   (1, 64, 8, 0)]:
+        assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+        got = b2.gated_linear_grad(dh.float(), x.float(), w.float(), z, activation=0)
+        for a, want in zip(got, wants):
+            assert torch.equal(a.double(), want), tiling
+
+
+def test_pieces_of_any_magnitude():
+    """Rows from 2^-60 to 2^60 in size, and a row of the largest numbers: each is as accurate as
+    the others.  What is not finite stays in its row or column."""
+    rows, n_in, n_out = 121, 1024, 600
+    g = gen(25)
+    x = tensor(g, (rows, n_in), torch.float32)
+    x *= (2.0 ** torch.arange(-60, 61, device="cuda")).unsqueeze(1)
+    w = tensor(g, (2 * n_out, n_in), torch.float32, 0.03)
+    _, z = b2.gated_linear(x, w, want_z=True)
+    want = x.double() @ w.double().t()
+    off = (z.double() - want).norm(dim=1) / want.norm(dim=1)
+    assert float(off.max()) <= 8 * 2.0 ** -24
+    top = torch.finfo(torch.float32).max
+    big = torch.zeros_like(x)
+    big[:, 0] = top
+    small = torch.full_like(w, 2.0 ** -130)
+    _, z = b2.gated_linear(big, small, want_z=True)
+    assert float(z.sub(top * 2.0 ** -130).abs().max()) <= 2.0 ** -24 * 2.0 ** -2
+    bad = x.clone()
+    bad[5, 7], bad[9, 1] = float("nan"), float("inf")
+    h, _ = b2.gated_linear(bad, w)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[5] = keep[9] = False
+    assert torch.equal(h[keep], b2.gated_linear(x, w)[0][keep])
+    assert bool(torch.isnan(h[5]).all()) and not bool(torch.isfinite(h[9]).any())
+
+
+@pytest.mark.parametrize("tiling", [(2, 256, 1, 0), (1, 128, 1, 0), (1, 128, 4, 0), (1, 16, 2, 1)])
+def test_waits_in_pieces_give_up(tiling):
+    lib = b2.library()
+    g = gen(26)
+    x, w = tensor(g, (16, 2048), torch.float32), tensor(g, (2 * 2200, 2048), torch.float32)
+    assert lib.b200norm_testing_force_linear(*tiling) == 0
+    want, _ = b2.gated_linear(x, w)
+    b2.linear_status()
+    try:
+        for stall in (True, False):
+            if stall:
+                assert lib.b200norm_testing_linear_stall(1, 20_000_000) == 0
+            else:
+                assert lib.b200norm_testing_linear_withhold(1, 20_000_000) == 0
+            t0 = time.monotonic()
+            b2.gated_linear(x, w)
+            with pytest.raises(b2.B200NormError) as e:
+                b2.linear_status()
+            assert e.value.status == TIMEOUT and time.monotonic() - t0 < 5.0
+            assert lib.b200norm_testing_linear_stall(0, 0) == 0
+    finally:
+        lib.b200norm_testing_linear_withhold(0, 0)
+    b2.linear_status()
+    assert torch.equal(b2.gated_linear(x, w)[0], want)

@@ -37,7 +37,7 @@ cudaError_t launch_product(const Product& p, cudaStream_t stream) {
   if (p.piece_a) return launch_mma(p, stream);
   const bool mma = mma_operand_ok(p.a, p.t) && mma_operand_ok(p.b, p.t) && p.K > 0;
   if (p.a.k_contiguous && p.b.k_contiguous && !(mma && p.forced.cg) &&
-      few_rows(p.M, p.gated ? 2 * p.N : p.N, p.K, p.t, mma)) {
+      (p.gated ? gated_few_rows(p.M, p.N, p.K, p.t, mma) : few_rows(p.M, p.N, p.K, p.t, mma))) {
     switch (p.t) {
       case DType::F32: return launch_rows<float>(p, stream);
       case DType::F16: return launch_rows<__half>(p, stream);

@@ -103,15 +103,17 @@ LinearPlan gated_plan(int64_t rows, int64_t in, int64_t out, DType t, bool align
 }
 
 LinearGradPlan gated_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {
-  if (t != DType::F32 || !gated_pieces(rows, in, out))
-    return linear_grad_plan(rows, in, 2 * out, t, kActSilu, aligned16);
   LinearGradPlan p = {};
-  p.make_dz = p.pieces = true;
-  p.ldz = 3 * piece_of(2 * out);
-  p.part = round_256(static_cast<size_t>(rows) * p.ldz * 2);
-  p.x = p.part + round_256(static_cast<size_t>(linear_db_parts(rows, 2 * out)) * 2 * out * 4);
-  p.w = p.x + round_256(static_cast<size_t>(rows) * 3 * piece_of(in) * 2);
-  p.bytes = p.w + round_256(static_cast<size_t>(2 * out) * 3 * piece_of(in) * 2);
+  const bool half = t != DType::F32;
+  p.make_dz = true;
+  p.pieces = !half && gated_pieces(rows, in, out);
+  p.pack = half && (in % 8 != 0 || !aligned16);
+  p.ldz = p.pieces ? 3 * piece_of(2 * out) : half ? pitch16(2 * out) : 2 * out;
+  const int64_t pitch = p.pieces ? 3 * piece_of(in) : p.pack ? pitch16(in) : 0;
+  p.part = round_256(static_cast<size_t>(rows) * p.ldz * (p.pieces ? 2 : dtype_size(t)));
+  p.x = p.part + round_256(static_cast<size_t>(gated_db_parts(rows, out, t)) * 2 * out * 4);
+  p.w = p.x + round_256(static_cast<size_t>(rows) * pitch * 2);
+  p.bytes = p.w + round_256(static_cast<size_t>(2 * out) * pitch * 2);
   return p;
 }
 

@@ -582,8 +582,6 @@ __global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const LinearDz
   }
 }
 
-// Of a gate and what it gates: dz = [dh * up * act'(gate) | dh * act(gate)], and the column
-// sums of both, in the same way: three reads and two writes per element of the result.
 // PIECES (float32): dz as the products' operand, three bfloat16 pieces.
 __device__ __forceinline__ void pieces_of(float v, __nv_bfloat16 (&p)[3]) {
   // each piece the rounding of what the ones before leave, which is exact in binary32; what
@@ -618,91 +616,78 @@ __device__ __forceinline__ void store_pieces(__nv_bfloat16* dst, int64_t piece,
   for (int i = 0; i < 3; ++i) *reinterpret_cast<Pack<__nv_bfloat16, VE>*>(dst + i * piece) = p[i];
 }
 
+// Of a gate and what it gates: dz = [dh * up * act'(gate) | dh * act(gate)], and the column
+// sums of both.  Bound by HBM: three reads and two writes per element of the result.  CTA
+// (stripe, part): a thread has VE columns and walks the part's rows, so that a row's accesses
+// lie side by side and its sums stay in its registers.
 template <typename T, int VE, int ACT, bool PIECES>
 __device__ __forceinline__ void gated_dz_rows(const LinearDzCall& c, int64_t r0, int64_t r1,
                                               int64_t col, float (&sum)[2][VE]) {
   const T* dh = static_cast<const T*>(c.dy) + col;
   const T* z = static_cast<const T*>(c.z) + col;
   T* dz = static_cast<T*>(c.dz);
-  constexpr int U = 4;  // rows on their way at once
-  for (int64_t r = r0; r < r1; r += U * kDzWarps) {
-    Pack<T, VE> d[U], a[U], b[U];
+  Pack<T, VE> d = {}, a = {}, b = {};
+  auto fetch = [&](int64_t row) {
+    if (row >= r1) return;
+    d = ld_stream<T, VE>(dh + row * c.out);
+    a = ld_stream<T, VE>(z + row * 2 * c.out);
+    b = ld_stream<T, VE>(z + (row * 2 + 1) * c.out);
+  };
+  fetch(r0);
+#pragma unroll 1
+  for (int64_t row = r0; row < r1; ++row) {
+    float f[VE], gate[VE], up[VE];
+    unpack(d, f);
+    unpack(a, gate);
+    unpack(b, up);
+    fetch(row + 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = r + u * kDzWarps;
-      if (row >= r1) continue;
-      d[u] = ld_stream<T, VE>(dh + row * c.out);
-      a[u] = ld_stream<T, VE>(z + row * 2 * c.out);
-      b[u] = ld_stream<T, VE>(z + (row * 2 + 1) * c.out);
+    for (int e = 0; e < VE; ++e) {
+      float value, slope;
+      act_both<ACT>(gate[e], value, slope);
+      gate[e] = __fmul_rn(__fmul_rn(f[e], up[e]), slope);
+      up[e] = __fmul_rn(f[e], value);
+      sum[0][e] = __fadd_rn(sum[0][e], gate[e]);  // same bits without dz
+      sum[1][e] = __fadd_rn(sum[1][e], up[e]);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = r + u * kDzWarps;
-      if (row >= r1) continue;
-      float f[VE], gate[VE], up[VE];
-      unpack(d[u], f);
-      unpack(a[u], gate);
-      unpack(b[u], up);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        float value, slope;
-        act_both<ACT>(gate[e], value, slope);
-        gate[e] = __fmul_rn(__fmul_rn(f[e], up[e]), slope);
-        up[e] = __fmul_rn(f[e], value);
-        sum[0][e] = __fadd_rn(sum[0][e], gate[e]);  // same bits without dz
-        sum[1][e] = __fadd_rn(sum[1][e], up[e]);
+    if constexpr (PIECES) {
+      __nv_bfloat16* at = static_cast<__nv_bfloat16*>(c.dz);
+      if (at) {
+        store_pieces<VE>(at + row * c.ldz + col, c.piece, gate);
+        store_pieces<VE>(at + row * c.ldz + c.out + col, c.piece, up);
       }
-      if constexpr (PIECES) {
-        __nv_bfloat16* at = static_cast<__nv_bfloat16*>(c.dz);
-        if (at) {
-          store_pieces<VE>(at + row * c.ldz + col, c.piece, gate);
-          store_pieces<VE>(at + row * c.ldz + c.out + col, c.piece, up);
-        }
-      } else if (dz) {
-        *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + col) = pack_from<T, VE>(gate);
-        *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + c.out + col) = pack_from<T, VE>(up);
-      }
+    } else if (dz) {
+      *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + col) = pack_from<T, VE>(gate);
+      *reinterpret_cast<Pack<T, VE>*>(dz + row * c.ldz + c.out + col) = pack_from<T, VE>(up);
     }
   }
 }
 
 template <typename T, int VE, bool PIECES = false>
-__global__ void __launch_bounds__(32 * kDzWarps) gated_dz_kernel(const LinearDzCall c, int parts) {
+__global__ void __launch_bounds__(kGatedDzThreads, 4) gated_dz_kernel(const LinearDzCall c,
+                                                                      int parts) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float red[kDzWarps][32 * VE];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * VE;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * VE;
   const int part = blockIdx.y;
   const int64_t r0 = c.rows * part / parts, r1 = c.rows * (part + 1) / parts;
-  float sum[2][VE] = {};
-  if (col < c.out)
-    with_act(c.act, [&](auto act) {
-      gated_dz_rows<T, VE, decltype(act)::value, PIECES>(c, r0 + warp, r1, col, sum);
-    });
   if (PIECES && c.dz && blockIdx.x == 0) {  // the rest of each piece: zeros
     const int rest = static_cast<int>(c.piece - 2 * c.out);
-    for (int64_t r = r0 + warp; r < r1; r += kDzWarps)
-      for (int i = lane; i < 3 * rest; i += 32)
+    for (int i = threadIdx.x; i < 3 * rest; i += blockDim.x)
+      for (int64_t r = r0; r < r1; ++r)
         static_cast<__nv_bfloat16*>(c.dz)[r * c.ldz + i / rest * c.piece + 2 * c.out + i % rest] =
             from_f32<__nv_bfloat16>(0.0f);
   }
+  if (col >= c.out) return;
+  float sum[2][VE] = {};
+  with_act(c.act, [&](auto act) {
+    gated_dz_rows<T, VE, decltype(act)::value, PIECES>(c, r0, r1, col, sum);
+  });
   if (!c.db) return;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int e = 0; e < VE; ++e) red[warp][lane * VE + e] = sum[s][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * VE; i += 32 * kDzWarps) {
-      const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 * VE + i;
-      if (at >= c.out) continue;
-      float t = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kDzWarps; ++w) t += red[w][i];
-      c.part[part * 2 * c.out + s * c.out + at] = t;
-    }
-    __syncthreads();
-  }
+    for (int e = 0; e < VE; ++e) c.part[(part * 2 + s) * c.out + col + e] = sum[s][e];
 }
 
 // The parts added in a fixed order: a CTA takes 32 columns, its 32 warps every

@@ -110,6 +110,17 @@ inline int linear_db_parts(int64_t rows, int64_t out) {
   if (p > 1024) p = 1024;
   return static_cast<int>(p < 1 ? 1 : p);
 }
+// The same of a gated call: about four CTAs of 256 threads (a thread has 16 bytes of a row)
+// for each SM, four rows or more in each part.
+constexpr int kGatedDzThreads = 256;
+inline int gated_db_parts(int64_t rows, int64_t out, DType t) {
+  const int64_t cols = kGatedDzThreads * (t == DType::F32 ? 4 : 8);
+  int64_t p = 152 * 4 / ((out + cols - 1) / cols);
+  const int64_t most = (rows + 3) / 4;
+  if (p > most) p = most;
+  if (p > 1024) p = 1024;
+  return static_cast<int>(p < 1 ? 1 : p);
+}
 // gated: `out` columns of the result, z and dz with twice as many.
 cudaError_t launch_linear_dz(const LinearDzCall& c, bool gated, cudaStream_t stream);
 

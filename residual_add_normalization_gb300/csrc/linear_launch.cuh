@@ -104,16 +104,17 @@ cudaError_t launch_dz(const LinearDzCall& c, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_gated_dz(const LinearDzCall& c, cudaStream_t stream) {
   constexpr int VE = 16 / sizeof(T);
-  const int parts = c.rows > 0 ? linear_db_parts(c.rows, 2 * c.out) : 0;
+  const int parts = c.rows > 0 ? gated_db_parts(c.rows, c.out, c.t) : 0;
   cudaError_t e = cudaSuccess;
   if (parts > 0) {
     // (pieces start at multiples of 64 elements, and so do their rows)
     const Operand dh{c.dy, c.out, true}, z{c.z, c.out, true}, dz{c.dz, c.ldz, true};
     const bool vec = vectors_ok(dh, sizeof(T)) && vectors_ok(z, sizeof(T)) &&
                      (c.piece || vectors_ok(dz, sizeof(T)));
-    const int cols = 32 * (vec ? VE : 1);
-    const dim3 grid(static_cast<unsigned>((c.out + cols - 1) / cols), parts);
-    auto go = [&](auto* fn) { return launch_pdl(fn, grid, 32 * kDzWarps, stream, c, parts); };
+    const int64_t per = vec ? VE : 1, threads = (c.out / per + 31) / 32 * 32;
+    const int block = static_cast<int>(threads < kGatedDzThreads ? threads : kGatedDzThreads);
+    const dim3 grid(static_cast<unsigned>((c.out + block * per - 1) / (block * per)), parts);
+    auto go = [&](auto* fn) { return launch_pdl(fn, grid, block, stream, c, parts); };
     if constexpr (sizeof(T) == 4) {
       if (c.piece) e = go(vec ? gated_dz_kernel<T, VE, true> : gated_dz_kernel<T, 1, true>);
     }

@@ -456,7 +456,9 @@ B200NORM_API b200norm_status b200norm_gated_linear(
  *              aligned16: x and weight start on 16-byte boundaries.
  *
  * Sums are binary32, in a fixed order; large float32 calls as in b200norm_gated_linear (and
- * dz in pieces too).  rows == 0 stores zeros in dw and db.
+ * dz in pieces too).  In 16-bit types the rounded dz has the type's range: in float16 a
+ * product dh * z above 65,504 in magnitude may become an infinity.  rows == 0 stores zeros
+ * in dw and db.
  */
 B200NORM_API size_t b200norm_gated_linear_grad_workspace_size(int64_t rows, int64_t in_features,
                                                               int64_t out_features,
@@ -486,9 +488,10 @@ B200NORM_API b200norm_status b200norm_linear_status(b200norm_stream_t stream);
  * the inverse has -s, and is the rotation's gradient.  With R = rotary_size, pair i
  * (i < R / 2) is elements (i, i + R / 2) of the head, or (2 i, 2 i + 1) when
  * interleaved; elements from R on stay as they are.  Angles are exact to about
- * 2^-25 of a radian, and 2^-53 of p f, at any position.
+ * 2^-25 of a radian, 2^-53 of p f and 2^-64 p of a turn, at any position.
  *
- * RMS norm of a head, before its rotation: u = x / sqrt(mean(x^2) + epsilon) * gamma.
+ * RMS norm of a head, before its rotation: u = x / sqrt(mean(x^2) + epsilon) * gamma,
+ * with binary32 sums of squares.
  */
 typedef struct b200norm_rotation {
   const void* positions;   /* int32 or int64: of token t of sequence b at

@@ -72,19 +72,19 @@ cudaError_t head_raise(Fn fn, size_t smem, std::atomic<unsigned long long>& rais
   return e;
 }
 
-// CTAs of a kernel that are resident at once (0: unknown); `seen` keeps the last answer,
+// CTAs of a kernel that are resident at once (152 if unknown); `seen` keeps the last answer,
 // which depends on the device and on the shared memory.
 template <class Fn>
 int64_t head_resident(Fn fn, size_t smem, std::atomic<unsigned long long>& seen) {
   int dev = 0, sms = 0, per = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
   const unsigned long long key = (static_cast<unsigned long long>(dev) << 32 | smem) + 1;
   const unsigned long long last = seen.load();  // key << 16 | CTAs
   if (last >> 16 == key) return static_cast<int64_t>(last & 0xffff);
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, 32 * kHeadWarps, smem) !=
           cudaSuccess)
-    return 0;
+    return 152;
   const int64_t ctas = static_cast<int64_t>(sms) * per;
   if (ctas <= 0xffff) seen.store(key << 16 | static_cast<unsigned long long>(ctas));
   return ctas;
@@ -104,8 +104,9 @@ cudaError_t launch_heads_t(const HeadsCall& c, cudaStream_t stream) {
       const size_t smem = head_smem<T, VE, K>(g, false);
       if (const cudaError_t e = head_raise(fn, smem, raised)) return e;
       int64_t grid = (all + kHeadWarps - 1) / kHeadWarps;
-      const int64_t most = grid > 1 ? head_resident(fn, smem, seen) : 0;
-      if (most > 0 && grid > most) grid = most;
+      // resident at once: a warp's share is an equal part of all steps
+      const int64_t most = grid > 1 ? head_resident(fn, smem, seen) : 1;
+      if (grid > most) grid = most;
       return launch_clusters(fn, dim3(static_cast<unsigned>(grid)), 32 * kHeadWarps, 1, smem,
                              stream, g);
     };

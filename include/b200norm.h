@@ -22,8 +22,9 @@
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer to a dense, contiguous,
- *     row-major tensor owned by the caller (heads have strides of their own).  The library never allocates,
- *     frees or synchronises; it only enqueues kernels on `stream`.
+ *     row-major tensor owned by the caller (heads have strides of their own).
+ *     The library never allocates, frees or synchronises; it only enqueues
+ *     kernels on `stream`.
  *   - Pointers need only be aligned to their element size.  16-byte aligned
  *     pointers (with spans that are whole 16-byte vectors) take the vector
  *     path; anything else takes a scalar path with identical results.
@@ -470,8 +471,9 @@ B200NORM_API b200norm_status b200norm_gated_linear_grad(
     void* workspace, size_t workspace_bytes, b200norm_stream_t stream);
 
 /* Synchronise `stream`, then read the device-side record of the linear
- * operator's kernels (the gated ones as well) on the current device.  With 16-bit types their roles wait
- * on one another through shared memory; the waits are bounded (a second and
+ * operator's kernels (the gated ones as well) on the current device.  On the
+ * tensor cores (16-bit types, large gated float32 calls) their roles wait on
+ * one another through shared memory; the waits are bounded (a second and
  * more for long sums), and one that gives up records
  * B200NORM_ERR_DEVICE_TIMEOUT in a per-device word, with the kind of the first
  * such wait, and ends early (that call's outputs are then undefined).  Returns B200NORM_OK, or

@@ -269,7 +269,8 @@ Wide heads_extent(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size) {
          static_cast<Wide>(a.heads - 1) * a.strides[2] + size;
 }
 
-b200norm_status check_heads(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size, size_t es) {
+b200norm_status check_heads(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size,
+                            size_t es) {
   if (!a.p) return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s is required", a.name);
   if (!aligned(a.p, es))
     return fail(B200NORM_ERR_INVALID_ARGUMENT, "%s is not aligned to its element size", a.name);
@@ -277,7 +278,8 @@ b200norm_status check_heads(const HeadsArg& a, int64_t batch, int64_t seq, int64
     if (a.strides[i] < 0)
       return fail(B200NORM_ERR_INVALID_ARGUMENT, "strides of %s must be >= 0", a.name);
   if (heads_extent(a, batch, seq, size) > static_cast<Wide>(INT64_MAX) / 8)
-    return fail(B200NORM_ERR_INVALID_ARGUMENT, "strides of %s reach past the address space", a.name);
+    return fail(B200NORM_ERR_INVALID_ARGUMENT, "strides of %s reach past the address space",
+                a.name);
   return B200NORM_OK;
 }
 
@@ -1042,11 +1044,13 @@ b200norm_status b200norm_head_rms_rotary_grad(
   for (int i = 0; i < nout; ++i) {
     for (int j = 0; j < nin; ++j)
       if (!heads_apart(out[i], in[j], batch, seq, head_size, es))
-        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", out[i].name, in[j].name);
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", out[i].name,
+                    in[j].name);
     const Range r = heads_range(out[i], batch, seq, head_size, es);
     for (int j = 0; j < nfin; ++j)
       if (overlaps(r, flat_in[j]))
-        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", r.name, flat_in[j].name);
+        return fail(B200NORM_ERR_INVALID_ARGUMENT, "output %s overlaps %s", r.name,
+                    flat_in[j].name);
     for (int j = 0; j < nfout; ++j)
       if (overlaps(r, flat_out[j]))
         return fail(B200NORM_ERR_INVALID_ARGUMENT, "outputs %s and %s overlap", r.name,
@@ -1072,10 +1076,12 @@ b200norm_status b200norm_head_rms_rotary_grad(
       const Range r = heads_range(out[i], batch, seq, head_size, es);
       all[n++] = {r.p, r.bytes, es, r.name, true};
     }
-    for (int i = 0; i < nfin; ++i) all[n++] = {flat_in[i].p, flat_in[i].bytes, 1, flat_in[i].name, false};
-    for (int i = 0; i < nfout; ++i) all[n++] = {flat_out[i].p, flat_out[i].bytes, 1, flat_out[i].name, true};
-    const size_t need =
-        head_parts_bytes(head_parts(batch * seq, c.set[0].heads, c.set[1].heads, head_size), head_size);
+    for (int i = 0; i < nfin; ++i)
+      all[n++] = {flat_in[i].p, flat_in[i].bytes, 1, flat_in[i].name, false};
+    for (int i = 0; i < nfout; ++i)
+      all[n++] = {flat_out[i].p, flat_out[i].bytes, 1, flat_out[i].name, true};
+    const HeadParts parts = head_parts(batch * seq, c.set[0].heads, c.set[1].heads, head_size);
+    const size_t need = head_parts_bytes(parts, head_size);
     if (b200norm_status st = check_workspace(workspace, workspace_bytes, need, all, n)) return st;
     c.part = static_cast<float*>(workspace);
   }

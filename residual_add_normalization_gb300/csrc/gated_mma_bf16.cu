@@ -3,7 +3,7 @@
 
 namespace b200norm {
 
-template cudaError_t launch_mma_gated_t<__nv_bfloat16>(const Product&, const MmaPlan&, int, unsigned*,
-                                             cudaStream_t);
+template cudaError_t launch_mma_gated_t<__nv_bfloat16>(const Product&, const MmaPlan&, int,
+                                                       unsigned*, cudaStream_t);
 
 }  // namespace b200norm

@@ -52,9 +52,11 @@ cudaError_t launch_product(const Product& p, cudaStream_t stream) {
 cudaError_t launch_linear_dz(const LinearDzCall& c, bool gated, cudaStream_t stream) {
   switch (c.t) {
     case DType::F32: return gated ? launch_gated_dz<float>(c, stream) : launch_dz<float>(c, stream);
-    case DType::F16: return gated ? launch_gated_dz<__half>(c, stream) : launch_dz<__half>(c, stream);
+    case DType::F16:
+      return gated ? launch_gated_dz<__half>(c, stream) : launch_dz<__half>(c, stream);
     default:
-      return gated ? launch_gated_dz<__nv_bfloat16>(c, stream) : launch_dz<__nv_bfloat16>(c, stream);
+      return gated ? launch_gated_dz<__nv_bfloat16>(c, stream)
+                   : launch_dz<__nv_bfloat16>(c, stream);
   }
 }
 

@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Plai
             acc[r][o].x = fmaf(to_f32(xv.v[0]), to_f32(q[u][o].v[0]), acc[r][o].x);
           } else {
 #pragma unroll
-            for (int i = 0; i < VE / 2; ++i) acc[r][o] = fma2(get2(xv, i), get2(q[u][o], i), acc[r][o]);
+            for (int i = 0; i < VE / 2; ++i)
+              acc[r][o] = fma2(get2(xv, i), get2(q[u][o], i), acc[r][o]);
           }
         }
       }

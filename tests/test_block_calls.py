@@ -133,7 +133,7 @@ def test_outputs_and_workspace_stay_until_the_stream_has_passed(entry):
     shapes = {"rotary": [q.shape, q.shape], "head_rms_rotary_grad": [q.shape, q.shape],
               "gated_linear": [dh.shape, z.shape], "gated_linear_grad": [x.shape, w.shape]}[entry]
     outs = [torch.empty(s, device="cuda") for s in shapes]
-    ws = torch.empty(64 * MIB, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(128 * MIB, dtype=torch.uint8, device="cuda")
     calls = {
         "rotary": lambda: b2.rotary(q, q, p, f, q_out=outs[0], k_out=outs[1], stream=side),
         "head_rms_rotary_grad": lambda: b2.head_rms_rotary_grad(
@@ -156,7 +156,7 @@ def test_outputs_and_workspace_stay_until_the_stream_has_passed(entry):
     outs.clear()
     del ws, call, calls
     again = [torch.empty(s, device="cuda") for s in shapes]
-    again.append(torch.empty(64 * MIB, dtype=torch.uint8, device="cuda"))
+    again.append(torch.empty(128 * MIB, dtype=torch.uint8, device="cuda"))
     assert not side.query()  # the call is still ahead
     assert not used & {t.data_ptr() for t in again}
     torch.cuda.synchronize()

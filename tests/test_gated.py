@@ -289,7 +289,8 @@ def test_results_past_2_31_elements():
     """z of more than 2^31 elements: its last rows against the same rows by themselves."""
     rows, n_in, n_out = (1 << 31) // 16384 + 300, 64, 8192
     g = gen(14)
-    x, w = tensor(g, (rows, n_in), torch.bfloat16), tensor(g, (2 * n_out, n_in), torch.bfloat16, 0.1)
+    x = tensor(g, (rows, n_in), torch.bfloat16)
+    w = tensor(g, (2 * n_out, n_in), torch.bfloat16, 0.1)
     h, z = b2.gated_linear(x, w, want_z=True)
     last, lz = b2.gated_linear(x[-300:].contiguous(), w, want_z=True)
     dx, _, _ = b2.gated_linear_grad(h, x, w, z, want_weight=False, want_bias=False)
@@ -314,7 +315,8 @@ def test_float32_in_pieces(rows, n_in, n_out):
     check_forward(rows, n_in, n_out, torch.float32, seed=21)
     g = gen(22)
     x, w = tensor(g, (rows, n_in), torch.float32), tensor(g, (2 * n_out, n_in), torch.float32, 0.05)
-    dh, z = tensor(g, (rows, n_out), torch.float32, 0.3), tensor(g, (rows, 2 * n_out), torch.float32)
+    dh = tensor(g, (rows, n_out), torch.float32, 0.3)
+    z = tensor(g, (rows, 2 * n_out), torch.float32)
     ref, bound = G.gated_grad(dh.cpu(), x.cpu(), w.cpu(), z.cpu(), "silu")
     got = b2.gated_linear_grad(dh, x, w, z)
     for a, r, e, name in zip(got, ref, bound, ("dx", "dw", "db")):

@@ -175,7 +175,8 @@ def test_in_place_and_into_rows(size, rot, t):
     gamma = torch.randn(size, generator=g, device="cuda")
     want = b2.head_rms_rotary(q, k, gamma, gamma, p, f)
     into = torch.full_like(base, 7.0)
-    out = b2.head_rms_rotary(q, k, gamma, gamma, p, f, q_out=into[:, :, 2:8], k_out=into[:, :, 8:10])
+    out = b2.head_rms_rotary(q, k, gamma, gamma, p, f, q_out=into[:, :, 2:8],
+                             k_out=into[:, :, 8:10])
     assert out[0].data_ptr() == into[:, :, 2:8].data_ptr()
     for v, w in zip(out, want):
         assert torch.equal(v, w)
@@ -212,7 +213,8 @@ def test_nan_and_infinity_stay_where_they_are(t, interleaved):
     same[list(pair)] = False
     same[60] = False
     assert torch.equal(y[0, 4, 2][same.cuda()], clean[0, 4, 2][same.cuda()])
-    assert bool(torch.isnan(y[0, 4, 2, 60])) and not bool(torch.isfinite(y[0, 4, 2, list(pair)]).any())
+    assert bool(torch.isnan(y[0, 4, 2, 60]))
+    assert not bool(torch.isfinite(y[0, 4, 2, list(pair)]).any())
     yn = b2.head_rms_rotary(bad, None, None, None, p, f, interleaved=interleaved)[0]
     rows = torch.ones(9, 5, dtype=torch.bool, device="cuda")
     rows[4, 2] = False

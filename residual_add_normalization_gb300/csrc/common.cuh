@@ -359,6 +359,13 @@ __device__ __forceinline__ Moments merge(Moments a, Moments b) {
 // at once.  pdl_trigger() lets the next grid on the stream be scheduled once
 // every CTA of this one has started (or exited); it does not release that
 // grid's own pdl_wait() early.
+//
+// A grid that needs nothing of the one before it, only of earlier ones, may run
+// beside it and wait at its own end (`late`), so that it is complete only after
+// all before it.  It may do so where the grid before it triggers after its own
+// wait, or is such a grid behind one that does: the trigger then says that all
+// earlier grids are complete.  It reads through L2 (tensor copies, __ldcg), as
+// no wait of its own stands before its loads.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void pdl_trigger() {

@@ -6,19 +6,22 @@ namespace b200norm {
 extern template cudaError_t launch_rows<float>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<float>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_gated_dz<float>(const LinearDzCall&, cudaStream_t);
+extern template cudaError_t launch_db<float>(const LinearDzCall&, bool, bool, cudaStream_t);
 extern template cudaError_t launch_rows<__half>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__half>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_gated_dz<__half>(const LinearDzCall&, cudaStream_t);
+extern template cudaError_t launch_db<__half>(const LinearDzCall&, bool, bool, cudaStream_t);
 extern template cudaError_t launch_pack<__half>(const void*, void*, int64_t, const void*,
                                       void*, int64_t, int64_t, cudaStream_t);
 extern template cudaError_t launch_rows<__nv_bfloat16>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__nv_bfloat16>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_gated_dz<__nv_bfloat16>(const LinearDzCall&, cudaStream_t);
+extern template cudaError_t launch_db<__nv_bfloat16>(const LinearDzCall&, bool, bool, cudaStream_t);
 extern template cudaError_t launch_pack<__nv_bfloat16>(const void*, void*, int64_t, const void*,
                                              void*, int64_t, int64_t, cudaStream_t);
 
 cudaError_t launch_pieces(const void* src0, void* dst0, int64_t rows0, const void* src1,
-                          void* dst1, int64_t rows1, int64_t n, cudaStream_t stream);
+                          void* dst1, int64_t rows1, int64_t n, bool late, cudaStream_t stream);
 
 namespace {
 
@@ -57,6 +60,15 @@ cudaError_t launch_linear_dz(const LinearDzCall& c, bool gated, cudaStream_t str
     default:
       return gated ? launch_gated_dz<__nv_bfloat16>(c, stream)
                    : launch_dz<__nv_bfloat16>(c, stream);
+  }
+}
+
+cudaError_t launch_linear_db(const LinearDzCall& c, bool gated, bool late, cudaStream_t stream) {
+  if (!c.db) return cudaSuccess;
+  switch (c.t) {
+    case DType::F32: return launch_db<float>(c, gated, late, stream);
+    case DType::F16: return launch_db<__half>(c, gated, late, stream);
+    default: return launch_db<__nv_bfloat16>(c, gated, late, stream);
   }
 }
 
@@ -134,7 +146,7 @@ cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStrea
   if (plan.pieces) {
     char* ws = static_cast<char*>(c.workspace);
     const cudaError_t e =
-        launch_pieces(c.x, ws + plan.x, c.rows, c.w, ws + plan.w, 2 * c.out, c.in, stream);
+        launch_pieces(c.x, ws + plan.x, c.rows, c.w, ws + plan.w, 2 * c.out, c.in, false, stream);
     if (e != cudaSuccess) return e;
     p.piece_a = p.piece_b = piece_of(c.in);
     p.a = {ws + plan.x, 3 * p.piece_a, true};
@@ -143,31 +155,40 @@ cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStrea
   return launch_product(p, stream);
 }
 
+// Launches that need nothing of one another run side by side: the pieces beside dz, dW beside
+// dx, and behind these the last step of db (one after another: gated bf16 512 x 1024 x 1024
+// 26 us, 22 so; 16384 x 768 x 768 117 and 97, with dz's four CTAs an SM).
 cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& plan,
                                cudaStream_t stream) {
   char* ws = static_cast<char*>(c.workspace);
   const int64_t out = c.gated ? 2 * c.out : c.out;  // rows of the weight
   void* made = plan.make_dz && (c.dx || c.dw) ? ws + plan.dz : nullptr;
   cudaError_t e = cudaSuccess;
+  const LinearDzCall d{c.dy, c.z, made, plan.ldz, c.db, reinterpret_cast<float*>(ws + plan.part),
+                       c.rows, c.out, c.act, c.t, plan.pieces ? piece_of(out) : 0};
   if (made || c.db) {
-    const LinearDzCall d{c.dy, c.z, made, plan.ldz, c.db, reinterpret_cast<float*>(ws + plan.part),
-                         c.rows, c.out, c.act, c.t, plan.pieces ? piece_of(out) : 0};
     e = launch_linear_dz(d, c.gated, stream);
     if (e != cudaSuccess) return e;
   }
+  if (c.rows == 0) {  // empty sums: the zero of every type is zero bits
+    e = launch_linear_db(d, c.gated, false, stream);
+    if (e != cudaSuccess || !c.dw) return e;
+    return cudaMemsetAsync(c.dw, 0, static_cast<size_t>(out) * c.in * dtype_size(c.t), stream);
+  }
   if (plan.pieces && (c.dx || c.dw)) {
     e = launch_pieces(c.x, ws + plan.x, c.dw ? c.rows : 0, c.w, ws + plan.w, c.dx ? out : 0, c.in,
-                      stream);
+                      true, stream);
     if (e != cudaSuccess) return e;
   }
-  if (plan.pack && c.rows > 0 && (c.dx || c.dw)) {
+  if (plan.pack && (c.dx || c.dw)) {
     e = pack_rows(c.t, c.x, ws + plan.x, c.dw ? c.rows : 0, c.w, ws + plan.w, c.dx ? out : 0,
                   c.in, stream);
     if (e != cudaSuccess) return e;
   }
+  int ctas = 0;  // of dx
   const void* dz = plan.make_dz ? made : c.dy;
   const int64_t ldz = plan.make_dz ? plan.ldz : out;
-  if (c.dx && c.rows > 0) {
+  if (c.dx) {
     Operand w{c.w, c.in, false};
     if (plan.pack) w = {ws + plan.w, pitch16(c.in), false};
     Product p{{dz, ldz, true}, w, c.rows, c.in, out,
@@ -177,11 +198,10 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& pl
       p.piece_b = piece_of(c.in);
       p.b = {ws + plan.w, 3 * p.piece_b, false};
     }
+    p.ctas = &ctas;
     e = launch_product(p, stream);
     if (e != cudaSuccess) return e;
   }
-  if (c.dw && c.rows == 0)  // empty sums: the zero of every type is zero bits
-    return cudaMemsetAsync(c.dw, 0, static_cast<size_t>(out) * c.in * dtype_size(c.t), stream);
   if (c.dw) {
     Operand x{c.x, c.in, false};
     if (plan.pack) x = {ws + plan.x, pitch16(c.in), false};
@@ -192,9 +212,13 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& pl
       p.piece_b = piece_of(c.in);
       p.b = {ws + plan.x, 3 * p.piece_b, false};
     }
+    // beside a dx that leaves many SMs, or none but at its end; the first CTAs on a few idle SMs
+    // cost dx more than they gain (128 CTAs, 512 x 2048 x 2048 bf16: 40.3 us, 36.3)
+    p.late = c.dx && (ctas <= 152 * 2 / 3 || ctas >= 152);
     e = launch_product(p, stream);
+    if (e != cudaSuccess) return e;
   }
-  return e;
+  return launch_linear_db(d, c.gated, c.dx || c.dw, stream);
 }
 
 }  // namespace b200norm

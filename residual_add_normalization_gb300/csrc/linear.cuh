@@ -695,8 +695,8 @@ __global__ void __launch_bounds__(kGatedDzThreads, 4) gated_dz_kernel(const Line
 // 32nd part each, then the warps' sums are added.
 template <typename T>
 __global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, T* db, int64_t out,
-                                                         int parts) {
-  pdl_wait();
+                                                         int parts, bool late) {
+  if (!late) pdl_wait();
   pdl_trigger();
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -704,15 +704,17 @@ __global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, T* d
   float t = 0.0f;
   if (col < out) {
 #pragma unroll 4
-    for (int p = warp; p < parts; p += 32) t += part[p * out + col];
+    for (int p = warp; p < parts; p += 32) t += __ldcg(part + p * out + col);
   }
   red[warp][lane] = t;
   __syncthreads();
-  if (warp != 0 || col >= out) return;
-  t = 0.0f;
+  if (warp == 0 && col < out) {
+    t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 32; ++w) t += red[w][lane];
-  db[col] = from_f32<T>(t);
+    for (int w = 0; w < 32; ++w) t += red[w][lane];
+    db[col] = from_f32<T>(t);
+  }
+  if (late) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -783,6 +785,6 @@ struct PieceRows {
 
 __global__ void __launch_bounds__(256) linear_pieces_kernel(const PieceRows first,
                                                             const PieceRows second, int64_t n,
-                                                            int64_t piece, bool vec);
+                                                            int64_t piece, bool vec, bool late);
 
 }  // namespace b200norm

@@ -49,6 +49,10 @@ struct Product {
   // row (a multiple of 64; where k is contiguous, the rest of a piece is zeros); t is F32.
   // (0: operands of type t.)
   int64_t piece_a = 0, piece_b = 0;
+  // The launch before this one is a product of the same call, of whose result nothing here is
+  // needed: the tensor-core kernels run beside it.
+  bool late = false;
+  int* ctas = nullptr;  // receives how many CTAs a tensor-core product was launched with
 };
 
 cudaError_t launch_product(const Product& p, cudaStream_t stream);
@@ -123,6 +127,9 @@ inline int gated_db_parts(int64_t rows, int64_t out, DType t) {
 }
 // gated: `out` columns of the result, z and dz with twice as many.
 cudaError_t launch_linear_dz(const LinearDzCall& c, bool gated, cudaStream_t stream);
+// Then the parts of the column sums into db (nothing without it); late: the launch before is a
+// product behind the former.
+cudaError_t launch_linear_db(const LinearDzCall& c, bool gated, bool late, cudaStream_t stream);
 
 // gated: y = act(gate) * up of out columns each; weight, bias, z (and db, dw) of both.
 struct LinearCall {

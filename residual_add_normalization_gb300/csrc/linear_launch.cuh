@@ -94,9 +94,6 @@ cudaError_t launch_dz(const LinearDzCall& c, cudaStream_t stream) {
     e = vec ? launch_pdl(linear_dz_kernel<T, VE>, grid, 32 * kDzWarps, stream, c, parts)
             : launch_pdl(linear_dz_kernel<T, 1>, grid, 32 * kDzWarps, stream, c, parts);
   }
-  if (e == cudaSuccess && c.db)
-    e = launch_pdl(linear_db_kernel<T>, dim3(static_cast<unsigned>((c.out + 31) / 32)), 1024,
-                   stream, static_cast<const float*>(c.part), static_cast<T*>(c.db), c.out, parts);
   return e;
 }
 
@@ -114,17 +111,29 @@ cudaError_t launch_gated_dz(const LinearDzCall& c, cudaStream_t stream) {
     const int64_t per = vec ? VE : 1, threads = (c.out / per + 31) / 32 * 32;
     const int block = static_cast<int>(threads < kGatedDzThreads ? threads : kGatedDzThreads);
     const dim3 grid(static_cast<unsigned>((c.out + block * per - 1) / (block * per)), parts);
-    auto go = [&](auto* fn) { return launch_pdl(fn, grid, block, stream, c, parts); };
+    // Four CTAs on each SM: without the shared memory that lets no fifth in, the SMs that the
+    // launch before left first took more, and 16384 x 512 x 512 bf16 gradients, one after
+    // another, took 85 us (63).  Fewer CTAs would wait for SMs that they can share.
+    const size_t smem = static_cast<int64_t>(grid.x) * grid.y > 2 * 152 ? 46 * 1024 : 0;
+    auto go = [&](auto* fn) {
+      return launch_clusters(fn, grid, block, 1, smem, stream, c, parts);
+    };
     if constexpr (sizeof(T) == 4) {
       if (c.piece) e = go(vec ? gated_dz_kernel<T, VE, true> : gated_dz_kernel<T, 1, true>);
     }
     if (!c.piece) e = go(vec ? gated_dz_kernel<T, VE> : gated_dz_kernel<T, 1>);
   }
-  if (e == cudaSuccess && c.db)
-    e = launch_pdl(linear_db_kernel<T>, dim3(static_cast<unsigned>((2 * c.out + 31) / 32)), 1024,
-                   stream, static_cast<const float*>(c.part), static_cast<T*>(c.db), 2 * c.out,
-                   parts);
   return e;
+}
+
+template <typename T>
+cudaError_t launch_db(const LinearDzCall& c, bool gated, bool late, cudaStream_t stream) {
+  const int64_t out = gated ? 2 * c.out : c.out;
+  const int parts = c.rows == 0 ? 0
+                    : gated     ? gated_db_parts(c.rows, c.out, c.t)
+                                : linear_db_parts(c.rows, c.out);
+  return launch_pdl(linear_db_kernel<T>, dim3(static_cast<unsigned>((out + 31) / 32)), 1024, stream,
+                    static_cast<const float*>(c.part), static_cast<T*>(c.db), out, parts, late);
 }
 
 // Dense rows of n elements to rows pitch16(n) apart, of one operand or two.

@@ -74,6 +74,7 @@ struct MmaArgs {
   bool vec;            // rows of the result, bias and residual are whole 16-byte vectors
   unsigned* status;
   unsigned long long limit_ns;
+  bool late;           // pdl_wait() at the end
   bool stall;          // a test: nothing is copied, and the waits give up
   unsigned withhold;   // a test: the site whose event is left out (0: none)
 };
@@ -750,7 +751,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
   if (CG == 2 || g.splits > 1) cluster_sync();  // the peers' barriers are ready
   tc_fence_after();
   const unsigned tmem = tmem_slot;
-  pdl_wait();
+  if (!g.late) pdl_wait();
   pdl_trigger();  // after the allocation: a later grid cannot take the columns first
 
   // this CTA's (pair's) tiles and its part of K
@@ -1139,6 +1140,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     tc_fence_after();
     tmem_free<CG>(tmem, S::kTmem);
   }
+  if (g.late) pdl_wait();
 }
 
 }  // namespace b200norm

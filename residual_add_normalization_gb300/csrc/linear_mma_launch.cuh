@@ -72,6 +72,7 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   g.status = status;
   // a wait lasts a tile at most: a second, and 4 us for each slice of K
   g.limit_ns = 1000000000ull + 4000ull * g.kblocks;
+  g.late = p.late;
   g.stall = linear_stall_limit_ns() != 0;
   if (g.stall) g.limit_ns = linear_stall_limit_ns();
   const LinearWithhold withhold = linear_withhold();
@@ -127,6 +128,7 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
+  if (p.ctas) *p.ctas = static_cast<int>(units * cluster);
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;

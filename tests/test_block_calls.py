@@ -107,6 +107,50 @@ def test_dependent_launch_changes_nothing():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("t,rows,n_in,n_out", [
+    (torch.bfloat16, 300, 264, 136), (torch.float16, 520, 1024, 520), (torch.float32, 300, 520, 520),
+    (torch.bfloat16, 4100, 512, 520), (torch.bfloat16, 130, 77, 65), (torch.float32, 40, 64, 36)])
+def test_gradients_one_after_another(t, rows, n_in, n_out):
+    """The launches of a gradient that run side by side: calls on end whose inputs the launch
+    before has just written, whose results the next reads and whose workspace is one, against
+    the same with every launch waiting for the one before it; eager and replayed."""
+    g, lib = gen(12), b2.library()
+    xs = [torch.randn(rows, n_in, generator=g, device="cuda").to(t) for _ in range(6)]
+    w = (torch.randn(2 * n_out, n_in, generator=g, device="cuda") * 0.05).to(t)
+    dh = torch.randn(rows, n_out, generator=g, device="cuda").to(t)
+    x, ws = torch.empty_like(xs[0]), torch.empty(64 * MIB, dtype=torch.uint8, device="cuda")
+
+    def run():
+        out = []
+        for v in xs:
+            x.copy_(v)
+            h, z = b2.gated_linear(x, w, want_z=True, workspace=ws)
+            dx, dw, db = b2.gated_linear_grad(dh, x, w, z, workspace=ws)
+            # the results, read by the next launches
+            out += [dx, dw, db, *b2.gated_linear_grad(h, dx, w, z, workspace=ws)]
+            _, dwl, dbl = b2.linear_grad(z, dx, dw, workspace=ws)
+            out += [dwl, dbl]
+        return out
+
+    assert lib.b200norm_testing_set_pdl(0) == OK
+    try:
+        want = run()
+        torch.cuda.synchronize()
+    finally:
+        assert lib.b200norm_testing_set_pdl(1) == OK
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(), want))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = run()
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    b2.linear_status()
+
+
 def test_a_side_stream_s_calls():
     run = everything(10)
     want = run()

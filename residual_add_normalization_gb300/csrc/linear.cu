@@ -97,17 +97,19 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, 
   return p;
 }
 
-// Below 2^26 products of a half the copies cost what the tensor cores gain: 128 x 768 x 768
-// (rows, in, out) takes 16.1 us forward on the binary32 units and 16.2 in pieces, 512 x 768 x 768
-// 40 and 24.5, its gradients 72 and 48, 2048 x 1024 x 2048 387 and 89, 1086 and 246, but
-// 256 x 256 x 256 9.4 and 10.5, 21 and 27.  The weight's copy wants a few rows to serve:
-// 32 x 4096 x 4096 126 and 110.
-bool gated_pieces(int64_t rows, int64_t in, int64_t out) {
-  return rows >= 16 && rows * in * out >= int64_t{1} << 26;
+// Where the copies in pieces pay, us on the binary32 units and in pieces.  Forward, 2^26 products
+// of a half: 256 x 512 x 512 (rows, in, out) 16.1 and 12.0, 2048 x 1024 x 2048 387 and 74, but
+// 512 x 256 x 256 9.5 and 11.0.  Gradients sooner: 512 x 256 x 256 30.5 and 16.4, 256 x 256 x 256
+// 19.9 and 15.5, 512 x 768 x 768 71 and 38.  The weight's copy wants a few rows to serve:
+// 16 x 4096 x 4096 124 and 100, 167 and 148, but the gradients of 16 x 2048 x 2048 50 and 58.
+bool gated_pieces(int64_t rows, int64_t in, int64_t out, bool grad) {
+  const int64_t products = rows * in * out;
+  if (!grad) return rows >= 16 && products >= int64_t{1} << 26;
+  return rows >= 16 && products >= int64_t{1} << (rows >= 64 ? 24 : 27);
 }
 
 LinearPlan gated_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {
-  if (t != DType::F32 || !gated_pieces(rows, in, out))
+  if (t != DType::F32 || !gated_pieces(rows, in, out, false))
     return linear_plan(rows, in, 2 * out, t, aligned16);
   LinearPlan p = {};
   p.pieces = true;
@@ -120,7 +122,7 @@ LinearGradPlan gated_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, b
   LinearGradPlan p = {};
   const bool half = t != DType::F32;
   p.make_dz = true;
-  p.pieces = !half && gated_pieces(rows, in, out);
+  p.pieces = !half && gated_pieces(rows, in, out, true);
   p.pack = half && (in % 8 != 0 || !aligned16);
   p.ldz = p.pieces ? 3 * piece_of(2 * out) : half ? pitch16(2 * out) : 2 * out;
   const int64_t pitch = p.pieces ? 3 * piece_of(in) : p.pack ? pitch16(in) : 0;

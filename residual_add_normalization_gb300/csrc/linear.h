@@ -65,7 +65,7 @@ inline bool mma_operand_ok(const Operand& o, DType t) {
   return t != DType::F32 && o.ld % 8 == 0 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0;
 }
 
-MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, bool gated, int sms);
+MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, bool gated, bool pieces, int sms);
 cudaError_t launch_mma(const Product& p, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_mma_t(const Product& p, const MmaPlan& plan, int sms, unsigned* status,
@@ -204,7 +204,7 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, 
                                 bool aligned16);
 // The plans of a gated call (`out` counts the result's columns).  float32 products are made
 // on the tensor cores where the copies in pieces pay (gated_pieces).
-bool gated_pieces(int64_t rows, int64_t in, int64_t out);
+bool gated_pieces(int64_t rows, int64_t in, int64_t out, bool grad);
 inline int64_t piece_of(int64_t n) { return (n + 63) / 64 * 64; }
 LinearPlan gated_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);
 LinearGradPlan gated_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16);

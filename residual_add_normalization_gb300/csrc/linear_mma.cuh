@@ -36,11 +36,13 @@
 //
 // TO float with bfloat16 operands: float32 products.  An operand's row holds three pieces
 // of its values side by side (each the rounding of what the ones before leave: 24 bits in
-// all), and K is walked six times, over the pairs of pieces whose products reach 2^-24 of
-// the whole, the smallest first.  The tensor cores cut a sum's last place at each addition of
-// 16 products (4.4e-6 in the norm over 4096 of k), so the last walk is added up in short
-// chunks, and the chunks' sums are added with rounding, in tensor memory, by the epilogue's
-// warps (5e-7 then; the library's float32 product 1.2e-6).
+// all).  The three pieces of a slice of K arrive one after another, and the six pairs of them
+// whose products reach 2^-24 of the whole are multiplied while they are in shared memory (K
+// walked once for each pair took twice the copies: 4096 x 4096 x 8192 1,124 us, 939 so).  The
+// tensor cores cut a sum's last place at each addition of 16 products (4.4e-6 in the norm over
+// 4096 of k), so each slice has a sum of its own, the pair of the first pieces last, and the
+// slices' sums are added with rounding by the epilogue's warps, in their registers (1.5e-7 over
+// 10,330 of k; the library's float32 product 1.8e-6).
 //
 // Every wait is bounded: the first that gives up records its site in `status`;
 // one that gives up ends its role, the others then run out as well, and all meet
@@ -68,8 +70,7 @@ struct MmaArgs {
   int tiles_m, tiles_n;
   int splits;
   int64_t gate;        // GATED: columns of the result (the weight has twice as many rows)
-  int walk;            // pieces: slices of one walk over K, and elements from an operand's
-  int piece_a, piece_b;  // piece to the next
+  int piece_a, piece_b;  // pieces: elements from one of an operand's to the next
   Epilogue e;
   bool vec;            // rows of the result, bias and residual are whole 16-byte vectors
   unsigned* status;
@@ -79,8 +80,8 @@ struct MmaArgs {
   unsigned withhold;   // a test: the site whose event is left out (0: none)
 };
 
-// Shared memory of a CTA: the ring, then 8 KB for each epilogue warp's results
-// (unless SWAP).  Two small CTAs share an SM.
+// Shared memory of a CTA: the ring, then room for each epilogue warp's results (unless
+// SWAP): two of 4 KB, or with pieces one of 32 by 33 floats.  Two small CTAs share an SM.
 constexpr int kMmaStageRows = 32 * 128;  // 32 rows of 64 results, 128 bytes each
 template <int CG, int BN, bool SWAP, bool GATED = false, bool PIECES = false>
 struct MmaShape {
@@ -94,14 +95,17 @@ struct MmaShape {
   static constexpr int kWarps = BN >= (GATED ? 256 : 128) ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kWarps;
   static constexpr int kCols = BN / (kWarps / 4);
-  static constexpr int kOut = SWAP ? 0 : kWarps * 2 * kMmaStageRows;
-  static constexpr int kBudget = (BN <= 64 ? 112 * 1024 : 225 * 1024) - kOut;
+  static constexpr int kStageOut = PIECES ? 32 * 33 * 4 : 2 * kMmaStageRows;
+  static constexpr int kOut = SWAP ? 0 : kWarps * kStageOut;
+  // (with pieces two slices of K, six stages, and for that the SM to itself)
+  static constexpr int kCtas = BN <= 64 && (SWAP || !PIECES) ? 2 : 1;  // on an SM
+  static constexpr int kBudget =
+      (kCtas == 2 ? 112 * 1024 : PIECES ? 226 * 1024 : 225 * 1024) - kOut;
   static constexpr int kStages = kBudget / kStageBytes > 8 ? 8 : kBudget / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
-  // buffers of columns for sums (with pieces of 256 columns, there is room for one beside
-  // the chunks' total), and what is allocated: a power of two
-  static constexpr int kBuffers = PIECES && BN == 256 ? 1 : 2;
-  static constexpr int kColumns = (kBuffers + (PIECES ? 1 : 0)) * BN;
+  // buffers of columns for sums, and what is allocated: a power of two
+  static constexpr int kBuffers = 2;
+  static constexpr int kColumns = kBuffers * BN;
   static constexpr int kTmem = kColumns <= 32    ? 32
                                : kColumns <= 64  ? 64
                                : kColumns <= 128 ? 128
@@ -695,12 +699,6 @@ __device__ __forceinline__ void gated_col(const Epilogue& e, int64_t m, int64_t 
 
 // -- kernel ---------------------------------------------------------------------
 
-// The pieces of A and of B on walk w over K, a hexadecimal digit each.
-constexpr unsigned kPieceA = 0x001012, kPieceB = 0x010210;
-constexpr int kWalks = 6;
-constexpr int kChunk = 4;         // slices of a chunk on the last walk,
-constexpr int kChunkBefore = 256;  // and on those before, whose sums are 2^-8 of the whole
-
 // (GATED: map_z is of z's gate columns, map_r of the others.)
 template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false,
           typename TO = T>
@@ -771,16 +769,6 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     tm = first + t % per % size;
     tn = t % per / size;
   };
-  // past the last slice of the chunk that slice kb begins: all of K, but for pieces
-  auto chunk_end = [&](int kb) {
-    if constexpr (kPieces) {
-      const int last = (kWalks - 1) * g.walk;
-      const int end = kb < last ? (last - kb < kChunkBefore ? last : kb + kChunkBefore)
-                                : kb + kChunk;
-      return end < k_hi ? end : k_hi;
-    }
-    return k_hi;
-  };
   auto give_up = [&](unsigned site) {
     if (atomicCAS(g.status, 0u, kStatusDeviceTimeout) == 0u) atomicExch(g.status + 1, site);
   };
@@ -798,7 +786,9 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
         const int n0 = GATED && !SWAP
                            ? tn * kTileN + (CG == 2 ? static_cast<int>(rank) * gate : 0)
                            : tn * BN + (CG == 2 ? static_cast<int>(rank) * S::kBRows : 0);
-        for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+        constexpr int kParts = kPieces ? 3 : 1;
+        for (int q = k_lo * kParts; q < k_hi * kParts; ++q, ++it) {
+          const int kb = q / kParts;
           const int s = it % kStages;
           if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, wait_limit(g, kSiteEmpty))) {
             give_up(kSiteEmpty);
@@ -809,12 +799,12 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           unsigned char* a = ring + s * S::kStageBytes;
           unsigned char* b = a + kMmaABytes;
           const unsigned bar = full0 + s * 8;
-          int k = kb * kMmaK, xa = 0, xb = 0;  // along K, and along the operands' rows
-          if constexpr (kPieces) {
-            const int w = kb / g.walk;
-            k = (kb - w * g.walk) * kMmaK;
-            xa = static_cast<int>(kPieceA >> (4 * w) & 15) * g.piece_a;
-            xb = static_cast<int>(kPieceB >> (4 * w) & 15) * g.piece_b;
+          const int k = kb * kMmaK;
+          int xa = 0, xb = 0;  // along the operands' rows
+          if constexpr (kPieces) {  // the second, the first, the third
+            const int r = q - kb * kParts, piece = r == 0 ? 1 : r == 1 ? 0 : 2;
+            xa = piece * g.piece_a;
+            xb = piece * g.piece_b;
           }
           if constexpr (kMeet) {
             tma_load<CG>(a, &map_a, xa + k, m0, bar);
@@ -854,6 +844,7 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       int it = 0, n = 0;
       bool alive = true;
       for (int t = unit; t < tiles && alive; t += units) {
+        // a sum over all of this CTA's K, or with pieces over a slice
         for (int kb = k_lo; kb < k_hi && alive; ++n) {
           const int buf = n % S::kBuffers;
           if (!mbar_wait(&drained[buf], ((n / S::kBuffers) & 1) ^ 1, wait_limit(g, kSiteDrained))) {
@@ -863,22 +854,47 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           }
           tc_fence_after();
           const unsigned d = tmem + buf * BN;
-          const int first = kb;
-          for (const int end = chunk_end(kb); kb < end; ++kb, ++it) {
-            const int s = it % kStages;
-            if (!mbar_wait(&full[s], (it / kStages) & 1, g.limit_ns)) {
-              give_up(kSiteFull);
-              alive = false;
-              break;
-            }
+          unsigned at[3];  // stages
+          auto arrived = [&](int i) {
+            const int s = (it + i) % kStages;
+            at[i] = smem_addr(ring + s * S::kStageBytes);
+            alive = mbar_wait(&full[s], ((it + i) / kStages) & 1, g.limit_ns);
+            if (!alive) give_up(kSiteFull);
             tc_fence_after();
-            const unsigned a = smem_addr(ring + s * S::kStageBytes);
+            return alive;
+          };
+          auto multiply = [&](unsigned a, unsigned b, bool add) {  // A of one stage, B of another
             const unsigned long long da = smem_desc(a, 8192);
-            const unsigned long long db = smem_desc(a + kMmaABytes, 8192);
+            const unsigned long long db = smem_desc(b + kMmaABytes, 8192);
 #pragma unroll
             for (int k = 0; k < kMmaK / 16; ++k)
-              mma_f16<CG>(d, da + k * step_a, db + k * step_b, idesc, kb > first || k > 0);
-            if (g.withhold != kSiteEmpty) mma_commit<CG>(&empty[s]);
+              mma_f16<CG>(d, da + k * step_a, db + k * step_b, idesc, add || k > 0);
+          };
+          auto used = [&](int i) {
+            if (g.withhold != kSiteEmpty) mma_commit<CG>(&empty[(it + i) % kStages]);
+          };
+          if constexpr (kPieces) {
+            // stages: the second pieces, the first, the third
+            if (!arrived(0)) break;
+            multiply(at[0], at[0], false);
+            if (!arrived(1)) break;
+            multiply(at[0], at[1], true);
+            multiply(at[1], at[0], true);
+            used(0);
+            if (!arrived(2)) break;
+            multiply(at[1], at[2], true);
+            multiply(at[2], at[1], true);
+            used(2);
+            multiply(at[1], at[1], true);
+            used(1);
+            it += 3;
+            ++kb;
+          } else {
+            const int first = kb;
+            for (; kb < k_hi && arrived(0); ++kb, ++it) {
+              multiply(at[0], at[0], kb > first);
+              used(0);
+            }
           }
           mma_commit<CG>(&sums[buf]);
         }
@@ -888,12 +904,12 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
     const int row = quarter * 32 + lane;
     const int c0 = (warp - 2) / 4 * S::kCols;  // this warp's columns of a tile: c0, kCols of them
-    unsigned char* stage = ring + S::kRing + (warp - 2) * 2 * kMmaStageRows;  // not SWAP
+    unsigned char* stage = ring + S::kRing + (warp - 2) * S::kStageOut;  // not SWAP
     unsigned phase = 0, turn = 0;
     int n = 0;
     bool alive = true;
     for (int t = unit; t < tiles && alive; t += units, ++n) {
-      auto await = [&] {  // a chunk's sums
+      auto await = [&] {  // a buffer's sums
         alive = warp_wait(&sums[n % S::kBuffers], (n / S::kBuffers) & 1, g.limit_ns);
         if (!alive && lane == 0) give_up(kSiteSums);
         tc_fence_after();
@@ -913,38 +929,35 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
       };
       unsigned at = tmem + n % S::kBuffers * BN + (static_cast<unsigned>(quarter * 32) << 16);
       if constexpr (kPieces) {
-        // the chunks added up behind the buffers, the columns that this warp stores
-        const unsigned lanes = static_cast<unsigned>(quarter * 32) << 16;
-        const unsigned total = tmem + S::kBuffers * BN + lanes;
+        // the slices' sums added up, the columns that this warp stores; then back to the last
+        // one's place
         constexpr bool kApart = GATED && !SWAP && BN == 256;  // 64 of each half
-        for (int kb = k_lo; kb < k_hi;) {
-          if (!await()) break;
-          const unsigned from = tmem + n % S::kBuffers * BN + lanes;
-#pragma unroll 1
-          for (int c = 0; c < S::kCols; c += 16) {
-            const int col = kApart ? (warp - 2) / 4 * 64 + c % 64 + c / 64 * 128 : c0 + c;
-            float v[16];
-            tmem_load16(from + col, v);
-            if (kb > k_lo) {
-              float w[16];
-              tmem_load16(total + col, w);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += w[i];
-            }
-            tmem_store16(total + col, v);
+        auto column = [&](int c) {
+          return kApart ? (warp - 2) / 4 * 64 + c % 64 + c / 64 * 128 : c0 + c;
+        };
+        float total[S::kCols / 16][16] = {};
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          if (kb > k_lo) {
+            release();
+            ++n;
           }
-          release();
-          kb = chunk_end(kb);
-          if (kb < k_hi) ++n;
+          if (!await()) break;
+          at = tmem + n % S::kBuffers * BN + (static_cast<unsigned>(quarter * 32) << 16);
+#pragma unroll
+          for (int c = 0; c < S::kCols / 16; ++c) {
+            float v[16];
+            tmem_load16(at + column(16 * c), v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) total[c][i] += v[i];
+          }
         }
         if (!alive) break;
-        at = total;
+#pragma unroll
+        for (int c = 0; c < S::kCols / 16; ++c) tmem_store16(at + column(16 * c), total[c]);
       } else if (!await()) {
         break;
       }
-      auto drain = [&] {
-        if constexpr (!kPieces) release();
-      };
+      auto drain = [&] { release(); };
       int tm, tn;
       tile_at(t, tm, tn);
       const int64_t m0 =

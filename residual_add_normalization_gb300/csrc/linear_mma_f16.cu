@@ -73,7 +73,7 @@ unsigned* linear_status_words() {
 // tile's end that nothing hides 0.8, a launch 3.0, and a sum split over a
 // cluster 2.0 and 0.5 per part.  With a gate a tile has half as many of the result's N
 // columns, and none is 128 x 64.
-MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, bool gated, int sms) {
+MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, bool gated, bool pieces, int sms) {
   const int64_t kblocks = (K + kMmaK - 1) / kMmaK;
   const int per = gated ? 2 : 1;
   const int64_t swapped = (N * per + kMmaRows - 1) / kMmaRows;
@@ -87,14 +87,14 @@ MmaPlan plan_mma(int64_t M, int64_t N, int64_t K, bool b_kc, bool gated, int sms
       p.splits *= 2;
     return p;
   }
-  MmaPlan best{1, gated ? 128 : 64, 1, false};
+  MmaPlan best{1, gated || pieces ? 128 : 64, 1, false};
   double least = 0.0;
   const struct {
     int cg, bn, slots, most;
     double slice;
   } shapes[] = {{2, 256, sms / 2, 1, 0.345}, {1, 128, sms, 4, 0.30}, {1, 64, 2 * sms, 8, 0.36}};
   for (const auto& s : shapes) {
-    if (gated && s.bn == 64) continue;
+    if ((gated || pieces) && s.bn == 64) continue;
     for (int splits = 1; splits <= s.most && splits <= kblocks; splits *= 2) {
       const int64_t rows = s.cg * kMmaRows;
       const int64_t tiles = (M + rows - 1) / rows * ((N * per + s.bn - 1) / s.bn) * splits;
@@ -131,8 +131,9 @@ cudaError_t launch_mma(const Product& p, cudaStream_t stream) {
   if (!status) return cudaErrorSymbolNotFound;
   const bool a_kc = p.a.k_contiguous, b_kc = p.b.k_contiguous;
   MmaPlan plan = p.forced;
-  const int64_t K = p.piece_a ? (p.K + kMmaK - 1) / kMmaK * kMmaK * kWalks : p.K;
-  if (plan.cg == 0) plan = plan_mma(p.M, p.N, K, b_kc, p.gated, sms);
+  // in pieces a slice of K has three times the bytes (and six times the products)
+  const int64_t K = p.piece_a ? 3 * ((p.K + kMmaK - 1) / kMmaK * kMmaK) : p.K;
+  if (plan.cg == 0) plan = plan_mma(p.M, p.N, K, b_kc, p.gated, p.piece_a != 0, sms);
   else if (!mma_plan_ok(plan, p.M, K, a_kc, b_kc, p.gated)) return cudaErrorNotSupported;
   if (p.piece_a) return launch_mma_f32(p, plan, sms, status, stream);
   if (p.gated)

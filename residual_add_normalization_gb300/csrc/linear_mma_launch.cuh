@@ -59,10 +59,8 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   g.tiles_m = static_cast<int>((g.M + CG * kTileM - 1) / (CG * kTileM));
   g.tiles_n = static_cast<int>((g.N + kTileN - 1) / kTileN);
   g.gate = GATED ? p.N : 0;
-  g.walk = g.kblocks;
   g.piece_a = static_cast<int>(SWAP ? p.piece_b : p.piece_a);
   g.piece_b = static_cast<int>(SWAP ? p.piece_a : p.piece_b);
-  if (kPieces) g.kblocks *= kWalks;
   g.splits = plan.splits;
   g.e = p.epi;
   const void* outs[] = {p.epi.y, p.epi.z, p.epi.bias, p.epi.residual};
@@ -71,7 +69,7 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
     if (reinterpret_cast<uintptr_t>(o) % 16 != 0) g.vec = false;
   g.status = status;
   // a wait lasts a tile at most: a second, and 4 us for each slice of K
-  g.limit_ns = 1000000000ull + 4000ull * g.kblocks;
+  g.limit_ns = 1000000000ull + 4000ull * g.kblocks * (kPieces ? 6 : 1);
   g.late = p.late;
   g.stall = linear_stall_limit_ns() != 0;
   if (g.stall) g.limit_ns = linear_stall_limit_ns();
@@ -122,7 +120,7 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   const int cluster = CG == 2 ? 2 : g.splits;
   int64_t units = tiles;
   if (g.splits == 1 && !kMeet) {  // persistent: as many as are resident at once
-    const int64_t most = static_cast<int64_t>(sms) * (BN <= 64 ? 2 : 1) / CG;
+    const int64_t most = static_cast<int64_t>(sms) * S::kCtas / CG;
     if (units > most) units = most;
   }
   cudaLaunchConfig_t cfg = {};

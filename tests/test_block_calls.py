@@ -109,7 +109,8 @@ def test_dependent_launch_changes_nothing():
 
 @pytest.mark.parametrize("t,rows,n_in,n_out", [
     (torch.bfloat16, 300, 264, 136), (torch.float16, 520, 1024, 520),
-    (torch.float32, 300, 520, 520), (torch.bfloat16, 4100, 512, 520), (torch.bfloat16, 130, 77, 65), (torch.float32, 40, 64, 36)])
+    (torch.float32, 300, 520, 520), (torch.bfloat16, 4100, 512, 520),
+    (torch.bfloat16, 130, 77, 65), (torch.float32, 40, 64, 36)])
 def test_gradients_one_after_another(t, rows, n_in, n_out):
     """The launches of a gradient that run side by side: calls on end whose inputs the launch
     before has just written, whose results the next reads and whose workspace is one, against

@@ -451,6 +451,9 @@ B200NORM_API b200norm_status b200norm_gated_linear(
  *   dw[o, i] = round_T(sum_r round_T(dz[r, o]) * x[r, i])
  *   db[o]    = round_T(sum_r dz[r, o])
  *
+ * (dz is not rounded where the weight and its gradient are passed in one launch: up to four
+ * rows, and up to eight of rows * in_features * F <= 2^25).
+ *
  *   dh         T, (rows, F): gradient of h.   z   of the forward call.
  *   x, weight  as in the forward call; x may be NULL without dw, weight without dx.
  *   dx, dw, db T, of x's, weight's and bias's shapes; any may be NULL when not wanted.

@@ -49,10 +49,10 @@ FAMILY_SOURCES = {
     "layer": ("common.cuh", "bulk.cuh", "pair.cuh", "launch.h", "launch_kernel.cuh", "layer.h",
               "layer.cuh", "layer_launch.cuh", "layer_f32.cu", "layer_f16.cu", "layer_bf16.cu"),
     "linear": ("common.cuh", "bulk.cuh", "pair.cuh", "launch.h", "linear.h", "linear.cuh",
-               "launch_kernel.cuh", "linear_launch.cuh", "linear.cu", "linear_f32.cu",
-               "linear_f16.cu", "linear_bf16.cu", "linear_mma.cuh", "linear_mma_launch.cuh",
-               "linear_mma_f16.cu", "linear_mma_bf16.cu", "gated_mma_f16.cu",
-               "gated_mma_bf16.cu", "gated_mma_f32.cu"),
+               "launch_kernel.cuh", "linear_launch.cuh", "gated_few.cuh", "linear.cu",
+               "linear_f32.cu", "linear_f16.cu", "linear_bf16.cu", "linear_mma.cuh",
+               "linear_mma_launch.cuh", "linear_mma_f16.cu", "linear_mma_bf16.cu",
+               "gated_mma_f16.cu", "gated_mma_bf16.cu", "gated_mma_f32.cu"),
     "heads": ("common.cuh", "launch.h", "launch_kernel.cuh", "heads.h", "heads.cuh",
               "heads_launch.cuh", "heads.cu", "heads_f32.cu", "heads_f16.cu", "heads_bf16.cu"),
 }

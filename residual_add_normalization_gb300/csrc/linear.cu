@@ -1,4 +1,5 @@
 // The linear operator's host side: which kernel a product takes.
+#include "gated_few.cuh"
 #include "linear_launch.cuh"
 
 namespace b200norm {
@@ -7,16 +8,20 @@ extern template cudaError_t launch_rows<float>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<float>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_gated_dz<float>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_db<float>(const LinearDzCall&, bool, bool, cudaStream_t);
+extern template cudaError_t launch_gated_few<float>(const GatedFewArgs&, void*, cudaStream_t);
 extern template cudaError_t launch_rows<__half>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__half>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_gated_dz<__half>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_db<__half>(const LinearDzCall&, bool, bool, cudaStream_t);
+extern template cudaError_t launch_gated_few<__half>(const GatedFewArgs&, void*, cudaStream_t);
 extern template cudaError_t launch_pack<__half>(const void*, void*, int64_t, const void*,
                                       void*, int64_t, int64_t, cudaStream_t);
 extern template cudaError_t launch_rows<__nv_bfloat16>(const Product&, cudaStream_t);
 extern template cudaError_t launch_dz<__nv_bfloat16>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_gated_dz<__nv_bfloat16>(const LinearDzCall&, cudaStream_t);
 extern template cudaError_t launch_db<__nv_bfloat16>(const LinearDzCall&, bool, bool, cudaStream_t);
+extern template cudaError_t launch_gated_few<__nv_bfloat16>(
+    const GatedFewArgs&, void*, cudaStream_t);
 extern template cudaError_t launch_pack<__nv_bfloat16>(const void*, void*, int64_t, const void*,
                                              void*, int64_t, int64_t, cudaStream_t);
 
@@ -120,6 +125,11 @@ LinearPlan gated_plan(int64_t rows, int64_t in, int64_t out, DType t, bool align
 
 LinearGradPlan gated_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {
   LinearGradPlan p = {};
+  if (gated_few(rows, in, out, t)) {
+    p.few = true;
+    p.bytes = round_256(static_cast<size_t>(gated_few_parts(rows, in, out, t)) * rows * in * 4);
+    return p;
+  }
   const bool half = t != DType::F32;
   p.make_dz = true;
   p.pieces = !half && gated_pieces(rows, in, out, true);
@@ -163,6 +173,15 @@ cudaError_t launch_linear(const LinearCall& c, const LinearPlan& plan, cudaStrea
 cudaError_t launch_linear_grad(const LinearGradCall& c, const LinearGradPlan& plan,
                                cudaStream_t stream) {
   char* ws = static_cast<char*>(c.workspace);
+  if (plan.few) {
+    const GatedFewArgs a{c.dy, c.x, c.w, c.z, c.dw, c.db,
+                         c.dx ? reinterpret_cast<float*>(ws) : nullptr, c.rows, c.in, c.out, c.act};
+    switch (c.t) {
+      case DType::F32: return launch_gated_few<float>(a, c.dx, stream);
+      case DType::F16: return launch_gated_few<__half>(a, c.dx, stream);
+      default: return launch_gated_few<__nv_bfloat16>(a, c.dx, stream);
+    }
+  }
   const int64_t out = c.gated ? 2 * c.out : c.out;  // rows of the weight
   void* made = plan.make_dz && (c.dx || c.dw) ? ws + plan.dz : nullptr;
   cudaError_t e = cudaSuccess;

@@ -125,6 +125,23 @@ inline int gated_db_parts(int64_t rows, int64_t out, DType t) {
   if (p > 1024) p = 1024;
   return static_cast<int>(p < 1 ? 1 : p);
 }
+// Gated gradients of so few rows read the weight and write its gradient in one launch; dx comes
+// in parts of the features, enough for two CTAs (of 256 columns, or 128) on each SM and 16
+// features or more in each.
+// (Four rows, float32 up to eight; of a 16-bit type up to eight with 2^25 products of a half:
+// 8 x 768 x 768 (rows, in, out) bf16 7.8 us, 15.0 on the tensor cores, 8 x 4096 x 4096 48.5 and
+// 45.4, 4 x 4096 x 4096 29.8 and 49.6.)
+inline bool gated_few(int64_t rows, int64_t in, int64_t out, DType t) {
+  return rows > 0 && (rows <= 4 || (rows <= 8 && (t == DType::F32 ||
+                                                  rows * in * out <= int64_t{1} << 25)));
+}
+inline int gated_few_parts(int64_t rows, int64_t in, int64_t out, DType t) {
+  const int64_t cols = t == DType::F32 || rows > 4 ? 128 : 256;
+  int64_t p = 152 * 2 / ((in + cols - 1) / cols);
+  const int64_t most = (out + 15) / 16;
+  if (p > most) p = most;
+  return static_cast<int>(p < 1 ? 1 : p);
+}
 // gated: `out` columns of the result, z and dz with twice as many.
 cudaError_t launch_linear_dz(const LinearDzCall& c, bool gated, cudaStream_t stream);
 // Then the parts of the column sums into db (nothing without it); late: the launch before is a
@@ -194,6 +211,7 @@ struct LinearGradPlan {
   bool make_dz;           // dz is stored: with an activation, or to realign dy
   bool pack;              // x and weight are copied
   bool pieces;            // dz, x and weight are stored in three pieces (float32)
+  bool few;               // gated, few rows: dx in parts, nothing else
   int64_t ldz;
   size_t dz, part, x, w, bytes;
 };

@@ -1,4 +1,5 @@
 // The linear operator without the tensor cores, float32.
+#include "gated_few.cuh"
 #include "linear_launch.cuh"
 
 namespace b200norm {
@@ -53,5 +54,6 @@ template cudaError_t launch_rows<float>(const Product&, cudaStream_t);
 template cudaError_t launch_dz<float>(const LinearDzCall&, cudaStream_t);
 template cudaError_t launch_gated_dz<float>(const LinearDzCall&, cudaStream_t);
 template cudaError_t launch_db<float>(const LinearDzCall&, bool, bool, cudaStream_t);
+template cudaError_t launch_gated_few<float>(const GatedFewArgs&, void*, cudaStream_t);
 
 }  // namespace b200norm

@@ -136,6 +136,52 @@ def test_gradient(rows, n_in, n_out, act, t):
         assert sum(v is not None for v in alone) == 1
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("rows,n_in,n_out", [
+    (1, 1, 1), (1, 4096, 600), (2, 256, 17), (2, 30, 300), (3, 264, 40), (4, 129, 65),
+    (5, 516, 130), (7, 64, 1000), (8, 1024, 333), (8, 33, 8), (9, 264, 40)])
+def test_gradient_of_few_rows(rows, n_in, n_out, odd, t):
+    """The weight, x and the weight's gradient at and off 16-byte boundaries; every part of the
+    result by itself and into given tensors, with what lies around them left alone."""
+    act = sorted(ACTIVATIONS)[rows % 5]
+    g = gen(31)
+    x, w = tensor(g, (rows, n_in), DTYPES[t]), tensor(g, (2 * n_out, n_in), DTYPES[t], n_in ** -0.5)
+    dh, z = tensor(g, (rows, n_out), DTYPES[t], 0.3), tensor(g, (rows, 2 * n_out), DTYPES[t], 2.0)
+    if odd:
+        x, w, dh, z = at_odd(x), at_odd(w), at_odd(dh), at_odd(z)
+    code, at = ACTIVATIONS[act], 1 if odd else 8
+    shapes = (x.shape, w.shape, (2 * n_out,))
+    bases = [torch.full((at + torch.Size(s).numel() + 8,), 7.0, dtype=DTYPES[t], device="cuda")
+             for s in shapes]
+    into = [b[at:-8].view(s) for b, s in zip(bases, shapes)]
+    got = b2.gated_linear_grad(dh, x, w, z, activation=code, dx=into[0], dw=into[1], db=into[2])
+    ref, bound = G.gated_grad(dh.cpu(), x.cpu(), w.cpu(), z.cpu(), act)
+    for a, r, e, name in zip(got, ref, bound, ("dx", "dw", "db")):
+        assert_within(a, r, e, name)
+    assert all(bool((b[:at] == 7).all()) and bool((b[-8:] == 7).all()) for b in bases)
+    for i, one in enumerate((dict(want_weight=False, want_bias=False),
+                             dict(want_input=False, want_bias=False),
+                             dict(want_input=False, want_weight=False))):
+        assert torch.equal(b2.gated_linear_grad(dh, x, w, z, activation=code, **one)[i], got[i])
+
+
+def test_gradient_of_few_rows_stays_in_its_row():
+    """NaN and infinities of one row: dx of the others is as it was, though rows share
+    registers."""
+    g = gen(32)
+    x, w = tensor(g, (3, 96), torch.bfloat16), tensor(g, (80, 96), torch.bfloat16)
+    dh, z = tensor(g, (3, 40), torch.bfloat16), tensor(g, (3, 80), torch.bfloat16)
+    want = b2.gated_linear_grad(dh, x, w, z)[0]
+    dh[1, 5], z[1, 50] = float("nan"), float("inf")
+    got = b2.gated_linear_grad(dh, x, w, z)
+    assert torch.equal(got[0][::2], want[::2]) and bool(torch.isnan(got[0][1]).all())
+    rows = torch.ones(80, dtype=torch.bool, device="cuda")
+    rows[[5, 45, 10]] = False
+    assert bool(torch.isfinite(got[1][rows].float()).all())
+    assert not bool(torch.isfinite(got[1][~rows].float()).any())
+
+
 @pytest.mark.parametrize("act", sorted(ACTIVATIONS))
 def test_slopes(act):
     """dz element by element: a row a token, the weight a unit matrix, so that dx is dz's

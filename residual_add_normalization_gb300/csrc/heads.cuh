@@ -229,6 +229,9 @@ __device__ __forceinline__ void head_copy(Pack<T, VE>* dst, const T* src, bool i
   if constexpr (kBytes == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(smem_addr(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+  else if constexpr (kBytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                 :: "r"(smem_addr(dst)), "l"(src), "r"(in ? 8 : 0) : "memory");
   else if constexpr (kBytes == 4)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
                  :: "r"(smem_addr(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");

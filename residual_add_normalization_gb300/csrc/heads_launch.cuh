@@ -48,11 +48,19 @@ cudaError_t with_head_layout(const HeadsCall& c, const HeadsPlan& p, F&& f) {
     if constexpr (sizeof(T) == 4) return f(Num<kVec>(), Num<4>(), Num<0>(), Num<0>());
   }
   if constexpr (sizeof(T) == 2) {
+    if (p.ve == 4) {
+      if (p.sets <= 1) return f(Num<4>(), Num<1>(), Num<0>(), Num<0>());
+      return f(Num<4>(), Num<2>(), Num<0>(), Num<0>());
+    }
     if (p.ve == 2) {
+      if (p.sets <= 1) return f(Num<2>(), Num<1>(), Num<0>(), Num<0>());
       if (p.sets <= 2) return f(Num<2>(), Num<2>(), Num<0>(), Num<0>());
+      if (p.sets <= 4) return f(Num<2>(), Num<4>(), Num<0>(), Num<0>());
       return f(Num<2>(), Num<8>(), Num<0>(), Num<0>());
     }
   }
+  if (p.sets <= 1) return f(Num<1>(), Num<1>(), Num<0>(), Num<0>());
+  if (p.sets <= 2) return f(Num<1>(), Num<2>(), Num<0>(), Num<0>());
   if (p.sets <= 4) return f(Num<1>(), Num<4>(), Num<0>(), Num<0>());
   return f(Num<1>(), Num<16>(), Num<0>(), Num<0>());
 }

@@ -84,6 +84,22 @@ def test_sizes(size, rot, interleaved, t):
     both(q, k, positions, frequencies(rot), interleaved, 1.0, DTYPES[t], DTYPES[t], 1)
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("size,rot", [
+    (9, 8), (17, 10), (20, 20), (36, 20), (50, 26), (96, 24), (98, 98), (100, 52), (100, 100),
+    (129, 64), (130, 66), (150, 150), (252, 252), (254, 6), (257, 256), (260, 100), (300, 300),
+    (508, 508), (510, 510), (512, 508), (516, 516)])
+def test_rows_in_few_lanes(size, rot, interleaved, t):
+    """Accesses of 2, 4 and 8 bytes, with one unit of a lane to sixteen, rows that fill their
+    lanes and rows that do not."""
+    g = gen(size * 11 + rot)
+    q, _ = heads(g, (1, 7, 5, size), DTYPES[t], "rows")
+    k, _ = heads(g, (1, 7, 3, size), DTYPES[t], "dense")
+    positions = torch.randint(0, 5000, (1, 7), generator=g, device="cuda")
+    both(q, k, positions, frequencies(rot), interleaved, 1.0, DTYPES[t], torch.float32, 1)
+
+
 @pytest.mark.parametrize("t,m", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
 @pytest.mark.parametrize("how", ["dense", "rows", "permuted", "odd"])
 @pytest.mark.parametrize("batch,seq,nq,nk", [(1, 1, 1, 1), (1, 1, 32, 8), (3, 1, 33, 1),

@@ -425,9 +425,9 @@ B200NORM_API b200norm_status b200norm_linear_grad(
  *   activation, workspace  as in b200norm_linear (of its own _workspace_size()).
  *
  * Limits as in b200norm_linear, with F in [1, 2^19]; rows == 0 is a no-op.  Sums are
- * binary32, in a fixed order.  Large float32 calls (from 16 rows and 2^26 products of
- * rows, in_features and F; gradients from 64 rows and 2^24, or 16 and 2^27) run on the
- * tensor cores: every value is split into three
+ * binary32, in a fixed order.  Large float32 calls (from 9 rows, or 5 of in_features
+ * that 4 does not divide, and 2^26 products of rows, in_features and F; gradients from 64
+ * rows and 2^24, or 9 and 2^27) run on the tensor cores: every value is split into three
  * bfloat16 numbers that add up to it (24 bits; below 2^-110 of magnitude some of the last
  * are lost), and six of their nine products are summed, which leaves errors of about
  * 2^-24 of a product (an operand below 2^-126 counts as that).  An infinity there gives

@@ -105,12 +105,13 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t in, int64_t out, DType t, 
 // Where the copies in pieces pay, us on the binary32 units and in pieces.  Forward, 2^26 products
 // of a half: 256 x 512 x 512 (rows, in, out) 16.1 and 12.0, 2048 x 1024 x 2048 387 and 74, but
 // 512 x 256 x 256 9.5 and 11.0.  Gradients sooner: 512 x 256 x 256 30.5 and 16.4, 256 x 256 x 256
-// 19.9 and 15.5, 512 x 768 x 768 71 and 38.  The weight's copy wants a few rows to serve:
-// 16 x 4096 x 4096 124 and 100, 167 and 148, but the gradients of 16 x 2048 x 2048 50 and 58.
+// 19.9 and 15.5, 512 x 768 x 768 71 and 38.  Few rows are bound by the weight and its copy:
+// 12 x 4096 x 4096 124 and 100, gradients 165 and 147, but of 16 x 2048 x 2048 50 and 58; those
+// that the row kernel takes are not copied.
 bool gated_pieces(int64_t rows, int64_t in, int64_t out, bool grad) {
   const int64_t products = rows * in * out;
-  if (!grad) return rows >= 16 && products >= int64_t{1} << 26;
-  return rows >= 16 && products >= int64_t{1} << (rows >= 64 ? 24 : 27);
+  if (!grad) return rows > (in % 4 == 0 ? 8 : 4) && products >= int64_t{1} << 26;
+  return products >= int64_t{1} << (rows >= 64 ? 24 : 27);
 }
 
 LinearPlan gated_plan(int64_t rows, int64_t in, int64_t out, DType t, bool aligned16) {

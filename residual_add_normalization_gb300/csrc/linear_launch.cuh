@@ -65,6 +65,8 @@ cudaError_t launch_rows_ve(const Product& p, cudaStream_t stream) {
     // that more warps use better; 1 x 4096 x 8192 bf16 22.8 us, 26.9 with four)
     if (p.M <= 1) return go(linear_rows_kernel<T, VE, 1, 2, sizeof(T) == 2 ? 1 : 4, true>, 1);
     if (p.M <= 2) return go(linear_rows_kernel<T, VE, 2, 2, 4, true>, 1);
+    if constexpr (sizeof(T) == 4)
+      if (p.M > 4) return go(linear_rows_kernel<T, VE, 8, 2, 2, true>, 1);
     return go(linear_rows_kernel<T, VE, 4, 2, 4, true>, 1);
   }
   if (p.M <= 1) return go(linear_rows_kernel<T, VE, 1, 1, 8>, 1);

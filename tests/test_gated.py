@@ -56,7 +56,8 @@ def check_forward(rows, n_in, n_out, t, act="silu", bias=True, want_z=True, odd=
 @pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,n_in,n_out", [
     (1, 1, 1), (1, 64, 8), (1, 768, 768), (2, 300, 33), (3, 512, 40), (4, 4096, 64),
-    (5, 200, 72), (16, 512, 100), (17, 1027, 130), (33, 256, 264), (64, 512, 512),
+    (5, 200, 72), (6, 516, 41), (8, 1024, 257), (16, 512, 100),
+    (17, 1027, 130), (33, 256, 264), (64, 512, 512),
     (65, 128, 72), (129, 64, 200), (130, 96, 1000), (300, 520, 1027), (777, 136, 96)])
 def test_forward(rows, n_in, n_out, t):
     check_forward(rows, n_in, n_out, DTYPES[t], bias=rows % 2 == 1, want_z=True)
@@ -348,10 +349,11 @@ def test_results_past_2_31_elements():
         assert float((a.float() - b.float()).norm() / b.float().norm()) <= 2.0 ** -8
 
 
-# -- float32 products in pieces: rows, in, out with 16 rows and 2^26 products or more ----------
+# -- float32 products in pieces: rows, in, out with 9 rows and 2^26 products or more -----------
 
 PIECES = [(700, 640, 160), (513, 1027, 131), (20, 2048, 1700), (40, 1500, 1200), (2100, 128, 260),
-          (90, 520, 1537)]
+          (90, 520, 1537), (10, 4096, 3300),
+          (5, 4095, 3300)]
 
 
 @pytest.mark.parametrize("rows,n_in,n_out", PIECES)

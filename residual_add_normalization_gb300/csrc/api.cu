@@ -378,7 +378,10 @@ b200norm_status check_heads_shape(int64_t batch, int64_t seq, int64_t q, int64_t
   return B200NORM_OK;
 }
 
-HeadStrides to_strides(const int64_t* s) { return {s[0], s[1], s[2]}; }
+// The steps that are taken: none along an axis of one, whatever is given for it.
+HeadStrides to_strides(const int64_t* s, int64_t batch, int64_t seq, int64_t heads) {
+  return {batch > 1 ? s[0] : 0, seq > 1 ? s[1] : 0, heads > 1 ? s[2] : 0};
+}
 
 HeadsCall heads_call(const b200norm_rotation* r, int64_t batch, int64_t seq, int64_t size,
                      b200norm_dtype T, b200norm_dtype M) {
@@ -447,8 +450,9 @@ b200norm_status heads_forward(const b200norm_heads* queries, const b200norm_head
                     names[i][2]);
       reads[nreads++] = {h->gamma, static_cast<size_t>(head_size) * ms, names[i][2]};
     }
-    c.set[i] = {h->x, nullptr, h->gamma, h->y, nullptr, h->heads, to_strides(h->x_strides), {},
-                to_strides(h->y_strides)};
+    auto steps = [&](const int64_t* s) { return to_strides(s, batch, seq, h->heads); };
+    c.set[i] = {h->x, nullptr, h->gamma, h->y, nullptr, h->heads, steps(h->x_strides), {},
+                steps(h->y_strides)};
     ++n;
   }
   if (n == 0) return ok();
@@ -1027,8 +1031,9 @@ b200norm_status b200norm_head_rms_rotary_grad(
                   names[i][3], names[i][4]);
     if (h->gamma) flat_in[nfin++] = {h->gamma, gb, names[i][3]};
     if (h->dgamma) flat_out[nfout++] = {h->dgamma, gb, names[i][4]};
-    c.set[i] = {h->x, h->dy, h->gamma, h->dx, h->dgamma, h->heads, to_strides(h->x_strides),
-                to_strides(h->dy_strides), to_strides(h->dx_strides)};
+    auto steps = [&](const int64_t* s) { return to_strides(s, batch, seq, h->heads); };
+    c.set[i] = {h->x, h->dy, h->gamma, h->dx, h->dgamma, h->heads, steps(h->x_strides),
+                steps(h->dy_strides), steps(h->dx_strides)};
     if (empty) continue;
     in[nin++] = {h->dy, h->heads, h->dy_strides, names[i][0]};
     in[nin++] = {h->x, h->heads, h->x_strides, names[i][1]};

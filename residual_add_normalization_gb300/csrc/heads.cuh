@@ -239,15 +239,17 @@ __device__ __forceinline__ void head_copy(Pack<T, VE>* dst, const T* src, bool i
     *dst = in ? ld_stream<T, VE>(src) : Pack<T, VE>{};
 }
 
+// A copy of no bytes names an aligned address all the same: `none`, the start of a tensor
+// (in lanes without a row p may lie anywhere).
 template <typename T, int VE, int K>
-__device__ __forceinline__ void head_fetch(HeadRow<T, VE, K>& r, const T* p, bool in,
-                                           const HeadUnits<VE, K>& u) {
+__device__ __forceinline__ void head_fetch(HeadRow<T, VE, K>& r, const T* p, const T* none,
+                                           bool in, const HeadUnits<VE, K>& u) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const bool l = in && u.lo[k] >= 0, h = in && u.hi[k] >= 0;
-    head_copy<T, VE>(&r.lo[k][lane], l ? p + u.lo[k] : p, l);
-    head_copy<T, VE>(&r.hi[k][lane], h ? p + u.hi[k] : p, h);
+    head_copy<T, VE>(&r.lo[k][lane], l ? p + u.lo[k] : none, l);
+    head_copy<T, VE>(&r.hi[k][lane], h ? p + u.hi[k] : none, h);
   }
 }
 
@@ -564,6 +566,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
   pdl_trigger();
 
   // what is fetched, some steps ahead of what is worked on
+  const T* none = static_cast<const T*>(g.c.set[g.c.set[0].heads ? 0 : 1].x);
   HeadCursor<T> c;
   c.at = at;
   auto seek = [&] {  // to step i of the token: queries first, then keys
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(32 * kHeadWarps) heads_kernel(const HeadsArgs 
   };
   auto fetch = [&](int stage) {
     if (c.at.left > 0) {
-      head_fetch<T, VE, K>(ring[stage], c.p, c.left > 0, u);
+      head_fetch<T, VE, K>(ring[stage], c.p, none, c.left > 0, u);
       if (c.fresh) head_fetch_position(g, sh, stage, c.at.b, c.at.t);
       c.fresh = false;
       --c.at.left;
@@ -692,6 +695,7 @@ heads_grad_kernel(const HeadsArgs g) {
   pdl_trigger();
 
   // what is fetched, some steps ahead of what is worked on
+  const T* none = static_cast<const T*>(set.x);
   HeadCursor<T> c;
   const T* pd = nullptr;
   const int64_t step_d = rows * set.dys.head, step_y = rows * set.ys.head;
@@ -710,8 +714,8 @@ heads_grad_kernel(const HeadsArgs g) {
   };
   auto fetch = [&](int stage) {
     if (c.at.left > 0) {
-      head_fetch<T, VE, K>(ring[2 * stage], c.p, c.left > 0, u);
-      head_fetch<T, VE, K>(ring[2 * stage + 1], pd, c.left > 0, u);
+      head_fetch<T, VE, K>(ring[2 * stage], c.p, none, c.left > 0, u);
+      head_fetch<T, VE, K>(ring[2 * stage + 1], pd, none, c.left > 0, u);
       if (c.fresh) head_fetch_position(g, sh, stage, c.at.b, c.at.t);
       c.fresh = false;
       --c.at.left;

@@ -115,6 +115,38 @@ def test_layouts(batch, seq, nq, nk, how, t, m):
 
 
 @pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("nq,nk", [(1, 1), (1, 0), (0, 1), (6, 1), (1, 6)])
+@pytest.mark.parametrize("size,step", [(128, 129), (64, 67), (40, 41), (36, 37), (34, 35),
+                                       (256, 1 << 61)])
+def test_one_head_with_any_step(size, step, nq, nk, t):
+    """The step between the heads of a tensor that has one is not taken: it may be odd where the
+    tokens are whole vectors apart, or reach past any memory.  The lanes without a row must not
+    go by it either."""
+    g = gen(size + nq)
+
+    def one(n):
+        if n == 0:
+            return None
+        if n > 1:
+            return torch.randn(2, 9, n, size, generator=g, device="cuda").to(DTYPES[t])
+        base = torch.randn(2 * 9 * 8 * 136 + 256, generator=g, device="cuda").to(DTYPES[t])
+        return base.as_strided((2, 9, 1, size), (9 * 1032, 1032, step, 1))
+    q, k, dq, dk = one(nq), one(nk), one(nq), one(nk)
+    p, f = torch.randint(0, 5000, (2, 9), generator=g, device="cuda"), frequencies(size)
+    gamma = torch.randn(size, generator=g, device="cuda")
+    gq, gk = gamma if nq else None, gamma if nk else None
+
+    def run(q, k, dq, dk):
+        return (b2.rotary(q, k, p, f) + b2.head_rms_rotary(q, k, gq, gk, p, f)
+                + b2.head_rms_rotary_grad(dq, dk, q, k, gq, gk, p, f))
+    same = [None if v is None else v.contiguous().clone() for v in (q, k, dq, dk)]
+    for got, want in zip(run(q, k, dq, dk), run(*same)):
+        assert (got is None and want is None) or torch.equal(got, want)
+    if nq and nk:
+        both(q, k, p, f, False, 1.0, DTYPES[t], torch.float32, 3)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
 def test_positions_by_sequence_or_for_all(t):
     """(seq,) positions serve every sequence, a column that steps over others as well."""
     g = gen(3)

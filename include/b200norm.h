@@ -555,7 +555,7 @@ typedef struct b200norm_heads_grad {
   const void* gamma;       /* M, or NULL (ones) */
   void* dx;                /* T, or NULL when not wanted */
   void* dgamma;            /* M, (head_size), or NULL when not wanted */
-  int64_t heads;           /* 0: none (the pointers are not used) */
+  int64_t heads;           /* 0: none (the pointers are not used: dgamma keeps what it has) */
   int64_t dy_strides[3], x_strides[3], dx_strides[3];
 } b200norm_heads_grad;
 

@@ -1019,7 +1019,7 @@ def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *,
     ``dq_out`` and ``dk_out`` receive those of the inputs (views of one tensor of
     rows, for the gradient of the product they came from).  An output that is not
     wanted is ``None``; one that is given is wanted; a gamma of ``None`` has no
-    gradient.
+    gradient.  Without tokens or heads a gamma's gradient is zeros.
     """
     x, lead, size, index, dt = _first_heads(q, k)
     sets = []
@@ -1043,6 +1043,7 @@ def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *,
     def run():
         lib = _lib or library()
         dxs, dgs, args, heads = [None, None], [None, None], [None, None], [0, 0]
+        empty = [None, None]  # no heads, whose sum the call for the others does not store
         for i, one in enumerate(sets):
             if one is None:
                 continue
@@ -1052,6 +1053,9 @@ def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *,
             if gamma is not None and (dg is not None or want_gamma):
                 dg = _like("dgamma_" + name, dg, gamma, index)
             dxs[i], dgs[i], heads[i] = o, dg, t_at[0]
+            if t_at[0] == 0 and dg is not None:
+                empty[i] = _HEADS_GRAD.pack(0, 0, 0, 0, dg.data_ptr(), 1, *_NO_STRIDES,
+                                            *_NO_STRIDES, *_NO_STRIDES)
             args[i] = _HEADS_GRAD.pack(
                 d.data_ptr(), t.data_ptr(), 0 if gamma is None else gamma.data_ptr(),
                 0 if o is None else o.data_ptr(), 0 if dg is None else dg.data_ptr(), t_at[0],
@@ -1063,6 +1067,9 @@ def head_rms_rotary_grad(dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, *,
         _check(lib.b200norm_head_rms_rotary_grad(*args, rotation, batch, seq, size, _DTYPES[dt],
                                                  _DTYPES[m], float(epsilon), _at(ws), n,
                                                  raw))
+        if empty != [None, None]:  # of no tokens: zeros
+            _check(lib.b200norm_head_rms_rotary_grad(*empty, rotation, 0, 0, size, _DTYPES[dt],
+                                                     _DTYPES[m], float(epsilon), None, 0, raw))
         return dxs[0], dxs[1], dgs[0], dgs[1]
 
     context = _on(index, stream, (dq, dk, q, k, gamma_q, gamma_k, positions, inv_freq, dq_out,

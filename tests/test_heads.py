@@ -355,6 +355,30 @@ def test_nothing_wanted_and_nothing_there():
             assert dx.shape == e.shape and bool((dg == 0).all())
 
 
+@pytest.mark.parametrize("m", ["bf16", "f32"])
+@pytest.mark.parametrize("nq,nk", [(0, 0), (0, 3), (3, 0)])
+@pytest.mark.parametrize("tokens", [(5,), (2, 5), (0,)])
+def test_gammas_without_heads_have_gradients_of_zeros(tokens, nq, nk, m):
+    """Given and new ones, beside those of a tensor that has heads and by themselves."""
+    g = gen(14)
+    q, k = (torch.randn(*tokens, n, 8, generator=g, device="cuda").bfloat16() for n in (nq, nk))
+    gamma = torch.rand(8, generator=g, device="cuda").to(DTYPES[m])
+    p, f = torch.zeros(tokens, dtype=torch.int64, device="cuda"), frequencies(8)
+    want = [torch.zeros_like(gamma) if v.numel() == 0 else
+            b2.head_rms_rotary_grad(v, None, v, None, gamma, None, p, f)[2] for v in (q, k)]
+    for _ in range(3):  # in memory that has been used
+        torch.full((1 << 16,), float("nan"), device="cuda")
+        out = b2.head_rms_rotary_grad(q, k, q, k, gamma, gamma, p, f)
+        assert torch.equal(out[2], want[0]) and torch.equal(out[3], want[1])
+        assert out[0].shape == q.shape and out[1].shape == k.shape
+    into = [torch.full_like(gamma, 7.0) for _ in range(2)]
+    out = b2.head_rms_rotary_grad(q, k, q, k, gamma, gamma, p, f, want_input=False,
+                                  dgamma_q=into[0], dgamma_k=into[1])
+    assert out[2] is into[0] and torch.equal(into[0], want[0]) and torch.equal(into[1], want[1])
+    alone = b2.head_rms_rotary_grad(q, None, q, None, gamma, None, p, f)[2]
+    assert torch.equal(alone, want[0])
+
+
 def test_offsets_past_32_bits():
     """Tokens more than 2^31 elements apart."""
     step = (1 << 31) + 8

@@ -494,7 +494,8 @@ B200NORM_API b200norm_status b200norm_linear_status(b200norm_stream_t stream);
  * the inverse has -s, and is the rotation's gradient.  With R = rotary_size, pair i
  * (i < R / 2) is elements (i, i + R / 2) of the head, or (2 i, 2 i + 1) when
  * interleaved; elements from R on stay as they are.  Angles are exact to about
- * 2^-25 of a radian, 2^-53 of p f and 2^-64 p of a turn, at any position.
+ * 2^-25 of a radian, 2^-53 of p f and 2^-64 p of a turn, at any position.  A frequency
+ * that is not finite makes its pair NaN.
  *
  * RMS norm of a head, before its rotation: u = x / sqrt(mean(x^2) + epsilon) * gamma,
  * with binary32 sums of squares.

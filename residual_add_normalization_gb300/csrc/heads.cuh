@@ -69,9 +69,13 @@ size_t head_smem(const HeadsArgs& g, bool gradient) {
 
 // -- angles -----------------------------------------------------------------------
 
-// Radians per position to turns per position, mod 1, in units of 2^-64.
+// Radians per position to turns per position, mod 1, in units of 2^-64.  A frequency that is
+// not finite has no angle, at any position: a number that no half turn and more can be (there
+// binary64 has steps of 2^-53 turns).
+constexpr unsigned long long kNoAngle = (1ull << 63) + 1;
 __device__ __forceinline__ unsigned long long phase_step(double radians) {
   constexpr double kInv2Pi = 0.15915494309189535;
+  if (!isfinite(radians)) return kNoAngle;
   double t = radians * kInv2Pi;
   t -= floor(t);
   return __double2ull_rz(t * 18446744073709551616.0);
@@ -362,8 +366,10 @@ __device__ __forceinline__ void head_angles(const HeadsArgs& g, const HeadShared
   for (int n = threadIdx.x & 31; n < g.pitch; n += 32) {
     float c = 1.0f, s = 0.0f;
     if (n < g.c.rot / 2) {
-      const unsigned long long phase = static_cast<unsigned long long>(p) * sh.steps[n];
+      const unsigned long long step = sh.steps[n];
+      const unsigned long long phase = static_cast<unsigned long long>(p) * step;
       phase_cos_sin(static_cast<unsigned>(phase >> 32), c, s);
+      if (step == kNoAngle) c = s = __int_as_float(0x7fffffff);
       c *= g.c.scale;
       s *= sine;
     }

@@ -183,6 +183,41 @@ def test_far_positions(first):
     assert bool((y[:, :3] ** 2 + y[:, 3:] ** 2 - 1).abs().max() <= 20 * H.ROT)
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_frequencies_that_are_not_finite(t, interleaved):
+    """Their pairs are NaN, at position 0 as well; no other element is another, and the gradient's
+    rows are NaN where they have such a pair."""
+    g = gen(15)
+    x, _ = heads(g, (1, 6, 3, 40), DTYPES[t], "dense")
+    p = torch.tensor([[0, 1, -1, 7, 100000, 1 << 40]], device="cuda")
+    f = frequencies(32)
+    # half a turn, and a step of binary64 more: the numbers next to what stands for no angle
+    f[4], f[5] = math.pi, math.pi + 2.0 ** -51
+    bad = f.clone()
+    where = {1: float("nan"), 3: float("inf"), 9: -float("inf")}
+    for i, v in where.items():
+        bad[i] = v
+    spoilt = torch.zeros(40, dtype=torch.bool, device="cuda")
+    for i in where:
+        spoilt[[2 * i, 2 * i + 1] if interleaved else [i, i + 16]] = True
+    for inverse in (False, True):
+        y = b2.rotary(x, None, p, bad, interleaved=interleaved, inverse=inverse)[0]
+        want = b2.rotary(x, None, p, f, interleaved=interleaved, inverse=inverse)[0]
+        assert bool(torch.isfinite(want).all())
+        assert bool(torch.isnan(y[..., spoilt]).all())
+        assert torch.equal(y[..., ~spoilt], want[..., ~spoilt])
+    y = b2.head_rms_rotary(x, None, None, None, p, bad, interleaved=interleaved)[0]
+    want = b2.head_rms_rotary(x, None, None, None, p, f, interleaved=interleaved)[0]
+    assert bool(torch.isnan(y[..., spoilt]).all())
+    assert torch.equal(y[..., ~spoilt], want[..., ~spoilt])
+    gamma = torch.ones(40, device="cuda")
+    dx, _, dg, _ = b2.head_rms_rotary_grad(x, None, x, None, gamma, None, p, bad,
+                                           interleaved=interleaved)
+    assert bool(torch.isnan(dx).all())
+    assert torch.equal(torch.isnan(dg), spoilt)
+
+
 def test_every_angle():
     """Cosine and sine of 2^20 angles over a turn, and of the smallest ones."""
     n = 1 << 20

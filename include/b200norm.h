@@ -430,8 +430,9 @@ B200NORM_API b200norm_status b200norm_linear_grad(
  * rows and 2^24, or 9 and 2^27) run on the tensor cores: every value is split into three
  * bfloat16 numbers that add up to it (24 bits; below 2^-110 of magnitude some of the last
  * are lost), and six of their nine products are summed, which leaves errors of about
- * 2^-24 of a product (an operand below 2^-126 counts as that).  An infinity there gives
- * NaN where the product itself would be infinite; the workspace holds the pieces.
+ * 2^-24 of a product (an operand below 2^-126 counts as that).  A sum that is not finite
+ * so is made again from the values: infinities, NaN and overflows are those of binary32
+ * sums.  The workspace holds the pieces.
  */
 B200NORM_API size_t b200norm_gated_linear_workspace_size(int64_t rows, int64_t in_features,
                                                          int64_t out_features, b200norm_dtype T,

@@ -42,7 +42,9 @@
 // tensor cores cut a sum's last place at each addition of 16 products (4.4e-6 in the norm over
 // 4096 of k), so each slice has a sum of its own, the pair of the first pieces last, and the
 // slices' sums are added with rounding by the epilogue's warps, in their registers (1.5e-7 over
-// 10,330 of k; the library's float32 product 1.8e-6).
+// 10,330 of k; the library's float32 product 1.8e-6).  An infinity, or a product past binary32,
+// meets zeros and terms of the other sign there that the values' own product has not: a sum that
+// is not finite is made again from the values, in binary32 (pieces_again).
 //
 // Every wait is bounded: the first that gives up records its site in `status`;
 // one that gives up ends its role, the others then run out as well, and all meet
@@ -79,6 +81,17 @@ struct MmaArgs {
   bool stall;          // a test: nothing is copied, and the waits give up
   unsigned withhold;   // a test: the site whose event is left out (0: none)
 };
+
+// The operands in pieces as they lie in memory, for sums that are not finite.  They take the
+// place of a tensor map that results in pieces do not need: 48 bytes more of arguments cost a
+// launch 0.4 us.
+struct MmaPieces {
+  const __nv_bfloat16 *a, *b;
+  int64_t lda, ldb, K;
+  int piece_a, piece_b;
+};
+template <bool PIECES>
+using MmaLastMap = typename std::conditional<PIECES, MmaPieces, CUtensorMap>::type;
 
 // Shared memory of a CTA: the ring, then room for each epilogue warp's results (unless
 // SWAP): two of 4 KB, or with pieces one of 32 by 33 floats.  Two small CTAs share an SM.
@@ -219,6 +232,19 @@ __device__ __forceinline__ void tmem_store16(unsigned addr, const float (&v)[16]
       :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
          "r"(r[15]), "r"(addr) : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// One column of this warp's 32 lanes.
+__device__ __forceinline__ float tmem_load1(unsigned addr) {
+  unsigned r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_store1(unsigned addr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};"
+               :: "r"(__float_as_uint(v)), "r"(addr) : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
@@ -697,9 +723,107 @@ __device__ __forceinline__ void gated_col(const Epilogue& e, int64_t m, int64_t 
   });
 }
 
+// -- sums in pieces that are not finite --------------------------------------------
+
+// N values of an operand in pieces: of row i, from k on (a multiple of N; zeros past K).
+// Through L2, as the tensor copies: a late launch has not waited when it gets here.
+template <bool KC, int N>
+__device__ __forceinline__ void piece_values(const __nv_bfloat16* p, int64_t ld, int piece,
+                                             int64_t i, int64_t k, int64_t K, float (&f)[N]) {
+  const unsigned short* at =
+      reinterpret_cast<const unsigned short*>(p) + (KC ? i * ld + k : k * ld + i);
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] = 0.0f;
+  // each sum exact (eight values at a time where registers matter less)
+#pragma unroll(N == 8 ? 3 : 1)
+  for (int j = 2; j >= 0; --j) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if constexpr (KC) {
+        if (e % 4) continue;
+        const uint2 q = __ldcg(reinterpret_cast<const uint2*>(at + j * piece + e));
+        f[e] += __uint_as_float(q.x << 16);
+        f[e + 1] += __uint_as_float(q.x & 0xffff0000u);
+        f[e + 2] += __uint_as_float(q.y << 16);
+        f[e + 3] += __uint_as_float(q.y & 0xffff0000u);
+      } else if (k + e < K) {
+        f[e] += __uint_as_float(static_cast<unsigned>(__ldcg(at + e * ld + j * piece)) << 16);
+      }
+    }
+  }
+}
+
+// t and N more products of row m of A and row n of B.
+template <bool A_KC, bool B_KC, int N>
+__device__ __forceinline__ float pieces_add(const MmaPieces& o, int64_t m, int64_t n, int64_t k,
+                                            float t) {
+  float a[N], b[N];
+  piece_values<A_KC, N>(o.a, o.lda, o.piece_a, m, k, o.K, a);
+  piece_values<B_KC, N>(o.b, o.ldb, o.piece_b, n, k, o.K, b);
+#pragma unroll
+  for (int e = 0; e < N; ++e) t = fmaf(a[e], b[e], t);
+  return t;
+}
+
+// A warp's sums of a tile, made again in binary32 where they are not finite: each lane's row m of
+// A (-1: none) and `cols` columns, over k in [k0, k1) (multiples of 64, or K).
+struct MmaAgain {
+  unsigned at;       // tensor memory, the tile's column 0
+  int first, far;    // column c of the warp's is first + c % 64 + c / 64 * far
+  int cols, half;    // columns from `half` on are of what is gated
+  int64_t m, n0;     // of column 0
+  int64_t N, gate;   // columns of the result; rows of B from a gate's to its other
+  int64_t k0, k1;
+};
+
+// A NaN stays one, and is soon known where all of x is NaN.  A few sums of a column are made by
+// the whole warp, one after another, many by a lane each.  4096 x 4096 x 4096, forward and
+// gradients: one infinity in x and dh 4 and 54 ms, all of them NaN 2.2 and 4 ms, all the same
+// infinity 0.7 and 4.7 s (otherwise 0.94 and 2.0 ms).  What this costs the other calls matters
+// more: it is a call, of few registers (inlined, or with twice as many loads on their way, the
+// gradients' CTAs found no room beside the launch before, 512 x 256 x 512 20.6 us; 19.4 so, 18.7
+// without).
+template <bool A_KC, bool B_KC>
+__device__ __noinline__ void pieces_again(const MmaPieces o, const MmaAgain p) {
+  constexpr int N = A_KC && B_KC ? 8 : 4;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int c = 0; c < p.cols; ++c) {
+    const int col = p.first + c % 64 + c / 64 * p.far;
+    const int64_t j = p.n0 + (col < p.half ? col : col - p.half);
+    const int64_t n = col < p.half ? j : p.gate + j;
+    float v = tmem_load1(p.at + col);
+    const bool off = p.m >= 0 && j < p.N && !isfinite(v);
+    float t = 0.0f;
+    if (off) t = pieces_add<A_KC, B_KC, N>(o, p.m, n, p.k0, t);
+    unsigned todo = __ballot_sync(0xffffffffu, off && t == t);
+    if (__popc(todo) > 4) {
+      if (off)
+#pragma unroll 1
+        for (int64_t k = p.k0 + N; k < p.k1 && t == t; k += N)
+          t = pieces_add<A_KC, B_KC, N>(o, p.m, n, k, t);
+      todo = 0;
+    }
+    if (off) v = t;
+#pragma unroll 1
+    for (; todo; todo &= todo - 1) {
+      const int source = __ffs(todo) - 1;
+      const int64_t row = __shfl_sync(0xffffffffu, p.m, source);
+      t = 0.0f;
+#pragma unroll 1
+      for (int64_t k = p.k0; k < p.k1 && !__any_sync(0xffffffffu, t != t); k += 32 * N)
+        if (k + lane * N < p.k1) t = pieces_add<A_KC, B_KC, N>(o, row, n, k + lane * N, t);
+      t = warp_sum(t);
+      if (lane == source) v = t;
+    }
+    __syncwarp();
+    tmem_store1(p.at + col, v);
+  }
+}
+
 // -- kernel ---------------------------------------------------------------------
 
-// (GATED: map_z is of z's gate columns, map_r of the others.)
+// (GATED: map_z is of z's gate columns, map_r of the others; in pieces map_r is the operands.)
 template <typename T, int CG, int BN, bool A_KC, bool B_KC, bool SWAP, bool GATED = false,
           typename TO = T>
 __global__ void __launch_bounds__(MmaShape<CG, BN, SWAP, GATED, sizeof(TO) == 4>::kThreads,
@@ -708,7 +832,8 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_y,
                   const __grid_constant__ CUtensorMap map_z,
-                  const __grid_constant__ CUtensorMap map_r, const MmaArgs g) {
+                  const __grid_constant__ MmaLastMap<!std::is_same<T, TO>::value> map_r,
+                  const MmaArgs g) {
   constexpr bool kPieces = !std::is_same<T, TO>::value;
   using S = MmaShape<CG, BN, SWAP, GATED, kPieces>;
   constexpr bool kFull = A_KC && B_KC;  // the gradients' products are stored as they are
@@ -952,8 +1077,25 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
           }
         }
         if (!alive) break;
+        float zero[4] = {};  // NaN if a sum is not finite
 #pragma unroll
-        for (int c = 0; c < S::kCols / 16; ++c) tmem_store16(at + column(16 * c), total[c]);
+        for (int c = 0; c < S::kCols / 16; ++c) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) zero[i % 4] = fmaf(total[c][i], 0.0f, zero[i % 4]);
+          tmem_store16(at + column(16 * c), total[c]);
+        }
+        if (__any_sync(0xffffffffu, (zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.0f)) {
+          int tm, tn;
+          tile_at(t, tm, tn);
+          const int64_t i = static_cast<int64_t>(tm * CG + (CG == 2 ? static_cast<int>(rank) : 0)) *
+                                kTileM + (kMeet ? row % kTileM : row);
+          const int64_t k1 = static_cast<int64_t>(k_hi) * kMmaK;
+          pieces_again<A_KC, B_KC>(
+              map_r, {at, column(0), kApart ? 128 : 64, S::kCols, GATED && !SWAP ? kTileN : BN,
+                      i >= g.M ? -1 : kMeet && row >= kTileM ? g.gate + i : i,
+                      static_cast<int64_t>(tn) * kTileN, g.N, g.gate,
+                      static_cast<int64_t>(k_lo) * kMmaK, k1 < map_r.K ? k1 : map_r.K});
+        }
       } else if (!await()) {
         break;
       }

@@ -68,8 +68,9 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   for (const void* o : outs)
     if (reinterpret_cast<uintptr_t>(o) % 16 != 0) g.vec = false;
   g.status = status;
-  // a wait lasts a tile at most: a second, and 4 us for each slice of K
-  g.limit_ns = 1000000000ull + 4000ull * g.kblocks * (kPieces ? 6 : 1);
+  // a wait lasts a tile at most: a second, and 4 us for each slice of K (in pieces 20 ms: all of
+  // a tile's sums may have to be made again, which took up to 5)
+  g.limit_ns = 1000000000ull + (kPieces ? 20000000ull : 4000ull) * g.kblocks;
   g.late = p.late;
   g.stall = linear_stall_limit_ns() != 0;
   if (g.stall) g.limit_ns = linear_stall_limit_ns();
@@ -88,9 +89,11 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   };
   if (!encode(&map_a, a, rows_a, g.piece_a, kTileM) || !encode(&map_b, b, rows_b, g.piece_b, kBoxB))
     return cudaErrorInvalidValue;
-  CUtensorMap map_y = {}, map_z = {}, map_r = {};
-  if (kPieces) {
-    // results leave by ordinary stores
+  CUtensorMap map_y = {}, map_z = {};
+  MmaLastMap<kPieces> map_r = {};
+  if constexpr (kPieces) {  // results leave by ordinary stores
+    map_r = {static_cast<const T*>(a.p), static_cast<const T*>(b.p), a.ld, b.ld, p.K, g.piece_a,
+             g.piece_b};
   } else if (GATED && !SWAP && g.vec && g.splits == 1) {
     T* z = static_cast<T*>(p.epi.z);
     const bool ok = encode_rows<T>(&map_y, p.epi.y, p.N, p.M, p.N, 32) &&

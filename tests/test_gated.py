@@ -445,6 +445,123 @@ def test_pieces_of_any_magnitude():
     assert bool(torch.isnan(h[5]).all()) and not bool(torch.isfinite(h[9]).any())
 
 
+def kind(v):
+    """0 finite, 1 and -1 the infinities, 2 NaN."""
+    return torch.where(torch.isnan(v), 2, torch.isposinf(v).int() - torch.isneginf(v).int())
+
+
+def same_specials(got, wants, name):
+    """NaN, infinities and finite values where one of the references has them.  There are two for
+    a product of finite values past binary32 that meets an infinity of the other sign: -inf +
+    3.9998e38 is -inf where one multiply-add makes it, and NaN where the sum is split, as the part
+    with 3.9998e38 > 2^128 (1 - 2^-25) alone has the sum +inf."""
+    ok = torch.zeros_like(got, dtype=torch.bool)
+    for want in wants:
+        ok |= kind(got) == kind(want.float())
+    assert bool(ok.all()), (name, (~ok).nonzero()[:5])
+
+
+def product(a, b):
+    """a b^T in binary64, term by term: the terms as they are, and rounded to binary32."""
+    return [torch.stack([f(r, b).double().sum(-1) for r in a])
+            for f in (lambda r, b: r.double() * b.double(), lambda r, b: r * b)]
+
+
+@pytest.mark.parametrize("tiling", [(0, 0, 0, 0)] + TILINGS)
+def test_infinities_and_overflow_in_pieces(tiling):
+    """What is not finite is what binary32 products of the values give, whatever their pieces'
+    products do: pieces that are zero, pieces of the other sign, first and second pieces whose
+    product overflows alone.  No other sum is another."""
+    rows, n_in, n_out = (16, 2112, 2001) if tiling[3] else (300, 640, 363)
+    assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+    g = gen(27)
+    x, w = tensor(g, (rows, n_in), torch.float32), tensor(g, (2 * n_out, n_in), torch.float32)
+    inf, last = float("inf"), rows - 1
+    w[:, 3] = torch.where(w[:, 3] > 0, 1.0, -1.0)      # one piece, the others zero
+    w[5, 3] = w[n_out + 7, 3] = 0.0                     # infinity times zero
+    clean = b2.gated_linear(x, w, activation=0, want_z=True)
+    assert all(bool(torch.isfinite(v).all()) for v in clean)
+    bad = x.clone()
+    bad[0, 3] = inf
+    bad[2, 100] = -inf
+    bad[4, 3], bad[4, n_in - 1] = inf, inf              # infinities of both signs meet
+    bad[6, 8] = torch.finfo(torch.float32).max          # overflows with most weights
+    bad[8, 9] = -1.99609375 * 2.0 ** 127                # its pieces: -2^128 + 2^119, cut
+    bad[last, 3], bad[last, 5] = inf, float("nan")
+    wide = w.clone()
+    wide[:, 8] *= 2.0 ** 20
+    wide[:, 9] = torch.where(wide[:, 9] > 0, 1.0, -1.0) * (1 + 2.0 ** -9) * 2.0 ** 2
+    want = product(bad[[0, 2, 4, 6, 8, last]], wide)
+    z = b2.gated_linear(bad, wide, activation=0, want_z=True)[1]
+    same_specials(z[[0, 2, 4, 6, 8, last]], want, "rows")
+    assert bool(torch.isinf(want[0].float()[[0, 1, 3, 4]]).any(1).all())
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[[0, 2, 4, 6, 8, last]] = False
+    assert torch.equal(z[keep], b2.gated_linear(x, wide, activation=0, want_z=True)[1][keep])
+    # the same in the weight: a gate's feature, one of what it gates, and the last ones
+    bad = w.clone()
+    features = [1, n_out - 1, n_out, 2 * n_out - 1, n_out + 9, 12]
+    bad[1, 3], bad[n_out - 1, 7], bad[n_out, 7] = inf, -inf, inf
+    bad[2 * n_out - 1, n_in - 1] = inf
+    bad[n_out + 9, 4], bad[12, 4] = (s * torch.finfo(torch.float32).max for s in (1, -1))
+    wide = x.clone()
+    wide[:, 4] *= 8.0
+    h, z = b2.gated_linear(wide, bad, activation=0, want_z=True)
+    same_specials(z[:, features], [v.t() for v in product(bad[features], wide)], "features")
+    keep = torch.ones(2 * n_out, dtype=torch.bool, device="cuda")
+    keep[features] = False
+    base = b2.gated_linear(wide, w, activation=0, want_z=True)[1]
+    assert torch.equal(z[:, keep], base[:, keep])
+    same_specials(h, [z[:, :n_out] * z[:, n_out:]], "h")
+
+
+@pytest.mark.parametrize("tiling", [(0, 0, 0, 0), (2, 256, 1, 0), (1, 128, 1, 0), (1, 128, 4, 0),
+                                    (1, 64, 1, 0), (1, 64, 8, 0)])
+def test_infinities_and_overflow_of_gradients_in_pieces(tiling):
+    """The same of dx and dw."""
+    rows, n_in, n_out = 333, 580, 420
+    assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+    g = gen(28)
+    x, w = tensor(g, (rows, n_in), torch.float32), tensor(g, (2 * n_out, n_in), torch.float32)
+    dh, z = tensor(g, (rows, n_out), torch.float32), tensor(g, (rows, 2 * n_out), torch.float32)
+    inf = float("inf")
+    z[rows - 1, 11], z[rows - 1, n_out + 11] = 1.0, 0.0
+    clean = b2.gated_linear_grad(dh, x, w, z, activation=0)
+    bad = dh.clone()
+    bad[0, 2], bad[40, n_out - 1], bad[rows - 1, 11] = inf, -inf, 2.0 ** 127
+    xb, wb = x.clone(), w.clone()
+    xb[7, 20], xb[9, n_in - 1] = inf, float("nan")
+    wb[3, 30], wb[n_out + 5, 0] = -inf, inf
+    dx, dw, _ = b2.gated_linear_grad(bad, xb, wb, z, activation=0)
+    dz = torch.cat((bad * z[:, n_out:], bad * z[:, :n_out]), 1)
+    rx, rw = [0, 40, rows - 1, 1, 2, 200], [2, n_out + 2, n_out - 1, 11, n_out + 11, 50]
+    same_specials(dx[rx], product(dz[rx], wb.t()), "dx")
+    same_specials(dw[rw], product(dz.t()[rw], xb.t()), "dw")
+    cols = torch.ones(n_in, dtype=torch.bool, device="cuda")
+    cols[[30, 0]] = False
+    assert torch.equal(dx[1:40][:, cols], clean[0][1:40][:, cols])
+    cols[:] = True
+    cols[[20, n_in - 1]] = False
+    one = [i for i in range(2 * n_out) if i % n_out not in (2, 11, n_out - 1)]
+    assert torch.equal(dw[one][:, cols], clean[1][one][:, cols])
+
+
+def test_nothing_finite_in_pieces():
+    """Every sum made again: the waits allow for it, and the results are as above."""
+    rows, n_in, n_out = 600, 1024, 512
+    g = gen(29)
+    w = tensor(g, (2 * n_out, n_in), torch.float32).abs() + 0.1
+    for value in (float("nan"), float("inf"), -float("inf")):
+        x = torch.full((rows, n_in), value, device="cuda")
+        h, z = b2.gated_linear(x, w, activation=0, want_z=True)
+        b2.linear_status()
+        same_specials(z, [torch.full_like(z, value)], "z")
+        dx, dw, _ = b2.gated_linear_grad(x[:, :n_out].contiguous(), x, w, torch.ones_like(z),
+                                         activation=0)
+        b2.linear_status()
+        assert not bool(torch.isfinite(dx).any()) and not bool(torch.isfinite(dw).any())
+
+
 @pytest.mark.parametrize("tiling", [(2, 256, 1, 0), (1, 128, 1, 0), (1, 128, 4, 0), (1, 16, 2, 1)])
 def test_waits_in_pieces_give_up(tiling):
     lib = b2.library()

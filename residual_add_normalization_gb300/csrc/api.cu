@@ -301,28 +301,33 @@ bool heads_distinct(const HeadsArg& a, int64_t batch, int64_t seq, int64_t size)
   return true;
 }
 
-// Whether two tensors of heads share no element, as far as it can be told: they lie
-// apart, or side by side inside rows of one step (queries and keys of one product).
+// Whether two tensors of heads share no element, as far as it can be told: they lie apart, or
+// side by side in every stretch of one of their steps (in a sequence, a product's row, or a
+// head's place of queries, keys and values).
 bool heads_apart(const HeadsArg& a, const HeadsArg& b, int64_t batch, int64_t seq, int64_t size,
                  size_t es) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
   if (a0 > b0) return heads_apart(b, a, batch, seq, size, es);
   const uintptr_t gap = (b0 - a0) / es;
   if (heads_extent(a, batch, seq, size) <= gap) return true;
-  // the step that all rows of both share: of the sequences, or of the tokens as well
-  auto beside = [&](int64_t step, int64_t tokens) {
-    const Wide an = static_cast<Wide>(tokens - 1) * a.strides[1] +
-                    static_cast<Wide>(a.heads - 1) * a.strides[2] + size;
-    const Wide bn = static_cast<Wide>(tokens - 1) * b.strides[1] +
-                    static_cast<Wide>(b.heads - 1) * b.strides[2] + size;
-    if (step <= 0) return false;
-    const Wide at = gap % static_cast<uintptr_t>(step);
-    return an <= at && at + bn <= static_cast<Wide>(step);
+  // elements from the first to one past the last, whole stretches left out
+  auto within = [&](const HeadsArg& t, int64_t step) {
+    const int64_t n[3] = {batch, seq, t.heads};
+    Wide extent = static_cast<Wide>(size);
+    for (int i = 0; i < 3; ++i)
+      if (t.strides[i] % step) extent += static_cast<Wide>(n[i] - 1) * t.strides[i];
+    return extent;
   };
-  if (batch > 1 && a.strides[0] == b.strides[0] && beside(a.strides[0], seq)) return true;
-  const int64_t step = a.strides[1];
-  return seq > 1 && step > 0 && step == b.strides[1] &&
-         (batch == 1 || (a.strides[0] % step == 0 && b.strides[0] % step == 0)) && beside(step, 1);
+  for (const HeadsArg* t : {&a, &b}) {
+    const int64_t n[3] = {batch, seq, t->heads};
+    for (int i = 0; i < 3; ++i) {
+      const int64_t step = t->strides[i];
+      if (n[i] < 2 || step < 1) continue;
+      const Wide at = gap % static_cast<uintptr_t>(step);
+      if (within(a, step) <= at && at + within(b, step) <= static_cast<Wide>(step)) return true;
+    }
+  }
+  return false;
 }
 
 bool heads_same(const HeadsArg& a, const HeadsArg& b, int64_t batch, int64_t seq) {

@@ -277,6 +277,31 @@ def test_in_place_and_into_rows(size, rot, t):
     assert bool((dst[:, :, 50] == 7).all())
 
 
+@pytest.mark.parametrize("shape", [(2, 9, 4, 3, 64), (1, 9, 4, 3, 64), (2, 1, 4, 3, 64),
+                                   (2, 9, 1, 3, 64), (9, 2, 5, 3, 20)])
+@pytest.mark.parametrize("order", [(0, 1, 2, 3), (2, 0, 1, 3), (0, 3, 1, 2), (3, 2, 1, 0)])
+def test_queries_keys_and_values_side_by_side_in_any_axis(shape, order):
+    """In place and into views of one tensor, where queries, keys and values alternate head by
+    head, or the axes lie in another order: the bits of dense results, and values as they were.
+    `order`: the axes (batch, seq, head, which of the three) from the outermost."""
+    g = gen(16)
+    lie = torch.randn([shape[i] for i in order] + [shape[4]], generator=g, device="cuda").bfloat16()
+    view = lie.permute([order.index(i) for i in range(4)] + [4])
+    q, k, v = view.unbind(3)
+    p, f = torch.arange(shape[1], device="cuda"), frequencies(shape[4])
+    gamma = torch.randn(shape[4], generator=g, device="cuda")
+    want = b2.head_rms_rotary(q, k, gamma, gamma, p, f)
+    dq, dk = (torch.randn(w.shape, generator=g, device="cuda").bfloat16() for w in want)
+    grads = b2.head_rms_rotary_grad(dq, dk, q, k, gamma, gamma, p, f)
+    into = torch.full_like(lie, 7.0)
+    gq, gk, gv = into.permute([order.index(i) for i in range(4)] + [4]).unbind(3)
+    got = b2.head_rms_rotary_grad(dq, dk, q, k, gamma, gamma, p, f, dq_out=gq, dk_out=gk)
+    assert all(torch.equal(a, b) for a, b in zip(got, grads)) and bool((gv == 7).all())
+    keep = v.clone()
+    b2.head_rms_rotary(q, k, gamma, gamma, p, f, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, keep)
+
+
 @pytest.mark.parametrize("t", ["bf16", "f32"])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_nan_and_infinity_stay_where_they_are(t, interleaved):

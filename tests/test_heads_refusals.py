@@ -105,6 +105,17 @@ def test_overlap_refusals(lib):
     assert b"outputs overlap" in lib.b200norm_last_error()
 
 
+def test_overlap_refusals_of_heads_that_alternate(lib):
+    """Queries and keys head by head in rows of 4 x 128: one element into the other's place."""
+    apart = dict(yb=2560, yt=512, yh=128)
+    for at in (63 * 2, 65 * 2, 127 * 2, (512 + 1) * 2):
+        assert rotary(lib, one(y=FAKE + G, **apart), keys(y=FAKE + G + at, **apart)) == INVALID, at
+        assert b"outputs overlap" in lib.b200norm_last_error()
+    # steps that are not each other's multiples
+    assert rotary(lib, one(y=FAKE + G, **apart),
+                  keys(y=FAKE + G + 128, **{**apart, "yh": 192})) == INVALID
+
+
 def test_empty_calls_do_nothing(lib):
     none = one(x=0, y=0)
     assert norm(lib, none, batch=0) == OK

@@ -198,8 +198,10 @@ inline bool few_rows(int64_t M, int64_t N, int64_t K, DType t, bool aligned) {
 }
 // The same of a gated product (N columns of the result): one row always goes to it
 // (1 x 4096 x 8192 bf16 22.8 us, 24.9 on the tensor cores; 1 x 1024 x 4096 4.9 and 7.3), and
-// float32 up to eight of whole vectors (8 x 4096 x 4096 64.5 us, 124 on the binary32 tiles and
-// 100 in pieces; 8 x 256 x 256 2.4 and 8.0; but 8 x 1027 x 1283 33 and 17).
+// float32 up to eight where 4 divides K (8 x 4096 x 4096 54 us, 124 on the binary32 tiles and 100
+// in pieces; 8 x 256 x 256 2.7 and 8.0; but 8 x 1027 x 1283 33 and 17).  Off 16-byte boundaries
+// as well, where its loads are of 4 bytes: 5 x 256 x 256 5.4 and 8.5, 6 x 2048 x 2048 32 and 43,
+// 8 x 1024 x 1024 16.8 and 16.3 (8 x 4096 x 1024 60 and 49), 8 x 4096 x 4096 131, in pieces 152.
 inline bool gated_few_rows(int64_t M, int64_t N, int64_t K, DType t, bool aligned) {
   return M == 1 || (t == DType::F32 && M <= 8 && K % 4 == 0) || few_rows(M, 2 * N, K, t, aligned);
 }

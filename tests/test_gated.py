@@ -77,6 +77,12 @@ def test_operands_at_odd_places(rows, n_in, n_out, t):
     check_forward(rows, n_in, n_out, DTYPES[t], odd=True)
 
 
+@pytest.mark.parametrize("rows", [2, 4, 5, 6, 8, 9])
+@pytest.mark.parametrize("n_in,n_out", [(256, 70), (258, 64), (4096, 3300)])
+def test_float32_at_odd_places(rows, n_in, n_out):
+    check_forward(rows, n_in, n_out, torch.float32, odd=True, bias=rows % 2 == 0)
+
+
 TILINGS = ([(2, 256, 1, 0)] + [(1, 128, s, 0) for s in (1, 2, 4, 8)]
            + [(1, bn, s, 1) for bn in (16, 32, 64) for s in (1, 2, 4, 8)])
 

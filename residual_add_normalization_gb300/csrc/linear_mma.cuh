@@ -877,7 +877,8 @@ linear_mma_kernel(const __grid_constant__ CUtensorMap map_a,
   if (!g.late) pdl_wait();
   pdl_trigger();  // after the allocation: a later grid cannot take the columns first
 
-  // this CTA's (pair's) tiles and its part of K
+  // this CTA's (pair's) tiles and its part of K (with pieces there may be more parts than slices,
+  // which the plan counts three times: the sums of a part without one are zeros)
   const int unit = CG == 2 || g.splits > 1 ? blockIdx.x / cluster_size() : blockIdx.x;
   const int units = CG == 2 || g.splits > 1 ? gridDim.x / cluster_size() : gridDim.x;
   const int tiles = g.tiles_m * g.tiles_n;

@@ -131,7 +131,8 @@ cudaError_t launch_mma(const Product& p, cudaStream_t stream) {
   if (!status) return cudaErrorSymbolNotFound;
   const bool a_kc = p.a.k_contiguous, b_kc = p.b.k_contiguous;
   MmaPlan plan = p.forced;
-  // in pieces a slice of K has three times the bytes (and six times the products)
+  // in pieces a slice of K has three times the bytes (and six times the products); so counted, a
+  // sum may be split into more parts than it has slices
   const int64_t K = p.piece_a ? 3 * ((p.K + kMmaK - 1) / kMmaK * kMmaK) : p.K;
   if (plan.cg == 0) plan = plan_mma(p.M, p.N, K, b_kc, p.gated, p.piece_a != 0, sms);
   else if (!mma_plan_ok(plan, p.M, K, a_kc, b_kc, p.gated)) return cudaErrorNotSupported;

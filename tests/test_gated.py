@@ -399,6 +399,30 @@ def test_every_tiling_in_pieces(tiling):
     assert torch.equal(h, (want[:, :n_out].float() * want[:, n_out:].float()))
 
 
+@pytest.mark.parametrize("rows,n_in,n_out,tiling", [
+    (64, 448, 2400, (0, 0, 0, 0)), (64, 448, 2400, (1, 64, 8, 1)), (30, 384, 6000, (1, 32, 8, 1)),
+    (64, 320, 3300, (1, 64, 8, 1)), (16, 192, 22000, (1, 16, 8, 1)), (300, 448, 520, (1, 128, 8, 0)),
+    (700, 150, 700, (1, 128, 8, 0))])
+def test_more_parts_than_slices_in_pieces(rows, n_in, n_out, tiling):
+    """A part of a sum may have no slice of 64 (448 are seven, in eight parts): in whole numbers,
+    exactly; and an infinity of another part is not lost."""
+    assert b2.library().b200norm_testing_force_linear(*tiling) == 0
+    g = gen(33)
+    x = torch.randint(-1500, 1501, (rows, n_in), generator=g, device="cuda")
+    x *= torch.rand(x.shape, generator=g, device="cuda") < 0.05
+    w = torch.randint(-300, 301, (2 * n_out, n_in), generator=g, device="cuda")
+    want = x.double() @ w.double().t()
+    assert float((x.double().abs() @ w.double().abs().t()).max()) < 2 ** 24
+    h, z = b2.gated_linear(x.float(), w.float(), activation=0, want_z=True)
+    assert torch.equal(z.double(), want)
+    assert torch.equal(h, (want[:, :n_out].float() * want[:, n_out:].float()))
+    bad = x.float()
+    bad[rows - 1, n_in - 1] = float("inf")
+    z = b2.gated_linear(bad, w.float(), activation=0, want_z=True)[1]
+    assert torch.equal(z[:-1].double(), want[:-1])
+    same_specials(z[-1:], product(bad[-1:], w.float()), "row")
+
+
 def test_the_gradients_tilings_in_pieces():
     """The same of both products of a gradient: z of gates 1 without an activation, so that dz
     is dh twice."""

@@ -53,8 +53,9 @@ FAMILY_SOURCES = {
                "linear_f32.cu", "linear_f16.cu", "linear_bf16.cu", "linear_mma.cuh",
                "linear_mma_launch.cuh", "linear_mma_f16.cu", "linear_mma_bf16.cu",
                "gated_mma_f16.cu", "gated_mma_bf16.cu", "gated_mma_f32.cu"),
-    "heads": ("common.cuh", "launch.h", "launch_kernel.cuh", "heads.h", "heads.cuh",
-              "heads_launch.cuh", "heads.cu", "heads_f32.cu", "heads_f16.cu", "heads_bf16.cu"),
+    "heads": ("common.cuh", "bulk.cuh", "pair.cuh", "launch.h", "launch_kernel.cuh", "heads.h",
+              "heads.cuh", "heads_launch.cuh", "heads.cu", "heads_f32.cu", "heads_f16.cu",
+              "heads_bf16.cu"),
 }
 
 

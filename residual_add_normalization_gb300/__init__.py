@@ -909,10 +909,11 @@ def _first_heads(q, k):
 
 def _gammas(q, gamma_q, k, gamma_k, size, x, index):
     """The type of both gammas (x's without any)."""
-    if (gamma_q is not None and gamma_k is not None and q is not None and k is not None
-            and gamma_q.dtype is gamma_k.dtype):
+    if gamma_q is not None and gamma_k is not None and q is not None and k is not None:
         _weights("gamma_q", gamma_q, size, x, index)
         _weights("gamma_k", gamma_k, size, x, index)
+        if gamma_q.dtype is not gamma_k.dtype:
+            raise TypeError("gamma_q and gamma_k must be of one type")
         return gamma_q.dtype
     m = None
     for name, heads, gamma in (("gamma_q", q, gamma_q), ("gamma_k", k, gamma_k)):

@@ -235,6 +235,20 @@ def test_python_refusals_of_cuda_tensors():
             pytest.fail(f"call {i} was taken")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("wrong", [[1.0] * 8, 1.0, "ones"])
+def test_gammas_that_are_no_tensors(wrong):
+    x = torch.zeros(4, 2, 8, device="cuda")
+    p = torch.zeros(4, dtype=torch.int64, device="cuda")
+    f = torch.zeros(4, dtype=torch.float64, device="cuda")
+    g = torch.ones(8, device="cuda")
+    for gq, gk in ((wrong, g), (g, wrong), (wrong, wrong)):
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            b2.head_rms_rotary(x, x, gq, gk, p, f)
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            b2.head_rms_rotary_grad(x, x, x, x, gq, gk, p, f)
+
+
 def freqs(lib, n, base=10000.0, scaling=0, factor=1.0, length=0.0, low=1.0, high=32.0):
     out = (ctypes.c_double * (max(n, 2) // 2))()
     st = lib.b200norm_rotary_frequencies(out, n, base, scaling, factor, length, low, high)

@@ -68,9 +68,9 @@ cudaError_t launch_mma_shape(const Product& p, const MmaPlan& plan, int sms, uns
   for (const void* o : outs)
     if (reinterpret_cast<uintptr_t>(o) % 16 != 0) g.vec = false;
   g.status = status;
-  // a wait lasts a tile at most: a second, and 4 us for each slice of K (in pieces 20 ms: all of
+  // a wait lasts a tile at most: a second, and 4 us for each slice of K (in pieces 10 ms: all of
   // a tile's sums may have to be made again, which took up to 5)
-  g.limit_ns = 1000000000ull + (kPieces ? 20000000ull : 4000ull) * g.kblocks;
+  g.limit_ns = 1000000000ull + (kPieces ? 10000000ull : 4000ull) * g.kblocks;
   g.late = p.late;
   g.stall = linear_stall_limit_ns() != 0;
   if (g.stall) g.limit_ns = linear_stall_limit_ns();

@@ -1017,7 +1017,6 @@ b200norm_status b200norm_head_rms_rotary_grad(
   if (b200norm_status st = check_rotation(rotation, batch, seq, head_size)) return st;
   if (b200norm_status st = check_eps(epsilon)) return st;
   HeadsCall c = heads_call(rotation, batch, seq, head_size, T, M);
-  c.inverse = true;
   c.norm = true;
   c.eps = epsilon;
   const size_t es = dtype_size(c.t), ms = dtype_size(c.m), gb = static_cast<size_t>(head_size) * ms;

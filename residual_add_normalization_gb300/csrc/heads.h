@@ -33,7 +33,8 @@ struct HeadsCall {
   const double* inv_freq;  // rot / 2 radians per position
   int64_t batch, seq;
   int size, rot;
-  bool interleaved, inverse, norm;
+  bool interleaved, norm;
+  bool inverse;            // forward only
   float scale, eps;
   DType t, m;
   float* part;             // gradient: sums over rows, head_parts() of them
